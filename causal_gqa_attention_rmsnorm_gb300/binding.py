@@ -8,9 +8,10 @@ and the current CUDA stream.  A missing library raises; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from ctypes import c_float, c_int32, c_size_t, c_void_p
+from ctypes import c_float, c_int32, c_int64, c_size_t, c_void_p
 from dataclasses import dataclass
 from typing import Dict, Optional
 
@@ -18,7 +19,7 @@ import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtb.so")
 
-TB_F32, TB_BF16, TB_I8 = 0, 1, 2
+TB_F32, TB_BF16, TB_I8, TB_E4M3 = 0, 1, 2, 3
 TB_DEVERR_CACHE_FULL, TB_DEVERR_TIMEOUT, TB_DEVERR_BAD_PAGE, TB_DEVERR_BAD_TOKEN = 1, 2, 4, 8
 STATUS = {0: "TB_OK", 1: "TB_ERR_INVALID_ARG", 2: "TB_ERR_UNSUPPORTED", 3: "TB_ERR_CUDA",
           4: "TB_ERR_CACHE_FULL", 5: "TB_ERR_TIMEOUT"}
@@ -27,7 +28,8 @@ EXPORTED = ("tb_packed_weights_bytes", "tb_pack_weights", "tb_workspace_bytes", 
             "tb_block_decode", "tb_block_decode_noalloc", "tb_kvcache_append", "tb_get_device_error", "tb_status_string",
             "tb_last_error_message", "tb_embed", "tb_lm_head_packed_bytes", "tb_pack_lm_head",
             "tb_lm_head_workspace_bytes", "tb_lm_head", "tb_stack_workspace_bytes", "tb_stack_prefill",
-            "tb_stack_decode")
+            "tb_stack_decode", "tb_rope_table", "tb_kvcache_append_rope", "tb_kvcache_attn_workspace_bytes",
+            "tb_kvcache_attn")
 
 
 class tb_block_cfg(ctypes.Structure):
@@ -48,6 +50,17 @@ class tb_kvcache(ctypes.Structure):
 
 class tb_head_cfg(ctypes.Structure):
     _fields_ = [("d", c_int32), ("V", c_int32), ("eps", c_float), ("dtype", c_int32)]
+
+
+class tb_append_rows(ctypes.Structure):
+    _fields_ = ([(n, c_void_p) for n in ("q", "k", "v", "q_out")]
+                + [(n, c_int64) for n in ("q_tok", "q_seq", "k_tok", "k_seq", "v_tok", "v_seq")]
+                + [("H", c_int32), ("n", c_int32), ("start", c_void_p), ("n_new", c_void_p)])
+
+
+class tb_attn_cfg(ctypes.Structure):
+    _fields_ = [("H", c_int32), ("Hkv", c_int32), ("dh", c_int32), ("dtype", c_int32), ("window", c_int32),
+                ("sinks", c_int32), ("scale", c_float)]
 
 
 class TbError(RuntimeError):
@@ -113,7 +126,13 @@ def lib() -> ctypes.CDLL:
                                        c_int32, P(tb_kvcache), c_void_p, c_size_t, c_void_p]
         L.tb_stack_decode.argtypes = [P(tb_block_cfg), c_int32, P(c_void_p), c_void_p, c_void_p, c_int32,
                                       P(tb_kvcache), c_void_p, c_size_t, c_void_p]
-        for fn in ("tb_pack_weights", "tb_block_prefill", "tb_block_decode", "tb_block_decode_noalloc",
+        L.tb_rope_table.argtypes = [c_int32, c_int32, c_float, c_void_p, c_void_p]
+        L.tb_kvcache_append_rope.argtypes = [P(tb_kvcache), P(tb_append_rows), c_void_p, c_int32, c_void_p]
+        L.tb_kvcache_attn_workspace_bytes.argtypes = [P(tb_attn_cfg), P(tb_kvcache), c_int32]
+        L.tb_kvcache_attn_workspace_bytes.restype = c_size_t
+        L.tb_kvcache_attn.argtypes = [P(tb_attn_cfg), c_void_p, P(tb_kvcache), c_void_p, c_int32, c_void_p, c_void_p,
+                                      c_size_t, c_void_p]
+        for fn in ("tb_rope_table", "tb_kvcache_append_rope", "tb_kvcache_attn", "tb_pack_weights", "tb_block_prefill", "tb_block_decode", "tb_block_decode_noalloc",
                    "tb_kvcache_append", "tb_embed", "tb_pack_lm_head", "tb_lm_head", "tb_stack_prefill",
                    "tb_stack_decode", "tb_get_device_error", "tbx_gemm_bf16"):
             getattr(L, fn).restype = c_int32
@@ -149,6 +168,9 @@ class BlockConfig:
         return torch.float32 if self.dtype == TB_F32 else torch.bfloat16
 
 
+_CACHE_DTYPES = {torch.float32: TB_F32, torch.bfloat16: TB_BF16, torch.int8: TB_I8, torch.float8_e4m3fn: TB_E4M3}
+
+
 @dataclass
 class KVCache:
     """Caller-owned cache tensors.  Contiguous: k, v [B, Hkv, T_max, dh].
@@ -156,7 +178,10 @@ class KVCache:
     and block_table int32 [B, T_max / page_size].  int8 (k, v of torch.int8):
     codes [B, Hkv, T_max, dh] with fp32 row scales k_scale, v_scale
     [B, Hkv, T_max], or paged: code pools [num_pages, Hkv, page_size, dh] and
-    scale pools [num_pages, Hkv, page_size].  lens int32 [B]."""
+    scale pools [num_pages, Hkv, page_size].  e4m3 (k, v of
+    torch.float8_e4m3fn): codes with one fp32 scale per block of tokens and KV
+    head, k_scale, v_scale [B, Hkv, T_max / block], or paged [num_pages, Hkv]
+    (a block is a page).  lens int32 [B]."""
     k: torch.Tensor
     v: torch.Tensor
     lens: torch.Tensor
@@ -170,9 +195,9 @@ class KVCache:
                 raise ValueError("cache tensors must be contiguous CUDA tensors")
         if self.v.shape != self.k.shape or self.v.dtype != self.k.dtype:
             raise ValueError("k and v caches must match")
-        dt = {torch.float32: TB_F32, torch.bfloat16: TB_BF16, torch.int8: TB_I8}.get(self.k.dtype)
+        dt = _CACHE_DTYPES.get(self.k.dtype)
         if dt is None:
-            raise ValueError(f"cache dtype {self.k.dtype} is not float32, bfloat16 or int8")
+            raise ValueError(f"cache dtype {self.k.dtype} is not float32, bfloat16, int8 or float8_e4m3fn")
         if self.block_table is None:
             B, Hkv, T_max, dh = self.k.shape
             bt, ps, npages = None, 0, 0
@@ -190,6 +215,19 @@ class KVCache:
                 if t is None:
                     raise ValueError(f"an int8 cache needs {name}")
                 _need(t, name, torch.float32, (B, Hkv, T_max) if bt is None else (npages, Hkv, ps))
+            ks, vs = self.k_scale.data_ptr(), self.v_scale.data_ptr()
+        elif dt == TB_E4M3:
+            if self.k_scale is None or self.v_scale is None:
+                raise ValueError("an e4m3 cache needs k_scale and v_scale")
+            if bt is None:
+                blocks = self.k_scale.shape[-1] if self.k_scale.dim() == 3 else 0
+                if blocks <= 0 or T_max % blocks:
+                    raise ValueError("k_scale must be [B, Hkv, T_max / block]")
+                ps, want = T_max // blocks, (B, Hkv, blocks)
+            else:
+                want = (npages, Hkv)
+            _need(self.k_scale, "k_scale", torch.float32, want)
+            _need(self.v_scale, "v_scale", torch.float32, want)
             ks, vs = self.k_scale.data_ptr(), self.v_scale.data_ptr()
         return tb_kvcache(self.k.data_ptr(), self.v.data_ptr(), self.lens.data_ptr(), B, Hkv, T_max, dh, dt,
                           None if bt is None else bt.data_ptr(), ps, npages, ks, vs)
@@ -210,6 +248,24 @@ class KVCache:
         codes = lambda: torch.zeros((B, Hkv, T_max, dh), dtype=torch.int8, device=device)
         scales = lambda: torch.zeros((B, Hkv, T_max), dtype=torch.float32, device=device)
         return KVCache(codes(), codes(), torch.zeros(B, dtype=torch.int32, device=device), None, scales(), scales())
+
+    @staticmethod
+    def empty_e4m3(B: int, Hkv: int, T_max: int, dh: int, block: int, device="cuda",
+                   block_table: Optional[torch.Tensor] = None, num_pages: int = 0) -> "KVCache":
+        """Zeroed e4m3 codes with a scale of 1 per block of `block` tokens and KV
+        head; with a block table [B, T_max / block], pools of num_pages pages."""
+        if T_max % block:
+            raise ValueError("block must divide T_max")
+        bt = block_table
+        if bt is not None:
+            if bt.shape != (B, T_max // block):
+                raise ValueError("block_table must be [B, T_max / block]")
+            bt = bt.to(device=device, dtype=torch.int32).contiguous()
+        shape = (B, Hkv, T_max, dh) if bt is None else (num_pages, Hkv, block, dh)
+        sshape = (B, Hkv, T_max // block) if bt is None else (num_pages, Hkv)
+        codes = lambda: torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+        scales = lambda: torch.ones(sshape, dtype=torch.float32, device=device)
+        return KVCache(codes(), codes(), torch.zeros(B, dtype=torch.int32, device=device), bt, scales(), scales())
 
     @staticmethod
     def empty_paged(B: int, Hkv: int, T_max: int, dh: int, page_size: int, num_pages: int, block_table: torch.Tensor,
@@ -503,3 +559,149 @@ def tb_stack_decode(cfg: BlockConfig, packed, x: torch.Tensor, kvs, y_dtype: int
                                                     y.data_ptr(), y_dtype, kv_arr, ws.data_ptr(), ws.numel(),
                                                     _stream(stream)))
     return y
+
+
+# ---- several tokens over a cache: append with rotation, attention ----------
+
+@dataclass(frozen=True)
+class AttnConfig:
+    """Python mirror of tb_attn_cfg."""
+    H: int
+    Hkv: int
+    dh: int
+    window: int = 0          # sliding-window width W (0: full causal)
+    sinks: int = 0           # first tokens that stay visible beside the window
+    scale: float = 0.0       # of the scores (0: 1/sqrt(dh))
+    dtype: int = TB_BF16     # of q and o
+
+    def c(self) -> tb_attn_cfg:
+        return tb_attn_cfg(self.H, self.Hkv, self.dh, self.dtype, self.window, self.sinks, self.scale)
+
+    @property
+    def torch_dtype(self) -> torch.dtype:
+        return torch.float32 if self.dtype == TB_F32 else torch.bfloat16
+
+
+def _stream_on(stream, device: torch.device) -> int:
+    """The raw stream of a call on `device`'s tensors, which must be the current device."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is {torch.cuda.current_device()}")
+    return _stream(stream)
+
+
+def _counts(t: Optional[torch.Tensor], name: str, B: int, device: torch.device) -> Optional[int]:
+    if t is None:
+        return None
+    _need(t, name, torch.int32, (B,))
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t.data_ptr()
+
+
+def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, B: int, n: int, dh: int, device: torch.device):
+    """Heads, token stride and sequence stride of rows [B, n, heads, dh] whose heads are dense."""
+    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != n or t.shape[3] != dh:
+        raise ValueError(f"{name} must be [{B}, {n}, heads, {dh}], got {tuple(t.shape)}")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    seq, tok, head, one = t.stride()
+    if (one != 1 and dh > 1) or (head != dh and t.shape[2] > 1):
+        raise ValueError(f"a token's heads must be dense in {name}")
+    return t.shape[2], (tok if n > 1 else t.shape[2] * dh), (seq if B > 1 else 0)
+
+
+def tb_rope_table(dh: int, max_pos: int, base: float, device="cuda", stream=None) -> torch.Tensor:
+    """The rotation table [max_pos, dh / 2, 2] fp32 of tb_kvcache_append_rope."""
+    with _alloc_on(stream):
+        table = torch.empty((max_pos, dh // 2, 2), dtype=torch.float32, device=device)
+    _check("tb_rope_table", lib().tb_rope_table(dh, max_pos, base, table.data_ptr(),
+                                                _stream_on(stream, table.device)))
+    return table
+
+
+def tb_kvcache_append_rope(kv: KVCache, k: torch.Tensor, v: torch.Tensor, rope: torch.Tensor,
+                           q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                           start: Optional[torch.Tensor] = None, n_new: Optional[torch.Tensor] = None,
+                           stream=None) -> Optional[torch.Tensor]:
+    """Append unrotated rows k, v [B, n, Hkv, dh] at positions start (default:
+    kv.lens) with the rotation applied; q [B, n, H, dh] comes back rotated (in
+    q_out, if given).  k, v and q may be column blocks of one projection.  n_new
+    [B]: how many of each sequence's n rows count."""
+    kvs = kv.c()
+    dev = kv.k.device
+    row = torch.float32 if kvs.dtype == TB_F32 else torch.bfloat16
+    if k.dim() != 4:
+        raise ValueError("k must be [B, n, Hkv, dh]")
+    B, n, dh = kvs.B, k.shape[1], kvs.dh
+    heads, k_tok, k_seq = _heads(k, "k", row, B, n, dh, dev)
+    heads_v, v_tok, v_seq = _heads(v, "v", row, B, n, dh, dev)
+    if heads != kvs.Hkv or heads_v != kvs.Hkv:
+        raise ValueError(f"k and v must have {kvs.Hkv} heads")
+    _need(rope, "rope", torch.float32)
+    if rope.dim() != 3 or rope.shape[1] != dh // 2 or rope.shape[2] != 2 or rope.device != dev:
+        raise ValueError(f"rope must be [max_pos, {dh // 2}, 2] on {dev}")
+    H, q_tok, q_seq, q_ptr, out_ptr = 0, 0, 0, None, None
+    if q is not None:
+        H, q_tok, q_seq = _heads(q, "q", row, B, n, dh, dev)
+        if q_out is None:
+            with _alloc_on(stream):
+                q_out = torch.empty((B, n, H, dh), dtype=row, device=dev)
+        _need(q_out, "q_out", row, (B, n, H, dh))
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+        if B == 1:
+            q_seq = q_tok * n
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rows = tb_append_rows(q_ptr, k.data_ptr(), v.data_ptr(), out_ptr, q_tok, q_seq, k_tok, k_seq, v_tok, v_seq, H, n,
+                          _counts(start, "start", B, dev), _counts(n_new, "n_new", B, dev))
+    _check("tb_kvcache_append_rope", lib().tb_kvcache_append_rope(ctypes.byref(kvs), ctypes.byref(rows),
+                                                                  rope.data_ptr(), rope.shape[0],
+                                                                  _stream_on(stream, dev)))
+    return q_out
+
+
+def _alloc_on(stream):
+    """Where a call's own buffers come from: its stream's pool, so that the
+    allocator does not hand them on while the call still runs there."""
+    if stream is None:
+        return contextlib.nullcontext()
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+    return torch.cuda.stream(s)
+
+
+def tb_kvcache_attn_workspace_bytes(cfg: AttnConfig, kv: KVCache, n: int) -> int:
+    return lib().tb_kvcache_attn_workspace_bytes(ctypes.byref(cfg.c()), ctypes.byref(kv.c()), n)
+
+
+def tb_kvcache_attn_workspace(cfg: AttnConfig, kv: KVCache, n: int) -> torch.Tensor:
+    """A workspace for tb_kvcache_attn calls of up to n tokens per sequence that do not overlap."""
+    return torch.empty(max(tb_kvcache_attn_workspace_bytes(cfg, kv, n), 256), dtype=torch.uint8, device=kv.k.device)
+
+
+def tb_kvcache_attn(cfg: AttnConfig, q: torch.Tensor, kv: KVCache, n_new: Optional[torch.Tensor] = None,
+                    o: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """Attention of the last tokens of each sequence, q [B, n, H, dh] (rotated),
+    over the cache they were appended to -> o [B, n, H, dh]."""
+    kvs, cc = kv.c(), cfg.c()
+    dev = kv.k.device
+    if q.dim() != 4:
+        raise ValueError("q must be [B, n, H, dh]")
+    n = q.shape[1]
+    shape = (kvs.B, n, cfg.H, cfg.dh)
+    _need(q, "q", cfg.torch_dtype, shape)
+    with _alloc_on(stream):
+        if o is None:
+            o = torch.zeros(shape, dtype=cfg.torch_dtype, device=dev) if n_new is not None else torch.empty(
+                shape, dtype=cfg.torch_dtype, device=dev)
+        if ws is None:
+            need = lib().tb_kvcache_attn_workspace_bytes(ctypes.byref(cc), ctypes.byref(kvs), n)
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _need(o, "o", cfg.torch_dtype, shape)
+    if q.device != dev or o.device != dev or ws.device != dev:
+        raise ValueError(f"q, o and ws must be on {dev}")
+    _check("tb_kvcache_attn", lib().tb_kvcache_attn(ctypes.byref(cc), q.data_ptr(), ctypes.byref(kvs),
+                                                    _counts(n_new, "n_new", kvs.B, dev), n, o.data_ptr(),
+                                                    ws.data_ptr(), ws.numel() * ws.element_size(),
+                                                    _stream_on(stream, dev)))
+    return o

@@ -107,6 +107,8 @@ tb_status report(tb_status st, const char* fmt, ...);
 // elementwise.cu
 cudaError_t launch_pack(int dtype, const Dims& D, const tb_block_weights& w, void* packed,
                         const Packed& P, float rope_base, cudaStream_t s);
+// (cos, sin) of t·base^(-2i/dh): table [max_pos, dh/2]
+cudaError_t launch_rope_table(float2* table, int max_pos, int dh, float base, cudaStream_t s);
 cudaError_t launch_row_stats(int dtype, const void* x, int M, int d, float eps, float* r,
                              int T, int32_t* lens_set, int32_t* lens_bump,
                              int32_t* pos_out, int T_max, int* zero_word, int* err, cudaStream_t s);

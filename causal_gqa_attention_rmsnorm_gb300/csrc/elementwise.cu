@@ -239,6 +239,12 @@ cudaError_t launch_pack(int dtype, const Dims& D, const tb_block_weights& w, voi
   return cudaGetLastError();
 }
 
+cudaError_t launch_rope_table(float2* table, int max_pos, int dh, float base, cudaStream_t s) {
+  const size_t n = (size_t)max_pos * (dh / 2);
+  k_rope_table<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(table, max_pos, dh / 2, dh, (double)base);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_row_stats(int dtype, const void* x, int M, int d, float eps, float* r, int T, int32_t* lens_set,
                              int32_t* lens_bump, int32_t* pos_out, int T_max, int* zero_word, int* err,
                              cudaStream_t s) {

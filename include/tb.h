@@ -56,9 +56,10 @@ typedef enum {
   TB_ERR_TIMEOUT = 5        /* reserved for a host-side wait that ran out */
 } tb_status;
 
-/* TB_I8 is a KV-cache storage type only (tb_kvcache.dtype): int8 codes with a
- * per-row fp32 scale. */
-typedef enum { TB_F32 = 0, TB_BF16 = 1, TB_I8 = 2 } tb_dtype;
+/* TB_I8 and TB_E4M3 are KV-cache storage types only (tb_kvcache.dtype): int8
+ * codes with a per-row fp32 scale, and e4m3 codes with one fp32 scale per block
+ * of tokens and KV head (tb_kvcache_append_rope, tb_kvcache_attn). */
+typedef enum { TB_F32 = 0, TB_BF16 = 1, TB_I8 = 2, TB_E4M3 = 3 } tb_dtype;
 
 /* Bits of the device error word (tb_get_device_error). */
 #define TB_DEVERR_CACHE_FULL 1  /* a decode/append row found lens[b] + n > T_max; that row was skipped */
@@ -294,6 +295,101 @@ TB_API tb_status tb_stack_prefill(const tb_block_cfg *cfg, int32_t L, const void
 TB_API tb_status tb_stack_decode(const tb_block_cfg *cfg, int32_t L, const void *const *packed, const void *x,
                                  void *y, int32_t y_dtype, const tb_kvcache *kvs, void *ws, size_t ws_bytes,
                                  void *stream);
+
+/* ---- Several tokens over a cache that already holds some ----
+ * The block's prefill starts from an empty cache and its decode step takes one
+ * token.  These calls take n tokens per sequence (a chunk of a prompt, drafted
+ * tokens, one token) from the caller's own projection: append their rows with
+ * the rotation applied on the way, then attend over the cache.
+ *
+ * Cache layouts: contiguous or paged, in TB_F32 or TB_BF16 as above, or
+ *  TB_E4M3, 8-bit floating-point codes (4 exponent bits, 3 mantissa bits, no
+ *  infinity) with one power-of-two fp32 scale per block of tokens and KV head:
+ *    contiguous: k, v codes [B, Hkv, T_max, dh]; page_size is the block, a
+ *                multiple of 16 that divides T_max; k_scale, v_scale
+ *                [B, Hkv, T_max / page_size].
+ *    paged:      k, v code pools [num_pages, Hkv, page_size, dh]; a block is a
+ *                page; k_scale, v_scale [num_pages, Hkv].
+ *    A row x of a block of scale s is stored as the codes of x / s, rounded to
+ *    nearest even, and reads back as code·s.  s = 2^e with e the smallest
+ *    integer for which the block's largest finite |x| is at most 448·2^e, held
+ *    to [-24, 60]; larger finite values saturate at ±448·2^60, infinities and
+ *    NaN are stored as NaN.
+ * TB_I8 caches are TB_ERR_UNSUPPORTED here. */
+
+/* The rotation table of tb_kvcache_append_rope: table [max_pos, dh/2, 2] fp32
+ * (device) receives (cos, sin) of t·base^(-2i/dh) for position t and pair i,
+ * the angle formed in fp64. */
+TB_API tb_status tb_rope_table(int32_t dh, int32_t max_pos, float base, float* table, void* stream);
+
+/* The new rows of a tb_kvcache_append_rope call.  q, k, v hold unrotated rows
+ * [B, n, heads, dh] of TB_BF16 (TB_F32 for a TB_F32 cache); a token's heads are
+ * dense, tokens are *_tok elements apart and sequences *_seq elements, so the
+ * three may be column blocks of one fused projection.  Pointers 16-byte
+ * aligned, strides multiples of 8 elements.
+ *  q     : H heads, or NULL; q_out (dense [B, n, H, dh], may be q itself where
+ *          q is dense) receives them rotated.
+ *  start : device int32 [B], the position of each sequence's first new row, or
+ *          NULL for lens.  A start below lens drops the rows from it on (taking
+ *          drafted tokens back); start may not overlap lens.
+ *  n_new : device int32 [B], how many of the n rows of each sequence count (the
+ *          others are padding: not stored, their q_out rows left as they were),
+ *          or NULL for all n.  Values are held to [0, n]. */
+typedef struct {
+  const void *q, *k, *v;
+  void* q_out;
+  int64_t q_tok, q_seq, k_tok, k_seq, v_tok, v_seq;
+  int32_t H, n;
+  const int32_t *start, *n_new;
+} tb_append_rows;
+
+/* Append rows with the rotation applied: row i of sequence b sits at position
+ * p = start[b] + i; adjacent pairs (2i, 2i+1) of its q and k are turned by row p
+ * of `rope` (tb_rope_table's, of max_pos >= kv->T_max rows), in fp32, and
+ * rounded once to the stored type; v is stored as it is.  lens[b] becomes
+ * start[b] + n_new[b].  A sequence that does not fit (start < 0 or start + n_new
+ * > T_max) sets TB_DEVERR_CACHE_FULL and keeps its cache, length and q_out; a
+ * page id outside the pool sets TB_DEVERR_BAD_PAGE and its rows are not stored.
+ * An e4m3 block that already holds rows of the sequence (a start inside it)
+ * keeps the larger of its scale and the one the new rows need; where that
+ * grows, the older codes of the block are rewritten for it (x / s again, from
+ * the values they stand for).  Otherwise a block's scale is that of the new
+ * rows.  Pages that a call writes may belong to one sequence only. */
+TB_API tb_status tb_kvcache_append_rope(const tb_kvcache* kv, const tb_append_rows* rows, const float* rope,
+                                        int32_t max_pos, void* stream);
+
+/* Attention over a cache.
+ *  H, Hkv, dh : H a multiple of Hkv, H/Hkv 1, 2, 4 or 8; dh 64 or 128 (TB_F32
+ *               also 16 and 32).
+ *  dtype      : of q and o: TB_F32 for a TB_F32 cache, else TB_BF16.
+ *  window W, sinks S : the query at position p sees key j iff j <= p and
+ *               (W = 0 or j > p - W or j < S): its W most recent positions, its
+ *               own included, and the first S.  Both non-negative.
+ *  scale      : of the scores; 0 stands for 1/sqrt(dh). */
+typedef struct {
+  int32_t H, Hkv, dh, dtype, window, sinks;
+  float scale;
+} tb_attn_cfg;
+
+/* Workspace of tb_kvcache_attn for n query tokens per sequence over kv (the
+ * layout and sizes of kv are read, not its tensors; it may be 0). */
+TB_API size_t tb_kvcache_attn_workspace_bytes(const tb_attn_cfg* cfg, const tb_kvcache* kv, int32_t n);
+
+/* o[b, i, h] = sum_j softmax_j(scale q·k_j) v_j over the keys the query sees,
+ * for the last tokens of each sequence: query i of sequence b sits at position
+ * lens[b] - n_new[b] + i (the tokens just appended).
+ *  q, o  : device, dense [B, n, H, dh] of cfg->dtype; q rotated; o may be q.
+ *  n_new : as in tb_append_rows; o rows of padding are left as they were.
+ *  ws    : 256-byte aligned workspace; calls that may overlap need their own.
+ * A query that sees no key (a negative position) gets zeros.  Rows no query of
+ * the call sees are not read: what they hold, and the pages they lie in, do not
+ * matter; a visible row in a page outside the pool counts as zeros and sets
+ * TB_DEVERR_BAD_PAGE.  lens[b] above T_max counts as T_max and sets
+ * TB_DEVERR_CACHE_FULL.  A non-finite value in a row reaches those queries only
+ * that see the row.  Scores, softmax statistics and sums are fp32; for TB_BF16
+ * the weights enter their product with v rounded to bf16, over e4m3 to fp16. */
+TB_API tb_status tb_kvcache_attn(const tb_attn_cfg* cfg, const void* q, const tb_kvcache* kv, const int32_t* n_new,
+                                 int32_t n, void* o, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
