@@ -81,8 +81,24 @@ __device__ __forceinline__ SeqRange seq_range(const AttnArgs& a, int b) {
   r.first = r.len - r.nn;
   return r;
 }
-// Keys a query at position p sees: [0, sink_end) and [win_lo, p], disjoint.
+// A query at position p sees keys [win_lo, p] and, below win_lo, the sinks.
 __device__ __forceinline__ int win_lo(int p, int window) { return window > 0 && p >= window ? p - window + 1 : 0; }
+
+// The runs of `unit` keys (aligned) that hold every key some query of a
+// sequence sees: the first `ns`, then from `wl` on; `count` in all, none beyond
+// the sequence.  Run g of the list starts at key run_key(r, g).
+struct KeyRuns {
+  int ns, wl, count;
+};
+__device__ __forceinline__ KeyRuns key_runs(int len, int first, int window, int sinks, int unit) {
+  KeyRuns r{0, 0, 0};
+  if (len <= 0) return r;
+  r.wl = win_lo(first, window) / unit;
+  r.ns = min((min(sinks, len) + unit - 1) / unit, r.wl);
+  r.count = r.ns + (len - 1) / unit - r.wl + 1;
+  return r;
+}
+__device__ __forceinline__ int run_index(const KeyRuns& r, int g) { return g < r.ns ? g : g - r.ns + r.wl; }
 
 // cache_append.cu
 struct AppendArgs {
@@ -95,6 +111,75 @@ struct AppendArgs {
   const float2* rope;
 };
 cudaError_t launch_append_rope(const AppendArgs& a, cudaStream_t s);
+
+// cache_attn_few.cu: up to kFewRows query rows (tokens x heads) per KV head,
+// 16-bit queries over bf16 or e4m3 rows of dh 64 or 128.
+constexpr int kFewRows = 64;
+size_t cache_attn_few_workspace(const AttnArgs& a);
+cudaError_t launch_cache_attn_few(const AttnArgs& a, void* ws, cudaStream_t s);
+
+// One query row by one warp, as the formula reads: keys it does not see are not
+// touched at all.  q points to dh elements; every lane returns with
+// out[u] = o[lane + 32u].  fp32 queries, and rows whose fast result is not
+// finite (a weight of 0 times an infinity or NaN in a row that the query does
+// not see, or a value that really is not finite).
+__device__ __forceinline__ float cache_elem(const CacheView& c, const void* base, long long row, int e) {
+  if (c.dtype == TB_F32) return __ldg((const float*)base + row * c.dh + e);
+  if (c.dtype == TB_BF16) return to_f(((const bf16*)base)[row * c.dh + e]);
+  const uint8_t code = __ldg((const uint8_t*)base + row * c.dh + e);
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)code));
+  float f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(h));
+  return f;
+}
+template <typename TQ>
+__device__ __noinline__ void attend_row(const AttnArgs& a, int b, int hkv, int pos, const TQ* q, float (&out)[4]) {
+  const int lane = threadIdx.x & 31, dh = a.c.dh;
+  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const int lo = win_lo(pos, a.window);
+  const int sinks = min(a.sinks, lo);
+  const int nkeys = pos < 0 ? 0 : sinks + pos + 1 - lo;
+  for (int j0 = 0; j0 < nkeys; j0 += 32) {
+    const int jj = j0 + lane;
+    const bool in = jj < nkeys;
+    const int j = in ? (jj < sinks ? jj : jj - sinks + lo) : 0;
+    long long sc = 0;
+    const long long row = in ? cache_row(a.c, b, hkv, j, &sc) : -1;
+    float s = 0.f;
+    if (row >= 0) {
+      for (int e = 0; e < dh; ++e) s = fmaf(to_f(q[e]), cache_elem(a.c, a.c.k, row, e), s);
+      if (a.c.dtype == TB_E4M3) s *= a.c.ks[sc];
+    }
+    s = in ? s * a.scale_log2 : -INFINITY;
+    float mx = s;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float mn = fmaxf(m, mx);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const float f = exp2f(m - base);
+    const float p = in ? exp2f(s - base) : 0.f;
+    m = mn;
+    l = l * f + warp_sum(p);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) acc[u] *= f;
+    const float vs = row >= 0 && a.c.dtype == TB_E4M3 ? a.c.vs[sc] : 1.f;
+    const int steps = min(32, nkeys - j0);
+    for (int k = 0; k < steps; ++k) {
+      const float pk = __shfl_sync(0xffffffffu, p, k) * __shfl_sync(0xffffffffu, vs, k);
+      const long long rk = __shfl_sync(0xffffffffu, row, k);
+      if (rk < 0) continue;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = lane + 32 * u;
+        if (e < dh) acc[u] = fmaf(pk, cache_elem(a.c, a.c.v, rk, e), acc[u]);
+      }
+    }
+  }
+  const bool none = l == 0.f;             // no visible key
+#pragma unroll
+  for (int u = 0; u < 4; ++u) out[u] = none ? 0.f : acc[u] / l;
+}
 
 // cache_attn.cu
 size_t cache_attn_workspace(const AttnArgs& a);

@@ -31,6 +31,8 @@ tb_status check_cache(const tb_kvcache* kv, bool tensors) {
   }
   if (kv->block_table) {
     if (kv->num_pages <= 0) return report(TB_ERR_INVALID_ARG, "num_pages must be positive");
+    if ((long long)kv->num_pages * kv->Hkv >= (1LL << 31) - 1)
+      return report(TB_ERR_UNSUPPORTED, "num_pages·Hkv above 2^31 - 2");
     if (!aligned4(kv->block_table)) return report(TB_ERR_INVALID_ARG, "block_table must be 4-byte aligned");
   }
   if (!tensors) return TB_OK;
@@ -188,15 +190,15 @@ tb_status tb_kvcache_attn(const tb_attn_cfg* cfg, const void* q, const tb_kvcach
   if (!q || !o) return report(TB_ERR_INVALID_ARG, "q and o must be non-NULL");
   if (!aligned16(q) || !aligned16(o) || !aligned4(n_new))
     return report(TB_ERR_INVALID_ARG, "q and o must be 16-byte aligned, n_new 4-byte");
-  int* err = device_error_word();
-  if (!err) return report(TB_ERR_CUDA, "cannot resolve the device error word");
-  AttnArgs a = attn_args(cfg, kv, n, err);
+  AttnArgs a = attn_args(cfg, kv, n, nullptr);
   a.q = q;
   a.o = o;
   a.n_new = n_new;
   const size_t need = cache_attn_workspace(a);
   if (need && (!ws || ((uintptr_t)ws & 255u) || ws_bytes < need))
     return report(TB_ERR_INVALID_ARG, "ws must be 256-byte aligned and hold %zu bytes (%zu)", need, ws_bytes);
+  a.c.err = device_error_word();
+  if (!a.c.err) return report(TB_ERR_CUDA, "cannot resolve the device error word");
   const cudaError_t e = launch_cache_attn(a, ws, (cudaStream_t)stream);
   return e == cudaSuccess ? TB_OK : report(TB_ERR_CUDA, "tb_kvcache_attn: %s", cudaGetErrorString(e));
 }

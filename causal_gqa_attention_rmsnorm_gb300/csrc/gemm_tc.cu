@@ -636,6 +636,23 @@ cudaError_t make_tmap_3d_u8(CUtensorMap* m, const void* base, uint64_t planes, u
                       box_cols, box_rows);
 }
 
+cudaError_t make_tmap_rows(CUtensorMap* m, int esize, const void* base, uint64_t planes, uint64_t rows, uint64_t cols,
+                           uint32_t box_cols, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const uint32_t bytes = box_cols * esize;
+  if (bytes != 64 && bytes != 128) return cudaErrorInvalidValue;
+  const cuuint64_t dims[3] = {cols, rows, planes};
+  const cuuint64_t strides[2] = {cols * esize, rows * cols * esize};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                        const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t gemm_tc_qkv(const void* A, const void* B, int M, int N, int K, const Dims& D, const QKVArgs& e,
                         cudaStream_t s) {
   const EpiQKV<bf16, true> epi{e, D.H, D.Hkv, D.dh, log2_dh(D.dh)};
