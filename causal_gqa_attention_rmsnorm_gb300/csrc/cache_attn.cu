@@ -30,18 +30,24 @@ __global__ void __launch_bounds__(256) k_attn_row(AttnArgs a) {
     if (lane + 32 * u < a.c.dh) ((TQ*)a.o)[(size_t)r * a.c.dh + lane + 32 * u] = from_f<TQ>(out[u]);
 }
 
-bool few(const AttnArgs& a) { return a.c.dtype != TB_F32 && a.n * (a.H / a.c.Hkv) <= kFewRows; }
-
 }  // namespace
 
-size_t cache_attn_workspace(const AttnArgs& a) { return few(a) ? cache_attn_few_workspace(a) : 0; }
+namespace {
+// fp32 queries: one warp per row; else by the rows that share a KV head.
+bool few(const AttnArgs& a) { return a.n * (a.H / a.c.Hkv) <= kFewRows; }
+}  // namespace
+
+size_t cache_attn_workspace(const AttnArgs& a) {
+  if (a.c.dtype == TB_F32) return 0;
+  return few(a) ? cache_attn_few_workspace(a) : cache_attn_many_workspace(a);
+}
 
 cudaError_t launch_cache_attn(const AttnArgs& a, void* ws, cudaStream_t s) {
-  if (few(a)) return launch_cache_attn_few(a, ws, s);
-  const long long rows = (long long)a.c.B * a.n * a.H;
-  const unsigned grid = (unsigned)((rows + 7) / 8);
-  if (a.c.dtype == TB_F32) return launch_pdl(k_attn_row<float>, dim3(grid), dim3(256), 0, s, a);
-  return launch_pdl(k_attn_row<bf16>, dim3(grid), dim3(256), 0, s, a);
+  if (a.c.dtype == TB_F32) {
+    const long long rows = (long long)a.c.B * a.n * a.H;
+    return launch_pdl(k_attn_row<float>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
+  }
+  return few(a) ? launch_cache_attn_few(a, ws, s) : launch_cache_attn_many(a, ws, s);
 }
 
 }  // namespace tb

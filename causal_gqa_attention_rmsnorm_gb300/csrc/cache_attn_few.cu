@@ -109,12 +109,6 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
-// Two pairs of codes to two fp16 pairs.
-__device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
 // 2^-e with x·2^-e in [0.5, 1) for a normal x > 0, held to normal powers of two; 1 otherwise.
 __device__ __forceinline__ float pow2_frame(float x) {
   if (!(x > 0.f)) return 1.f;
@@ -424,7 +418,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (r < nr) {
           const float2 v = sc[sl * C::RUNS + r];
           ks = v.x;
-          ve = (float)((int)(__float_as_uint(v.y) >> 23) - 127);
+          ve = scale_exp(v.y);
         }
       }
       const int key = run_index(kr, r0 + r) * kRun;
@@ -499,8 +493,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         const float p2 = ex2_approx(z[r][1][2 * i] - base), p3 = ex2_approx(z[r][1][2 * i + 1] - base);
         const float sum = (p0 + p1) + (p2 + p3);
         if constexpr (E4) {
-          const float inv = __uint_as_float((254u << 23) - __float_as_uint(sc[sl * C::RUNS + r].y));   // 1 / 2^e
-          l[i] = fmaf(sum, inv, l[i]);
+          l[i] = fmaf(sum, scale_inv(sc[sl * C::RUNS + r].y), l[i]);
         } else {
           l[i] += sum;
         }

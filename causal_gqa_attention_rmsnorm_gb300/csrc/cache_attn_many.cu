@@ -1,0 +1,1135 @@
+// Attention of many query rows over a bf16 or e4m3 cache on the 5th-generation
+// tensor cores: chunks of a prompt, and drafts of more rows than the streaming
+// kernel takes.
+//
+//   The n·G rows (tokens x query heads of a KV head, G = H/Hkv, token-major) of
+//   a (sequence, KV head) are packed into tiles of 128, so that every K/V tile
+//   staged in shared memory serves all heads of the group; a CTA works on two
+//   row tiles ("slots") over the same key tiles:
+//     S_g = Q_g·Kᵀ into tensor memory (M = 128, N = 128 keys), softmax in fp32
+//     by one thread per row, P back over S in 16 bits, O_g += P_g·V.
+//   Roles: warps 0..7 softmax (four per slot), warp 8 copies, warp 9 issues the
+//   MMAs; over e4m3 two more warps turn codes into fp16 tiles.  The MMA order
+//   per key tile is P·V of slot 0, S of slot 0 for the next tile, the same of
+//   slot 1, so that the tensor pipe works on one slot during the other's
+//   softmax.
+//
+//   Key tiles are 128 aligned keys: those with sinks, then those of the union of
+//   the two slots' windows, up to the last query; a slot sits out tiles that
+//   none of its rows sees.  Only tiles at a border are masked by element.  Rows
+//   of V that no query of the item sees are zeroed in shared memory (0·NaN is
+//   NaN inside an MMA), and pages that hold only such rows are not read.
+//
+//   Balance: an item (a pair of row tiles) costs its key tiles plus one; all
+//   items form one line that is cut into equal parts, one per CTA, whatever the
+//   lengths.  An item that a cut leaves whole is written out directly; pieces of
+//   a cut one leave (max, sum, O) in the workspace and k_many_merge joins them in
+//   order.  The line's prefix sums come from k_many_plan.
+//
+//   e4m3: TMA brings 32-key chunks of codes through a ring; a conversion warp
+//   writes them as fp16 (exact) into the swizzled K or V tile.  Queries become
+//   fp16 under a power of two per row.  K scales multiply the scores per 16
+//   keys; V scales 2^e enter the exponent, p' = 2^(z + e - m'), so that
+//   O = Σ p'·code and l = Σ p'·2^-e (see the streaming kernel).
+//
+// Rows whose result is not finite are computed once more by k_many_merge, key by
+// key, so that what a masked row holds never matters.
+#include <math.h>
+
+#include <algorithm>
+
+#include "cache.cuh"
+#include "gemm_tc.cuh"
+#include "sm100_ptx.cuh"
+
+namespace tb {
+namespace {
+
+using namespace ptx;
+
+constexpr int kBM = 128, kBN = 128;
+constexpr float kRescale = 8.f;
+constexpr int kChunk = 32;                     // keys per chunk of codes
+constexpr int kRaw = 8;                        // chunks in the ring: one K and one V tile
+constexpr int kScTiles = 8;                    // tiles whose block scales are kept
+
+template <int DH, bool E4> struct ManyCfg {
+  static constexpr int NB = DH / 64;                       // 64-column blocks of a 16-bit row
+  static constexpr uint32_t Q_BYTES = kBM * DH * 2;
+  static constexpr uint32_t KV_BYTES = kBN * DH * 2;
+  static constexpr uint32_t RAW = kChunk * DH;             // bytes of a chunk of codes
+  static constexpr uint32_t OFF_K = 2 * Q_BYTES;
+  static constexpr uint32_t OFF_V = OFF_K + 2 * KV_BYTES;
+  static constexpr uint32_t OFF_RAW = OFF_V + 2 * KV_BYTES;
+  static constexpr uint32_t OFF_SC = OFF_RAW + (E4 ? kRaw * RAW : 0);      // [kScTiles][16]: K, then V
+  static constexpr uint32_t OFF_BAR = OFF_SC + (E4 ? kScTiles * 64 : 0);
+  static constexpr size_t SMEM = OFF_BAR + 512 + 1024;
+  static constexpr uint32_t TMEM_O = 2 * kBN;
+  static constexpr int THREADS = E4 ? 384 : 320;
+};
+
+struct ManyArgs {
+  AttnArgs a;
+  int pairs;               // row-tile pairs of a sequence of n tokens
+  int tpt;                 // tokens per row tile: 128 / G
+  int n_cta;
+  int box;                 // keys per box
+  bool negate;             // the score scale is negative: the scores are negated, its magnitude applied
+  long long* pre;          // [B·pairs + 1] line position of (sequence, pair) within its KV head
+  uint8_t* flags;          // [B·Hkv·2·pairs] row tiles to look through again
+  float4* part;            // [2·n_cta][2][DH/4 + 1][128] pieces
+};
+
+// ---- items ------------------------------------------------------------------
+
+// One slot's row tile: `rows` rows of tokens tok0.., at positions p0 .. p1, and
+// the list positions it works on: [0, ia) and [ib, ic).
+struct SlotRange {
+  int tok0, rows, p0, p1, ia, ib, ic;
+  __device__ __forceinline__ bool on(int x) const { return x < ia || (x >= ib && x < ic); }
+  __device__ __forceinline__ int first_on(int t0, int t1) const {
+    if (t0 < min(ia, t1)) return t0;
+    const int f = max(t0, ib);
+    return f < min(ic, t1) ? f : -1;
+  }
+  __device__ __forceinline__ int last_on(int t0, int t1) const {
+    if (max(t0, ib) < min(ic, t1)) return min(ic, t1) - 1;
+    return t0 < min(ia, t1) ? min(ia, t1) - 1 : -1;
+  }
+};
+// A pair of row tiles: its key tiles (list position x is key tile x < ns ? x :
+// x - ns + wl), cnt of them; keys from `end` on and in [hid0, hid1) are hidden
+// from all its rows.
+struct Item {
+  SlotRange s0, s1;
+  int ns, wl, cnt, end, hid0, hid1;
+  __device__ __forceinline__ int tile(int x) const { return x < ns ? x : x - ns + wl; }
+};
+__device__ __forceinline__ SlotRange slot_range(const ManyArgs& m, const SeqRange& sr, int rt) {
+  SlotRange s{0, 0, 0, -1, 0, 0, 0};
+  s.tok0 = rt * m.tpt;
+  const int toks = min(m.tpt, sr.nn - s.tok0);
+  if (toks <= 0) return s;
+  s.rows = toks * (kBM / m.tpt);
+  s.p0 = sr.first + s.tok0;
+  s.p1 = s.p0 + toks - 1;
+  return s;
+}
+__device__ __forceinline__ void slot_list(SlotRange& s, const Item& it, const AttnArgs& a) {
+  if (s.rows == 0 || s.p1 < 0) {
+    s.ia = s.ib = s.ic = 0;
+    return;
+  }
+  const int hi = s.p1 / kBN, lo = win_lo(s.p0, a.window) / kBN;
+  const int sk = min((min(a.sinks, s.p1 + 1) + kBN - 1) / kBN, hi + 1);     // key tiles with sinks
+  s.ia = sk <= it.ns ? sk : (sk > it.wl ? sk - it.wl + it.ns : it.ns);
+  s.ib = lo - it.wl + it.ns;
+  s.ic = hi - it.wl + it.ns + 1;
+}
+__device__ __forceinline__ Item make_item(const ManyArgs& m, const SeqRange& sr, int p) {
+  const AttnArgs& a = m.a;
+  Item it{};
+  it.s0 = slot_range(m, sr, 2 * p);
+  it.s1 = slot_range(m, sr, 2 * p + 1);
+  const int last = it.s1.rows ? it.s1.p1 : it.s0.p1;
+  if (it.s0.rows == 0 || last < 0) return it;
+  it.hid1 = win_lo(it.s0.p0, a.window);
+  it.hid0 = min(a.sinks, it.hid1);
+  it.end = last + 1;
+  it.wl = it.hid1 / kBN;
+  it.ns = min((min(a.sinks, it.end) + kBN - 1) / kBN, it.wl);
+  it.cnt = it.ns + last / kBN - it.wl + 1;
+  slot_list(it.s0, it, a);
+  slot_list(it.s1, it, a);
+  return it;
+}
+// What an item costs on the line: its key tiles and one for its queries and
+// output; nothing without rows.
+__device__ __forceinline__ int item_cost(const ManyArgs& m, const SeqRange& sr, int p) {
+  const Item it = make_item(m, sr, p);
+  return it.s0.rows ? it.cnt + 1 : 0;
+}
+
+// Where line position x lies: sequence, KV head, pair and the item's start.
+struct Place {
+  int b, h, p;
+  long long start;
+};
+__device__ __forceinline__ Place find_item(const ManyArgs& m, long long x) {
+  Place r;
+  int lo = 0, hi = m.a.c.B - 1;
+  const int Hkv = m.a.c.Hkv;
+  while (lo < hi) {                              // the last sequence that starts at or before x
+    const int mid = (lo + hi + 1) >> 1;
+    if (m.pre[(size_t)mid * m.pairs] * Hkv <= x) lo = mid; else hi = mid - 1;
+  }
+  r.b = lo;
+  const long long* pb = m.pre + (size_t)lo * m.pairs;
+  const long long per = pb[m.pairs] - pb[0];     // positive: x lies inside the line
+  const long long off = x - pb[0] * Hkv;
+  r.h = (int)(off / per);
+  const long long in = off - r.h * per + pb[0];
+  lo = 0, hi = m.pairs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pb[mid] <= in) lo = mid; else hi = mid - 1;
+  }
+  r.p = lo;
+  r.start = pb[0] * Hkv + r.h * per + pb[lo] - pb[0];
+  return r;
+}
+// CTA c's part of the line.
+__device__ __forceinline__ long long cut(const ManyArgs& m, long long total, int c) {
+  return total * c / m.n_cta;
+}
+// The key tiles [t0, t1) of the item at [start, start + cnt + 1) in the part [x0, x1).
+__device__ __forceinline__ int2 piece_of(long long start, int cnt, long long x0, long long x1) {
+  const long long t0 = max(x0 - start, 1LL) - 1, t1 = min(x1 - start, (long long)cnt + 1) - 1;
+  return make_int2((int)t0, (int)max(t0, t1));
+}
+
+// The pieces of a CTA, in order; each role walks them alike.
+struct Pieces {
+  const ManyArgs& m;
+  long long x, x1, x0;
+  Place at;
+  Item it;
+  SeqRange sr;
+  int t0, t1, where;          // where: -1 the whole item, else the piece's slot in the workspace
+  __device__ Pieces(const ManyArgs& m_, long long a, long long b) : m(m_), x(a), x1(b), x0(a) {}
+  __device__ __forceinline__ bool next() {
+    while (x < x1) {
+      at = find_item(m, x);
+      sr = seq_range(m.a, at.b);
+      it = make_item(m, sr, at.p);
+      const int2 t = piece_of(at.start, it.cnt, x, x1);
+      const bool begins = x == at.start;
+      x = min(x1, at.start + it.cnt + 1);
+      t0 = t.x;
+      t1 = t.y;
+      if (t0 == 0 && t1 == it.cnt && (it.cnt > 0 || begins)) {
+        where = -1;
+        return true;
+      }
+      if (t0 < t1) {
+        where = 2 * (int)blockIdx.x + (begins ? 1 : 0);
+        return true;
+      }
+    }
+    return false;
+  }
+};
+
+// pre[e] for e = (sequence, pair) in order, and the flags cleared; one CTA.
+__global__ void __launch_bounds__(1024) k_many_plan(const ManyArgs m, int n_flag_words) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ long long warp_sum_s[32];
+  __shared__ long long carry_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < n_flag_words; i += 1024) reinterpret_cast<uint32_t*>(m.flags)[i] = 0u;
+  if (tid == 0) carry_s = 0;
+  __syncthreads();
+  const int E = m.a.c.B * m.pairs;
+  for (int e0 = 0; e0 < E; e0 += 1024) {
+    const int e = e0 + tid;
+    long long v = 0;
+    if (e < E) {
+      const int b = e / m.pairs;
+      v = item_cost(m, seq_range(m.a, b), e - b * m.pairs);
+    }
+    long long inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) warp_sum_s[warp] = inc;
+    __syncthreads();
+    long long base = carry_s;
+    for (int i = 0; i < warp; ++i) base += warp_sum_s[i];
+    if (e < E) m.pre[e] = base + inc - v;
+    if (e == E - 1) m.pre[E] = base + inc;
+    __syncthreads();
+    if (tid == 1023) carry_s = base + inc;
+    __syncthreads();
+  }
+}
+
+// ---- the kernel ---------------------------------------------------------------
+
+__device__ __forceinline__ void tma_load_4d(const CUtensorMap* m, void* dst, uint64_t* bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+template <bool E4>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t d;
+  if constexpr (E4)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float pow2_frame(float x) {
+  if (!(x > 0.f)) return 1.f;
+  const int e = max(-126, min(126, (int)((__float_as_uint(x) >> 23) & 0xffu) - 126));
+  return __uint_as_float((uint32_t)(127 - e) << 23);
+}
+// Instruction descriptor, kind::f16 with fp16 (E4) or bf16 operands, fp32 sums.
+template <bool E4>
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn) {
+  return idesc_bf16(M, N, false, b_mn) & ~(E4 ? (1u << 7 | 1u << 10) : 0u);
+}
+
+template <int DH, bool E4>
+__global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
+    k_attn_many(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const ManyArgs m) {
+  pdl_trigger();
+  using C = ManyCfg<DH, E4>;
+  const AttnArgs& a = m.a;
+  int* err = a.c.err;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* q_ready = bars + 2;      // E4: the queries are fp16
+  uint64_t* drain = bars + 3;
+  uint64_t* k_full = bars + 4;       // [2]
+  uint64_t* k_empty = bars + 6;
+  uint64_t* v_full = bars + 8;
+  uint64_t* v_empty = bars + 10;
+  uint64_t* s_full = bars + 12;      // [slot]
+  uint64_t* p_full = bars + 14;
+  uint64_t* pv_done = bars + 16;
+  uint64_t* o_full = bars + 18;
+  uint64_t* raw_full = bars + 20;    // [kRaw]
+  uint64_t* raw_empty = bars + 28;   // [kRaw]
+  uint64_t* sc_full = bars + 36;     // [kScTiles]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 44);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* sc = reinterpret_cast<float*>(smem + C::OFF_SC);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(q_ready, 8);
+    mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], E4 ? kBN / kChunk : 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], E4 ? kBN / kChunk : 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&o_full[i], 1);
+    }
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 1);
+    }
+    for (int i = 0; i < kScTiles; ++i) mbar_init(&sc_full[i], 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();                                   // the plan, and whatever wrote q and the cache
+  const long long total = m.pre[(size_t)a.c.B * m.pairs] * a.c.Hkv;
+  const long long x0 = cut(m, total, blockIdx.x), x1 = cut(m, total, blockIdx.x + 1);
+  const int G = kBM / m.tpt;
+
+  if (warp == 8) {
+    // ---------------- copies ----------------
+    int nq = 0, nt = 0;                         // pieces with queries, key tiles issued
+    int nraw = 0;                               // E4: chunks issued
+    bool ok = true;
+    Pieces pc(m, x0, x1);
+    while (ok && pc.next()) {
+      if (pc.t0 == pc.t1) continue;             // rows without keys
+      const Item& it = pc.it;
+      if (nq > 0 && !mbar_wait_warp(q_empty, (nq - 1) & 1, abort_flag, err)) break;
+      if (lane == 0) {
+        const int slots = it.s1.rows ? 2 : 1;
+        fence_proxy_async();                    // the queries were rewritten in place (E4)
+        mbar_arrive_expect_tx(q_full, slots * C::Q_BYTES);
+        for (int g = 0; g < slots; ++g)
+#pragma unroll
+          for (int blk = 0; blk < C::NB; ++blk)
+            tma_load_4d(&tmQ, smem + g * C::Q_BYTES + blk * kBM * 128, q_full, blk * 64, pc.at.h * G,
+                        g ? it.s1.tok0 : it.s0.tok0, pc.at.b);
+      }
+      __syncwarp();
+      ++nq;
+      // The page ids of a tile are read two tiles ahead, its scales one tile
+      // ahead: lane i, box i of the tile (E4: run i of 16 keys).
+      const int unit = E4 ? 16 : m.box;
+      const bool mine = lane < kBN / unit;
+      auto seen_at = [&](int key, int n) { return key < it.end && !(key >= it.hid0 && key + n <= it.hid1); };
+      auto page_ahead = [&](int x) {
+        if (x >= pc.t1 || !mine) return -1;
+        const int key = it.tile(x) * kBN + lane * unit;
+        return a.c.bt && seen_at(key, unit) ? a.c.bt[(size_t)pc.at.b * a.c.per + key / a.c.ps] : 0;
+      };
+      // the plane of a tile's keys (-1: not read), and the block scales
+      auto plane_of = [&](int x, int page, float& ks, float& vs) {
+        ks = vs = 1.f;
+        if (x >= pc.t1 || !mine) return -1;
+        const int key = it.tile(x) * kBN + lane * unit;
+        if (!seen_at(key, unit)) return -1;
+        int plane = pc.at.b * a.c.Hkv + pc.at.h;
+        size_t si = (size_t)plane * a.c.per + (E4 ? key / a.c.ps : 0);
+        if (a.c.bt) {
+          if (page < 0 || page >= a.c.num_pages) {
+            atomicOr(err, TB_DEVERR_BAD_PAGE);
+            return a.c.num_pages * a.c.Hkv;     // outside the pool: the copies read zeros
+          }
+          plane = page * a.c.Hkv + pc.at.h;
+          si = plane;
+        }
+        if constexpr (E4) {
+          ks = __ldg(a.c.ks + si);
+          vs = __ldg(a.c.vs + si);
+        }
+        return plane;
+      };
+      int page2 = page_ahead(pc.t0), plane1;
+      float ks1, vs1;
+      plane1 = plane_of(pc.t0, page2, ks1, vs1);
+      page2 = page_ahead(pc.t0 + 1);
+      for (int x = pc.t0; ok && x < pc.t1; ++x, ++nt) {
+        const int st = nt & 1;
+        const uint32_t ph = (nt >> 1) & 1;
+        const int key = it.tile(x) * kBN + lane * unit;
+        const int plane = plane1;
+        const float ks = ks1, vs = vs1;
+        plane1 = plane_of(x + 1, page2, ks1, vs1);
+        page2 = page_ahead(x + 2);
+        const bool want = plane >= 0;
+        const int y = a.c.bt ? key % a.c.ps : key;
+        if constexpr (!E4) {
+          const uint32_t loads = __ballot_sync(0xffffffffu, want);
+          const uint32_t bytes = (uint32_t)__popc(loads) * m.box * DH * 2;
+          if (!mbar_wait_warp(&k_empty[st], ph ^ 1u, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&k_full[st], bytes);
+          __syncwarp();
+          if (want) {
+#pragma unroll
+            for (int blk = 0; blk < C::NB; ++blk)
+              tma_load_3d(&tmK, smem + C::OFF_K + st * C::KV_BYTES + blk * kBN * 128 + lane * unit * 128, &k_full[st],
+                          blk * 64, y, plane);
+          }
+          if (!mbar_wait_warp(&v_empty[st], ph ^ 1u, abort_flag, err)) {
+            ok = false;
+            // the K boxes just issued land before the CTA ends
+            volatile int no_abort = 0;
+            mbar_wait(&k_full[st], ph, &no_abort, err);
+            break;
+          }
+          if (lane == 0) {
+            fence_proxy_async();                // rows zeroed in place, before the copy
+            mbar_arrive_expect_tx(&v_full[st], bytes);
+          }
+          __syncwarp();
+          if (want) {
+#pragma unroll
+            for (int blk = 0; blk < C::NB; ++blk)
+              tma_load_3d(&tmV, smem + C::OFF_V + st * C::KV_BYTES + blk * kBN * 128 + lane * unit * 128, &v_full[st],
+                          blk * 64, y, plane);
+          }
+        } else {
+          const int sl = nt % kScTiles;
+          if (mine) {
+            sc[sl * 16 + lane] = ks;
+            sc[sl * 16 + 8 + lane] = vs;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[sl]);
+          // a box is issued by the lane of its first run; with boxes of 32 keys
+          // a box whose first run alone is hidden is issued all the same
+          const int rpb = m.box / 16;
+          const uint32_t any = __ballot_sync(0xffffffffu, want);
+          const bool lead = mine && lane % rpb == 0;
+          const bool go = lead && ((any >> lane) & ((1u << rpb) - 1u));
+          const int zp = rpb == 2 ? __shfl_sync(0xffffffffu, plane, (lane | 1) & 7) : plane;
+          const int z = plane >= 0 ? plane : zp;
+          const uint32_t loads = __ballot_sync(0xffffffffu, go);
+#pragma unroll 1
+          for (int half = 0; half < 2 && ok; ++half)
+            for (int ch = 0; ch < kBN / kChunk; ++ch, ++nraw) {
+              const int rs = nraw % kRaw;
+              if (!mbar_wait_warp(&raw_empty[rs], ((nraw / kRaw) & 1) ^ 1u, abort_flag, err)) {
+                ok = false;
+                break;
+              }
+              const uint32_t in = (loads >> (2 * ch)) & 3u;      // runs 2ch, 2ch + 1 lead a box
+              if (lane == 0)
+                mbar_arrive_expect_tx(&raw_full[rs], (uint32_t)__popc(in) * m.box * DH);
+              __syncwarp();
+              if (go && (lane >> 1) == ch)
+                tma_load_3d(half ? &tmV : &tmK, smem + C::OFF_RAW + rs * C::RAW + (lane & 1) * 16 * DH, &raw_full[rs],
+                            0, y, z);
+              __syncwarp();
+            }
+        }
+      }
+    }
+    // every copy issued must land before the CTA may exit
+    __syncwarp();
+    if (lane == 0) {
+      volatile int no_abort = 0;
+      if (nq > 0) mbar_wait(q_full, (nq - 1) & 1, &no_abort, err);
+      if constexpr (E4) {
+        for (int t = max(0, nraw - kRaw); t < nraw; ++t)
+          mbar_wait(&raw_full[t % kRaw], (t / kRaw) & 1, &no_abort, err);
+      } else {
+        for (int t = max(0, nt - 2); t < nt; ++t) {
+          mbar_wait(&k_full[t & 1], (t >> 1) & 1, &no_abort, err);
+          mbar_wait(&v_full[t & 1], (t >> 1) & 1, &no_abort, err);
+        }
+      }
+    }
+  } else if (warp == 9) {
+    // ---------------- MMA issue ----------------
+    constexpr uint32_t id_qk = idesc<E4>(kBM, kBN, false), id_pv = idesc<E4>(kBM, DH, true);
+    const uint32_t sQ = smem_u32(smem);
+    const uint64_t dq0 = desc_kmajor_sw128(sQ), dq1 = desc_kmajor_sw128(sQ + C::Q_BYTES);
+    const uint64_t dk0 = desc_kmajor_sw128(sQ + C::OFF_K), dk1 = desc_kmajor_sw128(sQ + C::OFF_K + C::KV_BYTES);
+    const uint64_t dv0 = desc_mnmajor_sw128(sQ + C::OFF_V, kBN * 128, 1024);
+    const uint64_t dv1 = desc_mnmajor_sw128(sQ + C::OFF_V + C::KV_BYTES, kBN * 128, 1024);
+    auto issue_s = [&](int g, int t) {
+      if (lane == 0) {
+        mma_tile_ss<DH / 16>(tmem + g * kBN, g ? dq1 : dq0, (t & 1) ? dk1 : dk0, id_qk);
+        mma_commit(&s_full[g]);
+      }
+    };
+    auto issue_pv = [&](int g, int t, bool acc) {
+      if (lane == 0) {
+        mma_tile_ts128(tmem + C::TMEM_O + g * DH, tmem + g * kBN, (t & 1) ? dv1 : dv0, id_pv, acc ? 1u : 0u);
+        mma_commit(&pv_done[g]);
+      }
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (lane == 0) mma_commit(bar);
+    };
+    int kc = 0, nq = 0, c0 = 0, c1 = 0;
+    bool ok = true;
+    Pieces pc(m, x0, x1);
+    while (ok && pc.next()) {
+      if (pc.t0 == pc.t1) continue;
+      const Item& it = pc.it;
+      const int nt = pc.t1 - pc.t0;
+      const int f0 = it.s0.first_on(pc.t0, pc.t1), l0 = it.s0.last_on(pc.t0, pc.t1);
+      const int f1 = it.s1.first_on(pc.t0, pc.t1), l1 = it.s1.last_on(pc.t0, pc.t1);
+      if (!mbar_wait_warp(E4 ? q_ready : q_full, nq & 1, abort_flag, err) ||
+          !mbar_wait_warp(&k_full[kc & 1], (kc >> 1) & 1, abort_flag, err))
+        break;
+      ++nq;
+      tc_fence_after();
+      if (it.s0.on(pc.t0)) issue_s(0, kc);
+      if (it.s1.on(pc.t0)) issue_s(1, kc);
+      commit(&k_empty[kc & 1]);
+      if (nt == 1) commit(q_empty);
+      for (int jj = 0; jj < nt; ++jj) {
+        const int t = kc + jj, x = pc.t0 + jj;
+        const bool next = jj + 1 < nt;
+        if (!mbar_wait_warp(&v_full[t & 1], (t >> 1) & 1, abort_flag, err)) {
+          ok = false;
+          break;
+        }
+        if constexpr (!E4) {
+          // v rows that no row of the item sees
+          const int key = it.tile(x) * kBN;
+          if (key + kBN > it.end || (key < it.hid1 && key + kBN > it.hid0)) {
+            uint8_t* vt = smem + C::OFF_V + (t & 1) * C::KV_BYTES;
+            for (int r = lane; r < kBN; r += 32) {
+              const int j = key + r;
+              if (j < it.end && !(j >= it.hid0 && j < it.hid1)) continue;
+#pragma unroll
+              for (int i = 0; i < C::NB * 8; ++i)
+                *reinterpret_cast<uint4*>(vt + (i >> 3) * kBN * 128 + r * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async();
+            __syncwarp();
+          }
+        }
+        if (it.s0.on(x)) {
+          if (!mbar_wait_warp(&p_full[0], c0 & 1, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          ++c0;
+          tc_fence_after();
+          issue_pv(0, t, x != f0);
+          if (x == l0) commit(&o_full[0]);
+        }
+        if (next) {
+          if (!mbar_wait_warp(&k_full[(t + 1) & 1], ((t + 1) >> 1) & 1, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (it.s0.on(x + 1)) issue_s(0, t + 1);
+        }
+        if (it.s1.on(x)) {
+          if (!mbar_wait_warp(&p_full[1], c1 & 1, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          ++c1;
+          tc_fence_after();
+          issue_pv(1, t, x != f1);
+          if (x == l1) commit(&o_full[1]);
+        }
+        if (next) {
+          if (it.s1.on(x + 1)) issue_s(1, t + 1);
+          commit(&k_empty[(t + 1) & 1]);
+          if (jj + 2 == nt) commit(q_empty);
+        }
+        commit(&v_empty[t & 1]);
+      }
+      kc += nt;
+    }
+    commit(drain);
+    volatile int no_abort = 0;
+    mbar_wait_warp(drain, 0, &no_abort, err);
+  } else if (warp >= 10) {
+    // ---------------- codes to fp16 (E4): warp 10 takes even chunks, warp 11 odd ones ----------------
+    if constexpr (E4) {
+      const int me = warp - 10;
+      int nt = 0;
+      bool ok = true;
+      Pieces pc(m, x0, x1);
+      while (ok && pc.next()) {
+        const Item& it = pc.it;
+        for (int x = pc.t0; ok && x < pc.t1; ++x, ++nt) {
+          const int st = nt & 1;
+          const uint32_t ph = (nt >> 1) & 1;
+          const int tile_key = it.tile(x) * kBN;
+#pragma unroll 1
+          for (int q = me; q < 2 * kBN / kChunk; q += 2) {
+            const int half = q / (kBN / kChunk), ch = q % (kBN / kChunk);
+            const int rs = q;                                    // kRaw chunks: one tile of K and V
+            static_assert(kRaw == 2 * kBN / kChunk, "a ring round per tile");
+            if (!mbar_wait_warp(half ? &v_empty[st] : &k_empty[st], ph ^ 1u, abort_flag, err) ||
+                !mbar_wait_warp(&raw_full[rs], nt & 1, abort_flag, err)) {
+              ok = false;
+              break;
+            }
+            const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW;
+            uint8_t* dst = smem + (half ? C::OFF_V : C::OFF_K) + st * C::KV_BYTES;
+            const int key0 = tile_key + ch * kChunk;
+            const bool border = half && (key0 + kChunk > it.end || (key0 < it.hid1 && key0 + kChunk > it.hid0));
+            // 16-byte pieces of 16 codes, PPR per row.  The four lanes of a half
+            // quarter-warp take one half of a row, the next four the other half
+            // of its neighbour, so that reads and writes spread over the banks.
+            constexpr int PPR = DH / 16, RPS = 32 / PPR, STEPS = kChunk / RPS;
+            int r0 = lane / PPR, pc0 = lane % PPR;
+            if constexpr (PPR == 8) {
+              const int r2 = lane >> 3, c = lane & 7;
+              r0 = (r2 & ~1) + (c >> 2);
+              pc0 = (c & 3) + 4 * ((r2 & 1) ^ (c >> 2));
+            }
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+              const int row = i * RPS + r0;
+              uint4 w = *reinterpret_cast<const uint4*>(raw + row * DH + pc0 * 16);
+              if (border) {
+                const int j = key0 + row;
+                if (j >= it.end || (j >= it.hid0 && j < it.hid1)) w = make_uint4(0u, 0u, 0u, 0u);
+              }
+              uint4 lo, hi;
+              codes4(w.x, lo.x, lo.y);
+              codes4(w.y, lo.z, lo.w);
+              codes4(w.z, hi.x, hi.y);
+              codes4(w.w, hi.z, hi.w);
+              const int r = ch * kChunk + row, c = 2 * pc0;             // 16-byte piece of the fp16 row
+              uint8_t* base = dst + (c >> 3) * kBN * 128 + r * 128;
+              *reinterpret_cast<uint4*>(base + (((c ^ r) & 7) << 4)) = lo;
+              *reinterpret_cast<uint4*>(base + ((((c + 1) ^ r) & 7) << 4)) = hi;
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(half ? &v_full[st] : &k_full[st]);
+              mbar_arrive(&raw_empty[rs]);
+            }
+          }
+        }
+      }
+    }
+  } else {
+    // ---------------- softmax: one query row per thread ----------------
+    const int g = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t s_col = lane_base + g * kBN, o_col = lane_base + C::TMEM_O + g * DH;
+    int c = 0, nt = 0, nq = 0, no = 0;          // this slot's tiles; key tiles, pieces with keys, outputs
+    bool ok = true;
+    Pieces pc(m, x0, x1);
+    while (ok && pc.next()) {
+      const Item& it = pc.it;
+      const SlotRange s_r = g ? it.s1 : it.s0;
+      const int tok = s_r.tok0 + r / G;
+      const bool valid = r < s_r.rows;
+      const int qp = valid ? s_r.p0 + r / G : -1;
+      const int f_on = s_r.first_on(pc.t0, pc.t1), l_on = s_r.last_on(pc.t0, pc.t1);
+      float zs = fabsf(a.scale_log2);
+      if constexpr (E4) {
+        // this row of Q, as fp16 with its largest element in [0.5, 1)
+        if (pc.t0 < pc.t1) {
+          if (!mbar_wait_warp(q_full, nq & 1, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          if (s_r.rows) {
+            uint8_t* qrow = smem + g * C::Q_BYTES + r * 128;
+            uint4 w[C::NB * 8];
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < C::NB * 8; ++i) {
+              w[i] = *reinterpret_cast<const uint4*>(qrow + (i >> 3) * kBM * 128 + (((i ^ r) & 7) << 4));
+              const uint32_t* u = &w[i].x;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xffff0000u))));
+            }
+            const float fr = pow2_frame(amax);
+            zs /= fr;                           // exact
+#pragma unroll
+            for (int i = 0; i < C::NB * 8; ++i) {
+              uint32_t* u = &w[i].x;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                u[j] = pack16<true>(__uint_as_float(u[j] << 16) * fr, __uint_as_float(u[j] & 0xffff0000u) * fr);
+              *reinterpret_cast<uint4*>(qrow + (i >> 3) * kBM * 128 + (((i ^ r) & 7) << 4)) = w[i];
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_ready);
+        }
+      }
+      if (pc.t0 < pc.t1) ++nq;
+      float m_used = -INFINITY, l = 0.f;
+      const int wlo = win_lo(qp, a.window);
+      for (int x = pc.t0; x < pc.t1; ++x) {
+        const int tn = nt + x - pc.t0;          // the CTA's running key tile
+        if (!s_r.on(x)) continue;
+        if (!mbar_wait_warp(&s_full[g], c & 1, abort_flag, err)) {
+          ok = false;
+          break;
+        }
+        if constexpr (E4) {
+          if (!mbar_wait_warp(&sc_full[tn % kScTiles], (tn / kScTiles) & 1, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+        }
+        tc_fence_after();
+        float s[kBN];
+#pragma unroll
+        for (int cc = 0; cc < kBN; cc += 16) {
+          uint32_t u[16];
+          tmem_ld16(s_col + cc, u);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[cc + i] = __uint_as_float(u[i]);
+        }
+        tmem_wait_ld();
+        if (m.negate) {
+#pragma unroll
+          for (int cc = 0; cc < kBN; ++cc) s[cc] = -s[cc];
+        }
+        const int key = it.tile(x) * kBN;
+        if (key + kBN - 1 > s_r.p0) {           // keys ahead of a row
+          const int lim = qp - key;
+#pragma unroll
+          for (int cc = 0; cc < kBN; ++cc)
+            if (cc > lim) s[cc] = -INFINITY;
+        }
+        if (key < win_lo(s_r.p1, a.window) && key + kBN > a.sinks) {       // keys behind a row's window
+          const int wl = wlo - key, sl = a.sinks - key;
+#pragma unroll
+          for (int cc = 0; cc < kBN; ++cc)
+            if (cc < wl && cc >= sl) s[cc] = -INFINITY;
+        }
+        const float* scp = sc + (tn % kScTiles) * 16;
+        float mx;
+        if constexpr (!E4) {
+          float m4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = fmaxf(s[2 * i], s[2 * i + 1]);
+#pragma unroll
+            for (int cc = 8 + 2 * i; cc < kBN; cc += 8) v = fmax3(v, s[cc], s[cc + 1]);
+            m4[i] = v;
+          }
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * zs;
+        } else {
+          mx = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float v0 = fmaxf(s[16 * q], s[16 * q + 1]), v1 = fmaxf(s[16 * q + 2], s[16 * q + 3]);
+#pragma unroll
+            for (int i = 4; i < 16; i += 4) {
+              v0 = fmax3(v0, s[16 * q + i], s[16 * q + i + 1]);
+              v1 = fmax3(v1, s[16 * q + i + 2], s[16 * q + i + 3]);
+            }
+            mx = fmaxf(mx, fmaf(fmaxf(v0, v1), zs * scp[q], scale_exp(scp[8 + q])));
+          }
+        }
+        const float m_new = fmaxf(m_used, mx);
+        bool need = false;
+        if (x == f_on)
+          m_used = m_new;
+        else
+          need = m_new > m_used + kRescale;
+        if (__any_sync(0xffffffffu, need)) {
+          if (!mbar_wait_warp(&pv_done[g], (c - 1) & 1, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const float factor = need ? ex2_approx(m_used - m_new) : 1.f;
+#pragma unroll 1
+          for (int cc = 0; cc < DH; cc += 8) {
+            uint32_t u[8];
+            tmem_ld8(o_col + cc, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * factor);
+            tmem_st8(o_col + cc, u);
+          }
+          tmem_wait_st();
+          if (need) {
+            l *= factor;
+            m_used = m_new;
+          }
+        }
+        const float msub = m_used == -INFINITY ? 0.f : m_used;
+        float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int cc = 0; cc < kBN; cc += 16) {
+          float2 f2 = make_float2(zs, zs), n2 = make_float2(-msub, -msub);
+          float inv = 1.f;
+          if constexpr (E4) {
+            const float f = zs * scp[cc / 16], nn = scale_exp(scp[8 + cc / 16]) - msub;
+            f2 = make_float2(f, f);
+            n2 = make_float2(nn, nn);
+            inv = scale_inv(scp[8 + cc / 16]);
+            sum2[0] = sum2[1] = make_float2(0.f, 0.f);
+          }
+          uint32_t u[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 arg = __ffma2_rn(make_float2(s[cc + 2 * i], s[cc + 2 * i + 1]), f2, n2);
+            const float2 p = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
+            sum2[i & 1] = __fadd2_rn(sum2[i & 1], p);
+            u[i] = pack16<E4>(p.x, p.y);
+          }
+          if constexpr (E4) l = fmaf((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y), inv, l);
+          tmem_st8(s_col + cc / 2, u);
+        }
+        if constexpr (!E4) {
+          const float2 s01 = __fadd2_rn(sum2[0], sum2[1]);
+          l += s01.x + s01.y;
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[g]);
+        ++c;
+      }
+      if (!ok) break;
+      nt += pc.t1 - pc.t0;
+      if (s_r.rows == 0) continue;
+      const size_t orow = ((size_t)pc.at.b * a.n + tok) * a.H + pc.at.h * G + r % G;
+      if (f_on < 0) {                           // no tile of this piece
+        if (pc.where >= 0) {
+          m.part[((size_t)(pc.where * 2 + g) * (DH / 4 + 1)) * kBM + r] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        } else if (valid) {
+          uint4* dst = reinterpret_cast<uint4*>((bf16*)a.o + orow * DH);
+#pragma unroll
+          for (int i = 0; i < DH / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      if (!mbar_wait_warp(&o_full[g], no & 1, abort_flag, err)) {
+        ok = false;
+        break;
+      }
+      ++no;
+      tc_fence_after();
+      if (pc.where >= 0) {
+        float4* dst = m.part + ((size_t)(pc.where * 2 + g) * (DH / 4 + 1)) * kBM + r;
+        dst[0] = make_float4(m_used, l, 0.f, 0.f);
+#pragma unroll 2
+        for (int cc = 0; cc < DH; cc += 16) {
+          uint32_t u[16];
+          tmem_ld16(o_col + cc, u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[(size_t)(1 + cc / 4 + i) * kBM] =
+                make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]), __uint_as_float(u[4 * i + 2]),
+                            __uint_as_float(u[4 * i + 3]));
+        }
+      } else {
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        bf16* dst = (bf16*)a.o + orow * DH;
+        float probe = 0.f;                      // stays 0 while every output is finite
+#pragma unroll 2
+        for (int cc = 0; cc < DH; cc += 16) {
+          uint32_t u[16];
+          tmem_ld16(o_col + cc, u);
+          tmem_wait_ld();
+          uint4 wv[2];
+          uint32_t* wp = &wv[0].x;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float v0 = __uint_as_float(u[2 * i]) * inv, v1 = __uint_as_float(u[2 * i + 1]) * inv;
+            probe = fmaf(v0, 0.f, fmaf(v1, 0.f, probe));
+            wp[i] = pack16<false>(v0, v1);
+          }
+          if (valid) {
+            *reinterpret_cast<uint4*>(dst + cc) = wv[0];
+            *reinterpret_cast<uint4*>(dst + cc + 8) = wv[1];
+          }
+        }
+        if (valid && !(probe == 0.f))
+          m.flags[((size_t)pc.at.b * a.c.Hkv + pc.at.h) * 2 * m.pairs + 2 * pc.at.p + g] = 1;
+      }
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of the items that cuts went through, 128 threads per row
+// tile (CTA c: the item that cut c goes through first), then computes again,
+// one warp per row, every row whose result is not finite.
+template <int DH>
+__global__ void __launch_bounds__(128) k_many_merge(const ManyArgs m) {
+  pdl_trigger();
+  pdl_wait();
+  const AttnArgs& a = m.a;
+  const int G = kBM / m.tpt, r = threadIdx.x, lane = r & 31, warp = r >> 5;
+  const long long total = m.pre[(size_t)a.c.B * m.pairs] * a.c.Hkv;
+  const int c = blockIdx.x + 1, g = blockIdx.y;
+  const long long xc = cut(m, total, c), xb = cut(m, total, c - 1);
+  auto again = [&](int b, int h, int row, const SlotRange& s, const SeqRange& sr) {
+    // row `row` of the slot's tile, by this warp
+    const int tok = s.tok0 + row / G;
+    const size_t at = ((size_t)b * a.n + tok) * a.H + h * G + row % G;
+    float out[4];
+    attend_row<bf16>(a, b, h, sr.first + tok, (const bf16*)a.q + at * DH, out);
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < DH / 32; ++u) ((bf16*)a.o)[at * DH + lane + 32 * u] = from_f<bf16>(out[u]);
+    __syncwarp();
+  };
+  if (c < m.n_cta && xc < total && xc > xb) {
+    const Place at = find_item(m, xc);
+    if (at.start < xc && at.start >= xb) {          // the first cut through this item
+      const SeqRange sr = seq_range(a, at.b);
+      const Item it = make_item(m, sr, at.p);
+      const SlotRange s = g ? it.s1 : it.s0;
+      const long long end = at.start + it.cnt + 1;
+      // the pieces: those of CTAs c - 1, c, ... that hold key tiles
+      int k1 = c - 1, np = 0;
+      for (; k1 < m.n_cta && cut(m, total, k1) < end; ++k1) {
+        const int2 t = piece_of(at.start, it.cnt, max(cut(m, total, k1), at.start), cut(m, total, k1 + 1));
+        if (t.x < t.y) ++np;
+        if (t.x == 0 && t.y == it.cnt) np = 1 << 20;  // one CTA holds all key tiles: written out
+      }
+      if (s.rows && np < (1 << 20) && np > 0) {
+        auto slot_of = [&](int k, int& w) {
+          const long long xk = cut(m, total, k);
+          const int2 t = piece_of(at.start, it.cnt, max(xk, at.start), cut(m, total, k + 1));
+          w = 2 * k + (xk <= at.start ? 1 : 0);
+          return t.x < t.y;
+        };
+        float M = -INFINITY;
+        for (int k = c - 1; k < k1; ++k) {
+          int w;
+          if (!slot_of(k, w)) continue;
+          M = fmaxf(M, m.part[((size_t)(w * 2 + g) * (DH / 4 + 1)) * kBM + r].x);
+        }
+        const float base = M == -INFINITY ? 0.f : M;
+        float l = 0.f;
+        for (int k = c - 1; k < k1; ++k) {
+          int w;
+          if (!slot_of(k, w)) continue;
+          const float4 ml = m.part[((size_t)(w * 2 + g) * (DH / 4 + 1)) * kBM + r];
+          l = fmaf(ml.y, exp2f(ml.x - base), l);
+        }
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        const bool valid = r < s.rows;
+        const int tok = s.tok0 + r / G;
+        bf16* dst = (bf16*)a.o + (((size_t)at.b * a.n + tok) * a.H + at.h * G + r % G) * DH;
+        float probe = 0.f;
+        for (int q = 0; q < DH / 4; q += 2) {
+          float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+          for (int k = c - 1; k < k1; ++k) {
+            int w;
+            if (!slot_of(k, w)) continue;
+            const float4* p = m.part + ((size_t)(w * 2 + g) * (DH / 4 + 1)) * kBM + r;
+            const float mw = p[0].x;
+            if (mw == -INFINITY) continue;          // no visible key in this piece: its O may be unset
+            const float wgt = exp2f(mw - base);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float4 v = p[(size_t)(1 + q + u) * kBM];
+              acc[u].x = fmaf(v.x, wgt, acc[u].x);
+              acc[u].y = fmaf(v.y, wgt, acc[u].y);
+              acc[u].z = fmaf(v.z, wgt, acc[u].z);
+              acc[u].w = fmaf(v.w, wgt, acc[u].w);
+            }
+          }
+          uint4 wv;
+          uint32_t* wp = &wv.x;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float v0 = acc[u].x * inv, v1 = acc[u].y * inv, v2 = acc[u].z * inv, v3 = acc[u].w * inv;
+            probe = fmaf(v0, 0.f, fmaf(v1, 0.f, fmaf(v2, 0.f, fmaf(v3, 0.f, probe))));
+            wp[2 * u] = pack16<false>(v0, v1);
+            wp[2 * u + 1] = pack16<false>(v2, v3);
+          }
+          if (valid) *reinterpret_cast<uint4*>(dst + 4 * q) = wv;
+        }
+        uint32_t bad = __ballot_sync(0xffffffffu, valid && !(probe == 0.f));
+        while (bad) {
+          const int who = __ffs(bad) - 1;
+          bad &= bad - 1;
+          again(at.b, at.h, warp * 32 + who, s, sr);
+        }
+      }
+    }
+  }
+  // row tiles that the attention kernel wrote out with a value that is not finite
+  const long long tiles = (long long)a.c.B * a.c.Hkv * 2 * m.pairs;
+  const long long words = (tiles + 3) / 4;
+  const long long stride = (long long)gridDim.x * gridDim.y * 128;
+  for (long long i0 = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * 128; i0 < words; i0 += stride) {
+    uint32_t f = i0 + r < words ? reinterpret_cast<const uint32_t*>(m.flags)[i0 + r] : 0u;
+    for (uint32_t todo = __ballot_sync(0xffffffffu, f != 0u); todo; todo &= todo - 1) {
+      const int who = __ffs(todo) - 1;
+      const uint32_t fw = __shfl_sync(0xffffffffu, f, who);
+      for (int u = 0; u < 4; ++u) {
+        if (!((fw >> (8 * u)) & 255u)) continue;
+        const long long t = (i0 + warp * 32 + who) * 4 + u;
+        if (t >= tiles) break;
+        const int rt = (int)(t % (2 * m.pairs)), h = (int)(t / (2 * m.pairs) % a.c.Hkv);
+        const int b = (int)(t / (2 * m.pairs) / a.c.Hkv);
+        const SeqRange sr = seq_range(a, b);
+        const SlotRange s = slot_range(m, sr, rt);
+        for (int row = 0; row < s.rows; ++row) {
+          const size_t at = ((size_t)b * a.n + s.tok0 + row / G) * a.H + h * G + row % G;
+          float probe = 0.f;
+          for (int e = lane; e < DH; e += 32) probe = fmaf(to_f(((const bf16*)a.o)[at * DH + e]), 0.f, probe);
+          if (__any_sync(0xffffffffu, !(probe == 0.f))) again(b, h, row, s, sr);
+        }
+      }
+    }
+  }
+}
+
+struct ManyLayout {
+  size_t pre, flags, part, total;
+  int pairs, flag_words;
+};
+ManyLayout layout_of(const AttnArgs& a) {
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  ManyLayout L{};
+  const int G = a.H / a.c.Hkv, tpt = kBM / G;
+  L.pairs = ((a.n + tpt - 1) / tpt + 1) / 2;
+  const size_t flags = (size_t)a.c.B * a.c.Hkv * 2 * L.pairs;
+  L.flag_words = (int)((flags + 3) / 4);
+  L.pre = 0;
+  L.flags = up(((size_t)a.c.B * L.pairs + 1) * 8);
+  L.part = L.flags + up((size_t)L.flag_words * 4);
+  L.total = L.part + (size_t)2 * sm_count() * 2 * (a.c.dh / 4 + 1) * kBM * 16;
+  return L;
+}
+
+cudaError_t tmap_q(CUtensorMap* t, const AttnArgs& a, int G) {
+  return make_tmap_heads(t, a.q, a.c.B, a.n, a.H, a.c.dh, G, kBM / G);
+}
+
+template <int DH, bool E4>
+cudaError_t run(const AttnArgs& a, void* ws, cudaStream_t s) {
+  using C = ManyCfg<DH, E4>;
+  const int G = a.H / a.c.Hkv;
+  const ManyLayout L = layout_of(a);
+  ManyArgs m;
+  m.a = a;
+  m.pairs = L.pairs;
+  m.tpt = kBM / G;
+  m.n_cta = sm_count();
+  m.negate = a.scale_log2 < 0.f;
+  m.pre = (long long*)ws;
+  m.flags = (uint8_t*)ws + L.flags;
+  m.part = (float4*)((uint8_t*)ws + L.part);
+  m.box = E4 ? kChunk : kBN;
+  if (a.c.bt)
+    while (a.c.ps % m.box) m.box /= 2;           // page_size is a multiple of 16
+  CUtensorMap tq, tk, tv;
+  cudaError_t e = tmap_q(&tq, a, G);
+  if (e != cudaSuccess) return e;
+  const uint64_t planes = a.c.bt ? (uint64_t)a.c.num_pages * a.c.Hkv : (uint64_t)a.c.B * a.c.Hkv;
+  const uint64_t rows = a.c.bt ? (uint64_t)a.c.ps : (uint64_t)a.c.T;
+  if constexpr (E4) {
+    e = make_tmap_rows(&tk, 1, a.c.k, planes, rows, DH, DH, m.box, false);
+    if (e == cudaSuccess) e = make_tmap_rows(&tv, 1, a.c.v, planes, rows, DH, DH, m.box, false);
+  } else {
+    e = make_tmap_rows(&tk, 2, a.c.k, planes, rows, DH, 64, m.box);
+    if (e == cudaSuccess) e = make_tmap_rows(&tv, 2, a.c.v, planes, rows, DH, 64, m.box);
+  }
+  if (e != cudaSuccess) return e;
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(k_attn_many<DH, E4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
+  }
+  e = launch_pdl(k_many_plan, dim3(1), dim3(1024), 0, s, m, L.flag_words);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k_attn_many<DH, E4>, dim3(m.n_cta), dim3(C::THREADS), C::SMEM, s, tq, tk, tv, m);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_many_merge<DH>, dim3(std::max(m.n_cta - 1, 1), 2), dim3(128), 0, s, m);
+}
+
+}  // namespace
+
+size_t cache_attn_many_workspace(const AttnArgs& a) { return a.c.B && a.n ? layout_of(a).total : 0; }
+
+cudaError_t launch_cache_attn_many(const AttnArgs& a, void* ws, cudaStream_t s) {
+  if (a.c.dtype == TB_E4M3) return a.c.dh == 128 ? run<128, true>(a, ws, s) : run<64, true>(a, ws, s);
+  return a.c.dh == 128 ? run<128, false>(a, ws, s) : run<64, false>(a, ws, s);
+}
+
+}  // namespace tb

@@ -637,7 +637,7 @@ cudaError_t make_tmap_3d_u8(CUtensorMap* m, const void* base, uint64_t planes, u
 }
 
 cudaError_t make_tmap_rows(CUtensorMap* m, int esize, const void* base, uint64_t planes, uint64_t rows, uint64_t cols,
-                           uint32_t box_cols, uint32_t box_rows) {
+                           uint32_t box_cols, uint32_t box_rows, bool swizzle) {
   auto fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   const uint32_t bytes = box_cols * esize;
@@ -648,7 +648,23 @@ cudaError_t make_tmap_rows(CUtensorMap* m, int esize, const void* base, uint64_t
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(m, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        !swizzle      ? CU_TENSOR_MAP_SWIZZLE_NONE
+                        : bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                      : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tmap_heads(CUtensorMap* m, const void* base, uint64_t B, uint64_t n, uint64_t H, uint64_t dh,
+                            uint32_t heads, uint32_t tokens) {
+  auto fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[4] = {dh, H, n, B};
+  const cuuint64_t strides[3] = {dh * 2, H * dh * 2, n * H * dh * 2};
+  const cuuint32_t box[4] = {64, heads, tokens, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }

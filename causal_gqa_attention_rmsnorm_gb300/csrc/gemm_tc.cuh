@@ -20,9 +20,12 @@ cudaError_t make_tmap_3d_bf16(CUtensorMap* m, const void* base, uint64_t planes,
 cudaError_t make_tmap_3d_u8(CUtensorMap* m, const void* base, uint64_t planes, uint64_t rows, uint64_t cols,
                             uint64_t row_stride, uint64_t plane_stride, uint32_t box_cols, uint32_t box_rows);
 // Planes of dense rows of 1- or 2-byte elements [planes, rows, cols], a box of
-// box_cols x box_rows with the swizzle of its width (64 or 128 bytes).
+// box_cols x box_rows with the swizzle of its width (64 or 128 bytes), or none.
 cudaError_t make_tmap_rows(CUtensorMap* m, int esize, const void* base, uint64_t planes, uint64_t rows, uint64_t cols,
-                           uint32_t box_cols, uint32_t box_rows);
+                           uint32_t box_cols, uint32_t box_rows, bool swizzle = true);
+// bf16 rows [B, n, H, dh] with a box of 64 columns x `heads` heads x `tokens` tokens, 128-byte swizzle.
+cudaError_t make_tmap_heads(CUtensorMap* m, const void* base, uint64_t B, uint64_t n, uint64_t H, uint64_t dh,
+                            uint32_t heads, uint32_t tokens);
 int sm_count();
 
 cudaError_t gemm_tc_qkv(const void* A, const void* B, int M, int N, int K, const Dims& D, const QKVArgs& e,
