@@ -46,11 +46,18 @@ namespace {
 using namespace ptx;
 
 constexpr int kRun = 16;                      // keys per run: pages hold whole runs
-constexpr int kWarps = 8;
 constexpr uint32_t kStage = 8192;             // K then V bytes of one stage
-constexpr int kSlots = 3;                     // stages per warp of the CTA
 constexpr int kMaxB = 1024;                   // sequences per launch
 constexpr float kRescale = 8.f;               // rescale O only when the maximum grows by more than 2^8
+
+// Warps of a CTA and stages per warp, 24 stages in all.  The e4m3 form of up to
+// eight rows spends more instructions per byte and fewer registers: twelve warps
+// hide its latencies better than eight (PLACEHOLDER).
+template <bool E4, bool LO> struct FewShape {
+  static constexpr int WARPS = E4 && LO ? 12 : 8;
+  static constexpr int SLOTS = E4 && LO ? 2 : 3;
+};
+constexpr int kStages = 24;
 
 template <int DH, bool E4> struct FewCfg {
   static constexpr int ROW = E4 ? DH : 2 * DH;                    // bytes of a row
@@ -60,9 +67,9 @@ template <int DH, bool E4> struct FewCfg {
   static constexpr uint32_t BOX = kRun * BOXB;
   static constexpr uint32_t RUN = kRun * ROW;                     // bytes of a run (K or V)
   static constexpr uint32_t HALF = kStage / 2;
-  static constexpr uint32_t OFF_BAR = kWarps * kSlots * kStage;
-  static constexpr uint32_t OFF_SC = OFF_BAR + 2 * kWarps * kSlots * 8;
-  static constexpr uint32_t OFF_SEQ = OFF_SC + kWarps * kSlots * RUNS * 8;
+  static constexpr uint32_t OFF_BAR = kStages * kStage;
+  static constexpr uint32_t OFF_SC = OFF_BAR + 2 * kStages * 8;
+  static constexpr uint32_t OFF_SEQ = OFF_SC + kStages * RUNS * 8;
   static constexpr size_t smem(int B) { return OFF_SEQ + (size_t)B * 12 + 16 + 1024; }
 };
 
@@ -164,12 +171,13 @@ __device__ __forceinline__ void scan_in_place(int* pre, int n, int* tmp) {
 }
 
 template <int DH, bool E4, int TW, bool LO>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
     k_attn_few(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const FewArgs f) {
   pdl_trigger();
   pdl_wait();
   using C = FewCfg<DH, E4>;
-  constexpr int S = kSlots * TW;                // slots of a team
+  constexpr int kWarps = FewShape<E4, LO>::WARPS;
+  constexpr int S = FewShape<E4, LO>::SLOTS * TW;        // slots of a team
   constexpr int NR = LO ? 1 : 2;                // rows of a lane: g, and g + 8
   const AttnArgs& a = f.a;
   extern __shared__ uint8_t smem_raw[];
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   int* len_s = pre + f.B + 1;
   int* nn_s = len_s + f.B;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + team_in * S;
-  uint64_t* empty = full + kWarps * kSlots;
+  uint64_t* empty = full + kStages;
   float2* sc = reinterpret_cast<float2*>(smem + C::OFF_SC) + team_in * S * C::RUNS;
   __shared__ int abort_word, tmp[kWarps];
   const int Hkv = a.c.Hkv, G = a.H / Hkv;
@@ -193,9 +201,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
   if (threadIdx.x == 0) {
     abort_word = 0;
-    for (int i = 0; i < kWarps * kSlots; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + i, 1);
-      mbar_init(reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + kWarps * kSlots + i, TW);
+      mbar_init(reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + kStages + i, TW);
     }
     fence_barrier_init();
   }
@@ -310,7 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   // ---- consumer ----
   const int mi = lane >> 3;
   uint32_t qa[DH / 16][2 * NR];
-  float o[DH / 8][2 * NR];
+  float o[DH / 8][4];                          // (with eight rows the upper half stays 0)
   float m[NR], l[NR], zscale[NR];
   int qpos[NR];                                // position of the lane's rows; -1: none
   Walk w{};
@@ -372,7 +380,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
       for (int i = 0; i < DH / 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 2 * NR; ++j) o[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     }
     if (!mbar_wait_warp(&full[sl], (k / S) & 1, abort_flag, a.c.err)) {
       ok = false;
@@ -508,12 +516,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           uint32_t b[4];
           ldsm4t(piece<DH, E4>(vb, row, dt + (mi >> 1)), b);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            float acc[4] = {o[dt + u][0], o[dt + u][1], LO ? 0.f : o[dt + u][2 * NR - 2], LO ? 0.f : o[dt + u][2 * NR - 1]};
-            mma<E4>(acc, pa[0], LO ? 0u : pa[NR - 1], pa[NR], LO ? 0u : pa[2 * NR - 1], b[2 * u], b[2 * u + 1]);
-#pragma unroll
-            for (int j = 0; j < 2 * NR; ++j) o[dt + u][j] = acc[j];
-          }
+          for (int u = 0; u < 2; ++u)
+            mma<E4>(o[dt + u], pa[0], LO ? 0u : pa[NR - 1], pa[NR], LO ? 0u : pa[2 * NR - 1], b[2 * u], b[2 * u + 1]);
         }
       } else {
 #pragma unroll
@@ -525,14 +529,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             uint32_t e0, o0, e1, o1;           // even and odd dims; keys 0..7, 8..15
             codes4(__byte_perm(b[2 * u], 0, 0x3120), e0, o0);
             codes4(__byte_perm(b[2 * u + 1], 0, 0x3120), e1, o1);
-#pragma unroll
-            for (int par = 0; par < 2; ++par) {
-              const int d = 2 * (c + u) + par;
-              float acc[4] = {o[d][0], o[d][1], LO ? 0.f : o[d][2 * NR - 2], LO ? 0.f : o[d][2 * NR - 1]};
-              mma<E4>(acc, pa[0], LO ? 0u : pa[NR - 1], pa[NR], LO ? 0u : pa[2 * NR - 1], par ? o0 : e0, par ? o1 : e1);
-#pragma unroll
-              for (int j = 0; j < 2 * NR; ++j) o[d][j] = acc[j];
-            }
+            const int d = 2 * (c + u);
+            mma<E4>(o[d], pa[0], LO ? 0u : pa[NR - 1], pa[NR], LO ? 0u : pa[2 * NR - 1], e0, e1);
+            mma<E4>(o[d + 1], pa[0], LO ? 0u : pa[NR - 1], pa[NR], LO ? 0u : pa[2 * NR - 1], o0, o1);
           }
         }
       }
@@ -715,11 +714,12 @@ cudaError_t run(const AttnArgs& a, float* part, int Bl, cudaStream_t s) {
   f.a = a;
   f.part = part;
   f.R = a.n * (a.H / a.c.Hkv);
-  f.teams = sm_count() * (kWarps / TW);
+  constexpr int warps = FewShape<E4, LO>::WARPS;
+  f.teams = sm_count() * (warps / TW);
   for (int b0 = 0; b0 < a.c.B; b0 += Bl) {
     f.b0 = b0;
     f.B = std::min(Bl, a.c.B - b0);
-    e = launch_pdl(k_attn_few<DH, E4, TW, LO>, dim3(sm_count()), dim3(kWarps * 32), smem, s, tk, tv, f);
+    e = launch_pdl(k_attn_few<DH, E4, TW, LO>, dim3(sm_count()), dim3(warps * 32), smem, s, tk, tv, f);
     if (e != cudaSuccess) return e;
     e = launch_pdl(k_few_merge<DH, C::RUNS>, dim3(f.R, a.c.Hkv, f.B), dim3(kMergeThreads), 0, s, f);
     if (e != cudaSuccess) return e;
@@ -748,7 +748,8 @@ int batch_of(const AttnArgs& a) {
 size_t cache_attn_few_workspace(const AttnArgs& a) {
   const int R = a.n * (a.H / a.c.Hkv);
   if (a.c.B == 0 || R == 0) return 0;
-  const long long pieces = (long long)sm_count() * (kWarps / team_warps(R)) + (long long)batch_of(a) * a.c.Hkv;
+  const int warps = R <= 8 && a.c.dtype == TB_E4M3 ? FewShape<true, true>::WARPS : FewShape<false, false>::WARPS;
+  const long long pieces = (long long)sm_count() * (warps / team_warps(R)) + (long long)batch_of(a) * a.c.Hkv;
   return (size_t)pieces * R * (a.c.dh + 4) * 4;
 }
 

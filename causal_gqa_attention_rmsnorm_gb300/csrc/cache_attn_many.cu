@@ -188,20 +188,40 @@ __device__ __forceinline__ int2 piece_of(long long start, int cnt, long long x0,
   return make_int2((int)t0, (int)max(t0, t1));
 }
 
-// The pieces of a CTA, in order; each role walks them alike.
+// The pieces of a CTA, in order; each role walks them alike.  Only the first
+// item is looked up on the line; the next one follows from the one before.
 struct Pieces {
   const ManyArgs& m;
-  long long x, x1, x0;
+  long long x, x1;
   Place at;
   Item it;
   SeqRange sr;
   int t0, t1, where;          // where: -1 the whole item, else the piece's slot in the workspace
-  __device__ Pieces(const ManyArgs& m_, long long a, long long b) : m(m_), x(a), x1(b), x0(a) {}
-  __device__ __forceinline__ bool next() {
-    while (x < x1) {
+  bool any = false;
+  __device__ Pieces(const ManyArgs& m_, long long a, long long b) : m(m_), x(a), x1(b) {}
+  __device__ __forceinline__ void step() {
+    if (!any) {
+      any = true;
       at = find_item(m, x);
       sr = seq_range(m.a, at.b);
       it = make_item(m, sr, at.p);
+      return;
+    }
+    at.start += it.cnt + 1;
+    if (++at.p < m.pairs) {
+      it = make_item(m, sr, at.p);
+      if (it.s0.rows) return;
+    }
+    at.p = 0;
+    if (++at.h == m.a.c.Hkv) {
+      at.h = 0;
+      do sr = seq_range(m.a, ++at.b); while (sr.nn == 0);      // the line goes on: there is one
+    }
+    it = make_item(m, sr, 0);
+  }
+  __device__ __forceinline__ bool next() {
+    while (x < x1) {
+      step();
       const int2 t = piece_of(at.start, it.cnt, x, x1);
       const bool begins = x == at.start;
       x = min(x1, at.start + it.cnt + 1);
