@@ -391,6 +391,7 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
     // Scores, scaled to base 2 (over e4m3 with log2 of the V scale added), of
     // the stage's runs: z[run][8-key tile][row i: keys 2t, 2t+1]
     float z[C::RUNS][2][2 * NR];
+    float vsc[C::RUNS];                        // E4: the runs' V scales
 #pragma unroll
     for (int r = 0; r < C::RUNS; ++r) {
       float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
@@ -424,9 +425,10 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
       float ks = 1.f, ve = 0.f;
       if constexpr (E4) {
         if (r < nr) {
-          const float2 v = sc[sl * C::RUNS + r];
+          const float2 v = lds_f2(smem_u32(sc + sl * C::RUNS + r));
           ks = v.x;
           ve = scale_exp(v.y);
+          vsc[r] = v.y;
         }
       }
       const int key = run_index(kr, r0 + r) * kRun;
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
         const float p2 = ex2_approx(z[r][1][2 * i] - base), p3 = ex2_approx(z[r][1][2 * i + 1] - base);
         const float sum = (p0 + p1) + (p2 + p3);
         if constexpr (E4) {
-          l[i] = fmaf(sum, scale_inv(sc[sl * C::RUNS + r].y), l[i]);
+          l[i] = fmaf(sum, scale_inv(vsc[r]), l[i]);
         } else {
           l[i] += sum;
         }

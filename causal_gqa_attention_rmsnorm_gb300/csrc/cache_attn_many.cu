@@ -652,8 +652,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
               ok = false;
               break;
             }
-            const uint8_t* raw = smem + C::OFF_RAW + rs * C::RAW;
-            uint8_t* dst = smem + (half ? C::OFF_V : C::OFF_K) + st * C::KV_BYTES;
+            const uint32_t raw = smem_u32(smem) + C::OFF_RAW + rs * C::RAW;
+            const uint32_t dst = smem_u32(smem) + (half ? C::OFF_V : C::OFF_K) + st * C::KV_BYTES;
             const int key0 = tile_key + ch * kChunk;
             const bool border = half && (key0 + kChunk > it.end || (key0 < it.hid1 && key0 + kChunk > it.hid0));
             // 16-byte pieces of 16 codes, PPR per row.  The four lanes of a half
@@ -666,23 +666,25 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
               r0 = (r2 & ~1) + (c >> 2);
               pc0 = (c & 3) + 4 * ((r2 & 1) ^ (c >> 2));
             }
+            uint4 w[STEPS];
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) w[i] = lds128(raw + (i * RPS + r0) * DH + pc0 * 16);
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
               const int row = i * RPS + r0;
-              uint4 w = *reinterpret_cast<const uint4*>(raw + row * DH + pc0 * 16);
               if (border) {
                 const int j = key0 + row;
-                if (j >= it.end || (j >= it.hid0 && j < it.hid1)) w = make_uint4(0u, 0u, 0u, 0u);
+                if (j >= it.end || (j >= it.hid0 && j < it.hid1)) w[i] = make_uint4(0u, 0u, 0u, 0u);
               }
               uint4 lo, hi;
-              codes4(w.x, lo.x, lo.y);
-              codes4(w.y, lo.z, lo.w);
-              codes4(w.z, hi.x, hi.y);
-              codes4(w.w, hi.z, hi.w);
+              codes4(w[i].x, lo.x, lo.y);
+              codes4(w[i].y, lo.z, lo.w);
+              codes4(w[i].z, hi.x, hi.y);
+              codes4(w[i].w, hi.z, hi.w);
               const int r = ch * kChunk + row, c = 2 * pc0;             // 16-byte piece of the fp16 row
-              uint8_t* base = dst + (c >> 3) * kBN * 128 + r * 128;
-              *reinterpret_cast<uint4*>(base + (((c ^ r) & 7) << 4)) = lo;
-              *reinterpret_cast<uint4*>(base + ((((c + 1) ^ r) & 7) << 4)) = hi;
+              const uint32_t base = dst + (c >> 3) * kBN * 128 + r * 128;
+              sts128(base + (((c ^ r) & 7) << 4), lo);
+              sts128(base + ((((c + 1) ^ r) & 7) << 4), hi);
             }
             fence_proxy_async();
             __syncwarp();
@@ -719,12 +721,12 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
             break;
           }
           if (s_r.rows) {
-            uint8_t* qrow = smem + g * C::Q_BYTES + r * 128;
+            const uint32_t qrow = smem_u32(smem) + g * C::Q_BYTES + r * 128;
             uint4 w[C::NB * 8];
             float amax = 0.f;
 #pragma unroll
             for (int i = 0; i < C::NB * 8; ++i) {
-              w[i] = *reinterpret_cast<const uint4*>(qrow + (i >> 3) * kBM * 128 + (((i ^ r) & 7) << 4));
+              w[i] = lds128(qrow + (i >> 3) * kBM * 128 + (((i ^ r) & 7) << 4));
               const uint32_t* u = &w[i].x;
 #pragma unroll
               for (int j = 0; j < 4; ++j)
@@ -738,7 +740,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 u[j] = pack16<true>(__uint_as_float(u[j] << 16) * fr, __uint_as_float(u[j] & 0xffff0000u) * fr);
-              *reinterpret_cast<uint4*>(qrow + (i >> 3) * kBM * 128 + (((i ^ r) & 7) << 4)) = w[i];
+              sts128(qrow + (i >> 3) * kBM * 128 + (((i ^ r) & 7) << 4), w[i]);
             }
           }
           fence_proxy_async();
@@ -789,7 +791,16 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
           for (int cc = 0; cc < kBN; ++cc)
             if (cc < wl && cc >= sl) s[cc] = -INFINITY;
         }
-        const float* scp = sc + (tn % kScTiles) * 16;
+        float ksc[8], vsc[8];                   // E4: the block scales of the tile's eight runs
+        if constexpr (E4) {
+          const uint32_t scp = smem_u32(sc) + (tn % kScTiles) * 64;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float4 kq = lds_f4(scp + 16 * i), vq = lds_f4(scp + 32 + 16 * i);
+            ksc[4 * i] = kq.x, ksc[4 * i + 1] = kq.y, ksc[4 * i + 2] = kq.z, ksc[4 * i + 3] = kq.w;
+            vsc[4 * i] = vq.x, vsc[4 * i + 1] = vq.y, vsc[4 * i + 2] = vq.z, vsc[4 * i + 3] = vq.w;
+          }
+        }
         float mx;
         if constexpr (!E4) {
           float m4[4];
@@ -811,7 +822,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
               v0 = fmax3(v0, s[16 * q + i], s[16 * q + i + 1]);
               v1 = fmax3(v1, s[16 * q + i + 2], s[16 * q + i + 3]);
             }
-            mx = fmaxf(mx, fmaf(fmaxf(v0, v1), zs * scp[q], scale_exp(scp[8 + q])));
+            mx = fmaxf(mx, fmaf(fmaxf(v0, v1), zs * ksc[q], scale_exp(vsc[q])));
           }
         }
         const float m_new = fmaxf(m_used, mx);
@@ -849,10 +860,10 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
           float2 f2 = make_float2(zs, zs), n2 = make_float2(-msub, -msub);
           float inv = 1.f;
           if constexpr (E4) {
-            const float f = zs * scp[cc / 16], nn = scale_exp(scp[8 + cc / 16]) - msub;
+            const float f = zs * ksc[cc / 16], nn = scale_exp(vsc[cc / 16]) - msub;
             f2 = make_float2(f, f);
             n2 = make_float2(nn, nn);
-            inv = scale_inv(scp[8 + cc / 16]);
+            inv = scale_inv(vsc[cc / 16]);
             sum2[0] = sum2[1] = make_float2(0.f, 0.f);
           }
           uint32_t u[8];
