@@ -8,8 +8,9 @@
 //   row tiles ("slots") over the same key tiles:
 //     S_g = Q_g·Kᵀ into tensor memory (M = 128, N = 128 keys), softmax in fp32
 //     by one thread per row, P back over S in 16 bits, O_g += P_g·V.
-//   Roles: warps 0..7 softmax (four per slot), warp 8 copies, warp 9 issues the
-//   MMAs; over e4m3 two more warps turn codes into fp16 tiles.  The MMA order
+//   Roles: warps 0..7 softmax (four per slot), warp 8 copies and hands the pieces
+//   of work to the others, warp 9 issues the MMAs, warp 10 (over e4m3 and 11) sees
+//   to V tiles that cannot be used as they land.  The MMA order
 //   per key tile is P·V of slot 0, S of slot 0 for the next tile, the same of
 //   slot 1, so that the tensor pipe works on one slot during the other's
 //   softmax.
@@ -26,9 +27,15 @@
 //   a cut one leave (max, sum, O) in the workspace and k_many_merge joins them in
 //   order.  The line's prefix sums come from k_many_plan.
 //
-//   e4m3: TMA brings 32-key chunks of codes through a ring; a conversion warp
-//   writes them as fp16 (exact) into the swizzled K or V tile.  Queries become
-//   fp16 under a power of two per row.  K scales multiply the scores per 16
+//   e4m3: S is an 8-bit MMA on the K codes as they lie in the cache.  A query
+//   row, under a power of two that brings its largest element into [128, 256),
+//   is split into two e4m3 terms, q = q1 + q2: q1 takes the leading four bits of
+//   a bf16 element, the rest is at most half a step of q1 and has four bits
+//   itself, so the split is exact for elements down to 2^-2 and off by 2^-10 at
+//   most below (2^-17 of the row's largest); both terms multiply K, at twice the
+//   16-bit rate.  P has no such split that pays, so V becomes fp16 (exactly):
+//   TMA brings 32-key chunks of codes through a ring and conversion warps write
+//   them into the swizzled V tile.  K scales multiply the scores per 16
 //   keys; V scales 2^e enter the exponent, p' = 2^(z + e - m'), so that
 //   O = Σ p'·code and l = Σ p'·2^-e (see the streaming kernel).
 //
@@ -49,23 +56,31 @@ using namespace ptx;
 
 constexpr int kBM = 128, kBN = 128;
 constexpr float kRescale = 8.f;
-constexpr int kChunk = 32;                     // keys per chunk of codes
-constexpr int kRaw = 8;                        // chunks in the ring: one K and one V tile
+constexpr int kChunk = 32;                     // keys per chunk of V codes
+constexpr int kRaw = 8;                        // chunks in the ring: two V tiles
 constexpr int kScTiles = 8;                    // tiles whose block scales are kept
+constexpr int kConv = 2;                       // conversion warps
+template <bool E4> constexpr int kVWarps = E4 ? kConv : 1;
 
 template <int DH, bool E4> struct ManyCfg {
   static constexpr int NB = DH / 64;                       // 64-column blocks of a 16-bit row
-  static constexpr uint32_t Q_BYTES = kBM * DH * 2;
-  static constexpr uint32_t KV_BYTES = kBN * DH * 2;
+  static constexpr uint32_t Q_BYTES = kBM * DH * 2;        // a slot's queries, 16-bit
+  static constexpr uint32_t QT_BYTES = kBM * DH;           // E4: one term of them
+  static constexpr uint32_t K_BYTES = kBN * DH * (E4 ? 1 : 2);
+  static constexpr uint32_t V_BYTES = kBN * DH * 2;
   static constexpr uint32_t RAW = kChunk * DH;             // bytes of a chunk of codes
-  static constexpr uint32_t OFF_K = 2 * Q_BYTES;
-  static constexpr uint32_t OFF_V = OFF_K + 2 * KV_BYTES;
-  static constexpr uint32_t OFF_RAW = OFF_V + 2 * KV_BYTES;
-  static constexpr uint32_t OFF_SC = OFF_RAW + (E4 ? kRaw * RAW : 0);      // [kScTiles][16]: K, then V
+  // E4: the terms of rows of 128 dims replace the row in place (each of its two
+  // 128-byte halves); those of 64 dims have tiles of their own
+  static constexpr uint32_t OFF_QT = E4 && DH == 64 ? 2 * Q_BYTES : 0;
+  static constexpr uint32_t OFF_K = OFF_QT + 2 * Q_BYTES;
+  static constexpr uint32_t OFF_V = OFF_K + 2 * K_BYTES;
+  static constexpr uint32_t OFF_RAW = OFF_V + 2 * V_BYTES;
+  static constexpr uint32_t OFF_SC = OFF_RAW + (E4 ? kRaw * RAW : 0);      // [kScTiles][8 runs]{K, V}
   static constexpr uint32_t OFF_BAR = OFF_SC + (E4 ? kScTiles * 64 : 0);
-  static constexpr size_t SMEM = OFF_BAR + 512 + 1024;
+  static constexpr uint32_t OFF_DESC = OFF_BAR + 512;
+  static constexpr size_t SMEM = OFF_DESC + 512 + 1024;
   static constexpr uint32_t TMEM_O = 2 * kBN;
-  static constexpr int THREADS = E4 ? 384 : 320;
+  static constexpr int THREADS = E4 ? 384 : 352;
 };
 
 struct ManyArgs {
@@ -73,7 +88,8 @@ struct ManyArgs {
   int pairs;               // row-tile pairs of a sequence of n tokens
   int tpt;                 // tokens per row tile: 128 / G
   int n_cta;
-  int box;                 // keys per box
+  int box;                 // keys per box of a 16-bit tile, or of K codes
+  int vbox;                // keys per box of V codes
   bool negate;             // the score scale is negative: the scores are negated, its magnitude applied
   long long* pre;          // [B·pairs + 1] line position of (sequence, pair) within its KV head
   uint8_t* flags;          // [B·Hkv·2·pairs] row tiles to look through again
@@ -240,6 +256,20 @@ struct Pieces {
   }
 };
 
+// A piece as the copying warp hands it to the other roles, through a ring in
+// shared memory; `last` follows the last piece.
+struct PieceDesc {
+  int t0, t1, where, last, b, h, p;
+  int ns, wl, end, hid0, hid1;
+  SlotRange s[2];
+  __device__ __forceinline__ int key(int x) const { return (x < ns ? x : x - ns + wl) * kBN; }
+  // whether the tile at `key` holds rows that no row of the item sees
+  __device__ __forceinline__ bool border(int key) const {
+    return key + kBN > end || (key < hid1 && key + kBN > hid0);
+  }
+};
+constexpr int kDescs = 4;
+
 // pre[e] for e = (sequence, pair) in order, and the flags cleared; one CTA.
 __global__ void __launch_bounds__(1024) k_many_plan(const ManyArgs m, int n_flag_words) {
   pdl_trigger();
@@ -299,10 +329,26 @@ __device__ __forceinline__ float pow2_frame(float x) {
   const int e = max(-126, min(126, (int)((__float_as_uint(x) >> 23) & 0xffu) - 126));
   return __uint_as_float((uint32_t)(127 - e) << 23);
 }
-// Instruction descriptor, kind::f16 with fp16 (E4) or bf16 operands, fp32 sums.
+// Instruction descriptor of P·V, kind::f16 with fp16 (E4) or bf16 operands, fp32
+// sums, V MN-major.
 template <bool E4>
-__host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn) {
-  return idesc_bf16(M, N, false, b_mn) & ~(E4 ? (1u << 7 | 1u << 10) : 0u);
+__host__ __device__ constexpr uint32_t idesc_pv(int M, int N) {
+  return idesc_bf16(M, N, false, true) & ~(E4 ? (1u << 7 | 1u << 10) : 0u);
+}
+// Two values to e4m3 codes (low byte: lo), and back.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+  float2 r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(h));
+  return r;
 }
 
 template <int DH, bool E4>
@@ -331,7 +377,12 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
   uint64_t* raw_full = bars + 20;    // [kRaw]
   uint64_t* raw_empty = bars + 28;   // [kRaw]
   uint64_t* sc_full = bars + 36;     // [kScTiles]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 44);
+  uint64_t* d_full = bars + 44;      // [kDescs]
+  uint64_t* d_empty = bars + 48;     // [kDescs]
+  uint64_t* fix_full = bars + 52;    // [2]: a border V tile has landed, its hidden rows not yet zeroed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 54);
+  PieceDesc* descs = reinterpret_cast<PieceDesc*>(smem + C::OFF_DESC);
+  static_assert(sizeof(PieceDesc) * kDescs <= 512 && 54 * 8 + 8 <= 512, "layout");
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* sc = reinterpret_cast<float*>(smem + C::OFF_SC);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -342,7 +393,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
     mbar_init(q_ready, 8);
     mbar_init(drain, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], E4 ? kBN / kChunk : 1);
+      mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], E4 ? kBN / kChunk : 1);
       mbar_init(&v_empty[i], 1);
@@ -350,12 +401,17 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&o_full[i], 1);
+      mbar_init(&fix_full[i], 1);
     }
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 1);
     }
     for (int i = 0; i < kScTiles; ++i) mbar_init(&sc_full[i], 1);
+    for (int i = 0; i < kDescs; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], 9 + kVWarps<E4>);   // the MMA warp, eight softmax warps, those that see to V
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -371,17 +427,62 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
   const long long total = m.pre[(size_t)a.c.B * m.pairs] * a.c.Hkv;
   const long long x0 = cut(m, total, blockIdx.x), x1 = cut(m, total, blockIdx.x + 1);
   const int G = kBM / m.tpt;
+  // The k-th piece for a role other than the copying one; false after the last
+  // (or a wait that ran out).  done(k) hands the descriptor back.
+  auto piece = [&](int k, PieceDesc*& d) -> bool {
+    d = descs + k % kDescs;
+    return mbar_wait_warp(&d_full[k % kDescs], (k / kDescs) & 1, abort_flag, err) && !d->last;
+  };
+  auto done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&d_empty[k % kDescs]);
+  };
 
   if (warp == 8) {
     // ---------------- copies ----------------
-    int nq = 0, nt = 0;                         // pieces with queries, key tiles issued
-    int nraw = 0;                               // E4: chunks issued
+    int nq = 0, nt = 0;                         // pieces with queries, key tiles
+    int nk = 0, nv = 0;                         // K tiles and V tiles (E4: chunks) issued
+    int n_fix[2] = {0, 0};                      // border V tiles of each stage; whether its last was one
+    uint32_t fixed = 0;
     bool ok = true;
     Pieces pc(m, x0, x1);
-    while (ok && pc.next()) {
+    auto publish = [&](int k, bool last) -> bool {
+      if (k >= kDescs && !mbar_wait_warp(&d_empty[k % kDescs], ((k / kDescs) & 1) ^ 1u, abort_flag, err)) return false;
+      if (lane == 0) {
+        PieceDesc& d = descs[k % kDescs];
+        d.t0 = pc.t0;
+        d.t1 = pc.t1;
+        d.where = pc.where;
+        d.last = last;
+        d.b = pc.at.b;
+        d.h = pc.at.h;
+        d.p = pc.at.p;
+        d.ns = pc.it.ns;
+        d.wl = pc.it.wl;
+        d.end = pc.it.end;
+        d.hid0 = pc.it.hid0;
+        d.hid1 = pc.it.hid1;
+        d.s[0] = pc.it.s0;
+        d.s[1] = pc.it.s1;
+        mbar_arrive(&d_full[k % kDescs]);
+      }
+      __syncwarp();
+      return true;
+    };
+    int np = 0;
+    for (;; ++np) {
+      const bool more = pc.next();
+      if (!publish(np, !more)) {
+        ok = false;
+        break;
+      }
+      if (!more) break;
       if (pc.t0 == pc.t1) continue;             // rows without keys
       const Item& it = pc.it;
-      if (nq > 0 && !mbar_wait_warp(q_empty, (nq - 1) & 1, abort_flag, err)) break;
+      if (nq > 0 && !mbar_wait_warp(q_empty, (nq - 1) & 1, abort_flag, err)) {
+        ok = false;
+        break;
+      }
       if (lane == 0) {
         const int slots = it.s1.rows ? 2 : 1;
         fence_proxy_async();                    // the queries were rewritten in place (E4)
@@ -440,222 +541,233 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         page2 = page_ahead(x + 2);
         const bool want = plane >= 0;
         const int y = a.c.bt ? key % a.c.ps : key;
-        if constexpr (!E4) {
-          const uint32_t loads = __ballot_sync(0xffffffffu, want);
-          const uint32_t bytes = (uint32_t)__popc(loads) * m.box * DH * 2;
-          if (!mbar_wait_warp(&k_empty[st], ph ^ 1u, abort_flag, err)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&k_full[st], bytes);
-          __syncwarp();
-          if (want) {
-#pragma unroll
-            for (int blk = 0; blk < C::NB; ++blk)
-              tma_load_3d(&tmK, smem + C::OFF_K + st * C::KV_BYTES + blk * kBN * 128 + lane * unit * 128, &k_full[st],
-                          blk * 64, y, plane);
-          }
-          if (!mbar_wait_warp(&v_empty[st], ph ^ 1u, abort_flag, err)) {
-            ok = false;
-            // the K boxes just issued land before the CTA ends
-            volatile int no_abort = 0;
-            mbar_wait(&k_full[st], ph, &no_abort, err);
-            break;
-          }
-          if (lane == 0) {
-            fence_proxy_async();                // rows zeroed in place, before the copy
-            mbar_arrive_expect_tx(&v_full[st], bytes);
-          }
-          __syncwarp();
-          if (want) {
-#pragma unroll
-            for (int blk = 0; blk < C::NB; ++blk)
-              tma_load_3d(&tmV, smem + C::OFF_V + st * C::KV_BYTES + blk * kBN * 128 + lane * unit * 128, &v_full[st],
-                          blk * 64, y, plane);
-          }
-        } else {
+        // Boxes of `box` keys: lane i issues the box that its keys begin (E4: its
+        // run of 16; a box is issued if any of its runs is wanted, from the page of
+        // that run - all runs of a box lie in one page)
+        auto lead_of = [&](int box, int& z) {
+          const int per = E4 ? box / 16 : 1;
+          const uint32_t any = __ballot_sync(0xffffffffu, want);
+          const uint32_t runs = per >= 32 ? any : (any >> lane) & ((1u << per) - 1u);
+          const int src = runs ? lane + __ffs(runs) - 1 : lane;
+          z = __shfl_sync(0xffffffffu, plane, src & 31);
+          return mine && lane % per == 0 && runs != 0;
+        };
+        int zk, zv = 0;
+        const bool go_k = lead_of(m.box, zk);
+        const bool go_v = E4 ? lead_of(m.vbox, zv) : go_k;
+        const uint32_t loads = __ballot_sync(0xffffffffu, go_k), vloads = __ballot_sync(0xffffffffu, go_v);
+        if constexpr (E4) {
           const int sl = nt % kScTiles;
-          if (mine) {
-            sc[sl * 16 + lane] = ks;
-            sc[sl * 16 + 8 + lane] = vs;
-          }
+          if (mine) reinterpret_cast<float2*>(sc)[sl * 8 + lane] = make_float2(ks, vs);
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[sl]);
-          // a box is issued by the lane of its first run; with boxes of 32 keys
-          // a box whose first run alone is hidden is issued all the same
-          const int rpb = m.box / 16;
-          const uint32_t any = __ballot_sync(0xffffffffu, want);
-          const bool lead = mine && lane % rpb == 0;
-          const bool go = lead && ((any >> lane) & ((1u << rpb) - 1u));
-          const int zp = rpb == 2 ? __shfl_sync(0xffffffffu, plane, (lane | 1) & 7) : plane;
-          const int z = plane >= 0 ? plane : zp;
-          const uint32_t loads = __ballot_sync(0xffffffffu, go);
-#pragma unroll 1
-          for (int half = 0; half < 2 && ok; ++half)
-            for (int ch = 0; ch < kBN / kChunk; ++ch, ++nraw) {
-              const int rs = nraw % kRaw;
-              if (!mbar_wait_warp(&raw_empty[rs], ((nraw / kRaw) & 1) ^ 1u, abort_flag, err)) {
-                ok = false;
-                break;
-              }
-              const uint32_t in = (loads >> (2 * ch)) & 3u;      // runs 2ch, 2ch + 1 lead a box
-              if (lane == 0)
-                mbar_arrive_expect_tx(&raw_full[rs], (uint32_t)__popc(in) * m.box * DH);
-              __syncwarp();
-              if (go && (lane >> 1) == ch)
-                tma_load_3d(half ? &tmV : &tmK, smem + C::OFF_RAW + rs * C::RAW + (lane & 1) * 16 * DH, &raw_full[rs],
-                            0, y, z);
-              __syncwarp();
+        }
+        if (!mbar_wait_warp(&k_empty[st], ph ^ 1u, abort_flag, err)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[st], (uint32_t)__popc(loads) * m.box * DH * (E4 ? 1 : 2));
+        __syncwarp();
+        if (go_k) {
+          uint8_t* dst = smem + C::OFF_K + st * C::K_BYTES;
+          if constexpr (E4) {
+            tma_load_3d(&tmK, dst + lane * 16 * DH, &k_full[st], 0, y, zk);
+          } else {
+#pragma unroll
+            for (int blk = 0; blk < C::NB; ++blk)
+              tma_load_3d(&tmK, dst + blk * kBN * 128 + lane * unit * 128, &k_full[st], blk * 64, y, zk);
+          }
+        }
+        ++nk;
+        if constexpr (!E4) {
+          if (!mbar_wait_warp(&v_empty[st], ph ^ 1u, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          // a border tile goes by way of the warp that zeroes its hidden rows
+          const int k0 = it.tile(x) * kBN;
+          const bool border = k0 + kBN > it.end || (k0 < it.hid1 && k0 + kBN > it.hid0);
+          uint64_t* bar = border ? &fix_full[st] : &v_full[st];
+          n_fix[st] += border;
+          fixed = (fixed & ~(1u << st)) | (uint32_t)border << st;
+          if (lane == 0) {
+            fence_proxy_async();                // rows zeroed in place, before the copy
+            mbar_arrive_expect_tx(bar, (uint32_t)__popc(loads) * m.box * DH * 2);
+          }
+          __syncwarp();
+          if (go_k) {
+#pragma unroll
+            for (int blk = 0; blk < C::NB; ++blk)
+              tma_load_3d(&tmV, smem + C::OFF_V + st * C::V_BYTES + blk * kBN * 128 + lane * unit * 128, bar,
+                          blk * 64, y, zk);
+          }
+          ++nv;
+        } else {
+          for (int ch = 0; ch < kBN / kChunk; ++ch, ++nv) {
+            const int rs = nv % kRaw;
+            if (!mbar_wait_warp(&raw_empty[rs], ((nv / kRaw) & 1) ^ 1u, abort_flag, err)) {
+              ok = false;
+              break;
             }
+            const uint32_t in = (vloads >> (2 * ch)) & 3u;       // runs 2ch, 2ch + 1 lead a box
+            if (lane == 0) mbar_arrive_expect_tx(&raw_full[rs], (uint32_t)__popc(in) * m.vbox * DH);
+            __syncwarp();
+            if (go_v && (lane >> 1) == ch)
+              tma_load_3d(&tmV, smem + C::OFF_RAW + rs * C::RAW + (lane & 1) * 16 * DH, &raw_full[rs], 0, y, zv);
+            __syncwarp();
+          }
         }
       }
+      if (!ok) break;
     }
     // every copy issued must land before the CTA may exit
     __syncwarp();
     if (lane == 0) {
       volatile int no_abort = 0;
       if (nq > 0) mbar_wait(q_full, (nq - 1) & 1, &no_abort, err);
+      for (int t = max(0, nk - 2); t < nk; ++t) mbar_wait(&k_full[t & 1], (t >> 1) & 1, &no_abort, err);
       if constexpr (E4) {
-        for (int t = max(0, nraw - kRaw); t < nraw; ++t)
+        for (int t = max(0, nv - kRaw); t < nv; ++t)
           mbar_wait(&raw_full[t % kRaw], (t / kRaw) & 1, &no_abort, err);
       } else {
-        for (int t = max(0, nt - 2); t < nt; ++t) {
-          mbar_wait(&k_full[t & 1], (t >> 1) & 1, &no_abort, err);
-          mbar_wait(&v_full[t & 1], (t >> 1) & 1, &no_abort, err);
+        for (int t = max(0, nv - 2); t < nv; ++t) {
+          const int st = t & 1;
+          if ((fixed >> st) & 1)
+            mbar_wait(&fix_full[st], (n_fix[st] - 1) & 1, &no_abort, err);
+          else
+            mbar_wait(&v_full[st], (t >> 1) & 1, &no_abort, err);
         }
       }
     }
   } else if (warp == 9) {
     // ---------------- MMA issue ----------------
-    constexpr uint32_t id_qk = idesc<E4>(kBM, kBN, false), id_pv = idesc<E4>(kBM, DH, true);
-    const uint32_t sQ = smem_u32(smem);
-    const uint64_t dq0 = desc_kmajor_sw128(sQ), dq1 = desc_kmajor_sw128(sQ + C::Q_BYTES);
-    const uint64_t dk0 = desc_kmajor_sw128(sQ + C::OFF_K), dk1 = desc_kmajor_sw128(sQ + C::OFF_K + C::KV_BYTES);
-    const uint64_t dv0 = desc_mnmajor_sw128(sQ + C::OFF_V, kBN * 128, 1024);
-    const uint64_t dv1 = desc_mnmajor_sw128(sQ + C::OFF_V + C::KV_BYTES, kBN * 128, 1024);
-    auto issue_s = [&](int g, int t) {
-      if (lane == 0) {
-        mma_tile_ss<DH / 16>(tmem + g * kBN, g ? dq1 : dq0, (t & 1) ? dk1 : dk0, id_qk);
+    // by one thread, which shares its SM quarter with two softmax warps: every
+    // instruction it spends between a wait and an MMA delays the tile
+    if (lane == 0) {
+      // the sign of a negative score scale goes into S (bit 13: A is negated)
+      const uint32_t id_qk = (E4 ? idesc_e4m3(kBM, kBN) : idesc_bf16(kBM, kBN)) | (m.negate ? 1u << 13 : 0u);
+      constexpr uint32_t id_pv = idesc_pv<E4>(kBM, DH);
+      const uint32_t sQ = smem_u32(smem) + C::OFF_QT, sK = smem_u32(smem) + C::OFF_K, sV = smem_u32(smem) + C::OFF_V;
+      auto kmajor = [](uint32_t addr) { return E4 && DH == 64 ? desc_kmajor_sw64(addr) : desc_kmajor_sw128(addr); };
+      const uint64_t dq0 = kmajor(sQ), dq1 = kmajor(sQ + C::Q_BYTES);
+      const uint64_t dk0 = kmajor(sK), dk1 = kmajor(sK + C::K_BYTES);
+      const uint64_t dv0 = desc_mnmajor_sw128(sV, kBN * 128, 1024);
+      const uint64_t dv1 = desc_mnmajor_sw128(sV + C::V_BYTES, kBN * 128, 1024);
+      auto issue_s = [&](int g, int t) {
+        const uint64_t qd = g ? dq1 : dq0, kd = (t & 1) ? dk1 : dk0;
+        if constexpr (E4) {
+          // both terms of the queries, 32 dims (two 16-byte units) per MMA
+#pragma unroll
+          for (int i = 0; i < 2 * (DH / 32); ++i) {
+            const int term = i / (DH / 32), kk = i % (DH / 32);
+            mma_f8_ss(tmem + g * kBN, qd + term * (C::QT_BYTES >> 4) + 2 * kk, kd + 2 * kk, id_qk, i ? 1u : 0u);
+          }
+        } else {
+          mma_tile_ss<DH / 16>(tmem + g * kBN, qd, kd, id_qk);
+        }
         mma_commit(&s_full[g]);
-      }
-    };
-    auto issue_pv = [&](int g, int t, bool acc) {
-      if (lane == 0) {
+      };
+      auto issue_pv = [&](int g, int t, bool acc) {
         mma_tile_ts128(tmem + C::TMEM_O + g * DH, tmem + g * kBN, (t & 1) ? dv1 : dv0, id_pv, acc ? 1u : 0u);
         mma_commit(&pv_done[g]);
-      }
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (lane == 0) mma_commit(bar);
-    };
-    int kc = 0, nq = 0, c0 = 0, c1 = 0;
-    bool ok = true;
-    Pieces pc(m, x0, x1);
-    while (ok && pc.next()) {
-      if (pc.t0 == pc.t1) continue;
-      const Item& it = pc.it;
-      const int nt = pc.t1 - pc.t0;
-      const int f0 = it.s0.first_on(pc.t0, pc.t1), l0 = it.s0.last_on(pc.t0, pc.t1);
-      const int f1 = it.s1.first_on(pc.t0, pc.t1), l1 = it.s1.last_on(pc.t0, pc.t1);
-      if (!mbar_wait_warp(E4 ? q_ready : q_full, nq & 1, abort_flag, err) ||
-          !mbar_wait_warp(&k_full[kc & 1], (kc >> 1) & 1, abort_flag, err))
-        break;
-      ++nq;
-      tc_fence_after();
-      if (it.s0.on(pc.t0)) issue_s(0, kc);
-      if (it.s1.on(pc.t0)) issue_s(1, kc);
-      commit(&k_empty[kc & 1]);
-      if (nt == 1) commit(q_empty);
-      for (int jj = 0; jj < nt; ++jj) {
-        const int t = kc + jj, x = pc.t0 + jj;
-        const bool next = jj + 1 < nt;
-        if (!mbar_wait_warp(&v_full[t & 1], (t >> 1) & 1, abort_flag, err)) {
-          ok = false;
+      };
+      int kc = 0, nq = 0, c0 = 0, c1 = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!mbar_wait(&d_full[k % kDescs], (k / kDescs) & 1, abort_flag, err)) break;
+        const PieceDesc pc = descs[k % kDescs];
+        mbar_arrive(&d_empty[k % kDescs]);
+        if (pc.last) break;
+        if (pc.t0 == pc.t1) continue;
+        const SlotRange &s0 = pc.s[0], &s1 = pc.s[1];
+        const int nt = pc.t1 - pc.t0;
+        const int f0 = s0.first_on(pc.t0, pc.t1), l0 = s0.last_on(pc.t0, pc.t1);
+        const int f1 = s1.first_on(pc.t0, pc.t1), l1 = s1.last_on(pc.t0, pc.t1);
+        bool on0 = s0.on(pc.t0), on1 = s1.on(pc.t0);
+        if (!mbar_wait(E4 ? q_ready : q_full, nq & 1, abort_flag, err) ||
+            !mbar_wait(&k_full[kc & 1], (kc >> 1) & 1, abort_flag, err))
           break;
-        }
-        if constexpr (!E4) {
-          // v rows that no row of the item sees
-          const int key = it.tile(x) * kBN;
-          if (key + kBN > it.end || (key < it.hid1 && key + kBN > it.hid0)) {
-            uint8_t* vt = smem + C::OFF_V + (t & 1) * C::KV_BYTES;
-            for (int r = lane; r < kBN; r += 32) {
-              const int j = key + r;
-              if (j < it.end && !(j >= it.hid0 && j < it.hid1)) continue;
-#pragma unroll
-              for (int i = 0; i < C::NB * 8; ++i)
-                *reinterpret_cast<uint4*>(vt + (i >> 3) * kBN * 128 + r * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        ++nq;
+        tc_fence_after();
+        if (on0) issue_s(0, kc);
+        if (on1) issue_s(1, kc);
+        mma_commit(&k_empty[kc & 1]);
+        if (nt == 1) mma_commit(q_empty);
+        for (int jj = 0; jj < nt; ++jj) {
+          const int t = kc + jj, x = pc.t0 + jj;
+          const bool next = jj + 1 < nt, on0n = next && s0.on(x + 1), on1n = next && s1.on(x + 1);
+          if (!mbar_wait(&v_full[t & 1], (t >> 1) & 1, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          if (on0) {
+            if (!mbar_wait(&p_full[0], c0 & 1, abort_flag, err)) {
+              ok = false;
+              break;
             }
-            fence_proxy_async();
-            __syncwarp();
+            ++c0;
+            tc_fence_after();
+            issue_pv(0, t, x != f0);
+            if (x == l0) mma_commit(&o_full[0]);
           }
-        }
-        if (it.s0.on(x)) {
-          if (!mbar_wait_warp(&p_full[0], c0 & 1, abort_flag, err)) {
-            ok = false;
-            break;
+          if (next) {
+            if (!mbar_wait(&k_full[(t + 1) & 1], ((t + 1) >> 1) & 1, abort_flag, err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (on0n) issue_s(0, t + 1);
           }
-          ++c0;
-          tc_fence_after();
-          issue_pv(0, t, x != f0);
-          if (x == l0) commit(&o_full[0]);
-        }
-        if (next) {
-          if (!mbar_wait_warp(&k_full[(t + 1) & 1], ((t + 1) >> 1) & 1, abort_flag, err)) {
-            ok = false;
-            break;
+          if (on1) {
+            if (!mbar_wait(&p_full[1], c1 & 1, abort_flag, err)) {
+              ok = false;
+              break;
+            }
+            ++c1;
+            tc_fence_after();
+            issue_pv(1, t, x != f1);
+            if (x == l1) mma_commit(&o_full[1]);
           }
-          tc_fence_after();
-          if (it.s0.on(x + 1)) issue_s(0, t + 1);
-        }
-        if (it.s1.on(x)) {
-          if (!mbar_wait_warp(&p_full[1], c1 & 1, abort_flag, err)) {
-            ok = false;
-            break;
+          if (next) {
+            if (on1n) issue_s(1, t + 1);
+            mma_commit(&k_empty[(t + 1) & 1]);
+            if (jj + 2 == nt) mma_commit(q_empty);
           }
-          ++c1;
-          tc_fence_after();
-          issue_pv(1, t, x != f1);
-          if (x == l1) commit(&o_full[1]);
+          mma_commit(&v_empty[t & 1]);
+          on0 = on0n;
+          on1 = on1n;
         }
-        if (next) {
-          if (it.s1.on(x + 1)) issue_s(1, t + 1);
-          commit(&k_empty[(t + 1) & 1]);
-          if (jj + 2 == nt) commit(q_empty);
-        }
-        commit(&v_empty[t & 1]);
+        kc += nt;
       }
-      kc += nt;
+      mma_commit(drain);
+      volatile int no_abort = 0;
+      mbar_wait(drain, 0, &no_abort, err);
     }
-    commit(drain);
-    volatile int no_abort = 0;
-    mbar_wait_warp(drain, 0, &no_abort, err);
   } else if (warp >= 10) {
-    // ---------------- codes to fp16 (E4): warp 10 takes even chunks, warp 11 odd ones ----------------
+    // ---------------- V: codes to fp16, chunk by chunk in turn (E4); else the hidden rows of border tiles ----------------
     if constexpr (E4) {
       const int me = warp - 10;
       int nt = 0;
       bool ok = true;
-      Pieces pc(m, x0, x1);
-      while (ok && pc.next()) {
-        const Item& it = pc.it;
+      PieceDesc* d;
+      for (int k = 0; ok && piece(k, d); ++k) {
+        const PieceDesc pc = *d;
+        done(k);
         for (int x = pc.t0; ok && x < pc.t1; ++x, ++nt) {
           const int st = nt & 1;
-          const uint32_t ph = (nt >> 1) & 1;
-          const int tile_key = it.tile(x) * kBN;
+          const int tile_key = pc.key(x);
 #pragma unroll 1
-          for (int q = me; q < 2 * kBN / kChunk; q += 2) {
-            const int half = q / (kBN / kChunk), ch = q % (kBN / kChunk);
-            const int rs = q;                                    // kRaw chunks: one tile of K and V
-            static_assert(kRaw == 2 * kBN / kChunk, "a ring round per tile");
-            if (!mbar_wait_warp(half ? &v_empty[st] : &k_empty[st], ph ^ 1u, abort_flag, err) ||
-                !mbar_wait_warp(&raw_full[rs], nt & 1, abort_flag, err)) {
+          for (int ch = me; ch < kBN / kChunk; ch += kConv) {
+            const int n = nt * (kBN / kChunk) + ch, rs = n % kRaw;     // running chunk
+            if (!mbar_wait_warp(&v_empty[st], ((nt >> 1) & 1) ^ 1u, abort_flag, err) ||
+                !mbar_wait_warp(&raw_full[rs], (n / kRaw) & 1, abort_flag, err)) {
               ok = false;
               break;
             }
             const uint32_t raw = smem_u32(smem) + C::OFF_RAW + rs * C::RAW;
-            const uint32_t dst = smem_u32(smem) + (half ? C::OFF_V : C::OFF_K) + st * C::KV_BYTES;
+            const uint32_t dst = smem_u32(smem) + C::OFF_V + st * C::V_BYTES;
             const int key0 = tile_key + ch * kChunk;
-            const bool border = half && (key0 + kChunk > it.end || (key0 < it.hid1 && key0 + kChunk > it.hid0));
+            const bool border = key0 + kChunk > pc.end || (key0 < pc.hid1 && key0 + kChunk > pc.hid0);
             // 16-byte pieces of 16 codes, PPR per row.  The four lanes of a half
             // quarter-warp take one half of a row, the next four the other half
             // of its neighbour, so that reads and writes spread over the banks.
@@ -674,7 +786,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
               const int row = i * RPS + r0;
               if (border) {
                 const int j = key0 + row;
-                if (j >= it.end || (j >= it.hid0 && j < it.hid1)) w[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (j >= pc.end || (j >= pc.hid0 && j < pc.hid1)) w[i] = make_uint4(0u, 0u, 0u, 0u);
               }
               uint4 lo, hi;
               codes4(w[i].x, lo.x, lo.y);
@@ -689,10 +801,38 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(half ? &v_full[st] : &k_full[st]);
+              mbar_arrive(&v_full[st]);
               mbar_arrive(&raw_empty[rs]);
             }
           }
+        }
+      }
+    } else {
+      int nt = 0, n_fix[2] = {0, 0};
+      bool ok = true;
+      PieceDesc* d;
+      for (int k = 0; ok && piece(k, d); ++k) {
+        const PieceDesc pc = *d;
+        done(k);
+        for (int x = pc.t0; x < pc.t1; ++x, ++nt) {
+          const int key = pc.key(x), st = nt & 1;
+          if (!pc.border(key)) continue;
+          if (!mbar_wait_warp(&fix_full[st], n_fix[st] & 1, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          ++n_fix[st];
+          const uint32_t vt = smem_u32(smem) + C::OFF_V + st * C::V_BYTES;
+          for (int r = lane; r < kBN; r += 32) {
+            const int j = key + r;
+            if (j < pc.end && !(j >= pc.hid0 && j < pc.hid1)) continue;
+#pragma unroll
+            for (int i = 0; i < C::NB * 8; ++i)
+              sts128(vt + (i >> 3) * kBN * 128 + r * 128 + (i & 7) * 16, make_uint4(0u, 0u, 0u, 0u));
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_full[st]);
         }
       }
     }
@@ -704,18 +844,16 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
     const uint32_t s_col = lane_base + g * kBN, o_col = lane_base + C::TMEM_O + g * DH;
     int c = 0, nt = 0, nq = 0, no = 0;          // this slot's tiles; key tiles, pieces with keys, outputs
     bool ok = true;
-    Pieces pc(m, x0, x1);
-    while (ok && pc.next()) {
-      const Item& it = pc.it;
-      const SlotRange s_r = g ? it.s1 : it.s0;
-      const int tok = s_r.tok0 + r / G;
-      const bool valid = r < s_r.rows;
-      const int qp = valid ? s_r.p0 + r / G : -1;
-      const int f_on = s_r.first_on(pc.t0, pc.t1), l_on = s_r.last_on(pc.t0, pc.t1);
+    PieceDesc* d;
+    for (int pk = 0; ok && piece(pk, d); ++pk) {
+      const SlotRange& s_r = d->s[g];
+      const int t0 = d->t0, t1 = d->t1;
+      const int qp = r < s_r.rows ? s_r.p0 + r / G : -1;
+      const int f_on = s_r.first_on(t0, t1), l_on = s_r.last_on(t0, t1);
       float zs = fabsf(a.scale_log2);
       if constexpr (E4) {
-        // this row of Q, as fp16 with its largest element in [0.5, 1)
-        if (pc.t0 < pc.t1) {
+        // this row of Q as two e4m3 terms, its largest element in [128, 256)
+        if (t0 < t1) {
           if (!mbar_wait_warp(q_full, nq & 1, abort_flag, err)) {
             ok = false;
             break;
@@ -732,15 +870,27 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
               for (int j = 0; j < 4; ++j)
                 amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xffff0000u))));
             }
-            const float fr = pow2_frame(amax);
+            // an infinity must not saturate: its row becomes NaN
+            const float fr = amax <= 3.402823466e38f ? pow2_frame(fmaxf(amax, 0x1p-118f)) * 256.f : NAN;
             zs /= fr;                           // exact
+            const uint32_t t1 = smem_u32(smem) + C::OFF_QT + g * C::Q_BYTES, t2 = t1 + C::QT_BYTES;
 #pragma unroll
-            for (int i = 0; i < C::NB * 8; ++i) {
-              uint32_t* u = &w[i].x;
+            for (int i = 0; i < DH / 16; ++i) { // 16 elements: one 16-byte piece of each term
+              uint4 a1, a2;
+              uint32_t *u1 = &a1.x, *u2 = &a2.x;
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                u[j] = pack16<true>(__uint_as_float(u[j] << 16) * fr, __uint_as_float(u[j] & 0xffff0000u) * fr);
-              sts128(qrow + (i >> 3) * kBM * 128 + (((i ^ r) & 7) << 4), w[i]);
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t* u = &w[2 * i + (j >> 1)].x + 2 * (j & 1);
+                float v[4] = {__uint_as_float(u[0] << 16) * fr, __uint_as_float(u[0] & 0xffff0000u) * fr,
+                              __uint_as_float(u[1] << 16) * fr, __uint_as_float(u[1] & 0xffff0000u) * fr};
+                const uint32_t c0 = e4m3x2(v[0], v[1]), c1 = e4m3x2(v[2], v[3]);
+                const float2 f0 = from_e4m3x2(c0), f1 = from_e4m3x2(c1);
+                u1[j] = c0 | c1 << 16;
+                u2[j] = e4m3x2(v[0] - f0.x, v[1] - f0.y) | e4m3x2(v[2] - f1.x, v[3] - f1.y) << 16;
+              }
+              const uint32_t at = DH == 128 ? r * 128 + (((i ^ r) & 7) << 4) : r * 64 + (((i ^ (r >> 1)) & 3) << 4);
+              sts128(t1 + at, a1);
+              sts128(t2 + at, a2);
             }
           }
           fence_proxy_async();
@@ -748,12 +898,13 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
           if (lane == 0) mbar_arrive(q_ready);
         }
       }
-      if (pc.t0 < pc.t1) ++nq;
+      if (t0 < t1) ++nq;
       float m_used = -INFINITY, l = 0.f;
-      const int wlo = win_lo(qp, a.window);
-      for (int x = pc.t0; x < pc.t1; ++x) {
-        const int tn = nt + x - pc.t0;          // the CTA's running key tile
-        if (!s_r.on(x)) continue;
+      const int wlo = win_lo(qp, a.window), p0m = s_r.p0 - (kBN - 1), w1 = win_lo(s_r.p1, a.window);
+      const int ns = d->ns, shift = d->wl - ns, ia = s_r.ia, ib = s_r.ib, tn0 = nt - t0;
+      // the slot's tiles: every list position but those in [ia, ib)
+      for (int x = f_on; x >= 0 && x <= l_on; x = x + 1 >= ia && x + 1 < ib ? ib : x + 1) {
+        const int tn = tn0 + x;                 // the CTA's running key tile
         if (!mbar_wait_warp(&s_full[g], c & 1, abort_flag, err)) {
           ok = false;
           break;
@@ -765,6 +916,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
           }
         }
         tc_fence_after();
+        const int key = (x < ns ? x : x + shift) * kBN;
+        const uint32_t scp = smem_u32(sc) + (tn % kScTiles) * 64;
         float s[kBN];
 #pragma unroll
         for (int cc = 0; cc < kBN; cc += 16) {
@@ -774,32 +927,17 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
           for (int i = 0; i < 16; ++i) s[cc + i] = __uint_as_float(u[i]);
         }
         tmem_wait_ld();
-        if (m.negate) {
-#pragma unroll
-          for (int cc = 0; cc < kBN; ++cc) s[cc] = -s[cc];
-        }
-        const int key = it.tile(x) * kBN;
-        if (key + kBN - 1 > s_r.p0) {           // keys ahead of a row
+        if (key > p0m) {                        // keys ahead of a row
           const int lim = qp - key;
 #pragma unroll
           for (int cc = 0; cc < kBN; ++cc)
             if (cc > lim) s[cc] = -INFINITY;
         }
-        if (key < win_lo(s_r.p1, a.window) && key + kBN > a.sinks) {       // keys behind a row's window
+        if (key < w1 && key + kBN > a.sinks) {  // keys behind a row's window
           const int wl = wlo - key, sl = a.sinks - key;
 #pragma unroll
           for (int cc = 0; cc < kBN; ++cc)
             if (cc < wl && cc >= sl) s[cc] = -INFINITY;
-        }
-        float ksc[8], vsc[8];                   // E4: the block scales of the tile's eight runs
-        if constexpr (E4) {
-          const uint32_t scp = smem_u32(sc) + (tn % kScTiles) * 64;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float4 kq = lds_f4(scp + 16 * i), vq = lds_f4(scp + 32 + 16 * i);
-            ksc[4 * i] = kq.x, ksc[4 * i + 1] = kq.y, ksc[4 * i + 2] = kq.z, ksc[4 * i + 3] = kq.w;
-            vsc[4 * i] = vq.x, vsc[4 * i + 1] = vq.y, vsc[4 * i + 2] = vq.z, vsc[4 * i + 3] = vq.w;
-          }
         }
         float mx;
         if constexpr (!E4) {
@@ -822,7 +960,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
               v0 = fmax3(v0, s[16 * q + i], s[16 * q + i + 1]);
               v1 = fmax3(v1, s[16 * q + i + 2], s[16 * q + i + 3]);
             }
-            mx = fmaxf(mx, fmaf(fmaxf(v0, v1), zs * ksc[q], scale_exp(vsc[q])));
+            const float2 kv = lds_f2(scp + 8 * q);
+            mx = fmaxf(mx, fmaf(fmaxf(v0, v1), zs * kv.x, scale_exp(kv.y)));
           }
         }
         const float m_new = fmaxf(m_used, mx);
@@ -860,10 +999,11 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
           float2 f2 = make_float2(zs, zs), n2 = make_float2(-msub, -msub);
           float inv = 1.f;
           if constexpr (E4) {
-            const float f = zs * ksc[cc / 16], nn = scale_exp(vsc[cc / 16]) - msub;
+            const float2 kv = lds_f2(scp + cc / 2);
+            const float f = zs * kv.x, nn = scale_exp(kv.y) - msub;
             f2 = make_float2(f, f);
             n2 = make_float2(nn, nn);
-            inv = scale_inv(vsc[cc / 16]);
+            inv = scale_inv(kv.y);
             sum2[0] = sum2[1] = make_float2(0.f, 0.f);
           }
           uint32_t u[8];
@@ -888,12 +1028,16 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         ++c;
       }
       if (!ok) break;
-      nt += pc.t1 - pc.t0;
-      if (s_r.rows == 0) continue;
-      const size_t orow = ((size_t)pc.at.b * a.n + tok) * a.H + pc.at.h * G + r % G;
+      nt += t1 - t0;
+      const int where = d->where, rows = s_r.rows;
+      const size_t orow = ((size_t)d->b * a.n + s_r.tok0 + r / G) * a.H + d->h * G + r % G;
+      const size_t flag = ((size_t)d->b * a.c.Hkv + d->h) * 2 * m.pairs + 2 * d->p + g;
+      done(pk);
+      if (rows == 0) continue;
+      const bool valid = r < rows;
       if (f_on < 0) {                           // no tile of this piece
-        if (pc.where >= 0) {
-          m.part[((size_t)(pc.where * 2 + g) * (DH / 4 + 1)) * kBM + r] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        if (where >= 0) {
+          m.part[((size_t)(where * 2 + g) * (DH / 4 + 1)) * kBM + r] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
         } else if (valid) {
           uint4* dst = reinterpret_cast<uint4*>((bf16*)a.o + orow * DH);
 #pragma unroll
@@ -907,8 +1051,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
       }
       ++no;
       tc_fence_after();
-      if (pc.where >= 0) {
-        float4* dst = m.part + ((size_t)(pc.where * 2 + g) * (DH / 4 + 1)) * kBM + r;
+      if (where >= 0) {
+        float4* dst = m.part + ((size_t)(where * 2 + g) * (DH / 4 + 1)) * kBM + r;
         dst[0] = make_float4(m_used, l, 0.f, 0.f);
 #pragma unroll 2
         for (int cc = 0; cc < DH; cc += 16) {
@@ -944,7 +1088,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
           }
         }
         if (valid && !(probe == 0.f))
-          m.flags[((size_t)pc.at.b * a.c.Hkv + pc.at.h) * 2 * m.pairs + 2 * pc.at.p + g] = 1;
+          m.flags[flag] = 1;
       }
       tc_fence_before();
     }
@@ -1123,17 +1267,20 @@ cudaError_t run(const AttnArgs& a, void* ws, cudaStream_t s) {
   m.pre = (long long*)ws;
   m.flags = (uint8_t*)ws + L.flags;
   m.part = (float4*)((uint8_t*)ws + L.part);
-  m.box = E4 ? kChunk : kBN;
-  if (a.c.bt)
-    while (a.c.ps % m.box) m.box /= 2;           // page_size is a multiple of 16
+  m.box = kBN;
+  m.vbox = kChunk;
+  if (a.c.bt) {                                  // a box lies in one page (page_size is a multiple of 16)
+    while (a.c.ps % m.box) m.box /= 2;
+    while (a.c.ps % m.vbox) m.vbox /= 2;
+  }
   CUtensorMap tq, tk, tv;
   cudaError_t e = tmap_q(&tq, a, G);
   if (e != cudaSuccess) return e;
   const uint64_t planes = a.c.bt ? (uint64_t)a.c.num_pages * a.c.Hkv : (uint64_t)a.c.B * a.c.Hkv;
   const uint64_t rows = a.c.bt ? (uint64_t)a.c.ps : (uint64_t)a.c.T;
   if constexpr (E4) {
-    e = make_tmap_rows(&tk, 1, a.c.k, planes, rows, DH, DH, m.box, false);
-    if (e == cudaSuccess) e = make_tmap_rows(&tv, 1, a.c.v, planes, rows, DH, DH, m.box, false);
+    e = make_tmap_rows(&tk, 1, a.c.k, planes, rows, DH, DH, m.box);
+    if (e == cudaSuccess) e = make_tmap_rows(&tv, 1, a.c.v, planes, rows, DH, DH, m.vbox, false);
   } else {
     e = make_tmap_rows(&tk, 2, a.c.k, planes, rows, DH, 64, m.box);
     if (e == cudaSuccess) e = make_tmap_rows(&tv, 2, a.c.v, planes, rows, DH, 64, m.box);

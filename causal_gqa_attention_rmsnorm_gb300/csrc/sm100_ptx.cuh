@@ -230,6 +230,17 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uin
       : "memory");
 }
 
+// The same with 8-bit floating-point operands (kind::f8f6f4, 32 elements of K).
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Batched issue of the MMAs of one tile, for an issuing thread that must spend
 // as few instructions per MMA as possible: descriptors are passed as their low
 // and high 32-bit words, each MMA's operand offset is an immediate added to the
@@ -332,6 +343,17 @@ __device__ __forceinline__ uint64_t desc_kmajor_sw128(uint32_t saddr) {
   return d;
 }
 
+// The same for rows of 64 bytes with the 64-byte swizzle, 8-row groups 512 bytes apart.
+__device__ __forceinline__ uint64_t desc_kmajor_sw64(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)(512u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)4 << 61;                  // 64-byte swizzle
+  return d;
+}
+
 // Descriptor of an MN-major operand tile stored as 128-byte rows along MN,
 // swizzled, with K rows 128 bytes apart: 8-row K groups are `sbo` bytes apart
 // and 64-element MN blocks `lbo` bytes apart.
@@ -355,6 +377,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn = fals
          | ((b_mn ? 1u : 0u) << 16)         // B major-ness
          | ((uint32_t)(N >> 3) << 17)       // N / 8
          | ((uint32_t)(M >> 4) << 24);      // M / 16
+}
+
+// Instruction descriptor, kind::f8f6f4 with e4m3 A and B, both K-major, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // ---- CTA pairs (cta_group::2) --------------------------------------------
