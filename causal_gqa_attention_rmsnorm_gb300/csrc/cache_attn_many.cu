@@ -75,7 +75,7 @@ template <int DH, bool E4> struct ManyCfg {
   static constexpr uint32_t OFF_K = OFF_QT + 2 * Q_BYTES;
   static constexpr uint32_t OFF_V = OFF_K + 2 * K_BYTES;
   static constexpr uint32_t OFF_RAW = OFF_V + 2 * V_BYTES;
-  static constexpr uint32_t OFF_SC = OFF_RAW + (E4 ? kRaw * RAW : 0);      // [kScTiles][8 runs]{K, V}
+  static constexpr uint32_t OFF_SC = OFF_RAW + (E4 ? kRaw * RAW : 0);      // [kScTiles][8 runs]{K scale, log2 of V's}
   static constexpr uint32_t OFF_BAR = OFF_SC + (E4 ? kScTiles * 64 : 0);
   static constexpr uint32_t OFF_DESC = OFF_BAR + 512;
   static constexpr size_t SMEM = OFF_DESC + 512 + 1024;
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         const uint32_t loads = __ballot_sync(0xffffffffu, go_k), vloads = __ballot_sync(0xffffffffu, go_v);
         if constexpr (E4) {
           const int sl = nt % kScTiles;
-          if (mine) reinterpret_cast<float2*>(sc)[sl * 8 + lane] = make_float2(ks, vs);
+          if (mine) reinterpret_cast<float2*>(sc)[sl * 8 + lane] = make_float2(ks, scale_exp(vs));
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[sl]);
         }
@@ -778,25 +778,29 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
               r0 = (r2 & ~1) + (c >> 2);
               pc0 = (c & 3) + 4 * ((r2 & 1) ^ (c >> 2));
             }
-            uint4 w[STEPS];
+            constexpr int BATCH = 4;
+#pragma unroll 1
+            for (int i0 = 0; i0 < STEPS; i0 += BATCH) {
+              uint4 w[BATCH];
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) w[i] = lds128(raw + (i * RPS + r0) * DH + pc0 * 16);
+              for (int i = 0; i < BATCH; ++i) w[i] = lds128(raw + ((i0 + i) * RPS + r0) * DH + pc0 * 16);
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-              const int row = i * RPS + r0;
-              if (border) {
-                const int j = key0 + row;
-                if (j >= pc.end || (j >= pc.hid0 && j < pc.hid1)) w[i] = make_uint4(0u, 0u, 0u, 0u);
+              for (int i = 0; i < BATCH; ++i) {
+                const int row = (i0 + i) * RPS + r0;
+                if (border) {
+                  const int j = key0 + row;
+                  if (j >= pc.end || (j >= pc.hid0 && j < pc.hid1)) w[i] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                uint4 lo, hi;
+                codes4(w[i].x, lo.x, lo.y);
+                codes4(w[i].y, lo.z, lo.w);
+                codes4(w[i].z, hi.x, hi.y);
+                codes4(w[i].w, hi.z, hi.w);
+                const int r = ch * kChunk + row, c = 2 * pc0;           // 16-byte piece of the fp16 row
+                const uint32_t base = dst + (c >> 3) * kBN * 128 + r * 128;
+                sts128(base + (((c ^ r) & 7) << 4), lo);
+                sts128(base + ((((c + 1) ^ r) & 7) << 4), hi);
               }
-              uint4 lo, hi;
-              codes4(w[i].x, lo.x, lo.y);
-              codes4(w[i].y, lo.z, lo.w);
-              codes4(w[i].z, hi.x, hi.y);
-              codes4(w[i].w, hi.z, hi.w);
-              const int r = ch * kChunk + row, c = 2 * pc0;             // 16-byte piece of the fp16 row
-              const uint32_t base = dst + (c >> 3) * kBN * 128 + r * 128;
-              sts128(base + (((c ^ r) & 7) << 4), lo);
-              sts128(base + ((((c + 1) ^ r) & 7) << 4), hi);
             }
             fence_proxy_async();
             __syncwarp();
@@ -905,42 +909,80 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
       // the slot's tiles: every list position but those in [ia, ib)
       for (int x = f_on; x >= 0 && x <= l_on; x = x + 1 >= ia && x + 1 < ib ? ib : x + 1) {
         const int tn = tn0 + x;                 // the CTA's running key tile
-        if (!mbar_wait_warp(&s_full[g], c & 1, abort_flag, err)) {
-          ok = false;
-          break;
-        }
         if constexpr (E4) {
           if (!mbar_wait_warp(&sc_full[tn % kScTiles], (tn / kScTiles) & 1, abort_flag, err)) {
             ok = false;
             break;
           }
         }
+        if (!mbar_wait_warp(&s_full[g], c & 1, abort_flag, err)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         const int key = (x < ns ? x : x + shift) * kBN;
-        const uint32_t scp = smem_u32(sc) + (tn % kScTiles) * 64;
-        float s[kBN];
+        const bool ahead = key > p0m, behind = key < w1 && key + kBN > a.sinks;
+        // m_used (and with it l and O) follows the row's new maximum when that grew
+        // by more than 2^kRescale; false when a wait ran out
+        auto follow = [&](float mx) -> bool {
+          const float m_new = fmaxf(m_used, mx);
+          bool need = false;
+          if (x == f_on)
+            m_used = m_new;
+          else
+            need = m_new > m_used + kRescale;
+          if (__any_sync(0xffffffffu, need)) {
+            if (!mbar_wait_warp(&pv_done[g], (c - 1) & 1, abort_flag, err)) return false;
+            tc_fence_after();
+            const float factor = need ? ex2_approx(m_used - m_new) : 1.f;
+#pragma unroll 1
+            for (int cc = 0; cc < DH; cc += 8) {
+              uint32_t u[8];
+              tmem_ld8(o_col + cc, u);
+              tmem_wait_ld();
 #pragma unroll
-        for (int cc = 0; cc < kBN; cc += 16) {
-          uint32_t u[16];
-          tmem_ld16(s_col + cc, u);
+              for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * factor);
+              tmem_st8(o_col + cc, u);
+            }
+            tmem_wait_st();
+            if (need) {
+              l *= factor;
+              m_used = m_new;
+            }
+          }
+          return true;
+        };
+        if (ahead || behind) {
+          // A border tile: its hidden scores become -inf in tensor memory first, in a
+          // short loop, so that the common path stays small (the instruction cache
+          // holds the loops of all roles only just: with masks in line, or a second
+          // copy for border tiles, all tiles ran 15 to 20% slower).
+          const int lim = qp - key, wl = wlo - key, sl = a.sinks - key;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kBN; c0 += 16) {
+            uint32_t u[16];
+            tmem_ld16(s_col + c0, u);
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) s[cc + i] = __uint_as_float(u[i]);
+            for (int i = 0; i < 16; ++i) {
+              asm volatile("" : "+r"(u[i]));
+              const int cc = c0 + i;
+              if (cc > lim || (cc < wl && cc >= sl)) u[i] = 0xff800000u;
+            }
+            tmem_st16(s_col + c0, u);
+          }
+          tmem_wait_st();
         }
-        tmem_wait_ld();
-        if (key > p0m) {                        // keys ahead of a row
-          const int lim = qp - key;
-#pragma unroll
-          for (int cc = 0; cc < kBN; ++cc)
-            if (cc > lim) s[cc] = -INFINITY;
-        }
-        if (key < w1 && key + kBN > a.sinks) {  // keys behind a row's window
-          const int wl = wlo - key, sl = a.sinks - key;
-#pragma unroll
-          for (int cc = 0; cc < kBN; ++cc)
-            if (cc < wl && cc >= sl) s[cc] = -INFINITY;
-        }
-        float mx;
         if constexpr (!E4) {
+          float s[kBN];
+#pragma unroll
+          for (int cc = 0; cc < kBN; cc += 16) {
+            uint32_t u[16];
+            tmem_ld16(s_col + cc, u);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[cc + i] = __uint_as_float(u[i]);
+          }
+          tmem_wait_ld();
           float m4[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -949,77 +991,103 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
             for (int cc = 8 + 2 * i; cc < kBN; cc += 8) v = fmax3(v, s[cc], s[cc + 1]);
             m4[i] = v;
           }
-          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * zs;
-        } else {
-          mx = -INFINITY;
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            float v0 = fmaxf(s[16 * q], s[16 * q + 1]), v1 = fmaxf(s[16 * q + 2], s[16 * q + 3]);
-#pragma unroll
-            for (int i = 4; i < 16; i += 4) {
-              v0 = fmax3(v0, s[16 * q + i], s[16 * q + i + 1]);
-              v1 = fmax3(v1, s[16 * q + i + 2], s[16 * q + i + 3]);
-            }
-            const float2 kv = lds_f2(scp + 8 * q);
-            mx = fmaxf(mx, fmaf(fmaxf(v0, v1), zs * kv.x, scale_exp(kv.y)));
-          }
-        }
-        const float m_new = fmaxf(m_used, mx);
-        bool need = false;
-        if (x == f_on)
-          m_used = m_new;
-        else
-          need = m_new > m_used + kRescale;
-        if (__any_sync(0xffffffffu, need)) {
-          if (!mbar_wait_warp(&pv_done[g], (c - 1) & 1, abort_flag, err)) {
+          if (!follow(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * zs)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const float factor = need ? ex2_approx(m_used - m_new) : 1.f;
-#pragma unroll 1
-          for (int cc = 0; cc < DH; cc += 8) {
+          const float msub = m_used == -INFINITY ? 0.f : m_used;
+          const float2 f2 = make_float2(zs, zs), n2 = make_float2(-msub, -msub);
+          float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int cc = 0; cc < kBN; cc += 16) {
             uint32_t u[8];
-            tmem_ld8(o_col + cc, u);
-            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * factor);
-            tmem_st8(o_col + cc, u);
+            for (int i = 0; i < 8; ++i) {
+              const float2 arg = __ffma2_rn(make_float2(s[cc + 2 * i], s[cc + 2 * i + 1]), f2, n2);
+              const float2 p = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
+              sum2[i & 1] = __fadd2_rn(sum2[i & 1], p);
+              u[i] = pack16<E4>(p.x, p.y);
+            }
+            tmem_st8(s_col + cc / 2, u);
           }
-          tmem_wait_st();
-          if (need) {
-            l *= factor;
-            m_used = m_new;
-          }
-        }
-        const float msub = m_used == -INFINITY ? 0.f : m_used;
-        float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int cc = 0; cc < kBN; cc += 16) {
-          float2 f2 = make_float2(zs, zs), n2 = make_float2(-msub, -msub);
-          float inv = 1.f;
-          if constexpr (E4) {
-            const float2 kv = lds_f2(scp + cc / 2);
-            const float f = zs * kv.x, nn = scale_exp(kv.y) - msub;
-            f2 = make_float2(f, f);
-            n2 = make_float2(nn, nn);
-            inv = scale_inv(kv.y);
-            sum2[0] = sum2[1] = make_float2(0.f, 0.f);
-          }
-          uint32_t u[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 arg = __ffma2_rn(make_float2(s[cc + 2 * i], s[cc + 2 * i + 1]), f2, n2);
-            const float2 p = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
-            sum2[i & 1] = __fadd2_rn(sum2[i & 1], p);
-            u[i] = pack16<E4>(p.x, p.y);
-          }
-          if constexpr (E4) l = fmaf((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y), inv, l);
-          tmem_st8(s_col + cc / 2, u);
-        }
-        if constexpr (!E4) {
           const float2 s01 = __fadd2_rn(sum2[0], sum2[1]);
           l += s01.x + s01.y;
+        } else {
+          // 32 columns at a time, read twice (for the maximum, for the weights):
+          // with the scales a whole row does not fit in registers
+          const uint32_t scp = smem_u32(sc) + (tn % kScTiles) * 64;
+          auto load = [&](uint32_t (&v)[32], int c0) {
+            tmem_ld16(s_col + c0, *reinterpret_cast<uint32_t(*)[16]>(v));
+            tmem_ld16(s_col + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+          };
+          auto arrived = [](uint32_t (&v)[32]) {  // no use of v moves ahead of the wait
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
+          };
+          float mx = -INFINITY;
+          // (kv: score factor and exponent of V of the two runs)
+          auto top = [&](uint32_t (&v)[32], const float4& kv) {
+#pragma unroll
+            for (int q = 0; q < 32; q += 16) {
+              float v0 = fmaxf(__uint_as_float(v[q]), __uint_as_float(v[q + 1]));
+              float v1 = fmaxf(__uint_as_float(v[q + 2]), __uint_as_float(v[q + 3]));
+#pragma unroll
+              for (int i = 4; i < 16; i += 4) {
+                v0 = fmax3(v0, __uint_as_float(v[q + i]), __uint_as_float(v[q + i + 1]));
+                v1 = fmax3(v1, __uint_as_float(v[q + i + 2]), __uint_as_float(v[q + i + 3]));
+              }
+              mx = fmaxf(mx, fmaf(fmaxf(v0, v1), zs * (q ? kv.z : kv.x), q ? kv.w : kv.y));
+            }
+          };
+          uint32_t va[32], vb[32];
+          load(va, 0);
+          arrived(va);
+#pragma unroll 1
+          for (int c0 = 0; c0 < kBN; c0 += 64) {
+            load(vb, c0 + 32);
+            const float4 ka = lds_f4(scp + c0 / 2), kb = lds_f4(scp + c0 / 2 + 16);
+            top(va, ka);
+            arrived(vb);
+            load(va, (c0 + 64) & (kBN - 1));    // the last time: the first columns again
+            top(vb, kb);
+            arrived(va);
+          }
+          if (!follow(mx)) {
+            ok = false;
+            break;
+          }
+          const float msub = m_used == -INFINITY ? 0.f : m_used;
+          auto weights = [&](uint32_t (&v)[32], int c0, const float4& kv) {
+#pragma unroll
+            for (int q = 0; q < 32; q += 16) {
+              const float f = zs * (q ? kv.z : kv.x), e = q ? kv.w : kv.y, nn = e - msub;
+              const float2 f2 = make_float2(f, f), n2 = make_float2(nn, nn);
+              float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+              uint32_t u[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 arg = __ffma2_rn(
+                    make_float2(__uint_as_float(v[q + 2 * i]), __uint_as_float(v[q + 2 * i + 1])), f2, n2);
+                const float2 p = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
+                sum2[i & 1] = __fadd2_rn(sum2[i & 1], p);
+                u[i] = pack16<E4>(p.x, p.y);
+              }
+              const float2 s01 = __fadd2_rn(sum2[0], sum2[1]);
+              l = fmaf(s01.x + s01.y, __uint_as_float((uint32_t)(127 - (int)e) << 23), l);
+              tmem_st8(s_col + (c0 + q) / 2, u);          // over columns read for the last time
+            }
+          };
+#pragma unroll 1
+          for (int c0 = 0; c0 < kBN; c0 += 64) {
+            load(vb, c0 + 32);
+            const float4 ka = lds_f4(scp + c0 / 2), kb = lds_f4(scp + c0 / 2 + 16);
+            weights(va, c0, ka);
+            arrived(vb);
+            load(va, 64);                       // (the second time of no use)
+            weights(vb, c0 + 32, kb);
+            arrived(va);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
