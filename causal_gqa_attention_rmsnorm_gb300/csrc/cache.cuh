@@ -153,25 +153,36 @@ cudaError_t launch_cache_attn_few(const AttnArgs& a, void* ws, cudaStream_t s);
 size_t cache_attn_many_workspace(const AttnArgs& a);
 cudaError_t launch_cache_attn_many(const AttnArgs& a, void* ws, cudaStream_t s);
 
-// One query row by one warp, as the formula reads: keys it does not see are not
-// touched at all.  q points to dh elements; every lane returns with
-// out[u] = o[lane + 32u].  fp32 queries, and rows whose fast result is not
-// finite (a weight of 0 times an infinity or NaN in a row that the query does
-// not see, or a value that really is not finite).
-__device__ __forceinline__ float cache_elem(const CacheView& c, const void* base, long long row, int e) {
-  if (c.dtype == TB_F32) return __ldg((const float*)base + row * c.dh + e);
-  if (c.dtype == TB_BF16) return to_f(((const bf16*)base)[row * c.dh + e]);
-  const uint8_t code = __ldg((const uint8_t*)base + row * c.dh + e);
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)code));
-  float f;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(h));
-  return f;
+// One bf16 query row by one warp, as the formula reads: keys it does not see are
+// not touched at all.  For rows whose fast result is not finite (a weight of 0
+// times an infinity or NaN in a row that the query does not see, or a value that
+// really is not finite).  q points to DH elements; every lane returns with
+// out[u] = o[lane·DH/32 + u].
+__device__ __forceinline__ void eight_of(const CacheView& c, const void* base, long long row, int e, float (&x)[8]) {
+  if (c.dtype == TB_BF16) {
+    Vec16<bf16> v;
+    v.raw = *reinterpret_cast<const uint4*>((const bf16*)base + row * c.dh + e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v.get(i);
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2*>((const uint8_t*)base + row * c.dh + e);
+    uint32_t h[4];
+    codes4(w.x, h[0], h[1]);
+    codes4(w.y, h[2], h[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+          : "=f"(x[2 * i]), "=f"(x[2 * i + 1])
+          : "r"(h[i]));
+  }
 }
-template <typename TQ>
-__device__ __noinline__ void attend_row(const AttnArgs& a, int b, int hkv, int pos, const TQ* q, float (&out)[4]) {
-  const int lane = threadIdx.x & 31, dh = a.c.dh;
-  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+template <int DH>
+__device__ __noinline__ void attend_row(const AttnArgs& a, int b, int hkv, int pos, const bf16* q, float (&out)[DH / 32]) {
+  constexpr int D = DH / 32;              // output dims per lane: part of one eight
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.f, acc[D];
+#pragma unroll
+  for (int u = 0; u < D; ++u) acc[u] = 0.f;
   const int lo = win_lo(pos, a.window);
   const int sinks = min(a.sinks, lo);
   const int nkeys = pos < 0 ? 0 : sinks + pos + 1 - lo;
@@ -183,7 +194,14 @@ __device__ __noinline__ void attend_row(const AttnArgs& a, int b, int hkv, int p
     const long long row = in ? cache_row(a.c, b, hkv, j, &sc) : -1;
     float s = 0.f;
     if (row >= 0) {
-      for (int e = 0; e < dh; ++e) s = fmaf(to_f(q[e]), cache_elem(a.c, a.c.k, row, e), s);
+      for (int e = 0; e < DH; e += 8) {
+        Vec16<bf16> qv;
+        qv.raw = *reinterpret_cast<const uint4*>(q + e);
+        float k[8];
+        eight_of(a.c, a.c.k, row, e, k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s = fmaf(qv.get(i), k[i], s);
+      }
       if (a.c.dtype == TB_E4M3) s *= a.c.ks[sc];
     }
     s = in ? s * a.scale_log2 : -INFINITY;
@@ -197,23 +215,23 @@ __device__ __noinline__ void attend_row(const AttnArgs& a, int b, int hkv, int p
     m = mn;
     l = l * f + warp_sum(p);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) acc[u] *= f;
-    const float vs = row >= 0 && a.c.dtype == TB_E4M3 ? a.c.vs[sc] : 1.f;
+    for (int u = 0; u < D; ++u) acc[u] *= f;
+    const float pv = p * (row >= 0 && a.c.dtype == TB_E4M3 ? a.c.vs[sc] : 1.f);
     const int steps = min(32, nkeys - j0);
     for (int k = 0; k < steps; ++k) {
-      const float pk = __shfl_sync(0xffffffffu, p, k) * __shfl_sync(0xffffffffu, vs, k);
+      const float pk = __shfl_sync(0xffffffffu, pv, k);
       const long long rk = __shfl_sync(0xffffffffu, row, k);
       if (rk < 0) continue;
+      float v[8];
+      eight_of(a.c, a.c.v, rk, lane * D & ~7, v);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int e = lane + 32 * u;
-        if (e < dh) acc[u] = fmaf(pk, cache_elem(a.c, a.c.v, rk, e), acc[u]);
-      }
+      for (int i = 0; i < 8; ++i)
+        if ((i & ~(D - 1)) == (lane * D & 7)) acc[i & (D - 1)] = fmaf(pk, v[i], acc[i & (D - 1)]);
     }
   }
   const bool none = l == 0.f;             // no visible key
 #pragma unroll
-  for (int u = 0; u < 4; ++u) out[u] = none ? 0.f : acc[u] / l;
+  for (int u = 0; u < D; ++u) out[u] = none ? 0.f : acc[u] / l;
 }
 
 // cache_attn.cu

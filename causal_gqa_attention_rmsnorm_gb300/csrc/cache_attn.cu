@@ -4,50 +4,264 @@
 //   o = Σ_j p_j v_j / Σ_j p_j,  p_j = exp(scale·q·k_j - m),  j over the keys the
 //   query at position p sees: j <= p and (W = 0 or j > p - W or j < S).
 //
-// k_attn_row: one warp per query row, 32 keys per step.
+// This file: which kernel takes a call, and the fp32 path.
+//
+// fp32 (k_attn_f32): a CTA takes eight of the n·G rows (tokens x query heads) that
+// share a KV head, and a range of their visible keys; each of its warps walks 32
+// keys at a time.  Scores: a lane holds one key and reads its K row in 16-byte
+// pieces, the rows' queries come from shared memory as broadcasts.  Values: a lane
+// holds dims lane, lane + 32, ..., the 32 weights come by shuffle, and a weight of
+// a hidden key is never multiplied (a NaN there stays where it is).  The warps'
+// (max, sum, weighted sum of v) are joined in shared memory, the key ranges' by
+// k_f32_merge, both in order.  No tensor-core type holds fp32, so a key costs its
+// 4·dh operations per row on the FMA pipes; with few rows the cache's bytes bound it.
 #include <math.h>
 
+#include <algorithm>
+
 #include "cache.cuh"
+#include "gemm_tc.cuh"
 
 namespace tb {
 namespace {
 
-template <typename TQ>
-__global__ void __launch_bounds__(256) k_attn_row(AttnArgs a) {
-  pdl_trigger();
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long r = (long long)blockIdx.x * 8 + warp;
-  if (r >= (long long)a.c.B * a.n * a.H) return;
-  const int h = (int)(r % a.H), i = (int)(r / a.H % a.n), b = (int)(r / a.H / a.n);
-  const SeqRange sr = seq_range(a, b);
-  if (i >= sr.nn) return;
-  float out[4];
-  attend_row<TQ>(a, b, h / (a.H / a.c.Hkv), sr.first + i, (const TQ*)a.q + (size_t)r * a.c.dh, out);
-  __syncwarp();                          // o may be q
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-    if (lane + 32 * u < a.c.dh) ((TQ*)a.o)[(size_t)r * a.c.dh + lane + 32 * u] = from_f<TQ>(out[u]);
+constexpr int kRows = 8;              // rows per CTA
+constexpr int kFWarps = 8;
+constexpr int kKeys = 32;             // keys per warp and step
+
+struct F32Args {
+  AttnArgs a;
+  int n_tiles;            // row tiles of a (sequence, KV head)
+  int n_range;            // key ranges
+  float* part;            // [B][Hkv][n_tiles][n_range][kRows][dh + 2]: O, max, sum (n_range > 1)
+};
+
+// The visible 32-key runs of the rows of tile rt of sequence b.
+__device__ __forceinline__ KeyRuns tile_runs(const F32Args& f, const SeqRange& sr, int rt) {
+  const int G = f.a.H / f.a.c.Hkv;
+  const int i0 = rt * kRows / G, i1 = min((rt * kRows + kRows - 1) / G, sr.nn - 1);
+  if (i0 >= sr.nn) return KeyRuns{0, 0, 0};
+  return key_runs(sr.first + i1 + 1, sr.first + i0, f.a.window, f.a.sinks, kKeys);
 }
 
-}  // namespace
+template <int DH>
+__global__ void __launch_bounds__(kFWarps * 32) k_attn_f32(const F32Args f) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int D = (DH + 31) / 32;   // dims per lane
+  const AttnArgs& a = f.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rg = blockIdx.x % f.n_range, rt = blockIdx.x / f.n_range, h = blockIdx.y, b = blockIdx.z;
+  const int G = a.H / a.c.Hkv;
+  const SeqRange sr = seq_range(a, b);
+  const int rows = min(kRows, sr.nn * G - rt * kRows);      // of real tokens
+  if (rows <= 0) return;
+  const KeyRuns kr = tile_runs(f, sr, rt);
+  const int g0 = (int)((long long)kr.count * rg / f.n_range), g1 = (int)((long long)kr.count * (rg + 1) / f.n_range);
 
-namespace {
-// fp32 queries: one warp per row; else by the rows that share a KV head.
+  __shared__ __align__(16) float q_s[kRows][DH];
+  __shared__ float m_s[kFWarps][kRows], l_s[kFWarps][kRows];
+  __shared__ float acc_s[kFWarps][kRows][DH];
+  auto row_at = [&](int r) {          // where row r's q and o lie
+    const int t = rt * kRows + r;
+    return (((size_t)b * a.n + t / G) * a.H + h * G + t % G) * DH;
+  };
+  for (int i = threadIdx.x; i < kRows * DH; i += kFWarps * 32)
+    q_s[i / DH][i % DH] = i / DH < rows ? ((const float*)a.q)[row_at(i / DH) + i % DH] * a.scale_log2 : 0.f;
+  __syncthreads();
+  int pos[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) pos[r] = r < rows ? sr.first + (rt * kRows + r) / G : -1;
+
+  float m[kRows], l[kRows], acc[kRows][D];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int u = 0; u < D; ++u) acc[r][u] = 0.f;
+  }
+  for (int g = g0 + warp; g < g1; g += kFWarps) {
+    const int key = run_index(kr, g) * kKeys + lane;
+    bool any = false;
+    uint32_t vis[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const bool see = key <= pos[r] && (key >= win_lo(pos[r], a.window) || key < a.sinks);
+      any |= see;
+      vis[r] = __ballot_sync(0xffffffffu, see);
+    }
+    const long long row = any ? cache_row(a.c, b, h, key) : -1;
+    float s[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) s[r] = 0.f;
+    if (row >= 0) {
+      const float4* kp = reinterpret_cast<const float4*>((const float*)a.c.k + row * DH);
+#pragma unroll 8
+      for (int e = 0; e < DH / 4; ++e) {
+        const float4 kv = __ldg(kp + e);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const float4 qv = *reinterpret_cast<const float4*>(&q_s[r][4 * e]);
+          s[r] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[r]))));
+        }
+      }
+    }
+    float p[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const float z = (vis[r] >> lane) & 1u ? s[r] : -INFINITY;
+      float mx = z;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mn = fmaxf(m[r], mx), base = mn == -INFINITY ? 0.f : mn;
+      const float fac = exp2f(m[r] - base);
+      p[r] = exp2f(z - base);
+      l[r] = fmaf(l[r], fac, p[r]);   // per lane; summed at the end
+#pragma unroll
+      for (int u = 0; u < D; ++u) acc[r][u] *= fac;
+      m[r] = mn;
+    }
+    for (int k = 0; k < kKeys; ++k) {
+      const long long vr = __shfl_sync(0xffffffffu, row, k);
+      if (vr < 0) continue;           // seen by no row, or a page outside the pool
+      float v[D];
+#pragma unroll
+      for (int u = 0; u < D; ++u) v[u] = DH >= 32 || lane < DH ? __ldg((const float*)a.c.v + vr * DH + lane + 32 * u) : 0.f;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float pk = __shfl_sync(0xffffffffu, p[r], k);
+        if ((vis[r] >> k) & 1u) {
+#pragma unroll
+          for (int u = 0; u < D; ++u) acc[r][u] = fmaf(pk, v[u], acc[r][u]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const float ls = warp_sum(l[r]);
+    if (lane == 0) {
+      m_s[warp][r] = m[r];
+      l_s[warp][r] = ls;
+    }
+#pragma unroll
+    for (int u = 0; u < D; ++u)
+      if (DH >= 32 || lane < DH) acc_s[warp][r][lane + 32 * u] = acc[r][u];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * DH; i += kFWarps * 32) {
+    const int r = i / DH, e = i % DH;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kFWarps; ++w) M = fmaxf(M, m_s[w][r]);
+    const float base = M == -INFINITY ? 0.f : M;
+    float L = 0.f, A = 0.f;
+#pragma unroll
+    for (int w = 0; w < kFWarps; ++w) {
+      const float wgt = exp2f(m_s[w][r] - base);
+      L = fmaf(l_s[w][r], wgt, L);
+      A = fmaf(acc_s[w][r][e], wgt, A);
+    }
+    if (f.n_range == 1) {
+      ((float*)a.o)[row_at(r) + e] = L == 0.f ? 0.f : A / L;
+    } else {
+      float* p = f.part + ((((((size_t)b * a.c.Hkv + h) * f.n_tiles + rt) * f.n_range + rg) * kRows) + r) * (DH + 2);
+      p[e] = A;
+      if (e == 0) {
+        p[DH] = M;
+        p[DH + 1] = L;
+      }
+    }
+  }
+}
+
+// Joins the key ranges of a row, one warp per row.
+template <int DH>
+__global__ void __launch_bounds__(256) k_f32_merge(const F32Args f) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int D = (DH + 31) / 32;
+  const AttnArgs& a = f.a;
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;         // kRows warps
+  const int rt = blockIdx.x, h = blockIdx.y, b = blockIdx.z, G = a.H / a.c.Hkv;
+  const SeqRange sr = seq_range(a, b);
+  const int t = rt * kRows + r;
+  if (t >= sr.nn * G) return;
+  const float* p0 = f.part + (((((size_t)b * a.c.Hkv + h) * f.n_tiles + rt) * f.n_range) * kRows + r) * (DH + 2);
+  const size_t step = (size_t)kRows * (DH + 2);
+  float M = -INFINITY;
+  for (int i = lane; i < f.n_range; i += 32) M = fmaxf(M, p0[i * step + DH]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f, acc[D];
+#pragma unroll
+  for (int u = 0; u < D; ++u) acc[u] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < f.n_range; ++i) {
+    const float* p = p0 + i * step;
+    const float wgt = exp2f(p[DH] - base);
+    L = fmaf(p[DH + 1], wgt, L);
+#pragma unroll
+    for (int u = 0; u < D; ++u)
+      if (DH >= 32 || lane < DH) acc[u] = fmaf(p[lane + 32 * u], wgt, acc[u]);
+  }
+  float* out = (float*)a.o + (((size_t)b * a.n + t / G) * a.H + h * G + t % G) * DH;
+#pragma unroll
+  for (int u = 0; u < D; ++u)
+    if (DH >= 32 || lane < DH) out[lane + 32 * u] = L == 0.f ? 0.f : acc[u] / L;
+}
+
+// Row tiles, and key ranges: so many that the CTAs fill the GPU twice, with a
+// step of all eight warps (256 keys) in each at least.
+F32Args f32_plan(const AttnArgs& a, void* ws) {
+  F32Args f;
+  f.a = a;
+  f.part = (float*)ws;
+  const int G = a.H / a.c.Hkv;
+  f.n_tiles = (a.n * G + kRows - 1) / kRows;
+  const long long base = (long long)f.n_tiles * a.c.Hkv * a.c.B;
+  long long keys = a.c.T;                                    // a tile's keys at most
+  if (a.window > 0) keys = std::min<long long>(keys, (long long)a.window + a.sinks + kRows + 2 * kKeys);
+  const long long most = (keys + kFWarps * kKeys - 1) / (kFWarps * kKeys);
+  f.n_range = (int)std::max<long long>(1, std::min<long long>(most, (2LL * sm_count() + base - 1) / std::max<long long>(base, 1)));
+  return f;
+}
+
+template <int DH>
+cudaError_t run_f32(const AttnArgs& a, void* ws, cudaStream_t s) {
+  const F32Args f = f32_plan(a, ws);
+  cudaError_t e = launch_pdl(k_attn_f32<DH>, dim3((unsigned)(f.n_tiles * f.n_range), a.c.Hkv, a.c.B),
+                             dim3(kFWarps * 32), 0, s, f);
+  if (e == cudaSuccess && f.n_range > 1)
+    e = launch_pdl(k_f32_merge<DH>, dim3((unsigned)f.n_tiles, a.c.Hkv, a.c.B), dim3(kRows * 32), 0, s, f);
+  return e;
+}
+
+// Few rows per KV head stream the cache through warp-level MMAs; more take the
+// tensor-core kernel.
 bool few(const AttnArgs& a) { return a.n * (a.H / a.c.Hkv) <= kFewRows; }
+
 }  // namespace
 
 size_t cache_attn_workspace(const AttnArgs& a) {
-  if (a.c.dtype == TB_F32) return 0;
-  return few(a) ? cache_attn_few_workspace(a) : cache_attn_many_workspace(a);
+  if (a.c.dtype != TB_F32) return few(a) ? cache_attn_few_workspace(a) : cache_attn_many_workspace(a);
+  if (a.c.B == 0 || a.n == 0) return 0;
+  const F32Args f = f32_plan(a, nullptr);
+  return f.n_range == 1 ? 0
+                        : (size_t)a.c.B * a.c.Hkv * f.n_tiles * f.n_range * kRows * (a.c.dh + 2) * sizeof(float);
 }
 
 cudaError_t launch_cache_attn(const AttnArgs& a, void* ws, cudaStream_t s) {
-  if (a.c.dtype == TB_F32) {
-    const long long rows = (long long)a.c.B * a.n * a.H;
-    return launch_pdl(k_attn_row<float>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
+  if (a.c.dtype != TB_F32) return few(a) ? launch_cache_attn_few(a, ws, s) : launch_cache_attn_many(a, ws, s);
+  switch (a.c.dh) {
+    case 16: return run_f32<16>(a, ws, s);
+    case 32: return run_f32<32>(a, ws, s);
+    case 64: return run_f32<64>(a, ws, s);
+    case 128: return run_f32<128>(a, ws, s);
+    default: return cudaErrorInvalidValue;
   }
-  return few(a) ? launch_cache_attn_few(a, ws, s) : launch_cache_attn_many(a, ws, s);
 }
 
 }  // namespace tb

@@ -678,12 +678,12 @@ __global__ void __launch_bounds__(kMergeThreads) k_few_merge(const FewArgs f) {
   }
   if (__syncthreads_or(!(fabsf(res) <= 3.402823466e38f))) {       // see attend_row
     if (warp == 0) {
-      float r4[4];
-      attend_row<bf16>(a, f.b0 + b, h, sr.first + tok,
-                       (const bf16*)a.q + (((size_t)(f.b0 + b) * a.n + tok) * a.H + head) * DH, r4);
+      float r4[DH / 32];
+      attend_row<DH>(a, f.b0 + b, h, sr.first + tok,
+                     (const bf16*)a.q + (((size_t)(f.b0 + b) * a.n + tok) * a.H + head) * DH, r4);
       __syncwarp();
 #pragma unroll
-      for (int u = 0; u < DH / 32; ++u) out[lane + 32 * u] = from_f<bf16>(r4[u]);
+      for (int u = 0; u < DH / 32; ++u) out[lane * (DH / 32) + u] = from_f<bf16>(r4[u]);
     }
     return;
   }

@@ -92,6 +92,7 @@ struct ManyArgs {
   int vbox;                // keys per box of V codes
   bool negate;             // the score scale is negative: the scores are negated, its magnitude applied
   long long* pre;          // [B·pairs + 1] line position of (sequence, pair) within its KV head
+  int* any;                // whether any flag is set
   uint8_t* flags;          // [B·Hkv·2·pairs] row tiles to look through again
   float4* part;            // [2·n_cta][2][DH/4 + 1][128] pieces
 };
@@ -278,7 +279,10 @@ __global__ void __launch_bounds__(1024) k_many_plan(const ManyArgs m, int n_flag
   __shared__ long long carry_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < n_flag_words; i += 1024) reinterpret_cast<uint32_t*>(m.flags)[i] = 0u;
-  if (tid == 0) carry_s = 0;
+  if (tid == 0) {
+    carry_s = 0;
+    *m.any = 0;
+  }
   __syncthreads();
   const int E = m.a.c.B * m.pairs;
   for (int e0 = 0; e0 < E; e0 += 1024) {
@@ -1156,7 +1160,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
           }
         }
         if (valid && !(probe == 0.f))
-          m.flags[flag] = 1;
+          *m.any = m.flags[flag] = 1;
       }
       tc_fence_before();
     }
@@ -1186,11 +1190,11 @@ __global__ void __launch_bounds__(128) k_many_merge(const ManyArgs m) {
     // row `row` of the slot's tile, by this warp
     const int tok = s.tok0 + row / G;
     const size_t at = ((size_t)b * a.n + tok) * a.H + h * G + row % G;
-    float out[4];
-    attend_row<bf16>(a, b, h, sr.first + tok, (const bf16*)a.q + at * DH, out);
+    float out[DH / 32];
+    attend_row<DH>(a, b, h, sr.first + tok, (const bf16*)a.q + at * DH, out);
     __syncwarp();
 #pragma unroll
-    for (int u = 0; u < DH / 32; ++u) ((bf16*)a.o)[at * DH + lane + 32 * u] = from_f<bf16>(out[u]);
+    for (int u = 0; u < DH / 32; ++u) ((bf16*)a.o)[at * DH + lane * (DH / 32) + u] = from_f<bf16>(out[u]);
     __syncwarp();
   };
   if (c < m.n_cta && xc < total && xc > xb) {
@@ -1271,28 +1275,30 @@ __global__ void __launch_bounds__(128) k_many_merge(const ManyArgs m) {
       }
     }
   }
-  // row tiles that the attention kernel wrote out with a value that is not finite
-  const long long tiles = (long long)a.c.B * a.c.Hkv * 2 * m.pairs;
-  const long long words = (tiles + 3) / 4;
-  const long long stride = (long long)gridDim.x * gridDim.y * 128;
-  for (long long i0 = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * 128; i0 < words; i0 += stride) {
-    uint32_t f = i0 + r < words ? reinterpret_cast<const uint32_t*>(m.flags)[i0 + r] : 0u;
-    for (uint32_t todo = __ballot_sync(0xffffffffu, f != 0u); todo; todo &= todo - 1) {
+  // Row tiles that the attention kernel wrote out with a value that is not finite,
+  // their rows dealt to all warps of the grid.
+  if (!*m.any) return;
+  const int tiles = a.c.B * a.c.Hkv * 2 * m.pairs;
+  const int warps = (int)(gridDim.x * gridDim.y) * 4, me = (int)(blockIdx.y * gridDim.x + blockIdx.x) * 4 + warp;
+  for (int i0 = 0; i0 < tiles; i0 += 128) {
+    const int i = i0 + lane * 4;          // 4 flags per lane
+    const uint32_t fl = i < tiles ? reinterpret_cast<const uint32_t*>(m.flags)[i >> 2] : 0u;
+    for (uint32_t todo = __ballot_sync(0xffffffffu, fl != 0u); todo; todo &= todo - 1) {
       const int who = __ffs(todo) - 1;
-      const uint32_t fw = __shfl_sync(0xffffffffu, f, who);
+      const uint32_t fw = __shfl_sync(0xffffffffu, fl, who);
       for (int u = 0; u < 4; ++u) {
-        if (!((fw >> (8 * u)) & 255u)) continue;
-        const long long t = (i0 + warp * 32 + who) * 4 + u;
-        if (t >= tiles) break;
-        const int rt = (int)(t % (2 * m.pairs)), h = (int)(t / (2 * m.pairs) % a.c.Hkv);
-        const int b = (int)(t / (2 * m.pairs) / a.c.Hkv);
+        const int t = i0 + who * 4 + u;
+        if (!((fw >> (8 * u)) & 255u) || t >= tiles) continue;
+        const int rt = t % (2 * m.pairs), hk = t / (2 * m.pairs) % a.c.Hkv, b = t / (2 * m.pairs) / a.c.Hkv;
         const SeqRange sr = seq_range(a, b);
         const SlotRange s = slot_range(m, sr, rt);
-        for (int row = 0; row < s.rows; ++row) {
-          const size_t at = ((size_t)b * a.n + s.tok0 + row / G) * a.H + h * G + row % G;
+        // row r of tile t belongs to warp (128 t + r) mod warps
+        for (long long r = (me - (long long)t * kBM % warps + warps) % warps; r < s.rows; r += warps) {
+          const int row = (int)r;
+          const size_t at = ((size_t)b * a.n + s.tok0 + row / G) * a.H + hk * G + row % G;
           float probe = 0.f;
           for (int e = lane; e < DH; e += 32) probe = fmaf(to_f(((const bf16*)a.o)[at * DH + e]), 0.f, probe);
-          if (__any_sync(0xffffffffu, !(probe == 0.f))) again(b, h, row, s, sr);
+          if (__any_sync(0xffffffffu, !(probe == 0.f))) again(b, hk, row, s, sr);
         }
       }
     }
@@ -1311,7 +1317,7 @@ ManyLayout layout_of(const AttnArgs& a) {
   const size_t flags = (size_t)a.c.B * a.c.Hkv * 2 * L.pairs;
   L.flag_words = (int)((flags + 3) / 4);
   L.pre = 0;
-  L.flags = up(((size_t)a.c.B * L.pairs + 1) * 8);
+  L.flags = up(((size_t)a.c.B * L.pairs + 1) * 8) + 256;      // `any` in the 256 bytes before them
   L.part = L.flags + up((size_t)L.flag_words * 4);
   L.total = L.part + (size_t)2 * sm_count() * 2 * (a.c.dh / 4 + 1) * kBM * 16;
   return L;
@@ -1334,6 +1340,7 @@ cudaError_t run(const AttnArgs& a, void* ws, cudaStream_t s) {
   m.negate = a.scale_log2 < 0.f;
   m.pre = (long long*)ws;
   m.flags = (uint8_t*)ws + L.flags;
+  m.any = (int*)(m.flags - 256);
   m.part = (float4*)((uint8_t*)ws + L.part);
   m.box = kBN;
   m.vbox = kChunk;

@@ -584,3 +584,20 @@ def test_graph_capture_streams_and_repeats(kind, n):
         m = int(nn[b])
         assert torch.equal(got[b, :m], want[0][0][b, :m])
     assert tb.tb_get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 8, 700])
+def test_a_value_row_of_nan_in_every_head(kind, n):
+    """The first row's v is NaN and every query sees it: all NaN, in time."""
+    tb = tbm()
+    L, dh, Hkv, H = 1500, 128, 4, 16
+    kv = make_cache(kind, True, 2, Hkv, 1536, dh, 64, fill=0.0)
+    for b in range(2):
+        put_rows(kv, b, rows(1 + b, Hkv, L, dh), rows(2 + b, Hkv, L, dh))
+        (kv.v.view(torch.uint8) if kind == "e4m3" else kv.v)[int(kv.block_table[b, 0]), :, 0] = (
+            0x7F if kind == "e4m3" else math.nan)
+    kv.lens.fill_(L)
+    q = rows(5, 2, n, H, dh, dtype=torch.bfloat16).cuda()
+    o = tb.tb_kvcache_attn(tb.AttnConfig(H=H, Hkv=Hkv, dh=dh), q, kv)
+    assert torch.isnan(o).all() and tb.tb_get_device_error(clear=True) == 0
