@@ -582,32 +582,39 @@ class AttnConfig:
         return torch.float32 if self.dtype == TB_F32 else torch.bfloat16
 
 
-def _stream_on(stream, device: torch.device) -> int:
-    """The raw stream of a call on `device`'s tensors, which must be the current device."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is {torch.cuda.current_device()}")
-    return _stream(stream)
+def _stream_on(stream, dev: int) -> int:
+    """The raw stream of a call on tensors of CUDA device `dev`, which must be the current device."""
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is {torch.cuda.current_device()}")
+    # (the raw handle of the current stream, without a stream object around it)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _counts(t: Optional[torch.Tensor], name: str, B: int, device: torch.device) -> Optional[int]:
-    if t is None:
-        return None
-    _need(t, name, torch.int32, (B,))
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    return t.data_ptr()
+def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> int:
+    """The pointer of a dense tensor of this type and shape on CUDA device `dev`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
 
 
-def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, B: int, n: int, dh: int, device: torch.device):
+def _counts(t: Optional[torch.Tensor], name: str, B: int, dev: int) -> Optional[int]:
+    return None if t is None else _dense(t, name, torch.int32, (B,), dev)
+
+
+def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, B: int, n: int, heads: Optional[int], dh: int, dev: int):
     """Heads, token stride and sequence stride of rows [B, n, heads, dh] whose heads are dense."""
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != n or t.shape[3] != dh:
-        raise ValueError(f"{name} must be [{B}, {n}, heads, {dh}], got {tuple(t.shape)}")
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != n or shape[3] != dh or (heads is not None and shape[2] != heads):
+        raise ValueError(f"{name} must be [{B}, {n}, {'heads' if heads is None else heads}, {dh}], got {tuple(shape)}")
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be {dtype} on cuda:{dev}, got {t.dtype} on {t.device}")
     seq, tok, head, one = t.stride()
-    if (one != 1 and dh > 1) or (head != dh and t.shape[2] > 1):
+    if one != 1 or (head != dh and shape[2] > 1):
         raise ValueError(f"a token's heads must be dense in {name}")
-    return t.shape[2], (tok if n > 1 else t.shape[2] * dh), (seq if B > 1 else 0)
+    if n == 1:
+        tok = shape[2] * dh
+    return shape[2], tok, seq if B > 1 else tok * n
 
 
 def tb_rope_table(dh: int, max_pos: int, base: float, device="cuda", stream=None) -> torch.Tensor:
@@ -615,7 +622,7 @@ def tb_rope_table(dh: int, max_pos: int, base: float, device="cuda", stream=None
     with _alloc_on(stream):
         table = torch.empty((max_pos, dh // 2, 2), dtype=torch.float32, device=device)
     _check("tb_rope_table", lib().tb_rope_table(dh, max_pos, base, table.data_ptr(),
-                                                _stream_on(stream, table.device)))
+                                                _stream_on(stream, table.get_device())))
     return table
 
 
@@ -628,35 +635,30 @@ def tb_kvcache_append_rope(kv: KVCache, k: torch.Tensor, v: torch.Tensor, rope: 
     q_out, if given).  k, v and q may be column blocks of one projection.  n_new
     [B]: how many of each sequence's n rows count."""
     kvs = kv.c()
-    dev = kv.k.device
+    dev = kv.k.get_device()
     row = torch.float32 if kvs.dtype == TB_F32 else torch.bfloat16
     if k.dim() != 4:
         raise ValueError("k must be [B, n, Hkv, dh]")
     B, n, dh = kvs.B, k.shape[1], kvs.dh
-    heads, k_tok, k_seq = _heads(k, "k", row, B, n, dh, dev)
-    heads_v, v_tok, v_seq = _heads(v, "v", row, B, n, dh, dev)
-    if heads != kvs.Hkv or heads_v != kvs.Hkv:
-        raise ValueError(f"k and v must have {kvs.Hkv} heads")
-    _need(rope, "rope", torch.float32)
-    if rope.dim() != 3 or rope.shape[1] != dh // 2 or rope.shape[2] != 2 or rope.device != dev:
-        raise ValueError(f"rope must be [max_pos, {dh // 2}, 2] on {dev}")
+    _, k_tok, k_seq = _heads(k, "k", row, B, n, kvs.Hkv, dh, dev)
+    _, v_tok, v_seq = _heads(v, "v", row, B, n, kvs.Hkv, dh, dev)
+    max_pos = rope.shape[0] if rope.dim() else 0
+    rope_ptr = _dense(rope, "rope", torch.float32, (max_pos, dh // 2, 2), dev)
     H, q_tok, q_seq, q_ptr, out_ptr = 0, 0, 0, None, None
     if q is not None:
-        H, q_tok, q_seq = _heads(q, "q", row, B, n, dh, dev)
+        H, q_tok, q_seq = _heads(q, "q", row, B, n, None, dh, dev)
         if q_out is None:
             with _alloc_on(stream):
-                q_out = torch.empty((B, n, H, dh), dtype=row, device=dev)
-        _need(q_out, "q_out", row, (B, n, H, dh))
-        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
-        if B == 1:
-            q_seq = q_tok * n
+                q_out = torch.empty((B, n, H, dh), dtype=row, device=kv.k.device)
+        q_ptr, out_ptr = q.data_ptr(), _dense(q_out, "q_out", row, (B, n, H, dh), dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     rows = tb_append_rows(q_ptr, k.data_ptr(), v.data_ptr(), out_ptr, q_tok, q_seq, k_tok, k_seq, v_tok, v_seq, H, n,
                           _counts(start, "start", B, dev), _counts(n_new, "n_new", B, dev))
-    _check("tb_kvcache_append_rope", lib().tb_kvcache_append_rope(ctypes.byref(kvs), ctypes.byref(rows),
-                                                                  rope.data_ptr(), rope.shape[0],
-                                                                  _stream_on(stream, dev)))
+    status = lib().tb_kvcache_append_rope(ctypes.byref(kvs), ctypes.byref(rows), rope_ptr, max_pos,
+                                          _stream_on(stream, dev))
+    if status:
+        _check("tb_kvcache_append_rope", status)
     return q_out
 
 
@@ -684,24 +686,25 @@ def tb_kvcache_attn(cfg: AttnConfig, q: torch.Tensor, kv: KVCache, n_new: Option
     """Attention of the last tokens of each sequence, q [B, n, H, dh] (rotated),
     over the cache they were appended to -> o [B, n, H, dh]."""
     kvs, cc = kv.c(), cfg.c()
-    dev = kv.k.device
+    dev = kv.k.get_device()
     if q.dim() != 4:
         raise ValueError("q must be [B, n, H, dh]")
     n = q.shape[1]
-    shape = (kvs.B, n, cfg.H, cfg.dh)
-    _need(q, "q", cfg.torch_dtype, shape)
-    with _alloc_on(stream):
-        if o is None:
-            o = torch.zeros(shape, dtype=cfg.torch_dtype, device=dev) if n_new is not None else torch.empty(
-                shape, dtype=cfg.torch_dtype, device=dev)
-        if ws is None:
-            need = lib().tb_kvcache_attn_workspace_bytes(ctypes.byref(cc), ctypes.byref(kvs), n)
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    _need(o, "o", cfg.torch_dtype, shape)
-    if q.device != dev or o.device != dev or ws.device != dev:
-        raise ValueError(f"q, o and ws must be on {dev}")
-    _check("tb_kvcache_attn", lib().tb_kvcache_attn(ctypes.byref(cc), q.data_ptr(), ctypes.byref(kvs),
-                                                    _counts(n_new, "n_new", kvs.B, dev), n, o.data_ptr(),
-                                                    ws.data_ptr(), ws.numel() * ws.element_size(),
-                                                    _stream_on(stream, dev)))
+    shape, dtype = (kvs.B, n, cfg.H, cfg.dh), cfg.torch_dtype
+    q_ptr = _dense(q, "q", dtype, shape, dev)
+    n_ptr = _counts(n_new, "n_new", kvs.B, dev)
+    if o is None or ws is None:
+        with _alloc_on(stream):
+            if o is None:       # (rows of padding are not written)
+                o = (torch.empty if n_new is None else torch.zeros)(shape, dtype=dtype, device=q.device)
+            if ws is None:
+                need = lib().tb_kvcache_attn_workspace_bytes(ctypes.byref(cc), ctypes.byref(kvs), n)
+                ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    o_ptr = _dense(o, "o", dtype, shape, dev)
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on cuda:{dev}")
+    status = lib().tb_kvcache_attn(ctypes.byref(cc), q_ptr, ctypes.byref(kvs), n_ptr, n, o_ptr, ws.data_ptr(), ws.nbytes,
+                                   _stream_on(stream, dev))
+    if status:
+        _check("tb_kvcache_attn", status)
     return o

@@ -122,20 +122,27 @@ __global__ void __launch_bounds__(kFWarps * 32) k_attn_f32(const F32Args f) {
       for (int u = 0; u < D; ++u) acc[r][u] *= fac;
       m[r] = mn;
     }
-    for (int k = 0; k < kKeys; ++k) {
-      const long long vr = __shfl_sync(0xffffffffu, row, k);
-      if (vr < 0) continue;           // seen by no row, or a page outside the pool
-      float v[D];
+    // eight keys' values on their way at a time
+#pragma unroll 1
+    for (int k0 = 0; k0 < kKeys; k0 += 8) {
+      float v[8][D];
 #pragma unroll
-      for (int u = 0; u < D; ++u) v[u] = DH >= 32 || lane < DH ? __ldg((const float*)a.c.v + vr * DH + lane + 32 * u) : 0.f;
+      for (int k = 0; k < 8; ++k) {
+        const long long vr = __shfl_sync(0xffffffffu, row, k0 + k);
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        const float pk = __shfl_sync(0xffffffffu, p[r], k);
-        if ((vis[r] >> k) & 1u) {
-#pragma unroll
-          for (int u = 0; u < D; ++u) acc[r][u] = fmaf(pk, v[u], acc[r][u]);
-        }
+        for (int u = 0; u < D; ++u)        // (-1: seen by no row, or a page outside the pool)
+          v[k][u] = vr >= 0 && (DH >= 32 || lane < DH) ? __ldg((const float*)a.c.v + vr * DH + lane + 32 * u) : 0.f;
       }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float pk = __shfl_sync(0xffffffffu, p[r], k0 + k);
+          if ((vis[r] >> (k0 + k)) & 1u) {
+#pragma unroll
+            for (int u = 0; u < D; ++u) acc[r][u] = fmaf(pk, v[k][u], acc[r][u]);
+          }
+        }
     }
   }
 #pragma unroll
