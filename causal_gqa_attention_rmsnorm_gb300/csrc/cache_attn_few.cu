@@ -128,6 +128,7 @@ struct FewArgs {
   int b0;                 // first sequence of this launch (a's tensors start at sequence 0)
   int B;                  // sequences of this launch
   int teams;
+  int* pre;               // [B + 1] first stage of each sequence, left for the merge
   float* part;            // [teams + B·Hkv][R][DH + 4]
   int R;                  // rows per piece: n·G
 };
@@ -211,6 +212,8 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
   scan_in_place(pre, f.B, tmp);
   volatile int* abort_flag = &abort_word;
   const int total = pre[f.B];
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b <= f.B; b += blockDim.x) f.pre[b] = pre[b];
   const int teams = min(f.teams, total);        // each of them has a stage at least
   const int team = team_in * gridDim.x + blockIdx.x;
   const bool mine = team < teams;
@@ -581,119 +584,109 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
   }
 }
 
-// Joins the pieces of one (sequence, KV head) for one row: o = Σ w_i O_i / Σ w_i
-// l_i, w_i = 2^(m_i - M), in the order of the teams.  One CTA per row.
-constexpr int kMergeThreads = 256;
-constexpr int kMaxTeams = 2048;
-template <int DH, int RUNS>
-__global__ void __launch_bounds__(kMergeThreads) k_few_merge(const FewArgs f) {
+// Joins the pieces of a row of a (sequence, KV head): o = Σ w_i O_i / Σ w_i l_i,
+// w_i = 2^(m_i - M), in the order of the teams.  One warp per row, or with many
+// pieces (WIDE) eight warps, each a run of them, whose results are joined the same
+// way.  A lane holds DH/32 consecutive dims.
+template <int DH, bool WIDE>
+__global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
   pdl_trigger();
   pdl_wait();
-  constexpr int NG = kMergeThreads / DH;
+  constexpr int D = DH / 32;
   const AttnArgs& a = f.a;
-  __shared__ float w_s[kMaxTeams];
-  __shared__ float red[kMergeThreads / 32], red2[kMergeThreads / 32];
-  __shared__ int part_s[kMergeThreads / 32], tot_s[kMergeThreads / 32];
-  __shared__ float acc_s[NG][DH];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int Hkv = a.c.Hkv, G = a.H / Hkv;
-  const int row = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const SeqRange sr = seq_range(a, f.b0 + b);
+  const int row = WIDE ? blockIdx.x : blockIdx.x * 8 + warp, h = blockIdx.y, b = blockIdx.z;
+  const int total = f.pre[f.B], before = f.pre[b], n_st = (f.pre[b + 1] - before) / Hkv;
+  const int nn = a.n_new ? min(max(a.n_new[f.b0 + b], 0), a.n) : a.n;
   const int tok = row / G, head = h * G + row % G;
-  if (tok >= sr.nn) return;
-  // the line of stages: those before this sequence, and all of them
-  int before = 0, total = 0;
-  for (int i = tid; i < f.B; i += kMergeThreads) {
-    const int s = stages_of(a, seq_range(a, f.b0 + i), RUNS) * Hkv;
-    total += s;
-    if (i < b) before += s;
-  }
+  if (row >= f.R || tok >= nn) return;
+  const size_t at = (((size_t)(f.b0 + b) * a.n + tok) * a.H + head) * DH;
+  float M = -INFINITY, L = 0.f, acc[D];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-  }
-  if (lane == 0) {
-    part_s[warp] = before;
-    tot_s[warp] = total;
-  }
-  __syncthreads();
-  before = total = 0;
+  for (int u = 0; u < D; ++u) acc[u] = 0.f;
+  if (n_st > 0) {                               // (no stages: no rows in the cache)
+    // team t has stages [total·t / teams, total·(t+1) / teams): those of the pair's first and last stage
+    const int teams = min(f.teams, total);
+    const long long U0 = before + (long long)h * n_st, U1 = U0 + n_st;
+    const int t0 = (int)(((U0 + 1) * teams + total - 1) / total) - 1;
+    const int np = (int)((U1 * teams + total - 1) / total) - t0;
+    const float* p0 = f.part + ((t0 + (long long)b * Hkv + h) * f.R + row) * (DH + 4);
+    const size_t step = (size_t)f.R * (DH + 4);
+    const int i0 = WIDE ? np * warp / 8 : 0, i1 = WIDE ? np * (warp + 1) / 8 : np;
+    for (int i = i0 + lane; i < i1; i += 32) M = fmaxf(M, p0[i * step]);
 #pragma unroll
-  for (int i = 0; i < kMergeThreads / 32; ++i) {
-    before += part_s[i];
-    total += tot_s[i];
-  }
-  const int n_st = stages_of(a, sr, RUNS);
-  bf16* out = (bf16*)a.o + (((size_t)(f.b0 + b) * a.n + tok) * a.H + head) * DH;
-  if (n_st == 0) {                              // no rows
-    for (int e = tid; e < DH; e += kMergeThreads) out[e] = from_f<bf16>(0.f);
-    return;
-  }
-  // team t has stages [total·t / teams, total·(t+1) / teams): those of the pair's first and last stage
-  const int teams = min(f.teams, total);
-  const long long U0 = before + (long long)h * n_st, U1 = U0 + n_st;
-  const int t0 = (int)(((U0 + 1) * teams + total - 1) / total) - 1;
-  const int t1 = (int)((U1 * teams + total - 1) / total) - 1;
-  const long long pair = (long long)b * Hkv + h;
-  const float* p0 = f.part + ((t0 + pair) * f.R + row) * (DH + 4);
-  const size_t step = (size_t)f.R * (DH + 4);
-  const int np = t1 - t0 + 1;
-  float mx = -INFINITY;
-  for (int i = tid; i < np; i += kMergeThreads) {
-    const float mm = p0[i * step];
-    w_s[i] = mm;
-    mx = fmaxf(mx, mm);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) red[warp] = mx;
-  __syncthreads();
-  float M = red[0];
-#pragma unroll
-  for (int i = 1; i < kMergeThreads / 32; ++i) M = fmaxf(M, red[i]);
-  const float base = M == -INFINITY ? 0.f : M;
-  float ls = 0.f;
-  for (int i = tid; i < np; i += kMergeThreads) {
-    const float wgt = exp2f(w_s[i] - base);
-    ls = fmaf(p0[i * step + 1], wgt, ls);
-    w_s[i] = wgt;
-  }
-  ls = warp_sum(ls);
-  if (lane == 0) red2[warp] = ls;
-  __syncthreads();
-  float L = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMergeThreads / 32; ++i) L += red2[i];
-  const int e = tid % DH, grp = tid / DH;
-  float acc = 0.f;
-  for (int i = grp; i < np; i += NG) acc = fmaf(p0[i * step + 4 + e], w_s[i], acc);
-  acc_s[grp][e] = acc;
-  __syncthreads();
-  float res = 0.f;
-  if (grp == 0) {
-#pragma unroll
-    for (int i = 0; i < NG; ++i) res += acc_s[i][e];
-    res = L == 0.f ? 0.f : res / L;
-  }
-  if (__syncthreads_or(!(fabsf(res) <= 3.402823466e38f))) {       // see attend_row
-    if (warp == 0) {
-      float r4[DH / 32];
-      attend_row<DH>(a, f.b0 + b, h, sr.first + tok,
-                     (const bf16*)a.q + (((size_t)(f.b0 + b) * a.n + tok) * a.H + head) * DH, r4);
-      __syncwarp();
-#pragma unroll
-      for (int u = 0; u < DH / 32; ++u) out[lane * (DH / 32) + u] = from_f<bf16>(r4[u]);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+    for (int i = i0; i < i1; ++i) {
+      const float2 ml = *reinterpret_cast<const float2*>(p0 + i * step);
+      const float w = ex2_approx(ml.x - base);
+      L = fmaf(ml.y, w, L);
+      if constexpr (D == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p0 + i * step + 4 + 4 * lane);
+        acc[0] = fmaf(v.x, w, acc[0]);
+        acc[1] = fmaf(v.y, w, acc[1]);
+        acc[2] = fmaf(v.z, w, acc[2]);
+        acc[3] = fmaf(v.w, w, acc[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(p0 + i * step + 4 + 2 * lane);
+        acc[0] = fmaf(v.x, w, acc[0]);
+        acc[1] = fmaf(v.y, w, acc[1]);
+      }
     }
+    if constexpr (WIDE) {
+      __shared__ float m_s[8], l_s[8], acc_s[8][DH];
+      if (lane == 0) {
+        m_s[warp] = M;
+        l_s[warp] = L;
+      }
+#pragma unroll
+      for (int u = 0; u < D; ++u) acc_s[warp][lane * D + u] = acc[u];
+      __syncthreads();
+      if (warp > 0) return;
+      M = m_s[lane & 7];
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float all = M == -INFINITY ? 0.f : M;
+      L = 0.f;
+#pragma unroll
+      for (int u = 0; u < D; ++u) acc[u] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = ex2_approx(m_s[i] - all);
+        L = fmaf(l_s[i], w, L);
+#pragma unroll
+        for (int u = 0; u < D; ++u) acc[u] = fmaf(acc_s[i][lane * D + u], w, acc[u]);
+      }
+    }
+  } else if (WIDE && warp > 0) {
     return;
   }
-  if (grp == 0) out[e] = from_f<bf16>(res);
+  const float inv = L == 0.f ? 0.f : 1.0f / L;
+  float probe = 0.f;
+#pragma unroll
+  for (int u = 0; u < D; ++u) {
+    acc[u] *= inv;
+    probe = fmaf(acc[u], 0.f, probe);
+  }
+  if (__any_sync(0xffffffffu, !(probe == 0.f))) {        // not finite: see attend_row
+    const SeqRange sr = seq_range(a, f.b0 + b);
+    attend_row<DH>(a, f.b0 + b, h, sr.first + tok, (const bf16*)a.q + at, acc);
+    __syncwarp();
+  }
+  bf16* out = (bf16*)a.o + at + lane * D;
+  if constexpr (D == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack<false>(acc[0], acc[1]), pack<false>(acc[2], acc[3]));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack<false>(acc[0], acc[1]);
 }
 
+constexpr size_t kPreBytes = (kMaxB + 1) * 4 / 256 * 256 + 256;
 int team_warps(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
 
 template <int DH, bool E4, int TW, bool LO>
-cudaError_t run(const AttnArgs& a, float* part, int Bl, cudaStream_t s) {
+cudaError_t run(const AttnArgs& a, void* ws, int Bl, cudaStream_t s) {
   using C = FewCfg<DH, E4>;
   CUtensorMap tk, tv;
   const uint64_t planes = a.c.bt ? (uint64_t)a.c.num_pages * a.c.Hkv : (uint64_t)a.c.B * a.c.Hkv;
@@ -714,7 +707,8 @@ cudaError_t run(const AttnArgs& a, float* part, int Bl, cudaStream_t s) {
   }
   FewArgs f;
   f.a = a;
-  f.part = part;
+  f.pre = (int*)ws;
+  f.part = (float*)((uint8_t*)ws + kPreBytes);
   f.R = a.n * (a.H / a.c.Hkv);
   constexpr int warps = FewShape<E4, LO>::WARPS;
   f.teams = sm_count() * (warps / TW);
@@ -723,14 +717,19 @@ cudaError_t run(const AttnArgs& a, float* part, int Bl, cudaStream_t s) {
     f.B = std::min(Bl, a.c.B - b0);
     e = launch_pdl(k_attn_few<DH, E4, TW, LO>, dim3(sm_count()), dim3(warps * 32), smem, s, tk, tv, f);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(k_few_merge<DH, C::RUNS>, dim3(f.R, a.c.Hkv, f.B), dim3(kMergeThreads), 0, s, f);
+    // eight warps per row from 16 pieces of a pair on (at equal lengths)
+    const int rows = f.R;
+    if (f.teams >= 16 * f.B * a.c.Hkv)
+      e = launch_pdl(k_few_merge<DH, true>, dim3(rows, a.c.Hkv, f.B), dim3(256), 0, s, f);
+    else
+      e = launch_pdl(k_few_merge<DH, false>, dim3((rows + 7) / 8, a.c.Hkv, f.B), dim3(256), 0, s, f);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
 template <int DH, bool E4>
-cudaError_t by_rows(const AttnArgs& a, float* part, int Bl, cudaStream_t s) {
+cudaError_t by_rows(const AttnArgs& a, void* part, int Bl, cudaStream_t s) {
   const int R = a.n * (a.H / a.c.Hkv);
   if (R <= 8) return run<DH, E4, 1, true>(a, part, Bl, s);
   if (R <= 16) return run<DH, E4, 1, false>(a, part, Bl, s);
@@ -752,15 +751,14 @@ size_t cache_attn_few_workspace(const AttnArgs& a) {
   if (a.c.B == 0 || R == 0) return 0;
   const int warps = R <= 8 && a.c.dtype == TB_E4M3 ? FewShape<true, true>::WARPS : FewShape<false, false>::WARPS;
   const long long pieces = (long long)sm_count() * (warps / team_warps(R)) + (long long)batch_of(a) * a.c.Hkv;
-  return (size_t)pieces * R * (a.c.dh + 4) * 4;
+  return kPreBytes + (size_t)pieces * R * (a.c.dh + 4) * 4;
 }
 
 cudaError_t launch_cache_attn_few(const AttnArgs& a, void* ws, cudaStream_t s) {
   const int Bl = batch_of(a);
-  float* part = (float*)ws;
   if (a.c.dtype == TB_E4M3)
-    return a.c.dh == 128 ? by_rows<128, true>(a, part, Bl, s) : by_rows<64, true>(a, part, Bl, s);
-  return a.c.dh == 128 ? by_rows<128, false>(a, part, Bl, s) : by_rows<64, false>(a, part, Bl, s);
+    return a.c.dh == 128 ? by_rows<128, true>(a, ws, Bl, s) : by_rows<64, true>(a, ws, Bl, s);
+  return a.c.dh == 128 ? by_rows<128, false>(a, ws, Bl, s) : by_rows<64, false>(a, ws, Bl, s);
 }
 
 }  // namespace tb
