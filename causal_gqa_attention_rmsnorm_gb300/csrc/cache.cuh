@@ -62,6 +62,47 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
+// Two values to e4m3 codes (low byte: lo), saturating, NaN staying NaN; and back.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+  float2 r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(h));
+  return r;
+}
+// 2^-e with x·2^-e in [0.5, 1) for a normal x > 0, held to normal powers of two; 1 otherwise.
+__device__ __forceinline__ float pow2_frame(float x) {
+  if (!(x > 0.f)) return 1.f;
+  const int e = max(-126, min(126, (int)((__float_as_uint(x) >> 23) & 0xffu) - 126));
+  return __uint_as_float((uint32_t)(127 - e) << 23);
+}
+// bf16 queries as two e4m3 terms, q = q1 + q2, under a power of two that brings a
+// row's largest element into [128, 256): q1 takes the leading four bits of an
+// element, the rest is at most half a step of q1 and has four bits itself, so the
+// split is exact for elements down to 2^-2 and off by 2^-10 at most below (2^-17
+// of the row's largest).  Both terms multiply the K codes as they lie in the
+// cache.  The power of two: NaN for a row with an infinity, which must not
+// saturate.
+__device__ __forceinline__ float split_frame(float amax) {
+  return amax <= 3.402823466e38f ? pow2_frame(fmaxf(amax, 0x1p-118f)) * 256.f : NAN;
+}
+// Four bf16 elements (two words), times fr: codes of both terms.
+__device__ __forceinline__ void split4(uint32_t a, uint32_t b, float fr, uint32_t& t1, uint32_t& t2) {
+  const float v[4] = {__uint_as_float(a << 16) * fr, __uint_as_float(a & 0xffff0000u) * fr, __uint_as_float(b << 16) * fr,
+                      __uint_as_float(b & 0xffff0000u) * fr};
+  const uint32_t c0 = e4m3x2(v[0], v[1]), c1 = e4m3x2(v[2], v[3]);
+  const float2 f0 = from_e4m3x2(c0), f1 = from_e4m3x2(c1);
+  t1 = c0 | c1 << 16;
+  t2 = e4m3x2(v[0] - f0.x, v[1] - f0.y) | e4m3x2(v[2] - f1.x, v[3] - f1.y) << 16;
+}
+
 // Shared memory by 32-bit address: a pointer that went through an integer would
 // be taken for a generic one.
 __device__ __forceinline__ uint4 lds128(uint32_t a) {

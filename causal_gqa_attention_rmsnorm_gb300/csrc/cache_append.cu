@@ -124,21 +124,6 @@ __global__ void __launch_bounds__(256) k_append_rope(AppendArgs a, int with_kv) 
 
 // ---- e4m3 blocks -----------------------------------------------------------
 
-// Two values to e4m3 codes (low byte: lo), saturating at ±448; NaN stays NaN.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 e4m3x2_to_f(uint16_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-  float2 r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "r"(h));
-  return r;
-}
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // Smallest e in [kE4Min, kE4Max] with top <= 448·2^e (448 = 1.75·2^8).
 __device__ __forceinline__ int block_exp(float top) {
@@ -207,7 +192,7 @@ __global__ void __launch_bounds__(256) k_append_e4m3(AppendArgs a) {
       uint16_t* w = reinterpret_cast<uint16_t*>(&c);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float2 f = e4m3x2_to_f(w[u]);
+        const float2 f = from_e4m3x2(w[u]);
         w[u] = (uint16_t)e4m3x2(f.x * ratio, f.y * ratio);
       }
       *at = c;

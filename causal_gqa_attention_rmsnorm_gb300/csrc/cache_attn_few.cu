@@ -28,7 +28,9 @@
 //   product does not care which; ldmatrix.trans hands it two keys of two dims,
 //   which one byte permutation sorts into an even-dim and an odd-dim fragment.
 //   Queries enter as fp16 under a power of two per row that brings their
-//   largest element into [0.5, 1).
+//   largest element into [0.5, 1).  (8-bit warp-level MMAs on the K codes, with the
+//   queries split as for the tensor-memory kernel, ran slower: 108 against 100 us
+//   for 32 sequences of a 16k cache; they are not native here.)
 //   A V block's scale 2^e is never multiplied in: p' = 2^(z + e - m') carries
 //   it, O = Σ p'·code, l = Σ p'·2^-e, and the running maximum is that of z + e,
 //   so p' stays in fp16 whatever the scales.
@@ -116,13 +118,6 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
-// 2^-e with x·2^-e in [0.5, 1) for a normal x > 0, held to normal powers of two; 1 otherwise.
-__device__ __forceinline__ float pow2_frame(float x) {
-  if (!(x > 0.f)) return 1.f;
-  const int e = max(-126, min(126, (int)((__float_as_uint(x) >> 23) & 0xffu) - 126));
-  return __uint_as_float((uint32_t)(127 - e) << 23);
-}
-
 struct FewArgs {
   AttnArgs a;
   int b0;                 // first sequence of this launch (a's tensors start at sequence 0)

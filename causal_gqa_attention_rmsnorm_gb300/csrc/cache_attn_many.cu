@@ -27,13 +27,8 @@
 //   a cut one leave (max, sum, O) in the workspace and k_many_merge joins them in
 //   order.  The line's prefix sums come from k_many_plan.
 //
-//   e4m3: S is an 8-bit MMA on the K codes as they lie in the cache.  A query
-//   row, under a power of two that brings its largest element into [128, 256),
-//   is split into two e4m3 terms, q = q1 + q2: q1 takes the leading four bits of
-//   a bf16 element, the rest is at most half a step of q1 and has four bits
-//   itself, so the split is exact for elements down to 2^-2 and off by 2^-10 at
-//   most below (2^-17 of the row's largest); both terms multiply K, at twice the
-//   16-bit rate.  P has no such split that pays, so V becomes fp16 (exactly):
+//   e4m3: S is an 8-bit MMA on the K codes as they lie in the cache, the queries
+//   split into two e4m3 terms (split4), at twice the 16-bit rate.  P has no such split that pays, so V becomes fp16 (exactly):
 //   TMA brings 32-key chunks of codes through a ring and conversion warps write
 //   them into the swizzled V tile.  K scales multiply the scores per 16
 //   keys; V scales 2^e enter the exponent, p' = 2^(z + e - m'), so that
@@ -328,33 +323,12 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
-__device__ __forceinline__ float pow2_frame(float x) {
-  if (!(x > 0.f)) return 1.f;
-  const int e = max(-126, min(126, (int)((__float_as_uint(x) >> 23) & 0xffu) - 126));
-  return __uint_as_float((uint32_t)(127 - e) << 23);
-}
 // Instruction descriptor of P·V, kind::f16 with fp16 (E4) or bf16 operands, fp32
 // sums, V MN-major.
 template <bool E4>
 __host__ __device__ constexpr uint32_t idesc_pv(int M, int N) {
   return idesc_bf16(M, N, false, true) & ~(E4 ? (1u << 7 | 1u << 10) : 0u);
 }
-// Two values to e4m3 codes (low byte: lo), and back.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-  float2 r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "r"(h));
-  return r;
-}
-
 template <int DH, bool E4>
 __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
     k_attn_many(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -878,8 +852,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
               for (int j = 0; j < 4; ++j)
                 amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xffff0000u))));
             }
-            // an infinity must not saturate: its row becomes NaN
-            const float fr = amax <= 3.402823466e38f ? pow2_frame(fmaxf(amax, 0x1p-118f)) * 256.f : NAN;
+            const float fr = split_frame(amax);
             zs /= fr;                           // exact
             const uint32_t t1 = smem_u32(smem) + C::OFF_QT + g * C::Q_BYTES, t2 = t1 + C::QT_BYTES;
 #pragma unroll
@@ -889,12 +862,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const uint32_t* u = &w[2 * i + (j >> 1)].x + 2 * (j & 1);
-                float v[4] = {__uint_as_float(u[0] << 16) * fr, __uint_as_float(u[0] & 0xffff0000u) * fr,
-                              __uint_as_float(u[1] << 16) * fr, __uint_as_float(u[1] & 0xffff0000u) * fr};
-                const uint32_t c0 = e4m3x2(v[0], v[1]), c1 = e4m3x2(v[2], v[3]);
-                const float2 f0 = from_e4m3x2(c0), f1 = from_e4m3x2(c1);
-                u1[j] = c0 | c1 << 16;
-                u2[j] = e4m3x2(v[0] - f0.x, v[1] - f0.y) | e4m3x2(v[2] - f1.x, v[3] - f1.y) << 16;
+                split4(u[0], u[1], fr, u1[j], u2[j]);
               }
               const uint32_t at = DH == 128 ? r * 128 + (((i ^ r) & 7) << 4) : r * 64 + (((i ^ (r >> 1)) & 3) << 4);
               sts128(t1 + at, a1);
