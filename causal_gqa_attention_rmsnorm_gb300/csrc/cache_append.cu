@@ -85,41 +85,95 @@ __global__ void k_append_lens(AppendArgs a) {
   if (b < a.c.B) set_len(a, b);
 }
 
-// q, k and v rows of 16- and 32-bit types.  A thread holds one eight-element
-// piece of a token's head and that piece's four (cos, sin) pairs, and walks the
-// heads of the token: H of q (if any), then Hkv of k and of v.
+// Eight elements as they lie in memory.
+template <typename T> struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = sizeof(T) == 4 ? __uint_as_float((&v[0].x)[i])
+                            : __uint_as_float(i & 1 ? (&v[0].x)[i >> 1] & 0xffff0000u : (&v[0].x)[i >> 1] << 16);
+  }
+};
+
+// The rows of one token, by one CTA: q, and for 16- and 32-bit caches (with_kv) k
+// and v.  A thread holds one eight-element piece of a head and that piece's four
+// (cos, sin) pairs and walks the heads of the token, H of q (if any), then Hkv of k
+// and of v, three of them on their way at a time.
 template <typename T>
-__global__ void __launch_bounds__(256) k_append_rope(AppendArgs a, int with_kv) {
-  pdl_trigger();
-  pdl_wait();
+__device__ __forceinline__ void rotate_token(const AppendArgs& a, int b, int i, bool with_kv) {
   const int pieces = a.c.dh / kVec;
   const int per = blockDim.x / pieces;                  // heads in step
   const int e = (threadIdx.x % pieces) * kVec, h0 = threadIdx.x / pieces;
-  const int b = blockIdx.y, i = blockIdx.x;
-  if (a.start && i == 0 && threadIdx.x == 0) set_len(a, b);
+  if (h0 >= per) return;
+  const int Hkv = a.c.Hkv, H = a.q ? a.H : 0, dh = a.c.dh;
+  const T* src_q = (const T*)a.q + b * a.q_seq + i * a.q_tok + e;
+  const T* src_k = (const T*)a.k + b * a.k_seq + i * a.k_tok + e;
+  const T* src_v = (const T*)a.v + b * a.v_seq + i * a.v_tok + e;
+  const int total = H + (with_kv ? 2 * Hkv : 0);
+  constexpr int kAhead = 3;
+  Raw8<T> raw[kAhead];
+  auto load = [&](int hb) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = hb + u * per;
+      if (h < total)
+        raw[u].load(h < H ? src_q + (size_t)h * dh
+                          : h < H + Hkv ? src_k + (size_t)(h - H) * dh : src_v + (size_t)(h - H - Hkv) * dh);
+    }
+  };
+  load(h0);             // on their way while the position, the page and the angles arrive
   const Place p = place_of(a, b);
-  if (i >= p.nn || h0 >= per) return;
-  const int pos = p.t0 + i, Hkv = a.c.Hkv, H = a.q ? a.H : 0, dh = a.c.dh;
+  if (i >= p.nn) return;
+  const int pos = p.t0 + i;
   float4 cs[2];
   load_cs(a, pos, e, cs);
-  const int total = H + (with_kv ? 2 * Hkv : 0);
-  for (int h = h0; h < total; h += per) {
-    float x[8];
-    if (h < H) {
-      load8((const T*)a.q + b * a.q_seq + i * a.q_tok + (size_t)h * dh + e, x);
-      rotate8(x, cs);
-      store8((T*)a.q_out + (((size_t)b * a.n + i) * H + h) * dh + e, x);
-      continue;
-    }
-    const bool is_k = h < H + Hkv;
-    const int hk = h - H - (is_k ? 0 : Hkv);
-    load8(is_k ? (const T*)a.k + b * a.k_seq + i * a.k_tok + (size_t)hk * dh + e
-               : (const T*)a.v + b * a.v_seq + i * a.v_tok + (size_t)hk * dh + e,
-          x);
-    if (is_k) rotate8(x, cs);
-    const long long row = cache_row(a.c, b, hk, pos);
-    if (row >= 0) store8((T*)(is_k ? a.c.k : a.c.v) + row * dh + e, x);
+  // (plane of KV head 0, row in it): the same page for all heads
+  long long plane0 = (long long)b * Hkv;
+  int in_plane = pos, plane_rows = a.c.T;
+  if (with_kv && a.c.bt) {
+    const int page = cache_page(a.c, b, pos);
+    plane0 = page < 0 ? -1 : (long long)page * Hkv;
+    in_plane = pos % a.c.ps;
+    plane_rows = a.c.ps;
   }
+  T* dst_q = (T*)a.q_out + ((size_t)b * a.n + i) * H * dh + e;
+  for (int hb = h0; hb < total; hb += kAhead * per) {
+    if (hb != h0) load(hb);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = hb + u * per;
+      if (h >= total) break;
+      if (h < H + Hkv) {                                // (v is stored as it came)
+        float x[8];
+        raw[u].get(x);
+        rotate8(x, cs);
+        if (h < H) {
+          store8(dst_q + (size_t)h * dh, x);
+          continue;
+        }
+        if (plane0 >= 0) store8((T*)a.c.k + ((plane0 + h - H) * plane_rows + in_plane) * dh + e, x);
+      } else if (plane0 >= 0) {
+        raw[u].store((T*)a.c.v + ((plane0 + h - H - Hkv) * plane_rows + in_plane) * dh + e);
+      }
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) k_append_rope(AppendArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  if (a.start && blockIdx.x == 0 && threadIdx.x == 0) set_len(a, blockIdx.y);
+  rotate_token<T>(a, blockIdx.y, blockIdx.x, true);
 }
 
 // ---- e4m3 blocks -----------------------------------------------------------
@@ -134,26 +188,35 @@ __device__ __forceinline__ int block_exp(float top) {
 // An infinity is stored as NaN: the code has none.
 __device__ __forceinline__ float no_inf(float x) { return fabsf(x) <= 3.402823466e38f ? x : NAN; }
 
-// One CTA per (block of the cache, KV head, sequence and K or V): the largest
-// magnitude of the block's new rows, the scale, then the codes; the rows are
+// The blocks first, then q: CTA i of the first n_blocks takes one block of the
+// cache, one KV head, one sequence and K or V; each of the others one token's q.
+// For a block: the largest magnitude of its new rows, the scale, then the codes.
+// With NP > 0 a thread holds its NP eight-element pieces, rotated, from the one
+// pass to the other (32 bits each); with NP = 0 (blocks of more rows) the rows are
 // read twice, the second time from L1/L2.
-__global__ void __launch_bounds__(256) k_append_e4m3(AppendArgs a) {
+template <int NP>
+__global__ void __launch_bounds__(256) k_append_e4m3(AppendArgs a, int nb, unsigned n_blocks) {
   pdl_trigger();
   pdl_wait();
-  const int b = blockIdx.z >> 1, is_v = blockIdx.z & 1, h = blockIdx.y;
+  if (blockIdx.x >= n_blocks) {
+    const unsigned t = blockIdx.x - n_blocks;
+    rotate_token<bf16>(a, (int)(t / (unsigned)a.n), (int)(t % (unsigned)a.n), false);
+    return;
+  }
+  const int h = blockIdx.x % a.c.Hkv, is_v = blockIdx.x / a.c.Hkv & 1;
+  const int bi = blockIdx.x / (2 * a.c.Hkv) % nb, b = blockIdx.x / (2 * a.c.Hkv) / nb;
+  if (a.start && h == 0 && is_v == 0 && bi == 0 && threadIdx.x == 0) set_len(a, b);
   const Place p = place_of(a, b);
   if (p.nn <= 0) return;
   const int bs = a.c.ps, dh = a.c.dh;
-  const int blk = p.t0 / bs + blockIdx.x;
+  const int blk = p.t0 / bs + bi;
   const int t_lo = max(p.t0, blk * bs), t_hi = min(p.t0 + p.nn, (blk + 1) * bs);
   if (t_lo >= t_hi) return;
-  long long sc;
+  // (the page's look-up, and with it the scale's, is on its way with the rows)
+  long long sc = 0;
   const long long row0 = cache_row(a.c, b, h, blk * bs, &sc);
-  if (row0 < 0) return;
   const bf16* src = is_v ? (const bf16*)a.v + b * a.v_seq + (size_t)h * dh : (const bf16*)a.k + b * a.k_seq + (size_t)h * dh;
   const long long tok = is_v ? a.v_tok : a.k_tok;
-  uint8_t* dst = (uint8_t*)(is_v ? a.c.v : a.c.k) + row0 * dh;
-  float* scale = (is_v ? a.c.vs : a.c.ks) + sc;
   const int pieces = dh / kVec, n_pieces = (t_hi - t_lo) * pieces;
   auto fetch = [&](int i, float (&x)[8]) {
     const int t = t_lo + i / pieces, e = (i % pieces) * kVec;
@@ -163,14 +226,33 @@ __global__ void __launch_bounds__(256) k_append_e4m3(AppendArgs a) {
       load_cs(a, t, e, cs);
       rotate8(x, cs);
     }
-  };
-  float top = 0.f;
-  for (int i = threadIdx.x; i < n_pieces; i += blockDim.x) {
-    float x[8];
-    fetch(i, x);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) top = fmaxf(top, fabsf(no_inf(x[u])));     // fmaxf drops NaN
+    for (int u = 0; u < 8; ++u) x[u] = no_inf(x[u]);
+  };
+  float held[NP > 0 ? NP : 1][8];
+  float top = 0.f;
+  auto take = [&](const float (&x)[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) top = fmaxf(top, fabsf(x[u]));     // fmaxf drops NaN
+  };
+  if constexpr (NP > 0) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int i = threadIdx.x + j * blockDim.x;
+      if (i < n_pieces) {
+        fetch(i, held[j]);
+        take(held[j]);
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < n_pieces; i += blockDim.x) {
+      fetch(i, held[0]);
+      take(held[0]);
+    }
   }
+  if (row0 < 0) return;                                  // a page outside the pool
+  uint8_t* dst = (uint8_t*)(is_v ? a.c.v : a.c.k) + row0 * dh;
+  float* scale = (is_v ? a.c.vs : a.c.ks) + sc;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   __shared__ float red[8];
@@ -198,34 +280,54 @@ __global__ void __launch_bounds__(256) k_append_e4m3(AppendArgs a) {
       *at = c;
     }
   }
-  for (int i = threadIdx.x; i < n_pieces; i += blockDim.x) {
-    float x[8];
-    fetch(i, x);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) x[u] = no_inf(x[u]) * inv;
+  auto put = [&](int i, const float (&x)[8]) {
     uint2 w;
-    w.x = e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16;
-    w.y = e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16;
+    w.x = e4m3x2(x[0] * inv, x[1] * inv) | e4m3x2(x[2] * inv, x[3] * inv) << 16;
+    w.y = e4m3x2(x[4] * inv, x[5] * inv) | e4m3x2(x[6] * inv, x[7] * inv) << 16;
     const int t = t_lo + i / pieces, e = (i % pieces) * kVec;
     *reinterpret_cast<uint2*>(dst + (size_t)(t - blk * bs) * dh + e) = w;
+  };
+  if constexpr (NP > 0) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int i = threadIdx.x + j * blockDim.x;
+      if (i < n_pieces) put(i, held[j]);
+    }
+  } else {
+    for (int i = threadIdx.x; i < n_pieces; i += blockDim.x) {
+      fetch(i, held[0]);
+      put(i, held[0]);
+    }
   }
 }
 
 }  // namespace
 
 cudaError_t launch_append_rope(const AppendArgs& a, cudaStream_t s) {
-  const bool e4 = a.c.dtype == TB_E4M3;
   cudaError_t e = cudaSuccess;
-  const dim3 grid((unsigned)a.n, (unsigned)a.c.B);
-  if (a.c.dtype == TB_F32)
-    e = launch_pdl(k_append_rope<float>, grid, dim3(256), 0, s, a, 1);
-  else
-    e = launch_pdl(k_append_rope<bf16>, grid, dim3(256), 0, s, a, e4 ? 0 : 1);
-  if (e == cudaSuccess && e4) {
+  if (a.c.dtype != TB_E4M3) {
+    const dim3 grid((unsigned)a.n, (unsigned)a.c.B);
+    e = a.c.dtype == TB_F32 ? launch_pdl(k_append_rope<float>, grid, dim3(256), 0, s, a)
+                            : launch_pdl(k_append_rope<bf16>, grid, dim3(256), 0, s, a);
+  } else {
     const int nb = (a.n + a.c.ps - 2) / a.c.ps + 1;        // blocks that n rows can reach from any start
-    const int rows = std::min(a.n, a.c.ps);
-    const int threads = std::min(256, (rows * (a.c.dh / kVec) + 31) / 32 * 32);
-    e = launch_pdl(k_append_e4m3, dim3((unsigned)nb, a.c.Hkv, 2 * a.c.B), dim3(threads), 0, s, a);
+    const long long blocks = 2LL * a.c.Hkv * nb * a.c.B, tokens = a.q ? (long long)a.n * a.c.B : 0;
+    if (blocks + tokens > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const int pieces = std::min(a.n, a.c.ps) * (a.c.dh / kVec);      // of a block, at most
+    const int threads = std::min(256, std::max(a.q ? 128 : 32, (pieces + 31) / 32 * 32));
+    const dim3 grid((unsigned)(blocks + tokens));
+    const unsigned first = (unsigned)blocks;
+    const int np = (pieces + threads - 1) / threads;
+    if (np <= 1)
+      e = launch_pdl(k_append_e4m3<1>, grid, dim3(threads), 0, s, a, nb, first);
+    else if (np <= 2)
+      e = launch_pdl(k_append_e4m3<2>, grid, dim3(threads), 0, s, a, nb, first);
+    else if (np <= 4)
+      e = launch_pdl(k_append_e4m3<4>, grid, dim3(threads), 0, s, a, nb, first);
+    else if (np <= 8)
+      e = launch_pdl(k_append_e4m3<8>, grid, dim3(threads), 0, s, a, nb, first);
+    else
+      e = launch_pdl(k_append_e4m3<0>, grid, dim3(threads), 0, s, a, nb, first);
   }
   if (e == cudaSuccess && !a.start)
     e = launch_pdl(k_append_lens, dim3((a.c.B + 127) / 128), dim3(128), 0, s, a);
