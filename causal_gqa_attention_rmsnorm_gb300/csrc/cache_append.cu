@@ -104,22 +104,30 @@ template <typename T> struct Raw8 {
   }
 };
 
-// The rows of one token, by one CTA: q, and for 16- and 32-bit caches (with_kv) k
+// The rows of one token, by a group of threads (`me` of `group`): q, and for 16- and 32-bit caches (with_kv) k
 // and v.  A thread holds one eight-element piece of a head and that piece's four
 // (cos, sin) pairs and walks the heads of the token, H of q (if any), then Hkv of k
 // and of v, three of them on their way at a time.
+constexpr int kAhead = 3;
+// Threads of a group: a power of two that holds a head, and the token's `total`
+// heads kAhead to a thread where 256 threads can.
+int group_of(int dh, int total) {
+  const int pieces = dh / kVec;
+  int g = 32;
+  while (g < 256 && (g < pieces || g * kAhead < total * pieces)) g *= 2;
+  return g;
+}
 template <typename T>
-__device__ __forceinline__ void rotate_token(const AppendArgs& a, int b, int i, bool with_kv) {
+__device__ __forceinline__ void rotate_token(const AppendArgs& a, int b, int i, int me, int group, bool with_kv) {
   const int pieces = a.c.dh / kVec;
-  const int per = blockDim.x / pieces;                  // heads in step
-  const int e = (threadIdx.x % pieces) * kVec, h0 = threadIdx.x / pieces;
+  const int per = group / pieces;                       // heads in step
+  const int e = (me % pieces) * kVec, h0 = me / pieces;
   if (h0 >= per) return;
   const int Hkv = a.c.Hkv, H = a.q ? a.H : 0, dh = a.c.dh;
   const T* src_q = (const T*)a.q + b * a.q_seq + i * a.q_tok + e;
   const T* src_k = (const T*)a.k + b * a.k_seq + i * a.k_tok + e;
   const T* src_v = (const T*)a.v + b * a.v_seq + i * a.v_tok + e;
   const int total = H + (with_kv ? 2 * Hkv : 0);
-  constexpr int kAhead = 3;
   Raw8<T> raw[kAhead];
   auto load = [&](int hb) {
 #pragma unroll
@@ -169,11 +177,13 @@ __device__ __forceinline__ void rotate_token(const AppendArgs& a, int b, int i, 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) k_append_rope(AppendArgs a) {
+__global__ void __launch_bounds__(256, 6) k_append_rope(AppendArgs a, int group) {
   pdl_trigger();
   pdl_wait();
-  if (a.start && blockIdx.x == 0 && threadIdx.x == 0) set_len(a, blockIdx.y);
-  rotate_token<T>(a, blockIdx.y, blockIdx.x, true);
+  const int sh = 31 - __clz(group), i = blockIdx.x * (blockDim.x >> sh) + (threadIdx.x >> sh), me = threadIdx.x & (group - 1);
+  if (i >= a.n) return;
+  if (a.start && i == 0 && me == 0) set_len(a, blockIdx.y);
+  rotate_token<T>(a, blockIdx.y, i, me, group, true);
 }
 
 // ---- e4m3 blocks -----------------------------------------------------------
@@ -189,18 +199,19 @@ __device__ __forceinline__ int block_exp(float top) {
 __device__ __forceinline__ float no_inf(float x) { return fabsf(x) <= 3.402823466e38f ? x : NAN; }
 
 // The blocks first, then q: CTA i of the first n_blocks takes one block of the
-// cache, one KV head, one sequence and K or V; each of the others one token's q.
+// cache, one KV head, one sequence and K or V; the others take q's tokens.
 // For a block: the largest magnitude of its new rows, the scale, then the codes.
 // With NP > 0 a thread holds its NP eight-element pieces, rotated, from the one
 // pass to the other (32 bits each); with NP = 0 (blocks of more rows) the rows are
 // read twice, the second time from L1/L2.
 template <int NP>
-__global__ void __launch_bounds__(256) k_append_e4m3(AppendArgs a, int nb, unsigned n_blocks) {
+__global__ void __launch_bounds__(256) k_append_e4m3(AppendArgs a, int nb, unsigned n_blocks, int group, unsigned q_ctas) {
   pdl_trigger();
   pdl_wait();
   if (blockIdx.x >= n_blocks) {
-    const unsigned t = blockIdx.x - n_blocks;
-    rotate_token<bf16>(a, (int)(t / (unsigned)a.n), (int)(t % (unsigned)a.n), false);
+    const unsigned c = blockIdx.x - n_blocks, b = c / q_ctas;             // q_ctas: of a sequence
+    const int sh = 31 - __clz(group), i = (int)(c - b * q_ctas) * (blockDim.x >> sh) + (threadIdx.x >> sh);
+    if (i < a.n) rotate_token<bf16>(a, (int)b, i, threadIdx.x & (group - 1), group, false);
     return;
   }
   const int h = blockIdx.x % a.c.Hkv, is_v = blockIdx.x / a.c.Hkv & 1;
@@ -306,28 +317,39 @@ __global__ void __launch_bounds__(256) k_append_e4m3(AppendArgs a, int nb, unsig
 cudaError_t launch_append_rope(const AppendArgs& a, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (a.c.dtype != TB_E4M3) {
-    const dim3 grid((unsigned)a.n, (unsigned)a.c.B);
-    e = a.c.dtype == TB_F32 ? launch_pdl(k_append_rope<float>, grid, dim3(256), 0, s, a)
-                            : launch_pdl(k_append_rope<bf16>, grid, dim3(256), 0, s, a);
+    const int group = group_of(a.c.dh, (a.q ? a.H : 0) + 2 * a.c.Hkv);
+    int threads = group;
+    while (threads < 256 && threads / group < a.n) threads *= 2;
+    const dim3 grid((unsigned)((a.n + threads / group - 1) / (threads / group)), (unsigned)a.c.B);
+    e = a.c.dtype == TB_F32 ? launch_pdl(k_append_rope<float>, grid, dim3(threads), 0, s, a, group)
+                            : launch_pdl(k_append_rope<bf16>, grid, dim3(threads), 0, s, a, group);
   } else {
     const int nb = (a.n + a.c.ps - 2) / a.c.ps + 1;        // blocks that n rows can reach from any start
-    const long long blocks = 2LL * a.c.Hkv * nb * a.c.B, tokens = a.q ? (long long)a.n * a.c.B : 0;
-    if (blocks + tokens > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int pieces = std::min(a.n, a.c.ps) * (a.c.dh / kVec);      // of a block, at most
-    const int threads = std::min(256, std::max(a.q ? 128 : 32, (pieces + 31) / 32 * 32));
+    // (a step of few rows per block has many small CTAs: q takes no more than half
+    // of the usual threads there)
+    int group = group_of(a.c.dh, a.q ? a.H : 0);
+    if (pieces <= 128) group = std::min(group, 128);
+    // a power of two, so that whole groups of q's tokens fill a CTA
+    int threads = 32;
+    while (threads < 256 && (threads < pieces || (a.q && threads < group))) threads *= 2;
+    const long long blocks = 2LL * a.c.Hkv * nb * a.c.B;
+    const unsigned q_ctas = (unsigned)((a.n + threads / group - 1) / (threads / group));
+    const long long tokens = a.q ? (long long)q_ctas * a.c.B : 0;
+    if (blocks + tokens > 0x7fffffffLL) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)(blocks + tokens));
     const unsigned first = (unsigned)blocks;
     const int np = (pieces + threads - 1) / threads;
     if (np <= 1)
-      e = launch_pdl(k_append_e4m3<1>, grid, dim3(threads), 0, s, a, nb, first);
+      e = launch_pdl(k_append_e4m3<1>, grid, dim3(threads), 0, s, a, nb, first, group, q_ctas);
     else if (np <= 2)
-      e = launch_pdl(k_append_e4m3<2>, grid, dim3(threads), 0, s, a, nb, first);
+      e = launch_pdl(k_append_e4m3<2>, grid, dim3(threads), 0, s, a, nb, first, group, q_ctas);
     else if (np <= 4)
-      e = launch_pdl(k_append_e4m3<4>, grid, dim3(threads), 0, s, a, nb, first);
+      e = launch_pdl(k_append_e4m3<4>, grid, dim3(threads), 0, s, a, nb, first, group, q_ctas);
     else if (np <= 8)
-      e = launch_pdl(k_append_e4m3<8>, grid, dim3(threads), 0, s, a, nb, first);
+      e = launch_pdl(k_append_e4m3<8>, grid, dim3(threads), 0, s, a, nb, first, group, q_ctas);
     else
-      e = launch_pdl(k_append_e4m3<0>, grid, dim3(threads), 0, s, a, nb, first);
+      e = launch_pdl(k_append_e4m3<0>, grid, dim3(threads), 0, s, a, nb, first, group, q_ctas);
   }
   if (e == cudaSuccess && !a.start)
     e = launch_pdl(k_append_lens, dim3((a.c.B + 127) / 128), dim3(128), 0, s, a);
