@@ -307,6 +307,18 @@ __global__ void __launch_bounds__(1024) k_many_plan(const ManyArgs m, int n_flag
 
 // ---- the kernel ---------------------------------------------------------------
 
+// mbar_wait with all but the first attempt out of line: the loops of all roles run
+// at once and have to share the instruction cache.
+__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  return mbar_wait(bar, parity, abort, err);
+}
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  return mbar_try_wait(smem_u32(bar), parity) || wait_longer(bar, parity, abort, err);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  const bool ok = wait_one(bar, parity, abort, err);
+  return __all_sync(0xffffffffu, ok);
+}
 __device__ __forceinline__ void tma_load_4d(const CUtensorMap* m, void* dst, uint64_t* bar, int x, int y, int z, int w) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
@@ -409,7 +421,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
   // (or a wait that ran out).  done(k) hands the descriptor back.
   auto piece = [&](int k, PieceDesc*& d) -> bool {
     d = descs + k % kDescs;
-    return mbar_wait_warp(&d_full[k % kDescs], (k / kDescs) & 1, abort_flag, err) && !d->last;
+    return wait_warp(&d_full[k % kDescs], (k / kDescs) & 1, abort_flag, err) && !d->last;
   };
   auto done = [&](int k) {
     __syncwarp();
@@ -425,7 +437,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
     bool ok = true;
     Pieces pc(m, x0, x1);
     auto publish = [&](int k, bool last) -> bool {
-      if (k >= kDescs && !mbar_wait_warp(&d_empty[k % kDescs], ((k / kDescs) & 1) ^ 1u, abort_flag, err)) return false;
+      if (k >= kDescs && !wait_warp(&d_empty[k % kDescs], ((k / kDescs) & 1) ^ 1u, abort_flag, err)) return false;
       if (lane == 0) {
         PieceDesc& d = descs[k % kDescs];
         d.t0 = pc.t0;
@@ -457,7 +469,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
       if (!more) break;
       if (pc.t0 == pc.t1) continue;             // rows without keys
       const Item& it = pc.it;
-      if (nq > 0 && !mbar_wait_warp(q_empty, (nq - 1) & 1, abort_flag, err)) {
+      if (nq > 0 && !wait_warp(q_empty, (nq - 1) & 1, abort_flag, err)) {
         ok = false;
         break;
       }
@@ -540,7 +552,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[sl]);
         }
-        if (!mbar_wait_warp(&k_empty[st], ph ^ 1u, abort_flag, err)) {
+        if (!wait_warp(&k_empty[st], ph ^ 1u, abort_flag, err)) {
           ok = false;
           break;
         }
@@ -558,7 +570,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         }
         ++nk;
         if constexpr (!E4) {
-          if (!mbar_wait_warp(&v_empty[st], ph ^ 1u, abort_flag, err)) {
+          if (!wait_warp(&v_empty[st], ph ^ 1u, abort_flag, err)) {
             ok = false;
             break;
           }
@@ -583,7 +595,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         } else {
           for (int ch = 0; ch < kBN / kChunk; ++ch, ++nv) {
             const int rs = nv % kRaw;
-            if (!mbar_wait_warp(&raw_empty[rs], ((nv / kRaw) & 1) ^ 1u, abort_flag, err)) {
+            if (!wait_warp(&raw_empty[rs], ((nv / kRaw) & 1) ^ 1u, abort_flag, err)) {
               ok = false;
               break;
             }
@@ -652,7 +664,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
       int kc = 0, nq = 0, c0 = 0, c1 = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        if (!mbar_wait(&d_full[k % kDescs], (k / kDescs) & 1, abort_flag, err)) break;
+        if (!wait_one(&d_full[k % kDescs], (k / kDescs) & 1, abort_flag, err)) break;
         const PieceDesc pc = descs[k % kDescs];
         mbar_arrive(&d_empty[k % kDescs]);
         if (pc.last) break;
@@ -662,8 +674,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         const int f0 = s0.first_on(pc.t0, pc.t1), l0 = s0.last_on(pc.t0, pc.t1);
         const int f1 = s1.first_on(pc.t0, pc.t1), l1 = s1.last_on(pc.t0, pc.t1);
         bool on0 = s0.on(pc.t0), on1 = s1.on(pc.t0);
-        if (!mbar_wait(E4 ? q_ready : q_full, nq & 1, abort_flag, err) ||
-            !mbar_wait(&k_full[kc & 1], (kc >> 1) & 1, abort_flag, err))
+        if (!wait_one(E4 ? q_ready : q_full, nq & 1, abort_flag, err) ||
+            !wait_one(&k_full[kc & 1], (kc >> 1) & 1, abort_flag, err))
           break;
         ++nq;
         tc_fence_after();
@@ -674,12 +686,12 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         for (int jj = 0; jj < nt; ++jj) {
           const int t = kc + jj, x = pc.t0 + jj;
           const bool next = jj + 1 < nt, on0n = next && s0.on(x + 1), on1n = next && s1.on(x + 1);
-          if (!mbar_wait(&v_full[t & 1], (t >> 1) & 1, abort_flag, err)) {
+          if (!wait_one(&v_full[t & 1], (t >> 1) & 1, abort_flag, err)) {
             ok = false;
             break;
           }
           if (on0) {
-            if (!mbar_wait(&p_full[0], c0 & 1, abort_flag, err)) {
+            if (!wait_one(&p_full[0], c0 & 1, abort_flag, err)) {
               ok = false;
               break;
             }
@@ -689,7 +701,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
             if (x == l0) mma_commit(&o_full[0]);
           }
           if (next) {
-            if (!mbar_wait(&k_full[(t + 1) & 1], ((t + 1) >> 1) & 1, abort_flag, err)) {
+            if (!wait_one(&k_full[(t + 1) & 1], ((t + 1) >> 1) & 1, abort_flag, err)) {
               ok = false;
               break;
             }
@@ -697,7 +709,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
             if (on0n) issue_s(0, t + 1);
           }
           if (on1) {
-            if (!mbar_wait(&p_full[1], c1 & 1, abort_flag, err)) {
+            if (!wait_one(&p_full[1], c1 & 1, abort_flag, err)) {
               ok = false;
               break;
             }
@@ -737,8 +749,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
 #pragma unroll 1
           for (int ch = me; ch < kBN / kChunk; ch += kConv) {
             const int n = nt * (kBN / kChunk) + ch, rs = n % kRaw;     // running chunk
-            if (!mbar_wait_warp(&v_empty[st], ((nt >> 1) & 1) ^ 1u, abort_flag, err) ||
-                !mbar_wait_warp(&raw_full[rs], (n / kRaw) & 1, abort_flag, err)) {
+            if (!wait_warp(&v_empty[st], ((nt >> 1) & 1) ^ 1u, abort_flag, err) ||
+                !wait_warp(&raw_full[rs], (n / kRaw) & 1, abort_flag, err)) {
               ok = false;
               break;
             }
@@ -799,7 +811,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         for (int x = pc.t0; x < pc.t1; ++x, ++nt) {
           const int key = pc.key(x), st = nt & 1;
           if (!pc.border(key)) continue;
-          if (!mbar_wait_warp(&fix_full[st], n_fix[st] & 1, abort_flag, err)) {
+          if (!wait_warp(&fix_full[st], n_fix[st] & 1, abort_flag, err)) {
             ok = false;
             break;
           }
@@ -824,6 +836,10 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
     const int r = quad * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t s_col = lane_base + g * kBN, o_col = lane_base + C::TMEM_O + g * DH;
+    // (16-bit caches leave room for the whole wait in line, and a call costs registers)
+    auto soft_wait = [](uint64_t* bar, uint32_t parity, volatile int* abort, int* e) {
+      return E4 ? wait_warp(bar, parity, abort, e) : mbar_wait_warp(bar, parity, abort, e);
+    };
     int c = 0, nt = 0, nq = 0, no = 0;          // this slot's tiles; key tiles, pieces with keys, outputs
     bool ok = true;
     PieceDesc* d;
@@ -836,7 +852,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
       if constexpr (E4) {
         // this row of Q as two e4m3 terms, its largest element in [128, 256)
         if (t0 < t1) {
-          if (!mbar_wait_warp(q_full, nq & 1, abort_flag, err)) {
+          if (!soft_wait(q_full, nq & 1, abort_flag, err)) {
             ok = false;
             break;
           }
@@ -882,12 +898,12 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
       for (int x = f_on; x >= 0 && x <= l_on; x = x + 1 >= ia && x + 1 < ib ? ib : x + 1) {
         const int tn = tn0 + x;                 // the CTA's running key tile
         if constexpr (E4) {
-          if (!mbar_wait_warp(&sc_full[tn % kScTiles], (tn / kScTiles) & 1, abort_flag, err)) {
+          if (!soft_wait(&sc_full[tn % kScTiles], (tn / kScTiles) & 1, abort_flag, err)) {
             ok = false;
             break;
           }
         }
-        if (!mbar_wait_warp(&s_full[g], c & 1, abort_flag, err)) {
+        if (!soft_wait(&s_full[g], c & 1, abort_flag, err)) {
           ok = false;
           break;
         }
@@ -904,7 +920,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
           else
             need = m_new > m_used + kRescale;
           if (__any_sync(0xffffffffu, need)) {
-            if (!mbar_wait_warp(&pv_done[g], (c - 1) & 1, abort_flag, err)) return false;
+            if (!soft_wait(&pv_done[g], (c - 1) & 1, abort_flag, err)) return false;
             tc_fence_after();
             const float factor = need ? ex2_approx(m_used - m_new) : 1.f;
 #pragma unroll 1
@@ -1085,7 +1101,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         }
         continue;
       }
-      if (!mbar_wait_warp(&o_full[g], no & 1, abort_flag, err)) {
+      if (!soft_wait(&o_full[g], no & 1, abort_flag, err)) {
         ok = false;
         break;
       }
