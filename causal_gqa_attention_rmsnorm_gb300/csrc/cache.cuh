@@ -187,7 +187,7 @@ cudaError_t launch_append_rope(const AppendArgs& a, cudaStream_t s);
 
 // cache_attn_few.cu: up to kFewRows query rows (tokens x heads) per KV head,
 // 16-bit queries over bf16 or e4m3 rows of dh 64 or 128.
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 32;
 size_t cache_attn_few_workspace(const AttnArgs& a);
 cudaError_t launch_cache_attn_few(const AttnArgs& a, void* ws, cudaStream_t s);
 // cache_attn_many.cu: any number of rows, same types and widths.

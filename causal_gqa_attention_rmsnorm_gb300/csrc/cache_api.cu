@@ -10,6 +10,10 @@ namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return a < b + nq && b < a + np;
+}
 
 // Layout rules of a cache these calls take; its tensors too with `tensors`.
 tb_status check_cache(const tb_kvcache* kv, bool tensors) {
@@ -145,13 +149,26 @@ tb_status tb_kvcache_append_rope(const tb_kvcache* kv, const tb_append_rows* row
   for (int i = rows->q ? 0 : 2; i < 6; ++i)
     if (strides[i] % 8 || strides[i] < 0)
       return report(TB_ERR_INVALID_ARG, "row strides must be non-negative multiples of 8 elements");
-  if (rows->q == rows->q_out && rows->q &&
-      (rows->q_tok != (int64_t)rows->H * kv->dh || rows->q_seq != rows->q_tok * rows->n))
-    return report(TB_ERR_INVALID_ARG, "q_out may be q only where q is dense");
   if (!aligned4(rows->start) || !aligned4(rows->n_new))
     return report(TB_ERR_INVALID_ARG, "start and n_new must be 4-byte aligned");
-  if (rows->start && rows->start < kv->lens + kv->B && kv->lens < rows->start + kv->B)
-    return report(TB_ERR_INVALID_ARG, "start may not overlap lens (NULL stands for lens)");
+  const size_t lens_bytes = (size_t)kv->B * 4;
+  if ((rows->start && overlap(rows->start, lens_bytes, kv->lens, lens_bytes)) ||
+      (rows->n_new && overlap(rows->n_new, lens_bytes, kv->lens, lens_bytes)))
+    return report(TB_ERR_INVALID_ARG, "start and n_new may not overlap lens (a NULL start stands for lens)");
+  if (rows->q) {
+    const size_t es = kv->dtype == TB_F32 ? 4 : 2;
+    auto extent = [&](int64_t tok, int64_t seq, int heads) {
+      return ((size_t)(kv->B - 1) * seq + (size_t)(rows->n - 1) * tok + (size_t)heads * kv->dh) * es;
+    };
+    const size_t out = (size_t)kv->B * rows->n * rows->H * kv->dh * es;
+    const bool dense = (rows->n == 1 || rows->q_tok == (int64_t)rows->H * kv->dh) &&
+                       (kv->B == 1 || rows->q_seq == (int64_t)rows->H * kv->dh * rows->n);
+    if (rows->q == rows->q_out ? !dense : overlap(rows->q_out, out, rows->q, extent(rows->q_tok, rows->q_seq, rows->H)))
+      return report(TB_ERR_INVALID_ARG, "q_out overlaps q, and is not a dense q itself");
+    if (overlap(rows->q_out, out, rows->k, extent(rows->k_tok, rows->k_seq, kv->Hkv)) ||
+        overlap(rows->q_out, out, rows->v, extent(rows->v_tok, rows->v_seq, kv->Hkv)))
+      return report(TB_ERR_INVALID_ARG, "q_out overlaps k or v");
+  }
   int* err = device_error_word();
   if (!err) return report(TB_ERR_CUDA, "cannot resolve the device error word");
   AppendArgs a;
@@ -190,6 +207,8 @@ tb_status tb_kvcache_attn(const tb_attn_cfg* cfg, const void* q, const tb_kvcach
   if (!q || !o) return report(TB_ERR_INVALID_ARG, "q and o must be non-NULL");
   if (!aligned16(q) || !aligned16(o) || !aligned4(n_new))
     return report(TB_ERR_INVALID_ARG, "q and o must be 16-byte aligned, n_new 4-byte");
+  const size_t rows = (size_t)kv->B * n * cfg->H * cfg->dh * (cfg->dtype == TB_F32 ? 4 : 2);
+  if (overlap(q, rows, o, rows)) return report(TB_ERR_INVALID_ARG, "o may not overlap q");
   AttnArgs a = attn_args(cfg, kv, n, nullptr);
   a.q = q;
   a.o = o;

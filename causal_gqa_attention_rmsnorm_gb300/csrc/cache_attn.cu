@@ -246,9 +246,21 @@ cudaError_t run_f32(const AttnArgs& a, void* ws, cudaStream_t s) {
   return e;
 }
 
-// Few rows per KV head stream the cache through warp-level MMAs; more take the
-// tensor-core kernel.
-bool few(const AttnArgs& a) { return a.n * (a.H / a.c.Hkv) <= kFewRows; }
+// Few rows per KV head stream the cache through warp-level MMAs, more take the
+// tensor-core kernel.  Up to 16 rows one warp holds them all: 42 against 60 us
+// (4 sequences of 16k, 8 KV heads of 128, bf16).  From 17 to 32 two warps work on
+// every stage: over e4m3, where the other kernel has V to convert, still faster
+// (59 against 64, and 105 against 110 with 32 sequences of 4k); in bf16 only where
+// there is little to read, as the other one takes three launches (32 against 37 us
+// with 8 sequences and a window of 2048, 70 against 60 with 4 of 16k).
+bool few(const AttnArgs& a) {
+  const int R = a.n * (a.H / a.c.Hkv);
+  if (R <= 16) return true;
+  if (R > kFewRows) return false;
+  if (a.c.dtype == TB_E4M3) return true;
+  const long long keys = a.window > 0 ? std::min<long long>(a.c.T, (long long)a.window + a.sinks + a.n) : a.c.T;
+  return keys * a.c.B * a.c.Hkv <= 1 << 18;
+}
 
 }  // namespace
 

@@ -15,8 +15,8 @@
 //   workspace, and k_few_merge joins a pair's pieces in order.  Walking the
 //   line, each new piece enters the next pair, the next team or both, so
 //   team + pair numbers it without a table.
-//   A team is one warp for up to 16 rows, two or four for 32 or 64, sixteen
-//   rows each over the same stages.  Lane 0 of its first warp issues the
+//   A team is one warp for up to 16 rows, two for 32, sixteen rows each over the
+//   same stages.  Lane 0 of its first warp issues the
 //   copies; page ids and block scales are fetched 32 runs at a time by the
 //   warp, so no copy waits for a table look-up.
 //
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
 }
 
 constexpr size_t kPreBytes = (kMaxB + 1) * 4 / 256 * 256 + 256;
-int team_warps(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
+int team_warps(int R) { return R <= 16 ? 1 : 2; }
 
 template <int DH, bool E4, int TW, bool LO>
 cudaError_t run(const AttnArgs& a, void* ws, int Bl, cudaStream_t s) {
@@ -728,8 +728,7 @@ cudaError_t by_rows(const AttnArgs& a, void* part, int Bl, cudaStream_t s) {
   const int R = a.n * (a.H / a.c.Hkv);
   if (R <= 8) return run<DH, E4, 1, true>(a, part, Bl, s);
   if (R <= 16) return run<DH, E4, 1, false>(a, part, Bl, s);
-  if (R <= 32) return run<DH, E4, 2, false>(a, part, Bl, s);
-  if (R <= kFewRows) return run<DH, E4, 4, false>(a, part, Bl, s);
+  if (R <= kFewRows) return run<DH, E4, 2, false>(a, part, Bl, s);
   return cudaErrorInvalidValue;
 }
 

@@ -10,7 +10,8 @@
 //     by one thread per row, P back over S in 16 bits, O_g += P_g·V.
 //   Roles: warps 0..7 softmax (four per slot), warp 8 copies and hands the pieces
 //   of work to the others, warp 9 issues the MMAs, warp 10 (over e4m3 and 11) sees
-//   to V tiles that cannot be used as they land.  The MMA order
+//   to V tiles that cannot be used as they land.  Where there is but one row tile,
+//   both slots work on it, each on every second key tile, and slot 0 joins the two.  The MMA order
 //   per key tile is P·V of slot 0, S of slot 0 for the next tile, the same of
 //   slot 1, so that the tensor pipe works on one slot during the other's
 //   softmax.
@@ -73,9 +74,15 @@ template <int DH, bool E4> struct ManyCfg {
   static constexpr uint32_t OFF_SC = OFF_RAW + (E4 ? kRaw * RAW : 0);      // [kScTiles][8 runs]{K scale, log2 of V's}
   static constexpr uint32_t OFF_BAR = OFF_SC + (E4 ? kScTiles * 64 : 0);
   static constexpr uint32_t OFF_DESC = OFF_BAR + 512;
-  static constexpr size_t SMEM = OFF_DESC + 512 + 1024;
+  static constexpr uint32_t OFF_JOIN = OFF_DESC + 1024;    // [128] {max, sum} of slot 1, then slot 0's query factors
+  static constexpr size_t SMEM = OFF_JOIN + 1536 + 1024;
   static constexpr uint32_t TMEM_O = 2 * kBN;
   static constexpr int THREADS = E4 ? 384 : 352;
+};
+
+struct MergeRec {
+  int b, h, p, valid;
+  long long start;         // its place on the line
 };
 
 struct ManyArgs {
@@ -87,6 +94,7 @@ struct ManyArgs {
   int vbox;                // keys per box of V codes
   bool negate;             // the score scale is negative: the scores are negated, its magnitude applied
   long long* pre;          // [B·pairs + 1] line position of (sequence, pair) within its KV head
+  MergeRec* rec;    // [n_cta] the item that cut c + 1 goes through first
   int* any;                // whether any flag is set
   uint8_t* flags;          // [B·Hkv·2·pairs] row tiles to look through again
   float4* part;            // [2·n_cta][2][DH/4 + 1][128] pieces
@@ -257,7 +265,17 @@ struct Pieces {
 struct PieceDesc {
   int t0, t1, where, last, b, h, p;
   int ns, wl, end, hid0, hid1;
+  // One row tile only: slot 0 takes the key tiles t0, t0 + 2, ..., slot 1 the
+  // others (all of the list's are its), and slot 0 joins the two.
+  int split;
   SlotRange s[2];
+  __device__ __forceinline__ bool on(int g, int x) const { return split ? ((x - t0) & 1) == g : s[g].on(x); }
+  __device__ __forceinline__ int first_on(int g) const {
+    return split ? (t0 + g < t1 ? t0 + g : -1) : s[g].first_on(t0, t1);
+  }
+  __device__ __forceinline__ int last_on(int g) const {
+    return split ? (t0 + g < t1 ? t1 - 1 - ((t1 - 1 - t0 - g) & 1) : -1) : s[g].last_on(t0, t1);
+  }
   __device__ __forceinline__ int key(int x) const { return (x < ns ? x : x - ns + wl) * kBN; }
   // whether the tile at `key` holds rows that no row of the item sees
   __device__ __forceinline__ bool border(int key) const {
@@ -370,9 +388,13 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
   uint64_t* d_full = bars + 44;      // [kDescs]
   uint64_t* d_empty = bars + 48;     // [kDescs]
   uint64_t* fix_full = bars + 52;    // [2]: a border V tile has landed, its hidden rows not yet zeroed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 54);
+  uint64_t* join_full = bars + 54;   // a split piece: slot 1 is through; slot 0 has read its output
+  uint64_t* join_done = bars + 55;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 56);
+  float2* ml_s = reinterpret_cast<float2*>(smem + C::OFF_JOIN);
+  float* zs_s = reinterpret_cast<float*>(smem + C::OFF_JOIN + 1024);
   PieceDesc* descs = reinterpret_cast<PieceDesc*>(smem + C::OFF_DESC);
-  static_assert(sizeof(PieceDesc) * kDescs <= 512 && 54 * 8 + 8 <= 512, "layout");
+  static_assert(sizeof(PieceDesc) * kDescs <= 1024 && 56 * 8 + 8 <= 512, "layout");
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* sc = reinterpret_cast<float*>(smem + C::OFF_SC);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -382,6 +404,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
     mbar_init(q_empty, 1);
     mbar_init(q_ready, 8);
     mbar_init(drain, 1);
+    mbar_init(join_full, 4);
+    mbar_init(join_done, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
@@ -452,8 +476,9 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         d.end = pc.it.end;
         d.hid0 = pc.it.hid0;
         d.hid1 = pc.it.hid1;
+        d.split = pc.it.s1.rows == 0;
         d.s[0] = pc.it.s0;
-        d.s[1] = pc.it.s1;
+        d.s[1] = d.split ? pc.it.s0 : pc.it.s1;
         mbar_arrive(&d_full[k % kDescs]);
       }
       __syncwarp();
@@ -610,6 +635,13 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
       }
       if (!ok) break;
     }
+    // an item that begins here and goes on in the next CTA's part, for the merge
+    if (lane == 0) {
+      MergeRec rec{0, 0, 0, 0, 0};
+      if (ok && pc.any && pc.at.start >= x0 && pc.at.start + pc.it.cnt + 1 > x1)
+        rec = MergeRec{pc.at.b, pc.at.h, pc.at.p, 1, pc.at.start};
+      m.rec[blockIdx.x] = rec;
+    }
     // every copy issued must land before the CTA may exit
     __syncwarp();
     if (lane == 0) {
@@ -643,8 +675,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
       const uint64_t dk0 = kmajor(sK), dk1 = kmajor(sK + C::K_BYTES);
       const uint64_t dv0 = desc_mnmajor_sw128(sV, kBN * 128, 1024);
       const uint64_t dv1 = desc_mnmajor_sw128(sV + C::V_BYTES, kBN * 128, 1024);
-      auto issue_s = [&](int g, int t) {
-        const uint64_t qd = g ? dq1 : dq0, kd = (t & 1) ? dk1 : dk0;
+      auto issue_s = [&](int g, int t, uint64_t qd) {
+        const uint64_t kd = (t & 1) ? dk1 : dk0;
         if constexpr (E4) {
           // both terms of the queries, 32 dims (two 16-byte units) per MMA
 #pragma unroll
@@ -669,23 +701,22 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         mbar_arrive(&d_empty[k % kDescs]);
         if (pc.last) break;
         if (pc.t0 == pc.t1) continue;
-        const SlotRange &s0 = pc.s[0], &s1 = pc.s[1];
         const int nt = pc.t1 - pc.t0;
-        const int f0 = s0.first_on(pc.t0, pc.t1), l0 = s0.last_on(pc.t0, pc.t1);
-        const int f1 = s1.first_on(pc.t0, pc.t1), l1 = s1.last_on(pc.t0, pc.t1);
-        bool on0 = s0.on(pc.t0), on1 = s1.on(pc.t0);
+        const int f0 = pc.first_on(0), l0 = pc.last_on(0), f1 = pc.first_on(1), l1 = pc.last_on(1);
+        bool on0 = pc.on(0, pc.t0), on1 = pc.on(1, pc.t0);
+        const uint64_t dqs = pc.split ? dq0 : dq1;        // slot 1's queries
         if (!wait_one(E4 ? q_ready : q_full, nq & 1, abort_flag, err) ||
             !wait_one(&k_full[kc & 1], (kc >> 1) & 1, abort_flag, err))
           break;
         ++nq;
         tc_fence_after();
-        if (on0) issue_s(0, kc);
-        if (on1) issue_s(1, kc);
+        if (on0) issue_s(0, kc, dq0);
+        if (on1) issue_s(1, kc, dqs);
         mma_commit(&k_empty[kc & 1]);
         if (nt == 1) mma_commit(q_empty);
         for (int jj = 0; jj < nt; ++jj) {
           const int t = kc + jj, x = pc.t0 + jj;
-          const bool next = jj + 1 < nt, on0n = next && s0.on(x + 1), on1n = next && s1.on(x + 1);
+          const bool next = jj + 1 < nt, on0n = next && pc.on(0, x + 1), on1n = next && pc.on(1, x + 1);
           if (!wait_one(&v_full[t & 1], (t >> 1) & 1, abort_flag, err)) {
             ok = false;
             break;
@@ -706,7 +737,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
               break;
             }
             tc_fence_after();
-            if (on0n) issue_s(0, t + 1);
+            if (on0n) issue_s(0, t + 1, dq0);
           }
           if (on1) {
             if (!wait_one(&p_full[1], c1 & 1, abort_flag, err)) {
@@ -719,7 +750,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
             if (x == l1) mma_commit(&o_full[1]);
           }
           if (next) {
-            if (on1n) issue_s(1, t + 1);
+            if (on1n) issue_s(1, t + 1, dqs);
             mma_commit(&k_empty[(t + 1) & 1]);
             if (jj + 2 == nt) mma_commit(q_empty);
           }
@@ -840,14 +871,15 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
     auto soft_wait = [](uint64_t* bar, uint32_t parity, volatile int* abort, int* e) {
       return E4 ? wait_warp(bar, parity, abort, e) : mbar_wait_warp(bar, parity, abort, e);
     };
-    int c = 0, nt = 0, nq = 0, no = 0;          // this slot's tiles; key tiles, pieces with keys, outputs
+    int c = 0, nt = 0, nq = 0, no = 0, nj = 0;  // this slot's tiles; key tiles, pieces with keys, outputs, joins
     bool ok = true;
     PieceDesc* d;
     for (int pk = 0; ok && piece(pk, d); ++pk) {
       const SlotRange& s_r = d->s[g];
       const int t0 = d->t0, t1 = d->t1;
       const int qp = r < s_r.rows ? s_r.p0 + r / G : -1;
-      const int f_on = s_r.first_on(t0, t1), l_on = s_r.last_on(t0, t1);
+      const int f_on = d->first_on(g), l_on = d->last_on(g);
+      const bool split = d->split;
       float zs = fabsf(a.scale_log2);
       if constexpr (E4) {
         // this row of Q as two e4m3 terms, its largest element in [128, 256)
@@ -856,7 +888,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
             ok = false;
             break;
           }
-          if (s_r.rows) {
+          if (s_r.rows && !(split && g)) {
             const uint32_t qrow = smem_u32(smem) + g * C::Q_BYTES + r * 128;
             uint4 w[C::NB * 8];
             float amax = 0.f;
@@ -884,6 +916,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
               sts128(t1 + at, a1);
               sts128(t2 + at, a2);
             }
+            if (split) zs_s[r] = zs;            // slot 1 works on the same rows
           }
           fence_proxy_async();
           __syncwarp();
@@ -894,8 +927,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
       float m_used = -INFINITY, l = 0.f;
       const int wlo = win_lo(qp, a.window), p0m = s_r.p0 - (kBN - 1), w1 = win_lo(s_r.p1, a.window);
       const int ns = d->ns, shift = d->wl - ns, ia = s_r.ia, ib = s_r.ib, tn0 = nt - t0;
-      // the slot's tiles: every list position but those in [ia, ib)
-      for (int x = f_on; x >= 0 && x <= l_on; x = x + 1 >= ia && x + 1 < ib ? ib : x + 1) {
+      // the slot's tiles: every list position but those in [ia, ib), or every second
+      for (int x = f_on; x >= 0 && x <= l_on; x = split ? x + 2 : x + 1 >= ia && x + 1 < ib ? ib : x + 1) {
         const int tn = tn0 + x;                 // the CTA's running key tile
         if constexpr (E4) {
           if (!soft_wait(&sc_full[tn % kScTiles], (tn / kScTiles) & 1, abort_flag, err)) {
@@ -908,6 +941,9 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
           break;
         }
         tc_fence_after();
+        if constexpr (E4) {
+          if (split && g && x == f_on) zs = zs_s[r];
+        }
         const int key = (x < ns ? x : x + shift) * kBN;
         const bool ahead = key > p0m, behind = key < w1 && key + kBN > a.sinks;
         // m_used (and with it l and O) follows the row's new maximum when that grew
@@ -1091,7 +1127,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
       done(pk);
       if (rows == 0) continue;
       const bool valid = r < rows;
-      if (f_on < 0) {                           // no tile of this piece
+      if (f_on < 0 && !(split && t0 < t1)) {    // no tile of this piece
+        if (split && g) continue;               // (slot 0 writes the zeros)
         if (where >= 0) {
           m.part[((size_t)(where * 2 + g) * (DH / 4 + 1)) * kBM + r] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
         } else if (valid) {
@@ -1101,52 +1138,91 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         }
         continue;
       }
-      if (!soft_wait(&o_full[g], no & 1, abort_flag, err)) {
-        ok = false;
-        break;
+      if (f_on >= 0) {
+        if (!soft_wait(&o_full[g], no & 1, abort_flag, err)) {
+          ok = false;
+          break;
+        }
+        ++no;
+        tc_fence_after();
       }
-      ++no;
-      tc_fence_after();
-      if (where >= 0) {
-        float4* dst = m.part + ((size_t)(where * 2 + g) * (DH / 4 + 1)) * kBM + r;
-        dst[0] = make_float4(m_used, l, 0.f, 0.f);
-#pragma unroll 2
-        for (int cc = 0; cc < DH; cc += 16) {
-          uint32_t u[16];
-          tmem_ld16(o_col + cc, u);
+      float a0 = 1.f, a1 = 0.f;                 // factors of the slots' outputs
+      if (split) {
+        if (g) {
+          // hand (max, sum) over, and keep the output until it has been read
+          ml_s[r] = make_float2(m_used, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(join_full);
+          if (!soft_wait(join_done, nj & 1, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          ++nj;
+          continue;
+        }
+        if (!soft_wait(join_full, nj & 1, abort_flag, err)) {
+          ok = false;
+          break;
+        }
+        ++nj;
+        tc_fence_after();
+        const float2 ml = ml_s[r];
+        const float mj = fmaxf(m_used, ml.x), base = mj == -INFINITY ? 0.f : mj;
+        a0 = ex2_approx(m_used - base);
+        a1 = ex2_approx(ml.x - base);           // 0 where slot 1 saw no key: its columns are not looked at
+        l = l * a0 + ml.y * a1;
+        m_used = mj;
+      }
+      const float inv = where >= 0 ? 1.f : l == 0.f ? 0.f : 1.0f / l;
+      float4* piece_out = m.part + ((size_t)(max(where, 0) * 2 + g) * (DH / 4 + 1)) * kBM + r;
+      bf16* dst = (bf16*)a.o + orow * DH;
+      float probe = 0.f;                        // stays 0 while every output is finite
+      if (where >= 0) piece_out[0] = make_float4(m_used, l, 0.f, 0.f);
+#pragma unroll 1
+      for (int cc = 0; cc < DH; cc += 16) {
+        uint32_t u[16];
+        tmem_ld16(o_col + cc, u);
+        if (split) {
+          uint32_t u1[16];
+          tmem_ld16(o_col + DH + cc, u1);
           tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            asm volatile("" : "+r"(u[i]), "+r"(u1[i]));
+            const float v = __uint_as_float(u[i]) * a0;
+            u[i] = __float_as_uint(a1 > 0.f ? fmaf(__uint_as_float(u1[i]), a1, v) : v);
+          }
+        } else {
+          tmem_wait_ld();
+        }
+        if (where >= 0) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            dst[(size_t)(1 + cc / 4 + i) * kBM] =
+            piece_out[(size_t)(1 + cc / 4 + i) * kBM] =
                 make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]), __uint_as_float(u[4 * i + 2]),
                             __uint_as_float(u[4 * i + 3]));
+          continue;
         }
-      } else {
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
-        bf16* dst = (bf16*)a.o + orow * DH;
-        float probe = 0.f;                      // stays 0 while every output is finite
-#pragma unroll 2
-        for (int cc = 0; cc < DH; cc += 16) {
-          uint32_t u[16];
-          tmem_ld16(o_col + cc, u);
-          tmem_wait_ld();
-          uint4 wv[2];
-          uint32_t* wp = &wv[0].x;
+        uint4 wv[2];
+        uint32_t* wp = &wv[0].x;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float v0 = __uint_as_float(u[2 * i]) * inv, v1 = __uint_as_float(u[2 * i + 1]) * inv;
-            probe = fmaf(v0, 0.f, fmaf(v1, 0.f, probe));
-            wp[i] = pack16<false>(v0, v1);
-          }
-          if (valid) {
-            *reinterpret_cast<uint4*>(dst + cc) = wv[0];
-            *reinterpret_cast<uint4*>(dst + cc + 8) = wv[1];
-          }
+        for (int i = 0; i < 8; ++i) {
+          const float v0 = __uint_as_float(u[2 * i]) * inv, v1 = __uint_as_float(u[2 * i + 1]) * inv;
+          probe = fmaf(v0, 0.f, fmaf(v1, 0.f, probe));
+          wp[i] = pack16<false>(v0, v1);
         }
-        if (valid && !(probe == 0.f))
-          *m.any = m.flags[flag] = 1;
+        if (valid) {
+          *reinterpret_cast<uint4*>(dst + cc) = wv[0];
+          *reinterpret_cast<uint4*>(dst + cc + 8) = wv[1];
+        }
       }
+      if (where < 0 && valid && !(probe == 0.f)) *m.any = m.flags[flag] = 1;
       tc_fence_before();
+      if (split) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(join_done);
+      }
     }
   }
 
@@ -1158,8 +1234,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
   }
 }
 
-// Joins the pieces of the items that cuts went through, 128 threads per row
-// tile (CTA c: the item that cut c goes through first), then computes again,
+// Joins the pieces of the items that cuts went through: CTA (c, slot, columns) the
+// item that begins in part c and goes on, one thread per row; then computes again,
 // one warp per row, every row whose result is not finite.
 template <int DH>
 __global__ void __launch_bounds__(128) k_many_merge(const ManyArgs m) {
@@ -1167,95 +1243,90 @@ __global__ void __launch_bounds__(128) k_many_merge(const ManyArgs m) {
   pdl_wait();
   const AttnArgs& a = m.a;
   const int G = kBM / m.tpt, r = threadIdx.x, lane = r & 31, warp = r >> 5;
-  const long long total = m.pre[(size_t)a.c.B * m.pairs] * a.c.Hkv;
-  const int c = blockIdx.x + 1, g = blockIdx.y;
-  const long long xc = cut(m, total, c), xb = cut(m, total, c - 1);
-  auto again = [&](int b, int h, int row, const SlotRange& s, const SeqRange& sr) {
-    // row `row` of the slot's tile, by this warp
+  const int g = blockIdx.y, col = blockIdx.z * 32;
+  // row `row` of the slot's tile, by this warp; columns [c0, c1) of it are written
+  auto again = [&](int b, int h, int row, const SlotRange& s, const SeqRange& sr, int c0, int c1) {
     const int tok = s.tok0 + row / G;
     const size_t at = ((size_t)b * a.n + tok) * a.H + h * G + row % G;
     float out[DH / 32];
     attend_row<DH>(a, b, h, sr.first + tok, (const bf16*)a.q + at * DH, out);
-    __syncwarp();
 #pragma unroll
-    for (int u = 0; u < DH / 32; ++u) ((bf16*)a.o)[at * DH + lane * (DH / 32) + u] = from_f<bf16>(out[u]);
+    for (int u = 0; u < DH / 32; ++u) {
+      const int e = lane * (DH / 32) + u;
+      if (e >= c0 && e < c1) ((bf16*)a.o)[at * DH + e] = from_f<bf16>(out[u]);
+    }
     __syncwarp();
   };
-  if (c < m.n_cta && xc < total && xc > xb) {
-    const Place at = find_item(m, xc);
-    if (at.start < xc && at.start >= xb) {          // the first cut through this item
-      const SeqRange sr = seq_range(a, at.b);
-      const Item it = make_item(m, sr, at.p);
-      const SlotRange s = g ? it.s1 : it.s0;
-      const long long end = at.start + it.cnt + 1;
-      // the pieces: those of CTAs c - 1, c, ... that hold key tiles
-      int k1 = c - 1, np = 0;
-      for (; k1 < m.n_cta && cut(m, total, k1) < end; ++k1) {
-        const int2 t = piece_of(at.start, it.cnt, max(cut(m, total, k1), at.start), cut(m, total, k1 + 1));
-        if (t.x < t.y) ++np;
-        if (t.x == 0 && t.y == it.cnt) np = 1 << 20;  // one CTA holds all key tiles: written out
+  __shared__ int list[kBM * 4];                     // workspace slots of the item's pieces, -1: none
+  __shared__ int n_list, is_whole;
+  const MergeRec rec = m.rec[blockIdx.x];
+  if (rec.valid) {
+    const long long total = m.pre[(size_t)a.c.B * m.pairs] * a.c.Hkv;
+    const SeqRange sr = seq_range(a, rec.b);
+    const Item it = make_item(m, sr, rec.p);
+    const SlotRange s = g ? it.s1 : it.s0;
+    const long long end = rec.start + it.cnt + 1;
+    if (r == 0) n_list = is_whole = 0;
+    __syncthreads();
+    for (int k = blockIdx.x + r; k < m.n_cta; k += kBM) {
+      const long long xk = cut(m, total, k);
+      if (xk >= end) break;
+      const int2 t = piece_of(rec.start, it.cnt, max(xk, rec.start), cut(m, total, k + 1));
+      list[k - blockIdx.x] = t.x < t.y ? 2 * k + (xk <= rec.start ? 1 : 0) : -1;
+      atomicMax(&n_list, k - (int)blockIdx.x + 1);
+      if (t.x == 0 && t.y == it.cnt) is_whole = 1;  // one CTA holds all key tiles: written out
+    }
+    __syncthreads();
+    if (s.rows && !is_whole) {
+      auto at = [&](int w) { return m.part + ((size_t)(w * 2 + g) * (DH / 4 + 1)) * kBM + r; };
+      float M = -INFINITY;
+#pragma unroll 4
+      for (int i = 0; i < n_list; ++i)
+        if (list[i] >= 0) M = fmaxf(M, at(list[i])[0].x);
+      const float base = M == -INFINITY ? 0.f : M;
+      float l = 0.f;
+      float4 acc[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int i = 0; i < n_list; ++i) {
+        if (list[i] < 0) continue;
+        const float4* p = at(list[i]);
+        const float4 ml = p[0];
+        if (ml.x == -INFINITY) continue;            // no visible key in this piece: its O may be unset
+        const float wgt = ex2_approx(ml.x - base);
+        l = fmaf(ml.y, wgt, l);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float4 v = p[(size_t)(1 + col / 4 + u) * kBM];
+          acc[u].x = fmaf(v.x, wgt, acc[u].x);
+          acc[u].y = fmaf(v.y, wgt, acc[u].y);
+          acc[u].z = fmaf(v.z, wgt, acc[u].z);
+          acc[u].w = fmaf(v.w, wgt, acc[u].w);
+        }
       }
-      if (s.rows && np < (1 << 20) && np > 0) {
-        auto slot_of = [&](int k, int& w) {
-          const long long xk = cut(m, total, k);
-          const int2 t = piece_of(at.start, it.cnt, max(xk, at.start), cut(m, total, k + 1));
-          w = 2 * k + (xk <= at.start ? 1 : 0);
-          return t.x < t.y;
-        };
-        float M = -INFINITY;
-        for (int k = c - 1; k < k1; ++k) {
-          int w;
-          if (!slot_of(k, w)) continue;
-          M = fmaxf(M, m.part[((size_t)(w * 2 + g) * (DH / 4 + 1)) * kBM + r].x);
-        }
-        const float base = M == -INFINITY ? 0.f : M;
-        float l = 0.f;
-        for (int k = c - 1; k < k1; ++k) {
-          int w;
-          if (!slot_of(k, w)) continue;
-          const float4 ml = m.part[((size_t)(w * 2 + g) * (DH / 4 + 1)) * kBM + r];
-          l = fmaf(ml.y, exp2f(ml.x - base), l);
-        }
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
-        const bool valid = r < s.rows;
-        const int tok = s.tok0 + r / G;
-        bf16* dst = (bf16*)a.o + (((size_t)at.b * a.n + tok) * a.H + at.h * G + r % G) * DH;
-        float probe = 0.f;
-        for (int q = 0; q < DH / 4; q += 2) {
-          float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-          for (int k = c - 1; k < k1; ++k) {
-            int w;
-            if (!slot_of(k, w)) continue;
-            const float4* p = m.part + ((size_t)(w * 2 + g) * (DH / 4 + 1)) * kBM + r;
-            const float mw = p[0].x;
-            if (mw == -INFINITY) continue;          // no visible key in this piece: its O may be unset
-            const float wgt = exp2f(mw - base);
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
+      const bool valid = r < s.rows;
+      bf16* dst = (bf16*)a.o + (((size_t)rec.b * a.n + s.tok0 + r / G) * a.H + rec.h * G + r % G) * DH + col;
+      float probe = 0.f;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const float4 v = p[(size_t)(1 + q + u) * kBM];
-              acc[u].x = fmaf(v.x, wgt, acc[u].x);
-              acc[u].y = fmaf(v.y, wgt, acc[u].y);
-              acc[u].z = fmaf(v.z, wgt, acc[u].z);
-              acc[u].w = fmaf(v.w, wgt, acc[u].w);
-            }
-          }
-          uint4 wv;
-          uint32_t* wp = &wv.x;
+      for (int u = 0; u < 8; u += 2) {
+        uint4 wv;
+        uint32_t* wp = &wv.x;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float v0 = acc[u].x * inv, v1 = acc[u].y * inv, v2 = acc[u].z * inv, v3 = acc[u].w * inv;
-            probe = fmaf(v0, 0.f, fmaf(v1, 0.f, fmaf(v2, 0.f, fmaf(v3, 0.f, probe))));
-            wp[2 * u] = pack16<false>(v0, v1);
-            wp[2 * u + 1] = pack16<false>(v2, v3);
-          }
-          if (valid) *reinterpret_cast<uint4*>(dst + 4 * q) = wv;
+        for (int j = 0; j < 2; ++j) {
+          const float v0 = acc[u + j].x * inv, v1 = acc[u + j].y * inv, v2 = acc[u + j].z * inv, v3 = acc[u + j].w * inv;
+          probe = fmaf(v0, 0.f, fmaf(v1, 0.f, fmaf(v2, 0.f, fmaf(v3, 0.f, probe))));
+          wp[2 * j] = pack16<false>(v0, v1);
+          wp[2 * j + 1] = pack16<false>(v2, v3);
         }
-        uint32_t bad = __ballot_sync(0xffffffffu, valid && !(probe == 0.f));
-        while (bad) {
-          const int who = __ffs(bad) - 1;
-          bad &= bad - 1;
-          again(at.b, at.h, warp * 32 + who, s, sr);
-        }
+        if (valid) *reinterpret_cast<uint4*>(dst + 4 * u) = wv;
+      }
+      uint32_t bad = __ballot_sync(0xffffffffu, valid && !(probe == 0.f));
+      while (bad) {
+        const int who = __ffs(bad) - 1;
+        bad &= bad - 1;
+        again(rec.b, rec.h, warp * 32 + who, s, sr, col, col + 32);
       }
     }
   }
@@ -1263,7 +1334,8 @@ __global__ void __launch_bounds__(128) k_many_merge(const ManyArgs m) {
   // their rows dealt to all warps of the grid.
   if (!*m.any) return;
   const int tiles = a.c.B * a.c.Hkv * 2 * m.pairs;
-  const int warps = (int)(gridDim.x * gridDim.y) * 4, me = (int)(blockIdx.y * gridDim.x + blockIdx.x) * 4 + warp;
+  const int warps = (int)(gridDim.x * gridDim.y * gridDim.z) * 4;
+  const int me = (int)((blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * 4 + warp;
   for (int i0 = 0; i0 < tiles; i0 += 128) {
     const int i = i0 + lane * 4;          // 4 flags per lane
     const uint32_t fl = i < tiles ? reinterpret_cast<const uint32_t*>(m.flags)[i >> 2] : 0u;
@@ -1282,7 +1354,7 @@ __global__ void __launch_bounds__(128) k_many_merge(const ManyArgs m) {
           const size_t at = ((size_t)b * a.n + s.tok0 + row / G) * a.H + hk * G + row % G;
           float probe = 0.f;
           for (int e = lane; e < DH; e += 32) probe = fmaf(to_f(((const bf16*)a.o)[at * DH + e]), 0.f, probe);
-          if (__any_sync(0xffffffffu, !(probe == 0.f))) again(b, hk, row, s, sr);
+          if (__any_sync(0xffffffffu, !(probe == 0.f))) again(b, hk, row, s, sr, 0, DH);
         }
       }
     }
@@ -1290,7 +1362,7 @@ __global__ void __launch_bounds__(128) k_many_merge(const ManyArgs m) {
 }
 
 struct ManyLayout {
-  size_t pre, flags, part, total;
+  size_t pre, rec, flags, part, total;
   int pairs, flag_words;
 };
 ManyLayout layout_of(const AttnArgs& a) {
@@ -1301,7 +1373,8 @@ ManyLayout layout_of(const AttnArgs& a) {
   const size_t flags = (size_t)a.c.B * a.c.Hkv * 2 * L.pairs;
   L.flag_words = (int)((flags + 3) / 4);
   L.pre = 0;
-  L.flags = up(((size_t)a.c.B * L.pairs + 1) * 8) + 256;      // `any` in the 256 bytes before them
+  L.rec = up(((size_t)a.c.B * L.pairs + 1) * 8);
+  L.flags = L.rec + up((size_t)sm_count() * sizeof(MergeRec)) + 256;      // `any` in the 256 bytes before them
   L.part = L.flags + up((size_t)L.flag_words * 4);
   L.total = L.part + (size_t)2 * sm_count() * 2 * (a.c.dh / 4 + 1) * kBM * 16;
   return L;
@@ -1323,6 +1396,7 @@ cudaError_t run(const AttnArgs& a, void* ws, cudaStream_t s) {
   m.n_cta = sm_count();
   m.negate = a.scale_log2 < 0.f;
   m.pre = (long long*)ws;
+  m.rec = (MergeRec*)((uint8_t*)ws + L.rec);
   m.flags = (uint8_t*)ws + L.flags;
   m.any = (int*)(m.flags - 256);
   m.part = (float4*)((uint8_t*)ws + L.part);
@@ -1357,7 +1431,7 @@ cudaError_t run(const AttnArgs& a, void* ws, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(k_attn_many<DH, E4>, dim3(m.n_cta), dim3(C::THREADS), C::SMEM, s, tq, tk, tv, m);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_many_merge<DH>, dim3(std::max(m.n_cta - 1, 1), 2), dim3(128), 0, s, m);
+  return launch_pdl(k_many_merge<DH>, dim3(m.n_cta, 2, DH / 32), dim3(kBM), 0, s, m);
 }
 
 }  // namespace

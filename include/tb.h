@@ -327,11 +327,13 @@ TB_API tb_status tb_rope_table(int32_t dh, int32_t max_pos, float base, float* t
  * dense, tokens are *_tok elements apart and sequences *_seq elements, so the
  * three may be column blocks of one fused projection.  Pointers 16-byte
  * aligned, strides multiples of 8 elements.
- *  q     : H heads, or NULL; q_out (dense [B, n, H, dh], may be q itself where
- *          q is dense) receives them rotated.
+ *  q     : H heads, or NULL; q_out (dense [B, n, H, dh]) receives them rotated.
+ *          It may be q itself where q is dense, and overlaps none of the rows
+ *          otherwise.
  *  start : device int32 [B], the position of each sequence's first new row, or
  *          NULL for lens.  A start below lens drops the rows from it on (taking
- *          drafted tokens back); start may not overlap lens.
+ *          drafted tokens back); one above lens leaves the rows between as they
+ *          are.  Neither start nor n_new may overlap lens.
  *  n_new : device int32 [B], how many of the n rows of each sequence count (the
  *          others are padding: not stored, their q_out rows left as they were),
  *          or NULL for all n.  Values are held to [0, n]. */
@@ -378,7 +380,8 @@ TB_API size_t tb_kvcache_attn_workspace_bytes(const tb_attn_cfg* cfg, const tb_k
 /* o[b, i, h] = sum_j softmax_j(scale q·k_j) v_j over the keys the query sees,
  * for the last tokens of each sequence: query i of sequence b sits at position
  * lens[b] - n_new[b] + i (the tokens just appended).
- *  q, o  : device, dense [B, n, H, dh] of cfg->dtype; q rotated; o may be q.
+ *  q, o  : device, dense [B, n, H, dh] of cfg->dtype; q rotated; they may not
+ *          overlap.
  *  n_new : as in tb_append_rows; o rows of padding are left as they were.
  *  ws    : 256-byte aligned workspace; calls that may overlap need their own.
  * A query that sees no key (a negative position) gets zeros.  Rows no query of

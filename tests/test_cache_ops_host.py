@@ -31,7 +31,7 @@ def e4m3(**k):
 
 
 def append(lib, kv, rope=FAKE, max_pos=256, **k):
-    d = dict(q=FAKE, k=FAKE, v=FAKE, q_out=FAKE + 4096, q_tok=256, q_seq=256, k_tok=128, k_seq=128, v_tok=128,
+    d = dict(q=FAKE, k=FAKE + (1 << 20), v=FAKE + (1 << 21), q_out=FAKE + (1 << 22), q_tok=256, q_seq=256, k_tok=128, k_seq=128, v_tok=128,
              v_seq=128, H=4, n=1, start=None, n_new=None)
     d.update(k)
     rows = binding.tb_append_rows(*[d[n] for n, _ in binding.tb_append_rows._fields_])
@@ -71,7 +71,10 @@ def test_append_refusals(lib):
     assert append(lib, cache(), v=FAKE + 2) == 1
     assert append(lib, cache(), k_tok=132) == 1                  # stride not a multiple of 8
     assert append(lib, cache(), v_seq=-128) == 1
-    assert append(lib, cache(), q_out=FAKE, q_tok=512) == 1      # in place, but q not dense
+    assert append(lib, cache(), q_out=FAKE, q_seq=512) == 1      # in place, but q not dense
+    assert append(lib, cache(), q_out=FAKE + 16) == 1            # overlapping q
+    assert append(lib, cache(), q_out=FAKE + (1 << 20) + 16) == 1 and b"overlaps k" in lib.tb_last_error_message()
+    assert append(lib, cache(), n_new=FAKE + 4) == 1             # overlapping lens
     assert append(lib, cache(), start=FAKE) == 1                 # start is lens
     assert append(lib, cache(), start=FAKE + 4) == 1             # and overlapping it
     assert b"overlap" in lib.tb_last_error_message()
@@ -82,7 +85,7 @@ def test_append_refusals(lib):
 
 
 def test_attention_refusals(lib):
-    def call(cfg=None, kv=None, n=1, q=FAKE, o=FAKE, ws=FAKE, wsb=1 << 40, n_new=None):
+    def call(cfg=None, kv=None, n=1, q=FAKE, o=FAKE + (1 << 40), ws=FAKE, wsb=1 << 40, n_new=None):
         d = dict(H=4, Hkv=2, dh=64, dtype=tb.TB_BF16, window=0, sinks=0, scale=0.0)
         d.update(cfg or {})
         c = binding.tb_attn_cfg(*[d[n] for n, _ in binding.tb_attn_cfg._fields_])
@@ -103,6 +106,7 @@ def test_attention_refusals(lib):
     assert call(n=-1) == 1 and call(n=257) == 1
     assert call(q=None) == 1 and call(o=None) == 1 and call(q=FAKE + 8) == 1 and call(n_new=FAKE + 2) == 1
     assert call(dict(H=4, Hkv=2), cache(B=32767, T=1 << 20), n=1 << 20) == 2   # too many rows
+    assert call(o=FAKE) == 1 and call(o=FAKE + 16) == 1 and b"overlap" in lib.tb_last_error_message()
     assert call(n=0) == 0 and call(kv=cache(B=0, k=None, v=None, lens=None)) == 0
 
 

@@ -601,3 +601,77 @@ def test_a_value_row_of_nan_in_every_head(kind, n):
     q = rows(5, 2, n, H, dh, dtype=torch.bfloat16).cuda()
     o = tb.tb_kvcache_attn(tb.AttnConfig(H=H, Hkv=Hkv, dh=dh), q, kv)
     assert torch.isnan(o).all() and tb.tb_get_device_error(clear=True) == 0
+
+
+def test_more_sequences_than_one_launch_takes():
+    """1500 sequences of one token: two launches of the streaming kernel."""
+    tb = tbm()
+    B, Hkv, H, dh, T = 1500, 1, 2, 64, 32
+    kv = tb.KVCache.empty(B, Hkv, T, dh)
+    kv.k.copy_(rows(1, B, Hkv, T, dh))
+    kv.v.copy_(rows(2, B, Hkv, T, dh))
+    kv.lens.copy_(torch.arange(B, dtype=torch.int32) % (T + 1))
+    q = rows(3, B, 1, H, dh, dtype=torch.bfloat16).cuda()
+    o = tb.tb_kvcache_attn(tb.AttnConfig(H=H, Hkv=Hkv, dh=dh), q, kv).double().cpu().numpy()
+    assert tb.tb_get_device_error(clear=True) == 0
+    for b in list(range(0, 40)) + list(range(1000, 1060)) + list(range(1480, 1500)):
+        L = b % (T + 1)
+        out, mag, top = ref.attend(q[b].double().cpu().numpy(), kv.k[b, :, :L].double().cpu().numpy(),
+                                   kv.v[b, :, :L].double().cpu().numpy(), L - 1)
+        check_attention("bf16", o[b], out, mag, top, dh, max(L, 1), f"sequence {b}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dh", [48, 256])
+def test_append_of_other_widths(kind, dh):
+    """Widths that the attention has no kernel for can be appended all the same."""
+    tb = tbm()
+    B, n, H, Hkv, T, bs = 2, 21, 3, 1, 64, 16
+    kv = make_cache(kind, False, B, Hkv, T, dh, bs, fill=0.0)
+    q, k, v = fused_rows(7, B, n, H, Hkv, dh, torch.bfloat16)
+    qr = tb.tb_kvcache_append_rope(kv, k, v, tb.tb_rope_table(dh, T, BASE), q=q, start=i32(0, 40))
+    assert kv.lens.tolist() == [21, 61] and tb.tb_get_device_error(clear=True) == 0
+    for b, t0 in enumerate((0, 40)):
+        want = ref.rotated(q[b].double().cpu().numpy(), t0, BASE)
+        assert np.abs(qr[b].double().cpu().numpy() - want).max() <= 2.0 ** -8 * np.abs(want).max() * 1.01
+        for name, x in (("k", ref.rotated(k[b].double().cpu().numpy(), t0, BASE)), ("v", v[b].double().cpu().numpy())):
+            got = values(kv, name, b)[:, t0:t0 + n]
+            rel = 2.0 ** -4 if kind == "e4m3" else 2.0 ** -8
+            assert (np.abs(got - x.transpose(1, 0, 2)) <= rel * np.abs(x).max()).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,Hkv", [(8, 8), (8, 1), (4, 2)])
+@pytest.mark.parametrize("n", [18, 40, 70, 129])
+def test_one_and_two_row_tiles_over_long_caches(kind, H, Hkv, n):
+    """Few row tiles and many key tiles: the slots share the tile, cuts go through every item."""
+    run_attention(kind, True, (1500, 700), n, H, Hkv, 128, 1536, 64, 0, 0, (n, n - 1), seed=n)
+    run_attention(kind, True, (1500, 131), n, H, Hkv, 64, 1536, 32, 300, 140, seed=n + 1)
+
+
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_small_addends_survive_large_ones(n):
+    """A score whose products cancel but for one 2^-17 of them: sums are fp32."""
+    tb = tbm()
+    dh = 128
+    for kind in ("e4m3", "bf16"):
+        kv = make_cache(kind, False, 1, 1, 320, dh, 16, fill=0.0)
+        if kind == "e4m3":
+            kv.k_scale.fill_(1.0)
+            kv.v_scale.fill_(1.0)
+        k, v = torch.zeros(2, dh), torch.zeros(2, dh)
+        k[:, 0:30:2], k[:, 1:30:2] = 256.0, -256.0
+        k[0, 30] = 2.0 ** -9
+        v[0] = 1
+        for name, x in (("k", k), ("v", v)):
+            buf = getattr(kv, name)
+            if kind == "e4m3":
+                buf.view(torch.uint8)[0, 0, :2] = x.to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+            else:
+                buf[0, 0, :2] = x.to(buf.dtype).cuda()
+        kv.lens.fill_(2)
+        q = torch.ones(1, n, 2, dh, dtype=torch.bfloat16, device="cuda")
+        o = tb.tb_kvcache_attn(tb.AttnConfig(H=2, Hkv=1, dh=dh, scale=2.0 ** 9), q, kv, n_new=i32(1))
+        # weights e / (1 + e) and 1 / (1 + e); one rounding of the weight, one of the output
+        assert abs(float(o[0, 0, 0, 0]) - math.e / (1 + math.e)) <= 2 * 2.0 ** -8, kind
+    assert tb.tb_get_device_error(clear=True) == 0
