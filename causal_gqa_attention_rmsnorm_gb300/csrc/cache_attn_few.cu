@@ -3,22 +3,20 @@
 //
 // Such a call reads every visible K and V row once and does 4·R operations per
 // element, far below what the tensor cores could do in that time, so it is
-// built to stream: teams of warps hold rings of 8 KB stages that TMA fills, and
-// the small products run as warp-level MMAs so that the instruction count per
-// key stays low.
+// built to stream: each warp holds a ring of 8 KB stages that TMA fills, and the
+// small products run as warp-level MMAs so that the instruction count per key
+// stays low.
 //
 //   Work: the visible keys of a (sequence, KV head) are a list of 16-key runs
 //   (sinks, then the window); the stages of all pairs form one line, cut into
-//   equal parts, one per team, so that ragged lengths cost no balance and no
-//   counter or atomic orders anything.  Each part of a pair that a team covers
+//   equal parts, one per warp ("team"), so that ragged lengths cost no balance and
+//   no counter or atomic orders anything.  Each part of a pair that a team covers
 //   is a piece: its softmax state (max, sum, weighted sum of v) goes to the
 //   workspace, and k_few_merge joins a pair's pieces in order.  Walking the
 //   line, each new piece enters the next pair, the next team or both, so
 //   team + pair numbers it without a table.
-//   A team is one warp for up to 16 rows, two for 32, sixteen rows each over the
-//   same stages.  Lane 0 of its first warp issues the
-//   copies; page ids and block scales are fetched 32 runs at a time by the
-//   warp, so no copy waits for a table look-up.
+//   Lane 0 issues the copies; page ids and block scales are fetched 32 runs at a
+//   time by the warp, so no copy waits for a table look-up.
 //
 //   Products (m16n8k16, fp32 sums): S[16 x 16 keys] = Q·Kᵀ, O[16 x dh] += P·V,
 //   P straight from S's accumulators.  bf16: K by ldmatrix, V by
@@ -52,12 +50,14 @@ constexpr uint32_t kStage = 8192;             // K then V bytes of one stage
 constexpr int kMaxB = 1024;                   // sequences per launch
 constexpr float kRescale = 8.f;               // rescale O only when the maximum grows by more than 2^8
 
-// Warps of a CTA and stages per warp, 24 stages in all.  The e4m3 form of up to
-// eight rows spends more instructions per byte and fewer registers: twelve warps
-// hide its latencies better than eight (PLACEHOLDER).
-template <bool E4, bool LO> struct FewShape {
+// Warps of a CTA and stages per warp, by 16-row tiles MT of a warp (LO: half a
+// tile, up to eight rows).  The e4m3 form of up to eight rows spends more
+// instructions per byte and fewer registers: twelve warps hide its latencies
+// better than eight (107 against 125 us for 32 sequences of a 16k cache).  With
+// two tiles the queries lie in shared memory, in the room of the third stage.
+template <bool E4, int MT, bool LO> struct FewShape {
   static constexpr int WARPS = E4 && LO ? 12 : 8;
-  static constexpr int SLOTS = E4 && LO ? 2 : 3;
+  static constexpr int SLOTS = (E4 && LO) || MT == 2 ? 2 : 3;
 };
 constexpr int kStages = 24;
 
@@ -69,8 +69,9 @@ template <int DH, bool E4> struct FewCfg {
   static constexpr uint32_t BOX = kRun * BOXB;
   static constexpr uint32_t RUN = kRun * ROW;                     // bytes of a run (K or V)
   static constexpr uint32_t HALF = kStage / 2;
+  static constexpr uint32_t OFF_Q = 16 * kStage;                  // MT = 2: 8 warps x [2][DH/16][32] fragments
   static constexpr uint32_t OFF_BAR = kStages * kStage;
-  static constexpr uint32_t OFF_SC = OFF_BAR + 2 * kStages * 8;
+  static constexpr uint32_t OFF_SC = OFF_BAR + kStages * 8;
   static constexpr uint32_t OFF_SEQ = OFF_SC + kStages * RUNS * 8;
   static constexpr size_t smem(int B) { return OFF_SEQ + (size_t)B * 12 + 16 + 1024; }
 };
@@ -124,19 +125,22 @@ struct FewArgs {
   int B;                  // sequences of this launch
   int teams;
   int* pre;               // [B + 1] first stage of each sequence, left for the merge
-  float* part;            // [teams + B·Hkv][R][DH + 4]
-  int R;                  // rows per piece: n·G
+  float* part;            // [teams + B·P][rows][DH + 4]
+  int R;                  // rows of a KV head: n·G
+  int rows;               // rows per pair
+  int tiles;              // pairs per KV head, 1 or 2, of `rows` rows each
+  int P;                  // pairs of a sequence: Hkv·tiles
 };
 
-// Stages of sequence b (per KV head).
+// Stages of a pair of sequence b.
 __device__ __forceinline__ int stages_of(const AttnArgs& a, const SeqRange& s, int runs) {
   if (s.nn <= 0) return 0;
   return (key_runs(s.len, s.first, a.window, a.sinks, kRun).count + runs - 1) / runs;
 }
 
-// A walk along the line of stages: (sequence, KV head, stage).
+// A walk along the line of stages: (sequence, pair, stage).
 struct Walk {
-  int b, h, st, n_st;
+  int b, p, st, n_st;
 };
 
 // pre[i] = Σ_{j < i} cnt[j] in place over smem ints, i <= n, by the whole CTA
@@ -166,26 +170,25 @@ __device__ __forceinline__ void scan_in_place(int* pre, int n, int* tmp) {
   __syncthreads();
 }
 
-template <int DH, bool E4, int TW, bool LO>
-__global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
+template <int DH, bool E4, int MT, bool LO>
+__global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
     k_attn_few(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const FewArgs f) {
   pdl_trigger();
   pdl_wait();
   using C = FewCfg<DH, E4>;
-  constexpr int kWarps = FewShape<E4, LO>::WARPS;
-  constexpr int S = FewShape<E4, LO>::SLOTS * TW;        // slots of a team
-  constexpr int NR = LO ? 1 : 2;                // rows of a lane: g, and g + 8
+  constexpr int kWarps = FewShape<E4, MT, LO>::WARPS;
+  constexpr int S = FewShape<E4, MT, LO>::SLOTS;
+  constexpr int NR = LO ? 1 : 2;                // rows of a lane and tile: g, and g + 8
+  static_assert(MT == 1 || !LO, "half a tile stands alone");
   const AttnArgs& a = f.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int team_in = warp / TW, tw = warp % TW;
   int* pre = reinterpret_cast<int*>(smem + C::OFF_SEQ);   // [B + 1] first stage of each sequence
   int* len_s = pre + f.B + 1;
   int* nn_s = len_s + f.B;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + team_in * S;
-  uint64_t* empty = full + kStages;
-  float2* sc = reinterpret_cast<float2*>(smem + C::OFF_SC) + team_in * S * C::RUNS;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * S;
+  float2* sc = reinterpret_cast<float2*>(smem + C::OFF_SC) + warp * S * C::RUNS;
   __shared__ int abort_word, tmp[kWarps];
   const int Hkv = a.c.Hkv, G = a.H / Hkv;
 
@@ -193,14 +196,11 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
     const SeqRange s = seq_range(a, f.b0 + b);
     len_s[b] = s.len;
     nn_s[b] = s.nn;
-    pre[b] = stages_of(a, s, C::RUNS) * Hkv;
+    pre[b] = stages_of(a, s, C::RUNS) * f.P;
   }
   if (threadIdx.x == 0) {
     abort_word = 0;
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + i, 1);
-      mbar_init(reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + kStages + i, TW);
-    }
+    for (int i = 0; i < kWarps * S; ++i) mbar_init(reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + i, 1);
     fence_barrier_init();
   }
   __syncthreads();
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b <= f.B; b += blockDim.x) f.pre[b] = pre[b];
   const int teams = min(f.teams, total);        // each of them has a stage at least
-  const int team = team_in * gridDim.x + blockIdx.x;
+  const int team = warp * gridDim.x + blockIdx.x;
   const bool mine = team < teams;
   const int x0 = mine ? (int)((long long)total * team / teams) : 0;
   const int x1 = mine ? (int)((long long)total * (team + 1) / teams) : 0;
@@ -223,21 +223,21 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
     }
     Walk w;
     w.b = lo;                                   // the last with pre <= x: it has stages
-    w.n_st = (pre[lo + 1] - pre[lo]) / Hkv;
-    w.h = (x - pre[lo]) / w.n_st;
+    w.n_st = (pre[lo + 1] - pre[lo]) / f.P;
+    w.p = (x - pre[lo]) / w.n_st;
     w.st = (x - pre[lo]) % w.n_st;
     return w;
   };
   auto next_pair = [&](Walk& w) {
     w.st = 0;
-    if (++w.h < Hkv) return;
-    w.h = 0;
+    if (++w.p < f.P) return;
+    w.p = 0;
     do ++w.b; while (w.b < f.B && pre[w.b + 1] == pre[w.b]);
-    if (w.b < f.B) w.n_st = (pre[w.b + 1] - pre[w.b]) / Hkv;
+    if (w.b < f.B) w.n_st = (pre[w.b + 1] - pre[w.b]) / f.P;
   };
   auto runs_of = [&](int b) { return key_runs(len_s[b], len_s[b] - nn_s[b], a.window, a.sinks, kRun); };
 
-  // ---- producer state (the team's first warp, all lanes alike) ----
+  // ---- producer state (all lanes alike) ----
   Walk pw{};
   KeyRuns pr{};
   int issued = x0, pbase = 0, ppage = 0;        // lane i: plane, and scales, of run pbase + i
@@ -248,27 +248,23 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
     pr = runs_of(pw.b);
     pbase = -64;
   }
-  uint8_t* ring = smem + (size_t)team_in * S * kStage;
-  auto produce = [&](int consumed) -> bool {
-    // (one slot of slack for the other warps of a team)
-    while (issued < x1 && issued < consumed + S - (TW > 1 ? 1 : 0)) {
+  uint8_t* ring = smem + (size_t)warp * S * kStage;
+  auto produce = [&](int consumed) {
+    while (issued < x1 && issued < consumed + S) {
       const int k = issued - x0, sl = k % S;
-      if constexpr (TW > 1) {
-        if (k >= S && !mbar_wait_warp(&empty[sl], ((k / S) - 1) & 1, abort_flag, f.a.c.err)) return false;
-      }
       const int r0 = pw.st * C::RUNS, nr = min(C::RUNS, pr.count - r0);
       if (r0 < pbase || r0 + nr > pbase + 32) {          // the next 32 runs of this pair
         pbase = r0;
-        const int r = r0 + lane;
+        const int r = r0 + lane, h = pw.p >> (f.tiles - 1);
         if (r < pr.count) {
           const int key = run_index(pr, r) * kRun;
           long long si = 0;
           if (a.c.bt) {
             const int page = cache_page(a.c, f.b0 + pw.b, key);
-            ppage = page < 0 ? -1 : page * Hkv + pw.h;
+            ppage = page < 0 ? -1 : page * Hkv + h;
             si = ppage;
           } else {
-            ppage = (f.b0 + pw.b) * Hkv + pw.h;
+            ppage = (f.b0 + pw.b) * Hkv + h;
             si = (long long)ppage * a.c.per + key / a.c.ps;
           }
           if constexpr (E4) {
@@ -310,15 +306,16 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
         pbase = -64;
       }
     }
-    return true;
   };
 
   // ---- consumer ----
   const int mi = lane >> 3;
-  uint32_t qa[DH / 16][2 * NR];
-  float o[DH / 8][4];                          // (with eight rows the upper half stays 0)
-  float m[NR], l[NR], zscale[NR];
-  int qpos[NR];                                // position of the lane's rows; -1: none
+  // A fragments of the queries: registers, or with two tiles shared memory
+  uint32_t qa[MT == 1 ? DH / 16 : 1][2 * NR];
+  const uint32_t q_s = smem_u32(smem + C::OFF_Q) + (uint32_t)(warp * (2 * DH / 16) * 32 + lane) * 16;
+  float o[MT][DH / 8][4];                      // (with eight rows the upper half stays 0)
+  float m[MT * NR], l[MT * NR], zscale[MT * NR];
+  int qpos[MT * NR];                           // position of the lane's rows; -1: none
   Walk w{};
   KeyRuns kr{};
   int len = 0, first = 0, last = 0;
@@ -326,10 +323,7 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
   if (x0 < x1) w = enter(x0);
   bool fresh = true;
   for (int x = x0; x < x1; ++x) {
-    if (tw == 0 && !produce(x)) {
-      ok = false;
-      break;
-    }
+    produce(x);
     const int k = x - x0, sl = k % S;
     if (fresh) {                               // a new pair: its queries
       fresh = false;
@@ -338,47 +332,62 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
       const int nn = nn_s[w.b];
       first = len - nn;
       last = len - 1;
+      const int h = w.p >> (f.tiles - 1), row0 = (w.p & (f.tiles - 1)) * f.rows;
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const int row = tw * 16 + g + 8 * i;
-        const int tok = row / G;
-        const bool in = tok < nn;
-        qpos[i] = in ? first + tok : -1;
-        const bf16* q = (const bf16*)a.q +
-                        (((size_t)(f.b0 + w.b) * a.n + (in ? tok : 0)) * a.H + w.h * G + row % G) * DH;
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-        zscale[i] = a.scale_log2;
-        if constexpr (!E4) {
+      for (int mt = 0; mt < MT; ++mt) {
+        uint32_t fr_[DH / 16][2 * NR];
 #pragma unroll
-          for (int p = 0; p < DH / 16; ++p) {
-            qa[p][i] = in ? *reinterpret_cast<const uint32_t*>(q + 16 * p + 2 * t) : 0u;
-            qa[p][NR + i] = in ? *reinterpret_cast<const uint32_t*>(q + 16 * p + 8 + 2 * t) : 0u;
-          }
-        } else {
-          float amax = 0.f;
-          uint2 raw[DH / 16];
+        for (int i = 0; i < NR; ++i) {
+          const int ri = mt * NR + i, row = row0 + mt * 16 + g + 8 * i;
+          const int tok = row / G;
+          const bool in = tok < nn;
+          qpos[ri] = in ? first + tok : -1;
+          const bf16* q = (const bf16*)a.q +
+                          (((size_t)(f.b0 + w.b) * a.n + (in ? tok : 0)) * a.H + h * G + row % G) * DH;
+          m[ri] = -INFINITY;
+          l[ri] = 0.f;
+          zscale[ri] = a.scale_log2;
+          if constexpr (!E4) {
 #pragma unroll
-          for (int p = 0; p < DH / 16; ++p) {
-            raw[p] = in ? *reinterpret_cast<const uint2*>(q + 16 * p + 4 * t) : make_uint2(0u, 0u);
-            amax = fmaxf(fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[p].x << 16)), fabsf(__uint_as_float(raw[p].x & 0xffff0000u)))),
-                         fmaxf(fabsf(__uint_as_float(raw[p].y << 16)), fabsf(__uint_as_float(raw[p].y & 0xffff0000u))));
-          }
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          const float fr = pow2_frame(amax);
-          zscale[i] = a.scale_log2 / fr;       // exact
+            for (int p = 0; p < DH / 16; ++p) {
+              fr_[p][i] = in ? *reinterpret_cast<const uint32_t*>(q + 16 * p + 2 * t) : 0u;
+              fr_[p][NR + i] = in ? *reinterpret_cast<const uint32_t*>(q + 16 * p + 8 + 2 * t) : 0u;
+            }
+          } else {
+            float amax = 0.f;
+            uint2 raw[DH / 16];
 #pragma unroll
-          for (int p = 0; p < DH / 16; ++p) {
-            qa[p][i] = pack<true>(__uint_as_float(raw[p].x << 16) * fr, __uint_as_float(raw[p].x & 0xffff0000u) * fr);
-            qa[p][NR + i] = pack<true>(__uint_as_float(raw[p].y << 16) * fr, __uint_as_float(raw[p].y & 0xffff0000u) * fr);
+            for (int p = 0; p < DH / 16; ++p) {
+              raw[p] = in ? *reinterpret_cast<const uint2*>(q + 16 * p + 4 * t) : make_uint2(0u, 0u);
+              amax = fmaxf(fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[p].x << 16)), fabsf(__uint_as_float(raw[p].x & 0xffff0000u)))),
+                           fmaxf(fabsf(__uint_as_float(raw[p].y << 16)), fabsf(__uint_as_float(raw[p].y & 0xffff0000u))));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            const float fr = pow2_frame(amax);
+            zscale[ri] = a.scale_log2 / fr;    // exact
+#pragma unroll
+            for (int p = 0; p < DH / 16; ++p) {
+              fr_[p][i] = pack<true>(__uint_as_float(raw[p].x << 16) * fr, __uint_as_float(raw[p].x & 0xffff0000u) * fr);
+              fr_[p][NR + i] = pack<true>(__uint_as_float(raw[p].y << 16) * fr, __uint_as_float(raw[p].y & 0xffff0000u) * fr);
+            }
           }
         }
+        if constexpr (MT == 1) {
+#pragma unroll
+          for (int p = 0; p < DH / 16; ++p)
+#pragma unroll
+            for (int j = 0; j < 2 * NR; ++j) qa[p][j] = fr_[p][j];
+        } else {
+#pragma unroll
+          for (int p = 0; p < DH / 16; ++p)
+            sts128(q_s + (mt * (DH / 16) + p) * 512, make_uint4(fr_[p][0], fr_[p][1], fr_[p][NR], fr_[p][2 * NR - 1]));
+        }
+#pragma unroll
+        for (int i = 0; i < DH / 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[mt][i][j] = 0.f;
       }
-#pragma unroll
-      for (int i = 0; i < DH / 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     }
     if (!mbar_wait_warp(&full[sl], (k / S) & 1, abort_flag, a.c.err)) {
       ok = false;
@@ -386,41 +395,79 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
     }
     const uint32_t kb0 = smem_u32(ring + sl * kStage), vb0 = kb0 + C::HALF;
     const int r0 = w.st * C::RUNS, nr = min(C::RUNS, kr.count - r0);
-    // Scores, scaled to base 2 (over e4m3 with log2 of the V scale added), of
-    // the stage's runs: z[run][8-key tile][row i: keys 2t, 2t+1]
-    float z[C::RUNS][2][2 * NR];
+    // Scores of the stage's runs, z[run][8-key tile][row tile][row i: keys 2t, 2t+1]
+    float z[C::RUNS][2][MT][4];
+#pragma unroll
+    for (int r = 0; r < C::RUNS; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z[r][h][mt][j] = 0.f;
+    constexpr int PS = E4 ? 2 : 1;             // 16-dim slices per step: an ldmatrix holds that many
+    auto step = [&](int r, int p, const uint32_t(&qf)[PS][MT][4]) {
+      const uint32_t kb = kb0 + r * C::RUN;
+      uint32_t b[4];
+      if constexpr (!E4) {
+        ldsm4(piece<DH, E4>(kb, 8 * (mi >> 1) + (lane & 7), 2 * p + (mi & 1)), b);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma<E4>(z[r][0][mt], qf[0][mt][0], qf[0][mt][1], qf[0][mt][2], qf[0][mt][3], b[0], b[1]);
+          mma<E4>(z[r][1][mt], qf[0][mt][0], qf[0][mt][1], qf[0][mt][2], qf[0][mt][3], b[2], b[3]);
+        }
+      } else {
+        ldsm4(piece<DH, E4>(kb, 8 * (mi & 1) + (lane & 7), p + (mi >> 1)), b);
+#pragma unroll
+        for (int u = 0; u < PS; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t lo, hi;
+            codes4(b[2 * u + h], lo, hi);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              mma<E4>(z[r][h][mt], qf[u][mt][0], qf[u][mt][1], qf[u][mt][2], qf[u][mt][3], lo, hi);
+          }
+      }
+    };
+    if constexpr (MT == 2) {
+#pragma unroll
+      for (int p = 0; p < DH / 16; p += PS) {  // a slice of the queries is loaded once for all runs
+        uint32_t qf[PS][MT][4];
+#pragma unroll
+        for (int u = 0; u < PS; ++u)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const uint4 v = lds128(q_s + (mt * (DH / 16) + p + u) * 512);
+            qf[u][mt][0] = v.x, qf[u][mt][1] = v.y, qf[u][mt][2] = v.z, qf[u][mt][3] = v.w;
+          }
+#pragma unroll
+        for (int r = 0; r < C::RUNS; ++r) {
+          if (r >= nr) break;
+          step(r, p, qf);
+        }
+      }
+    }
+    // scaled to base 2, over e4m3 with log2 of the V scale added; hidden ones -inf
     float vsc[C::RUNS];                        // E4: the runs' V scales
 #pragma unroll
     for (int r = 0; r < C::RUNS; ++r) {
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-      if (r < nr) {
-        const uint32_t kb = kb0 + r * C::RUN;
-        if constexpr (!E4) {
-          const int row = 8 * (mi >> 1) + (lane & 7);
+      if (MT == 1 && r < nr) {
 #pragma unroll
-          for (int p = 0; p < DH / 16; ++p) {
-            uint32_t b[4];
-            ldsm4(piece<DH, E4>(kb, row, 2 * p + (mi & 1)), b);
-            mma<E4>(s0, qa[p][0], LO ? 0u : qa[p][NR - 1], qa[p][NR], LO ? 0u : qa[p][2 * NR - 1], b[0], b[1]);
-            mma<E4>(s1, qa[p][0], LO ? 0u : qa[p][NR - 1], qa[p][NR], LO ? 0u : qa[p][2 * NR - 1], b[2], b[3]);
+        for (int p = 0; p < DH / 16; p += PS) {
+          uint32_t qf[PS][MT][4];
+#pragma unroll
+          for (int u = 0; u < PS; ++u) {
+            qf[u][0][0] = qa[MT == 1 ? p + u : 0][0];
+            qf[u][0][1] = LO ? 0u : qa[MT == 1 ? p + u : 0][NR - 1];
+            qf[u][0][2] = qa[MT == 1 ? p + u : 0][NR];
+            qf[u][0][3] = LO ? 0u : qa[MT == 1 ? p + u : 0][2 * NR - 1];
           }
-        } else {
-          const int row = 8 * (mi & 1) + (lane & 7);
-#pragma unroll
-          for (int p = 0; p < DH / 16; p += 2) {
-            uint32_t b[4], lo, hi;
-            ldsm4(piece<DH, E4>(kb, row, p + (mi >> 1)), b);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              codes4(b[2 * u], lo, hi);
-              mma<E4>(s0, qa[p + u][0], LO ? 0u : qa[p + u][NR - 1], qa[p + u][NR], LO ? 0u : qa[p + u][2 * NR - 1], lo, hi);
-              codes4(b[2 * u + 1], lo, hi);
-              mma<E4>(s1, qa[p + u][0], LO ? 0u : qa[p + u][NR - 1], qa[p + u][NR], LO ? 0u : qa[p + u][2 * NR - 1], lo, hi);
-            }
-          }
+          step(r, p, qf);
         }
       }
       float ks = 1.f, ve = 0.f;
+      vsc[r] = 1.f;
       if constexpr (E4) {
         if (r < nr) {
           const float2 v = lds_f2(smem_u32(sc + sl * C::RUNS + r));
@@ -434,37 +481,35 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
       const bool all = r < nr && key + kRun - 1 <= first &&
                        (a.window == 0 || key >= win_lo(last, a.window) || key + kRun <= a.sinks);
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const float zs = E4 ? zscale[i] * ks : zscale[i];
+      for (int ri = 0; ri < MT * NR; ++ri) {
+        const int mt = ri / NR, i = ri % NR;
+        const float zs = E4 ? zscale[ri] * ks : zscale[ri];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          z[r][0][2 * i + j] = E4 ? fmaf(s0[2 * i + j], zs, ve) : s0[2 * i + j] * zs;
-          z[r][1][2 * i + j] = E4 ? fmaf(s1[2 * i + j], zs, ve) : s1[2 * i + j] * zs;
-        }
+        for (int j = 2 * i; j < 2 * i + 2; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) z[r][h][mt][j] = E4 ? fmaf(z[r][h][mt][j], zs, ve) : z[r][h][mt][j] * zs;
         if (!all) {
-          const int lo = win_lo(qpos[i], a.window);
+          const int lo = win_lo(qpos[ri], a.window);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int kk = key + 8 * h + 2 * t + j;
-              const bool see = r < nr && kk <= qpos[i] && (kk >= lo || kk < a.sinks);
-              if (!see) z[r][h][2 * i + j] = -INFINITY;
+              const bool see = r < nr && kk <= qpos[ri] && (kk >= lo || kk < a.sinks);
+              if (!see) z[r][h][mt][2 * i + j] = -INFINITY;
             }
         }
       }
       // v rows that no query of the call sees: 0·NaN is NaN inside an MMA
       if (r < nr) {
-        const int hid0 = min(max(a.sinks, 0), win_lo(first, a.window));   // hidden: [hid0, win_lo(first)) and [len, ..)
-        const int hid1 = win_lo(first, a.window);
+        const int hid1 = win_lo(first, a.window), hid0 = min(a.sinks, hid1);   // hidden: [hid0, hid1) and [len, ..)
         if (key + kRun > len || (key < hid1 && key + kRun > hid0)) {
-          uint8_t* vr = ring + sl * kStage + C::HALF + r * C::RUN;
+          const uint32_t vr = vb0 + r * C::RUN;
           for (int i = lane; i < kRun * C::ROW / 16; i += 32) {
             const int nb = i / (kRun * C::BOXB / 16), row = i / (C::BOXB / 16) % kRun;
             const int kk = key + row;
             if (kk >= len || (kk >= hid0 && kk < hid1))
-              *reinterpret_cast<uint4*>(vr + nb * C::BOX + row * C::BOXB + i % (C::BOXB / 16) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+              sts128(vr + nb * C::BOX + row * C::BOXB + i % (C::BOXB / 16) * 16, make_uint4(0u, 0u, 0u, 0u));
           }
           __syncwarp();
         }
@@ -472,96 +517,92 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
     }
     // online softmax
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
+    for (int ri = 0; ri < MT * NR; ++ri) {
+      const int mt = ri / NR, i = ri % NR;
       float mx = -INFINITY;
 #pragma unroll
       for (int r = 0; r < C::RUNS; ++r)
-        mx = fmaxf(mx, fmaxf(fmaxf(z[r][0][2 * i], z[r][0][2 * i + 1]), fmaxf(z[r][1][2 * i], z[r][1][2 * i + 1])));
+        mx = fmaxf(mx, fmaxf(fmaxf(z[r][0][mt][2 * i], z[r][0][mt][2 * i + 1]),
+                             fmaxf(z[r][1][mt][2 * i], z[r][1][mt][2 * i + 1])));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (mx > m[i] + kRescale || (m[i] == -INFINITY && mx > -INFINITY)) {
-        const float fac = ex2_approx(m[i] - mx);          // 0 from -inf
-        l[i] *= fac;
+      if (mx > m[ri] + kRescale || (m[ri] == -INFINITY && mx > -INFINITY)) {
+        const float fac = ex2_approx(m[ri] - mx);         // 0 from -inf
+        l[ri] *= fac;
 #pragma unroll
         for (int d = 0; d < DH / 8; ++d) {
-          o[d][2 * i] *= fac;
-          o[d][2 * i + 1] *= fac;
+          o[mt][d][2 * i] *= fac;
+          o[mt][d][2 * i + 1] *= fac;
         }
-        m[i] = mx;
+        m[ri] = mx;
       }
     }
 #pragma unroll
     for (int r = 0; r < C::RUNS; ++r) {
       if (r >= nr) break;
-      uint32_t pa[2 * NR];
+      uint32_t pa[MT][4];
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const float base = m[i] == -INFINITY ? 0.f : m[i];
-        const float p0 = ex2_approx(z[r][0][2 * i] - base), p1 = ex2_approx(z[r][0][2 * i + 1] - base);
-        const float p2 = ex2_approx(z[r][1][2 * i] - base), p3 = ex2_approx(z[r][1][2 * i + 1] - base);
+      for (int mt = 0; mt < MT; ++mt) pa[mt][1] = pa[mt][3] = 0u;
+#pragma unroll
+      for (int ri = 0; ri < MT * NR; ++ri) {
+        const int mt = ri / NR, i = ri % NR;
+        const float base = m[ri] == -INFINITY ? 0.f : m[ri];
+        const float p0 = ex2_approx(z[r][0][mt][2 * i] - base), p1 = ex2_approx(z[r][0][mt][2 * i + 1] - base);
+        const float p2 = ex2_approx(z[r][1][mt][2 * i] - base), p3 = ex2_approx(z[r][1][mt][2 * i + 1] - base);
         const float sum = (p0 + p1) + (p2 + p3);
-        if constexpr (E4) {
-          l[i] = fmaf(sum, scale_inv(vsc[r]), l[i]);
-        } else {
-          l[i] += sum;
-        }
-        pa[i] = pack<E4>(p0, p1);
-        pa[NR + i] = pack<E4>(p2, p3);
+        l[ri] = E4 ? fmaf(sum, scale_inv(vsc[r]), l[ri]) : l[ri] + sum;
+        pa[mt][i] = pack<E4>(p0, p1);
+        pa[mt][2 + i] = pack<E4>(p2, p3);
       }
       const uint32_t vb = vb0 + r * C::RUN;
       const int row = 8 * (mi & 1) + (lane & 7);
-      if constexpr (!E4) {
 #pragma unroll
-        for (int dt = 0; dt < DH / 8; dt += 2) {
-          uint32_t b[4];
-          ldsm4t(piece<DH, E4>(vb, row, dt + (mi >> 1)), b);
+      for (int c = 0; c < (E4 ? DH / 16 : DH / 8); c += 2) {
+        uint32_t b[4];
+        ldsm4t(piece<DH, E4>(vb, row, c + (mi >> 1)), b);
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-            mma<E4>(o[dt + u], pa[0], LO ? 0u : pa[NR - 1], pa[NR], LO ? 0u : pa[2 * NR - 1], b[2 * u], b[2 * u + 1]);
-        }
-      } else {
+        for (int u = 0; u < 2; ++u) {
+          if constexpr (!E4) {
 #pragma unroll
-        for (int c = 0; c < DH / 16; c += 2) {
-          uint32_t b[4];
-          ldsm4t(piece<DH, E4>(vb, row, c + (mi >> 1)), b);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
+            for (int mt = 0; mt < MT; ++mt)
+              mma<E4>(o[mt][c + u], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], b[2 * u], b[2 * u + 1]);
+          } else {
             uint32_t e0, o0, e1, o1;           // even and odd dims; keys 0..7, 8..15
             codes4(__byte_perm(b[2 * u], 0, 0x3120), e0, o0);
             codes4(__byte_perm(b[2 * u + 1], 0, 0x3120), e1, o1);
-            const int d = 2 * (c + u);
-            mma<E4>(o[d], pa[0], LO ? 0u : pa[NR - 1], pa[NR], LO ? 0u : pa[2 * NR - 1], e0, e1);
-            mma<E4>(o[d + 1], pa[0], LO ? 0u : pa[NR - 1], pa[NR], LO ? 0u : pa[2 * NR - 1], o0, o1);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma<E4>(o[mt][2 * (c + u)], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], e0, e1);
+              mma<E4>(o[mt][2 * (c + u) + 1], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], o0, o1);
+            }
           }
         }
       }
     }
     __syncwarp();                              // the slot may be refilled
-    if constexpr (TW > 1) {
-      if (lane == 0) mbar_arrive(&empty[sl]);
-    }
     const bool pair_ends = w.st + 1 == w.n_st;
     if (pair_ends || x + 1 == x1) {            // this piece's state
-      const long long pc = (long long)team + (long long)w.b * Hkv + w.h;
+      const long long pc = (long long)team + (long long)w.b * f.P + w.p;
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        float ls = l[i];
+      for (int ri = 0; ri < MT * NR; ++ri) {
+        const int mt = ri / NR, i = ri % NR;
+        float ls = l[ri];
         ls += __shfl_xor_sync(0xffffffffu, ls, 1);
         ls += __shfl_xor_sync(0xffffffffu, ls, 2);
-        const int row = tw * 16 + g + 8 * i;
-        if (row >= f.R) continue;
-        float* dst = f.part + (pc * f.R + row) * (DH + 4);
+        const int row = mt * 16 + g + 8 * i;
+        if (row >= f.rows) continue;
+        float* dst = f.part + (pc * f.rows + row) * (DH + 4);
         if constexpr (!E4) {
 #pragma unroll
           for (int d = 0; d < DH / 8; ++d)
-            *reinterpret_cast<float2*>(dst + 4 + 8 * d + 2 * t) = make_float2(o[d][2 * i], o[d][2 * i + 1]);
+            *reinterpret_cast<float2*>(dst + 4 + 8 * d + 2 * t) = make_float2(o[mt][d][2 * i], o[mt][d][2 * i + 1]);
         } else {
 #pragma unroll
           for (int c = 0; c < DH / 16; ++c)
-            *reinterpret_cast<float4*>(dst + 4 + 16 * c + 4 * t) =
-                make_float4(o[2 * c][2 * i], o[2 * c + 1][2 * i], o[2 * c][2 * i + 1], o[2 * c + 1][2 * i + 1]);
+            *reinterpret_cast<float4*>(dst + 4 + 16 * c + 4 * t) = make_float4(
+                o[mt][2 * c][2 * i], o[mt][2 * c + 1][2 * i], o[mt][2 * c][2 * i + 1], o[mt][2 * c + 1][2 * i + 1]);
         }
-        if (t == 0) *reinterpret_cast<float2*>(dst) = make_float2(m[i], ls);
+        if (t == 0) *reinterpret_cast<float2*>(dst) = make_float2(m[ri], ls);
       }
     }
     if (pair_ends) {
@@ -572,14 +613,14 @@ __global__ void __launch_bounds__((FewShape<E4, LO>::WARPS * 32), 1)
     }
   }
   // copies issued but not consumed (after a wait that ran out) must land first
-  if (!ok && tw == 0 && lane == 0) {
+  if (!ok && lane == 0) {
     volatile int no_abort = 0;
     for (int x = x0 > issued - S ? x0 : issued - S; x < issued; ++x)
       mbar_wait(&full[(x - x0) % S], ((x - x0) / S) & 1, &no_abort, a.c.err);
   }
 }
 
-// Joins the pieces of a row of a (sequence, KV head): o = Σ w_i O_i / Σ w_i l_i,
+// Joins the pieces of a row of a pair: o = Σ w_i O_i / Σ w_i l_i,
 // w_i = 2^(m_i - M), in the order of the teams.  One warp per row, or with many
 // pieces (WIDE) eight warps, each a run of them, whose results are joined the same
 // way.  A lane holds DH/32 consecutive dims.
@@ -590,9 +631,10 @@ __global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
   constexpr int D = DH / 32;
   const AttnArgs& a = f.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int Hkv = a.c.Hkv, G = a.H / Hkv;
+  const int G = a.H / a.c.Hkv;
   const int row = WIDE ? blockIdx.x : blockIdx.x * 8 + warp, h = blockIdx.y, b = blockIdx.z;
-  const int total = f.pre[f.B], before = f.pre[b], n_st = (f.pre[b + 1] - before) / Hkv;
+  const int tile = row >= f.rows, pair = h * f.tiles + tile;
+  const int total = f.pre[f.B], before = f.pre[b], n_st = (f.pre[b + 1] - before) / f.P;
   const int nn = a.n_new ? min(max(a.n_new[f.b0 + b], 0), a.n) : a.n;
   const int tok = row / G, head = h * G + row % G;
   if (row >= f.R || tok >= nn) return;
@@ -603,11 +645,11 @@ __global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
   if (n_st > 0) {                               // (no stages: no rows in the cache)
     // team t has stages [total·t / teams, total·(t+1) / teams): those of the pair's first and last stage
     const int teams = min(f.teams, total);
-    const long long U0 = before + (long long)h * n_st, U1 = U0 + n_st;
+    const long long U0 = before + (long long)pair * n_st, U1 = U0 + n_st;
     const int t0 = (int)(((U0 + 1) * teams + total - 1) / total) - 1;
     const int np = (int)((U1 * teams + total - 1) / total) - t0;
-    const float* p0 = f.part + ((t0 + (long long)b * Hkv + h) * f.R + row) * (DH + 4);
-    const size_t step = (size_t)f.R * (DH + 4);
+    const float* p0 = f.part + ((t0 + (long long)b * f.P + pair) * f.rows + row - tile * f.rows) * (DH + 4);
+    const size_t step = (size_t)f.rows * (DH + 4);
     const int i0 = WIDE ? np * warp / 8 : 0, i1 = WIDE ? np * (warp + 1) / 8 : np;
     for (int i = i0 + lane; i < i1; i += 32) M = fmaxf(M, p0[i * step]);
 #pragma unroll
@@ -678,10 +720,33 @@ __global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
 }
 
 constexpr size_t kPreBytes = (kMaxB + 1) * 4 / 256 * 256 + 256;
-int team_warps(int R) { return R <= 16 ? 1 : 2; }
 
-template <int DH, bool E4, int TW, bool LO>
-cudaError_t run(const AttnArgs& a, void* ws, int Bl, cudaStream_t s) {
+// How the rows of a KV head are dealt: pairs of `rows` rows, warps with `mt`
+// tiles of 16.  From 17 rows on a warp holds two tiles, so that a key is read and
+// converted once for both: 53 against 62 us over e4m3 (4 sequences of 16k, 32
+// rows), 56 against 69 in bf16, 84 against 106 (32 of 4k, e4m3).  With little to
+// read the tiles are pairs of their own, as twice the parts shorten the line more
+// than the second read from L2 costs: 31 against 38 us (8 sequences, window 2048).
+struct Deal {
+  int mt, rows, tiles, warps;
+};
+Deal deal_of(const AttnArgs& a) {
+  const int R = a.n * (a.H / a.c.Hkv);
+  const bool e4 = a.c.dtype == TB_E4M3;
+  if (R <= 16) return {1, R, 1, e4 && R <= 8 ? FewShape<true, 1, true>::WARPS : FewShape<false, 1, false>::WARPS};
+  const long long keys = a.window > 0 ? std::min<long long>(a.c.T, (long long)a.window + a.sinks + a.n) : a.c.T;
+  if (keys * a.c.B * a.c.Hkv <= 1 << 18) return {1, 16, 2, FewShape<false, 1, false>::WARPS};
+  return {2, R, 1, FewShape<false, 2, false>::WARPS};
+}
+
+// Sequences per launch: the line's stage numbers stay below 2^30.
+int batch_of(const AttnArgs& a, const Deal& d) {
+  const long long per = (long long)a.c.Hkv * d.tiles * ((a.c.T + kRun - 1) / kRun + 1);
+  return (int)std::min<long long>(std::min(a.c.B, kMaxB), std::max<long long>(1, (1LL << 30) / per));
+}
+
+template <int DH, bool E4, int MT, bool LO>
+cudaError_t run(const AttnArgs& a, const Deal& d, void* ws, cudaStream_t s) {
   using C = FewCfg<DH, E4>;
   CUtensorMap tk, tv;
   const uint64_t planes = a.c.bt ? (uint64_t)a.c.num_pages * a.c.Hkv : (uint64_t)a.c.B * a.c.Hkv;
@@ -691,68 +756,60 @@ cudaError_t run(const AttnArgs& a, void* ws, int Bl, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = make_tmap_rows(&tv, es, a.c.v, planes, rows, DH, C::BOXB / es, kRun);
   if (e != cudaSuccess) return e;
-  const size_t smem = C::smem(Bl);
-  static size_t attr_set[64] = {0};             // raised only when a launch needs more than before
+  static bool attr_set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || attr_set[dev] < smem) {
-    e = cudaFuncSetAttribute(k_attn_few<DH, E4, TW, LO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(k_attn_few<DH, E4, MT, LO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)C::smem(kMaxB));
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) attr_set[dev] = smem;
+    if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
   FewArgs f;
   f.a = a;
   f.pre = (int*)ws;
   f.part = (float*)((uint8_t*)ws + kPreBytes);
   f.R = a.n * (a.H / a.c.Hkv);
-  constexpr int warps = FewShape<E4, LO>::WARPS;
-  f.teams = sm_count() * (warps / TW);
+  f.rows = d.rows;
+  f.tiles = d.tiles;
+  f.P = a.c.Hkv * d.tiles;
+  f.teams = sm_count() * d.warps;
+  const int Bl = batch_of(a, d);
   for (int b0 = 0; b0 < a.c.B; b0 += Bl) {
     f.b0 = b0;
     f.B = std::min(Bl, a.c.B - b0);
-    e = launch_pdl(k_attn_few<DH, E4, TW, LO>, dim3(sm_count()), dim3(warps * 32), smem, s, tk, tv, f);
+    e = launch_pdl(k_attn_few<DH, E4, MT, LO>, dim3(sm_count()), dim3(d.warps * 32), C::smem(f.B), s, tk, tv, f);
     if (e != cudaSuccess) return e;
     // eight warps per row from 16 pieces of a pair on (at equal lengths)
-    const int rows = f.R;
-    if (f.teams >= 16 * f.B * a.c.Hkv)
-      e = launch_pdl(k_few_merge<DH, true>, dim3(rows, a.c.Hkv, f.B), dim3(256), 0, s, f);
+    if (f.teams >= 16 * f.B * f.P)
+      e = launch_pdl(k_few_merge<DH, true>, dim3(f.R, a.c.Hkv, f.B), dim3(256), 0, s, f);
     else
-      e = launch_pdl(k_few_merge<DH, false>, dim3((rows + 7) / 8, a.c.Hkv, f.B), dim3(256), 0, s, f);
+      e = launch_pdl(k_few_merge<DH, false>, dim3((f.R + 7) / 8, a.c.Hkv, f.B), dim3(256), 0, s, f);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
 template <int DH, bool E4>
-cudaError_t by_rows(const AttnArgs& a, void* part, int Bl, cudaStream_t s) {
-  const int R = a.n * (a.H / a.c.Hkv);
-  if (R <= 8) return run<DH, E4, 1, true>(a, part, Bl, s);
-  if (R <= 16) return run<DH, E4, 1, false>(a, part, Bl, s);
-  if (R <= kFewRows) return run<DH, E4, 2, false>(a, part, Bl, s);
-  return cudaErrorInvalidValue;
-}
-
-// Sequences per launch: the line's stage numbers stay below 2^30.
-int batch_of(const AttnArgs& a) {
-  const long long per = (long long)a.c.Hkv * ((a.c.T + kRun - 1) / kRun + 1);
-  return (int)std::min<long long>(std::min(a.c.B, kMaxB), std::max<long long>(1, (1LL << 30) / per));
+cudaError_t by_rows(const AttnArgs& a, void* ws, cudaStream_t s) {
+  const Deal d = deal_of(a);
+  if (d.mt == 2) return run<DH, E4, 2, false>(a, d, ws, s);
+  return d.rows <= 8 ? run<DH, E4, 1, true>(a, d, ws, s) : run<DH, E4, 1, false>(a, d, ws, s);
 }
 
 }  // namespace
 
 size_t cache_attn_few_workspace(const AttnArgs& a) {
-  const int R = a.n * (a.H / a.c.Hkv);
-  if (a.c.B == 0 || R == 0) return 0;
-  const int warps = R <= 8 && a.c.dtype == TB_E4M3 ? FewShape<true, true>::WARPS : FewShape<false, false>::WARPS;
-  const long long pieces = (long long)sm_count() * (warps / team_warps(R)) + (long long)batch_of(a) * a.c.Hkv;
-  return kPreBytes + (size_t)pieces * R * (a.c.dh + 4) * 4;
+  if (a.c.B == 0 || a.n == 0) return 0;
+  const Deal d = deal_of(a);
+  const long long pieces = (long long)sm_count() * d.warps + (long long)batch_of(a, d) * a.c.Hkv * d.tiles;
+  return kPreBytes + (size_t)pieces * d.rows * (a.c.dh + 4) * 4;
 }
 
 cudaError_t launch_cache_attn_few(const AttnArgs& a, void* ws, cudaStream_t s) {
-  const int Bl = batch_of(a);
-  if (a.c.dtype == TB_E4M3)
-    return a.c.dh == 128 ? by_rows<128, true>(a, ws, Bl, s) : by_rows<64, true>(a, ws, Bl, s);
-  return a.c.dh == 128 ? by_rows<128, false>(a, ws, Bl, s) : by_rows<64, false>(a, ws, Bl, s);
+  if (a.n * (a.H / a.c.Hkv) > kFewRows) return cudaErrorInvalidValue;
+  if (a.c.dtype == TB_E4M3) return a.c.dh == 128 ? by_rows<128, true>(a, ws, s) : by_rows<64, true>(a, ws, s);
+  return a.c.dh == 128 ? by_rows<128, false>(a, ws, s) : by_rows<64, false>(a, ws, s);
 }
 
 }  // namespace tb
