@@ -277,6 +277,7 @@ __device__ __noinline__ void attend_row(const AttnArgs& a, int b, int hkv, int p
 
 // cache_attn.cu
 size_t cache_attn_workspace(const AttnArgs& a);
+size_t cache_attn_workspace_upto(const AttnArgs& a);
 cudaError_t launch_cache_attn(const AttnArgs& a, void* ws, cudaStream_t s);
 
 }  // namespace tb

@@ -194,7 +194,7 @@ tb_status tb_kvcache_append_rope(const tb_kvcache* kv, const tb_append_rows* row
 
 size_t tb_kvcache_attn_workspace_bytes(const tb_attn_cfg* cfg, const tb_kvcache* kv, int32_t n) {
   if (check_attn(cfg, kv, n, false) != TB_OK) return 0;
-  return cache_attn_workspace(attn_args(cfg, kv, n, nullptr));
+  return cache_attn_workspace_upto(attn_args(cfg, kv, n, nullptr));
 }
 
 tb_status tb_kvcache_attn(const tb_attn_cfg* cfg, const void* q, const tb_kvcache* kv, const int32_t* n_new, int32_t n,

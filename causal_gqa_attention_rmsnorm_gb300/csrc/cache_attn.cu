@@ -247,20 +247,11 @@ cudaError_t run_f32(const AttnArgs& a, void* ws, cudaStream_t s) {
 }
 
 // Few rows per KV head stream the cache through warp-level MMAs, more take the
-// tensor-core kernel.  Up to 16 rows one warp holds them all: 42 against 60 us
-// (4 sequences of 16k, 8 KV heads of 128, bf16).  From 17 to 32 two warps work on
-// every stage: over e4m3, where the other kernel has V to convert, still faster
-// (59 against 64, and 105 against 110 with 32 sequences of 4k); in bf16 only where
-// there is little to read, as the other one takes three launches (32 against 37 us
-// with 8 sequences and a window of 2048, 70 against 60 with 4 of 16k).
-bool few(const AttnArgs& a) {
-  const int R = a.n * (a.H / a.c.Hkv);
-  if (R <= 16) return true;
-  if (R > kFewRows) return false;
-  if (a.c.dtype == TB_E4M3) return true;
-  const long long keys = a.window > 0 ? std::min<long long>(a.c.T, (long long)a.window + a.sinks + a.n) : a.c.T;
-  return keys * a.c.B * a.c.Hkv <= 1 << 18;
-}
+// tensor-core kernel, whose work does not grow with the rows up to 128.  bf16,
+// 20 and 32 rows against that kernel: 53 and 56 against 60 us (4 sequences of 16k,
+// 8 KV heads of 128), 63 and 66 against 76 (one of 64k), 89 and 92 against 94 (32 of
+// 4k); e4m3: 50 and 53 against 64, 57 and 59 against 81, 81 and 84 against 110.
+bool few(const AttnArgs& a) { return a.n * (a.H / a.c.Hkv) <= kFewRows; }
 
 }  // namespace
 
@@ -270,6 +261,19 @@ size_t cache_attn_workspace(const AttnArgs& a) {
   const F32Args f = f32_plan(a, nullptr);
   return f.n_range == 1 ? 0
                         : (size_t)a.c.B * a.c.Hkv * f.n_tiles * f.n_range * kRows * (a.c.dh + 2) * sizeof(float);
+}
+
+// The most that any call of up to a.n tokens needs.  Streaming calls need less
+// where their rows are dealt differently, fp32 ones where there are tiles enough
+// to leave the keys whole; the tensor-core kernel's need grows with n.
+size_t cache_attn_workspace_upto(const AttnArgs& a) {
+  size_t most = cache_attn_workspace(a);
+  const int G = a.H / a.c.Hkv;
+  AttnArgs b = a;
+  const int step = a.c.dtype == TB_F32 ? kRows / std::min(G, kRows) : 1;
+  const int rows = a.c.dtype == TB_F32 ? 2 * sm_count() * kRows : kFewRows;
+  for (b.n = step; b.n < a.n && b.n * G <= rows; b.n += step) most = std::max(most, cache_attn_workspace(b));
+  return most;
 }
 
 cudaError_t launch_cache_attn(const AttnArgs& a, void* ws, cudaStream_t s) {

@@ -373,8 +373,8 @@ typedef struct {
   float scale;
 } tb_attn_cfg;
 
-/* Workspace of tb_kvcache_attn for n query tokens per sequence over kv (the
- * layout and sizes of kv are read, not its tensors; it may be 0). */
+/* Workspace of tb_kvcache_attn calls of up to n query tokens per sequence over kv
+ * (the layout and sizes of kv are read, not its tensors; it may be 0). */
 TB_API size_t tb_kvcache_attn_workspace_bytes(const tb_attn_cfg* cfg, const tb_kvcache* kv, int32_t n);
 
 /* o[b, i, h] = sum_j softmax_j(scale q·k_j) v_j over the keys the query sees,

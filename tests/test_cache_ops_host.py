@@ -121,6 +121,15 @@ def test_attention_workspace_is_checked(lib):
             assert lib.tb_kvcache_attn(ctypes.byref(c), FAKE, ctypes.byref(kv), None, 1, FAKE, ws, wsb, None) == 1
 
 
+@pytest.mark.parametrize("dtype", [tb.TB_F32, tb.TB_BF16, tb.TB_E4M3])
+@pytest.mark.parametrize("H,Hkv,B,T,window", [(32, 8, 1, 65536, 0), (8, 8, 40, 4096, 0), (16, 2, 3, 2048, 300), (4, 4, 900, 512, 0)])
+def test_a_workspace_holds_for_fewer_tokens(lib, dtype, H, Hkv, B, T, window):
+    c = binding.tb_attn_cfg(H, Hkv, 128, tb.TB_F32 if dtype == tb.TB_F32 else tb.TB_BF16, window, 4, 0.0)
+    kv = cache(B=B, Hkv=Hkv, T=T, dh=128, dtype=dtype, ps=32, ks=FAKE, vs=FAKE)
+    need = [lib.tb_kvcache_attn_workspace_bytes(ctypes.byref(c), ctypes.byref(kv), n) for n in range(0, 200)]
+    assert need == sorted(need) and need[0] == 0
+
+
 def test_rope_table_refusals(lib):
     assert lib.tb_rope_table(63, 8, 1e4, FAKE, None) == 1
     assert lib.tb_rope_table(64, -1, 1e4, FAKE, None) == 1

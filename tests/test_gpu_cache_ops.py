@@ -2,6 +2,9 @@
 cache layout and type, head layouts, lengths from nothing to many key tiles,
 windows and sinks, ragged batches, and what must stay untouched."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -674,4 +677,132 @@ def test_small_addends_survive_large_ones(n):
         o = tb.tb_kvcache_attn(tb.AttnConfig(H=2, Hkv=1, dh=dh, scale=2.0 ** 9), q, kv, n_new=i32(1))
         # weights e / (1 + e) and 1 / (1 + e); one rounding of the weight, one of the output
         assert abs(float(o[0, 0, 0, 0]) - math.e / (1 + math.e)) <= 2 * 2.0 ** -8, kind
+    assert tb.tb_get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "e4m3"])
+def test_two_calls_at_once(kind):
+    """Steps of two caches on two streams, each with a workspace of its own."""
+    tb = tbm()
+    B, H, Hkv, dh, T, bs = 2, 8, 2, 64, 1024, 32
+    cfg = tb.AttnConfig(H=H, Hkv=Hkv, dh=dh, window=300, sinks=4, dtype=tb.TB_F32 if kind == "f32" else tb.TB_BF16)
+    table = tb.tb_rope_table(dh, T, BASE)
+    sizes = (1, 150, 6, 40)
+
+    def fresh(seed):
+        kv = make_cache(kind, True, B, Hkv, T, dh, bs, seed=seed, fill=0.0)
+        for b in range(B):
+            put_rows(kv, b, rows(seed + b, Hkv, T, dh), rows(seed + b + 9, Hkv, T, dh))
+        kv.lens.copy_(i32(500, 700))
+        return kv, tb.tb_kvcache_attn_workspace(cfg, kv, max(sizes))
+
+    xs = [[fused_rows(7 * s + n, B, n, H, Hkv, dh, ROW[kind]) for n in sizes] for s in range(2)]
+
+    def steps(kv, ws, x):
+        return [tb.tb_kvcache_attn(cfg, tb.tb_kvcache_append_rope(kv, k, v, table, q=q), kv, ws=ws) for q, k, v in x]
+
+    want = [steps(*fresh(s), xs[s]) for s in range(2)]
+    states = [fresh(s) for s in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for s in range(2):
+        with torch.cuda.stream(streams[s]):
+            got.append(steps(*states[s], xs[s]))
+    torch.cuda.synchronize()
+    for s in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(got[s], want[s]))
+    assert tb.tb_get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "e4m3"])
+def test_one_workspace_for_fewer_tokens(kind):
+    tb = tbm()
+    H, Hkv, dh, T = 8, 4, 64, 512
+    kv = make_cache(kind, True, 3, Hkv, T, dh, 16, fill=0.0)
+    for b in range(3):
+        put_rows(kv, b, rows(b, Hkv, T, dh), rows(b + 5, Hkv, T, dh))
+    kv.lens.copy_(i32(512, 300, 77))
+    cfg = tb.AttnConfig(H=H, Hkv=Hkv, dh=dh, dtype=tb.TB_F32 if kind == "f32" else tb.TB_BF16)
+    ws = tb.tb_kvcache_attn_workspace(cfg, kv, 70)
+    for n in (70, 1, 4, 5, 8, 9, 16, 17, 64, 65):
+        q = rows(n, 3, n, H, dh, dtype=ROW[kind]).cuda()
+        ws.fill_(255)
+        assert torch.equal(tb.tb_kvcache_attn(cfg, q, kv, ws=ws), tb.tb_kvcache_attn(cfg, q, kv))
+    assert tb.tb_get_device_error(clear=True) == 0
+
+
+FIRST_CALL = """
+import sys, torch
+sys.path[:0] = [%r, %r]
+import causal_gqa_attention_rmsnorm_gb300 as tb
+from cache_helpers import make_cache, put_rows, rows
+kind, n = %r, %d
+kv = make_cache(kind, True, 2, 2, 512, 64, 32, fill=0.0)
+for b in range(2):
+    put_rows(kv, b, rows(b, 2, 512, 64), rows(b + 5, 2, 512, 64))
+f32 = kind == "f32"
+q, k, v = (rows(s, 2, n, h, 64, dtype=torch.float32 if f32 else torch.bfloat16).cuda() for s, h in ((1, 4), (2, 2), (3, 2)))
+start = torch.tensor([100, 300], dtype=torch.int32, device="cuda")
+cfg = tb.AttnConfig(H=4, Hkv=2, dh=64, dtype=tb.TB_F32 if f32 else tb.TB_BF16)
+ws = tb.tb_kvcache_attn_workspace(cfg, kv, n)
+o, qr = torch.zeros_like(q), torch.zeros_like(q)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    table = tb.tb_rope_table(64, 512, 1e4)
+    tb.tb_kvcache_append_rope(kv, k, v, table, q=q, q_out=qr, start=start)
+    tb.tb_kvcache_attn(cfg, qr, kv, o=o, ws=ws)
+g.replay()
+got = o.clone()
+tb.tb_kvcache_append_rope(kv, k, v, tb.tb_rope_table(64, 512, 1e4), q=q, q_out=qr, start=start)
+tb.tb_kvcache_attn(cfg, qr, kv, o=o, ws=ws)
+assert torch.equal(o, got) and o.abs().max() > 0 and tb.tb_get_device_error() == 0
+print("same")
+"""
+
+
+@pytest.mark.parametrize("kind,n", [("f32", 3), ("bf16", 1), ("bf16", 60), ("e4m3", 12), ("e4m3", 130)])
+def test_first_calls_of_a_process_may_be_captured(kind, n):
+    here = os.path.dirname(os.path.abspath(__file__))
+    out = subprocess.run([sys.executable, "-c", FIRST_CALL % (os.path.dirname(here), here, kind, n)], cwd=here, timeout=300,
+                         capture_output=True, text=True)
+    assert out.stdout.split()[-1:] == ["same"], out.stderr[-2000:]
+
+
+def test_the_binding_refuses_tensors_that_do_not_fit():
+    tb = tbm()
+    kv = make_cache("bf16", True, 2, 2, 128, 64, 16, fill=0.0)
+    table = tb.tb_rope_table(64, 128, BASE)
+    x = lambda *s, dtype=torch.bfloat16, device="cuda": torch.zeros(*s, dtype=dtype, device=device)
+    q, k, v = x(2, 3, 4, 64), x(2, 3, 2, 64), x(2, 3, 2, 64)
+    bad_rows = [x(2, 3, 2, 32), x(1, 3, 2, 64), x(2, 4, 2, 64), x(2, 3, 4, 64), x(2, 3, 2, 64, dtype=torch.float32),
+                x(2, 3, 2, 64, device="cpu"), x(2, 3, 64, 2).transpose(2, 3), x(2, 2, 3, 64).transpose(1, 2), x(2, 3, 64)]
+    for r in bad_rows:
+        with pytest.raises(ValueError):
+            tb.tb_kvcache_append_rope(kv, k, r, table)
+    for kw in (dict(q_out=q), dict(q=q, q_out=x(2, 3, 4, 32)), dict(q=q, q_out=x(2, 3, 4, 64, dtype=torch.float32)),
+               dict(start=i32(0)), dict(start=torch.zeros(2, dtype=torch.int64, device="cuda")),
+               dict(n_new=torch.zeros(2, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            tb.tb_kvcache_append_rope(kv, k, v, table, **kw)
+    for t in (table.half(), table[:, :16].contiguous(), table.cpu(), table.reshape(-1)):
+        with pytest.raises(ValueError):
+            tb.tb_kvcache_append_rope(kv, k, v, t)
+    with pytest.raises(tb.TbError):
+        tb.tb_kvcache_append_rope(kv, k, v, table[:64])                       # shorter than the cache
+    assert kv.lens.tolist() == [0, 0]
+    cfg = tb.AttnConfig(H=4, Hkv=2, dh=64)
+    for bad in (x(2, 3, 2, 64), x(2, 3, 4, 64, dtype=torch.float32), x(2, 3, 4, 64, device="cpu"), x(6, 4, 64),
+                x(2, 4, 3, 64).transpose(1, 2)):
+        with pytest.raises(ValueError):
+            tb.tb_kvcache_attn(cfg, bad, kv)
+        with pytest.raises(ValueError):
+            tb.tb_kvcache_attn(cfg, q, kv, o=bad)
+    for kw in (dict(n_new=i32(1)), dict(ws=torch.empty(1 << 24, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            tb.tb_kvcache_attn(cfg, q, kv, **kw)
+    for kw in (dict(ws=torch.empty(256, dtype=torch.uint8, device="cuda")), dict(o=q)):
+        with pytest.raises(tb.TbError):
+            tb.tb_kvcache_attn(cfg, q, kv, **kw)
     assert tb.tb_get_device_error(clear=True) == 0
