@@ -623,7 +623,9 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
 // Joins the pieces of a row of a pair: o = Σ w_i O_i / Σ w_i l_i,
 // w_i = 2^(m_i - M), in the order of the teams.  One warp per row, or with many
 // pieces (WIDE) eight warps, each a run of them, whose results are joined the same
-// way.  A lane holds DH/32 consecutive dims.
+// way.  A lane holds DH/32 consecutive dims.  Latency counts here: eight pieces are
+// loaded at a time, under a running maximum (a pass for the maximum before it would
+// wait for memory twice).
 template <int DH, bool WIDE>
 __global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
   pdl_trigger();
@@ -651,26 +653,42 @@ __global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
     const float* p0 = f.part + ((t0 + (long long)b * f.P + pair) * f.rows + row - tile * f.rows) * (DH + 4);
     const size_t step = (size_t)f.rows * (DH + 4);
     const int i0 = WIDE ? np * warp / 8 : 0, i1 = WIDE ? np * (warp + 1) / 8 : np;
-    for (int i = i0 + lane; i < i1; i += 32) M = fmaxf(M, p0[i * step]);
+    constexpr int U = 8;                        // pieces in flight
+    for (int i = i0; i < i1; i += U) {
+      float2 ml[U];
+      float v[U][D];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-    for (int i = i0; i < i1; ++i) {
-      const float2 ml = *reinterpret_cast<const float2*>(p0 + i * step);
-      const float w = ex2_approx(ml.x - base);
-      L = fmaf(ml.y, w, L);
-      if constexpr (D == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p0 + i * step + 4 + 4 * lane);
-        acc[0] = fmaf(v.x, w, acc[0]);
-        acc[1] = fmaf(v.y, w, acc[1]);
-        acc[2] = fmaf(v.z, w, acc[2]);
-        acc[3] = fmaf(v.w, w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(p0 + i * step + 4 + 2 * lane);
-        acc[0] = fmaf(v.x, w, acc[0]);
-        acc[1] = fmaf(v.y, w, acc[1]);
+      for (int j = 0; j < U; ++j) {
+        ml[j] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int u = 0; u < D; ++u) v[j][u] = 0.f;
+        if (i + j < i1) {
+          const float* p = p0 + (i + j) * step;
+          ml[j] = *reinterpret_cast<const float2*>(p);
+          if constexpr (D == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(p + 4 + 4 * lane);
+            v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(p + 4 + 2 * lane);
+            v[j][0] = x.x, v[j][1] = x.y;
+          }
+        }
       }
+      float mx = M;
+#pragma unroll
+      for (int j = 0; j < U; ++j) mx = fmaxf(mx, ml[j].x);
+      const float base = mx == -INFINITY ? 0.f : mx, fac = ex2_approx(M - base);
+      L *= fac;
+#pragma unroll
+      for (int u = 0; u < D; ++u) acc[u] *= fac;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const float w = ex2_approx(ml[j].x - base);
+        L = fmaf(ml[j].y, w, L);
+#pragma unroll
+        for (int u = 0; u < D; ++u) acc[u] = fmaf(v[j][u], w, acc[u]);
+      }
+      M = mx;
     }
     if constexpr (WIDE) {
       __shared__ float m_s[8], l_s[8], acc_s[8][DH];
