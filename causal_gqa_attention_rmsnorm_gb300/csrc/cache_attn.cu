@@ -197,22 +197,36 @@ __global__ void __launch_bounds__(256) k_f32_merge(const F32Args f) {
   if (t >= sr.nn * G) return;
   const float* p0 = f.part + (((((size_t)b * a.c.Hkv + h) * f.n_tiles + rt) * f.n_range) * kRows + r) * (DH + 2);
   const size_t step = (size_t)kRows * (DH + 2);
-  float M = -INFINITY;
-  for (int i = lane; i < f.n_range; i += 32) M = fmaxf(M, p0[i * step + DH]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f, acc[D];
+  constexpr int U = 8;                  // ranges in flight, under a running maximum
+  float M = -INFINITY, L = 0.f, acc[D];
 #pragma unroll
   for (int u = 0; u < D; ++u) acc[u] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < f.n_range; ++i) {
-    const float* p = p0 + i * step;
-    const float wgt = exp2f(p[DH] - base);
-    L = fmaf(p[DH + 1], wgt, L);
+  for (int i = 0; i < f.n_range; i += U) {
+    float m[U], l[U], v[U][D];
 #pragma unroll
-    for (int u = 0; u < D; ++u)
-      if (DH >= 32 || lane < DH) acc[u] = fmaf(p[lane + 32 * u], wgt, acc[u]);
+    for (int j = 0; j < U; ++j) {
+      const float* p = p0 + (i + j) * step;
+      const bool in = i + j < f.n_range;
+      m[j] = in ? p[DH] : -INFINITY;
+      l[j] = in ? p[DH + 1] : 0.f;
+#pragma unroll
+      for (int u = 0; u < D; ++u) v[j][u] = in && (DH >= 32 || lane < DH) ? p[lane + 32 * u] : 0.f;
+    }
+    float mx = M;
+#pragma unroll
+    for (int j = 0; j < U; ++j) mx = fmaxf(mx, m[j]);
+    const float base = mx == -INFINITY ? 0.f : mx, fac = exp2f(M - base);
+    L *= fac;
+#pragma unroll
+    for (int u = 0; u < D; ++u) acc[u] *= fac;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const float wgt = exp2f(m[j] - base);
+      L = fmaf(l[j], wgt, L);
+#pragma unroll
+      for (int u = 0; u < D; ++u) acc[u] = fmaf(v[j][u], wgt, acc[u]);
+    }
+    M = mx;
   }
   float* out = (float*)a.o + (((size_t)b * a.n + t / G) * a.H + h * G + t % G) * DH;
 #pragma unroll
