@@ -5,6 +5,12 @@
 // row p of a table formed in fp64.  Every product and sum rounds to fp32 on its
 // own (no contraction), so that the stored bits do not depend on how a compiler
 // fuses them; the result is rounded once to the stored type.
+//
+// The bytes bound it: every row is read and written once, the table's rows are
+// reused by all heads of a token.  Measured: 4 x 4096 bf16 rows of 32 + 2·8 heads
+// of 128 into 64-row pages, 61 us, 0.81 of the copy bandwidth; 3 x 1371 rows of
+// 12 + 2·12 heads of 64 into e4m3 blocks of 64, 10.7 us (0.38: three waves of
+// dependent reads: positions, rows and page, old scale); one token 2.1 us, a launch.
 #include <algorithm>
 
 #include "cache.cuh"
@@ -104,10 +110,12 @@ template <typename T> struct Raw8 {
   }
 };
 
-// The rows of one token, by a group of threads (`me` of `group`): q, and for 16- and 32-bit caches (with_kv) k
-// and v.  A thread holds one eight-element piece of a head and that piece's four
-// (cos, sin) pairs and walks the heads of the token, H of q (if any), then Hkv of k
-// and of v, three of them on their way at a time.
+// The rows of one token, by a group of threads (`me` of `group`): q, and for
+// 16- and 32-bit caches (with_kv) k and v.  A thread holds one eight-element piece
+// of a head and that piece's four (cos, sin) pairs and walks the heads of the
+// token, H of q (if any), then Hkv of k and of v, three of them on their way at a
+// time: the angles and the page are looked up once per thread, not once per head,
+// and the first rows are asked for before the position is known.
 constexpr int kAhead = 3;
 // Threads of a group: a power of two that holds a head, and the token's `total`
 // heads kAhead to a thread where 256 threads can.
@@ -176,6 +184,8 @@ __device__ __forceinline__ void rotate_token(const AppendArgs& a, int b, int i, 
   }
 }
 
+// Six CTAs per SM: 60.5 us for the 4 x 4096 rows, against 62.3 with five and 75.9
+// with seven (fewer registers than the rows on their way need).
 template <typename T>
 __global__ void __launch_bounds__(256, 6) k_append_rope(AppendArgs a, int group) {
   pdl_trigger();

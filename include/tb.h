@@ -314,8 +314,11 @@ TB_API tb_status tb_stack_decode(const tb_block_cfg *cfg, int32_t L, const void 
  *    nearest even, and reads back as code·s.  s = 2^e with e the smallest
  *    integer for which the block's largest finite |x| is at most 448·2^e, held
  *    to [-24, 60]; larger finite values saturate at ±448·2^60, infinities and
- *    NaN are stored as NaN.
- * TB_I8 caches are TB_ERR_UNSUPPORTED here. */
+ *    NaN are stored as NaN.  Scales that a caller writes itself have to be such
+ *    powers of two.
+ * TB_I8 caches are TB_ERR_UNSUPPORTED here, and so are dh that is no multiple of
+ * 16 or above 256, B above 32767, Hkv above 65535, num_pages·Hkv above 2^31 - 2;
+ * the block's calls take no TB_E4M3 cache. */
 
 /* The rotation table of tb_kvcache_append_rope: table [max_pos, dh/2, 2] fp32
  * (device) receives (cos, sin) of t·base^(-2i/dh) for position t and pair i,
@@ -356,7 +359,8 @@ typedef struct {
  * keeps the larger of its scale and the one the new rows need; where that
  * grows, the older codes of the block are rewritten for it (x / s again, from
  * the values they stand for).  Otherwise a block's scale is that of the new
- * rows.  Pages that a call writes may belong to one sequence only. */
+ * rows.  (A start above lens and inside a block takes the scale that it finds
+ * there.)  Pages that a call writes may belong to one sequence only. */
 TB_API tb_status tb_kvcache_append_rope(const tb_kvcache* kv, const tb_append_rows* rows, const float* rope,
                                         int32_t max_pos, void* stream);
 
@@ -366,7 +370,8 @@ TB_API tb_status tb_kvcache_append_rope(const tb_kvcache* kv, const tb_append_ro
  *  dtype      : of q and o: TB_F32 for a TB_F32 cache, else TB_BF16.
  *  window W, sinks S : the query at position p sees key j iff j <= p and
  *               (W = 0 or j > p - W or j < S): its W most recent positions, its
- *               own included, and the first S.  Both non-negative.
+ *               own included, and the first S.  Both non-negative; without a
+ *               window S has no effect.
  *  scale      : of the scores; 0 stands for 1/sqrt(dh). */
 typedef struct {
   int32_t H, Hkv, dh, dtype, window, sinks;
