@@ -19,15 +19,23 @@ struct CacheView {
   int32_t* lens = nullptr;
   int B = 0, Hkv = 0, T = 0, dh = 0;
   int ps = 1;              // rows per page, or per scale block of a contiguous e4m3 cache
+  int ps_sh = -1;          // log2 of it where it is a power of two
   int per = 0;             // pages (or blocks) per sequence
   int num_pages = 0;
   int dtype = TB_BF16;
   int* err = nullptr;
 };
 
+// x / n where sh is log2 n or -1: the look-ups below stand in chains of latencies.
+__device__ __forceinline__ int div_sh(int x, int n, int sh) { return sh >= 0 ? x >> sh : x / n; }
+inline int shift_of(int n) { return n > 0 && (n & (n - 1)) == 0 ? __builtin_ctz((unsigned)n) : -1; }
+// Page (or scale block) of a sequence that token t lies in, and its row there.
+__device__ __forceinline__ int block_of(const CacheView& c, int t) { return div_sh(t, c.ps, c.ps_sh); }
+__device__ __forceinline__ int in_block(const CacheView& c, int t) { return t - block_of(c, t) * c.ps; }
+
 // Page of token t of sequence b; -1 (flagged) for an id outside the pool.
 __device__ __forceinline__ int cache_page(const CacheView& c, int b, int t) {
-  const int page = c.bt[(size_t)b * c.per + t / c.ps];
+  const int page = c.bt[(size_t)b * c.per + block_of(c, t)];
   if (page >= 0 && page < c.num_pages) return page;
   atomicOr(c.err, TB_DEVERR_BAD_PAGE);
   return -1;
@@ -38,14 +46,14 @@ __device__ __forceinline__ int cache_page(const CacheView& c, int b, int t) {
 __device__ __forceinline__ long long cache_row(const CacheView& c, int b, int h, int t, long long* sc = nullptr) {
   if (!c.bt) {
     const long long plane = (long long)b * c.Hkv + h;
-    if (sc) *sc = plane * c.per + t / c.ps;
+    if (sc) *sc = plane * c.per + block_of(c, t);
     return plane * c.T + t;
   }
   const int page = cache_page(c, b, t);
   if (page < 0) return -1;
   const long long plane = (long long)page * c.Hkv + h;
   if (sc) *sc = plane;
-  return plane * c.ps + t % c.ps;
+  return plane * c.ps + in_block(c, t);
 }
 
 // e4m3 block scales are 2^e with e in [kE4Min, kE4Max]: the block's largest
@@ -133,6 +141,7 @@ struct AttnArgs {
   void* o = nullptr;
   const int32_t* n_new = nullptr;
   int n = 0, H = 0;
+  int g_sh = 0;                    // log2 of G = H/Hkv
   int window = 0, sinks = 0;
   float scale_log2 = 0.f;          // score scale · log2 e
 };
@@ -180,6 +189,7 @@ struct AppendArgs {
   void* q_out;
   long long q_tok, q_seq, k_tok, k_seq, v_tok, v_seq;
   int H, n;
+  int pieces, piece_sh, hkv_sh;    // eight-element pieces of a row, log2 of them or -1, of Hkv or -1
   const int32_t *start, *n_new;    // start == nullptr: lens
   const float2* rope;
 };

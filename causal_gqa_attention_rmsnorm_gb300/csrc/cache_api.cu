@@ -62,6 +62,7 @@ CacheView view_of(const tb_kvcache* kv, int* err) {
   c.dh = kv->dh;
   const bool blocks = kv->block_table || kv->dtype == TB_E4M3;
   c.ps = blocks ? kv->page_size : kv->T_max;
+  c.ps_sh = shift_of(c.ps);
   c.per = blocks ? kv->T_max / kv->page_size : 1;
   c.num_pages = kv->num_pages;
   c.dtype = kv->dtype;
@@ -103,6 +104,7 @@ AttnArgs attn_args(const tb_attn_cfg* cfg, const tb_kvcache* kv, int n, int* err
   a.c = view_of(kv, err);
   a.n = n;
   a.H = cfg->H;
+  a.g_sh = shift_of(cfg->H / cfg->Hkv);
   a.window = cfg->window;
   a.sinks = cfg->window > 0 ? cfg->sinks : 0;
   const float scale = cfg->scale != 0.f ? cfg->scale : 1.0f / sqrtf((float)cfg->dh);
@@ -187,6 +189,9 @@ tb_status tb_kvcache_append_rope(const tb_kvcache* kv, const tb_append_rows* row
   a.n = rows->n;
   a.start = rows->start;
   a.n_new = rows->n_new;
+  a.pieces = kv->dh / 8;
+  a.piece_sh = shift_of(a.pieces);
+  a.hkv_sh = shift_of(kv->Hkv);
   a.rope = (const float2*)rope;
   const cudaError_t e = launch_append_rope(a, (cudaStream_t)stream);
   return e == cudaSuccess ? TB_OK : report(TB_ERR_CUDA, "tb_kvcache_append_rope: %s", cudaGetErrorString(e));

@@ -8,9 +8,9 @@
 //
 // The bytes bound it: every row is read and written once, the table's rows are
 // reused by all heads of a token.  Measured: 4 x 4096 bf16 rows of 32 + 2·8 heads
-// of 128 into 64-row pages, 61 us, 0.81 of the copy bandwidth; 3 x 1371 rows of
-// 12 + 2·12 heads of 64 into e4m3 blocks of 64, 10.7 us (0.38: three waves of
-// dependent reads: positions, rows and page, old scale); one token 2.1 us, a launch.
+// of 128 into 64-row pages, 60 us, 0.82 of the copy bandwidth; 3 x 1371 rows of
+// 12 + 2·12 heads of 64 into e4m3 blocks of 64, 9.3 us (0.43: waves of dependent
+// reads, positions, rows and page, old scale); one token 2.0 us, a launch.
 #include <algorithm>
 
 #include "cache.cuh"
@@ -127,9 +127,8 @@ int group_of(int dh, int total) {
 }
 template <typename T>
 __device__ __forceinline__ void rotate_token(const AppendArgs& a, int b, int i, int me, int group, bool with_kv) {
-  const int pieces = a.c.dh / kVec;
-  const int per = group / pieces;                       // heads in step
-  const int e = (me % pieces) * kVec, h0 = me / pieces;
+  const int per = div_sh(group, a.pieces, a.piece_sh);  // heads in step
+  const int h0 = div_sh(me, a.pieces, a.piece_sh), e = (me - h0 * a.pieces) * kVec;
   if (h0 >= per) return;
   const int Hkv = a.c.Hkv, H = a.q ? a.H : 0, dh = a.c.dh;
   const T* src_q = (const T*)a.q + b * a.q_seq + i * a.q_tok + e;
@@ -158,7 +157,7 @@ __device__ __forceinline__ void rotate_token(const AppendArgs& a, int b, int i, 
   if (with_kv && a.c.bt) {
     const int page = cache_page(a.c, b, pos);
     plane0 = page < 0 ? -1 : (long long)page * Hkv;
-    in_plane = pos % a.c.ps;
+    in_plane = in_block(a.c, pos);
     plane_rows = a.c.ps;
   }
   T* dst_q = (T*)a.q_out + ((size_t)b * a.n + i) * H * dh + e;
@@ -184,10 +183,10 @@ __device__ __forceinline__ void rotate_token(const AppendArgs& a, int b, int i, 
   }
 }
 
-// Six CTAs per SM: 60.5 us for the 4 x 4096 rows, against 62.3 with five and 75.9
+// Five CTAs per SM: 59.9 us for the 4 x 4096 rows, against 61.5 with six and 75.9
 // with seven (fewer registers than the rows on their way need).
 template <typename T>
-__global__ void __launch_bounds__(256, 6) k_append_rope(AppendArgs a, int group) {
+__global__ void __launch_bounds__(256, 5) k_append_rope(AppendArgs a, int group) {
   pdl_trigger();
   pdl_wait();
   const int sh = 31 - __clz(group), i = blockIdx.x * (blockDim.x >> sh) + (threadIdx.x >> sh), me = threadIdx.x & (group - 1);
@@ -208,29 +207,28 @@ __device__ __forceinline__ int block_exp(float top) {
 // An infinity is stored as NaN: the code has none.
 __device__ __forceinline__ float no_inf(float x) { return fabsf(x) <= 3.402823466e38f ? x : NAN; }
 
-// The blocks first, then q: CTA i of the first n_blocks takes one block of the
-// cache, one KV head, one sequence and K or V; the others take q's tokens.
+// The blocks first, then q: of a sequence's CTAs the first n_blocks take one block
+// of the cache, one KV head and K or V each, the others q's tokens.
 // For a block: the largest magnitude of its new rows, the scale, then the codes.
 // With NP > 0 a thread holds its NP eight-element pieces, rotated, from the one
 // pass to the other (32 bits each); with NP = 0 (blocks of more rows) the rows are
 // read twice, the second time from L1/L2.
 template <int NP>
-__global__ void __launch_bounds__(256) k_append_e4m3(AppendArgs a, int nb, unsigned n_blocks, int group, unsigned q_ctas) {
+__global__ void __launch_bounds__(256) k_append_e4m3(AppendArgs a, int n_blocks, int group) {
   pdl_trigger();
   pdl_wait();
-  if (blockIdx.x >= n_blocks) {
-    const unsigned c = blockIdx.x - n_blocks, b = c / q_ctas;             // q_ctas: of a sequence
-    const int sh = 31 - __clz(group), i = (int)(c - b * q_ctas) * (blockDim.x >> sh) + (threadIdx.x >> sh);
-    if (i < a.n) rotate_token<bf16>(a, (int)b, i, threadIdx.x & (group - 1), group, false);
+  const int b = blockIdx.y, c = blockIdx.x;
+  if (c >= n_blocks) {
+    const int sh = 31 - __clz(group), i = (c - n_blocks) * (blockDim.x >> sh) + (threadIdx.x >> sh);
+    if (i < a.n) rotate_token<bf16>(a, b, i, threadIdx.x & (group - 1), group, false);
     return;
   }
-  const int h = blockIdx.x % a.c.Hkv, is_v = blockIdx.x / a.c.Hkv & 1;
-  const int bi = blockIdx.x / (2 * a.c.Hkv) % nb, b = blockIdx.x / (2 * a.c.Hkv) / nb;
+  const int half = div_sh(c, a.c.Hkv, a.hkv_sh), h = c - half * a.c.Hkv, is_v = half & 1, bi = half >> 1;
   if (a.start && h == 0 && is_v == 0 && bi == 0 && threadIdx.x == 0) set_len(a, b);
   const Place p = place_of(a, b);
   if (p.nn <= 0) return;
   const int bs = a.c.ps, dh = a.c.dh;
-  const int blk = p.t0 / bs + bi;
+  const int blk = block_of(a.c, p.t0) + bi;
   const int t_lo = max(p.t0, blk * bs), t_hi = min(p.t0 + p.nn, (blk + 1) * bs);
   if (t_lo >= t_hi) return;
   // (the page's look-up, and with it the scale's, is on its way with the rows)
@@ -238,9 +236,9 @@ __global__ void __launch_bounds__(256) k_append_e4m3(AppendArgs a, int nb, unsig
   const long long row0 = cache_row(a.c, b, h, blk * bs, &sc);
   const bf16* src = is_v ? (const bf16*)a.v + b * a.v_seq + (size_t)h * dh : (const bf16*)a.k + b * a.k_seq + (size_t)h * dh;
   const long long tok = is_v ? a.v_tok : a.k_tok;
-  const int pieces = dh / kVec, n_pieces = (t_hi - t_lo) * pieces;
+  const int n_pieces = (t_hi - t_lo) * a.pieces;
   auto fetch = [&](int i, float (&x)[8]) {
-    const int t = t_lo + i / pieces, e = (i % pieces) * kVec;
+    const int r = div_sh(i, a.pieces, a.piece_sh), t = t_lo + r, e = (i - r * a.pieces) * kVec;
     load8(src + (long long)(t - p.t0) * tok + e, x);
     if (!is_v) {
       float4 cs[2];
@@ -289,7 +287,7 @@ __global__ void __launch_bounds__(256) k_append_e4m3(AppendArgs a, int nb, unsig
   if (threadIdx.x == 0) *scale = s;
   if (partial && s > was_s) {
     const float ratio = was_s / s;                       // a power of two, below 1
-    for (int i = threadIdx.x; i < (t_lo - blk * bs) * pieces; i += blockDim.x) {
+    for (int i = threadIdx.x; i < (t_lo - blk * bs) * a.pieces; i += blockDim.x) {
       uint2* at = reinterpret_cast<uint2*>(dst + (size_t)i * kVec);
       uint2 c = *at;
       uint16_t* w = reinterpret_cast<uint16_t*>(&c);
@@ -305,7 +303,7 @@ __global__ void __launch_bounds__(256) k_append_e4m3(AppendArgs a, int nb, unsig
     uint2 w;
     w.x = e4m3x2(x[0] * inv, x[1] * inv) | e4m3x2(x[2] * inv, x[3] * inv) << 16;
     w.y = e4m3x2(x[4] * inv, x[5] * inv) | e4m3x2(x[6] * inv, x[7] * inv) << 16;
-    const int t = t_lo + i / pieces, e = (i % pieces) * kVec;
+    const int r = div_sh(i, a.pieces, a.piece_sh), t = t_lo + r, e = (i - r * a.pieces) * kVec;
     *reinterpret_cast<uint2*>(dst + (size_t)(t - blk * bs) * dh + e) = w;
   };
   if constexpr (NP > 0) {
@@ -343,23 +341,22 @@ cudaError_t launch_append_rope(const AppendArgs& a, cudaStream_t s) {
     // a power of two, so that whole groups of q's tokens fill a CTA
     int threads = 32;
     while (threads < 256 && (threads < pieces || (a.q && threads < group))) threads *= 2;
-    const long long blocks = 2LL * a.c.Hkv * nb * a.c.B;
-    const unsigned q_ctas = (unsigned)((a.n + threads / group - 1) / (threads / group));
-    const long long tokens = a.q ? (long long)q_ctas * a.c.B : 0;
+    const long long blocks = 2LL * a.c.Hkv * nb;
+    const long long tokens = a.q ? (a.n + threads / group - 1) / (threads / group) : 0;
     if (blocks + tokens > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)(blocks + tokens));
-    const unsigned first = (unsigned)blocks;
+    const dim3 grid((unsigned)(blocks + tokens), (unsigned)a.c.B);
+    const int first = (int)blocks;
     const int np = (pieces + threads - 1) / threads;
     if (np <= 1)
-      e = launch_pdl(k_append_e4m3<1>, grid, dim3(threads), 0, s, a, nb, first, group, q_ctas);
+      e = launch_pdl(k_append_e4m3<1>, grid, dim3(threads), 0, s, a, first, group);
     else if (np <= 2)
-      e = launch_pdl(k_append_e4m3<2>, grid, dim3(threads), 0, s, a, nb, first, group, q_ctas);
+      e = launch_pdl(k_append_e4m3<2>, grid, dim3(threads), 0, s, a, first, group);
     else if (np <= 4)
-      e = launch_pdl(k_append_e4m3<4>, grid, dim3(threads), 0, s, a, nb, first, group, q_ctas);
+      e = launch_pdl(k_append_e4m3<4>, grid, dim3(threads), 0, s, a, first, group);
     else if (np <= 8)
-      e = launch_pdl(k_append_e4m3<8>, grid, dim3(threads), 0, s, a, nb, first, group, q_ctas);
+      e = launch_pdl(k_append_e4m3<8>, grid, dim3(threads), 0, s, a, first, group);
     else
-      e = launch_pdl(k_append_e4m3<0>, grid, dim3(threads), 0, s, a, nb, first, group, q_ctas);
+      e = launch_pdl(k_append_e4m3<0>, grid, dim3(threads), 0, s, a, first, group);
   }
   if (e == cudaSuccess && !a.start)
     e = launch_pdl(k_append_lens, dim3((a.c.B + 127) / 128), dim3(128), 0, s, a);

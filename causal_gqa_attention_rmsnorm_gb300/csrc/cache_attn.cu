@@ -38,8 +38,7 @@ struct F32Args {
 
 // The visible 32-key runs of the rows of tile rt of sequence b.
 __device__ __forceinline__ KeyRuns tile_runs(const F32Args& f, const SeqRange& sr, int rt) {
-  const int G = f.a.H / f.a.c.Hkv;
-  const int i0 = rt * kRows / G, i1 = min((rt * kRows + kRows - 1) / G, sr.nn - 1);
+  const int i0 = rt * kRows >> f.a.g_sh, i1 = min((rt * kRows + kRows - 1) >> f.a.g_sh, sr.nn - 1);
   if (i0 >= sr.nn) return KeyRuns{0, 0, 0};
   return key_runs(sr.first + i1 + 1, sr.first + i0, f.a.window, f.a.sinks, kKeys);
 }
@@ -52,7 +51,7 @@ __global__ void __launch_bounds__(kFWarps * 32) k_attn_f32(const F32Args f) {
   const AttnArgs& a = f.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rg = blockIdx.x % f.n_range, rt = blockIdx.x / f.n_range, h = blockIdx.y, b = blockIdx.z;
-  const int G = a.H / a.c.Hkv;
+  const int G = 1 << a.g_sh;
   const SeqRange sr = seq_range(a, b);
   const int rows = min(kRows, sr.nn * G - rt * kRows);      // of real tokens
   if (rows <= 0) return;
@@ -64,14 +63,14 @@ __global__ void __launch_bounds__(kFWarps * 32) k_attn_f32(const F32Args f) {
   __shared__ float acc_s[kFWarps][kRows][DH];
   auto row_at = [&](int r) {          // where row r's q and o lie
     const int t = rt * kRows + r;
-    return (((size_t)b * a.n + t / G) * a.H + h * G + t % G) * DH;
+    return (((size_t)b * a.n + (t >> a.g_sh)) * a.H + h * G + (t & (G - 1))) * DH;
   };
   for (int i = threadIdx.x; i < kRows * DH; i += kFWarps * 32)
     q_s[i / DH][i % DH] = i / DH < rows ? ((const float*)a.q)[row_at(i / DH) + i % DH] * a.scale_log2 : 0.f;
   __syncthreads();
   int pos[kRows];
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) pos[r] = r < rows ? sr.first + (rt * kRows + r) / G : -1;
+  for (int r = 0; r < kRows; ++r) pos[r] = r < rows ? sr.first + ((rt * kRows + r) >> a.g_sh) : -1;
 
   float m[kRows], l[kRows], acc[kRows][D];
 #pragma unroll
@@ -191,7 +190,7 @@ __global__ void __launch_bounds__(256) k_f32_merge(const F32Args f) {
   constexpr int D = (DH + 31) / 32;
   const AttnArgs& a = f.a;
   const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;         // kRows warps
-  const int rt = blockIdx.x, h = blockIdx.y, b = blockIdx.z, G = a.H / a.c.Hkv;
+  const int rt = blockIdx.x, h = blockIdx.y, b = blockIdx.z, G = 1 << a.g_sh;
   const SeqRange sr = seq_range(a, b);
   const int t = rt * kRows + r;
   if (t >= sr.nn * G) return;
@@ -228,7 +227,7 @@ __global__ void __launch_bounds__(256) k_f32_merge(const F32Args f) {
     }
     M = mx;
   }
-  float* out = (float*)a.o + (((size_t)b * a.n + t / G) * a.H + h * G + t % G) * DH;
+  float* out = (float*)a.o + (((size_t)b * a.n + (t >> a.g_sh)) * a.H + h * G + (t & (G - 1))) * DH;
 #pragma unroll
   for (int u = 0; u < D; ++u)
     if (DH >= 32 || lane < DH) out[lane + 32 * u] = L == 0.f ? 0.f : acc[u] / L;

@@ -73,7 +73,7 @@ template <int DH, bool E4> struct FewCfg {
   static constexpr uint32_t OFF_BAR = kStages * kStage;
   static constexpr uint32_t OFF_SC = OFF_BAR + kStages * 8;
   static constexpr uint32_t OFF_SEQ = OFF_SC + kStages * RUNS * 8;
-  static constexpr size_t smem(int B) { return OFF_SEQ + (size_t)B * 12 + 16 + 1024; }
+  static constexpr size_t smem(int B) { return OFF_SEQ + (size_t)B * 16 + 16 + 1024; }
 };
 
 // Address of 16-byte piece `c` (of 16 bytes along the row) of row `r` of a run.
@@ -124,7 +124,7 @@ struct FewArgs {
   int b0;                 // first sequence of this launch (a's tensors start at sequence 0)
   int B;                  // sequences of this launch
   int teams;
-  int* pre;               // [B + 1] first stage of each sequence, left for the merge
+  int2* ends;             // [B·P] teams of a pair's first and last stage, for the merge
   float* part;            // [teams + B·P][rows][DH + 4]
   int R;                  // rows of a KV head: n·G
   int rows;               // rows per pair
@@ -187,16 +187,18 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
   int* pre = reinterpret_cast<int*>(smem + C::OFF_SEQ);   // [B + 1] first stage of each sequence
   int* len_s = pre + f.B + 1;
   int* nn_s = len_s + f.B;
+  int* st_s = nn_s + f.B;                                 // stages of a pair
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * S;
   float2* sc = reinterpret_cast<float2*>(smem + C::OFF_SC) + warp * S * C::RUNS;
   __shared__ int abort_word, tmp[kWarps];
-  const int Hkv = a.c.Hkv, G = a.H / Hkv;
+  const int Hkv = a.c.Hkv, G = 1 << a.g_sh;
 
   for (int b = threadIdx.x; b < f.B; b += blockDim.x) {
     const SeqRange s = seq_range(a, f.b0 + b);
     len_s[b] = s.len;
     nn_s[b] = s.nn;
-    pre[b] = stages_of(a, s, C::RUNS) * f.P;
+    st_s[b] = stages_of(a, s, C::RUNS);
+    pre[b] = st_s[b] * f.P;
   }
   if (threadIdx.x == 0) {
     abort_word = 0;
@@ -207,8 +209,6 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
   scan_in_place(pre, f.B, tmp);
   volatile int* abort_flag = &abort_word;
   const int total = pre[f.B];
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b <= f.B; b += blockDim.x) f.pre[b] = pre[b];
   const int teams = min(f.teams, total);        // each of them has a stage at least
   const int team = warp * gridDim.x + blockIdx.x;
   const bool mine = team < teams;
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
     }
     Walk w;
     w.b = lo;                                   // the last with pre <= x: it has stages
-    w.n_st = (pre[lo + 1] - pre[lo]) / f.P;
+    w.n_st = st_s[lo];
     w.p = (x - pre[lo]) / w.n_st;
     w.st = (x - pre[lo]) % w.n_st;
     return w;
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
     if (++w.p < f.P) return;
     w.p = 0;
     do ++w.b; while (w.b < f.B && pre[w.b + 1] == pre[w.b]);
-    if (w.b < f.B) w.n_st = (pre[w.b + 1] - pre[w.b]) / f.P;
+    if (w.b < f.B) w.n_st = st_s[w.b];
   };
   auto runs_of = [&](int b) { return key_runs(len_s[b], len_s[b] - nn_s[b], a.window, a.sinks, kRun); };
 
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
             si = ppage;
           } else {
             ppage = (f.b0 + pw.b) * Hkv + h;
-            si = (long long)ppage * a.c.per + key / a.c.ps;
+            si = (long long)ppage * a.c.per + block_of(a.c, key);
           }
           if constexpr (E4) {
             pks = ppage < 0 ? 1.f : __ldg(a.c.ks + si);
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
       for (int r = 0; r < nr; ++r) {
         const int key = run_index(pr, r0 + r) * kRun;
         const int plane = __shfl_sync(0xffffffffu, ppage, r0 + r - pbase);
-        const int y = a.c.bt ? key % a.c.ps : key;
+        const int y = a.c.bt ? in_block(a.c, key) : key;
         const int z = plane < 0 ? a.c.num_pages * Hkv : plane;   // outside the pool: the copy reads zeros
         if (lane == 0) {
           uint8_t* dst = ring + sl * kStage + r * C::RUN;
@@ -339,11 +339,11 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
           const int ri = mt * NR + i, row = row0 + mt * 16 + g + 8 * i;
-          const int tok = row / G;
+          const int tok = row >> a.g_sh;
           const bool in = tok < nn;
           qpos[ri] = in ? first + tok : -1;
           const bf16* q = (const bf16*)a.q +
-                          (((size_t)(f.b0 + w.b) * a.n + (in ? tok : 0)) * a.H + h * G + row % G) * DH;
+                          (((size_t)(f.b0 + w.b) * a.n + (in ? tok : 0)) * a.H + h * G + (row & (G - 1))) * DH;
           m[ri] = -INFINITY;
           l[ri] = 0.f;
           zscale[ri] = a.scale_log2;
@@ -582,6 +582,9 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
     __syncwarp();                              // the slot may be refilled
     const bool pair_ends = w.st + 1 == w.n_st;
     if (pair_ends || x + 1 == x1) {            // this piece's state
+      int* e = reinterpret_cast<int*>(f.ends + w.b * f.P + w.p);
+      if (lane == 0 && x - w.st >= x0) e[0] = team;
+      if (lane == 0 && pair_ends) e[1] = team;
       const long long pc = (long long)team + (long long)w.b * f.P + w.p;
 #pragma unroll
       for (int ri = 0; ri < MT * NR; ++ri) {
@@ -633,23 +636,21 @@ __global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
   constexpr int D = DH / 32;
   const AttnArgs& a = f.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int G = a.H / a.c.Hkv;
+  const int G = 1 << a.g_sh;
   const int row = WIDE ? blockIdx.x : blockIdx.x * 8 + warp, h = blockIdx.y, b = blockIdx.z;
   const int tile = row >= f.rows, pair = h * f.tiles + tile;
-  const int total = f.pre[f.B], before = f.pre[b], n_st = (f.pre[b + 1] - before) / f.P;
-  const int nn = a.n_new ? min(max(a.n_new[f.b0 + b], 0), a.n) : a.n;
-  const int tok = row / G, head = h * G + row % G;
-  if (row >= f.R || tok >= nn) return;
+  if (row >= f.R) return;
+  const int2 ends = f.ends[b * f.P + pair];     // (unless the sequence is empty)
+  const SeqRange sr = seq_range(a, f.b0 + b);
+  const int tok = row >> a.g_sh, head = h * G + (row & (G - 1));
+  if (tok >= sr.nn) return;
   const size_t at = (((size_t)(f.b0 + b) * a.n + tok) * a.H + head) * DH;
   float M = -INFINITY, L = 0.f, acc[D];
 #pragma unroll
   for (int u = 0; u < D; ++u) acc[u] = 0.f;
-  if (n_st > 0) {                               // (no stages: no rows in the cache)
-    // team t has stages [total·t / teams, total·(t+1) / teams): those of the pair's first and last stage
-    const int teams = min(f.teams, total);
-    const long long U0 = before + (long long)pair * n_st, U1 = U0 + n_st;
-    const int t0 = (int)(((U0 + 1) * teams + total - 1) / total) - 1;
-    const int np = (int)((U1 * teams + total - 1) / total) - t0;
+  if (sr.len > 0) {
+    // (held to the teams: after a wait that ran out they may not have been written)
+    const int t0 = min(max(ends.x, 0), f.teams - 1), np = min(max(ends.y, t0), f.teams - 1) + 1 - t0;
     const float* p0 = f.part + ((t0 + (long long)b * f.P + pair) * f.rows + row - tile * f.rows) * (DH + 4);
     const size_t step = (size_t)f.rows * (DH + 4);
     const int i0 = WIDE ? np * warp / 8 : 0, i1 = WIDE ? np * (warp + 1) / 8 : np;
@@ -726,7 +727,6 @@ __global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
     probe = fmaf(acc[u], 0.f, probe);
   }
   if (__any_sync(0xffffffffu, !(probe == 0.f))) {        // not finite: see attend_row
-    const SeqRange sr = seq_range(a, f.b0 + b);
     attend_row<DH>(a, f.b0 + b, h, sr.first + tok, (const bf16*)a.q + at, acc);
     __syncwarp();
   }
@@ -736,8 +736,6 @@ __global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
   else
     *reinterpret_cast<uint32_t*>(out) = pack<false>(acc[0], acc[1]);
 }
-
-constexpr size_t kPreBytes = (kMaxB + 1) * 4 / 256 * 256 + 256;
 
 // How the rows of a KV head are dealt: pairs of `rows` rows, warps with `mt`
 // tiles of 16.  From 17 rows on a warp holds two tiles, so that a key is read and
@@ -763,6 +761,10 @@ int batch_of(const AttnArgs& a, const Deal& d) {
   return (int)std::min<long long>(std::min(a.c.B, kMaxB), std::max<long long>(1, (1LL << 30) / per));
 }
 
+size_t ends_bytes(const AttnArgs& a, const Deal& d) {
+  return ((size_t)batch_of(a, d) * a.c.Hkv * d.tiles * 8 + 255) / 256 * 256;
+}
+
 template <int DH, bool E4, int MT, bool LO>
 cudaError_t run(const AttnArgs& a, const Deal& d, void* ws, cudaStream_t s) {
   using C = FewCfg<DH, E4>;
@@ -785,14 +787,14 @@ cudaError_t run(const AttnArgs& a, const Deal& d, void* ws, cudaStream_t s) {
   }
   FewArgs f;
   f.a = a;
-  f.pre = (int*)ws;
-  f.part = (float*)((uint8_t*)ws + kPreBytes);
   f.R = a.n * (a.H / a.c.Hkv);
   f.rows = d.rows;
   f.tiles = d.tiles;
   f.P = a.c.Hkv * d.tiles;
   f.teams = sm_count() * d.warps;
   const int Bl = batch_of(a, d);
+  f.ends = (int2*)ws;
+  f.part = (float*)((uint8_t*)ws + ends_bytes(a, d));
   for (int b0 = 0; b0 < a.c.B; b0 += Bl) {
     f.b0 = b0;
     f.B = std::min(Bl, a.c.B - b0);
@@ -821,7 +823,7 @@ size_t cache_attn_few_workspace(const AttnArgs& a) {
   if (a.c.B == 0 || a.n == 0) return 0;
   const Deal d = deal_of(a);
   const long long pieces = (long long)sm_count() * d.warps + (long long)batch_of(a, d) * a.c.Hkv * d.tiles;
-  return kPreBytes + (size_t)pieces * d.rows * (a.c.dh + 4) * 4;
+  return ends_bytes(a, d) + (size_t)pieces * d.rows * (a.c.dh + 4) * 4;
 }
 
 cudaError_t launch_cache_attn_few(const AttnArgs& a, void* ws, cudaStream_t s) {

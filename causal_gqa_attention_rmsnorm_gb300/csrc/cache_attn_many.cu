@@ -518,7 +518,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
       auto page_ahead = [&](int x) {
         if (x >= pc.t1 || !mine) return -1;
         const int key = it.tile(x) * kBN + lane * unit;
-        return a.c.bt && seen_at(key, unit) ? a.c.bt[(size_t)pc.at.b * a.c.per + key / a.c.ps] : 0;
+        return a.c.bt && seen_at(key, unit) ? a.c.bt[(size_t)pc.at.b * a.c.per + block_of(a.c, key)] : 0;
       };
       // the plane of a tile's keys (-1: not read), and the block scales
       auto plane_of = [&](int x, int page, float& ks, float& vs) {
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         const int key = it.tile(x) * kBN + lane * unit;
         if (!seen_at(key, unit)) return -1;
         int plane = pc.at.b * a.c.Hkv + pc.at.h;
-        size_t si = (size_t)plane * a.c.per + (E4 ? key / a.c.ps : 0);
+        size_t si = (size_t)plane * a.c.per + (E4 ? block_of(a.c, key) : 0);
         if (a.c.bt) {
           if (page < 0 || page >= a.c.num_pages) {
             atomicOr(err, TB_DEVERR_BAD_PAGE);
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         plane1 = plane_of(x + 1, page2, ks1, vs1);
         page2 = page_ahead(x + 2);
         const bool want = plane >= 0;
-        const int y = a.c.bt ? key % a.c.ps : key;
+        const int y = a.c.bt ? in_block(a.c, key) : key;
         // Boxes of `box` keys: lane i issues the box that its keys begin (E4: its
         // run of 16; a box is issued if any of its runs is wanted, from the page of
         // that run - all runs of a box lie in one page)
