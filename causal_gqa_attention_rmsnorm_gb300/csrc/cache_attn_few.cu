@@ -18,13 +18,17 @@
 //   Lane 0 issues the copies; page ids and block scales are fetched 32 runs at a
 //   time by the warp, so no copy waits for a table look-up.
 //
-//   Products (m16n8k16, fp32 sums): S[16 x 16 keys] = Q·Kᵀ, O[16 x dh] += P·V,
-//   P straight from S's accumulators.  bf16: K by ldmatrix, V by
-//   ldmatrix.trans.  e4m3: the codes become fp16 exactly (cvt.f16x2.e4m3x2).
-//   ldmatrix on 16-bit units hands a lane four consecutive dims of a key, which
-//   serve as the k pairs (2t, 2t+1) and (2t+8, 2t+9) in both operands - a dot
-//   product does not care which; ldmatrix.trans hands it two keys of two dims,
-//   which one byte permutation sorts into an even-dim and an odd-dim fragment.
+//   Products (m16n8k16, fp32 sums): S[16 rows x 16 keys] = Q·Kᵀ, O[16 x dh] +=
+//   P·V, P straight from S's accumulators.  Up to eight rows the rows are the
+//   narrow side instead, Sᵀ[16 keys x 8] = K·Qᵀ, Oᵀ[dh x 8] += Vᵀ·Pᵀ with Pᵀ's
+//   8 x 8 quarters transposed between lanes: half the MMAs and half the registers
+//   for O (e4m3, 32 sequences of a 16k cache 96 -> 94 us, one of 64k 35 -> 33).
+//   bf16: K by ldmatrix, V by ldmatrix.trans.  e4m3: the codes become fp16 exactly
+//   (cvt.f16x2.e4m3x2).  ldmatrix on 16-bit units hands a lane four consecutive
+//   dims of a key, which serve as the k pairs (2t, 2t+1) and (2t+8, 2t+9) in both
+//   operands - a dot product does not care which; ldmatrix.trans hands it two keys
+//   of two dims, which one byte permutation sorts into an even-dim and an odd-dim
+//   fragment.
 //   Queries enter as fp16 under a power of two per row that brings their
 //   largest element into [0.5, 1).  (8-bit warp-level MMAs on the K codes, with the
 //   queries split as for the tensor-memory kernel, ran slower: 108 against 100 us
@@ -32,6 +36,12 @@
 //   A V block's scale 2^e is never multiplied in: p' = 2^(z + e - m') carries
 //   it, O = Σ p'·code, l = Σ p'·2^-e, and the running maximum is that of z + e,
 //   so p' stays in fp16 whatever the scales.
+//
+// Measured (8 KV heads of 128, 4 query heads each, one token): 32 sequences,
+// bf16, window 4096: 82.5 us, 0.88 of the copy bandwidth; 32 sequences of up to 16k
+// over e4m3 94.3 us, 0.89; one of 64k over e4m3 33 us, 0.59, of which some 9 us are
+// the two launches and their dependent reads (what a call of one short sequence
+// takes).  7 tokens of 8 sequences, window 2048, e4m3: 27.4 us.
 #include <math.h>
 
 #include <algorithm>
@@ -50,14 +60,15 @@ constexpr uint32_t kStage = 8192;             // K then V bytes of one stage
 constexpr int kMaxB = 1024;                   // sequences per launch
 constexpr float kRescale = 8.f;               // rescale O only when the maximum grows by more than 2^8
 
-// Warps of a CTA and stages per warp, by 16-row tiles MT of a warp (LO: half a
-// tile, up to eight rows).  The e4m3 form of up to eight rows spends more
-// instructions per byte and fewer registers: twelve warps hide its latencies
-// better than eight (107 against 125 us for 32 sequences of a 16k cache).  With
-// two tiles the queries lie in shared memory, in the room of the third stage.
-template <bool E4, int MT, bool LO> struct FewShape {
-  static constexpr int WARPS = E4 && LO ? 12 : 8;
-  static constexpr int SLOTS = (E4 && LO) || MT == 2 ? 2 : 3;
+// Warps of a CTA and stages per warp, by 16-row tiles MT of a warp (LO: up to
+// eight rows).  What costs time beside the reads is the latency of a warp's own
+// instructions, so a CTA has as many warps as the registers allow: with LO twelve
+// (e4m3, 32 sequences of a 16k cache: 110 us with ten, 101 with eleven, 96 with
+// twelve; thirteen would leave 128 registers, and spill: 162).  With two tiles the
+// queries lie in shared memory, in the room of the third stage.
+template <int MT, bool LO> struct FewShape {
+  static constexpr int WARPS = LO ? 12 : 8;
+  static constexpr int SLOTS = LO || MT == 2 ? 2 : 3;
 };
 constexpr int kStages = 24;
 
@@ -109,6 +120,12 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit elements (a lane holds [g][2t, 2t + 1]) transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 template <bool E4>
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -171,14 +188,16 @@ __device__ __forceinline__ void scan_in_place(int* pre, int n, int* tmp) {
 }
 
 template <int DH, bool E4, int MT, bool LO>
-__global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
+__global__ void __launch_bounds__((FewShape<MT, LO>::WARPS * 32), 1)
     k_attn_few(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const FewArgs f) {
   pdl_trigger();
   pdl_wait();
   using C = FewCfg<DH, E4>;
-  constexpr int kWarps = FewShape<E4, MT, LO>::WARPS;
-  constexpr int S = FewShape<E4, MT, LO>::SLOTS;
-  constexpr int NR = LO ? 1 : 2;                // rows of a lane and tile: g, and g + 8
+  constexpr int kWarps = FewShape<MT, LO>::WARPS;
+  constexpr int S = FewShape<MT, LO>::SLOTS;
+  constexpr int NQ = LO ? 1 : 2;                // query rows of a lane and tile as operand: g, and g + 8
+  constexpr int NR = LO ? 2 : MT * 2;           // rows of a lane as result: 2t and 2t + 1, or g and g + 8 of each tile
+  constexpr int NE = LO ? 2 : 4;                // keys of a run in a lane's rows
   static_assert(MT == 1 || !LO, "half a tile stands alone");
   const AttnArgs& a = f.a;
   extern __shared__ uint8_t smem_raw[];
@@ -310,12 +329,14 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
 
   // ---- consumer ----
   const int mi = lane >> 3;
-  // A fragments of the queries: registers, or with two tiles shared memory
-  uint32_t qa[MT == 1 ? DH / 16 : 1][2 * NR];
+  // Fragments of the queries: registers, or with two tiles shared memory
+  uint32_t qa[MT == 1 ? DH / 16 : 1][2 * NQ];
   const uint32_t q_s = smem_u32(smem + C::OFF_Q) + (uint32_t)(warp * (2 * DH / 16) * 32 + lane) * 16;
-  float o[MT][DH / 8][4];                      // (with eight rows the upper half stays 0)
-  float m[MT * NR], l[MT * NR], zscale[MT * NR];
-  int qpos[MT * NR];                           // position of the lane's rows; -1: none
+  constexpr int NO = LO ? DH / 16 : DH / 8;
+  float o[MT][NO][4];
+  float m[NR], l[NR], zscale[NR];
+  int qpos[NR];                                // position of the lane's rows; -1: none
+  auto row_of = [&](int ri) { return LO ? 2 * t + ri : ri / 2 * 16 + g + 8 * (ri % 2); };
   Walk w{};
   KeyRuns kr{};
   int len = 0, first = 0, last = 0;
@@ -334,24 +355,27 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
       last = len - 1;
       const int h = w.p >> (f.tiles - 1), row0 = (w.p & (f.tiles - 1)) * f.rows;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        uint32_t fr_[DH / 16][2 * NR];
+      for (int ri = 0; ri < NR; ++ri) {
+        const int tok = (row0 + row_of(ri)) >> a.g_sh;
+        qpos[ri] = tok < nn ? first + tok : -1;
+        m[ri] = -INFINITY;
+        l[ri] = 0.f;
+        zscale[ri] = a.scale_log2;
+      }
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          const int ri = mt * NR + i, row = row0 + mt * 16 + g + 8 * i;
-          const int tok = row >> a.g_sh;
+      for (int mt = 0; mt < MT; ++mt) {
+        uint32_t fr_[DH / 16][2 * NQ];
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          const int row = row0 + mt * 16 + g + 8 * i, tok = row >> a.g_sh;
           const bool in = tok < nn;
-          qpos[ri] = in ? first + tok : -1;
           const bf16* q = (const bf16*)a.q +
                           (((size_t)(f.b0 + w.b) * a.n + (in ? tok : 0)) * a.H + h * G + (row & (G - 1))) * DH;
-          m[ri] = -INFINITY;
-          l[ri] = 0.f;
-          zscale[ri] = a.scale_log2;
           if constexpr (!E4) {
 #pragma unroll
             for (int p = 0; p < DH / 16; ++p) {
               fr_[p][i] = in ? *reinterpret_cast<const uint32_t*>(q + 16 * p + 2 * t) : 0u;
-              fr_[p][NR + i] = in ? *reinterpret_cast<const uint32_t*>(q + 16 * p + 8 + 2 * t) : 0u;
+              fr_[p][NQ + i] = in ? *reinterpret_cast<const uint32_t*>(q + 16 * p + 8 + 2 * t) : 0u;
             }
           } else {
             float amax = 0.f;
@@ -364,12 +388,17 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
             }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const float fr = pow2_frame(amax);
-            zscale[ri] = a.scale_log2 / fr;    // exact
+            const float fr = pow2_frame(amax), zs = a.scale_log2 / fr;         // exact
+            if constexpr (LO) {                // (this lane's row g, wanted for rows 2t and 2t + 1)
+              zscale[0] = __shfl_sync(0xffffffffu, zs, 8 * t);
+              zscale[1] = __shfl_sync(0xffffffffu, zs, 8 * t + 4);
+            } else {
+              zscale[2 * mt + i] = zs;
+            }
 #pragma unroll
             for (int p = 0; p < DH / 16; ++p) {
               fr_[p][i] = pack<true>(__uint_as_float(raw[p].x << 16) * fr, __uint_as_float(raw[p].x & 0xffff0000u) * fr);
-              fr_[p][NR + i] = pack<true>(__uint_as_float(raw[p].y << 16) * fr, __uint_as_float(raw[p].y & 0xffff0000u) * fr);
+              fr_[p][NQ + i] = pack<true>(__uint_as_float(raw[p].y << 16) * fr, __uint_as_float(raw[p].y & 0xffff0000u) * fr);
             }
           }
         }
@@ -377,14 +406,14 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
 #pragma unroll
           for (int p = 0; p < DH / 16; ++p)
 #pragma unroll
-            for (int j = 0; j < 2 * NR; ++j) qa[p][j] = fr_[p][j];
+            for (int j = 0; j < 2 * NQ; ++j) qa[p][j] = fr_[p][j];
         } else {
 #pragma unroll
           for (int p = 0; p < DH / 16; ++p)
-            sts128(q_s + (mt * (DH / 16) + p) * 512, make_uint4(fr_[p][0], fr_[p][1], fr_[p][NR], fr_[p][2 * NR - 1]));
+            sts128(q_s + (mt * (DH / 16) + p) * 512, make_uint4(fr_[p][0], fr_[p][1], fr_[p][NQ], fr_[p][2 * NQ - 1]));
         }
 #pragma unroll
-        for (int i = 0; i < DH / 8; ++i)
+        for (int i = 0; i < NO; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[mt][i][j] = 0.f;
       }
@@ -395,39 +424,50 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
     }
     const uint32_t kb0 = smem_u32(ring + sl * kStage), vb0 = kb0 + C::HALF;
     const int r0 = w.st * C::RUNS, nr = min(C::RUNS, kr.count - r0);
-    // Scores of the stage's runs, z[run][8-key tile][row tile][row i: keys 2t, 2t+1]
-    float z[C::RUNS][2][MT][4];
+    // Scores of the stage's runs: zat(run, row, e) is key koff(e) of the run
+    float z[C::RUNS][LO ? 1 : 2][MT][4];
+    auto zat = [&](int r, int ri, int e) -> float& {
+      return LO ? z[r][0][0][2 * e + ri] : z[r][LO ? 0 : e >> 1][ri / 2][2 * (ri % 2) + (e & 1)];
+    };
+    auto koff = [&](int e) { return LO ? 8 * e + g : 8 * (e >> 1) + 2 * t + (e & 1); };
 #pragma unroll
     for (int r = 0; r < C::RUNS; ++r)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int ri = 0; ri < NR; ++ri)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) z[r][h][mt][j] = 0.f;
+        for (int e = 0; e < NE; ++e) zat(r, ri, e) = 0.f;
     constexpr int PS = E4 ? 2 : 1;             // 16-dim slices per step: an ldmatrix holds that many
     auto step = [&](int r, int p, const uint32_t(&qf)[PS][MT][4]) {
       const uint32_t kb = kb0 + r * C::RUN;
       uint32_t b[4];
       if constexpr (!E4) {
         ldsm4(piece<DH, E4>(kb, 8 * (mi >> 1) + (lane & 7), 2 * p + (mi & 1)), b);
+        if constexpr (LO) {
+          mma<E4>(z[r][0][0], b[0], b[2], b[1], b[3], qf[0][0][0], qf[0][0][2]);
+        } else {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma<E4>(z[r][0][mt], qf[0][mt][0], qf[0][mt][1], qf[0][mt][2], qf[0][mt][3], b[0], b[1]);
-          mma<E4>(z[r][1][mt], qf[0][mt][0], qf[0][mt][1], qf[0][mt][2], qf[0][mt][3], b[2], b[3]);
+          for (int mt = 0; mt < MT; ++mt) {
+            mma<E4>(z[r][0][mt], qf[0][mt][0], qf[0][mt][1], qf[0][mt][2], qf[0][mt][3], b[0], b[1]);
+            mma<E4>(z[r][1][mt], qf[0][mt][0], qf[0][mt][1], qf[0][mt][2], qf[0][mt][3], b[2], b[3]);
+          }
         }
       } else {
         ldsm4(piece<DH, E4>(kb, 8 * (mi & 1) + (lane & 7), p + (mi >> 1)), b);
 #pragma unroll
-        for (int u = 0; u < PS; ++u)
+        for (int u = 0; u < PS; ++u) {
+          uint32_t lo[2], hi[2];               // keys 0..7, 8..15
+          codes4(b[2 * u], lo[0], hi[0]);
+          codes4(b[2 * u + 1], lo[1], hi[1]);
+          if constexpr (LO) {
+            mma<E4>(z[r][0][0], lo[0], lo[1], hi[0], hi[1], qf[u][0][0], qf[u][0][2]);
+          } else {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t lo, hi;
-            codes4(b[2 * u + h], lo, hi);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              mma<E4>(z[r][h][mt], qf[u][mt][0], qf[u][mt][1], qf[u][mt][2], qf[u][mt][3], lo, hi);
+              for (int mt = 0; mt < MT; ++mt)
+                mma<E4>(z[r][h][mt], qf[u][mt][0], qf[u][mt][1], qf[u][mt][2], qf[u][mt][3], lo[h], hi[h]);
           }
+        }
       }
     };
     if constexpr (MT == 2) {
@@ -458,10 +498,11 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
           uint32_t qf[PS][MT][4];
 #pragma unroll
           for (int u = 0; u < PS; ++u) {
-            qf[u][0][0] = qa[MT == 1 ? p + u : 0][0];
-            qf[u][0][1] = LO ? 0u : qa[MT == 1 ? p + u : 0][NR - 1];
-            qf[u][0][2] = qa[MT == 1 ? p + u : 0][NR];
-            qf[u][0][3] = LO ? 0u : qa[MT == 1 ? p + u : 0][2 * NR - 1];
+            const int pu = MT == 1 ? p + u : 0;
+            qf[u][0][0] = qa[pu][0];
+            qf[u][0][1] = qa[pu][NQ - 1];      // (LO: not used, nor [3])
+            qf[u][0][2] = qa[pu][NQ];
+            qf[u][0][3] = qa[pu][2 * NQ - 1];
           }
           step(r, p, qf);
         }
@@ -481,23 +522,18 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
       const bool all = r < nr && key + kRun - 1 <= first &&
                        (a.window == 0 || key >= win_lo(last, a.window) || key + kRun <= a.sinks);
 #pragma unroll
-      for (int ri = 0; ri < MT * NR; ++ri) {
-        const int mt = ri / NR, i = ri % NR;
+      for (int ri = 0; ri < NR; ++ri) {
         const float zs = E4 ? zscale[ri] * ks : zscale[ri];
 #pragma unroll
-        for (int j = 2 * i; j < 2 * i + 2; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) z[r][h][mt][j] = E4 ? fmaf(z[r][h][mt][j], zs, ve) : z[r][h][mt][j] * zs;
+        for (int e = 0; e < NE; ++e) zat(r, ri, e) = E4 ? fmaf(zat(r, ri, e), zs, ve) : zat(r, ri, e) * zs;
         if (!all) {
           const int lo = win_lo(qpos[ri], a.window);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int kk = key + 8 * h + 2 * t + j;
-              const bool see = r < nr && kk <= qpos[ri] && (kk >= lo || kk < a.sinks);
-              if (!see) z[r][h][mt][2 * i + j] = -INFINITY;
-            }
+          for (int e = 0; e < NE; ++e) {
+            const int kk = key + koff(e);
+            const bool see = r < nr && kk <= qpos[ri] && (kk >= lo || kk < a.sinks);
+            if (!see) zat(r, ri, e) = -INFINITY;
+          }
         }
       }
       // v rows that no query of the call sees: 0·NaN is NaN inside an MMA
@@ -517,22 +553,21 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
     }
     // online softmax
 #pragma unroll
-    for (int ri = 0; ri < MT * NR; ++ri) {
-      const int mt = ri / NR, i = ri % NR;
+    for (int ri = 0; ri < NR; ++ri) {
       float mx = -INFINITY;
 #pragma unroll
       for (int r = 0; r < C::RUNS; ++r)
-        mx = fmaxf(mx, fmaxf(fmaxf(z[r][0][mt][2 * i], z[r][0][mt][2 * i + 1]),
-                             fmaxf(z[r][1][mt][2 * i], z[r][1][mt][2 * i + 1])));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+#pragma unroll
+        for (int e = 0; e < NE; ++e) mx = fmaxf(mx, zat(r, ri, e));
+#pragma unroll
+      for (int d = LO ? 4 : 1; d < (LO ? 32 : 4); d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
       if (mx > m[ri] + kRescale || (m[ri] == -INFINITY && mx > -INFINITY)) {
         const float fac = ex2_approx(m[ri] - mx);         // 0 from -inf
         l[ri] *= fac;
 #pragma unroll
-        for (int d = 0; d < DH / 8; ++d) {
-          o[mt][d][2 * i] *= fac;
-          o[mt][d][2 * i + 1] *= fac;
+        for (int d = 0; d < NO; ++d) {
+          o[LO ? 0 : ri / 2][d][LO ? ri : 2 * (ri % 2)] *= fac;
+          o[LO ? 0 : ri / 2][d][LO ? 2 + ri : 2 * (ri % 2) + 1] *= fac;
         }
         m[ri] = mx;
       }
@@ -540,19 +575,28 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
 #pragma unroll
     for (int r = 0; r < C::RUNS; ++r) {
       if (r >= nr) break;
+      // P as an operand: rows by keys, or (LO) keys by rows, its 8 x 8 quarters transposed
       uint32_t pa[MT][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) pa[mt][1] = pa[mt][3] = 0u;
-#pragma unroll
-      for (int ri = 0; ri < MT * NR; ++ri) {
-        const int mt = ri / NR, i = ri % NR;
+      for (int ri = 0; ri < NR; ++ri) {
         const float base = m[ri] == -INFINITY ? 0.f : m[ri];
-        const float p0 = ex2_approx(z[r][0][mt][2 * i] - base), p1 = ex2_approx(z[r][0][mt][2 * i + 1] - base);
-        const float p2 = ex2_approx(z[r][1][mt][2 * i] - base), p3 = ex2_approx(z[r][1][mt][2 * i + 1] - base);
-        const float sum = (p0 + p1) + (p2 + p3);
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+          zat(r, ri, e) = ex2_approx(zat(r, ri, e) - base);
+          sum += zat(r, ri, e);
+        }
         l[ri] = E4 ? fmaf(sum, scale_inv(vsc[r]), l[ri]) : l[ri] + sum;
-        pa[mt][i] = pack<E4>(p0, p1);
-        pa[mt][2 + i] = pack<E4>(p2, p3);
+      }
+      if constexpr (LO) {
+        pa[0][0] = transpose8(pack<E4>(zat(r, 0, 0), zat(r, 1, 0)));
+        pa[0][1] = transpose8(pack<E4>(zat(r, 0, 1), zat(r, 1, 1)));
+      } else {
+#pragma unroll
+        for (int ri = 0; ri < NR; ++ri) {
+          pa[ri / 2][ri % 2] = pack<E4>(zat(r, ri, 0), zat(r, ri, 1));
+          pa[ri / 2][2 + ri % 2] = pack<E4>(zat(r, ri, 2), zat(r, ri, 3));
+        }
       }
       const uint32_t vb = vb0 + r * C::RUN;
       const int row = 8 * (mi & 1) + (lane & 7);
@@ -560,20 +604,30 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
       for (int c = 0; c < (E4 ? DH / 16 : DH / 8); c += 2) {
         uint32_t b[4];
         ldsm4t(piece<DH, E4>(vb, row, c + (mi >> 1)), b);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if constexpr (!E4) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              mma<E4>(o[mt][c + u], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], b[2 * u], b[2 * u + 1]);
+        if constexpr (!E4) {
+          if constexpr (LO) {                  // dims 8c + g, 8c + 8 + g
+            mma<E4>(o[0][c / 2], b[0], b[2], b[1], b[3], pa[0][0], pa[0][1]);
           } else {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                mma<E4>(o[mt][LO ? 0 : c + u], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], b[2 * u], b[2 * u + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
             uint32_t e0, o0, e1, o1;           // even and odd dims; keys 0..7, 8..15
             codes4(__byte_perm(b[2 * u], 0, 0x3120), e0, o0);
             codes4(__byte_perm(b[2 * u + 1], 0, 0x3120), e1, o1);
+            if constexpr (LO) {                // dims 16(c + u) + 2g, + 2g + 1
+              mma<E4>(o[0][c + u], e0, o0, e1, o1, pa[0][0], pa[0][1]);
+            } else {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma<E4>(o[mt][2 * (c + u)], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], e0, e1);
-              mma<E4>(o[mt][2 * (c + u) + 1], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], o0, o1);
+              for (int mt = 0; mt < MT; ++mt) {
+                mma<E4>(o[mt][2 * (c + u)], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], e0, e1);
+                mma<E4>(o[mt][2 * (c + u) + 1], pa[mt][0], pa[mt][1], pa[mt][2], pa[mt][3], o0, o1);
+              }
             }
           }
         }
@@ -587,25 +641,40 @@ __global__ void __launch_bounds__((FewShape<E4, MT, LO>::WARPS * 32), 1)
       if (lane == 0 && pair_ends) e[1] = team;
       const long long pc = (long long)team + (long long)w.b * f.P + w.p;
 #pragma unroll
-      for (int ri = 0; ri < MT * NR; ++ri) {
-        const int mt = ri / NR, i = ri % NR;
+      for (int ri = 0; ri < NR; ++ri) {
         float ls = l[ri];
-        ls += __shfl_xor_sync(0xffffffffu, ls, 1);
-        ls += __shfl_xor_sync(0xffffffffu, ls, 2);
-        const int row = mt * 16 + g + 8 * i;
+#pragma unroll
+        for (int d = LO ? 4 : 1; d < (LO ? 32 : 4); d <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+        const int row = row_of(ri);
         if (row >= f.rows) continue;
         float* dst = f.part + (pc * f.rows + row) * (DH + 4);
-        if constexpr (!E4) {
+        if constexpr (LO) {
 #pragma unroll
-          for (int d = 0; d < DH / 8; ++d)
-            *reinterpret_cast<float2*>(dst + 4 + 8 * d + 2 * t) = make_float2(o[mt][d][2 * i], o[mt][d][2 * i + 1]);
+          for (int c = 0; c < NO; ++c) {
+            if constexpr (E4) {
+              *reinterpret_cast<float2*>(dst + 4 + 16 * c + 2 * g) = make_float2(o[0][c][ri], o[0][c][2 + ri]);
+            } else {
+              dst[4 + 16 * c + g] = o[0][c][ri];
+              dst[4 + 16 * c + 8 + g] = o[0][c][2 + ri];
+            }
+          }
         } else {
+          const int mt = ri / 2, i = ri % 2;
+          if constexpr (!E4) {
 #pragma unroll
-          for (int c = 0; c < DH / 16; ++c)
-            *reinterpret_cast<float4*>(dst + 4 + 16 * c + 4 * t) = make_float4(
-                o[mt][2 * c][2 * i], o[mt][2 * c + 1][2 * i], o[mt][2 * c][2 * i + 1], o[mt][2 * c + 1][2 * i + 1]);
+            for (int d = 0; d < DH / 8; ++d)
+              *reinterpret_cast<float2*>(dst + 4 + 8 * d + 2 * t) =
+                  make_float2(o[mt][LO ? 0 : d][2 * i], o[mt][LO ? 0 : d][2 * i + 1]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < DH / 16; ++c) {
+              const int d = LO ? 0 : 2 * c;
+              *reinterpret_cast<float4*>(dst + 4 + 16 * c + 4 * t) =
+                  make_float4(o[mt][d][2 * i], o[mt][d + !LO][2 * i], o[mt][d][2 * i + 1], o[mt][d + !LO][2 * i + 1]);
+            }
+          }
         }
-        if (t == 0) *reinterpret_cast<float2*>(dst) = make_float2(m[ri], ls);
+        if ((LO ? g : t) == 0) *reinterpret_cast<float2*>(dst) = make_float2(m[ri], ls);
       }
     }
     if (pair_ends) {
@@ -748,11 +817,10 @@ struct Deal {
 };
 Deal deal_of(const AttnArgs& a) {
   const int R = a.n * (a.H / a.c.Hkv);
-  const bool e4 = a.c.dtype == TB_E4M3;
-  if (R <= 16) return {1, R, 1, e4 && R <= 8 ? FewShape<true, 1, true>::WARPS : FewShape<false, 1, false>::WARPS};
+  if (R <= 16) return {1, R, 1, R <= 8 ? FewShape<1, true>::WARPS : FewShape<1, false>::WARPS};
   const long long keys = a.window > 0 ? std::min<long long>(a.c.T, (long long)a.window + a.sinks + a.n) : a.c.T;
-  if (keys * a.c.B * a.c.Hkv <= 1 << 18) return {1, 16, 2, FewShape<false, 1, false>::WARPS};
-  return {2, R, 1, FewShape<false, 2, false>::WARPS};
+  if (keys * a.c.B * a.c.Hkv <= 1 << 18) return {1, 16, 2, FewShape<1, false>::WARPS};
+  return {2, R, 1, FewShape<2, false>::WARPS};
 }
 
 // Sequences per launch: the line's stage numbers stay below 2^30.
