@@ -145,6 +145,7 @@ tb_status tb_kvcache_append_rope(const tb_kvcache* kv, const tb_append_rows* row
   if (!rows->k || !rows->v) return report(TB_ERR_INVALID_ARG, "k and v must be non-NULL");
   if ((rows->q == nullptr) != (rows->q_out == nullptr)) return report(TB_ERR_INVALID_ARG, "q and q_out go together");
   if (rows->q && rows->H <= 0) return report(TB_ERR_INVALID_ARG, "H must be positive");
+  if (rows->q && rows->H > 65535) return report(TB_ERR_UNSUPPORTED, "at most 65535 query heads (%d)", rows->H);
   if (!aligned16(rows->q) || !aligned16(rows->q_out) || !aligned16(rows->k) || !aligned16(rows->v))
     return report(TB_ERR_INVALID_ARG, "q, q_out, k and v must be 16-byte aligned");
   const int64_t strides[6] = {rows->q_tok, rows->q_seq, rows->k_tok, rows->k_seq, rows->v_tok, rows->v_seq};

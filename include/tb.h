@@ -317,8 +317,8 @@ TB_API tb_status tb_stack_decode(const tb_block_cfg *cfg, int32_t L, const void 
  *    NaN are stored as NaN.  Scales that a caller writes itself have to be such
  *    powers of two.
  * TB_I8 caches are TB_ERR_UNSUPPORTED here, and so are dh that is no multiple of
- * 16 or above 256, B above 32767, Hkv above 65535, num_pages·Hkv above 2^31 - 2;
- * the block's calls take no TB_E4M3 cache. */
+ * 16 or above 256, B above 32767, H or Hkv above 65535, num_pages·Hkv above
+ * 2^31 - 2; the block's calls take no TB_E4M3 cache. */
 
 /* The rotation table of tb_kvcache_append_rope: table [max_pos, dh/2, 2] fp32
  * (device) receives (cos, sin) of t·base^(-2i/dh) for position t and pair i,

@@ -68,6 +68,7 @@ def test_append_refusals(lib):
     assert append(lib, cache(), q=None) == 1                     # q_out without q
     assert append(lib, cache(), q_out=None) == 1
     assert append(lib, cache(), H=0) == 1
+    assert append(lib, cache(), H=65536, q_tok=65536 * 64, q_seq=65536 * 64 * 4) == 2
     assert append(lib, cache(), v=FAKE + 2) == 1
     assert append(lib, cache(), k_tok=132) == 1                  # stride not a multiple of 8
     assert append(lib, cache(), v_seq=-128) == 1
@@ -119,6 +120,15 @@ def test_attention_workspace_is_checked(lib):
     if need:
         for ws, wsb in ((None, need), (FAKE, need - 1), (FAKE + 128, need)):
             assert lib.tb_kvcache_attn(ctypes.byref(c), FAKE, ctypes.byref(kv), None, 1, FAKE, ws, wsb, None) == 1
+
+
+def test_the_blocks_calls_take_no_e4m3_cache(lib):
+    kv = e4m3()
+    assert lib.tb_kvcache_append(ctypes.byref(kv), FAKE, FAKE, 1, None) == 1
+    c = binding.BlockConfig(d=128, H=2, Hkv=2, dh=64, f=256, max_pos=256, rope_base=1e4, eps=1e-6, dtype=tb.TB_BF16).c()
+    y = FAKE + (1 << 30)
+    assert lib.tb_block_decode(ctypes.byref(c), FAKE, FAKE, y, tb.TB_F32, ctypes.byref(kv), FAKE, 1 << 40, None) == 1
+    assert lib.tb_block_prefill(ctypes.byref(c), FAKE, FAKE, y, tb.TB_F32, 2, 16, ctypes.byref(kv), FAKE, 1 << 40, None) == 1
 
 
 @pytest.mark.parametrize("dtype", [tb.TB_F32, tb.TB_BF16, tb.TB_E4M3])
