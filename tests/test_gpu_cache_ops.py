@@ -412,6 +412,27 @@ def test_large_and_tiny_queries_over_e4m3(n):
     assert np.isfinite(o[:, 0]).all()
 
 
+@pytest.mark.parametrize("n", [1, 5, 12, 40, 200])
+def test_queries_with_one_large_element_over_e4m3(n):
+    """An element of a query row 1000 times the others.  Chunks multiply queries
+    as two 8-bit terms, which leaves an element off by at most 2^-17 of its row's
+    largest: a score by 2^-17 max|q| sum|k| scale, counted on top."""
+    tb = tbm()
+    L, dh = 300, 64
+    kv = make_cache("e4m3", False, 1, 2, 320, dh, 32, fill=0.0)
+    put_rows(kv, 0, rows(1, 2, L, dh), rows(2, 2, L, dh))
+    kv.k.view(torch.uint8)[..., 7] = 0                        # its dim is zero in the keys
+    kv.lens.fill_(L)
+    q = rows(5, 1, n, 4, dh)
+    q[..., 7] = 1000
+    q = q.to(torch.bfloat16).cuda()
+    o = tb.tb_kvcache_attn(tb.AttnConfig(H=4, Hkv=2, dh=dh), q, kv)[0].double().cpu().numpy()
+    k, v = values(kv, "k", 0)[:, :L], values(kv, "v", 0)[:, :L]
+    out, mag, top = ref.attend(q[0].double().cpu().numpy(), k, v, L - n)
+    off = 2.0 ** -17 * 1000 * np.abs(k).sum(-1).max() / math.sqrt(dh)
+    check_attention("e4m3", o, out, mag, top + off / ((dh + 6) * 2.0 ** -24), dh, L)
+
+
 def test_lens_above_capacity_counts_as_capacity():
     tb = tbm()
     kv = make_cache("bf16", False, 1, 2, 160, 64, 0, fill=0.0)
