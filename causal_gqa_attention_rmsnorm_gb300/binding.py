@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from ctypes import c_float, c_int32, c_int64, c_size_t, c_void_p
 from dataclasses import dataclass
@@ -69,6 +70,7 @@ class TbError(RuntimeError):
         self.status = status
 
 
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
 _lib = None
 
 
@@ -190,24 +192,27 @@ class KVCache:
     v_scale: Optional[torch.Tensor] = None
 
     def c(self) -> tb_kvcache:
-        for t in (self.k, self.v):
-            if not (t.is_cuda and t.is_contiguous()):
-                raise ValueError("cache tensors must be contiguous CUDA tensors")
-        if self.v.shape != self.k.shape or self.v.dtype != self.k.dtype:
+        k, v, lens, bt = self.k, self.v, self.lens, self.block_table
+        dev = k.get_device()
+        if dev < 0 or v.get_device() != dev or not (k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("cache tensors must be contiguous CUDA tensors on one device")
+        shape, dtype = k.shape, k.dtype
+        if v.shape != shape or v.dtype is not dtype:
             raise ValueError("k and v caches must match")
-        dt = _CACHE_DTYPES.get(self.k.dtype)
+        dt = _CACHE_DTYPES.get(dtype)
         if dt is None:
-            raise ValueError(f"cache dtype {self.k.dtype} is not float32, bfloat16, int8 or float8_e4m3fn")
-        if self.block_table is None:
-            B, Hkv, T_max, dh = self.k.shape
-            bt, ps, npages = None, 0, 0
+            raise ValueError(f"cache dtype {dtype} is not float32, bfloat16, int8 or float8_e4m3fn")
+        if bt is None:
+            B, Hkv, T_max, dh = shape
+            ps, npages = 0, 0
         else:
-            npages, Hkv, ps, dh = self.k.shape
-            bt = self.block_table
-            if not (bt.is_cuda and bt.dtype == torch.int32 and bt.dim() == 2 and bt.is_contiguous()):
+            npages, Hkv, ps, dh = shape
+            table = bt.shape
+            if not (bt.get_device() == dev and bt.dtype is _I32 and len(table) == 2 and bt.is_contiguous()):
                 raise ValueError("block_table must be a contiguous CUDA int32 tensor [B, pages per sequence]")
-            B, T_max = bt.shape[0], bt.shape[1] * ps
-        if not (self.lens.is_cuda and self.lens.dtype == torch.int32 and self.lens.numel() == B):
+            B, T_max = table
+            T_max *= ps
+        if not (lens.get_device() == dev and lens.dtype is _I32 and lens.numel() == B):
             raise ValueError("lens must be a CUDA int32 tensor of B entries")
         ks = vs = None
         if dt == TB_I8:
@@ -226,10 +231,9 @@ class KVCache:
                 ps, want = T_max // blocks, (B, Hkv, blocks)
             else:
                 want = (npages, Hkv)
-            _need(self.k_scale, "k_scale", torch.float32, want)
-            _need(self.v_scale, "v_scale", torch.float32, want)
-            ks, vs = self.k_scale.data_ptr(), self.v_scale.data_ptr()
-        return tb_kvcache(self.k.data_ptr(), self.v.data_ptr(), self.lens.data_ptr(), B, Hkv, T_max, dh, dt,
+            ks = _dense(self.k_scale, "k_scale", _F32, want, dev)
+            vs = _dense(self.v_scale, "v_scale", _F32, want, dev)
+        return tb_kvcache(k.data_ptr(), v.data_ptr(), lens.data_ptr(), B, Hkv, T_max, dh, dt,
                           None if bt is None else bt.data_ptr(), ps, npages, ks, vs)
 
     @property
@@ -575,6 +579,10 @@ class AttnConfig:
     dtype: int = TB_BF16     # of q and o
 
     def c(self) -> tb_attn_cfg:
+        return self._struct
+
+    @functools.cached_property
+    def _struct(self) -> tb_attn_cfg:
         return tb_attn_cfg(self.H, self.Hkv, self.dh, self.dtype, self.window, self.sinks, self.scale)
 
     @property
@@ -599,22 +607,29 @@ def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: in
 
 
 def _counts(t: Optional[torch.Tensor], name: str, B: int, dev: int) -> Optional[int]:
-    return None if t is None else _dense(t, name, torch.int32, (B,), dev)
+    if t is None:
+        return None
+    if t.dtype is _I32 and t.shape == (B,) and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _dense(t, name, _I32, (B,), dev)
 
 
 def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, B: int, n: int, heads: Optional[int], dh: int, dev: int):
     """Heads, token stride and sequence stride of rows [B, n, heads, dh] whose heads are dense."""
     shape = t.shape
-    if len(shape) != 4 or shape[0] != B or shape[1] != n or shape[3] != dh or (heads is not None and shape[2] != heads):
+    if len(shape) != 4:
+        raise ValueError(f"{name} must be [B, n, heads, dh], got {tuple(shape)}")
+    rows, toks, h, width = shape
+    if rows != B or toks != n or width != dh or (heads is not None and h != heads):
         raise ValueError(f"{name} must be [{B}, {n}, {'heads' if heads is None else heads}, {dh}], got {tuple(shape)}")
     if t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{name} must be {dtype} on cuda:{dev}, got {t.dtype} on {t.device}")
     seq, tok, head, one = t.stride()
-    if one != 1 or (head != dh and shape[2] > 1):
+    if one != 1 or (head != dh and h > 1):
         raise ValueError(f"a token's heads must be dense in {name}")
     if n == 1:
-        tok = shape[2] * dh
-    return shape[2], tok, seq if B > 1 else tok * n
+        tok = h * dh
+    return h, tok, seq if B > 1 else tok * n
 
 
 def tb_rope_table(dh: int, max_pos: int, base: float, device="cuda", stream=None) -> torch.Tensor:
@@ -636,14 +651,14 @@ def tb_kvcache_append_rope(kv: KVCache, k: torch.Tensor, v: torch.Tensor, rope: 
     [B]: how many of each sequence's n rows count."""
     kvs = kv.c()
     dev = kv.k.get_device()
-    row = torch.float32 if kvs.dtype == TB_F32 else torch.bfloat16
+    row = _F32 if kvs.dtype == TB_F32 else _BF16
     if k.dim() != 4:
         raise ValueError("k must be [B, n, Hkv, dh]")
-    B, n, dh = kvs.B, k.shape[1], kvs.dh
-    _, k_tok, k_seq = _heads(k, "k", row, B, n, kvs.Hkv, dh, dev)
-    _, v_tok, v_seq = _heads(v, "v", row, B, n, kvs.Hkv, dh, dev)
-    max_pos = rope.shape[0] if rope.dim() else 0
-    rope_ptr = _dense(rope, "rope", torch.float32, (max_pos, dh // 2, 2), dev)
+    B, n, Hkv, dh = kvs.B, k.size(1), kvs.Hkv, kvs.dh
+    _, k_tok, k_seq = _heads(k, "k", row, B, n, Hkv, dh, dev)
+    _, v_tok, v_seq = _heads(v, "v", row, B, n, Hkv, dh, dev)
+    max_pos = rope.size(0) if rope.dim() else 0
+    rope_ptr = _dense(rope, "rope", _F32, (max_pos, dh // 2, 2), dev)
     H, q_tok, q_seq, q_ptr, out_ptr = 0, 0, 0, None, None
     if q is not None:
         H, q_tok, q_seq = _heads(q, "q", row, B, n, None, dh, dev)
