@@ -130,6 +130,14 @@ def test_append(kind, paged, B, n, H, Hkv, dh, T, block, start, n_new):
             assert np.array_equal(bits(x)[other], was[other])
 
 
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("block,dh", [(128, 128), (512, 128), (144, 256), (1536, 48)])
+def test_append_into_large_blocks(paged, block, dh):
+    """e4m3 blocks of more rows than a CTA's threads hold at once, and sizes that are no power of two."""
+    T = 3 * block if block < 1536 else block
+    test_append("e4m3", paged, 2, T // 2 + 5, 6, 3, dh, T, block, (T // 2 - 7, 3), (T // 2 + 5, T // 2 - 40))
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_append_at_lens_equals_append_at_start(kind):
     """start=None reads the positions from lens; q may be rotated in place."""
