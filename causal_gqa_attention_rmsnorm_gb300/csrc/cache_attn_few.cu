@@ -38,10 +38,10 @@
 //   so p' stays in fp16 whatever the scales.
 //
 // Measured (8 KV heads of 128, 4 query heads each, one token): 32 sequences,
-// bf16, window 4096: 82.5 us, 0.88 of the copy bandwidth; 32 sequences of up to 16k
-// over e4m3 94.3 us, 0.89; one of 64k over e4m3 33 us, 0.59, of which some 9 us are
+// bf16, window 4096: 82.7 us, 0.88 of the copy bandwidth; 32 sequences of up to 16k
+// over e4m3 93.4 us, 0.90; one of 64k over e4m3 33 us, 0.59, of which some 9 us are
 // the two launches and their dependent reads (what a call of one short sequence
-// takes).  7 tokens of 8 sequences, window 2048, e4m3: 27.4 us.
+// takes).  7 tokens of 8 sequences, window 2048, e4m3: 27 us.
 #include <math.h>
 
 #include <algorithm>
@@ -231,8 +231,10 @@ __global__ void __launch_bounds__((FewShape<MT, LO>::WARPS * 32), 1)
   const int teams = min(f.teams, total);        // each of them has a stage at least
   const int team = warp * gridDim.x + blockIdx.x;
   const bool mine = team < teams;
-  const int x0 = mine ? (int)((long long)total * team / teams) : 0;
-  const int x1 = mine ? (int)((long long)total * (team + 1) / teams) : 0;
+  // [total·team / teams, total·(team + 1) / teams), in 32 bits (teams < 2^15)
+  const unsigned each = mine ? (unsigned)total / (unsigned)teams : 0, rest = mine ? total - each * teams : 0;
+  const int x0 = mine ? (int)(each * team + rest * team / teams) : 0;
+  const int x1 = mine ? (int)(each * (team + 1) + rest * (team + 1) / teams) : 0;
 
   auto enter = [&](int x) {                     // the walk's state at stage x < total
     int lo = 0, hi = f.B - 1;
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__((FewShape<MT, LO>::WARPS * 32), 1)
   KeyRuns kr{};
   int len = 0, first = 0, last = 0;
   bool ok = true;
-  if (x0 < x1) w = enter(x0);
+  w = pw;
   bool fresh = true;
   for (int x = x0; x < x1; ++x) {
     produce(x);
