@@ -228,7 +228,11 @@ __global__ void __launch_bounds__((FewShape<MT, LO>::WARPS * 32), 1)
   scan_in_place(pre, f.B, tmp);
   volatile int* abort_flag = &abort_word;
   const int total = pre[f.B];
-  const int teams = min(f.teams, total);        // each of them has a stage at least
+  // Each team has a stage at least.  With s stages in a pair a call waits for s / t
+  // of them and for t pieces in the merge, so teams beyond some multiple of sqrt(s)
+  // per pair only cost: one sequence of 64k, one KV head, e4m3 21.8 us without the
+  // limit, 16.5 with 16 sqrt(s) as with 12, 18.4 with 9.
+  const int teams = min(min(f.teams, total), (int)(16.f * sqrtf((float)total * (float)(f.B * f.P))) + 1);
   const int team = warp * gridDim.x + blockIdx.x;
   const bool mine = team < teams;
   // [total·team / teams, total·(team + 1) / teams), in 32 bits (teams < 2^15)
@@ -696,19 +700,20 @@ __global__ void __launch_bounds__((FewShape<MT, LO>::WARPS * 32), 1)
 
 // Joins the pieces of a row of a pair: o = Σ w_i O_i / Σ w_i l_i,
 // w_i = 2^(m_i - M), in the order of the teams.  One warp per row, or with many
-// pieces (WIDE) eight warps, each a run of them, whose results are joined the same
-// way.  A lane holds DH/32 consecutive dims.  Latency counts here: eight pieces are
-// loaded at a time, under a running maximum (a pass for the maximum before it would
-// wait for memory twice).
-template <int DH, bool WIDE>
-__global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
+// pieces W, each a run of them, whose results are joined the same way (one
+// sequence of 64k over e4m3: eight warps 33.1 us, 32 29.8; with one KV head 46.7
+// and 21.8).  A lane holds DH/32 consecutive dims.  Latency counts here: eight
+// pieces are loaded at a time, under a running maximum (a pass for the maximum
+// before it would wait for memory twice).
+template <int DH, int W>
+__global__ void __launch_bounds__(W == 1 ? 256 : 32 * W) k_few_merge(const FewArgs f) {
   pdl_trigger();
   pdl_wait();
   constexpr int D = DH / 32;
   const AttnArgs& a = f.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = 1 << a.g_sh;
-  const int row = WIDE ? blockIdx.x : blockIdx.x * 8 + warp, h = blockIdx.y, b = blockIdx.z;
+  const int row = W > 1 ? blockIdx.x : blockIdx.x * 8 + warp, h = blockIdx.y, b = blockIdx.z;
   const int tile = row >= f.rows, pair = h * f.tiles + tile;
   if (row >= f.R) return;
   const int2 ends = f.ends[b * f.P + pair];     // (unless the sequence is empty)
@@ -724,7 +729,7 @@ __global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
     const int t0 = min(max(ends.x, 0), f.teams - 1), np = min(max(ends.y, t0), f.teams - 1) + 1 - t0;
     const float* p0 = f.part + ((t0 + (long long)b * f.P + pair) * f.rows + row - tile * f.rows) * (DH + 4);
     const size_t step = (size_t)f.rows * (DH + 4);
-    const int i0 = WIDE ? np * warp / 8 : 0, i1 = WIDE ? np * (warp + 1) / 8 : np;
+    const int i0 = W > 1 ? np * warp / W : 0, i1 = W > 1 ? np * (warp + 1) / W : np;
     constexpr int U = 8;                        // pieces in flight
     for (int i = i0; i < i1; i += U) {
       float2 ml[U];
@@ -762,8 +767,9 @@ __global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
       }
       M = mx;
     }
-    if constexpr (WIDE) {
-      __shared__ float m_s[8], l_s[8], acc_s[8][DH];
+    if constexpr (W > 1) {
+      __shared__ float m_s[W], l_s[W];
+      __shared__ __align__(16) float acc_s[W][DH];
       if (lane == 0) {
         m_s[warp] = M;
         l_s[warp] = L;
@@ -772,22 +778,24 @@ __global__ void __launch_bounds__(256) k_few_merge(const FewArgs f) {
       for (int u = 0; u < D; ++u) acc_s[warp][lane * D + u] = acc[u];
       __syncthreads();
       if (warp > 0) return;
-      M = m_s[lane & 7];
+      const float m = lane < W ? m_s[lane] : -INFINITY;
+      M = m;
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float all = M == -INFINITY ? 0.f : M;
-      L = 0.f;
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float w = ex2_approx(m - (M == -INFINITY ? 0.f : M));
+      L = lane < W ? w * l_s[lane] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
 #pragma unroll
       for (int u = 0; u < D; ++u) acc[u] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float w = ex2_approx(m_s[i] - all);
-        L = fmaf(l_s[i], w, L);
+      for (int i = 0; i < W; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
 #pragma unroll
-        for (int u = 0; u < D; ++u) acc[u] = fmaf(acc_s[i][lane * D + u], w, acc[u]);
+        for (int u = 0; u < D; ++u) acc[u] = fmaf(acc_s[i][lane * D + u], wi, acc[u]);
       }
     }
-  } else if (WIDE && warp > 0) {
+  } else if (W > 1 && warp > 0) {
     return;
   }
   const float inv = L == 0.f ? 0.f : 1.0f / L;
@@ -870,11 +878,14 @@ cudaError_t run(const AttnArgs& a, const Deal& d, void* ws, cudaStream_t s) {
     f.B = std::min(Bl, a.c.B - b0);
     e = launch_pdl(k_attn_few<DH, E4, MT, LO>, dim3(sm_count()), dim3(d.warps * 32), C::smem(f.B), s, tk, tv, f);
     if (e != cudaSuccess) return e;
-    // eight warps per row from 16 pieces of a pair on (at equal lengths)
-    if (f.teams >= 16 * f.B * f.P)
-      e = launch_pdl(k_few_merge<DH, true>, dim3(f.R, a.c.Hkv, f.B), dim3(256), 0, s, f);
+    // warps per row by the pieces of a pair, at equal lengths
+    const long long pairs = (long long)f.B * f.P;
+    if (f.teams >= 64 * pairs)
+      e = launch_pdl(k_few_merge<DH, 32>, dim3(f.R, a.c.Hkv, f.B), dim3(1024), 0, s, f);
+    else if (f.teams >= 16 * pairs)
+      e = launch_pdl(k_few_merge<DH, 8>, dim3(f.R, a.c.Hkv, f.B), dim3(256), 0, s, f);
     else
-      e = launch_pdl(k_few_merge<DH, false>, dim3((f.R + 7) / 8, a.c.Hkv, f.B), dim3(256), 0, s, f);
+      e = launch_pdl(k_few_merge<DH, 1>, dim3((f.R + 7) / 8, a.c.Hkv, f.B), dim3(256), 0, s, f);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
