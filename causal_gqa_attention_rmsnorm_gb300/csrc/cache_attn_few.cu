@@ -39,7 +39,7 @@
 //
 // Measured (8 KV heads of 128, 4 query heads each, one token): 32 sequences,
 // bf16, window 4096: 82.7 us, 0.88 of the copy bandwidth; 32 sequences of up to 16k
-// over e4m3 93.4 us, 0.90; one of 64k over e4m3 33 us, 0.59, of which some 9 us are
+// over e4m3 95 us, 0.89; one of 64k over e4m3 30 us, 0.64, of which some 9 us are
 // the two launches and their dependent reads (what a call of one short sequence
 // takes).  7 tokens of 8 sequences, window 2048, e4m3: 27 us.
 #include <math.h>

@@ -67,6 +67,7 @@ constexpr int kChunk = 32;                     // keys per chunk of V codes
 constexpr int kRaw = 8;                        // chunks in the ring: two V tiles
 constexpr int kScTiles = 8;                    // tiles whose block scales are kept
 constexpr int kConv = 2;                       // conversion warps
+constexpr float kParts = 1.3f;                 // see parts_of
 template <bool E4> constexpr int kVWarps = E4 ? kConv : 1;
 
 template <int DH, bool E4> struct ManyCfg {
@@ -209,9 +210,16 @@ __device__ __forceinline__ Place find_item(const ManyArgs& m, long long x) {
   r.start = pb[0] * Hkv + r.h * per + pb[lo] - pb[0];
   return r;
 }
-// CTA c's part of the line.
-__device__ __forceinline__ long long cut(const ManyArgs& m, long long total, int c) {
-  return total * c / m.n_cta;
+// How many parts the line has.  An item of s key tiles in t parts takes the time of
+// s / t of them and of t pieces in the merge, so parts beyond some multiple of
+// sqrt(s) per item only cost: 64 rows over one sequence of 64k with one KV head 121
+// us without the limit, 57 with 1.3 sqrt(s), 58 with 1 and 64 with 2.
+__device__ __forceinline__ int parts_of(const ManyArgs& m, long long total) {
+  return min(m.n_cta, 1 + (int)(kParts * sqrtf((float)total * ((float)m.a.c.B * m.a.c.Hkv * m.pairs))));
+}
+// Where part c begins.
+__device__ __forceinline__ long long cut(int parts, long long total, int c) {
+  return total * min(c, parts) / parts;
 }
 // The key tiles [t0, t1) of the item at [start, start + cnt + 1) in the part [x0, x1).
 __device__ __forceinline__ int2 piece_of(long long start, int cnt, long long x0, long long x1) {
@@ -450,7 +458,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();                                   // the plan, and whatever wrote q and the cache
   const long long total = m.pre[(size_t)a.c.B * m.pairs] * a.c.Hkv;
-  const long long x0 = cut(m, total, blockIdx.x), x1 = cut(m, total, blockIdx.x + 1);
+  const int parts = parts_of(m, total);
+  const long long x0 = cut(parts, total, blockIdx.x), x1 = cut(parts, total, blockIdx.x + 1);
   const int G = kBM / m.tpt;
   // The k-th piece for a role other than the copying one; false after the last
   // (or a wait that ran out).  done(k) hands the descriptor back.
@@ -1279,10 +1288,11 @@ __global__ void __launch_bounds__(128) k_many_merge(const ManyArgs m) {
     const long long end = rec.start + it.cnt + 1;
     if (r == 0) n_list = is_whole = 0;
     __syncthreads();
-    for (int k = blockIdx.x + r; k < m.n_cta; k += kBM) {
-      const long long xk = cut(m, total, k);
+    const int parts = parts_of(m, total);
+    for (int k = blockIdx.x + r; k < parts; k += kBM) {
+      const long long xk = cut(parts, total, k);
       if (xk >= end) break;
-      const int2 t = piece_of(rec.start, it.cnt, max(xk, rec.start), cut(m, total, k + 1));
+      const int2 t = piece_of(rec.start, it.cnt, max(xk, rec.start), cut(parts, total, k + 1));
       list[k - blockIdx.x] = t.x < t.y ? 2 * k + (xk <= rec.start ? 1 : 0) : -1;
       atomicMax(&n_list, k - (int)blockIdx.x + 1);
       if (t.x == 0 && t.y == it.cnt) is_whole = 1;  // one CTA holds all key tiles: written out
