@@ -232,7 +232,7 @@ __global__ void __launch_bounds__((FewShape<MT, LO>::WARPS * 32), 1)
   // of them and for t pieces in the merge, so teams beyond some multiple of sqrt(s)
   // per pair only cost: one sequence of 64k, one KV head, e4m3 21.8 us without the
   // limit, 16.5 with 16 sqrt(s) as with 12, 18.4 with 9.
-  const int teams = min(min(f.teams, total), (int)(16.f * sqrtf((float)total * (float)(f.B * f.P))) + 1);
+  const int teams = min(total, 1 + (int)fminf((float)(f.teams - 1), 16.f * sqrtf((float)total * (float)(f.B * f.P))));
   const int team = warp * gridDim.x + blockIdx.x;
   const bool mine = team < teams;
   // [total·team / teams, total·(team + 1) / teams), in 32 bits (teams < 2^15)

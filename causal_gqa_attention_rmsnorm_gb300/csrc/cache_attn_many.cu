@@ -215,7 +215,8 @@ __device__ __forceinline__ Place find_item(const ManyArgs& m, long long x) {
 // sqrt(s) per item only cost: 64 rows over one sequence of 64k with one KV head 121
 // us without the limit, 57 with 1.3 sqrt(s), 58 with 1 and 64 with 2.
 __device__ __forceinline__ int parts_of(const ManyArgs& m, long long total) {
-  return min(m.n_cta, 1 + (int)(kParts * sqrtf((float)total * ((float)m.a.c.B * m.a.c.Hkv * m.pairs))));
+  const float items = (float)m.a.c.B * m.a.c.Hkv * m.pairs;
+  return 1 + (int)fminf((float)(m.n_cta - 1), kParts * sqrtf((float)total * items));
 }
 // Where part c begins.
 __device__ __forceinline__ long long cut(int parts, long long total, int c) {

@@ -681,6 +681,14 @@ def test_one_and_two_row_tiles_over_long_caches(kind, H, Hkv, n):
     run_attention(kind, True, (1500, 131), n, H, Hkv, 64, 1536, 32, 300, 140, seed=n + 1)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("lens", [(9001,), (9001, 1, 0, 5000)])
+@pytest.mark.parametrize("n", [1, 2, 4, 60])
+def test_one_head_over_long_caches(kind, lens, n):
+    """Many parts of one row's keys to join, and sequences with next to none beside it."""
+    run_attention(kind, True, lens, n, 8, 1, 128, 9216, 64, seed=n)
+
+
 @pytest.mark.parametrize("n", [1, 40, 300])
 def test_small_addends_survive_large_ones(n):
     """A score whose products cancel but for one 2^-17 of them: sums are fp32."""
