@@ -395,9 +395,11 @@ TB_API size_t tb_kvcache_attn_workspace_bytes(const tb_attn_cfg* cfg, const tb_k
  * TB_DEVERR_BAD_PAGE.  lens[b] above T_max counts as T_max and sets
  * TB_DEVERR_CACHE_FULL.  A non-finite value in a row reaches those queries only
  * that see the row.  Scores, softmax statistics and sums are fp32; for TB_BF16
- * the weights enter their product with v rounded to bf16, over e4m3 to fp16, and
- * there the elements of a query may be off by 2^-17 of its largest one (the
- * products of many rows take it as two 8-bit terms). */
+ * the weights enter their product with v rounded to bf16.  Over e4m3 what enters
+ * is weight x V scale, in fp16 relative to the row's largest: off by 2^-11 of
+ * itself, or 2^-25 of that largest where it is far smaller; and the elements of a
+ * query may be off by 2^-17 of its largest one (the products of many rows take it
+ * as two 8-bit terms). */
 TB_API tb_status tb_kvcache_attn(const tb_attn_cfg* cfg, const void* q, const tb_kvcache* kv, const int32_t* n_new,
                                  int32_t n, void* o, void* ws, size_t ws_bytes, void* stream);
 
