@@ -212,8 +212,8 @@ class KVCache:
                 raise ValueError("block_table must be a contiguous CUDA int32 tensor [B, pages per sequence]")
             B, T_max = table
             T_max *= ps
-        if not (lens.get_device() == dev and lens.dtype is _I32 and lens.numel() == B):
-            raise ValueError("lens must be a CUDA int32 tensor of B entries")
+        if not (lens.get_device() == dev and lens.dtype is _I32 and lens.numel() == B and lens.is_contiguous()):
+            raise ValueError("lens must be a contiguous CUDA int32 tensor of B entries")
         ks = vs = None
         if dt == TB_I8:
             for name, t in (("k_scale", self.k_scale), ("v_scale", self.v_scale)):
