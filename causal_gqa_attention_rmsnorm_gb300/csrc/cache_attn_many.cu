@@ -1151,7 +1151,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
       if (f_on < 0 && !(split && t0 < t1)) {    // no tile of this piece
         if (split && g) continue;               // (slot 0 writes the zeros)
         if (where >= 0) {
-          m.part[((size_t)(where * 2 + g) * (DH / 4 + 1)) * kBM + r] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+          // (a sum below zero: no output follows)
+          m.part[((size_t)(where * 2 + g) * (DH / 4 + 1)) * kBM + r] = make_float4(-INFINITY, -1.f, 0.f, 0.f);
         } else if (valid) {
           uint4* dst = reinterpret_cast<uint4*>((bf16*)a.o + orow * DH);
 #pragma unroll
@@ -1168,6 +1169,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         tc_fence_after();
       }
       float a0 = 1.f, a1 = 0.f;                 // factors of the slots' outputs
+      const bool both = t0 + 1 < t1;            // split: slot 1 had a tile, its output is set
       if (split) {
         if (g) {
           // hand (max, sum) over, and keep the output until it has been read
@@ -1191,7 +1193,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         const float2 ml = ml_s[r];
         const float mj = fmaxf(m_used, ml.x), base = mj == -INFINITY ? 0.f : mj;
         a0 = ex2_approx(m_used - base);
-        a1 = ex2_approx(ml.x - base);           // 0 where slot 1 saw no key: its columns are not looked at
+        a1 = ex2_approx(ml.x - base);
         l = l * a0 + ml.y * a1;
         m_used = mj;
       }
@@ -1212,7 +1214,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
           for (int i = 0; i < 16; ++i) {
             asm volatile("" : "+r"(u[i]), "+r"(u1[i]));
             const float v = __uint_as_float(u[i]) * a0;
-            u[i] = __float_as_uint(a1 > 0.f ? fmaf(__uint_as_float(u1[i]), a1, v) : v);
+            // (a factor of 0 too: scores of -inf or NaN leave no maximum, but count)
+            u[i] = __float_as_uint(both ? fmaf(__uint_as_float(u1[i]), a1, v) : v);
           }
         } else {
           tmem_wait_ld();
@@ -1315,7 +1318,7 @@ __global__ void __launch_bounds__(128) k_many_merge(const ManyArgs m) {
         if (list[i] < 0) continue;
         const float4* p = at(list[i]);
         const float4 ml = p[0];
-        if (ml.x == -INFINITY) continue;            // no visible key in this piece: its O may be unset
+        if (ml.y < 0.f) continue;                   // no key tile of this slot in this piece: its O is unset
         const float wgt = ex2_approx(ml.x - base);
         l = fmaf(ml.y, wgt, l);
 #pragma unroll

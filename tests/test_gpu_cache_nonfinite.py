@@ -1,0 +1,115 @@
+"""tb_kvcache_attn over caches and queries that hold infinities and NaN: what a
+query sees reaches it as IEEE arithmetic says, what it does not see never does."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.cache as ref
+from cache_helpers import ROW, attn_tolerance, make_cache, put_rows, rows, values
+
+pytestmark = pytest.mark.gpu
+
+
+def tbm():
+    import causal_gqa_attention_rmsnorm_gb300 as tb
+    return tb
+
+
+def filled(kind, L, Hkv, dh, T, block=16, paged=True):
+    kv = make_cache(kind, paged, 1, Hkv, T, dh, block, fill=float("nan"))
+    put_rows(kv, 0, rows(1, Hkv, L, dh), rows(2, Hkv, L, dh))
+    kv.lens.fill_(L)
+    return kv
+
+
+def poke(kv, name, h, t, d, x):
+    """Element (KV head h, token t, dim d) of a one-sequence cache becomes x (e4m3: a code)."""
+    buf = getattr(kv, name)
+    e4m3 = buf.dtype == torch.float8_e4m3fn
+    buf = buf.view(torch.uint8) if e4m3 else buf
+    at = (0, h, t, d) if kv.block_table is None else (int(kv.block_table[0, t // buf.shape[2]]), h, t % buf.shape[2], d)
+    buf[at] = x
+
+
+def attend(kv, q, window=0, sinks=0):
+    tb = tbm()
+    H, dh = q.shape[2:]
+    cfg = tb.AttnConfig(H=H, Hkv=kv.k.shape[1], dh=dh, window=window, sinks=sinks,
+                        dtype=tb.TB_F32 if q.dtype == torch.float32 else tb.TB_BF16)
+    o = tb.tb_kvcache_attn(cfg, q, kv)[0].double().cpu().numpy()
+    assert tb.tb_get_device_error(clear=True) == 0
+    return o
+
+
+def expect(q, k, v, first, window=0, sinks=0):
+    """The formula in 64 bits with the infinities and NaN of its inputs, and the
+    same with the keys of an infinite or NaN score left out, for tolerances.  q [m,
+    H, dh], k and v [Hkv, L, dh]."""
+    m, H, dh = q.shape
+    Hkv, L, _ = k.shape
+    out, mag, top = np.zeros((m, H, dh)), np.zeros((m, H, dh)), np.zeros((m, H))
+    with np.errstate(all="ignore"):
+        for i in range(m):
+            see = ref.visible(first + i, L, window, sinks)
+            for h in range(H):
+                kk, vv = k[h // (H // Hkv)][see], v[h // (H // Hkv)][see]
+                if not see.any():
+                    continue
+                z = kk @ q[i, h] / np.sqrt(dh)
+                w = np.exp(z - z.max())
+                w /= w.sum()
+                out[i, h] = w @ vv
+                ok = np.isfinite(z)
+                mag[i, h] = w[ok] @ np.abs(vv[ok]) if ok.any() else 0
+                top[i, h] = (np.abs(kk[ok]) @ np.abs(q[i, h])).max() / np.sqrt(dh) if ok.any() else 0
+    return out, mag, top
+
+
+def same(kind, got, out, mag, top, dh, nkeys):
+    """NaN and infinities in the same places, the rest within its bound."""
+    wrong = int((np.isnan(got) != np.isnan(out)).sum())
+    assert wrong == 0, f"{wrong} of {out.size} NaN where no NaN belongs, or none where one does"
+    inf = np.isinf(out)
+    wrong = int((np.isinf(got) != inf).sum() + (got[inf] != out[inf]).sum())
+    assert wrong == 0, f"{wrong} infinities"
+    fine = np.isfinite(out)
+    with np.errstate(all="ignore"):
+        tol = attn_tolerance(kind, out, mag, top, dh, nkeys)
+        off = int((np.abs(got - out) > tol)[fine].sum())
+    assert off == 0, f"{off} of {int(fine.sum())} finite outputs off"
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("n,L", [(40, 129), (40, 257), (129, 129)])
+def test_a_piece_of_one_nan_score_is_joined(kind, dh, n, L):
+    """The last key is alone in its key tile and its score is NaN: the piece of
+    that tile has no finite score, but the last query sees it."""
+    kv = filled(kind, L, 1, dh, 272)
+    k, v = values(kv, "k", 0)[:, :L], values(kv, "v", 0)[:, :L]
+    poke(kv, "k", 0, L - 1, 5, 0x7F if kind == "e4m3" else math.nan)
+    k[0, L - 1, 5] = math.nan
+    q = rows(5, 1, n, 1, dh, dtype=torch.bfloat16).cuda()
+    want = expect(q[0].double().cpu().numpy(), k, v, L - n)
+    assert np.isnan(want[0][-1]).all() and np.isfinite(want[0][:-1]).all()
+    same(kind, attend(kv, q), *want, dh, L)
+
+
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("n,L", [(40, 129), (40, 257), (129, 129)])
+def test_a_piece_of_one_weightless_infinity_is_joined(dh, n, L):
+    """The last key is alone in its key tile, its score is -inf and its value
+    infinite: 0 times infinity is NaN for the query that sees it."""
+    kv = filled("bf16", L, 1, dh, 272)
+    k, v = values(kv, "k", 0)[:, :L], values(kv, "v", 0)[:, :L]
+    poke(kv, "k", 0, L - 1, 5, -math.inf)
+    poke(kv, "v", 0, L - 1, 7, math.inf)
+    k[0, L - 1, 5], v[0, L - 1, 7] = -math.inf, math.inf
+    q = rows(5, 1, n, 1, dh)
+    q[..., 5] = 1
+    q = q.to(torch.bfloat16).cuda()
+    want = expect(q[0].double().cpu().numpy(), k, v, L - n)
+    assert np.isnan(want[0][-1, 0, 7]) and np.isfinite(np.delete(want[0][-1, 0], 7)).all()
+    same("bf16", attend(kv, q), *want, dh, L)
