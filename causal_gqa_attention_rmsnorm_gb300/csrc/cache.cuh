@@ -280,9 +280,8 @@ __device__ __noinline__ void attend_row(const AttnArgs& a, int b, int hkv, int p
         if ((i & ~(D - 1)) == (lane * D & 7)) acc[i & (D - 1)] = fmaf(pk, v[i], acc[i & (D - 1)]);
     }
   }
-  const bool none = l == 0.f;             // no visible key
 #pragma unroll
-  for (int u = 0; u < D; ++u) out[u] = none ? 0.f : acc[u] / l;
+  for (int u = 0; u < D; ++u) out[u] = nkeys == 0 ? 0.f : acc[u] / l;     // (0 / 0 where all scores are -inf)
 }
 
 // cache_attn.cu

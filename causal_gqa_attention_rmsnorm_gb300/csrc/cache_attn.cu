@@ -170,7 +170,9 @@ __global__ void __launch_bounds__(kFWarps * 32) k_attn_f32(const F32Args f) {
       A = fmaf(acc_s[w][r][e], wgt, A);
     }
     if (f.n_range == 1) {
-      ((float*)a.o)[row_at(r) + e] = L == 0.f ? 0.f : A / L;
+      // zeros for a negative position, which sees no key; where keys are seen and all
+      // scores are -inf the sum is 0 too, and 0 / 0 the answer
+      ((float*)a.o)[row_at(r) + e] = sr.first + ((rt * kRows + r) >> a.g_sh) < 0 ? 0.f : A / L;
     } else {
       float* p = f.part + ((((((size_t)b * a.c.Hkv + h) * f.n_tiles + rt) * f.n_range + rg) * kRows) + r) * (DH + 2);
       p[e] = A;
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(256) k_f32_merge(const F32Args f) {
   float* out = (float*)a.o + (((size_t)b * a.n + (t >> a.g_sh)) * a.H + h * G + (t & (G - 1))) * DH;
 #pragma unroll
   for (int u = 0; u < D; ++u)
-    if (DH >= 32 || lane < DH) out[lane + 32 * u] = L == 0.f ? 0.f : acc[u] / L;
+    if (DH >= 32 || lane < DH) out[lane + 32 * u] = sr.first + (t >> a.g_sh) < 0 ? 0.f : acc[u] / L;
 }
 
 // Row tiles, and key ranges: so many that the CTAs fill the GPU twice, with a

@@ -798,7 +798,8 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W) k_few_merge(const FewAr
   } else if (W > 1 && warp > 0) {
     return;
   }
-  const float inv = L == 0.f ? 0.f : 1.0f / L;
+  // (a negative position sees no key; a sum of 0 elsewhere is that of scores of -inf, and no answer)
+  const float inv = sr.first + tok < 0 ? 0.f : 1.0f / L;
   float probe = 0.f;
 #pragma unroll
   for (int u = 0; u < D; ++u) {

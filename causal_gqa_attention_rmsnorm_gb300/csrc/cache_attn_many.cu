@@ -1197,7 +1197,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
         l = l * a0 + ml.y * a1;
         m_used = mj;
       }
-      const float inv = where >= 0 ? 1.f : l == 0.f ? 0.f : 1.0f / l;
+      // (a negative position sees no key; a sum of 0 elsewhere is that of scores of -inf, and no answer)
+      const float inv = where >= 0 ? 1.f : qp < 0 ? 0.f : 1.0f / l;
       float4* piece_out = m.part + ((size_t)(max(where, 0) * 2 + g) * (DH / 4 + 1)) * kBM + r;
       bf16* dst = (bf16*)a.o + orow * DH;
       float probe = 0.f;                        // stays 0 while every output is finite
@@ -1330,7 +1331,7 @@ __global__ void __launch_bounds__(128) k_many_merge(const ManyArgs m) {
           acc[u].w = fmaf(v.w, wgt, acc[u].w);
         }
       }
-      const float inv = l == 0.f ? 0.f : 1.0f / l;
+      const float inv = s.p0 + r / G < 0 ? 0.f : 1.0f / l;       // (as in the attention kernel)
       const bool valid = r < s.rows;
       bf16* dst = (bf16*)a.o + (((size_t)rec.b * a.n + s.tok0 + r / G) * a.H + rec.h * G + r % G) * DH + col;
       float probe = 0.f;

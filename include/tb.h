@@ -389,7 +389,8 @@ TB_API size_t tb_kvcache_attn_workspace_bytes(const tb_attn_cfg* cfg, const tb_k
  *          overlap.
  *  n_new : as in tb_append_rows; o rows of padding are left as they were.
  *  ws    : 256-byte aligned workspace; calls that may overlap need their own.
- * A query that sees no key (a negative position) gets zeros.  Rows no query of
+ * A query that sees no key (a negative position) gets zeros; one whose visible
+ * scores are all -inf gets NaN.  Rows no query of
  * the call sees are not read: what they hold, and the pages they lie in, do not
  * matter; a visible row in a page outside the pool counts as zeros and sets
  * TB_DEVERR_BAD_PAGE.  lens[b] above T_max counts as T_max and sets

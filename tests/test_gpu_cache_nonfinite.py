@@ -113,3 +113,50 @@ def test_a_piece_of_one_weightless_infinity_is_joined(dh, n, L):
     want = expect(q[0].double().cpu().numpy(), k, v, L - n)
     assert np.isnan(want[0][-1, 0, 7]) and np.isfinite(np.delete(want[0][-1, 0], 7)).all()
     same("bf16", attend(kv, q), *want, dh, L)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("n,L,H,Hkv", [(1, 1, 4, 1), (3, 3, 2, 2), (8, 8, 8, 2), (12, 12, 4, 2), (40, 40, 2, 2),
+                                      (200, 200, 4, 2), (3, 2, 4, 2), (40, 38, 2, 1), (6, 700, 4, 2), (150, 700, 4, 2)])
+def test_scores_that_are_all_minus_infinity_give_nan(kind, dh, n, L, H, Hkv):
+    """Key 0 of KV head 0 scores -inf, and so do all keys of KV head 1 (where there
+    is one): NaN where a query sees nothing else, a weight of 0 beside other keys,
+    zeros at negative positions all the same."""
+    T = -(-L // 16) * 16
+    kv = filled(kind, L, Hkv, dh, T)
+    k, v = values(kv, "k", 0)[:, :L], values(kv, "v", 0)[:, :L]
+    poke(kv, "k", 0, 0, 5, -math.inf)
+    k[0, 0, 5] = -math.inf
+    if Hkv > 1:
+        for t in range(L):
+            poke(kv, "k", 1, t, 5, -math.inf)
+        k[1, :, 5] = -math.inf
+    q = rows(5, 1, n, H, dh)
+    q[..., 5] = 1
+    q = q.to(ROW[kind]).cuda()
+    want = expect(q[0].double().cpu().numpy(), k, v, L - n)
+    at0 = n - L                                           # the query at position 0
+    if at0 >= 0:
+        assert np.isnan(want[0][at0]).all() and (want[0][:at0] == 0).all()
+    assert np.isfinite(want[0][max(at0 + 1, 0):, :H // Hkv]).all()
+    same(kind, attend(kv, q), *want, dh, L)
+
+
+@pytest.mark.parametrize("n,L", [(1, 1), (1, 300), (8, 300), (40, 300), (200, 300), (3, 2)])
+def test_an_infinite_query_over_e4m3_gives_nan(n, L):
+    """A query with an infinite element against keys whose element is negative:
+    every score -inf."""
+    kv = filled("e4m3", L, 2, 64, 304)
+    for t in range(L):
+        for h in range(2):
+            poke(kv, "k", h, t, 5, 0xB8)                  # -1
+    k, v = values(kv, "k", 0)[:, :L], values(kv, "v", 0)[:, :L]
+    assert (k[:, :, 5] < 0).all()
+    q = rows(5, 1, n, 4, 64)
+    q[:, -1, 1, 5] = math.inf
+    q[:, -1, 2, 5] = -math.inf
+    q = q.to(torch.bfloat16).cuda()
+    want = expect(q[0].double().cpu().numpy(), k, v, L - n)
+    assert np.isnan(want[0][-1, 1:3]).all() and np.isfinite(want[0][-1, ::3]).all()
+    same("e4m3", attend(kv, q), *want, 64, L)
