@@ -198,6 +198,8 @@ cudaError_t launch_append_rope(const AppendArgs& a, cudaStream_t s);
 // cache_attn_few.cu: up to kFewRows query rows (tokens x heads) per KV head,
 // 16-bit queries over bf16 or e4m3 rows of dh 64 or 128.
 constexpr int kFewRows = 32;
+// Whether the stages of one sequence can be numbered (at most 2^30).
+bool cache_attn_few_fits(const AttnArgs& a);
 size_t cache_attn_few_workspace(const AttnArgs& a);
 cudaError_t launch_cache_attn_few(const AttnArgs& a, void* ws, cudaStream_t s);
 // cache_attn_many.cu: any number of rows, same types and widths.
@@ -285,6 +287,7 @@ __device__ __noinline__ void attend_row(const AttnArgs& a, int b, int hkv, int p
 }
 
 // cache_attn.cu
+bool cache_attn_fits(const AttnArgs& a);
 size_t cache_attn_workspace(const AttnArgs& a);
 size_t cache_attn_workspace_upto(const AttnArgs& a);
 cudaError_t launch_cache_attn(const AttnArgs& a, void* ws, cudaStream_t s);

@@ -70,6 +70,19 @@ CacheView view_of(const tb_kvcache* kv, int* err) {
   return c;
 }
 
+AttnArgs attn_args(const tb_attn_cfg* cfg, const tb_kvcache* kv, int n, int* err) {
+  AttnArgs a;
+  a.c = view_of(kv, err);
+  a.n = n;
+  a.H = cfg->H;
+  a.g_sh = shift_of(cfg->H / cfg->Hkv);
+  a.window = cfg->window;
+  a.sinks = cfg->window > 0 ? cfg->sinks : 0;
+  const float scale = cfg->scale != 0.f ? cfg->scale : 1.0f / sqrtf((float)cfg->dh);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return a;
+}
+
 tb_status check_attn(const tb_attn_cfg* cfg, const tb_kvcache* kv, int n, bool tensors) {
   if (!cfg) return report(TB_ERR_INVALID_ARG, "cfg is NULL");
   const tb_status st = check_cache(kv, tensors);
@@ -96,20 +109,9 @@ tb_status check_attn(const tb_attn_cfg* cfg, const tb_kvcache* kv, int n, bool t
   if (n > kv->T_max) return report(TB_ERR_INVALID_ARG, "n (%d) exceeds kv->T_max (%d)", n, kv->T_max);
   if ((long long)kv->B * n * cfg->H > (1LL << 31) - 1)
     return report(TB_ERR_UNSUPPORTED, "B·n·H above 2^31 - 1 query rows");
+  if (!cache_attn_fits(attn_args(cfg, kv, n, nullptr)))
+    return report(TB_ERR_UNSUPPORTED, "few rows over a sequence of more than 2^30 pieces (16 keys of a KV head each)");
   return TB_OK;
-}
-
-AttnArgs attn_args(const tb_attn_cfg* cfg, const tb_kvcache* kv, int n, int* err) {
-  AttnArgs a;
-  a.c = view_of(kv, err);
-  a.n = n;
-  a.H = cfg->H;
-  a.g_sh = shift_of(cfg->H / cfg->Hkv);
-  a.window = cfg->window;
-  a.sinks = cfg->window > 0 ? cfg->sinks : 0;
-  const float scale = cfg->scale != 0.f ? cfg->scale : 1.0f / sqrtf((float)cfg->dh);
-  a.scale_log2 = scale * 1.4426950408889634f;
-  return a;
 }
 
 }  // namespace

@@ -270,6 +270,8 @@ bool few(const AttnArgs& a) { return a.n * (a.H / a.c.Hkv) <= kFewRows; }
 
 }  // namespace
 
+bool cache_attn_fits(const AttnArgs& a) { return a.c.dtype == TB_F32 || !few(a) || cache_attn_few_fits(a); }
+
 size_t cache_attn_workspace(const AttnArgs& a) {
   if (a.c.dtype != TB_F32) return few(a) ? cache_attn_few_workspace(a) : cache_attn_many_workspace(a);
   if (a.c.B == 0 || a.n == 0) return 0;

@@ -834,7 +834,8 @@ Deal deal_of(const AttnArgs& a) {
   return {2, R, 1, FewShape<2, false>::WARPS};
 }
 
-// Sequences per launch: the line's stage numbers stay below 2^30.
+// Sequences per launch: the line's stage numbers stay below 2^30 (one sequence
+// alone does, see cache_attn_few_fits).
 int batch_of(const AttnArgs& a, const Deal& d) {
   const long long per = (long long)a.c.Hkv * d.tiles * ((a.c.T + kRun - 1) / kRun + 1);
   return (int)std::min<long long>(std::min(a.c.B, kMaxB), std::max<long long>(1, (1LL << 30) / per));
@@ -900,6 +901,12 @@ cudaError_t by_rows(const AttnArgs& a, void* ws, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool cache_attn_few_fits(const AttnArgs& a) {
+  long long runs = a.c.T / kRun + 1;
+  if (a.window > 0) runs = std::min(runs, ((long long)a.window + a.n) / kRun + a.sinks / kRun + 3);
+  return runs * a.c.Hkv * deal_of(a).tiles <= 1LL << 30;
+}
 
 size_t cache_attn_few_workspace(const AttnArgs& a) {
   if (a.c.B == 0 || a.n == 0) return 0;

@@ -1,0 +1,44 @@
+"""Sizes at which the cache operators' 32-bit counts would run over: refused on the
+host, before anything is launched."""
+import ctypes
+
+import pytest
+
+import causal_gqa_attention_rmsnorm_gb300 as tb
+from causal_gqa_attention_rmsnorm_gb300 import binding
+from test_cache_ops_host import FAKE, append, cache, e4m3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return binding.lib()
+
+
+def attn(lib, kv, n=1, G=1, **k):
+    """Status of a call that has nothing wrong beside its sizes."""
+    c = binding.tb_attn_cfg(kv.Hkv * G, kv.Hkv, kv.dh, tb.TB_F32 if kv.dtype == tb.TB_F32 else tb.TB_BF16,
+                            k.get("window", 0), k.get("sinks", 0), k.get("scale", 0.0))
+    return lib.tb_kvcache_attn(ctypes.byref(c), FAKE, ctypes.byref(kv), None, n, FAKE + (1 << 45), None, 0, None)
+
+
+def need(lib, kv, n=1, G=1, window=0, sinks=0):
+    c = binding.tb_attn_cfg(kv.Hkv * G, kv.Hkv, kv.dh, tb.TB_F32 if kv.dtype == tb.TB_F32 else tb.TB_BF16, window,
+                            sinks, 0.0)
+    return lib.tb_kvcache_attn_workspace_bytes(ctypes.byref(c), ctypes.byref(kv), n)
+
+
+def many_pages(Hkv, T, dtype=tb.TB_BF16, dh=128):
+    """A page may stand in the table more than once, so long sequences of many heads need no memory."""
+    return cache(B=1, Hkv=Hkv, T=T, dh=dh, dtype=dtype, bt=FAKE, ps=32, pages=9, ks=FAKE, vs=FAKE)
+
+
+@pytest.mark.parametrize("dtype", [tb.TB_BF16, tb.TB_E4M3])
+def test_stages_of_one_sequence_are_counted_in_32_bits(lib, dtype):
+    big = many_pages(65535, 600000, dtype)                # 65535 heads x 37501 runs: above 2^31
+    assert attn(lib, big) == 2 and b"2^30" in lib.tb_last_error_message()
+    assert need(lib, big) == 0
+    assert attn(lib, many_pages(32768, 32 * 20000, dtype), G=8, n=4) == 2
+    # what can be counted is not refused: fewer heads, a window, and the tensor-core kernel's 64-bit line
+    assert need(lib, many_pages(1024, 600000, dtype)) > 0
+    assert need(lib, big, window=1000, sinks=4) > 0
+    assert need(lib, many_pages(1024, 600000, dtype), n=64) > 0
