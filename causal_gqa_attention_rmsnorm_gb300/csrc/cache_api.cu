@@ -107,6 +107,8 @@ tb_status check_attn(const tb_attn_cfg* cfg, const tb_kvcache* kv, int n, bool t
   if (cfg->dh != 64 && cfg->dh != 128 && !(small && cfg->dtype == TB_F32))
     return report(TB_ERR_UNSUPPORTED, "dh %d: attention kernels exist for 64 and 128 (fp32 also 16 and 32)", cfg->dh);
   if (n > kv->T_max) return report(TB_ERR_INVALID_ARG, "n (%d) exceeds kv->T_max (%d)", n, kv->T_max);
+  // (the kernels round positions up to whole tiles of 128 keys, in 32 bits)
+  if (kv->T_max > INT32_MAX - 256) return report(TB_ERR_UNSUPPORTED, "T_max (%d) above 2^31 - 257", kv->T_max);
   if ((long long)kv->B * n * cfg->H > (1LL << 31) - 1)
     return report(TB_ERR_UNSUPPORTED, "B·n·H above 2^31 - 1 query rows");
   if (!cache_attn_fits(attn_args(cfg, kv, n, nullptr)))

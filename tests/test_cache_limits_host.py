@@ -42,3 +42,12 @@ def test_stages_of_one_sequence_are_counted_in_32_bits(lib, dtype):
     assert need(lib, many_pages(1024, 600000, dtype)) > 0
     assert need(lib, big, window=1000, sinks=4) > 0
     assert need(lib, many_pages(1024, 600000, dtype), n=64) > 0
+
+
+@pytest.mark.parametrize("dtype", [tb.TB_F32, tb.TB_BF16, tb.TB_E4M3])
+@pytest.mark.parametrize("n", [1, 64])
+def test_positions_leave_room_for_a_whole_tile(lib, dtype, n):
+    """A position rounded up to a tile of keys stays a 32-bit number."""
+    for T in (2 ** 31 - 32, 2 ** 31 - 256 + 32):
+        assert attn(lib, many_pages(1, T, dtype), n=n) == 2 and b"T_max" in lib.tb_last_error_message()
+    assert need(lib, many_pages(1, 2 ** 31 - 512, dtype), n=n) > 0
