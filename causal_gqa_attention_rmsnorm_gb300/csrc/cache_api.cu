@@ -143,6 +143,9 @@ tb_status tb_kvcache_append_rope(const tb_kvcache* kv, const tb_append_rows* row
   st = check_cache(kv, true);
   if (st != TB_OK) return st;
   if (rows->n > kv->T_max) return report(TB_ERR_INVALID_ARG, "n (%d) exceeds kv->T_max (%d)", rows->n, kv->T_max);
+  // (the eight-element pieces of a block are counted in 32 bits)
+  if (kv->dtype == TB_E4M3 && kv->page_size > 1 << 24)
+    return report(TB_ERR_UNSUPPORTED, "appending to e4m3 blocks of at most 2^24 tokens (%d)", kv->page_size);
   if (max_pos < kv->T_max)
     return report(TB_ERR_INVALID_ARG, "the rotation table's max_pos (%d) is below kv->T_max (%d)", max_pos, kv->T_max);
   if (!rope || !aligned16(rope)) return report(TB_ERR_INVALID_ARG, "rope must be non-NULL and 16-byte aligned");

@@ -332,7 +332,7 @@ cudaError_t launch_append_rope(const AppendArgs& a, cudaStream_t s) {
     e = a.c.dtype == TB_F32 ? launch_pdl(k_append_rope<float>, grid, dim3(threads), 0, s, a, group)
                             : launch_pdl(k_append_rope<bf16>, grid, dim3(threads), 0, s, a, group);
   } else {
-    const int nb = (a.n + a.c.ps - 2) / a.c.ps + 1;        // blocks that n rows can reach from any start
+    const int nb = (int)(((long long)a.n + a.c.ps - 2) / a.c.ps) + 1;        // blocks that n rows can reach from any start
     const int pieces = std::min(a.n, a.c.ps) * (a.c.dh / kVec);      // of a block, at most
     // (a step of few rows per block has many small CTAs: q takes no more than half
     // of the usual threads there)

@@ -318,9 +318,10 @@ TB_API tb_status tb_stack_decode(const tb_block_cfg *cfg, int32_t L, const void 
  *    powers of two.
  * TB_I8 caches are TB_ERR_UNSUPPORTED here, and so are dh that is no multiple of
  * 16 or above 256, B above 32767, H or Hkv above 65535, num_pages·Hkv above
- * 2^31 - 2; so is attention of few rows (n·H/Hkv <= 32) where the 16-key runs that
- * one sequence may show, times Hkv, pass 2^30 (2^29 always fit), and any attention
- * over T_max above 2^31 - 257.  The block's calls take no TB_E4M3 cache. */
+ * 2^31 - 2, an append to e4m3 blocks of more than 2^24 tokens, attention over T_max
+ * above 2^31 - 257, and attention of few rows (n·H/Hkv <= 32) where the 16-key runs
+ * that one sequence may show, times Hkv, pass 2^30 (2^29 always fit).  The block's
+ * calls take no TB_E4M3 cache. */
 
 /* The rotation table of tb_kvcache_append_rope: table [max_pos, dh/2, 2] fp32
  * (device) receives (cos, sin) of t·base^(-2i/dh) for position t and pair i,

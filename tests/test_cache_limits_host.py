@@ -51,3 +51,15 @@ def test_positions_leave_room_for_a_whole_tile(lib, dtype, n):
     for T in (2 ** 31 - 32, 2 ** 31 - 256 + 32):
         assert attn(lib, many_pages(1, T, dtype), n=n) == 2 and b"T_max" in lib.tb_last_error_message()
     assert need(lib, many_pages(1, 2 ** 31 - 512, dtype), n=n) > 0
+
+
+def test_pieces_of_an_e4m3_block_are_counted_in_32_bits(lib):
+    """2^24 tokens of 256 elements are 2^29 pieces; far larger blocks ran over, and
+    their older codes were not rewritten for a new scale."""
+    for block in (1 << 25, 1 << 27, (1 << 31) - 16):
+        kv = e4m3(B=1, Hkv=1, T=block, dh=128, ps=block)
+        assert append(lib, kv, max_pos=block) == 2 and b"2^24" in lib.tb_last_error_message()
+        # reading such a block has no such count
+        assert need(lib, e4m3(B=1, Hkv=1, T=1 << 27, dh=128, ps=1 << 27)) > 0
+    # (a block of 2^24 gets as far as the next check)
+    assert append(lib, e4m3(B=1, Hkv=1, T=1 << 24, dh=128, ps=1 << 24), max_pos=16) == 1
