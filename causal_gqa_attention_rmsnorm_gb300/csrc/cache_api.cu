@@ -99,7 +99,9 @@ tb_status check_attn(const tb_attn_cfg* cfg, const tb_kvcache* kv, int n, bool t
     return report(TB_ERR_INVALID_ARG, "fp32 queries go with an fp32 cache, bf16 queries with a bf16 or e4m3 one");
   if (cfg->window < 0 || cfg->sinks < 0)
     return report(TB_ERR_INVALID_ARG, "window (%d) and sinks (%d) must be non-negative", cfg->window, cfg->sinks);
-  if (!isfinite(cfg->scale)) return report(TB_ERR_INVALID_ARG, "scale must be finite");
+  // (the kernels apply scale·log2 e, in fp32)
+  if (!isfinite(cfg->scale * 1.4426950408889634f))
+    return report(TB_ERR_INVALID_ARG, "scale must be finite, and its product with log2(e) too");
   const int G = cfg->H / cfg->Hkv;
   if (G != 1 && G != 2 && G != 4 && G != 8)
     return report(TB_ERR_UNSUPPORTED, "H/Hkv = %d: attention kernels exist for 1, 2, 4 and 8", G);

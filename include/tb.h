@@ -375,7 +375,8 @@ TB_API tb_status tb_kvcache_append_rope(const tb_kvcache* kv, const tb_append_ro
  *               (W = 0 or j > p - W or j < S): its W most recent positions, its
  *               own included, and the first S.  Both non-negative; without a
  *               window S has no effect.
- *  scale      : of the scores; 0 stands for 1/sqrt(dh). */
+ *  scale      : of the scores, of at most 2^127 in magnitude; 0 stands for
+ *               1/sqrt(dh). */
 typedef struct {
   int32_t H, Hkv, dh, dtype, window, sinks;
   float scale;

@@ -63,3 +63,13 @@ def test_pieces_of_an_e4m3_block_are_counted_in_32_bits(lib):
         assert need(lib, e4m3(B=1, Hkv=1, T=1 << 27, dh=128, ps=1 << 27)) > 0
     # (a block of 2^24 gets as far as the next check)
     assert append(lib, e4m3(B=1, Hkv=1, T=1 << 24, dh=128, ps=1 << 24), max_pos=16) == 1
+
+
+@pytest.mark.parametrize("dtype", [tb.TB_F32, tb.TB_BF16, tb.TB_E4M3])
+def test_the_scale_times_log2_e_is_finite(lib, dtype):
+    kv = e4m3(dtype=dtype)
+    for scale in (3e38, -3e38, float("inf")):
+        assert attn(lib, kv, scale=scale) == 1 and b"scale" in lib.tb_last_error_message()
+    for scale in (2.0 ** 127, -2.0 ** 127, 1e-45):
+        c = binding.tb_attn_cfg(2, 2, 64, tb.TB_F32 if dtype == tb.TB_F32 else tb.TB_BF16, 0, 0, scale)
+        assert lib.tb_kvcache_attn(ctypes.byref(c), FAKE, ctypes.byref(kv), None, 0, FAKE, None, 0, None) == 0
