@@ -6,6 +6,11 @@
 
 namespace tb {
 
+// Everything that lies in global memory is read with plain loads: these grids are
+// resident before the kernel in front of them ends (pdl_trigger), which may still be
+// writing lengths, rows, scales or the rotation table, and a non-coherent load
+// (ld.global.nc) wants memory that nobody writes while its grid lives.
+
 // A cache as the kernels see it.  Row t of (sequence b, KV head h):
 //   contiguous (bt == nullptr): row (b·Hkv + h)·T + t
 //   paged: row (page·Hkv + h)·ps + t % ps, page = bt[b·per + t / ps]

@@ -60,8 +60,8 @@ __device__ __forceinline__ void rotate8(float (&x)[8], const float4 (&cs)[2]) {
 }
 __device__ __forceinline__ void load_cs(const AppendArgs& a, int pos, int e, float4 (&cs)[2]) {
   const float4* p = reinterpret_cast<const float4*>(a.rope + (size_t)pos * (a.c.dh >> 1) + (e >> 1));
-  cs[0] = __ldg(p);
-  cs[1] = __ldg(p + 1);
+  cs[0] = p[0];
+  cs[1] = p[1];
 }
 
 // Position of sequence b's first new row and how many rows it gets; nn = -1

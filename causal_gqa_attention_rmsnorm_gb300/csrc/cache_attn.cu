@@ -43,6 +43,17 @@ __device__ __forceinline__ KeyRuns tile_runs(const F32Args& f, const SeqRange& s
   return key_runs(sr.first + i1 + 1, sr.first + i0, f.a.window, f.a.sinks, kKeys);
 }
 
+// *p, or 0: a predicated load spelled out up to 64 dims (one token of 32 sequences of
+// up to 8k rows, 8 and 2 heads of 64: 90 us, from the plain expression 108), left to
+// the compiler at 128 (32 and 8 heads: 503 us, spelled out 512).
+template <int DH>
+__device__ __forceinline__ float load_if(bool in, const float* p) {
+  if constexpr (DH == 128) return in ? *p : 0.f;
+  float v = 0.f;
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.f32 %0, [%1];\n\t}" : "+f"(v) : "l"(p), "r"((int)in));
+  return v;
+}
+
 template <int DH>
 __global__ void __launch_bounds__(kFWarps * 32) k_attn_f32(const F32Args f) {
   pdl_trigger();
@@ -98,7 +109,7 @@ __global__ void __launch_bounds__(kFWarps * 32) k_attn_f32(const F32Args f) {
       const float4* kp = reinterpret_cast<const float4*>((const float*)a.c.k + row * DH);
 #pragma unroll 8
       for (int e = 0; e < DH / 4; ++e) {
-        const float4 kv = __ldg(kp + e);
+        const float4 kv = kp[e];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
           const float4 qv = *reinterpret_cast<const float4*>(&q_s[r][4 * e]);
@@ -130,7 +141,7 @@ __global__ void __launch_bounds__(kFWarps * 32) k_attn_f32(const F32Args f) {
         const long long vr = __shfl_sync(0xffffffffu, row, k0 + k);
 #pragma unroll
         for (int u = 0; u < D; ++u)        // (-1: seen by no row, or a page outside the pool)
-          v[k][u] = vr >= 0 && (DH >= 32 || lane < DH) ? __ldg((const float*)a.c.v + vr * DH + lane + 32 * u) : 0.f;
+          v[k][u] = load_if<DH>(vr >= 0 && (DH >= 32 || lane < DH), (const float*)a.c.v + vr * DH + lane + 32 * u);
       }
 #pragma unroll
       for (int r = 0; r < kRows; ++r)

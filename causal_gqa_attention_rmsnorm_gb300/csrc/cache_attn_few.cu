@@ -293,8 +293,8 @@ __global__ void __launch_bounds__((FewShape<MT, LO>::WARPS * 32), 1)
             si = (long long)ppage * a.c.per + block_of(a.c, key);
           }
           if constexpr (E4) {
-            pks = ppage < 0 ? 1.f : __ldg(a.c.ks + si);
-            pvs = ppage < 0 ? 1.f : __ldg(a.c.vs + si);
+            pks = ppage < 0 ? 1.f : a.c.ks[si];
+            pvs = ppage < 0 ? 1.f : a.c.vs[si];
           }
         }
       }

@@ -558,8 +558,8 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
           si = plane;
         }
         if constexpr (E4) {
-          ks = __ldg(a.c.ks + si);
-          vs = __ldg(a.c.vs + si);
+          ks = a.c.ks[si];
+          vs = a.c.vs[si];
         }
         return plane;
       };
