@@ -1,12 +1,12 @@
-"""Sizes at which the cache operators' 32-bit counts would run over: refused on the
-host, before anything is launched."""
+"""Refusals of the cache operators, on the host and before anything is launched: sizes
+at which their 32-bit counts would run over, caches and workspaces that do not do."""
 import ctypes
 
 import pytest
 
 import causal_gqa_attention_rmsnorm_gb300 as tb
 from causal_gqa_attention_rmsnorm_gb300 import binding
-from test_cache_ops_host import FAKE, append, cache, e4m3
+from test_cache_ops_host import BAD_CACHES, FAKE, append, cache, e4m3
 
 
 @pytest.fixture(scope="module")
@@ -73,3 +73,29 @@ def test_the_scale_times_log2_e_is_finite(lib, dtype):
     for scale in (2.0 ** 127, -2.0 ** 127, 1e-45):
         c = binding.tb_attn_cfg(2, 2, 64, tb.TB_F32 if dtype == tb.TB_F32 else tb.TB_BF16, 0, 0, scale)
         assert lib.tb_kvcache_attn(ctypes.byref(c), FAKE, ctypes.byref(kv), None, 0, FAKE, None, 0, None) == 0
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_the_attention_refuses_the_cache_for_the_reason_the_append_gives(lib, bad, status):
+    """q, o, ws and cfg are right, so that only the cache can be refused."""
+    kv = cache(**bad)
+    assert append(lib, kv) == status
+    why = lib.tb_last_error_message()
+    c = binding.tb_attn_cfg(4, kv.Hkv or 2, kv.dh, tb.TB_BF16, 0, 0, 0.0)
+    assert lib.tb_kvcache_attn(ctypes.byref(c), FAKE, ctypes.byref(kv), None, 1, FAKE + (1 << 40), FAKE, 1 << 40, None) == status
+    assert lib.tb_last_error_message() == why
+
+
+@pytest.mark.parametrize("kv,n,H", [
+    (cache(B=1, Hkv=8, T=65536, dh=128), 1, 32),                               # streaming kernel
+    (cache(B=1, Hkv=8, T=65536, dh=128), 64, 32),                              # tensor-core kernel
+    (e4m3(B=3, Hkv=8, T=4096, dh=64), 7, 32),
+])
+def test_a_workspace_that_does_not_do_is_named(lib, kv, n, H):
+    dtype = tb.TB_F32 if kv.dtype == tb.TB_F32 else tb.TB_BF16
+    c = binding.tb_attn_cfg(H, kv.Hkv, kv.dh, dtype, 0, 0, 0.0)
+    bytes_ = lib.tb_kvcache_attn_workspace_bytes(ctypes.byref(c), ctypes.byref(kv), n)
+    assert bytes_ > 0
+    for ws, have in ((None, bytes_), (FAKE, bytes_ // 2), (FAKE + 128, bytes_), (FAKE, 0)):
+        status = lib.tb_kvcache_attn(ctypes.byref(c), FAKE, ctypes.byref(kv), None, n, FAKE + (1 << 45), ws, have, None)
+        assert status == 1 and b"ws must be" in lib.tb_last_error_message()
