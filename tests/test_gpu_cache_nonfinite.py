@@ -160,3 +160,67 @@ def test_an_infinite_query_over_e4m3_gives_nan(n, L):
     want = expect(q[0].double().cpu().numpy(), k, v, L - n)
     assert np.isnan(want[0][-1, 1:3]).all() and np.isfinite(want[0][-1, ::3]).all()
     same("e4m3", attend(kv, q), *want, 64, L)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 4, 12, 40, 200])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_a_nan_key_reaches_the_queries_that_see_it(kind, n, dh):
+    """NaN in the K of a row that leaves the window inside the call, of the last row
+    and of a sink: each seen by some queries, or heads, and not by others."""
+    L, W, S, H, Hkv = 400, 64, 3, 8, 4
+    kv = filled(kind, L, Hkv, dh, 416)
+    k, v = values(kv, "k", 0)[:, :L], values(kv, "v", 0)[:, :L]
+    leaves = L - n - W + 1 + n // 2
+    for h, t in ((0, leaves), (1, L - 1), (2, 1)):
+        poke(kv, "k", h, t, 5, 0x7F if kind == "e4m3" else math.nan)
+        k[h, t, 5] = math.nan
+    q = rows(5, 1, n, H, dh, dtype=ROW[kind]).cuda()
+    want = expect(q[0].double().cpu().numpy(), k, v, L - n, W, S)
+    nan = np.isnan(want[0]).all(-1)
+    assert np.array_equal(nan, np.isnan(want[0]).any(-1))
+    assert nan[:, 4:6].all() and not nan[:, 6:].any() and nan[:, :2].any() and (n == 1 or not nan[:, :2].all())
+    assert nan[-1, 2:4].all() and not nan[:-1, 2:4].any()
+    same(kind, attend(kv, q, W, S), *want, dh, L)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 4, 12, 40, 200])
+@pytest.mark.parametrize("window", [0, 64])
+def test_infinities_in_the_cache(kind, n, window):
+    """In K: a score of +inf is NaN for its query, one of -inf a weight of 0.  In V:
+    an infinity for the queries that give the row a weight, NaN beside a second one
+    of the other sign."""
+    L, S, H, Hkv, dh = 400, 0, 8, 4, 64
+    kv = filled(kind, L, Hkv, dh, 416)
+    k, v = values(kv, "k", 0)[:, :L], values(kv, "v", 0)[:, :L]
+    t = L - n - 5                                          # inside the window of the first queries
+    for name, x, h, at, d, val in (("k", k, 0, t, 5, math.inf), ("k", k, 1, t, 5, -math.inf),
+                                   ("v", v, 2, t, 6, math.inf), ("v", v, 2, t + 1, 7, -math.inf),
+                                   ("v", v, 3, t, 8, math.inf), ("v", v, 3, t + 2, 8, -math.inf)):
+        poke(kv, name, h, at, d, val)
+        x[h, at, d] = val
+    q = rows(5, 1, n, H, dh)
+    q[..., 5] = 1
+    q = q.to(ROW[kind]).cuda()
+    want = expect(q[0].double().cpu().numpy(), k, v, L - n, window, S)
+    assert np.isnan(want[0][0, :2]).all() and np.isfinite(want[0][:, 2:4]).all()
+    assert np.isinf(want[0][0, 4:6, 6:8]).all() and np.isnan(want[0][0, 6:, 8]).all()
+    same(kind, attend(kv, q, window, S), *want, dh, L)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 12, 40])
+def test_infinite_and_nan_queries_stay_alone(kind, n):
+    """A query row of infinities or NaN is NaN itself; the rows beside it are not."""
+    L, H, Hkv, dh = 300, 8, 2, 64
+    kv = filled(kind, L, Hkv, dh, 304)
+    k, v = values(kv, "k", 0)[:, :L], values(kv, "v", 0)[:, :L]
+    q = rows(5, 1, n, H, dh)
+    q[0, -1, 1, 5], q[0, -1, 6, 9], q[0, 0, 3, :] = math.inf, math.nan, -math.inf
+    q = q.to(ROW[kind]).cuda()
+    want = expect(q[0].double().cpu().numpy(), k, v, L - n)
+    bad = np.zeros((n, H), dtype=bool)
+    bad[-1, 1] = bad[-1, 6] = bad[0, 3] = True
+    assert np.array_equal(np.isnan(want[0]).all(-1), bad)
+    same(kind, attend(kv, q), *want, dh, L)
