@@ -265,3 +265,121 @@ def test_attention_beside_the_blocks_decode_step(H, Hkv, dh, window):
             assert (np.abs(mine[b, h] - out[0, h]) <= tol).all()
             # (x + attention in fp32)
             assert (np.abs(theirs[b, h] - out[0, h]) <= tol + 2.0 ** -22 * (np.abs(out[0, h]) + 8)).all()
+
+
+# ---- calls that are allowed and unusual ------------------------------------------
+
+@pytest.mark.parametrize("kind,T,block", [("bf16", 1, 0), ("bf16", 5, 0), ("bf16", 77, 0), ("bf16", 333, 0),
+                                          ("e4m3", 16, 16), ("e4m3", 48, 48), ("e4m3", 80, 16), ("e4m3", 336, 112),
+                                          ("f32", 1, 0), ("f32", 77, 0)])
+@pytest.mark.parametrize("H,Hkv,dh", [(4, 4, 64), (8, 1, 128)])
+def test_short_and_odd_contiguous_caches(kind, T, block, H, Hkv, dh):
+    """Capacities below a tile and no multiple of anything: the last rows of a plane
+    lie before the first of the next one, which no query sees."""
+    for n in sorted({1, min(T, 3), min(T, 7), min(T, 40), min(T, 140)}):
+        run_attention(kind, False, (T, max(T - 1, n), n, n // 2, 0), n, H, Hkv, dh, T, block, seed=n + T)
+        run_attention(kind, False, (T, max(T - 1, n)), n, H, Hkv, dh, T, block, 9, 2, seed=n + T + 1)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 3, 12, 20, 60])
+def test_negative_and_small_scales(kind, n):
+    for scale in (-0.05, 1e-30, -1e-30):
+        run_attention(kind, True, (150, 20), n, 4, 2, 64, 160, 32, 30, 5, (n, min(n, 20)), scale=scale, seed=n)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 12, 60, 200])
+def test_zero_queries_over_zero_keys(kind, n):
+    """All weights equal: the mean of what is seen.  e4m3: the smallest block scale."""
+    tb = tbm()
+    L, dh = 300, 64
+    kv = make_cache(kind, False, 1, 2, 304, dh, 16)
+    put_rows(kv, 0, torch.zeros(2, L, dh), rows(2, 2, L, dh))
+    if kind == "e4m3":
+        kv.k_scale.fill_(2.0 ** -24)
+    kv.lens.fill_(L)
+    q = torch.zeros(1, n, 4, dh, dtype=ROW[kind], device="cuda")
+    cfg = tb.AttnConfig(H=4, Hkv=2, dh=dh, window=100, sinks=3, dtype=tb.TB_F32 if kind == "f32" else tb.TB_BF16)
+    o = tb.tb_kvcache_attn(cfg, q, kv)[0].double().cpu().numpy()
+    out, mag, top = ref.attend(q[0].double().cpu().numpy(), values(kv, "k", 0)[:, :L], values(kv, "v", 0)[:, :L], L - n, 100, 3)
+    check_attention(kind, o, out, mag, top, dh, L)
+    assert tb.tb_get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_many_sequences_of_many_rows(kind):
+    """1300 short sequences of 20 tokens on the tensor-core kernel, lengths from nothing on."""
+    tb = tbm()
+    B, Hkv, H, dh, T, n = 1300, 1, 2, 64, 48, 20
+    kv = make_cache(kind, False, B, Hkv, T, dh, 16, fill=0.0)
+    g = torch.Generator().manual_seed(1)
+    for x in (kv.k, kv.v):
+        if kind == "e4m3":
+            x.view(torch.uint8).copy_((torch.randn(x.shape, generator=g) * 100).to(torch.float8_e4m3fn).view(torch.uint8))
+        else:
+            x.copy_(torch.randn(x.shape, generator=g))
+    if kind == "e4m3":
+        kv.k_scale.fill_(2.0 ** -7)
+        kv.v_scale.fill_(2.0 ** -7)
+    kv.lens.copy_(torch.arange(B, dtype=torch.int32) % (T + 1))
+    q = rows(3, B, n, H, dh, dtype=torch.bfloat16).cuda()
+    o = tb.tb_kvcache_attn(tb.AttnConfig(H=H, Hkv=Hkv, dh=dh), q, kv).double().cpu().numpy()
+    assert tb.tb_get_device_error(clear=True) == 0
+    for b in list(range(0, 52)) + list(range(700, 730)) + list(range(1270, 1300)):
+        L = b % (T + 1)
+        out, mag, top = ref.attend(q[b].double().cpu().numpy(), values(kv, "k", b)[:, :L], values(kv, "v", b)[:, :L], L - n)
+        check_attention(kind, o[b], out, mag, top, dh, max(L, 1), f"sequence {b}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 7, 60])
+def test_sequences_that_share_pages(kind, n):
+    """A common prefix lies once in the pool and stands in both tables, a page even
+    twice in one of them."""
+    tb = tbm()
+    H, Hkv, dh, ps, L = 8, 2, 128, 32, 256
+    kv = make_cache(kind, True, 2, Hkv, L, dh, ps, fill=0.0)
+    kv.block_table[1, :4] = kv.block_table[0, :4]
+    kv.block_table[1, 5] = kv.block_table[1, 1]
+    for b in (1, 0):
+        put_rows(kv, b, rows(b, Hkv, L, dh), rows(b + 9, Hkv, L, dh))
+    kv.lens.fill_(L)
+    q = rows(3, 2, n, H, dh, dtype=torch.bfloat16).cuda()
+    o = tb.tb_kvcache_attn(tb.AttnConfig(H=H, Hkv=Hkv, dh=dh), q, kv).double().cpu().numpy()
+    assert tb.tb_get_device_error(clear=True) == 0
+    for b in range(2):
+        out, mag, top = ref.attend(q[b].double().cpu().numpy(), values(kv, "k", b), values(kv, "v", b), L - n)
+        check_attention(kind, o[b], out, mag, top, dh, L)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "e4m3"])
+def test_append_of_rows_that_repeat(kind):
+    """Strides of 0: one row for all tokens, or one sequence's rows for all sequences."""
+    tb = tbm()
+    B, n, Hkv, dh, T, bs = 3, 9, 2, 64, 64, 16
+    table = tb.tb_rope_table(dh, T, BASE)
+    one = rows(1, 1, 1, Hkv, dh, dtype=ROW[kind]).cuda()
+    seq = rows(2, 1, n, Hkv, dh, dtype=ROW[kind]).cuda()
+    a, b = (make_cache(kind, True, B, Hkv, T, dh, bs, fill=0.0) for _ in range(2))
+    tb.tb_kvcache_append_rope(a, one.expand(B, n, Hkv, dh), seq.expand(B, n, Hkv, dh), table, start=i32(0, 5, 55))
+    tb.tb_kvcache_append_rope(b, one.expand(B, n, Hkv, dh).contiguous(), seq.expand(B, n, Hkv, dh).contiguous(), table,
+                              start=i32(0, 5, 55))
+    assert a.lens.tolist() == b.lens.tolist() == [9, 14, 64] and tb.tb_get_device_error(clear=True) == 0
+    for x, y in ((a.k, b.k), (a.v, b.v)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_calls_with_nothing_to_do():
+    tb = tbm()
+    kv = make_cache("bf16", False, 2, 2, 64, 64, 0, fill=0.0)
+    kv.lens.fill_(5)
+    e = lambda B, n, h: torch.empty(B, n, h, 64, dtype=torch.bfloat16, device="cuda")
+    cfg = tb.AttnConfig(H=4, Hkv=2, dh=64)
+    table = tb.tb_rope_table(64, 64, BASE)
+    assert tb.tb_kvcache_append_rope(kv, e(2, 0, 2), e(2, 0, 2), table, q=e(2, 0, 4)).shape == (2, 0, 4, 64)
+    assert tb.tb_kvcache_attn(cfg, e(2, 0, 4), kv).shape == (2, 0, 4, 64)
+    none = tb.KVCache.empty(0, 2, 64, 64)
+    assert tb.tb_kvcache_append_rope(none, e(0, 3, 2), e(0, 3, 2), table) is None
+    assert tb.tb_kvcache_attn(cfg, e(0, 3, 4), none).shape == (0, 3, 4, 64)
+    assert kv.lens.tolist() == [5, 5] and tb.tb_get_device_error(clear=True) == 0
