@@ -383,3 +383,35 @@ def test_calls_with_nothing_to_do():
     assert tb.tb_kvcache_append_rope(none, e(0, 3, 2), e(0, 3, 2), table) is None
     assert tb.tb_kvcache_attn(cfg, e(0, 3, 4), none).shape == (0, 3, 4, 64)
     assert kv.lens.tolist() == [5, 5] and tb.tb_get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("n", [8, 512])
+def test_zero_rows_cost_what_others_do(kind, n):
+    """Rows of zeros at the end of a cache, as a padded batch has them, are not
+    computed key by key (which takes some hundred times as long; ten is the bound
+    here, for the noise of a clock)."""
+    tb = tbm()
+    H, Hkv, dh, T = 16, 4, 128, 2048
+    row = ROW[kind]
+    kv = make_cache(kind, False, 1, Hkv, T, dh, 64, fill=0.0)
+    table = tb.tb_rope_table(dh, T, BASE)
+    cfg = tb.AttnConfig(H=H, Hkv=Hkv, dh=dh, dtype=tb.TB_F32 if kind == "f32" else tb.TB_BF16)
+    took = []
+    for zeros in (False, True):
+        x, q = rows(1, 1, T, Hkv, dh, dtype=row).cuda(), rows(2, 1, n, H, dh, dtype=row).cuda()
+        if zeros:
+            x[:, -n:] = 0
+            q.zero_()
+        tb.tb_kvcache_append_rope(kv, x, x, table, start=i32(0))
+        best = math.inf
+        for _ in range(6):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            o = tb.tb_kvcache_attn(cfg, q, kv)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        took.append(best)
+    assert torch.isfinite(o).all() and tb.tb_get_device_error(clear=True) == 0
+    assert took[1] <= 10 * took[0], took
