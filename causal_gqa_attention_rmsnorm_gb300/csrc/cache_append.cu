@@ -9,8 +9,10 @@
 // The bytes bound it: every row is read and written once, the table's rows are
 // reused by all heads of a token.  Measured: 4 x 4096 bf16 rows of 32 + 2·8 heads
 // of 128 into 64-row pages, 60 us, 0.82 of the copy bandwidth; 3 x 1371 rows of
-// 12 + 2·12 heads of 64 into e4m3 blocks of 64, 9.3 us (0.43: waves of dependent
-// reads, positions, rows and page, old scale); one token 2.0 us, a launch.
+// 12 + 2·12 heads of 64 into e4m3 blocks of 64, 9.3 us (0.43: a CTA reads its block,
+// reduces and writes, and nothing overlaps one block's reduction with the next one's
+// reads), 4 x 4096 rows of 32 + 2·8 heads of 128 into e4m3 pages of 64 78 us (0.58);
+// fp32, 4 x 2048 rows, 63 us (0.77); one token 2.0 us, fp32 2.4, a launch.
 #include <algorithm>
 
 #include "cache.cuh"

@@ -29,6 +29,11 @@
 //   operands - a dot product does not care which; ldmatrix.trans hands it two keys
 //   of two dims, which one byte permutation sorts into an even-dim and an odd-dim
 //   fragment.
+//   Over bf16 the weights are rounded to bf16 for their product with v, their sum is
+//   not: the MMA takes one type for both operands, v's range does not fit fp16, and a
+//   second product for the rest would double the work on V.  The exponentials are
+//   ex2.approx (2^-22), far below either rounding.  Error against 64 bits of one token
+//   over 32 sequences: 0.0023 of the output, 0.0017 of it the output's own rounding.
 //   Queries enter as fp16 under a power of two per row that brings their
 //   largest element into [0.5, 1).  (8-bit warp-level MMAs on the K codes, with the
 //   queries split as for the tensor-memory kernel, ran slower: 108 against 100 us

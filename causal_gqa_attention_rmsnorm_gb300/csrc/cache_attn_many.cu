@@ -35,6 +35,11 @@
 //   keys; V scales 2^e enter the exponent, p' = 2^(z + e - m'), so that
 //   O = Σ p'·code and l = Σ p'·2^-e (see the streaming kernel).
 //
+// Over bf16 the weights enter P·V rounded to bf16, their sum is taken before: one
+// MMA has one type for both operands, and v's range does not fit fp16.  (A chunk of
+// 2 x 8192 tokens: error against 64 bits 0.0020 of the output, 0.0016 of it the
+// output's own rounding.)
+//
 // What bounds it: per key tile and slot the chain S ready -> row maximum ->
 // exponentials -> P ready, half of which hides behind the other slot's MMAs; and
 // the instruction cache, which all roles share: waits that give up live out of
@@ -43,8 +48,8 @@
 // 472 us; a copy of the softmax for border tiles: 852 against 734; MMAs issued by a
 // whole warp instead of one lane: 836 against 734).
 // Measured, 32 + 8 heads of 128: 2 x 8192 bf16 tokens, window 4096, 128 sinks, pages
-// of 64: 727 us, 1157 TFLOP/s, 0.61 of the 8192-cubed bf16 matrix product; 2048
-// tokens at the end of 16000: bf16 388 us, 1290 TFLOP/s, e4m3 434 us, 1157.
+// of 64: 728 us, 1156 TFLOP/s, 0.61 of the 8192-cubed bf16 matrix product; 2048
+// tokens at the end of 16000: bf16 389 us, 1292 TFLOP/s, e4m3 432 us, 1163.
 //
 // Rows whose result is not finite are computed once more by k_many_merge, key by
 // key, so that what a masked row holds never matters.
