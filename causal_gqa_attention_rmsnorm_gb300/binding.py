@@ -183,7 +183,7 @@ class KVCache:
     scale pools [num_pages, Hkv, page_size].  e4m3 (k, v of
     torch.float8_e4m3fn): codes with one fp32 scale per block of tokens and KV
     head, k_scale, v_scale [B, Hkv, T_max / block], or paged [num_pages, Hkv]
-    (a block is a page).  lens int32 [B]."""
+    (a block is a page).  lens int32 [B], dense: the calls write it."""
     k: torch.Tensor
     v: torch.Tensor
     lens: torch.Tensor
