@@ -927,7 +927,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
                 amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xffff0000u))));
             }
             const float fr = split_frame(amax);
-            // Exact, but for rows of elements below 2^-90: held to 2^-102, so that the product
+            // Exact, but where the elements of a row, or the scale, are below 2^-90: held to 2^-102, so that the product
             // with a K scale (2^-24 at least) is a normal number.  With 0 the -inf of hidden
             // scores became NaN, and rows of zeros over blocks of zeros (a padded prompt's) were
             // all computed again key by key: 1024 of 8192 tokens 161 ms, now 0.14.  What is held

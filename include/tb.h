@@ -404,7 +404,8 @@ TB_API size_t tb_kvcache_attn_workspace_bytes(const tb_attn_cfg* cfg, const tb_k
  * is weight x V scale, in fp16 relative to the row's largest: off by 2^-11 of
  * itself, or 2^-25 of that largest where it is far smaller; and the elements of a
  * query may be off by 2^-17 of its largest one (the products of many rows take it
- * as two 8-bit terms), scores of a query below 2^-90 throughout by 2^-18. */
+ * as two 8-bit terms), scores by 2^-18 where the elements of a query, or the scale,
+ * are all below 2^-90. */
 TB_API tb_status tb_kvcache_attn(const tb_attn_cfg* cfg, const void* q, const tb_kvcache* kv, const int32_t* n_new,
                                  int32_t n, void* o, void* ws, size_t ws_bytes, void* stream);
 
