@@ -30,7 +30,7 @@ EXPORTED = ("tb_packed_weights_bytes", "tb_pack_weights", "tb_workspace_bytes", 
             "tb_last_error_message", "tb_embed", "tb_lm_head_packed_bytes", "tb_pack_lm_head",
             "tb_lm_head_workspace_bytes", "tb_lm_head", "tb_stack_workspace_bytes", "tb_stack_prefill",
             "tb_stack_decode", "tb_rope_table", "tb_kvcache_append_rope", "tb_kvcache_attn_workspace_bytes",
-            "tb_kvcache_attn")
+            "tb_kvcache_attn", "tb_rmsnorm_e4m3", "tb_quant_e4m3", "tb_pack_e4m3", "tb_gemm_e4m3", "tb_gated_e4m3")
 
 
 class tb_block_cfg(ctypes.Structure):
@@ -70,7 +70,12 @@ class TbError(RuntimeError):
         self.status = status
 
 
+class tb_e4m3(ctypes.Structure):
+    _fields_ = [("codes", c_void_p), ("scale", c_void_p), ("rows", c_int32), ("cols", c_int32)]
+
+
 _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 _lib = None
 
 
@@ -134,7 +139,12 @@ def lib() -> ctypes.CDLL:
         L.tb_kvcache_attn_workspace_bytes.restype = c_size_t
         L.tb_kvcache_attn.argtypes = [P(tb_attn_cfg), c_void_p, P(tb_kvcache), c_void_p, c_int32, c_void_p, c_void_p,
                                       c_size_t, c_void_p]
-        for fn in ("tb_rope_table", "tb_kvcache_append_rope", "tb_kvcache_attn", "tb_pack_weights", "tb_block_prefill", "tb_block_decode", "tb_block_decode_noalloc",
+        L.tb_rmsnorm_e4m3.argtypes = [c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_float, P(tb_e4m3), c_void_p]
+        L.tb_quant_e4m3.argtypes = [c_void_p, c_int32, P(tb_e4m3), c_void_p]
+        L.tb_pack_e4m3.argtypes = [c_void_p, c_int32, P(tb_e4m3), c_void_p]
+        L.tb_gemm_e4m3.argtypes = [P(tb_e4m3), P(tb_e4m3), c_void_p, c_void_p, c_int32, c_void_p]
+        L.tb_gated_e4m3.argtypes = [P(tb_e4m3), P(tb_e4m3), P(tb_e4m3), c_void_p, c_int32, c_void_p, c_void_p]
+        for fn in ("tb_rmsnorm_e4m3", "tb_quant_e4m3", "tb_pack_e4m3", "tb_gemm_e4m3", "tb_gated_e4m3", "tb_rope_table", "tb_kvcache_append_rope", "tb_kvcache_attn", "tb_pack_weights", "tb_block_prefill", "tb_block_decode", "tb_block_decode_noalloc",
                    "tb_kvcache_append", "tb_embed", "tb_pack_lm_head", "tb_lm_head", "tb_stack_prefill",
                    "tb_stack_decode", "tb_get_device_error", "tbx_gemm_bf16"):
             getattr(L, fn).restype = c_int32
@@ -723,3 +733,199 @@ def tb_kvcache_attn(cfg: AttnConfig, q: torch.Tensor, kv: KVCache, n_new: Option
     if status:
         _check("tb_kvcache_attn", status)
     return o
+
+
+# ---- projections in 8 bits ---------------------------------------------------
+
+E4M3_BLOCK = 128             # columns (and rows of weights) per scale
+
+
+def _blocks(n: int) -> int:
+    return -(-n // E4M3_BLOCK)
+
+
+class _Coded:
+    """Codes [rows, cols] and their scales: two dense tensors, read once, here.  (A
+    handle to keep: a tensor that is resized or given other memory needs a new one.)"""
+    __slots__ = ("codes", "scale", "dev", "_struct", "_ref")
+
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor):
+        if codes.dim() != 2:
+            raise ValueError(f"codes must be [rows, cols], got {tuple(codes.shape)}")
+        rows, cols = codes.shape
+        dev = codes.get_device()
+        code_ptr = _dense(codes, "codes", _E4M3, (rows, cols), dev)
+        scale_ptr = _dense(scale, "scale", _E8M0, self._scales(rows, cols), dev)
+        self.codes, self.scale, self.dev = codes, scale, dev
+        self._struct = tb_e4m3(code_ptr, scale_ptr, rows, cols)
+        self._ref = ctypes.byref(self._struct)
+
+    @property
+    def rows(self) -> int:
+        return self._struct.rows
+
+    @property
+    def cols(self) -> int:
+        return self._struct.cols
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device="cuda"):
+        return cls(torch.empty((rows, cols), dtype=torch.uint8, device=device).view(_E4M3),
+                   torch.empty(cls._scales(rows, cols), dtype=torch.uint8, device=device).view(_E8M0))
+
+
+class E4M3Rows(_Coded):
+    """Rows of codes [M, K] (torch.float8_e4m3fn) with one power-of-two scale per 128
+    columns, scale [M, ceil(K / 128)] (torch.float8_e8m0fnu)."""
+    __slots__ = ()
+
+    @staticmethod
+    def _scales(rows: int, cols: int) -> tuple:
+        return rows, _blocks(cols)
+
+
+class E4M3Weight(_Coded):
+    """Weights as codes [out, in] with one power-of-two scale per block of 128 x 128,
+    scale [ceil(out / 128), ceil(in / 128)] (tb_pack_e4m3 makes them)."""
+    __slots__ = ()
+
+    @staticmethod
+    def _scales(rows: int, cols: int) -> tuple:
+        return _blocks(rows), _blocks(cols)
+
+
+_FLOATS = {torch.float32: TB_F32, torch.bfloat16: TB_BF16}
+
+
+def _float_dtype(t: torch.Tensor, name: str) -> int:
+    dt = _FLOATS.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return dt
+
+
+def _kind(m, cls, name: str, dev: Optional[int] = None):
+    if m.__class__ is not cls:
+        raise ValueError(f"{name} must be {cls.__name__}, got {type(m).__name__}")
+    if dev is not None and m.dev != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got cuda:{m.dev}")
+    return m._ref
+
+
+def _out_rows(out: Optional[E4M3Rows], M: int, cols: int, dev: int, stream, name: str = "out") -> E4M3Rows:
+    if out is None:
+        with _alloc_on(stream):
+            return E4M3Rows.empty(M, cols, device=f"cuda:{dev}")
+    _kind(out, E4M3Rows, name, dev)
+    if out.rows != M or out.cols != cols:
+        raise ValueError(f"{name} must have {M} rows of {cols} codes, got {out.rows} of {out.cols}")
+    return out
+
+
+def tb_rmsnorm_e4m3(x: torch.Tensor, g: torch.Tensor, eps: float, r: Optional[torch.Tensor] = None,
+                    h: Optional[torch.Tensor] = None, out: Optional[E4M3Rows] = None, stream=None):
+    """RMSNorm of the rows x [..., d] (or of x + r) times the gain g [d], as e4m3 rows.
+    Returns (out, h): h [..., d] is the sum in x's type where r is given (x itself will
+    do), else None."""
+    dt = _float_dtype(x, "x")
+    dev, shape = x.get_device(), x.shape
+    d = shape[-1] if shape else 0
+    x_ptr = _dense(x, "x", x.dtype, shape, dev)
+    g_ptr = _dense(g, "g", x.dtype, (d,), dev)
+    r_ptr, h_ptr, r_dt = None, None, 0
+    if r is not None:
+        r_dt = _float_dtype(r, "r")
+        r_ptr = _dense(r, "r", r.dtype, shape, dev)
+        if h is None:
+            with _alloc_on(stream):
+                h = torch.empty_like(x)
+        h_ptr = _dense(h, "h", x.dtype, shape, dev)
+    elif h is not None:
+        raise ValueError("h without r")
+    out = _out_rows(out, x.numel() // d if d else 0, d, dev, stream)
+    status = lib().tb_rmsnorm_e4m3(x_ptr, dt, r_ptr, r_dt, h_ptr, g_ptr, eps, out._ref, _stream_on(stream, dev))
+    if status:
+        _check("tb_rmsnorm_e4m3", status)
+    return out, h
+
+
+def tb_quant_e4m3(x: torch.Tensor, out: Optional[E4M3Rows] = None, stream=None) -> E4M3Rows:
+    """The rows x [..., d] as e4m3 rows."""
+    dt = _float_dtype(x, "x")
+    dev, shape = x.get_device(), x.shape
+    d = shape[-1] if shape else 0
+    x_ptr = _dense(x, "x", x.dtype, shape, dev)
+    out = _out_rows(out, x.numel() // d if d else 0, d, dev, stream)
+    status = lib().tb_quant_e4m3(x_ptr, dt, out._ref, _stream_on(stream, dev))
+    if status:
+        _check("tb_quant_e4m3", status)
+    return out
+
+
+def tb_pack_e4m3(w: torch.Tensor, out: Optional[E4M3Weight] = None, stream=None) -> E4M3Weight:
+    """Weights w [in, out] as e4m3 codes [out, in]."""
+    dt = _float_dtype(w, "w")
+    if w.dim() != 2:
+        raise ValueError("w must be [in, out]")
+    dev = w.get_device()
+    K, N = w.shape
+    w_ptr = _dense(w, "w", w.dtype, (K, N), dev)
+    if out is None:
+        with _alloc_on(stream):
+            out = E4M3Weight.empty(N, K, device=w.device)
+    _kind(out, E4M3Weight, "out", dev)
+    if out.rows != N or out.cols != K:
+        raise ValueError(f"out must have {N} rows of {K} codes, got {out.rows} of {out.cols}")
+    _check("tb_pack_e4m3", lib().tb_pack_e4m3(w_ptr, dt, out._ref, _stream_on(stream, dev)))
+    return out
+
+
+def tb_gemm_e4m3(x: E4M3Rows, w: E4M3Weight, res: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                 y_dtype: Optional[int] = None, stream=None) -> torch.Tensor:
+    """y [M, N] = x·wᵀ (+ res), x rows [M, K], w weights [N, K]; y in y_dtype (default:
+    that of y or res, else bf16).  y may be res itself."""
+    x_ref = _kind(x, E4M3Rows, "x")
+    dev = x.dev
+    w_ref = _kind(w, E4M3Weight, "w", dev)
+    shape = (x.rows, w.rows)
+    if y is None:
+        dtype = _F32 if y_dtype == TB_F32 else res.dtype if y_dtype is None and res is not None else _BF16
+        with _alloc_on(stream):
+            y = torch.empty(shape, dtype=dtype, device=x.codes.device)
+    dt = _float_dtype(y, "y")
+    if y_dtype is not None and y_dtype != dt:
+        raise ValueError("y has another type than y_dtype")
+    y_ptr = _dense(y, "y", y.dtype, shape, dev)
+    res_ptr = None if res is None else _dense(res, "res", y.dtype, shape, dev)
+    status = lib().tb_gemm_e4m3(x_ref, w_ref, res_ptr, y_ptr, dt, _stream_on(stream, dev))
+    if status:
+        _check("tb_gemm_e4m3", status)
+    return y
+
+
+def tb_gated_e4m3(x: E4M3Rows, w1: E4M3Weight, w3: E4M3Weight, out=None, out_dtype: Optional[int] = None, stream=None):
+    """SiLU(x·w1ᵀ) * (x·w3ᵀ), x rows [M, K], w1 and w3 weights [F, K]: e4m3 rows [M, F],
+    or with out_dtype TB_BF16 or TB_F32 (or such a tensor as out) a tensor [M, F]."""
+    x_ref = _kind(x, E4M3Rows, "x")
+    dev = x.dev
+    w1_ref, w3_ref = _kind(w1, E4M3Weight, "w1", dev), _kind(w3, E4M3Weight, "w3", dev)
+    M, F = x.rows, w1.rows
+    if out_dtype not in (None, TB_E4M3, TB_BF16, TB_F32):
+        raise ValueError("out_dtype must be TB_E4M3, TB_BF16 or TB_F32")
+    if out_dtype == TB_E4M3 or (out_dtype is None and not isinstance(out, torch.Tensor)):
+        out = _out_rows(out, M, F, dev, stream)
+        dt, y_ptr, s_ptr = TB_E4M3, out._struct.codes, out._struct.scale
+    else:
+        if out is None:
+            with _alloc_on(stream):
+                out = torch.empty((M, F), dtype=_F32 if out_dtype == TB_F32 else _BF16, device=x.codes.device)
+        if not isinstance(out, torch.Tensor):
+            raise ValueError("out must be a tensor [M, F] for this out_dtype")
+        dt = _float_dtype(out, "out")
+        if out_dtype is not None and out_dtype != dt:
+            raise ValueError("out has another type than out_dtype")
+        y_ptr, s_ptr = _dense(out, "out", out.dtype, (M, F), dev), None
+    status = lib().tb_gated_e4m3(x_ref, w1_ref, w3_ref, y_ptr, dt, s_ptr, _stream_on(stream, dev))
+    if status:
+        _check("tb_gated_e4m3", status)
+    return out

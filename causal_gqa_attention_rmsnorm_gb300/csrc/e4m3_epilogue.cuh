@@ -1,0 +1,39 @@
+// What the two products of e4m3.cuh do with finished sums: four neighbouring columns of
+// a row at a time.
+#pragma once
+
+#include "e4m3.cuh"
+
+namespace tb {
+
+// SiLU(gate)·up, as in the block's W1/W3 epilogue.
+__device__ __forceinline__ float gated(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+__device__ __forceinline__ void put4(void* y, int y_dtype, size_t at, float4 v) {
+  if (y_dtype == TB_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(y) + at) = v;
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(static_cast<bf16*>(y) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+__device__ __forceinline__ float4 get4(const void* y, int y_dtype, size_t at) {
+  if (y_dtype == TB_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(y) + at);
+  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(y) + at);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+
+// Up to four exponent bytes of consecutive K blocks as one word, the first in the low
+// byte; `n` of them exist.  Missing ones read as 2^0.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int n) {
+  if (n >= 4 && ((uintptr_t)p & 3u) == 0) return *reinterpret_cast<const uint32_t*>(p);
+  uint32_t w = 0x7f7f7f7fu;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) w = (w & ~(0xffu << (8 * i))) | (uint32_t)p[i] << (8 * i);
+  return w;
+}
+
+}  // namespace tb

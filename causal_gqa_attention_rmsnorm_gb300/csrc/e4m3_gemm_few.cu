@@ -1,0 +1,355 @@
+// Products of e4m3 rows with e4m3 weights, for few rows (and for any): C = X·Wᵀ, or
+// SiLU(X·W1ᵀ) * (X·W3ᵀ), where every 128 columns of a row of X and every 128 x 128 of a
+// W have a power-of-two scale.
+//
+//   C[m, n] = sum_b 2^(sx[m, b] + sw[n / 128, b]) · sum_{k in block b} x[m, k] w[n, k]
+//
+// The scales go into the tensor core's instruction (kind::mxf8f6f4, which takes one per
+// 32 elements of K: the four instructions of a K block name the same byte), so no sum
+// is touched on its way.  With few rows the product is bound by the weights' stream, so
+// it is formed transposed, Cᵀ = W·Xᵀ: 128 weight rows are the instruction's M and the
+// rows of X, padded to NT, its N.  The `splits` CTAs of a tile form a cluster, CTA rank
+// r taking part r of the K blocks:
+//   warp 0      TMA: a K block's weight tiles [128, 128] and row tile [NT, 128] into a
+//               ring of stages (the first weights before the wait for the kernel
+//               before, which they do not depend on);
+//   warp 1      issues the instructions, K blocks in order, and hands a chunk of K back
+//               after every kChunk scale sets;
+//   warps 2..5  put the scales into tensor memory, four K blocks at a time, ahead of
+//               the instructions; add the chunks' sums up in registers; then turn them
+//               around in shared memory, and after a cluster barrier each CTA adds
+//               its share of the rows up over the cluster, in rank order, and finishes
+//               them.
+// Chunks: the tensor core's accumulation cuts sums off instead of rounding them, which
+// shifts a sum of n instructions by up to n/2 steps of fp32.  A chunk is 64
+// instructions (2048 of K); the chunks are added with rounding.
+#include "e4m3_epilogue.cuh"
+#include "gemm_tc.cuh"
+#include "sm100_ptx.cuh"
+
+namespace tb {
+namespace {
+
+using namespace ptx;
+
+constexpr int kSet = 4;          // K blocks per scale set: one exponent byte each in a word
+constexpr int kChunk = 4;        // scale sets per chunk
+constexpr int kSets = 8;         // scale sets held in tensor memory: two chunks
+constexpr int kMaxSplits = 8;
+
+// NT rows of X; MATS 1 or 2 weight matrices; CPS CTAs per SM.
+template <int NT, int MATS, int CPS> struct FewCfg {
+  static constexpr uint32_t W_BYTES = MATS * kBlk * kBlk;
+  static constexpr uint32_t STAGE_BYTES = W_BYTES + NT * kBlk;
+  static constexpr uint32_t ROOM = CPS == 2 ? 110 * 1024 : 220 * 1024;
+  static constexpr int FIT = ROOM / STAGE_BYTES;
+  static constexpr int STAGES = FIT > 12 ? 12 : FIT;
+  static constexpr uint32_t OFF_BAR = STAGES * STAGE_BYTES;
+  static constexpr size_t SMEM = OFF_BAR + 512 + 1024;
+  static constexpr uint32_t ACC = MATS * NT;                 // columns of one accumulator
+  static constexpr uint32_t SET_COLS = 4 * MATS + 4;         // a word per weight row / 32 and row / 32
+  static constexpr uint32_t SETS_AT = 2 * ACC;
+  static constexpr uint32_t NEED = SETS_AT + kSets * SET_COLS;
+  static constexpr uint32_t TMEM_COLS = NEED <= 128 ? 128 : NEED <= 256 ? 256 : 512;
+  static_assert(CPS * TMEM_COLS <= 512, "tensor memory of an SM");
+  static_assert(STAGES >= 2 && (2 * STAGES + 2 * kSets + 6) * 8 + 8 <= 512, "barriers");
+  static_assert(MATS * NT * kBlk * 4 <= OFF_BAR, "the sums reuse the ring");
+};
+
+template <int NT, int MATS, int CPS>
+__global__ void __launch_bounds__(192, CPS)
+    k_e4m3_few(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW3,
+               const __grid_constant__ CUtensorMap tmX, GemmArgs a, int wtiles, int splits, int* err) {
+  using C = FewCfg<NT, MATS, CPS>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* empty = full + STAGES;
+  uint64_t* sfull = empty + STAGES;       // scale sets
+  uint64_t* sempty = sfull + kSets;
+  uint64_t* tfull = sempty + kSets;       // accumulators
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* part_s = reinterpret_cast<float*>(smem);       // [MATS][NT][128] after the main loop
+
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();              // blockIdx.x % splits
+  const int tile = (int)(blockIdx.x / splits);
+  const int wt = tile % wtiles, m0 = tile / wtiles * NT;
+  const int kblocks = (a.K + kBlk - 1) / kBlk;
+  const int kb0 = (int)((long long)kblocks * rank / splits);
+  const int nkb = (int)((long long)kblocks * (rank + 1) / splits) - kb0;   // >= 1: splits <= kblocks
+  const int nsets = (nkb + kSet - 1) / kSet, nchunks = (nsets + kChunk - 1) / kChunk;
+  const int rows = min(NT, a.M - m0);
+  const int tpr = (rows + splits - 1) / splits;         // rows each CTA of the cluster finishes
+  const int t0 = min(rows, rank * tpr), t1 = min(rows, t0 + tpr);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kSets; ++s) {
+      mbar_init(&sfull[s], 4);
+      mbar_init(&sempty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&tfull[s], 1);
+      mbar_init(&tempty[s], 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tmW);
+    if (MATS == 2) prefetch_tmap(&tmW3);
+    prefetch_tmap(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_first();
+      const bool once = a.M <= NT;              // the weights are read once: they need not stay in L2
+      bool dep = false;
+      auto release = [&]() {
+        pdl_wait();
+        dep = true;
+        const int held = nkb < STAGES ? nkb : STAGES;
+        for (int h = 0; h < held; ++h)
+          tma_load_3d(&tmX, smem + h * C::STAGE_BYTES + C::W_BYTES, &full[h], (kb0 + h) * kBlk, m0, 0);
+      };
+      int j = 0;
+      for (; j < nkb; ++j) {
+        const int st = j % STAGES;
+        if (!mbar_wait(&empty[st], ((j / STAGES) & 1) ^ 1u, abort_flag, err)) break;
+        uint8_t* sw = smem + st * C::STAGE_BYTES;
+        const int k = (kb0 + j) * kBlk;
+        mbar_arrive_expect_tx(&full[st], C::STAGE_BYTES);
+        if (once) {
+          tma_load_3d_hint(&tmW, sw, &full[st], k, wt * kBlk, 0, pol);
+          if constexpr (MATS == 2) tma_load_3d_hint(&tmW3, sw + kBlk * kBlk, &full[st], k, wt * kBlk, 0, pol);
+        } else {
+          tma_load_3d(&tmW, sw, &full[st], k, wt * kBlk, 0);
+          if constexpr (MATS == 2) tma_load_3d(&tmW3, sw + kBlk * kBlk, &full[st], k, wt * kBlk, 0);
+        }
+        if (dep) tma_load_3d(&tmX, sw + C::W_BYTES, &full[st], k, m0, 0);
+        else if (j + 1 == STAGES) release();
+      }
+      if (!dep) release();
+      // every copy issued must land before the CTA may exit (earlier copies into the
+      // same stages were consumed, hence complete)
+      volatile int no_abort = 0;
+      for (int t = j - STAGES < 0 ? 0 : j - STAGES; t < j; ++t)
+        mbar_wait(&full[t % STAGES], (t / STAGES) & 1, &no_abort, err);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int j = 0; ok && j < nkb; ++j) {
+        const int st = j % STAGES, set = j / kSet, chunk = set / kChunk, buf = chunk & 1;
+        if (j % kSet == 0) {
+          if (j % (kSet * kChunk) == 0 && !mbar_wait(&tempty[buf], ((chunk >> 1) & 1) ^ 1u, abort_flag, err)) break;
+          if (!mbar_wait(&sfull[set % kSets], (set / kSets) & 1, abort_flag, err)) break;
+        }
+        if (!mbar_wait(&full[st], (j / STAGES) & 1, abort_flag, err)) break;
+        tc_fence_after();
+        const uint32_t w0 = smem_u32(smem + st * C::STAGE_BYTES), x0 = w0 + C::W_BYTES;
+        const uint32_t d = tmem + buf * C::ACC, sf = tmem + C::SETS_AT + (set % kSets) * C::SET_COLS;
+        const uint32_t idesc = idesc_mx_e4m3(kBlk, NT, j % kSet);
+#pragma unroll
+        for (int m = 0; m < MATS; ++m)
+#pragma unroll
+          for (int k = 0; k < kBlk / 32; ++k)
+            mma_mx_ss(d + m * NT, desc_kmajor_sw128(w0 + m * kBlk * kBlk + k * 32), desc_kmajor_sw128(x0 + k * 32),
+                      idesc, sf + 4 * m, sf + 4 * MATS, j % (kSet * kChunk) != 0 || k != 0);
+        mma_commit(&empty[st]);
+        const bool last = j + 1 == nkb;
+        if (last || (j + 1) % kSet == 0) mma_commit(&sempty[set % kSets]);
+        if (last || (j + 1) % (kSet * kChunk) == 0) mma_commit(&tfull[buf]);
+      }
+      // all of them must be done before tensor memory is released
+      mma_commit(drain);
+      volatile int no_abort = 0;
+      mbar_wait(drain, 0, &no_abort, err);
+    }
+  } else {
+    pdl_wait();
+    const int quad = warp & 3;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    // scale set s: a word per row for its K blocks; the weights' is the same for all rows of the tile
+    auto feed = [&](int s) {
+      if (!mbar_wait_warp(&sempty[s % kSets], ((s / kSets) & 1) ^ 1u, abort_flag, err)) return false;
+      const int kb = kb0 + s * kSet, n = min(kSet, kb0 + nkb - kb);
+      const uint32_t at = tmem + lanes + C::SETS_AT + (s % kSets) * C::SET_COLS;
+      uint32_t w[MATS], x[4];
+      w[0] = scale_word(a.w.scale + (size_t)wt * kblocks + kb, n);
+      if constexpr (MATS == 2) w[1] = scale_word(a.w3.scale + (size_t)wt * kblocks + kb, n);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int m = m0 + c * 32 + lane;
+        x[c] = c * 32 < NT && m < a.M ? scale_word(a.x.scale + (size_t)m * kblocks + kb, n) : 0x7f7f7f7fu;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int m = 0; m < MATS; ++m) tmem_st4(at + 4 * m, w[m], w[m], w[m], w[m]);
+      tmem_st4(at + 4 * MATS, x[0], x[1], x[2], x[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sfull[s % kSets]);
+      return true;
+    };
+    float acc[MATS * NT];
+#pragma unroll
+    for (int i = 0; i < MATS * NT; ++i) acc[i] = 0.f;
+    bool ok = true;
+    int fed = 0;
+    for (int c = 0; ok && c < nchunks; ++c) {
+      // the sets of this chunk and of the next one: those they replace belong to the
+      // chunk before, whose sums are in registers already
+      for (const int upto = min(nsets, (c + 2) * kChunk); ok && fed < upto; ++fed) ok = feed(fed);
+      if (!ok || !(ok = mbar_wait_warp(&tfull[c & 1], (c >> 1) & 1, abort_flag, err))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < MATS * NT; i += 16) {
+        uint32_t u[16];
+        tmem_ld16(tmem + lanes + (c & 1) * C::ACC + i, u);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc[i + k] += __uint_as_float(u[k]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[c & 1]);
+    }
+    // lane l of quarter q holds weight row 32 q + l.  (The last chunk's sums come after
+    // every instruction, and so after every read of the ring.)
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < MATS * NT; ++i) part_s[i * kBlk + quad * 32 + lane] = acc[i];
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();
+
+  if (warp >= 2) {
+    const int col = wt * kBlk + 4 * lane;
+    const uint32_t base = smem_u32(part_s) + 16u * lane;
+    for (int t = t0 + (warp - 2); t < t1; t += 4) {
+      const size_t at = (size_t)(m0 + t) * a.N + col;
+      float4 res = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (MATS == 1 && a.res && col < a.N) res = get4(a.res, a.y_dtype, at);
+      float4 v[MATS];
+#pragma unroll
+      for (int m = 0; m < MATS; ++m) {
+        float4 p[kMaxSplits];
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r)
+          if (r < splits) p[r] = ld_dsmem_f4(mapa_shared(base + (uint32_t)((m * NT + t) * kBlk * 4), (uint32_t)r));
+        v[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < kMaxSplits; ++r)
+          if (r < splits) v[m] = make_float4(v[m].x + p[r].x, v[m].y + p[r].y, v[m].z + p[r].z, v[m].w + p[r].w);
+      }
+      if constexpr (MATS == 1) {
+        v[0] = make_float4(v[0].x + res.x, v[0].y + res.y, v[0].z + res.z, v[0].w + res.w);
+        if (col < a.N) put4(a.y, a.y_dtype, at, v[0]);
+      } else {
+        v[0] = make_float4(gated(v[0].x, v[1].x), gated(v[0].y, v[1].y), gated(v[0].z, v[1].z), gated(v[0].w, v[1].w));
+        if (a.y_dtype != TB_E4M3) {
+          if (col < a.N) put4(a.y, a.y_dtype, at, v[0]);
+          continue;
+        }
+        // (columns past N hold zeros: weight rows past N read as zeros)
+        float top = fmaxf(fmaxf(finite_mag(v[0].x), finite_mag(v[0].y)), fmaxf(finite_mag(v[0].z), finite_mag(v[0].w)));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int e = block_exponent(top);
+        const float inv = pow2i(-e);
+        if (col < a.N)
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + at) =
+              codes_of4(to_code(v[0].x, inv), to_code(v[0].y, inv), to_code(v[0].z, inv), to_code(v[0].w, inv));
+        if (lane == 0) a.y_scale[(size_t)(m0 + t) * ((a.N + kBlk - 1) / kBlk) + wt] = (uint8_t)(e + 127);
+      }
+    }
+  }
+
+  // no CTA leaves (and frees its shared memory) while another still reads it
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStream_t s) {
+  using C = FewCfg<NT, MATS, CPS>;
+  CUtensorMap tw, tw3, tx;
+  cudaError_t e = make_tmap_rows(&tw, 1, a.w.codes, 1, (uint64_t)a.N, (uint64_t)a.K, kBlk, kBlk);
+  if (e != cudaSuccess) return e;
+  tw3 = tw;
+  if (MATS == 2 && (e = make_tmap_rows(&tw3, 1, a.w3.codes, 1, (uint64_t)a.N, (uint64_t)a.K, kBlk, kBlk)) != cudaSuccess)
+    return e;
+  e = make_tmap_rows(&tx, 1, a.x.codes, 1, (uint64_t)a.M, (uint64_t)a.K, kBlk, NT);
+  if (e != cudaSuccess) return e;
+  static bool set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!set[dev]) {
+    e = cudaFuncSetAttribute(k_e4m3_few<NT, MATS, CPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    set[dev] = true;
+  }
+  const int wtiles = (a.N + kBlk - 1) / kBlk, kblocks = (a.K + kBlk - 1) / kBlk;
+  const long long tiles = (long long)wtiles * ((a.M + NT - 1) / NT);
+  const long long slots = (long long)CPS * sm_count();
+  const int sp = tiles > slots ? 1 : skinny_split_count((int)tiles, kblocks, (int)slots);
+  if (tiles * sp > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * sp));
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = sp;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_e4m3_few<NT, MATS, CPS>, tw, tw3, tx, a, wtiles, sp, device_error_word());
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_e4m3_few(const GemmArgs& a, cudaStream_t s) {
+  if (a.M <= 16) return go<16, 1, 2>(a, s);
+  if (a.M <= 32) return go<32, 1, 2>(a, s);
+  if (a.M <= 64) return go<64, 1, 2>(a, s);
+  return go<128, 1, 1>(a, s);
+}
+cudaError_t launch_gated_e4m3_few(const GemmArgs& a, cudaStream_t s) {
+  if (a.M <= 16) return go<16, 2, 2>(a, s);
+  if (a.M <= 32) return go<32, 2, 2>(a, s);
+  return go<64, 2, 1>(a, s);
+}
+
+}  // namespace tb

@@ -241,6 +241,22 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t adesc, uint6
       : "memory");
 }
 
+// The same with a power-of-two scale (one exponent byte, 2^(byte-127)) for each
+// 32 elements of K of a row of A and of B (kind::mxf8f6f4, scale_vec::1X).  The
+// scale of row r lies in tensor memory at lane r % 32, column sf + r / 32, in the
+// byte of the 32-bit word that the instruction descriptor names (idesc_mx_e4m3),
+// the same in each of the four quarters of the lanes.
+__device__ __forceinline__ void mma_mx_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
 // Batched issue of the MMAs of one tile, for an issuing thread that must spend
 // as few instructions per MMA as possible: descriptors are passed as their low
 // and high 32-bit words, each MMA's operand offset is an immediate added to the
@@ -337,6 +353,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// 32 lanes x 4 and 1 consecutive 32-bit columns from registers into TMEM.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -391,6 +412,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn = fals
 // Instruction descriptor, kind::f8f6f4 with e4m3 A and B, both K-major, fp32 D.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Instruction descriptor, kind::mxf8f6f4 with e4m3 A and B, both K-major, exponent
+// bytes as scales; `byte` of a scale word counts for A and for B.
+__host__ __device__ constexpr uint32_t idesc_mx_e4m3(int M, int N, uint32_t byte = 0) {
+  return (byte << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) | (byte << 29);
 }
 
 // ---- CTA pairs (cta_group::2) --------------------------------------------

@@ -58,7 +58,8 @@ typedef enum {
 
 /* TB_I8 and TB_E4M3 are KV-cache storage types only (tb_kvcache.dtype): int8
  * codes with a per-row fp32 scale, and e4m3 codes with one fp32 scale per block
- * of tokens and KV head (tb_kvcache_append_rope, tb_kvcache_attn). */
+ * of tokens and KV head (tb_kvcache_append_rope, tb_kvcache_attn).  (TB_E4M3 also
+ * names the result of tb_gated_e4m3.) */
 typedef enum { TB_F32 = 0, TB_BF16 = 1, TB_I8 = 2, TB_E4M3 = 3 } tb_dtype;
 
 /* Bits of the device error word (tb_get_device_error). */
@@ -408,6 +409,62 @@ TB_API size_t tb_kvcache_attn_workspace_bytes(const tb_attn_cfg* cfg, const tb_k
  * are all below 2^-90. */
 TB_API tb_status tb_kvcache_attn(const tb_attn_cfg* cfg, const void* q, const tb_kvcache* kv, const int32_t* n_new,
                                  int32_t n, void* o, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Projections in 8 bits ----
+ * The projections around the cache operators, and the MLP, over 8-bit floating-point
+ * codes (e4m3: 4 exponent bits, 3 mantissa bits, no infinity): rows quantised with the
+ * norm in front of them, and their products with weights quantised once.
+ *
+ * tb_e4m3: a matrix of codes [rows, cols], row-major and dense, with one power-of-two
+ *  scale per block, as exponent bytes (the scale is 2^(byte-127); 255 reads as NaN):
+ *    rows (activations)   : blocks of 128 columns of a row, scale [rows, ceil(cols/128)];
+ *    weights ([out, in])  : blocks of 128 x 128, scale [ceil(rows/128), ceil(cols/128)].
+ *  The last block of a row (or column) may be shorter.  cols is a multiple of 16; codes
+ *  are 16-byte aligned, scales byte-aligned; rows·cols at most 2^39.
+ *    The scale of a block that these calls write is 2^e with e the smallest integer in
+ *    [-100, 120] for which the block's largest finite |x| is at most 448·2^e (-100 for a
+ *    block of zeros).  A value x is held as x / 2^e rounded to nearest even; infinities
+ *    and NaN as NaN.
+ * These calls need no workspace.  rows of 0 is an empty call that returns TB_OK. */
+typedef struct {
+  void *codes, *scale;
+  int32_t rows, cols;
+} tb_e4m3;
+
+/* Rows to codes, with the norm and the residual's addition on the way:
+ *   h = x + r,  codes of  h / sqrt(mean h^2 + eps) * g
+ *  x     : device, dense [out->rows, out->cols] of dtype (TB_F32 or TB_BF16).
+ *  r, h  : NULL, or both given: r dense [rows, cols] of r_dtype, h receives the sum in
+ *          dtype.  h may be x itself, or r itself where the types agree.  The norm takes
+ *          the fp32 sum, before h's rounding.
+ *  g     : device [cols] of dtype.
+ *  out   : rows; at most 32768 columns (TB_ERR_UNSUPPORTED above).
+ * Pointers 16-byte aligned; but for h, what is written overlaps nothing that is read. */
+TB_API tb_status tb_rmsnorm_e4m3(const void* x, int32_t dtype, const void* r, int32_t r_dtype, void* h, const void* g,
+                                 float eps, const tb_e4m3* out, void* stream);
+
+/* The rows x (device, dense [out->rows, out->cols] of dtype) to codes as they are, for
+ * instance the attention's output before its projection. */
+TB_API tb_status tb_quant_e4m3(const void* x, int32_t dtype, const tb_e4m3* out, void* stream);
+
+/* Weights w (device, [in, out] of dtype, as everywhere in this header) to codes:
+ * out->rows is `out`, out->cols is `in`.  Done once per weight set. */
+TB_API tb_status tb_pack_e4m3(const void* w, int32_t dtype, const tb_e4m3* out, void* stream);
+
+/* y[m, n] = res[m, n] + sum_k x[m, k] w[n, k]
+ *  x    : rows [M, K];  w : weights [N, K], N a multiple of 16.
+ *  res  : NULL, or device, dense [M, N] of y_dtype.
+ *  y    : device, dense [M, N] of y_dtype (TB_F32 or TB_BF16), 16-byte aligned.  It may
+ *         be res itself and overlaps nothing else that is read.
+ * Products and sums are fp32, rounded once to y_dtype. */
+TB_API tb_status tb_gemm_e4m3(const tb_e4m3* x, const tb_e4m3* w, const void* res, void* y, int32_t y_dtype, void* stream);
+
+/* The gated half of the MLP: SiLU(x·w1) * (x·w3), x rows [M, K], w1 and w3 weights
+ * [F, K], F a multiple of 16.  With y_dtype TB_F32 or TB_BF16, y is dense [M, F]; with
+ * TB_E4M3, y receives codes [M, F] and y_scale their scales [M, ceil(F/128)], rows as
+ * tb_gemm_e4m3 takes them (y_scale NULL otherwise). */
+TB_API tb_status tb_gated_e4m3(const tb_e4m3* x, const tb_e4m3* w1, const tb_e4m3* w3, void* y, int32_t y_dtype,
+                               void* y_scale, void* stream);
 
 #ifdef __cplusplus
 }

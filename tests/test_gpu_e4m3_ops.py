@@ -1,0 +1,343 @@
+"""The 8-bit projections against fp64, element by element (e4m3_helpers derives the
+tolerances)."""
+import numpy as np
+import pytest
+import torch
+
+import causal_gqa_attention_rmsnorm_gb300 as tb
+from e4m3_helpers import (BF16, CODE, F32, HALF, SCALE, bytes_of, check_product, check_rows, gated_and_off, make_rows,
+                          make_weight, product, random_codes, rows_np, weight_np)
+from oracle import e4m3 as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def no_error():
+    assert tb.tb_get_device_error(clear=True) == 0
+
+
+# ---- rows ---------------------------------------------------------------------
+
+def stream_rows(M, d, dtype, g):
+    """Rows as a residual stream has them: a few large channels, rows of many sizes."""
+    x = torch.randn(M, d, generator=g) * torch.exp2(torch.randint(-6, 7, (M, 1), generator=g).float())
+    x[:, torch.randint(0, d, (2,), generator=g)] *= 30
+    return x.to(dtype).cuda()
+
+
+# A thread adds at most 64 squares one after another, then 5 + 15 levels; a square root,
+# two quotients and two products follow, and the sum x + r before them: 100 roundings.
+NORM_OFF = 100 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("M,d", [(1, 16), (1, 4096), (3, 128), (7, 144), (5, 768), (305, 1008), (306, 4096), (400, 784),
+                                 (2, 11008), (310, 16384), (311, 16400), (3, 32768), (1, 14336), (700, 32)])
+@pytest.mark.parametrize("dtype,r_dtype", [(BF16, None), (BF16, BF16), (BF16, F32), (F32, None), (F32, BF16), (F32, F32)])
+def test_norm(M, d, dtype, r_dtype):
+    g = gen(M * 7 + d)
+    x = stream_rows(M, d, dtype, g)
+    gain = (1 + 0.1 * torch.randn(d, generator=g)).to(dtype).cuda()
+    r = None if r_dtype is None else torch.randn(M, d, generator=g).to(r_dtype).cuda()
+    out, h = tb.tb_rmsnorm_e4m3(x, gain, 1e-5, r=r)
+    no_error()
+    total = f64(x) + (0 if r is None else f64(r))
+    if r is None:
+        assert h is None
+    else:
+        one = np.abs(f64(h) - total) <= 2 * (HALF[dtype] + 2.0 ** -24) * np.abs(total)
+        assert one.all()
+    y = ref.norm(total, f64(gain), 1e-5)
+    # (the sum's own rounding is relative to itself: x + r is one fp32 addition)
+    check_rows(bytes_of(out.codes), bytes_of(out.scale), y, NORM_OFF * np.abs(y))
+
+
+@pytest.mark.parametrize("M,d", [(1, 16), (1, 4096), (3, 128), (7, 144), (305, 784), (2, 11008), (309, 11008), (1, 65536),
+                                 (3, 53248), (313, 8208)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_quant(M, d, dtype):
+    x = stream_rows(M, d, dtype, gen(M + d))
+    out = tb.tb_quant_e4m3(x)
+    no_error()
+    # the quotients are exact: nothing but the codes' rounding
+    check_rows(bytes_of(out.codes), bytes_of(out.scale), f64(x), np.zeros((M, d)))
+    e = bytes_of(out.scale).astype(int) - 127
+    assert (e == ref.rows_exponents(f64(x))).all()
+
+
+def test_quant_ties_go_to_the_even_code_and_borders_keep_their_scale():
+    x = torch.zeros(3, 256)
+    x[0, :8] = torch.tensor([448.0, 17.0, 19.0, -17.0, 2.0 ** -10, 3 * 2.0 ** -10, 1.0625, 1.1875])
+    x[1, :2] = torch.tensor([448.0 * (1 + 2.0 ** -23), 1.0])           # one step above: the next scale
+    x[1, 128:130] = torch.tensor([448.0 * 2.0 ** -60, 2.0 ** -60])
+    x[2, :2] = torch.tensor([2.0 ** -140, 3e38])
+    x[2, 128:130] = torch.tensor([2.0 ** -149, 0.0])                    # below the smallest scale
+    out = tb.tb_quant_e4m3(x.cuda())
+    v = ref.VALUES[bytes_of(out.codes)]
+    assert v[0, :8].tolist() == [448, 16, 20, -16, 0, 2.0 ** -8, 1.0, 1.25]
+    e = bytes_of(out.scale).astype(int) - 127
+    assert e.tolist() == [[0, -100], [1, -60], [120, -100]]
+    assert (v[0, 128:] == 0).all() and v[1, 128] == 448 and v[2, 128] == 0
+
+
+def test_rows_with_infinities_and_nan():
+    inf, nan = float("inf"), float("nan")
+    x = torch.randn(4, 400, generator=gen(2))
+    x[0, 5], x[0, 200], x[1, 399], x[2, :128] = nan, inf, -inf, nan
+    for dtype in (BF16, F32):
+        y = x.to(dtype).cuda()
+        out = tb.tb_quant_e4m3(y)
+        check_rows(bytes_of(out.codes), bytes_of(out.scale), f64(y), np.zeros((4, 400)))
+        assert bytes_of(out.scale)[2, 0] == 27                       # no finite value at all: as a block of zeros
+        # the norm: a NaN or an infinity is in its row's mean; the others are as they were
+        n, _ = tb.tb_rmsnorm_e4m3(y, torch.ones(400, dtype=dtype, device="cuda"), 1e-5)
+        alone, _ = tb.tb_rmsnorm_e4m3(y[3:].clone(), torch.ones(400, dtype=dtype, device="cuda"), 1e-5)
+        assert np.isnan(ref.VALUES[bytes_of(n.codes)[0]]).all() and np.isnan(ref.VALUES[bytes_of(n.codes)[2]]).all()
+        v = ref.VALUES[bytes_of(n.codes)[1]]
+        assert np.isnan(v[399]) and (v[:399] == 0).all()
+        assert (bytes_of(n.codes)[3] == bytes_of(alone.codes)[0]).all()
+        assert (bytes_of(n.scale)[3] == bytes_of(alone.scale)[0]).all()
+    no_error()
+
+
+@pytest.mark.parametrize("M,d", [(2, 400), (400, 768)])
+def test_norm_in_place_gives_the_same(M, d):
+    g = gen(5)
+    x, r = (torch.randn(M, d, generator=g).to(BF16).cuda() for _ in range(2))
+    gain = torch.randn(d, generator=g).to(BF16).cuda()
+    out, h = tb.tb_rmsnorm_e4m3(x, gain, 1e-6, r=r)
+    for into in ("x", "r"):
+        a, b = x.clone(), r.clone()
+        mine, got = tb.tb_rmsnorm_e4m3(a, gain, 1e-6, r=b, h=a if into == "x" else b)
+        assert torch.equal(got, h) and (bytes_of(mine.codes) == bytes_of(out.codes)).all()
+    # rows of any leading shape
+    again, h3 = tb.tb_rmsnorm_e4m3(x.view(2, M // 2, d), gain, 1e-6, r=r.view(2, M // 2, d))
+    assert h3.shape == (2, M // 2, d) and (bytes_of(again.codes) == bytes_of(out.codes)).all()
+
+
+@pytest.mark.parametrize("K,N", [(16, 16), (128, 128), (144, 272), (768, 2304), (400, 48)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_pack(K, N, dtype):
+    g = gen(K + N)
+    w = (0.02 * torch.randn(K, N, generator=g) * torch.exp2(torch.randint(-8, 8, (K, 1), generator=g).float())).to(dtype)
+    w[0, 0], w[K - 1, N - 1] = float("nan"), float("inf")
+    got = tb.tb_pack_e4m3(w.cuda())
+    no_error()
+    x = f64(w).T
+    e = bytes_of(got.scale).astype(int) - 127
+    assert (e == ref.weight_exponents(x)).all()
+    v = weight_np(got)
+    fine = np.isfinite(x)
+    assert (np.isnan(v) == ~fine).all()
+    s = np.repeat(np.repeat(np.ldexp(1.0, e), 128, 0)[:N], 128, 1)[:, :K]
+    assert (np.abs(v - np.where(fine, x, 0))[fine] <= (ref.half_step(np.where(fine, x, 0) / s) * s)[fine]).all()
+
+
+# ---- the product ----------------------------------------------------------------
+
+SIZES = [(1, 16, 16), (1, 128, 128), (1, 2304, 768), (3, 144, 400), (16, 256, 512), (17, 112, 2064), (33, 400, 640),
+         (64, 128, 4096), (65, 272, 1168), (128, 768, 2176), (129, 144, 144), (200, 1040, 912), (300, 2304, 768),
+         (7, 4096, 1024), (2, 128, 9216), (5, 32, 14336)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("dtype,with_res", [(F32, False), (BF16, True)])
+def test_gemm(M, N, K, dtype, with_res):
+    g = gen(M + N + K)
+    x, w = make_rows(tb, M, K, g), make_weight(tb, N, K, g)
+    res = (torch.randn(M, N, generator=g) * 100).to(dtype).cuda() if with_res else None
+    y = tb.tb_gemm_e4m3(x, w, res=res, y_dtype=tb.TB_F32 if dtype is F32 else tb.TB_BF16)
+    no_error()
+    assert y.dtype is dtype and y.shape == (M, N)
+    check_product(y, *product(rows_np(x), weight_np(w), None if res is None else f64(res)), K, dtype)
+    if with_res:                                    # in place
+        z = tb.tb_gemm_e4m3(x, w, res=res, y=res)
+        assert z is res and torch.equal(z, y)
+
+
+def test_gemm_every_code_and_scale_counts():
+    """Rows of one code each against weights of single ones: every code, at every scale
+    byte that keeps the product an fp32 value, comes back exactly."""
+    K = 256
+    codes = torch.zeros(256, K, dtype=torch.uint8)
+    codes[:, 130] = torch.arange(256, dtype=torch.uint8)
+    scale = torch.full((256, 2), 127, dtype=torch.uint8)
+    scale[:, 1] = 20 + (torch.arange(256) * 37 % 200).to(torch.uint8)
+    w = torch.zeros(256, K, dtype=torch.uint8)
+    w[:, 130] = 0x38                                # 1.0
+    ws = torch.tensor([[127, 127], [127, 130]], dtype=torch.uint8)
+    y = tb.tb_gemm_e4m3(tb.E4M3Rows(codes.view(CODE).cuda(), scale.view(SCALE).cuda()),
+                        tb.E4M3Weight(w.view(CODE).cuda(), ws.view(SCALE).cuda()), y_dtype=tb.TB_F32)
+    no_error()
+    got = y.cpu().numpy().astype(np.float64)
+    v = ref.VALUES[np.arange(256)] * np.ldexp(1.0, scale[:, 1].numpy().astype(int) - 127)
+    for n, f in ((0, 1.0), (127, 1.0), (128, 8.0), (255, 8.0)):
+        assert np.array_equal(got[:, n], v * f, equal_nan=True)
+
+
+def test_gemm_nan_stays_in_its_row_and_its_column():
+    g = gen(9)
+    M, N, K = 70, 272, 528
+    x, w = make_rows(tb, M, K, g), make_weight(tb, N, K, g)
+    clean = tb.tb_gemm_e4m3(x, w)
+    x.codes.view(torch.uint8)[3, 100] = 0x7F
+    x.scale.view(torch.uint8)[66, 4] = 255
+    w.codes.view(torch.uint8)[5, 527] = 0xFF
+    w.scale.view(torch.uint8)[2, 1] = 255           # rows 256 to 271
+    y = tb.tb_gemm_e4m3(x, w)
+    no_error()
+    hit = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    hit[3], hit[66], hit[:, 5], hit[:, 256:] = True, True, True, True
+    assert torch.equal(torch.isnan(y), hit)
+    assert torch.equal(y[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("M", [1, 16, 40, 100, 130])
+def test_gemm_writes_its_rows_only(M):
+    g = gen(M)
+    N, K = 144, 272
+    buf = torch.full((M + 5, N), 7.0, dtype=BF16, device="cuda")
+    x, w = make_rows(tb, M, K, g), make_weight(tb, N, K, g)
+    tb.tb_gemm_e4m3(x, w, y=buf[2:2 + M])
+    no_error()
+    assert (buf[:2] == 7).all() and (buf[2 + M:] == 7).all()
+    check_product(buf[2:2 + M], *product(rows_np(x), weight_np(w)), K, BF16)
+
+
+# ---- the gated half ---------------------------------------------------------------
+
+@pytest.mark.parametrize("M,F,K", [(1, 16, 16), (1, 256, 128), (5, 144, 400), (16, 2048, 768), (17, 272, 2064), (32, 400, 1024),
+                                   (33, 128, 640), (65, 144, 272), (130, 1040, 528), (333, 2048, 768), (2, 128, 9216)])
+@pytest.mark.parametrize("out_dtype", ["codes", BF16, F32])
+def test_gated(M, F, K, out_dtype):
+    g = gen(M + F + K)
+    x, w1, w3 = make_rows(tb, M, K, g), make_weight(tb, F, K, g), make_weight(tb, F, K, g)
+    # gates of sizes where SiLU bends
+    w1.scale.view(torch.uint8).sub_(int(np.log2(K) / 2) + 11)
+    exact, off = gated_and_off(rows_np(x), weight_np(w1), weight_np(w3), K)
+    if out_dtype == "codes":
+        out = tb.tb_gated_e4m3(x, w1, w3)
+        no_error()
+        check_rows(bytes_of(out.codes), bytes_of(out.scale), exact, off)
+    else:
+        y = tb.tb_gated_e4m3(x, w1, w3, out_dtype=tb.TB_F32 if out_dtype is F32 else tb.TB_BF16)
+        no_error()
+        assert y.dtype is out_dtype
+        assert (np.abs(f64(y) - exact) <= off + 2 * HALF[out_dtype] * (np.abs(exact) + off)).all()
+
+
+def test_gated_far_gates():
+    """Gates far below and above zero: SiLU gives 0 and the gate itself, not NaN."""
+    M, F, K = 4, 128, 128
+    x = torch.zeros(M, K, dtype=torch.uint8)
+    x[:, 0] = 0x38
+    w1, w3 = torch.zeros(F, K, dtype=torch.uint8), torch.zeros(F, K, dtype=torch.uint8)
+    w1[:, 0], w3[:, 0] = torch.arange(F, dtype=torch.uint8).bitwise_xor(0x80), 0x38
+    w1[64:, 0] = 0x78                                  # 256
+    one = torch.full((M, 1), 127, dtype=torch.uint8).view(SCALE).cuda()
+    big = torch.full((1, 1), 127, dtype=torch.uint8).view(SCALE).cuda()
+    y = tb.tb_gated_e4m3(tb.E4M3Rows(x.view(CODE).cuda(), one), tb.E4M3Weight(w1.view(CODE).cuda(), big),
+                         tb.E4M3Weight(w3.view(CODE).cuda(), big), out_dtype=tb.TB_F32)
+    no_error()
+    gates = ref.VALUES[w1[:, 0].numpy()]
+    with np.errstate(over="ignore"):
+        want = ref.silu(gates)
+    assert (np.abs(f64(y) - want[None]) <= 8 * 2.0 ** -24 * np.abs(want) + 2.0 ** -126).all()
+
+
+def test_empty_calls():
+    w = make_weight(tb, 32, 64, gen(1))
+    x = tb.E4M3Rows.empty(0, 64)
+    assert tb.tb_gemm_e4m3(x, w).shape == (0, 32)
+    assert tb.tb_gated_e4m3(x, w, w).rows == 0
+    assert tb.tb_gated_e4m3(x, w, w, out_dtype=tb.TB_BF16).shape == (0, 32)
+    e = torch.empty(0, 64, dtype=BF16, device="cuda")
+    assert tb.tb_quant_e4m3(e).rows == 0
+    out, h = tb.tb_rmsnorm_e4m3(e, torch.ones(64, dtype=BF16, device="cuda"), 1e-5, r=e)
+    assert out.rows == 0 and h.shape == (0, 64)
+    no_error()
+
+
+# ---- together -----------------------------------------------------------------------
+
+def test_repeated_calls_streams_and_graphs_give_the_same_bits():
+    g = gen(11)
+    M, d, f = 40, 512, 1040
+    x = torch.randn(M, d, generator=g).to(BF16).cuda()
+    gain = torch.ones(d, dtype=BF16, device="cuda")
+    w1, w3, w2 = (tb.tb_pack_e4m3((0.05 * torch.randn(*s, generator=g)).to(BF16).cuda()) for s in ((d, f), (d, f), (f, d)))
+    n, a, y = tb.E4M3Rows.empty(M, d), tb.E4M3Rows.empty(M, f), torch.empty_like(x)
+
+    def mlp(stream=None):
+        tb.tb_rmsnorm_e4m3(x, gain, 1e-5, out=n, stream=stream)
+        tb.tb_gated_e4m3(n, w1, w3, out=a, stream=stream)
+        return tb.tb_gemm_e4m3(a, w2, res=x, y=y, stream=stream)
+
+    first = mlp().clone()
+    for _ in range(3):
+        assert torch.equal(mlp(), first)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y.zero_()
+    torch.cuda.synchronize()
+    mlp(side)
+    side.synchronize()
+    assert torch.equal(y, first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mlp()
+    x2 = x.flip(0).contiguous()
+    x.copy_(x2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, first.flip(0))               # rows do not know each other
+    no_error()
+
+
+@pytest.mark.parametrize("B,n", [(3, 1), (2, 37)])
+def test_a_decoder_layer_in_8_bits(B, n):
+    """Norm, projection, append with rotation, attention, quantisation, projection onto
+    the stream, norm, gated half, projection onto the stream, over an e4m3 cache: each
+    step against fp64 on the very inputs that it got."""
+    H, Hkv, dh, f, T = 8, 2, 64, 1040, 256
+    d, M = H * dh, B * n
+    g = gen(B * n)
+    x = torch.randn(M, d, generator=g).to(BF16).cuda()
+    gains = [(1 + 0.1 * torch.randn(d, generator=g)).to(BF16).cuda() for _ in range(2)]
+    shapes = dict(qkv=(d, (H + 2 * Hkv) * dh), o=(d, d), w1=(d, f), w3=(d, f), w2=(f, d))
+    w = {k: tb.tb_pack_e4m3((0.05 * torch.randn(*s, generator=g)).to(BF16).cuda()) for k, s in shapes.items()}
+    rope = tb.tb_rope_table(dh, T, 1e4)
+    kv = tb.KVCache.empty_e4m3(B, Hkv, T, dh, 64)
+    cfg = tb.AttnConfig(H=H, Hkv=Hkv, dh=dh)
+
+    n1, _ = tb.tb_rmsnorm_e4m3(x, gains[0], 1e-5)
+    qkv = tb.tb_gemm_e4m3(n1, w["qkv"])
+    q, k, v = qkv.view(B, n, -1, dh).split([H, Hkv, Hkv], 2)
+    qr = tb.tb_kvcache_append_rope(kv, k, v, rope, q=q)
+    o = tb.tb_kvcache_attn(cfg, qr, kv)
+    o8 = tb.tb_quant_e4m3(o.view(M, d))
+    branch = tb.tb_gemm_e4m3(o8, w["o"])
+    n2, h = tb.tb_rmsnorm_e4m3(x, gains[1], 1e-5, r=branch)
+    a = tb.tb_gated_e4m3(n2, w["w1"], w["w3"])
+    y = tb.tb_gemm_e4m3(a, w["w2"], res=h)
+    no_error()
+
+    z = ref.norm(f64(x), f64(gains[0]), 1e-5)
+    check_rows(bytes_of(n1.codes), bytes_of(n1.scale), z, NORM_OFF * np.abs(z))
+    check_product(qkv, *product(rows_np(n1), weight_np(w["qkv"])), d, BF16)
+    check_rows(bytes_of(o8.codes), bytes_of(o8.scale), f64(o).reshape(M, d), np.zeros((M, d)))
+    check_product(branch, *product(rows_np(o8), weight_np(w["o"])), d, BF16)
+    total = f64(x) + f64(branch)
+    assert (np.abs(f64(h) - total) <= 2 * HALF[BF16] * np.abs(total) + 2.0 ** -23 * np.abs(total)).all()
+    z = ref.norm(total, f64(gains[1]), 1e-5)
+    check_rows(bytes_of(n2.codes), bytes_of(n2.scale), z, NORM_OFF * np.abs(z))
+    exact, off = gated_and_off(rows_np(n2), weight_np(w["w1"]), weight_np(w["w3"]), d)
+    check_rows(bytes_of(a.codes), bytes_of(a.scale), exact, off)
+    check_product(y, *product(rows_np(a), weight_np(w["w2"]), f64(h)), f, BF16)
