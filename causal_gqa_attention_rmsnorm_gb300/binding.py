@@ -119,6 +119,8 @@ def lib() -> ctypes.CDLL:
         L.tbx_decode_chunk_keys.restype = c_int32
         L.tbx_set_stat_poll_ns.argtypes = [ctypes.c_uint64]
         L.tbx_set_stat_poll_ns.restype = ctypes.c_uint64
+        L.tbx_e4m3_form.argtypes = [c_int32]
+        L.tbx_e4m3_form.restype = c_int32
         L.tb_embed.argtypes = [c_void_p, c_int32, c_int32, c_int32, c_void_p, ctypes.c_int64, c_void_p, c_void_p]
         L.tb_lm_head_packed_bytes.argtypes = [P(tb_head_cfg)]
         L.tb_lm_head_packed_bytes.restype = c_size_t
@@ -442,6 +444,12 @@ def tbx_set_stat_poll_ns(ns: int) -> int:
     RMSNorm-1 statistics before forming its rows' scales itself; returns the
     previous value."""
     return int(lib().tbx_set_stat_poll_ns(int(ns)))
+
+
+def tbx_e4m3_form(form: int) -> int:
+    """Test hook: the kernel that later 8-bit products take (0: by the rule, 1: few
+    rows, 2: many rows); returns the previous value."""
+    return int(lib().tbx_e4m3_form(int(form)))
 
 
 def tbx_trace_enable(slots: int) -> None:

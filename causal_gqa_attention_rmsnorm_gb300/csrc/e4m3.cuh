@@ -82,5 +82,8 @@ struct GemmArgs {
 // e4m3_gemm_few.cu: any sizes
 cudaError_t launch_gemm_e4m3_few(const GemmArgs& a, cudaStream_t s);
 cudaError_t launch_gated_e4m3_few(const GemmArgs& a, cudaStream_t s);
+// e4m3_gemm_many.cu: CTA pairs, any sizes
+cudaError_t launch_gemm_e4m3_many(const GemmArgs& a, cudaStream_t s);
+cudaError_t launch_gated_e4m3_many(const GemmArgs& a, cudaStream_t s);
 
 }  // namespace tb

@@ -3,6 +3,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "e4m3.cuh"
 
 namespace tb {
@@ -66,6 +68,14 @@ tb_status check_weights(const tb_e4m3* w, const char* name, const tb_e4m3* x, bo
   if (w->cols != x->cols)
     return report(TB_ERR_INVALID_ARG, "%s has %d columns, x has %d", name, w->cols, x->cols);
   return TB_OK;
+}
+
+// Which kernel a product takes.
+std::atomic<int> g_form{0};            // test hook: 1 few, 2 many
+bool many(const GemmArgs& a) {
+  const int form = g_form.load(std::memory_order_relaxed);
+  if (form) return form == 2;
+  return a.M >= 256 && (a.y_dtype != TB_F32 || a.K <= 2048);
 }
 
 RowsArgs rows_args(const void* x, const tb_e4m3* out) {
@@ -172,7 +182,8 @@ tb_status tb_gemm_e4m3(const tb_e4m3* x, const tb_e4m3* w, const void* res, void
   a.res = res;
   a.y = y;
   a.y_dtype = y_dtype;
-  return done(launch_gemm_e4m3_few(a, (cudaStream_t)stream), "tb_gemm_e4m3");
+  return done(many(a) ? launch_gemm_e4m3_many(a, (cudaStream_t)stream) : launch_gemm_e4m3_few(a, (cudaStream_t)stream),
+              "tb_gemm_e4m3");
 }
 
 tb_status tb_gated_e4m3(const tb_e4m3* x, const tb_e4m3* w1, const tb_e4m3* w3, void* y, int32_t y_dtype,
@@ -203,7 +214,12 @@ tb_status tb_gated_e4m3(const tb_e4m3* x, const tb_e4m3* w1, const tb_e4m3* w3, 
   a.y = y;
   a.y_dtype = y_dtype;
   a.y_scale = static_cast<uint8_t*>(y_scale);
-  return done(launch_gated_e4m3_few(a, (cudaStream_t)stream), "tb_gated_e4m3");
+  return done(many(a) ? launch_gated_e4m3_many(a, (cudaStream_t)stream) : launch_gated_e4m3_few(a, (cudaStream_t)stream),
+              "tb_gated_e4m3");
 }
+
+// Test hook: the kernel that later products of this process take (0: by the rule, 1:
+// few rows, 2: many rows).  Returns the previous value.
+TB_API int32_t tbx_e4m3_form(int32_t form) { return g_form.exchange(form); }
 
 }  // extern "C"

@@ -1,0 +1,405 @@
+// The products of e4m3_gemm_few.cu for many rows: 256 x 256 tiles on CTA pairs.
+//
+// The clusters of two CTAs walk the tiles (persistent).  A CTA stages its own 128 rows
+// of X and 128 rows of W per K block of 128 (32 KB, six stages); the even CTA issues
+// M = 256 instructions that read B from both CTAs' shared memory.  In the gated product
+// the even CTA stages rows of W1 and the odd one the same rows of W3, so that the
+// accumulator's columns 0..127 are gates and 128..255 what they gate: one tile is one
+// block of 128 columns of the result, and a row's scale is decided in one thread.
+//   warp 0      TMA;
+//   warp 1      issues the instructions (even CTA);
+//   warps 2..5  epilogue, a row of the tile per lane;
+//   warps 6..9  put the scales into tensor memory, four K blocks at a time.
+// Tensor memory holds two accumulators of 256 columns and two scale sets of 12, which
+// is more than its 512 columns: accumulator 0 takes columns 0..255, accumulator 1
+// columns 224..479, and the 32 columns that they share are read first when a tile is
+// finished; the next tile's instructions wait for that (and not for the rest).
+#include <algorithm>
+
+#include "e4m3_epilogue.cuh"
+#include "gemm_tc.cuh"
+#include "sm100_ptx.cuh"
+
+namespace tb {
+namespace {
+
+using namespace ptx;
+
+constexpr int kSet = 4;          // K blocks per scale set
+constexpr int kRowsCta = 128;    // rows of X per CTA
+
+struct ManyCfg {
+  static constexpr int STAGES = 6;
+  static constexpr uint32_t A_BYTES = kRowsCta * kBlk, B_BYTES = 128 * kBlk, STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr uint32_t OFF_BAR = STAGES * STAGE_BYTES;
+  static constexpr uint32_t OFF_EPI = OFF_BAR + 256;         // 4 warps x 32 rows x 144 bytes
+  static constexpr uint32_t ROW_BYTES = 144;                 // 128 bytes of a row and 16 of padding
+  static constexpr size_t SMEM = OFF_EPI + 4 * 32 * ROW_BYTES + 1024;
+  static constexpr uint32_t ACC1 = 224, SETS_AT = 480, SET_COLS = 16;
+  static constexpr int THREADS = 320;
+};
+
+// Tile -> (row unit of 256, column tile): column tiles fastest, or in groups of
+// `group` row units, rows fastest inside a group.
+__device__ __forceinline__ void place(int tile, int m_units, int n_tiles, int group, int& mu, int& nt) {
+  if (group <= 0) {
+    mu = tile / n_tiles;
+    nt = tile - mu * n_tiles;
+    return;
+  }
+  const int per = group * n_tiles, g = tile / per, first = g * group, gm = min(group, m_units - first);
+  const int local = tile - g * per;
+  nt = local / gm;
+  mu = first + local - nt * gm;
+}
+
+template <bool GATED>
+__global__ void __launch_bounds__(ManyCfg::THREADS, 1)
+    k_e4m3_many(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                const __grid_constant__ CUtensorMap tmW3, GemmArgs a, int m_units, int n_tiles, int group, int* err) {
+  using C = ManyCfg;
+  constexpr int STAGES = C::STAGES;
+  constexpr int COLS = GATED ? 128 : 256;               // columns of y per tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* empty = full + STAGES;
+  uint64_t* sfull = empty + STAGES;                     // scale sets
+  uint64_t* sempty = sfull + 2;
+  uint64_t* tfull = sempty + 2;                         // accumulators
+  uint64_t* tempty = tfull + 2;
+  uint64_t* shared_free = tempty + 2;                   // the columns both accumulators use
+  uint64_t* drain = shared_free + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((2 * STAGES + 8) * 8 + 8 <= 256, "barriers");
+
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tiles = m_units * n_tiles;
+  const int kblocks = (a.K + kBlk - 1) / kBlk, nsets = (kblocks + kSet - 1) / kSet;
+  const uint32_t rank = cluster_ctarank();
+  const int tile0 = (int)cluster_id_x(), tstep = (int)nclusters_x();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sfull[s], 8);        // four warps of each CTA, on the even CTA's
+      mbar_init(&sempty[s], 1);
+      mbar_init(&tfull[s], 1);
+      mbar_init(&tempty[s], 8);
+    }
+    mbar_init(shared_free, 8);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tmX);
+    prefetch_tmap(&tmW);
+    if (GATED) prefetch_tmap(&tmW3);
+  }
+  // both CTAs' barriers exist before either CTA's copies or commits reach them
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      pdl_wait();
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      bool ok = true;
+      for (int tile = tile0; ok && tile < tiles; tile += tstep) {
+        int mu, nt;
+        place(tile, m_units, n_tiles, group, mu, nt);
+        const int xrow = (mu * 2 + (int)rank) * kRowsCta;       // a block past M reads zeros
+        const CUtensorMap* tw = GATED && rank ? &tmW3 : &tmW;
+        const int wrow = GATED ? nt * 128 : nt * 256 + (int)rank * 128;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + stage * C::STAGE_BYTES;
+          // both CTAs' copies complete on the even CTA's barrier
+          const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
+          tma_load_3d_pair(&tmX, sa, fb, kb * kBlk, xrow, 0);
+          tma_load_3d_pair(tw, sa + C::A_BYTES, fb, kb * kBlk, wrow, 0);
+          if (issued < STAGES) ++issued;
+          if (++stage == STAGES) stage = 0, phase ^= 1u;
+        }
+      }
+      // every copy must have landed before the CTA may exit (the odd CTA waits for the
+      // even one at the cluster barrier)
+      if (rank == 0) {
+        volatile int no_abort = 0;
+        for (int i = 0; i < issued; ++i) {
+          if (stage == 0) stage = STAGES, phase ^= 1u;
+          --stage;
+          mbar_wait(&full[stage], phase, &no_abort, err);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // The whole warp walks the blocks; its elected lane issues (mma2_mx_k128).
+    if (rank == 0) {
+      const uint32_t elected = elect_one();
+      const uint64_t desc = desc_kmajor_sw128(smem_u32(smem));
+      const uint32_t desc_hi = (uint32_t)(desc >> 32), desc0 = (uint32_t)desc;
+      constexpr uint32_t NEXT = C::STAGE_BYTES >> 4;      // in a descriptor's address field
+      const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+      uint32_t stage = 0, phase = 0, set = 0;             // set: scale sets used so far
+      int local = 0;
+      bool ok = true;
+      for (int tile = tile0; ok && tile < tiles; tile += tstep, ++local) {
+        const int acc = local & 1;
+        if (!mbar_wait_warp(&tempty[acc], ((local >> 1) & 1) ^ 1u, abort_flag, err)) break;
+        if (local && !mbar_wait_warp(shared_free, (local - 1) & 1, abort_flag, err)) break;
+        const uint32_t d = tmem + acc * C::ACC1;
+        for (int kb = 0; ok && kb < kblocks; kb += kSet, ++set) {
+          const uint32_t sb = set & 1, sf = tmem + C::SETS_AT + sb * C::SET_COLS;
+          if (!(ok = mbar_wait_warp(&sfull[sb], (set >> 1) & 1, abort_flag, err))) break;
+#pragma unroll
+          for (int b = 0; b < kSet; ++b) {
+            if (kb + b < kblocks) {
+              if (!__all_sync(0xffffffffu, mbar_try_wait(full0 + stage * 8, phase)) &&
+                  !(ok = mbar_wait_warp(&full[stage], phase, abort_flag, err)))
+                break;
+              tc_fence_after();
+              const uint32_t lo = desc0 + stage * NEXT;
+              mma2_mx_k128(d, lo, lo + (C::A_BYTES >> 4), desc_hi, idesc_mx_e4m3(2 * kRowsCta, 256, b), sf, sf + 4,
+                           kb + b != 0, elected);
+              mma_commit_pair_elected(empty0 + stage * 8, elected);      // frees the stage in both CTAs
+              if (++stage == STAGES) stage = 0, phase ^= 1u;
+            }
+          }
+          mma_commit_pair_elected(smem_u32(&sempty[sb]), elected);
+        }
+        if (ok) mma_commit_pair_elected(smem_u32(&tfull[acc]), elected);
+      }
+      // all of them must be done before tensor memory is released
+      mma_commit_pair_elected(smem_u32(drain), elected);
+      volatile int no_abort = 0;
+      mbar_wait_warp(drain, 0, &no_abort, err);
+    }
+  } else if (warp >= 6) {
+    // Scales.  Words of set s + 1 are requested before the wait for set s's place.
+    pdl_wait();
+    const uint32_t at0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::SETS_AT;
+    const int nb = (a.N + kBlk - 1) / kBlk;
+    int set = 0;
+    int tile = tile0, s = 0;
+    uint32_t x[4], w[2];
+    auto load = [&]() {
+      int mu, nt;
+      place(tile, m_units, n_tiles, group, mu, nt);
+      const int kb = s * kSet, n = min(kSet, kblocks - kb);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int m = (mu * 2 + (int)rank) * kRowsCta + c * 32 + lane;
+        x[c] = m < a.M ? scale_word(a.x.scale + (size_t)m * kblocks + kb, n) : 0x7f7f7f7fu;
+      }
+      const int b0 = GATED ? nt : 2 * nt, b1 = GATED ? nt : 2 * nt + 1;
+      w[0] = scale_word(a.w.scale + (size_t)b0 * kblocks + kb, n);
+      w[1] = b1 < nb ? scale_word((GATED ? a.w3.scale : a.w.scale) + (size_t)b1 * kblocks + kb, n) : 0x7f7f7f7fu;
+    };
+    const uint32_t sfull_cl[2] = {mapa_shared(smem_u32(&sfull[0]), 0), mapa_shared(smem_u32(&sfull[1]), 0)};
+    bool more = tile < tiles;
+    if (more) load();
+    for (; more; ++set) {
+      if (!mbar_wait_warp(&sempty[set & 1], ((set >> 1) & 1) ^ 1u, abort_flag, err)) break;
+      tc_fence_after();
+      const uint32_t at = at0 + (set & 1) * C::SET_COLS;
+      tmem_st4(at, x[0], x[1], x[2], x[3]);
+      tmem_st4(at + 4, w[0], w[0], w[0], w[0]);
+      tmem_st4(at + 8, w[1], w[1], w[1], w[1]);
+      if (++s == nsets) s = 0, tile += tstep;
+      more = tile < tiles;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(sfull_cl[set & 1]);
+      if (more) load();
+    }
+  } else {
+    // Epilogue: a lane's row of the tile, 32 columns (or pairs of 32) at a time.
+    pdl_wait();
+    const int quad = warp & 3;
+    uint8_t* stage = smem + C::OFF_EPI + (warp - 2) * 32 * C::ROW_BYTES;
+    const uint32_t tempty_cl[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
+    const uint32_t shared_cl = mapa_shared(smem_u32(shared_free), 0);
+    const int sub_row = lane >> 3, sub = lane & 7;        // 8 lanes to a row of the stage
+    int local = 0;
+    for (int tile = tile0; tile < tiles; tile += tstep, ++local) {
+      const int acc = local & 1;
+      if (!mbar_wait_warp(&tfull[acc], (local >> 1) & 1, abort_flag, err)) break;
+      tc_fence_after();
+      int mu, nt;
+      place(tile, m_units, n_tiles, group, mu, nt);
+      const int row0 = (mu * 2 + (int)rank) * kRowsCta + quad * 32;
+      const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + acc * C::ACC1;
+      // Chunks of 32 columns of y, the one in the shared columns first: the last of
+      // accumulator 0, the first of accumulator 1.
+      constexpr int CHUNKS = COLS / 32;
+      auto chunk_of = [&](int i) { return acc ? i : (i + CHUNKS - 1) % CHUNKS; };
+      // the 32 values of this lane's row, finished but for the residual
+      auto take = [&](int i, float (&v)[32]) {
+        const int c = chunk_of(i);
+        uint32_t r[32], u[32];
+        tmem_ld32(taddr + c * 32, r);
+        if constexpr (GATED) tmem_ld32(taddr + 128 + c * 32, u);
+        tmem_wait_ld();
+        // the shared columns, or all of them, are in registers
+        if (i == 0 || i == CHUNKS - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(i == 0 ? shared_cl : tempty_cl[acc]);
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          v[j] = GATED ? gated(__uint_as_float(r[j]), __uint_as_float(u[j])) : __uint_as_float(r[j]);
+      };
+      if (GATED && a.y_dtype == TB_E4M3) {
+        float v[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) take(i, v[i]);
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) top = fmaxf(top, finite_mag(v[i][j]));
+        const int e = block_exponent(top);
+        const float inv = pow2i(-e);
+        uint4* my = reinterpret_cast<uint4*>(stage + lane * C::ROW_BYTES);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t q[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            q[j] = codes_of4(to_code(v[i][4 * j], inv), to_code(v[i][4 * j + 1], inv), to_code(v[i][4 * j + 2], inv),
+                             to_code(v[i][4 * j + 3], inv));
+          const int c = chunk_of(i);
+          my[2 * c] = make_uint4(q[0], q[1], q[2], q[3]);
+          my[2 * c + 1] = make_uint4(q[4], q[5], q[6], q[7]);
+        }
+        if (row0 + lane < a.M) a.y_scale[(size_t)(row0 + lane) * n_tiles + nt] = (uint8_t)(e + 127);
+        __syncwarp();
+        const int col = nt * 128 + sub * 16;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = sub_row + 4 * i, row = row0 + r;
+          if (row < a.M && col < a.N)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.y) + (size_t)row * a.N + col) =
+                *reinterpret_cast<const uint4*>(stage + r * C::ROW_BYTES + sub * 16);
+        }
+        __syncwarp();
+        continue;
+      }
+#pragma unroll 1
+      for (int i = 0; i < CHUNKS; ++i) {
+        // the residual is requested first; 8 lanes then finish and store a row's 32 columns
+        const int col = nt * COLS + chunk_of(i) * 32 + sub * 4;
+        float4 res[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = row0 + sub_row + 4 * k;
+          res[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (!GATED && a.res && row < a.M && col < a.N) res[k] = get4(a.res, a.y_dtype, (size_t)row * a.N + col);
+        }
+        float v[32];
+        take(i, v);
+        float4* my = reinterpret_cast<float4*>(stage + lane * C::ROW_BYTES);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) my[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = sub_row + 4 * k, row = row0 + r;
+          const float4 t = *reinterpret_cast<const float4*>(stage + r * C::ROW_BYTES + sub * 16);
+          if (row < a.M && col < a.N)
+            put4(a.y, a.y_dtype, (size_t)row * a.N + col,
+                 make_float4(t.x + res[k].x, t.y + res[k].y, t.z + res[k].z, t.w + res[k].w));
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  // Every instruction of the pair is done (the issuer waited on its drain) before
+  // either CTA releases the pair's tensor memory.
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <bool GATED> cudaError_t go(const GemmArgs& a, cudaStream_t s) {
+  using C = ManyCfg;
+  CUtensorMap tx, tw, tw3;
+  cudaError_t e = make_tmap_rows(&tx, 1, a.x.codes, 1, (uint64_t)a.M, (uint64_t)a.K, kBlk, kRowsCta);
+  if (e != cudaSuccess) return e;
+  e = make_tmap_rows(&tw, 1, a.w.codes, 1, (uint64_t)a.N, (uint64_t)a.K, kBlk, 128);
+  if (e != cudaSuccess) return e;
+  tw3 = tw;
+  if (GATED && (e = make_tmap_rows(&tw3, 1, a.w3.codes, 1, (uint64_t)a.N, (uint64_t)a.K, kBlk, 128)) != cudaSuccess)
+    return e;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  static int clusters[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!clusters[dev]) {
+    e = cudaFuncSetAttribute(k_e4m3_many<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    int n = 0;
+    cfg.gridDim = dim3(2 * (sm_count() / 2));
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, k_e4m3_many<GATED>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n <= 0) return cudaErrorNotSupported;
+    clusters[dev] = n;
+  }
+  const int m_units = (int)((a.M + 2LL * kRowsCta - 1) / (2 * kRowsCta));
+  const int n_tiles = GATED ? (a.N + 127) / 128 : (a.N + 255) / 256;
+  const long long tiles = (long long)m_units * n_tiles;
+  if (tiles > 0x7fffffffLL / 2) return cudaErrorInvalidValue;
+  // Weights beyond what L2 keeps, short rows: groups of 32 row units, so that a weight
+  // tile is read once per group.
+  const size_t w_bytes = (size_t)a.N * a.K * (GATED ? 2 : 1);
+  const int group = a.K <= 8192 && w_bytes > (size_t(48) << 20) && m_units > 1 ? std::min(m_units, 32) : 0;
+  cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(tiles, clusters[dev]));
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_e4m3_many<GATED>, tx, tw, tw3, a, m_units, n_tiles, group, device_error_word());
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_e4m3_many(const GemmArgs& a, cudaStream_t s) { return go<false>(a, s); }
+cudaError_t launch_gated_e4m3_many(const GemmArgs& a, cudaStream_t s) { return go<true>(a, s); }
+
+}  // namespace tb

@@ -331,6 +331,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+// 32 lanes × 32 consecutive 32-bit columns: thread i gets lane (base lane + i).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
 // 32 lanes × 8 consecutive 32-bit columns: thread i gets lane (base lane + i).
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -536,6 +548,45 @@ __device__ __forceinline__ void mma2_bf16_ss(uint32_t d_tmem, uint64_t adesc, ui
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p;
+}
+
+// The pair form of mma_mx_ss over 128 elements of K (four instructions under one scale
+// each, both operands K-major rows of 128 bytes with the 128-byte swizzle).  The scales
+// of A's rows lie in the tensor memory of the CTA that holds the rows; those of B's
+// columns, all N of them, in both CTAs'.  The whole warp calls it and the elected lane
+// issues: the operands stay in uniform registers, where a branch on the lane would have
+// each of them moved there for each instruction.
+#define TB_MMA2_MX_STEP(K, PRED)                                               \
+  "add.u32 la, %1, " #K "*2;\n\t"                                             \
+  "add.u32 lb, %2, " #K "*2;\n\t"                                             \
+  "mov.b64 da, {la, %3};\n\t"                                                 \
+  "mov.b64 db, {lb, %3};\n\t"                                                 \
+  "@pe tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %4, [%5], [%6], " #PRED ";\n\t"
+__device__ __forceinline__ void mma2_mx_k128(uint32_t d_tmem, uint32_t adesc_lo, uint32_t bdesc_lo, uint32_t desc_hi,
+                                             uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate,
+                                             uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred pe, pf, pt;\n\t.reg .b32 la, lb;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 pe, %8, 0;\n\tsetp.ne.b32 pf, %7, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\t"
+      TB_MMA2_MX_STEP(0, pf) TB_MMA2_MX_STEP(1, pt) TB_MMA2_MX_STEP(2, pt) TB_MMA2_MX_STEP(3, pt) "}" ::"r"(d_tmem),
+      "r"(adesc_lo), "r"(bdesc_lo), "r"(desc_hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+#undef TB_MMA2_MX_STEP
+// mma_commit_pair by the elected lane of a warp, on the barrier at shared::cta address `bar`.
+__device__ __forceinline__ void mma_commit_pair_elected(uint32_t bar, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred pe;\n\tsetp.ne.b32 pe, %2, 0;\n\t"
+      "@pe tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          bar),
+      "h"((uint16_t)3), "r"(elected)
       : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import causal_gqa_attention_rmsnorm_gb300 as tb
+from causal_gqa_attention_rmsnorm_gb300.binding import tbx_e4m3_form
 from e4m3_helpers import (BF16, CODE, F32, HALF, SCALE, bytes_of, check_product, check_rows, gated_and_off, make_rows,
                           make_weight, product, random_codes, rows_np, weight_np)
 from oracle import e4m3 as ref
@@ -22,6 +23,13 @@ def f64(t):
 
 def no_error():
     assert tb.tb_get_device_error(clear=True) == 0
+
+
+@pytest.fixture
+def form():
+    """Sets the kernel that the products of a test take."""
+    yield tbx_e4m3_form
+    tbx_e4m3_form(0)
 
 
 # ---- rows ---------------------------------------------------------------------
@@ -263,6 +271,71 @@ def test_empty_calls():
     out, h = tb.tb_rmsnorm_e4m3(e, torch.ones(64, dtype=BF16, device="cuda"), 1e-5, r=e)
     assert out.rows == 0 and h.shape == (0, 64)
     no_error()
+
+
+# ---- many rows ----------------------------------------------------------------------
+# One row to some tiles per cluster (both accumulators, more tiles than clusters), a row
+# unit whose second half lies past M, K of one set and of an odd number of them.
+
+MANY = [(1, 16, 16), (128, 256, 128), (129, 272, 144), (256, 512, 512), (300, 112, 2064), (400, 2304, 640), (511, 784, 1168),
+        (1371, 2304, 768), (700, 8192, 400), (5000, 1040, 272), (260, 256, 9216)]
+
+
+@pytest.mark.parametrize("M,N,K", MANY)
+@pytest.mark.parametrize("dtype,with_res", [(F32, False), (BF16, True), (F32, True)])
+def test_gemm_many(form, M, N, K, dtype, with_res):
+    form(2)
+    g = gen(M + N + K)
+    x, w = make_rows(tb, M, K, g), make_weight(tb, N, K, g)
+    res = (torch.randn(M, N, generator=g) * 100).to(dtype).cuda() if with_res else None
+    buf = torch.full((M + 4, N), 7.0, dtype=dtype, device="cuda")
+    y = tb.tb_gemm_e4m3(x, w, res=res, y=buf[2:2 + M])
+    no_error()
+    assert (buf[:2] == 7).all() and (buf[2 + M:] == 7).all()
+    check_product(y, *product(rows_np(x), weight_np(w), None if res is None else f64(res)), K, dtype)
+    if with_res:
+        assert torch.equal(tb.tb_gemm_e4m3(x, w, res=res, y=res), y)
+
+
+@pytest.mark.parametrize("M,F,K", [(1, 16, 16), (129, 144, 400), (333, 2048, 768), (300, 272, 2064), (1000, 1040, 528),
+                                   (2100, 1296, 272)])
+@pytest.mark.parametrize("out_dtype", ["codes", BF16, F32])
+def test_gated_many(form, M, F, K, out_dtype):
+    form(2)
+    g = gen(M + F + K)
+    x, w1, w3 = make_rows(tb, M, K, g), make_weight(tb, F, K, g), make_weight(tb, F, K, g)
+    w1.scale.view(torch.uint8).sub_(int(np.log2(K) / 2) + 11)
+    exact, off = gated_and_off(rows_np(x), weight_np(w1), weight_np(w3), K)
+    if out_dtype == "codes":
+        buf = torch.full((M + 4, F), 9, dtype=torch.uint8, device="cuda")
+        sc = torch.full((M + 4, -(-F // 128)), 9, dtype=torch.uint8, device="cuda")
+        out = tb.tb_gated_e4m3(x, w1, w3, out=tb.E4M3Rows(buf[2:2 + M].view(CODE), sc[2:2 + M].view(SCALE)))
+        no_error()
+        for t in (buf, sc):
+            assert (t[:2] == 9).all() and (t[2 + M:] == 9).all()
+        check_rows(bytes_of(out.codes), bytes_of(out.scale), exact, off)
+    else:
+        y = tb.tb_gated_e4m3(x, w1, w3, out_dtype=tb.TB_F32 if out_dtype is F32 else tb.TB_BF16)
+        no_error()
+        assert (np.abs(f64(y) - exact) <= off + 2 * HALF[out_dtype] * (np.abs(exact) + off)).all()
+
+
+def test_both_kernels_agree_on_what_nan_reaches(form):
+    g = gen(9)
+    M, N, K = 300, 272, 528
+    x, w = make_rows(tb, M, K, g), make_weight(tb, N, K, g)
+    x.codes.view(torch.uint8)[3, 100] = 0x7F
+    x.scale.view(torch.uint8)[266, 4] = 255
+    w.codes.view(torch.uint8)[5, 527] = 0xFF
+    w.scale.view(torch.uint8)[2, 1] = 255
+    got = []
+    for f in (1, 2):
+        form(f)
+        got.append(torch.isnan(tb.tb_gemm_e4m3(x, w)))
+    no_error()
+    hit = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    hit[3], hit[266], hit[:, 5], hit[:, 256:] = True, True, True, True
+    assert torch.equal(got[0], hit) and torch.equal(got[1], hit)
 
 
 # ---- together -----------------------------------------------------------------------
