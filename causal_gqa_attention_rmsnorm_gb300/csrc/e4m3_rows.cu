@@ -89,11 +89,12 @@ __device__ __forceinline__ void put_block(const float (&v)[8], float s, const Ei
 // RT: the type of r (void: none).  A row takes `tpr` threads (a multiple of 32), NV
 // eights each, a CTA blockDim.x / tpr rows; with NORM that is one, or a row per warp.
 // Without NORM, blockIdx.y counts pieces of tpr·NV·8 columns.
+template <typename T, typename RT, int NV> constexpr bool kLean = sizeof(T) == 2 && NV == 4 && std::is_same<RT, void>::value;
 // (64 registers without r keep four CTAs of 256 on an SM: 16384 x 4096 of bf16 54 -> 45
-// us; with r they cost fp32 10 us of 123.)
+// us.  Elsewhere no number of CTAs is asked for, which is not the same as one: 16384 x
+// 4096 of fp32 with r 123 and 147 us.)
 template <typename T, typename RT, bool NORM, int NV>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : sizeof(T) == 2 && NV == 4 ? 256 : 512,
-                                  sizeof(T) == 2 && NV == 4 && std::is_same<RT, void>::value ? 4 : 1) k_rows_e4m3(RowsArgs a, int tpr) {
+__global__ void __launch_bounds__(NV == 1 ? 1024 : kLean<T, RT, NV> ? 256 : 512, kLean<T, RT, NV> ? 4 : 0) k_rows_e4m3(RowsArgs a, int tpr) {
   constexpr bool RES = !std::is_same<RT, void>::value;
   __shared__ float part[32];
   pdl_trigger();
