@@ -154,35 +154,42 @@ __global__ void __launch_bounds__(192, CPS)
         mbar_wait(&full[t % STAGES], (t / STAGES) & 1, &no_abort, err);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      bool ok = true;
-      for (int j = 0; ok && j < nkb; ++j) {
-        const int st = j % STAGES, set = j / kSet, chunk = set / kChunk, buf = chunk & 1;
-        if (j % kSet == 0) {
-          if (j % (kSet * kChunk) == 0 && !mbar_wait(&tempty[buf], ((chunk >> 1) & 1) ^ 1u, abort_flag, err)) break;
-          if (!mbar_wait(&sfull[set % kSets], (set / kSets) & 1, abort_flag, err)) break;
+    // The whole warp walks the blocks; its elected lane issues (mma_mx_k128).
+    const uint32_t elected = elect_one();
+    const uint64_t desc = desc_kmajor_sw128(smem_u32(smem));
+    const uint32_t desc_hi = (uint32_t)(desc >> 32), desc0 = (uint32_t)desc;
+    const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int set = 0; ok && set < nsets; ++set) {
+      const int chunk = set / kChunk, buf = chunk & 1;
+      const bool first = set % kChunk == 0, last = set + 1 == nsets;
+      if (first && !mbar_wait_warp(&tempty[buf], ((chunk >> 1) & 1) ^ 1u, abort_flag, err)) break;
+      if (!mbar_wait_warp(&sfull[set % kSets], (set / kSets) & 1, abort_flag, err)) break;
+      const uint32_t d = tmem + buf * C::ACC, sf = tmem + C::SETS_AT + (set % kSets) * C::SET_COLS;
+#pragma unroll
+      for (int b = 0; b < kSet; ++b) {
+        if (set * kSet + b < nkb) {
+          if (!__all_sync(0xffffffffu, mbar_try_wait(full0 + stage * 8, phase)) &&
+              !(ok = mbar_wait_warp(&full[stage], phase, abort_flag, err)))
+            break;
+          tc_fence_after();
+          const uint32_t w = desc0 + stage * (C::STAGE_BYTES >> 4), x = w + (C::W_BYTES >> 4);
+#pragma unroll
+          for (int m = 0; m < MATS; ++m)
+            mma_mx_k128<1>(d + m * NT, w + m * (kBlk * kBlk >> 4), x, desc_hi, idesc_mx_e4m3(kBlk, NT, b), sf + 4 * m,
+                           sf + 4 * MATS, !(first && b == 0), elected);
+          mma_commit_elected(empty0 + stage * 8, elected);
+          if (++stage == STAGES) stage = 0, phase ^= 1u;
         }
-        if (!mbar_wait(&full[st], (j / STAGES) & 1, abort_flag, err)) break;
-        tc_fence_after();
-        const uint32_t w0 = smem_u32(smem + st * C::STAGE_BYTES), x0 = w0 + C::W_BYTES;
-        const uint32_t d = tmem + buf * C::ACC, sf = tmem + C::SETS_AT + (set % kSets) * C::SET_COLS;
-        const uint32_t idesc = idesc_mx_e4m3(kBlk, NT, j % kSet);
-#pragma unroll
-        for (int m = 0; m < MATS; ++m)
-#pragma unroll
-          for (int k = 0; k < kBlk / 32; ++k)
-            mma_mx_ss(d + m * NT, desc_kmajor_sw128(w0 + m * kBlk * kBlk + k * 32), desc_kmajor_sw128(x0 + k * 32),
-                      idesc, sf + 4 * m, sf + 4 * MATS, j % (kSet * kChunk) != 0 || k != 0);
-        mma_commit(&empty[st]);
-        const bool last = j + 1 == nkb;
-        if (last || (j + 1) % kSet == 0) mma_commit(&sempty[set % kSets]);
-        if (last || (j + 1) % (kSet * kChunk) == 0) mma_commit(&tfull[buf]);
       }
-      // all of them must be done before tensor memory is released
-      mma_commit(drain);
-      volatile int no_abort = 0;
-      mbar_wait(drain, 0, &no_abort, err);
+      mma_commit_elected(smem_u32(&sempty[set % kSets]), elected);
+      if (ok && (last || (set + 1) % kChunk == 0)) mma_commit_elected(smem_u32(&tfull[buf]), elected);
     }
+    // all of them must be done before tensor memory is released
+    mma_commit_elected(smem_u32(drain), elected);
+    volatile int no_abort = 0;
+    mbar_wait_warp(drain, 0, &no_abort, err);
   } else {
     pdl_wait();
     const int quad = warp & 3;

@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    // The whole warp walks the blocks; its elected lane issues (mma2_mx_k128).
+    // The whole warp walks the blocks; its elected lane issues (mma_mx_k128).
     if (rank == 0) {
       const uint32_t elected = elect_one();
       const uint64_t desc = desc_kmajor_sw128(smem_u32(smem));
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
                 break;
               tc_fence_after();
               const uint32_t lo = desc0 + stage * NEXT;
-              mma2_mx_k128(d, lo, lo + (C::A_BYTES >> 4), desc_hi, idesc_mx_e4m3(2 * kRowsCta, 256, b), sf, sf + 4,
+              mma_mx_k128<2>(d, lo, lo + (C::A_BYTES >> 4), desc_hi, idesc_mx_e4m3(2 * kRowsCta, 256, b), sf, sf + 4,
                            kb + b != 0, elected);
               mma_commit_pair_elected(empty0 + stage * 8, elected);      // frees the stage in both CTAs
               if (++stage == STAGES) stage = 0, phase ^= 1u;

@@ -241,22 +241,6 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t adesc, uint6
       : "memory");
 }
 
-// The same with a power-of-two scale (one exponent byte, 2^(byte-127)) for each
-// 32 elements of K of a row of A and of B (kind::mxf8f6f4, scale_vec::1X).  The
-// scale of row r lies in tensor memory at lane r % 32, column sf + r / 32, in the
-// byte of the 32-bit word that the instruction descriptor names (idesc_mx_e4m3),
-// the same in each of the four quarters of the lanes.
-__device__ __forceinline__ void mma_mx_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-          d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
-}
-
 // Batched issue of the MMAs of one tile, for an issuing thread that must spend
 // as few instructions per MMA as possible: descriptors are passed as their low
 // and high 32-bit words, each MMA's operand offset is an immediate added to the
@@ -550,45 +534,6 @@ __device__ __forceinline__ void mma2_bf16_ss(uint32_t d_tmem, uint64_t adesc, ui
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// One lane of a converged warp, the same one every time.
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p;
-}
-
-// The pair form of mma_mx_ss over 128 elements of K (four instructions under one scale
-// each, both operands K-major rows of 128 bytes with the 128-byte swizzle).  The scales
-// of A's rows lie in the tensor memory of the CTA that holds the rows; those of B's
-// columns, all N of them, in both CTAs'.  The whole warp calls it and the elected lane
-// issues: the operands stay in uniform registers, where a branch on the lane would have
-// each of them moved there for each instruction.
-#define TB_MMA2_MX_STEP(K, PRED)                                               \
-  "add.u32 la, %1, " #K "*2;\n\t"                                             \
-  "add.u32 lb, %2, " #K "*2;\n\t"                                             \
-  "mov.b64 da, {la, %3};\n\t"                                                 \
-  "mov.b64 db, {lb, %3};\n\t"                                                 \
-  "@pe tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %4, [%5], [%6], " #PRED ";\n\t"
-__device__ __forceinline__ void mma2_mx_k128(uint32_t d_tmem, uint32_t adesc_lo, uint32_t bdesc_lo, uint32_t desc_hi,
-                                             uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate,
-                                             uint32_t elected) {
-  asm volatile(
-      "{\n\t.reg .pred pe, pf, pt;\n\t.reg .b32 la, lb;\n\t.reg .b64 da, db;\n\t"
-      "setp.ne.b32 pe, %8, 0;\n\tsetp.ne.b32 pf, %7, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\t"
-      TB_MMA2_MX_STEP(0, pf) TB_MMA2_MX_STEP(1, pt) TB_MMA2_MX_STEP(2, pt) TB_MMA2_MX_STEP(3, pt) "}" ::"r"(d_tmem),
-      "r"(adesc_lo), "r"(bdesc_lo), "r"(desc_hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(elected)
-      : "memory");
-}
-#undef TB_MMA2_MX_STEP
-// mma_commit_pair by the elected lane of a warp, on the barrier at shared::cta address `bar`.
-__device__ __forceinline__ void mma_commit_pair_elected(uint32_t bar, uint32_t elected) {
-  asm volatile(
-      "{\n\t.reg .pred pe;\n\tsetp.ne.b32 pe, %2, 0;\n\t"
-      "@pe tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
-          bar),
-      "h"((uint16_t)3), "r"(elected)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
                : "memory");
@@ -650,6 +595,70 @@ __device__ __forceinline__ void mma2_tile_ts128(uint32_t d_tmem, uint32_t a_tmem
       : "memory");
 }
 #undef TB_MMA2_TS_STEP
+
+// ---- block-scaled 8-bit MMAs (kind::mxf8f6f4, scale_vec::1X) ---------------
+//
+// e4m3 operands with a power-of-two scale (one exponent byte, 2^(byte-127)) for each 32
+// elements of K of a row of A and of B.  The scale of row r lies in tensor memory at
+// lane r % 32, column sf + r / 32, in the byte of the 32-bit word that the instruction
+// descriptor names (idesc_mx_e4m3), the same in each of the four quarters of the lanes.
+// Of a pair, the scales of A's rows lie in the tensor memory of the CTA that holds the
+// rows; those of B's columns, all N of them, in both CTAs'.
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p;
+}
+
+// D (+)= A·Bᵀ over 128 elements of K under one scale each (four instructions; both
+// operands K-major rows of 128 bytes with the 128-byte swizzle; CG CTAs).  The whole warp
+// calls it and the elected lane issues: the operands stay in uniform registers, where a
+// branch on the lane would have each of them moved there for each instruction.
+#define TB_MMA_MX_STEP(CG, K, PRED)                                            \
+  "add.u32 la, %1, " #K "*2;\n\t"                                             \
+  "add.u32 lb, %2, " #K "*2;\n\t"                                             \
+  "mov.b64 da, {la, %3};\n\t"                                                 \
+  "mov.b64 db, {lb, %3};\n\t"                                                 \
+  "@pe tcgen05.mma.cta_group::" #CG ".kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %4, [%5], [%6], " #PRED ";\n\t"
+#define TB_MMA_MX_K128(CG)                                                     \
+  asm volatile(                                                                \
+      "{\n\t.reg .pred pe, pf, pt;\n\t.reg .b32 la, lb;\n\t.reg .b64 da, db;\n\t" \
+      "setp.ne.b32 pe, %8, 0;\n\tsetp.ne.b32 pf, %7, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\t" \
+      TB_MMA_MX_STEP(CG, 0, pf) TB_MMA_MX_STEP(CG, 1, pt) TB_MMA_MX_STEP(CG, 2, pt) TB_MMA_MX_STEP(CG, 3, pt) "}" ::"r"( \
+          d_tmem),                                                             \
+      "r"(adesc_lo), "r"(bdesc_lo), "r"(desc_hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(elected) \
+      : "memory")
+template <int CG>
+__device__ __forceinline__ void mma_mx_k128(uint32_t d_tmem, uint32_t adesc_lo, uint32_t bdesc_lo, uint32_t desc_hi,
+                                            uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate,
+                                            uint32_t elected) {
+  if constexpr (CG == 2) {
+    TB_MMA_MX_K128(2);
+  } else {
+    TB_MMA_MX_K128(1);
+  }
+}
+#undef TB_MMA_MX_K128
+#undef TB_MMA_MX_STEP
+
+// mma_commit (of one CTA) and mma_commit_pair by the elected lane of a warp, on the
+// barrier at shared::cta address `bar`.
+__device__ __forceinline__ void mma_commit_elected(uint32_t bar, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred pe;\n\tsetp.ne.b32 pe, %1, 0;\n\t"
+      "@pe tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair_elected(uint32_t bar, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred pe;\n\tsetp.ne.b32 pe, %2, 0;\n\t"
+      "@pe tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          bar),
+      "h"((uint16_t)3), "r"(elected)
+      : "memory");
+}
 
 }  // namespace ptx
 }  // namespace tb
