@@ -121,6 +121,8 @@ def lib() -> ctypes.CDLL:
         L.tbx_set_stat_poll_ns.restype = ctypes.c_uint64
         L.tbx_e4m3_form.argtypes = [c_int32]
         L.tbx_e4m3_form.restype = c_int32
+        L.tbx_e4m3_few_tile.argtypes = [c_int32] * 5
+        L.tbx_e4m3_few_tile.restype = c_int32
         L.tb_embed.argtypes = [c_void_p, c_int32, c_int32, c_int32, c_void_p, ctypes.c_int64, c_void_p, c_void_p]
         L.tb_lm_head_packed_bytes.argtypes = [P(tb_head_cfg)]
         L.tb_lm_head_packed_bytes.restype = c_size_t
@@ -447,8 +449,9 @@ def tbx_set_stat_poll_ns(ns: int) -> int:
 
 
 def tbx_e4m3_form(form: int) -> int:
-    """Test hook: the kernel that later 8-bit products take (0: by the rule, 1: few
-    rows, 2: many rows); returns the previous value."""
+    """Test hook: the form that later 8-bit products take (0: by the rule; 16, 32, 64 or
+    128: the few-rows kernel with so many rows per tile; -1: the many-rows kernel);
+    returns the previous one."""
     return int(lib().tbx_e4m3_form(int(form)))
 
 

@@ -6,6 +6,7 @@
 #include <atomic>
 
 #include "e4m3.cuh"
+#include "gemm_tc.cuh"
 
 namespace tb {
 namespace {
@@ -39,6 +40,9 @@ tb_status check(const tb_e4m3* m, const char* name, bool tensors) {
   if (!m) return report(TB_ERR_INVALID_ARG, "%s is NULL", name);
   if (m->rows < 0 || m->cols <= 0) return report(TB_ERR_INVALID_ARG, "%s: cols must be positive, rows non-negative", name);
   if (m->cols % 16) return report(TB_ERR_UNSUPPORTED, "%s: cols (%d) must be a multiple of 16", name, m->cols);
+  // (the kernels round both up to whole tiles, in 32 bits)
+  if (m->rows > INT32_MAX - 1023 || m->cols > INT32_MAX - 1023)
+    return report(TB_ERR_UNSUPPORTED, "%s: more than 2^31 - 1024 rows or cols", name);
   if ((long long)m->rows * m->cols > 1LL << 39) return report(TB_ERR_UNSUPPORTED, "%s: more than 2^39 codes", name);
   if (!tensors) return TB_OK;
   if (!m->codes || !m->scale) return report(TB_ERR_INVALID_ARG, "%s: codes and scale must be non-NULL", name);
@@ -70,12 +74,18 @@ tb_status check_weights(const tb_e4m3* w, const char* name, const tb_e4m3* x, bo
   return TB_OK;
 }
 
-// Which kernel a product takes.
-std::atomic<int> g_form{0};            // test hook: 1 few, 2 many
-bool many(const GemmArgs& a) {
+// The rows per tile of k_e4m3_few, or 0 for k_e4m3_many.  An fp32 result keeps fp32's
+// sums: k_e4m3_many has one accumulator for all of K, whose cut-off sums are off by up to
+// 2^-24 per instruction of 32 (relative to 64 bits, normal rows: K 4096 2.2e-7, 14336
+// 1.0e-6, against 1.2e-7 in chunks), so from K = 4096 on an fp32 result is formed in
+// chunks.
+std::atomic<int> g_form{0};            // test hook: 16 to 128 rows per tile, or -1 for many
+int tile_of(const GemmArgs& a, int mats) {
   const int form = g_form.load(std::memory_order_relaxed);
-  if (form) return form == 2;
-  return a.M >= 256 && (a.y_dtype != TB_F32 || a.K <= 2048);
+  if (form) return form < 0 ? 0 : mats == 2 && form > 64 ? 64 : form;
+  const int tile = e4m3_few_tile(a.M, a.N, a.K, mats, sm_count());
+  if (tile == 0 && a.y_dtype == TB_F32 && a.K > 4096) return mats == 2 ? 64 : 128;
+  return tile;
 }
 
 RowsArgs rows_args(const void* x, const tb_e4m3* out) {
@@ -136,6 +146,8 @@ tb_status tb_rmsnorm_e4m3(const void* x, int32_t dtype, const void* r, int32_t r
 tb_status tb_quant_e4m3(const void* x, int32_t dtype, const tb_e4m3* out, void* stream) {
   TB_OR_RETURN(check(out, "out", false));
   if (!is_float(dtype)) return report(TB_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  // (pieces of at least 2048 columns are counted in the grid's second dimension)
+  if (out->cols > 1 << 26) return report(TB_ERR_UNSUPPORTED, "rows of at most 2^26 columns (%d)", out->cols);
   if (out->rows == 0) return TB_OK;
   TB_OR_RETURN(check(out, "out", true));
   TB_OR_RETURN(check_in(x, "x"));
@@ -182,7 +194,8 @@ tb_status tb_gemm_e4m3(const tb_e4m3* x, const tb_e4m3* w, const void* res, void
   a.res = res;
   a.y = y;
   a.y_dtype = y_dtype;
-  return done(many(a) ? launch_gemm_e4m3_many(a, (cudaStream_t)stream) : launch_gemm_e4m3_few(a, (cudaStream_t)stream),
+  const int tile = tile_of(a, 1);
+  return done(tile ? launch_gemm_e4m3_few(a, tile, (cudaStream_t)stream) : launch_gemm_e4m3_many(a, (cudaStream_t)stream),
               "tb_gemm_e4m3");
 }
 
@@ -214,12 +227,19 @@ tb_status tb_gated_e4m3(const tb_e4m3* x, const tb_e4m3* w1, const tb_e4m3* w3, 
   a.y = y;
   a.y_dtype = y_dtype;
   a.y_scale = static_cast<uint8_t*>(y_scale);
-  return done(many(a) ? launch_gated_e4m3_many(a, (cudaStream_t)stream) : launch_gated_e4m3_few(a, (cudaStream_t)stream),
+  const int tile = tile_of(a, 2);
+  return done(tile ? launch_gated_e4m3_few(a, tile, (cudaStream_t)stream) : launch_gated_e4m3_many(a, (cudaStream_t)stream),
               "tb_gated_e4m3");
 }
 
-// Test hook: the kernel that later products of this process take (0: by the rule, 1:
-// few rows, 2: many rows).  Returns the previous value.
-TB_API int32_t tbx_e4m3_form(int32_t form) { return g_form.exchange(form); }
+// Test hooks: the form that later products of this process take (0: by the rule; 16, 32,
+// 64 or 128: k_e4m3_few with so many rows per tile; -1: k_e4m3_many), returning the
+// previous one; and the rule itself.
+TB_API int32_t tbx_e4m3_form(int32_t form) {
+  return g_form.exchange(form == 16 || form == 32 || form == 64 || form == 128 || form == -1 ? form : 0);
+}
+TB_API int32_t tbx_e4m3_few_tile(int32_t M, int32_t N, int32_t K, int32_t mats, int32_t sms) {
+  return e4m3_few_tile(M, N, K, mats, sms);
+}
 
 }  // extern "C"

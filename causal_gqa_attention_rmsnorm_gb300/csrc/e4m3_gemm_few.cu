@@ -37,8 +37,9 @@ constexpr int kChunk = 4;        // scale sets per chunk
 constexpr int kSets = 8;         // scale sets held in tensor memory: two chunks
 constexpr int kMaxSplits = 8;
 
-// NT rows of X; MATS 1 or 2 weight matrices; CPS CTAs per SM.
-template <int NT, int MATS, int CPS> struct FewCfg {
+// NT rows of X; MATS 1 or 2 weight matrices; CPS CTAs per SM; ONE: a CTA's part of K is
+// at most one chunk, whose sums go from tensor memory straight on.
+template <int NT, int MATS, int CPS, bool ONE> struct FewCfg {
   static constexpr uint32_t W_BYTES = MATS * kBlk * kBlk;
   static constexpr uint32_t STAGE_BYTES = W_BYTES + NT * kBlk;
   static constexpr uint32_t ROOM = CPS == 2 ? 110 * 1024 : 220 * 1024;
@@ -48,19 +49,19 @@ template <int NT, int MATS, int CPS> struct FewCfg {
   static constexpr size_t SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t ACC = MATS * NT;                 // columns of one accumulator
   static constexpr uint32_t SET_COLS = 4 * MATS + 4;         // a word per weight row / 32 and row / 32
-  static constexpr uint32_t SETS_AT = 2 * ACC;
-  static constexpr uint32_t NEED = SETS_AT + kSets * SET_COLS;
+  static constexpr uint32_t SETS_AT = ONE ? ACC : 2 * ACC;
+  static constexpr uint32_t NEED = SETS_AT + (ONE ? kChunk : kSets) * SET_COLS;
   static constexpr uint32_t TMEM_COLS = NEED <= 128 ? 128 : NEED <= 256 ? 256 : 512;
   static_assert(CPS * TMEM_COLS <= 512, "tensor memory of an SM");
   static_assert(STAGES >= 2 && (2 * STAGES + 2 * kSets + 6) * 8 + 8 <= 512, "barriers");
   static_assert(MATS * NT * kBlk * 4 <= OFF_BAR, "the sums reuse the ring");
 };
 
-template <int NT, int MATS, int CPS>
+template <int NT, int MATS, int CPS, bool ONE>
 __global__ void __launch_bounds__(192, CPS)
     k_e4m3_few(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW3,
                const __grid_constant__ CUtensorMap tmX, GemmArgs a, int wtiles, int splits, int* err) {
-  using C = FewCfg<NT, MATS, CPS>;
+  using C = FewCfg<NT, MATS, CPS, ONE>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -217,95 +218,163 @@ __global__ void __launch_bounds__(192, CPS)
       if (lane == 0) mbar_arrive(&sfull[s % kSets]);
       return true;
     };
-    float acc[MATS * NT];
+    // Lane l of quarter q holds weight row 32 q + l, that is a column of y, of every row
+    // of the tile: of `P` rows from `i` on, in u.  Without a split they are finished here,
+    // and stored if nothing has to be known of the row's other columns; else all goes to
+    // shared memory.  (The last chunk's sums come after every instruction, and so after
+    // every read of the ring.)
+    constexpr int P = NT < 32 ? NT : 32;
+    const int f = quad * 32 + lane, col = wt * kBlk + f;
+    auto put = [&](int i, const float (&u)[MATS][P]) {
+      if (splits > 1) {
 #pragma unroll
-    for (int i = 0; i < MATS * NT; ++i) acc[i] = 0.f;
+        for (int m = 0; m < MATS; ++m)
+#pragma unroll
+          for (int k = 0; k < P; ++k) part_s[(m * NT + i + k) * kBlk + f] = u[m][k];
+        return;
+      }
+      float v[P];
+#pragma unroll
+      for (int k = 0; k < P; ++k) v[k] = MATS == 2 ? gated(u[0][k], u[MATS - 1][k]) : u[0][k];
+      if (a.y_dtype == TB_E4M3) {
+#pragma unroll
+        for (int k = 0; k < P; ++k) part_s[(i + k) * kBlk + f] = v[k];
+        return;
+      }
+      if (col >= a.N) return;
+      const size_t at = (size_t)(m0 + i) * a.N + col;
+      if (MATS == 1 && a.res) {
+        float r[P];
+#pragma unroll
+        for (int k = 0; k < P; ++k) r[k] = i + k < rows ? get1(a.res, a.y_dtype, at + (size_t)k * a.N) : 0.f;
+#pragma unroll
+        for (int k = 0; k < P; ++k) v[k] += r[k];
+      }
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+        if (i + k < rows) put1(a.y, a.y_dtype, at + (size_t)k * a.N, v[k]);
+    };
     bool ok = true;
     int fed = 0;
-    for (int c = 0; ok && c < nchunks; ++c) {
-      // the sets of this chunk and of the next one: those they replace belong to the
-      // chunk before, whose sums are in registers already
-      for (const int upto = min(nsets, (c + 2) * kChunk); ok && fed < upto; ++fed) ok = feed(fed);
-      if (!ok || !(ok = mbar_wait_warp(&tfull[c & 1], (c >> 1) & 1, abort_flag, err))) break;
-      tc_fence_after();
+    if constexpr (ONE) {
+      for (; ok && fed < nsets; ++fed) ok = feed(fed);
+      if (ok && mbar_wait_warp(tfull, 0, abort_flag, err)) {
+        tc_fence_after();
 #pragma unroll
-      for (int i = 0; i < MATS * NT; i += 16) {
-        uint32_t u[16];
-        tmem_ld16(tmem + lanes + (c & 1) * C::ACC + i, u);
-        tmem_wait_ld();
+        for (int i = 0; i < NT; i += P) {
+          float u[MATS][P];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) acc[i + k] += __uint_as_float(u[k]);
+          for (int m = 0; m < MATS; ++m)
+#pragma unroll
+            for (int k = 0; k < P; k += 16)
+              tmem_ld16(tmem + lanes + m * NT + i + k, *reinterpret_cast<uint32_t(*)[16]>(&u[m][k]));
+          tmem_wait_ld();
+          put(i, u);
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[c & 1]);
-    }
-    // lane l of quarter q holds weight row 32 q + l.  (The last chunk's sums come after
-    // every instruction, and so after every read of the ring.)
-    if (ok) {
+    } else {
+      float acc[MATS][NT];
 #pragma unroll
-      for (int i = 0; i < MATS * NT; ++i) part_s[i * kBlk + quad * 32 + lane] = acc[i];
+      for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[m][i] = 0.f;
+      for (int c = 0; ok && c < nchunks; ++c) {
+        // the sets of this chunk and of the next one: those they replace belong to the
+        // chunk before, whose sums are in registers already
+        for (const int upto = min(nsets, (c + 2) * kChunk); ok && fed < upto; ++fed) ok = feed(fed);
+        if (!ok || !(ok = mbar_wait_warp(&tfull[c & 1], (c >> 1) & 1, abort_flag, err))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int m = 0; m < MATS; ++m)
+#pragma unroll
+          for (int i = 0; i < NT; i += 16) {
+            uint32_t u[16];
+            tmem_ld16(tmem + lanes + (c & 1) * C::ACC + m * NT + i, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) acc[m][i + k] += __uint_as_float(u[k]);
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[c & 1]);
+      }
+      if (ok) {
+#pragma unroll
+        for (int i = 0; i < NT; i += P) {
+          float u[MATS][P];
+#pragma unroll
+          for (int m = 0; m < MATS; ++m)
+#pragma unroll
+            for (int k = 0; k < P; ++k) u[m][k] = acc[m][i + k];
+          put(i, u);
+        }
+      }
     }
   }
 
+  // the sums of every CTA of the cluster are in shared memory
   tc_fence_before();
   __syncwarp();
-  cluster_sync();
+  if (splits > 1) cluster_sync();
+  else __syncthreads();
 
-  if (warp >= 2) {
+  if (warp >= 2 && (splits > 1 || a.y_dtype == TB_E4M3)) {
     const int col = wt * kBlk + 4 * lane;
     const uint32_t base = smem_u32(part_s) + 16u * lane;
+#pragma unroll 2
     for (int t = t0 + (warp - 2); t < t1; t += 4) {
       const size_t at = (size_t)(m0 + t) * a.N + col;
       float4 res = make_float4(0.f, 0.f, 0.f, 0.f);
       if (MATS == 1 && a.res && col < a.N) res = get4(a.res, a.y_dtype, at);
       float4 v[MATS];
-#pragma unroll
-      for (int m = 0; m < MATS; ++m) {
-        float4 p[kMaxSplits];
-#pragma unroll
-        for (int r = 0; r < kMaxSplits; ++r)
-          if (r < splits) p[r] = ld_dsmem_f4(mapa_shared(base + (uint32_t)((m * NT + t) * kBlk * 4), (uint32_t)r));
-        v[m] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int r = 0; r < kMaxSplits; ++r)
-          if (r < splits) v[m] = make_float4(v[m].x + p[r].x, v[m].y + p[r].y, v[m].z + p[r].z, v[m].w + p[r].w);
-      }
-      if constexpr (MATS == 1) {
-        v[0] = make_float4(v[0].x + res.x, v[0].y + res.y, v[0].z + res.z, v[0].w + res.w);
-        if (col < a.N) put4(a.y, a.y_dtype, at, v[0]);
+      if (splits == 1) {
+        v[0] = *reinterpret_cast<const float4*>(part_s + t * kBlk + 4 * lane);
       } else {
-        v[0] = make_float4(gated(v[0].x, v[1].x), gated(v[0].y, v[1].y), gated(v[0].z, v[1].z), gated(v[0].w, v[1].w));
-        if (a.y_dtype != TB_E4M3) {
-          if (col < a.N) put4(a.y, a.y_dtype, at, v[0]);
-          continue;
-        }
-        // (columns past N hold zeros: weight rows past N read as zeros)
-        float top = fmaxf(fmaxf(finite_mag(v[0].x), finite_mag(v[0].y)), fmaxf(finite_mag(v[0].z), finite_mag(v[0].w)));
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int e = block_exponent(top);
-        const float inv = pow2i(-e);
-        if (col < a.N)
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + at) =
-              codes_of4(to_code(v[0].x, inv), to_code(v[0].y, inv), to_code(v[0].z, inv), to_code(v[0].w, inv));
-        if (lane == 0) a.y_scale[(size_t)(m0 + t) * ((a.N + kBlk - 1) / kBlk) + wt] = (uint8_t)(e + 127);
+        for (int m = 0; m < MATS; ++m) {
+          float4 p[kMaxSplits];
+#pragma unroll
+          for (int r = 0; r < kMaxSplits; ++r)
+            if (r < splits) p[r] = ld_dsmem_f4(mapa_shared(base + (uint32_t)((m * NT + t) * kBlk * 4), (uint32_t)r));
+          v[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int r = 0; r < kMaxSplits; ++r)
+            if (r < splits) v[m] = make_float4(v[m].x + p[r].x, v[m].y + p[r].y, v[m].z + p[r].z, v[m].w + p[r].w);
+        }
+        if constexpr (MATS == 2)
+          v[0] = make_float4(gated(v[0].x, v[1].x), gated(v[0].y, v[1].y), gated(v[0].z, v[1].z), gated(v[0].w, v[1].w));
       }
+      if (MATS == 1 || a.y_dtype != TB_E4M3) {
+        if (col < a.N)
+          put4(a.y, a.y_dtype, at, make_float4(v[0].x + res.x, v[0].y + res.y, v[0].z + res.z, v[0].w + res.w));
+        continue;
+      }
+      // (columns past N hold zeros: weight rows past N read as zeros)
+      float top = fmaxf(fmaxf(finite_mag(v[0].x), finite_mag(v[0].y)), fmaxf(finite_mag(v[0].z), finite_mag(v[0].w)));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = block_exponent(top);
+      const float inv = pow2i(-e);
+      if (col < a.N)
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + at) =
+            codes_of4(to_code(v[0].x, inv), to_code(v[0].y, inv), to_code(v[0].z, inv), to_code(v[0].w, inv));
+      if (lane == 0) a.y_scale[(size_t)(m0 + t) * ((a.N + kBlk - 1) / kBlk) + wt] = (uint8_t)(e + 127);
     }
   }
 
   // no CTA leaves (and frees its shared memory) while another still reads it
   tc_fence_before();
   __syncwarp();
-  cluster_sync();
+  if (splits > 1) cluster_sync();
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
-template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStream_t s) {
-  using C = FewCfg<NT, MATS, CPS>;
+template <int NT, int MATS, int CPS, bool ONE> cudaError_t launch(const GemmArgs& a, int wtiles, int sp, cudaStream_t s) {
+  using C = FewCfg<NT, MATS, CPS, ONE>;
   CUtensorMap tw, tw3, tx;
   cudaError_t e = make_tmap_rows(&tw, 1, a.w.codes, 1, (uint64_t)a.N, (uint64_t)a.K, kBlk, kBlk);
   if (e != cudaSuccess) return e;
@@ -319,44 +388,82 @@ template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStrea
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!set[dev]) {
-    e = cudaFuncSetAttribute(k_e4m3_few<NT, MATS, CPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    e = cudaFuncSetAttribute(k_e4m3_few<NT, MATS, CPS, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;
     set[dev] = true;
   }
-  const int wtiles = (a.N + kBlk - 1) / kBlk, kblocks = (a.K + kBlk - 1) / kBlk;
-  const long long tiles = (long long)wtiles * ((a.M + NT - 1) / NT);
-  const long long slots = (long long)CPS * sm_count();
-  const int sp = tiles > slots ? 1 : skinny_split_count((int)tiles, kblocks, (int)slots);
-  if (tiles * sp > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long ctas = (long long)wtiles * ((a.M + NT - 1) / NT) * sp;
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * sp));
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(192);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = sp;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = sp;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_e4m3_few<NT, MATS, CPS>, tw, tw3, tx, a, wtiles, sp, device_error_word());
+  cfg.numAttrs = sp > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_e4m3_few<NT, MATS, CPS, ONE>, tw, tw3, tx, a, wtiles, sp, device_error_word());
+}
+
+// CPS: CTAs per SM of the form with several chunks (the one with one chunk has two).
+template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStream_t s) {
+  const int wtiles = (a.N + kBlk - 1) / kBlk, kblocks = (a.K + kBlk - 1) / kBlk;
+  const long long tiles = (long long)wtiles * ((a.M + NT - 1) / NT);
+  auto split = [&](int cps) {
+    const long long slots = (long long)cps * sm_count();
+    return tiles > slots ? 1 : skinny_split_count((int)tiles, kblocks, (int)slots);
+  };
+  const int two = split(2);
+  if ((kblocks + two - 1) / two <= kSet * kChunk) return launch<NT, MATS, 2, true>(a, wtiles, two, s);
+  return launch<NT, MATS, CPS, false>(a, wtiles, CPS == 2 ? two : split(CPS), s);
 }
 
 }  // namespace
 
-cudaError_t launch_gemm_e4m3_few(const GemmArgs& a, cudaStream_t s) {
-  if (a.M <= 16) return go<16, 1, 2>(a, s);
-  if (a.M <= 32) return go<32, 1, 2>(a, s);
-  if (a.M <= 64) return go<64, 1, 2>(a, s);
-  return go<128, 1, 1>(a, s);
+// Rows of X per tile for M rows, or 0 where k_e4m3_many is the better one.  The smallest
+// tile that has all tiles resident at once, two CTAs per SM; wider ones read the weights
+// less often but finish later.  Beyond that, 128-row tiles still beat the 256 x 256 ones
+// of k_e4m3_many where K is a few blocks, since those take 8 us before and after their
+// blocks.  Measured, us, few (rows per tile) and many:
+//   K 768, N 2304:   512 rows 6.0 (32), 6.1 (64), 8.2 (128), 11.1; 1024: 7.0 (64), 11.1;
+//                    1371: 12.1 (64), 9.3 (128), 12.1; 2048: 10.5 (128), 13.1
+//   K 4096, N 4096:  128: 10.3 (32), 9.4 (64), 10.9 (128), 17.7; 512: 14.8 (64), 18.1;
+//                    768: 27.0 (64), 28.5 (128), 18.8
+//   K 14336, N 4096: 256: 24.2 (64), 38.9; 512: 37.6 (64), 39.5; 768: 70.6 (64), 40.4
+//   K 4096, N 14336: 128: 17.0 (64), 20.8; 192: 28.3 (64), 20.9
+//   gated, K 4096, F 14336: 64: 28.7 (32), 28.1 (64), 31.7; 128: 45.0 (64), 32.2
+//   gated, K 768, F 2048:   64: 6.9 (32), 9.8 (64), 9.5; 512: 8.4 (32), 10.3;
+//                    1024: 16.0 (32), 11.9 (64), 11.0
+int e4m3_few_tile(int M, int N, int K, int mats, int sms) {
+  const long long wtiles = (N + kBlk - 1LL) / kBlk, slots = 2LL * sms;
+  auto fits = [&](int nt) { return wtiles * ((M + nt - 1LL) / nt) <= slots; };
+  const bool brief = K <= 8 * kBlk;
+  if (M <= 16) return 16;
+  if (M <= 32 || (brief && fits(32))) return 32;
+  if (M <= 64 || (mats == 1 && fits(64))) return 64;
+  return mats == 1 && brief && fits(128) ? 128 : 0;
 }
-cudaError_t launch_gated_e4m3_few(const GemmArgs& a, cudaStream_t s) {
-  if (a.M <= 16) return go<16, 2, 2>(a, s);
-  if (a.M <= 32) return go<32, 2, 2>(a, s);
-  return go<64, 2, 1>(a, s);
+
+cudaError_t launch_gemm_e4m3_few(const GemmArgs& a, int tile, cudaStream_t s) {
+  switch (tile) {
+    case 16: return go<16, 1, 2>(a, s);
+    case 32: return go<32, 1, 2>(a, s);
+    case 64: return go<64, 1, 2>(a, s);
+    default: return go<128, 1, 1>(a, s);
+  }
+}
+cudaError_t launch_gated_e4m3_few(const GemmArgs& a, int tile, cudaStream_t s) {
+  switch (tile) {
+    case 16: return go<16, 2, 2>(a, s);
+    case 32: return go<32, 2, 2>(a, s);
+    default: return go<64, 2, 1>(a, s);
+  }
 }
 
 }  // namespace tb

@@ -420,7 +420,8 @@ TB_API tb_status tb_kvcache_attn(const tb_attn_cfg* cfg, const void* q, const tb
  *    rows (activations)   : blocks of 128 columns of a row, scale [rows, ceil(cols/128)];
  *    weights ([out, in])  : blocks of 128 x 128, scale [ceil(rows/128), ceil(cols/128)].
  *  The last block of a row (or column) may be shorter.  cols is a multiple of 16; codes
- *  are 16-byte aligned, scales byte-aligned; rows·cols at most 2^39.
+ *  are 16-byte aligned, scales byte-aligned; rows·cols at most 2^39, each at most
+ *  2^31 - 1024.
  *    The scale of a block that these calls write is 2^e with e the smallest integer in
  *    [-100, 120] for which the block's largest finite |x| is at most 448·2^e (-100 for a
  *    block of zeros).  A value x is held as x / 2^e rounded to nearest even; infinities
@@ -443,8 +444,9 @@ typedef struct {
 TB_API tb_status tb_rmsnorm_e4m3(const void* x, int32_t dtype, const void* r, int32_t r_dtype, void* h, const void* g,
                                  float eps, const tb_e4m3* out, void* stream);
 
-/* The rows x (device, dense [out->rows, out->cols] of dtype) to codes as they are, for
- * instance the attention's output before its projection. */
+/* The rows x (device, dense [out->rows, out->cols] of dtype, 16-byte aligned, apart from
+ * out) to codes as they are, for instance the attention's output before its projection;
+ * at most 2^26 columns. */
 TB_API tb_status tb_quant_e4m3(const void* x, int32_t dtype, const tb_e4m3* out, void* stream);
 
 /* Weights w (device, [in, out] of dtype, as everywhere in this header) to codes:

@@ -58,7 +58,8 @@ def test_norm_refusals(lib, kw, text, status):
 
 @pytest.mark.parametrize("m,text,status", [
     ((4, 0), "cols must be positive", 1), ((-1, 16), "rows non-negative", 1), ((4, 24), "multiple of 16", 2),
-    ((4, 32784), "at most 32768", 2), ((2 ** 31 - 1, 1024), "2^39", 2), ((4, 256, None), "non-NULL", 1),
+    ((4, 32784), "at most 32768", 2), ((2 ** 30, 1024), "2^39", 2), ((2 ** 31 - 1, 16), "2^31 - 1024", 2),
+    ((2, 2 ** 31 - 16), "2^31 - 1024", 2), ((4, 256, None), "non-NULL", 1),
     ((4, 256, at(20), None), "non-NULL", 1), ((4, 256, at(20) + 8), "codes must be 16-byte", 1),
     ((4, 256, at(20), at(20) + 100), "two outputs overlap", 1),
 ])
@@ -67,6 +68,10 @@ def test_out_refusals(lib, m, text, status):
     if "32768" not in text:
         refused(lib, lib.tb_quant_e4m3(at(1), 1, mat(*m), None), text, status)
         refused(lib, lib.tb_pack_e4m3(at(1), 1, mat(*m), None), text, status)
+
+
+def test_quant_of_too_wide_rows(lib):
+    refused(lib, lib.tb_quant_e4m3(at(1), 1, mat(1, 2 ** 26 + 16), None), "2^26 columns", 2)
 
 
 def test_null_structs(lib):
@@ -121,6 +126,18 @@ def test_empty_calls_need_no_pointers(lib):
     assert lib.tb_pack_e4m3(None, 0, none, None) == 0
     assert lib.tb_gemm_e4m3(none, mat(32, 256), None, None, 1, None) == 0
     assert lib.tb_gated_e4m3(none, mat(32, 256), mat(32, 256), None, 3, None, None) == 0
+
+
+# ---- the rule for the kernel --------------------------------------------------------
+
+@pytest.mark.parametrize("M,N,K,mats,tile", [
+    (1, 6144, 4096, 1, 16), (16, 6144, 4096, 1, 16), (17, 6144, 4096, 1, 32), (33, 6144, 4096, 1, 64),
+    (512, 2304, 768, 1, 32), (513, 2304, 768, 1, 64), (1371, 2304, 768, 1, 128), (2049, 2304, 768, 1, 0),
+    (576, 4096, 4096, 1, 64), (577, 4096, 4096, 1, 0), (128, 14336, 4096, 1, 64), (129, 14336, 4096, 1, 0),
+    (32, 14336, 4096, 2, 32), (64, 14336, 4096, 2, 64), (65, 14336, 4096, 2, 0), (333, 2048, 768, 2, 32),
+    (1024, 2048, 768, 2, 0), (2 ** 31 - 1, 16, 16, 1, 0), (2 ** 31 - 1, 16, 16, 2, 0), (64, 2 ** 31 - 16, 16, 1, 64)])
+def test_tile_rule(lib, M, N, K, mats, tile):
+    assert lib.tbx_e4m3_few_tile(M, N, K, mats, 152) == tile
 
 
 # ---- the binding ----------------------------------------------------------------

@@ -27,7 +27,7 @@ def no_error():
 
 @pytest.fixture
 def form():
-    """Sets the kernel that the products of a test take."""
+    """Sets the form that the products of a test take."""
     yield tbx_e4m3_form
     tbx_e4m3_form(0)
 
@@ -241,6 +241,28 @@ def test_gated(M, F, K, out_dtype):
         assert (np.abs(f64(y) - exact) <= off + 2 * HALF[out_dtype] * (np.abs(exact) + off)).all()
 
 
+def test_gated_gates_far_below_zero():
+    """SiLU of gates down to -448·2^4: below -87 it is under 1e-35 and may come back as 0."""
+    M, F, K = 20, 128, 128
+    x = torch.zeros(M, K, dtype=torch.uint8)
+    x[:, 0] = 0x38
+    w1, w3 = torch.zeros(F, K, dtype=torch.uint8), torch.zeros(F, K, dtype=torch.uint8)
+    w1[:, 0], w3[:, 0] = 0x80 + torch.arange(F, dtype=torch.uint8).clamp(max=126), 0x38
+    one = torch.full((M, 1), 127, dtype=torch.uint8).view(SCALE).cuda()
+    big = torch.full((1, 1), 131, dtype=torch.uint8).view(SCALE).cuda()
+    unit = torch.full((1, 1), 127, dtype=torch.uint8).view(SCALE).cuda()
+    for form in (16, 64, -1):
+        tbx_e4m3_form(form)
+        y = tb.tb_gated_e4m3(tb.E4M3Rows(x.view(CODE).cuda(), one), tb.E4M3Weight(w1.view(CODE).cuda(), big),
+                             tb.E4M3Weight(w3.view(CODE).cuda(), unit), out_dtype=tb.TB_F32)
+        tbx_e4m3_form(0)
+        no_error()
+        gates = ref.VALUES[w1[:, 0].numpy()] * 16
+        with np.errstate(over="ignore"):
+            want = ref.silu(gates)
+        assert (np.abs(f64(y) - want[None]) <= 8 * 2.0 ** -24 * np.abs(want) + 1e-35).all()
+
+
 def test_gated_far_gates():
     """Gates far below and above zero: SiLU gives 0 and the gate itself, not NaN."""
     M, F, K = 4, 128, 128
@@ -273,6 +295,43 @@ def test_empty_calls():
     no_error()
 
 
+# ---- each width of tile, several tiles of rows ---------------------------------------
+
+@pytest.mark.parametrize("tile", [16, 32, 64, 128])
+@pytest.mark.parametrize("M,N,K", [(1, 272, 400), (131, 144, 2064), (300, 400, 640), (129, 128, 9216)])
+def test_gemm_tiles(form, tile, M, N, K):
+    form(tile)
+    g = gen(M + N + K)
+    x, w = make_rows(tb, M, K, g), make_weight(tb, N, K, g)
+    for dtype, with_res in ((F32, True), (BF16, False), (BF16, True)):
+        res = (torch.randn(M, N, generator=g) * 100).to(dtype).cuda() if with_res else None
+        buf = torch.full((M + 4, N), 7.0, dtype=dtype, device="cuda")
+        y = tb.tb_gemm_e4m3(x, w, res=res, y=buf[2:2 + M])
+        no_error()
+        assert (buf[:2] == 7).all() and (buf[2 + M:] == 7).all()
+        check_product(y, *product(rows_np(x), weight_np(w), None if res is None else f64(res)), K, dtype)
+
+
+@pytest.mark.parametrize("tile", [16, 32, 64])
+@pytest.mark.parametrize("M,F,K", [(1, 272, 400), (131, 144, 2064), (300, 400, 640), (70, 128, 9216)])
+def test_gated_tiles(form, tile, M, F, K):
+    form(tile)
+    g = gen(M + F + K)
+    x, w1, w3 = make_rows(tb, M, K, g), make_weight(tb, F, K, g), make_weight(tb, F, K, g)
+    w1.scale.view(torch.uint8).sub_(int(np.log2(K) / 2) + 11)
+    exact, off = gated_and_off(rows_np(x), weight_np(w1), weight_np(w3), K)
+    buf = torch.full((M + 4, F), 9, dtype=torch.uint8, device="cuda")
+    sc = torch.full((M + 4, -(-F // 128)), 9, dtype=torch.uint8, device="cuda")
+    out = tb.tb_gated_e4m3(x, w1, w3, out=tb.E4M3Rows(buf[2:2 + M].view(CODE), sc[2:2 + M].view(SCALE)))
+    no_error()
+    for t in (buf, sc):
+        assert (t[:2] == 9).all() and (t[2 + M:] == 9).all()
+    check_rows(bytes_of(out.codes), bytes_of(out.scale), exact, off)
+    y = tb.tb_gated_e4m3(x, w1, w3, out_dtype=tb.TB_F32)
+    no_error()
+    assert (np.abs(f64(y) - exact) <= off + 2 * HALF[F32] * (np.abs(exact) + off)).all()
+
+
 # ---- many rows ----------------------------------------------------------------------
 # One row to some tiles per cluster (both accumulators, more tiles than clusters), a row
 # unit whose second half lies past M, K of one set and of an odd number of them.
@@ -284,7 +343,7 @@ MANY = [(1, 16, 16), (128, 256, 128), (129, 272, 144), (256, 512, 512), (300, 11
 @pytest.mark.parametrize("M,N,K", MANY)
 @pytest.mark.parametrize("dtype,with_res", [(F32, False), (BF16, True), (F32, True)])
 def test_gemm_many(form, M, N, K, dtype, with_res):
-    form(2)
+    form(-1)
     g = gen(M + N + K)
     x, w = make_rows(tb, M, K, g), make_weight(tb, N, K, g)
     res = (torch.randn(M, N, generator=g) * 100).to(dtype).cuda() if with_res else None
@@ -301,7 +360,7 @@ def test_gemm_many(form, M, N, K, dtype, with_res):
                                    (2100, 1296, 272)])
 @pytest.mark.parametrize("out_dtype", ["codes", BF16, F32])
 def test_gated_many(form, M, F, K, out_dtype):
-    form(2)
+    form(-1)
     g = gen(M + F + K)
     x, w1, w3 = make_rows(tb, M, K, g), make_weight(tb, F, K, g), make_weight(tb, F, K, g)
     w1.scale.view(torch.uint8).sub_(int(np.log2(K) / 2) + 11)
@@ -329,13 +388,13 @@ def test_both_kernels_agree_on_what_nan_reaches(form):
     w.codes.view(torch.uint8)[5, 527] = 0xFF
     w.scale.view(torch.uint8)[2, 1] = 255
     got = []
-    for f in (1, 2):
+    for f in (16, 32, 64, 128, -1):
         form(f)
         got.append(torch.isnan(tb.tb_gemm_e4m3(x, w)))
     no_error()
     hit = torch.zeros(M, N, dtype=torch.bool, device="cuda")
     hit[3], hit[266], hit[:, 5], hit[:, 256:] = True, True, True, True
-    assert torch.equal(got[0], hit) and torch.equal(got[1], hit)
+    assert all(torch.equal(t, hit) for t in got)
 
 
 # ---- together -----------------------------------------------------------------------
