@@ -441,8 +441,8 @@ template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStrea
 //   gated, K 768, F 2048:   64: 6.9 (32), 9.8 (64), 9.5; 512: 8.4 (32), 10.3;
 //                    1024: 16.0 (32), 11.9 (64), 11.0
 int e4m3_few_tile(int M, int N, int K, int mats, int sms) {
-  const long long wtiles = (N + kBlk - 1LL) / kBlk, slots = 2LL * sms;
-  auto fits = [&](int nt) { return wtiles * ((M + nt - 1LL) / nt) <= slots; };
+  const long long wtiles = ((long long)N + kBlk - 1) / kBlk, slots = 2LL * sms;
+  auto fits = [&](int nt) { return wtiles * (((long long)M + nt - 1) / nt) <= slots; };
   const bool brief = K <= 8 * kBlk;
   if (M <= 16) return 16;
   if (M <= 32 || (brief && fits(32))) return 32;
