@@ -68,6 +68,8 @@ tb_status check_weights(const tb_e4m3* w, const char* name, const tb_e4m3* x, bo
   const tb_status st = check(w, name, tensors);
   if (st != TB_OK) return st;
   if (w->rows <= 0) return report(TB_ERR_INVALID_ARG, "%s: rows must be positive", name);
+  // (columns of the result are counted in bytes, in 32 bits)
+  if (w->rows > 1 << 28) return report(TB_ERR_UNSUPPORTED, "%s: at most 2^28 rows (%d)", name, w->rows);
   if (w->rows % 16) return report(TB_ERR_UNSUPPORTED, "%s: rows (%d) must be a multiple of 16", name, w->rows);
   if (w->cols != x->cols)
     return report(TB_ERR_INVALID_ARG, "%s has %d columns, x has %d", name, w->cols, x->cols);

@@ -31,10 +31,10 @@ constexpr int kRowsCta = 128;    // rows of X per CTA
 struct ManyCfg {
   static constexpr int STAGES = 6;
   static constexpr uint32_t A_BYTES = kRowsCta * kBlk, B_BYTES = 128 * kBlk, STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr uint32_t OFF_BAR = STAGES * STAGE_BYTES;
-  static constexpr uint32_t OFF_EPI = OFF_BAR + 256;         // 4 warps x 32 rows x 144 bytes
-  static constexpr uint32_t ROW_BYTES = 144;                 // 128 bytes of a row and 16 of padding
-  static constexpr size_t SMEM = OFF_EPI + 4 * 32 * ROW_BYTES + 1024;
+  // two pieces of 32 rows x 128 bytes of y for each epilogue warp
+  static constexpr uint32_t OFF_EPI = STAGES * STAGE_BYTES, PIECE = 32 * 128;
+  static constexpr uint32_t OFF_BAR = OFF_EPI + 4 * 2 * PIECE;
+  static constexpr size_t SMEM = OFF_BAR + 256 + 1024;
   static constexpr uint32_t ACC1 = 224, SETS_AT = 480, SET_COLS = 16;
   static constexpr int THREADS = 320;
 };
@@ -53,10 +53,12 @@ __device__ __forceinline__ void place(int tile, int m_units, int n_tiles, int gr
   mu = first + local - nt * gm;
 }
 
-template <bool GATED>
+// ESIZE: bytes of an element of y.
+template <bool GATED, int ESIZE>
 __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
     k_e4m3_many(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                const __grid_constant__ CUtensorMap tmW3, GemmArgs a, int m_units, int n_tiles, int group, int* err) {
+                const __grid_constant__ CUtensorMap tmW3, const __grid_constant__ CUtensorMap tmY,
+                const __grid_constant__ CUtensorMap tmRes, GemmArgs a, int m_units, int n_tiles, int group, int* err) {
   using C = ManyCfg;
   constexpr int STAGES = C::STAGES;
   constexpr int COLS = GATED ? 128 : 256;               // columns of y per tile
@@ -69,10 +71,11 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
   uint64_t* tfull = sempty + 2;                         // accumulators
   uint64_t* tempty = tfull + 2;
   uint64_t* shared_free = tempty + 2;                   // the columns both accumulators use
-  uint64_t* drain = shared_free + 1;
+  uint64_t* rfull = shared_free + 1;                    // residual pieces, two for each epilogue warp
+  uint64_t* drain = rfull + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * STAGES + 8) * 8 + 8 <= 256, "barriers");
+  static_assert((2 * STAGES + 16) * 8 + 8 <= 256, "barriers");
 
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -93,12 +96,14 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
       mbar_init(&tempty[s], 8);
     }
     mbar_init(shared_free, 8);
+    for (int i = 0; i < 8; ++i) mbar_init(&rfull[i], 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&tmX);
     prefetch_tmap(&tmW);
     if (GATED) prefetch_tmap(&tmW3);
+    prefetch_tmap(&tmY);
   }
   // both CTAs' barriers exist before either CTA's copies or commits reach them
   __syncthreads();
@@ -233,107 +238,189 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
       if (more) load();
     }
   } else {
-    // Epilogue: a lane's row of the tile, 32 columns (or pairs of 32) at a time.
+    // Epilogue: a lane has a row of the tile.  A piece of 128 bytes of each of the warp's
+    // 32 rows goes through shared memory (128-byte swizzle) to a TMA store, which drops what
+    // lies past M or N; the next piece's residual is on its way into the other buffer
+    // meanwhile, the next tile's first one before its sums are there.
     pdl_wait();
-    const int quad = warp & 3;
-    uint8_t* stage = smem + C::OFF_EPI + (warp - 2) * 32 * C::ROW_BYTES;
+    const int quad = warp & 3, w = warp - 2;
+    uint8_t* buf = smem + C::OFF_EPI + w * 2 * C::PIECE;
     const uint32_t tempty_cl[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
     const uint32_t shared_cl = mapa_shared(smem_u32(shared_free), 0);
-    const int sub_row = lane >> 3, sub = lane & 7;        // 8 lanes to a row of the stage
-    int local = 0;
-    for (int tile = tile0; tile < tiles; tile += tstep, ++local) {
-      const int acc = local & 1;
-      if (!mbar_wait_warp(&tfull[acc], (local >> 1) & 1, abort_flag, err)) break;
-      tc_fence_after();
+    constexpr int pieces = COLS * ESIZE / 128, wide = 128 / ESIZE;   // of a tile; columns of one
+    const bool res = !GATED && a.res;
+    // piece i of a tile in accumulator `acc`, the one with the shared columns first: the
+    // last of accumulator 0, the first of accumulator 1
+    auto piece_of = [&](int i, int acc) { return acc ? i : (i == 0 ? pieces - 1 : i - 1); };
+    auto where = [&](int tile, int acc, int i, int& row, int& col) {
       int mu, nt;
       place(tile, m_units, n_tiles, group, mu, nt);
-      const int row0 = (mu * 2 + (int)rank) * kRowsCta + quad * 32;
+      row = (mu * 2 + (int)rank) * kRowsCta + quad * 32;
+      col = nt * COLS + piece_of(i, acc) * wide;
+      return row < a.M && col < a.N;
+    };
+    uint32_t n = 0, rphase = 0;        // pieces so far; bit b: the parity of buffer b's next residual
+    auto request = [&](int tile, int acc, int i, uint32_t b) {
+      int row, col;
+      if (tile >= tiles || !where(tile, acc, i, row, col) || lane != 0) return;
+      mbar_arrive_expect_tx(&rfull[w * 2 + b], C::PIECE);
+      tma_load_3d(&tmRes, buf + b * C::PIECE, &rfull[w * 2 + b], col * ESIZE, row, 0);
+    };
+    if (res) request(tile0, 0, 0, 0);
+    bool ok = true;
+    int local = 0;
+    for (int tile = tile0; ok && tile < tiles; tile += tstep, ++local) {
+      const int acc = local & 1;
+      if (!(ok = mbar_wait_warp(&tfull[acc], (local >> 1) & 1, abort_flag, err))) break;
+      tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + acc * C::ACC1;
-      // Chunks of 32 columns of y, the one in the shared columns first: the last of
-      // accumulator 0, the first of accumulator 1.
-      constexpr int CHUNKS = COLS / 32;
-      auto chunk_of = [&](int i) { return acc ? i : (i + CHUNKS - 1) % CHUNKS; };
-      // the 32 values of this lane's row, finished but for the residual
-      auto take = [&](int i, float (&v)[32]) {
-        const int c = chunk_of(i);
+      // 32 columns of this lane's row, finished but for the residual; `last`: the piece's
+      auto take = [&](int c, bool free_shared, bool free_all, float (&v)[32]) {
         uint32_t r[32], u[32];
-        tmem_ld32(taddr + c * 32, r);
-        if constexpr (GATED) tmem_ld32(taddr + 128 + c * 32, u);
+        tmem_ld32(taddr + c, r);
+        if constexpr (GATED) tmem_ld32(taddr + 128 + c, u);
         tmem_wait_ld();
-        // the shared columns, or all of them, are in registers
-        if (i == 0 || i == CHUNKS - 1) {
+        if (free_shared || free_all) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(i == 0 ? shared_cl : tempty_cl[acc]);
+          if (lane == 0) {
+            if (free_shared) mbar_arrive_cluster(shared_cl);
+            if (free_all) mbar_arrive_cluster(tempty_cl[acc]);
+          }
         }
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           v[j] = GATED ? gated(__uint_as_float(r[j]), __uint_as_float(u[j])) : __uint_as_float(r[j]);
       };
-      if (GATED && a.y_dtype == TB_E4M3) {
-        float v[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) take(i, v[i]);
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) top = fmaxf(top, finite_mag(v[i][j]));
-        const int e = block_exponent(top);
-        const float inv = pow2i(-e);
-        uint4* my = reinterpret_cast<uint4*>(stage + lane * C::ROW_BYTES);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t q[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            q[j] = codes_of4(to_code(v[i][4 * j], inv), to_code(v[i][4 * j + 1], inv), to_code(v[i][4 * j + 2], inv),
-                             to_code(v[i][4 * j + 3], inv));
-          const int c = chunk_of(i);
-          my[2 * c] = make_uint4(q[0], q[1], q[2], q[3]);
-          my[2 * c + 1] = make_uint4(q[4], q[5], q[6], q[7]);
-        }
-        if (row0 + lane < a.M) a.y_scale[(size_t)(row0 + lane) * n_tiles + nt] = (uint8_t)(e + 127);
-        __syncwarp();
-        const int col = nt * 128 + sub * 16;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = sub_row + 4 * i, row = row0 + r;
-          if (row < a.M && col < a.N)
-            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.y) + (size_t)row * a.N + col) =
-                *reinterpret_cast<const uint4*>(stage + r * C::ROW_BYTES + sub * 16);
-        }
-        __syncwarp();
-        continue;
-      }
 #pragma unroll 1
-      for (int i = 0; i < CHUNKS; ++i) {
-        // the residual is requested first; 8 lanes then finish and store a row's 32 columns
-        const int col = nt * COLS + chunk_of(i) * 32 + sub * 4;
-        float4 res[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int row = row0 + sub_row + 4 * k;
-          res[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (!GATED && a.res && row < a.M && col < a.N) res[k] = get4(a.res, a.y_dtype, (size_t)row * a.N + col);
+      for (int i = 0; i < pieces; ++i, ++n) {
+        const uint32_t b = n & 1;
+        int row, col;
+        const bool in = where(tile, acc, i, row, col);
+        const int c0 = piece_of(i, acc) * wide;
+        const bool first = i == 0, last = i + 1 == pieces;
+        uint8_t* mine = buf + b * C::PIECE + lane * 128;
+        if (res) {
+          // the next piece's residual, once the store before this one has left its buffer
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          if (last) request(tile + tstep, acc ^ 1, 0, b ^ 1);
+          else request(tile, acc, i + 1, b ^ 1);
+          if (in) {
+            if (!(ok = mbar_wait_warp(&rfull[w * 2 + b], rphase >> b & 1, abort_flag, err))) break;
+            rphase ^= 1u << b;
+          }
+        } else {
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
         }
-        float v[32];
-        take(i, v);
-        float4* my = reinterpret_cast<float4*>(stage + lane * C::ROW_BYTES);
+        // a piece's 16-byte part p lies at p ^ (row % 8)
+        auto part = [&](int p) { return reinterpret_cast<uint4*>(mine + ((p ^ (lane & 7)) << 4)); };
+        if constexpr (ESIZE == 1) {
+          // The values go back to tensor memory, into those of their columns that no other
+          // tile uses, until the row's scale is known: 128 of them would not stay in registers.
+          const uint32_t keep = taddr + (acc ? 128 : 0);
+          float top = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) my[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-        __syncwarp();
+          for (int q = 0; q < 4; ++q) {
+            const int cq = acc ? q : (q + 3) & 3;      // shared columns first, as the pieces go
+            float v[32];
+            take(cq * 32, q == 0, false, v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = sub_row + 4 * k, row = row0 + r;
-          const float4 t = *reinterpret_cast<const float4*>(stage + r * C::ROW_BYTES + sub * 16);
-          if (row < a.M && col < a.N)
-            put4(a.y, a.y_dtype, (size_t)row * a.N + col,
-                 make_float4(t.x + res[k].x, t.y + res[k].y, t.z + res[k].z, t.w + res[k].w));
+            for (int j = 0; j < 32; j += 2) top = fmax3(top, fabsf(v[j]), fabsf(v[j + 1]));
+            tmem_st32(keep + cq * 32, *reinterpret_cast<const uint32_t(*)[32]>(v));
+          }
+          tmem_wait_st();
+          const bool wild = top == INFINITY;           // an infinity: told from values one by one
+          if (wild) top = 0.f;
+          if (__any_sync(0xffffffffu, wild)) {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t r[32];
+              tmem_ld32(keep + q * 32, r);
+              tmem_wait_ld();
+              if (wild) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) top = fmaxf(top, finite_mag(__uint_as_float(r[j])));
+              }
+            }
+          }
+          const int e = block_exponent(top);
+          const float inv = pow2i(-e);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t r[32], k[8];
+            tmem_ld32(keep + q * 32, r);
+            tmem_wait_ld();
+            if (q == 3) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(tempty_cl[acc]);
+            }
+            if (wild) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(to_code(__uint_as_float(r[j]), 1.f));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              k[j] = codes_of4(__uint_as_float(r[4 * j]) * inv, __uint_as_float(r[4 * j + 1]) * inv,
+                               __uint_as_float(r[4 * j + 2]) * inv, __uint_as_float(r[4 * j + 3]) * inv);
+            *part(2 * q) = make_uint4(k[0], k[1], k[2], k[3]);
+            *part(2 * q + 1) = make_uint4(k[4], k[5], k[6], k[7]);
+          }
+          if (row + lane < a.M) a.y_scale[(size_t)(row + lane) * n_tiles + col / 128] = (uint8_t)(e + 127);
+        } else if constexpr (ESIZE == 4) {
+          float v[32];
+          take(c0, first, last, v);
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            float4 t = make_float4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+            float4* at = reinterpret_cast<float4*>(part(p));
+            if (res) {
+              const float4 r = *at;
+              t = make_float4(t.x + r.x, t.y + r.y, t.z + r.z, t.w + r.w);
+            }
+            *at = t;
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // (of accumulator 0's first piece the upper half holds the shared columns, of
+            // accumulator 1's the lower: that half first)
+            const int hh = acc ? h : h ^ 1;
+            float v[32];
+            take(c0 + 32 * hh, first && h == 0, last && h == 1, v);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              uint4* at = part(4 * hh + p);
+              uint4 r = make_uint4(0, 0, 0, 0), o;
+              if (res) r = *at;
+              const uint32_t* rr = &r.x;
+              uint32_t* oo = &o.x;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float lo = v[8 * p + 2 * k] + __uint_as_float(rr[k] << 16);
+                const float hi = v[8 * p + 2 * k + 1] + __uint_as_float(rr[k] & 0xffff0000u);
+                const __nv_bfloat162 t = res ? __floats2bfloat162_rn(lo, hi)
+                                             : __floats2bfloat162_rn(v[8 * p + 2 * k], v[8 * p + 2 * k + 1]);
+                oo[k] = *reinterpret_cast<const uint32_t*>(&t);
+              }
+              *at = o;
+            }
+          }
         }
+        fence_proxy_async();
         __syncwarp();
+        if (in && lane == 0) tma_store_3d(&tmY, buf + b * C::PIECE, col * ESIZE, row, 0);
+        if (lane == 0) bulk_commit();
       }
     }
+    // a residual that was requested lands before the CTA ends, whatever became of its sums
+    if (!ok && res) {
+      volatile int no_abort = 0;
+      for (uint32_t b = 0; b < 2; ++b) mbar_wait(&rfull[w * 2 + b], rphase >> b & 1, &no_abort, err);
+    }
+    if (lane == 0) bulk_wait_all();
   }
 
   // Every instruction of the pair is done (the issuer waited on its drain) before
@@ -347,9 +434,9 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
   }
 }
 
-template <bool GATED> cudaError_t go(const GemmArgs& a, cudaStream_t s) {
+template <bool GATED, int ESIZE> cudaError_t go(const GemmArgs& a, cudaStream_t s) {
   using C = ManyCfg;
-  CUtensorMap tx, tw, tw3;
+  CUtensorMap tx, tw, tw3, ty, tr;
   cudaError_t e = make_tmap_rows(&tx, 1, a.x.codes, 1, (uint64_t)a.M, (uint64_t)a.K, kBlk, kRowsCta);
   if (e != cudaSuccess) return e;
   e = make_tmap_rows(&tw, 1, a.w.codes, 1, (uint64_t)a.N, (uint64_t)a.K, kBlk, 128);
@@ -357,6 +444,11 @@ template <bool GATED> cudaError_t go(const GemmArgs& a, cudaStream_t s) {
   tw3 = tw;
   if (GATED && (e = make_tmap_rows(&tw3, 1, a.w3.codes, 1, (uint64_t)a.N, (uint64_t)a.K, kBlk, 128)) != cudaSuccess)
     return e;
+  // y and the residual by bytes: a piece is 128 of each of 32 rows
+  const uint64_t row_bytes = (uint64_t)a.N * ESIZE;
+  if ((e = make_tmap_rows(&ty, 1, a.y, 1, (uint64_t)a.M, row_bytes, 128, 32)) != cudaSuccess) return e;
+  tr = ty;
+  if (a.res && (e = make_tmap_rows(&tr, 1, a.res, 1, (uint64_t)a.M, row_bytes, 128, 32)) != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -374,12 +466,12 @@ template <bool GATED> cudaError_t go(const GemmArgs& a, cudaStream_t s) {
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!clusters[dev]) {
-    e = cudaFuncSetAttribute(k_e4m3_many<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    e = cudaFuncSetAttribute(k_e4m3_many<GATED, ESIZE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;
     int n = 0;
     cfg.gridDim = dim3(2 * (sm_count() / 2));
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&n, k_e4m3_many<GATED>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, k_e4m3_many<GATED, ESIZE>, &cfg);
     if (e != cudaSuccess) return e;
     if (n <= 0) return cudaErrorNotSupported;
     clusters[dev] = n;
@@ -394,12 +486,16 @@ template <bool GATED> cudaError_t go(const GemmArgs& a, cudaStream_t s) {
   const int group = a.K <= 8192 && w_bytes > (size_t(48) << 20) && m_units > 1 ? std::min(m_units, 32) : 0;
   cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(tiles, clusters[dev]));
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_e4m3_many<GATED>, tx, tw, tw3, a, m_units, n_tiles, group, device_error_word());
+  return cudaLaunchKernelEx(&cfg, k_e4m3_many<GATED, ESIZE>, tx, tw, tw3, ty, tr, a, m_units, n_tiles, group, device_error_word());
 }
 
 }  // namespace
 
-cudaError_t launch_gemm_e4m3_many(const GemmArgs& a, cudaStream_t s) { return go<false>(a, s); }
-cudaError_t launch_gated_e4m3_many(const GemmArgs& a, cudaStream_t s) { return go<true>(a, s); }
+cudaError_t launch_gemm_e4m3_many(const GemmArgs& a, cudaStream_t s) {
+  return a.y_dtype == TB_F32 ? go<false, 4>(a, s) : go<false, 2>(a, s);
+}
+cudaError_t launch_gated_e4m3_many(const GemmArgs& a, cudaStream_t s) {
+  return a.y_dtype == TB_E4M3 ? go<true, 1>(a, s) : a.y_dtype == TB_F32 ? go<true, 4>(a, s) : go<true, 2>(a, s);
+}
 
 }  // namespace tb

@@ -454,7 +454,7 @@ TB_API tb_status tb_quant_e4m3(const void* x, int32_t dtype, const tb_e4m3* out,
 TB_API tb_status tb_pack_e4m3(const void* w, int32_t dtype, const tb_e4m3* out, void* stream);
 
 /* y[m, n] = res[m, n] + sum_k x[m, k] w[n, k]
- *  x    : rows [M, K];  w : weights [N, K], N a multiple of 16.
+ *  x    : rows [M, K];  w : weights [N, K], N a multiple of 16 of at most 2^28.
  *  res  : NULL, or device, dense [M, N] of y_dtype.
  *  y    : device, dense [M, N] of y_dtype (TB_F32 or TB_BF16), 16-byte aligned.  It may
  *         be res itself and overlaps nothing else that is read.

@@ -88,6 +88,7 @@ W = dict(codes=at(10), scale=at(11))
     (mat(4, 256), mat(32, 272, **W), None, at(1), 1, "columns", 1),
     (mat(4, 256), mat(0, 256, **W), None, at(1), 1, "rows must be positive", 1),
     (mat(4, 256), mat(40, 256, **W), None, at(1), 1, "multiple of 16", 2),
+    (mat(4, 256), mat(2 ** 28 + 16, 256, **W), None, at(1), 1, "2^28 rows", 2),
     (mat(4, 256), mat(32, 256, **W), None, at(1), 3, "unknown y_dtype", 1),
     (mat(4, 256), mat(32, 256, **W), None, None, 1, "y must be", 1),
     (mat(4, 256), mat(32, 256, **W), None, at(1) + 8, 1, "y must be", 1),
