@@ -35,7 +35,6 @@ using namespace ptx;
 constexpr int kSet = 4;          // K blocks per scale set: one exponent byte each in a word
 constexpr int kChunk = 4;        // scale sets per chunk
 constexpr int kSets = 8;         // scale sets held in tensor memory: two chunks
-constexpr int kMaxSplits = 8;
 
 // NT rows of X; MATS 1 or 2 weight matrices; CPS CTAs per SM; ONE: a CTA's part of K is
 // at most one chunk, whose sums go from tensor memory straight on.
@@ -56,6 +55,67 @@ template <int NT, int MATS, int CPS, bool ONE> struct FewCfg {
   static_assert(STAGES >= 2 && (2 * STAGES + 2 * kSets + 6) * 8 + 8 <= 512, "barriers");
   static_assert(MATS * NT * kBlk * 4 <= OFF_BAR, "the sums reuse the ring");
 };
+
+// Rows t, t + 4, ... below t1 of a tile by one warp, four columns to a lane: the sums of
+// the S CTAs of the cluster added up in rank order and finished.  B rows at a time, so that
+// S·B loads (of each matrix) are on their way together.  S 1: what lies in part_s is the
+// gated result already, to become codes.
+template <int NT, int MATS, int S, int B>
+__device__ __forceinline__ void finish_rows(const GemmArgs& a, const float* part_s, int m0, int wt, int t, int t1, int lane) {
+  const int col = wt * kBlk + 4 * lane;
+  const uint32_t base = smem_u32(part_s) + 16u * lane;
+  for (; t < t1; t += 4 * B) {
+    float4 v[B], p[B][MATS][S];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int tb = min(t + 4 * b, t1 - 1);         // (past the last: again, not stored)
+      v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (MATS == 1 && a.res && col < a.N) v[b] = get4(a.res, a.y_dtype, (size_t)(m0 + tb) * a.N + col);
+#pragma unroll
+      for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int r = 0; r < S; ++r) {
+          const uint32_t at = base + (uint32_t)((m * NT + tb) * kBlk * 4);
+          if constexpr (S == 1) p[b][m][r] = *reinterpret_cast<const float4*>(part_s + tb * kBlk + 4 * lane);
+          else p[b][m][r] = ld_dsmem_f4(mapa_shared(at, (uint32_t)r));
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const bool in = t + 4 * b < t1;
+      const size_t at = (size_t)(m0 + t + 4 * b) * a.N + col;
+      float4 u[MATS];
+#pragma unroll
+      for (int m = 0; m < MATS; ++m) {
+        u[m] = p[b][m][0];
+#pragma unroll
+        for (int r = 1; r < S; ++r)
+          u[m] = make_float4(u[m].x + p[b][m][r].x, u[m].y + p[b][m][r].y, u[m].z + p[b][m][r].z, u[m].w + p[b][m][r].w);
+      }
+      float4 y = u[0];
+      if constexpr (MATS == 1) {
+        y = make_float4(y.x + v[b].x, y.y + v[b].y, y.z + v[b].z, y.w + v[b].w);
+      } else if constexpr (S > 1) {
+        y = make_float4(gated(u[0].x, u[1].x), gated(u[0].y, u[1].y), gated(u[0].z, u[1].z), gated(u[0].w, u[1].w));
+      }
+      if (MATS == 1 || a.y_dtype != TB_E4M3) {
+        if (in && col < a.N) put4(a.y, a.y_dtype, at, y);
+        continue;
+      }
+      // (columns past N hold zeros: weight rows past N read as zeros)
+      float top = fmaxf(fmaxf(finite_mag(y.x), finite_mag(y.y)), fmaxf(finite_mag(y.z), finite_mag(y.w)));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = block_exponent(top);
+      const float inv = pow2i(-e);
+      if (in && col < a.N)
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + at) =
+            codes_of4(to_code(y.x, inv), to_code(y.y, inv), to_code(y.z, inv), to_code(y.w, inv));
+      if (in && lane == 0)
+        a.y_scale[(size_t)(m0 + t + 4 * b) * ((a.N + kBlk - 1) / kBlk) + wt] = (uint8_t)(e + 127);
+    }
+  }
+}
 
 template <int NT, int MATS, int CPS, bool ONE>
 __global__ void __launch_bounds__(192, CPS)
@@ -195,27 +255,39 @@ __global__ void __launch_bounds__(192, CPS)
     pdl_wait();
     const int quad = warp & 3;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    // scale set s: a word per row for its K blocks; the weights' is the same for all rows of the tile
-    auto feed = [&](int s) {
-      if (!mbar_wait_warp(&sempty[s % kSets], ((s / kSets) & 1) ^ 1u, abort_flag, err)) return false;
+    // Scale set s: a word per row for its K blocks; the weights' is the same for all rows
+    // of the tile.
+    constexpr int XC = NT < 32 ? 1 : NT / 32;
+    struct Words {
+      uint32_t w[MATS], x[XC];
+    };
+    auto words = [&](int s) {
       const int kb = kb0 + s * kSet, n = min(kSet, kb0 + nkb - kb);
-      const uint32_t at = tmem + lanes + C::SETS_AT + (s % kSets) * C::SET_COLS;
-      uint32_t w[MATS], x[4];
-      w[0] = scale_word(a.w.scale + (size_t)wt * kblocks + kb, n);
-      if constexpr (MATS == 2) w[1] = scale_word(a.w3.scale + (size_t)wt * kblocks + kb, n);
+      Words v;
+      v.w[0] = scale_word(a.w.scale + (size_t)wt * kblocks + kb, n);
+      if constexpr (MATS == 2) v.w[1] = scale_word(a.w3.scale + (size_t)wt * kblocks + kb, n);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < XC; ++c) {
         const int m = m0 + c * 32 + lane;
-        x[c] = c * 32 < NT && m < a.M ? scale_word(a.x.scale + (size_t)m * kblocks + kb, n) : 0x7f7f7f7fu;
+        v.x[c] = m < a.M ? scale_word(a.x.scale + (size_t)m * kblocks + kb, n) : 0x7f7f7f7fu;
       }
-      tc_fence_after();
+      return v;
+    };
+    auto place = [&](int s, const Words& v) {
+      const uint32_t at = tmem + lanes + C::SETS_AT + (s % kSets) * C::SET_COLS;
 #pragma unroll
-      for (int m = 0; m < MATS; ++m) tmem_st4(at + 4 * m, w[m], w[m], w[m], w[m]);
-      tmem_st4(at + 4 * MATS, x[0], x[1], x[2], x[3]);
+      for (int m = 0; m < MATS; ++m) tmem_st4(at + 4 * m, v.w[m], v.w[m], v.w[m], v.w[m]);
+      tmem_st4(at + 4 * MATS, v.x[0], v.x[XC > 1 ? 1 : 0], v.x[XC > 2 ? 2 : 0], v.x[XC > 3 ? 3 : 0]);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sfull[s % kSets]);
+    };
+    auto feed = [&](int s) {
+      if (!mbar_wait_warp(&sempty[s % kSets], ((s / kSets) & 1) ^ 1u, abort_flag, err)) return false;
+      const Words v = words(s);
+      tc_fence_after();
+      place(s, v);
       return true;
     };
     // Lane l of quarter q holds weight row 32 q + l, that is a column of y, of every row
@@ -254,11 +326,16 @@ __global__ void __launch_bounds__(192, CPS)
       for (int k = 0; k < P; ++k)
         if (i + k < rows) put1(a.y, a.y_dtype, at + (size_t)k * a.N, v[k]);
     };
-    bool ok = true;
-    int fed = 0;
     if constexpr (ONE) {
-      for (; ok && fed < nsets; ++fed) ok = feed(fed);
-      if (ok && mbar_wait_warp(tfull, 0, abort_flag, err)) {
+      // all sets at once: one latency
+      Words v[kChunk];
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (i < nsets) v[i] = words(i);
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (i < nsets) place(i, v[i]);
+      if (mbar_wait_warp(tfull, 0, abort_flag, err)) {
         tc_fence_after();
 #pragma unroll
         for (int i = 0; i < NT; i += P) {
@@ -273,6 +350,8 @@ __global__ void __launch_bounds__(192, CPS)
         }
       }
     } else {
+      bool ok = true;
+      int fed = 0;
       float acc[MATS][NT];
 #pragma unroll
       for (int m = 0; m < MATS; ++m)
@@ -318,48 +397,12 @@ __global__ void __launch_bounds__(192, CPS)
   if (splits > 1) cluster_sync();
   else __syncthreads();
 
-  if (warp >= 2 && (splits > 1 || a.y_dtype == TB_E4M3)) {
-    const int col = wt * kBlk + 4 * lane;
-    const uint32_t base = smem_u32(part_s) + 16u * lane;
-#pragma unroll 2
-    for (int t = t0 + (warp - 2); t < t1; t += 4) {
-      const size_t at = (size_t)(m0 + t) * a.N + col;
-      float4 res = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (MATS == 1 && a.res && col < a.N) res = get4(a.res, a.y_dtype, at);
-      float4 v[MATS];
-      if (splits == 1) {
-        v[0] = *reinterpret_cast<const float4*>(part_s + t * kBlk + 4 * lane);
-      } else {
-#pragma unroll
-        for (int m = 0; m < MATS; ++m) {
-          float4 p[kMaxSplits];
-#pragma unroll
-          for (int r = 0; r < kMaxSplits; ++r)
-            if (r < splits) p[r] = ld_dsmem_f4(mapa_shared(base + (uint32_t)((m * NT + t) * kBlk * 4), (uint32_t)r));
-          v[m] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int r = 0; r < kMaxSplits; ++r)
-            if (r < splits) v[m] = make_float4(v[m].x + p[r].x, v[m].y + p[r].y, v[m].z + p[r].z, v[m].w + p[r].w);
-        }
-        if constexpr (MATS == 2)
-          v[0] = make_float4(gated(v[0].x, v[1].x), gated(v[0].y, v[1].y), gated(v[0].z, v[1].z), gated(v[0].w, v[1].w));
-      }
-      if (MATS == 1 || a.y_dtype != TB_E4M3) {
-        if (col < a.N)
-          put4(a.y, a.y_dtype, at, make_float4(v[0].x + res.x, v[0].y + res.y, v[0].z + res.z, v[0].w + res.w));
-        continue;
-      }
-      // (columns past N hold zeros: weight rows past N read as zeros)
-      float top = fmaxf(fmaxf(finite_mag(v[0].x), finite_mag(v[0].y)), fmaxf(finite_mag(v[0].z), finite_mag(v[0].w)));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = block_exponent(top);
-      const float inv = pow2i(-e);
-      if (col < a.N)
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.y) + at) =
-            codes_of4(to_code(v[0].x, inv), to_code(v[0].y, inv), to_code(v[0].z, inv), to_code(v[0].w, inv));
-      if (lane == 0) a.y_scale[(size_t)(m0 + t) * ((a.N + kBlk - 1) / kBlk) + wt] = (uint8_t)(e + 127);
-    }
+  if (warp >= 2) {
+    const int t = t0 + warp - 2;
+    if (splits == 8) finish_rows<NT, MATS, 8, 1>(a, part_s, m0, wt, t, t1, lane);
+    else if (splits == 4) finish_rows<NT, MATS, 4, 2>(a, part_s, m0, wt, t, t1, lane);
+    else if (splits == 2) finish_rows<NT, MATS, 2, 4>(a, part_s, m0, wt, t, t1, lane);
+    else if (MATS == 2 && a.y_dtype == TB_E4M3) finish_rows<NT, MATS, 1, 4>(a, part_s, m0, wt, t, t1, lane);
   }
 
   // no CTA leaves (and frees its shared memory) while another still reads it
@@ -426,28 +469,39 @@ template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStrea
 
 }  // namespace
 
-// Rows of X per tile for M rows, or 0 where k_e4m3_many is the better one.  The smallest
-// tile that has all tiles resident at once, two CTAs per SM; wider ones read the weights
-// less often but finish later.  Beyond that, 128-row tiles still beat the 256 x 256 ones
-// of k_e4m3_many where K is a few blocks, since those take 8 us before and after their
-// blocks.  Measured, us, few (rows per tile) and many:
-//   K 768, N 2304:   512 rows 6.0 (32), 6.1 (64), 8.2 (128), 11.1; 1024: 7.0 (64), 11.1;
-//                    1371: 12.1 (64), 9.3 (128), 12.1; 2048: 10.5 (128), 13.1
-//   K 4096, N 4096:  128: 10.3 (32), 9.4 (64), 10.9 (128), 17.7; 512: 14.8 (64), 18.1;
-//                    768: 27.0 (64), 28.5 (128), 18.8
-//   K 14336, N 4096: 256: 24.2 (64), 38.9; 512: 37.6 (64), 39.5; 768: 70.6 (64), 40.4
-//   K 4096, N 14336: 128: 17.0 (64), 20.8; 192: 28.3 (64), 20.9
-//   gated, K 4096, F 14336: 64: 28.7 (32), 28.1 (64), 31.7; 128: 45.0 (64), 32.2
-//   gated, K 768, F 2048:   64: 6.9 (32), 9.8 (64), 9.5; 512: 8.4 (32), 10.3;
-//                    1024: 16.0 (32), 11.9 (64), 11.0
-int e4m3_few_tile(int M, int N, int K, int mats, int sms) {
+// Rows of X per tile for M rows, or 0 where k_e4m3_many is the better one.
+//
+// Short K (up to 2048): a call is its fixed cost, which grows with the tile, so the
+// smallest tile whose tiles are all resident at once, two CTAs per SM; then 256 x 256
+// tiles, except for fp32 results.  Long K: the first tile whose tiles are resident twice
+// over, that is with K split in two or more; then 256 x 256 tiles, or up to 64 gated rows
+// one split less.  Measured, us, by rows per tile, and k_e4m3_many:
+//                                32     64    128   many
+//   K 768, N 2304:    512 rows   6.0    6.2    8.5    8.0      1024: 11.1   7.2   9.0   8.1
+//        1371: 15.9  12.3   9.6   9.0   (of fp32: 16.4  13.0  10.5  11.3)
+//   K 1536, N 2304:   512        7.2    7.9    9.0    8.9
+//   K 4096, N 4096:   256       12.6   10.8   12.1   14.7       512: 24.2  14.9  14.0  14.8
+//   K 4096, N 14336:  128       26.1   17.1   15.7   17.4       256: 38.9  29.6  30.3  17.9
+//   K 14336, N 4096:  256       31.9   22.8   21.2   35.8       512: 62.9  37.4  34.9  36.2
+//   gated, K 768, F 2048:    333   8.1  10.4    -    9.5       1024: 15.8  12.0    -  10.5
+//   gated, K 4096, F 2048:   256  13.4  14.7    -   16.0        333: 18.9  18.1    -  16.2
+//   gated, K 4096, F 14336:   64  28.6  25.3    -   30.7        128: 52.4  43.9    -  31.3
+int e4m3_few_tile(int M, int N, int K, int mats, bool f32, int sms) {
   const long long wtiles = ((long long)N + kBlk - 1) / kBlk, slots = 2LL * sms;
-  auto fits = [&](int nt) { return wtiles * (((long long)M + nt - 1) / nt) <= slots; };
-  const bool brief = K <= 8 * kBlk;
+  auto fits = [&](int nt, int times) { return wtiles * (((long long)M + nt - 1) / nt) * times <= slots; };
   if (M <= 16) return 16;
-  if (M <= 32 || (brief && fits(32))) return 32;
-  if (M <= 64 || (mats == 1 && fits(64))) return 64;
-  return mats == 1 && brief && fits(128) ? 128 : 0;
+  if (M <= 32) return 32;
+  if (K <= 2048) {
+    if (fits(32, 1)) return 32;
+    if (mats == 1 && fits(64, 1)) return 64;
+    if (mats == 1 && f32 && fits(128, 1)) return 128;
+  } else if (mats == 1) {
+    if (fits(64, 2)) return 64;
+    if (M > 64 && fits(128, 2)) return 128;
+  } else if (fits(32, 2)) {
+    return 32;
+  }
+  return M <= 64 ? 64 : 0;
 }
 
 cudaError_t launch_gemm_e4m3_few(const GemmArgs& a, int tile, cudaStream_t s) {
