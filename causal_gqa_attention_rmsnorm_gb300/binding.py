@@ -613,10 +613,11 @@ class AttnConfig:
 
 def _stream_on(stream, dev: int) -> int:
     """The raw stream of a call on tensors of CUDA device `dev`, which must be the current device."""
-    if dev != torch._C._cuda_getDevice():
+    C = torch._C
+    if dev != C._cuda_getDevice():
         raise ValueError(f"tensors are on cuda:{dev}, the current device is {torch.cuda.current_device()}")
     # (the raw handle of the current stream, without a stream object around it)
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    return C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> int:
@@ -758,7 +759,7 @@ def _blocks(n: int) -> int:
 class _Coded:
     """Codes [rows, cols] and their scales: two dense tensors, read once, here.  (A
     handle to keep: a tensor that is resized or given other memory needs a new one.)"""
-    __slots__ = ("codes", "scale", "dev", "_struct", "_ref")
+    __slots__ = ("codes", "scale", "dev", "rows", "cols", "_struct", "_ref")
 
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor):
         if codes.dim() != 2:
@@ -767,17 +768,9 @@ class _Coded:
         dev = codes.get_device()
         code_ptr = _dense(codes, "codes", _E4M3, (rows, cols), dev)
         scale_ptr = _dense(scale, "scale", _E8M0, self._scales(rows, cols), dev)
-        self.codes, self.scale, self.dev = codes, scale, dev
+        self.codes, self.scale, self.dev, self.rows, self.cols = codes, scale, dev, rows, cols
         self._struct = tb_e4m3(code_ptr, scale_ptr, rows, cols)
         self._ref = ctypes.byref(self._struct)
-
-    @property
-    def rows(self) -> int:
-        return self._struct.rows
-
-    @property
-    def cols(self) -> int:
-        return self._struct.cols
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda"):
@@ -833,28 +826,49 @@ def _out_rows(out: Optional[E4M3Rows], M: int, cols: int, dev: int, stream, name
     return out
 
 
+def _input_rows(x: torch.Tensor, out: Optional[E4M3Rows]):
+    """(dtype, shape, columns, device) of rows x [..., d] to be coded into `out`, if given."""
+    dtype, shape, dev = x.dtype, x.shape, x.get_device()
+    dt = _FLOATS.get(dtype)
+    if dt is None or not x.is_contiguous() or dev < 0:
+        _float_dtype(x, "x")
+        _dense(x, "x", dtype, shape, dev)
+    d = shape[-1] if shape else 0
+    if out is not None and (out.__class__ is not E4M3Rows or out.dev != dev or out.cols != d or out.rows * d != x.numel()):
+        _out_rows(out, x.numel() // d if d else 0, d, dev, None)
+    return dt, shape, d, dev
+
+
+# (The checks below look at each tensor once, in place: of a call of 5 us the tensors'
+# attributes are half.)
+
 def tb_rmsnorm_e4m3(x: torch.Tensor, g: torch.Tensor, eps: float, r: Optional[torch.Tensor] = None,
                     h: Optional[torch.Tensor] = None, out: Optional[E4M3Rows] = None, stream=None):
     """RMSNorm of the rows x [..., d] (or of x + r) times the gain g [d], as e4m3 rows.
     Returns (out, h): h [..., d] is the sum in x's type where r is given (x itself will
     do), else None."""
-    dt = _float_dtype(x, "x")
-    dev, shape = x.get_device(), x.shape
-    d = shape[-1] if shape else 0
-    x_ptr = _dense(x, "x", x.dtype, shape, dev)
-    g_ptr = _dense(g, "g", x.dtype, (d,), dev)
+    dt, shape, d, dev = _input_rows(x, out)
+    dtype = x.dtype
+    if g.dtype is not dtype or g.shape != (d,) or g.get_device() != dev or not g.is_contiguous():
+        _dense(g, "g", dtype, (d,), dev)
     r_ptr, h_ptr, r_dt = None, None, 0
     if r is not None:
-        r_dt = _float_dtype(r, "r")
-        r_ptr = _dense(r, "r", r.dtype, shape, dev)
+        r_dt = _FLOATS.get(r.dtype)
+        if r_dt is None or r.shape != shape or r.get_device() != dev or not r.is_contiguous():
+            _float_dtype(r, "r")
+            _dense(r, "r", r.dtype, shape, dev)
+        r_ptr = r.data_ptr()
         if h is None:
             with _alloc_on(stream):
-                h = torch.empty_like(x)
-        h_ptr = _dense(h, "h", x.dtype, shape, dev)
+                h = torch.empty(shape, dtype=dtype, device=x.device)
+        elif h.dtype is not dtype or h.shape != shape or h.get_device() != dev or not h.is_contiguous():
+            _dense(h, "h", dtype, shape, dev)
+        h_ptr = h.data_ptr()
     elif h is not None:
         raise ValueError("h without r")
-    out = _out_rows(out, x.numel() // d if d else 0, d, dev, stream)
-    status = lib().tb_rmsnorm_e4m3(x_ptr, dt, r_ptr, r_dt, h_ptr, g_ptr, eps, out._ref, _stream_on(stream, dev))
+    if out is None:
+        out = _out_rows(None, x.numel() // d if d else 0, d, dev, stream)
+    status = lib().tb_rmsnorm_e4m3(x.data_ptr(), dt, r_ptr, r_dt, h_ptr, g.data_ptr(), eps, out._ref, _stream_on(stream, dev))
     if status:
         _check("tb_rmsnorm_e4m3", status)
     return out, h
@@ -862,12 +876,10 @@ def tb_rmsnorm_e4m3(x: torch.Tensor, g: torch.Tensor, eps: float, r: Optional[to
 
 def tb_quant_e4m3(x: torch.Tensor, out: Optional[E4M3Rows] = None, stream=None) -> E4M3Rows:
     """The rows x [..., d] as e4m3 rows."""
-    dt = _float_dtype(x, "x")
-    dev, shape = x.get_device(), x.shape
-    d = shape[-1] if shape else 0
-    x_ptr = _dense(x, "x", x.dtype, shape, dev)
-    out = _out_rows(out, x.numel() // d if d else 0, d, dev, stream)
-    status = lib().tb_quant_e4m3(x_ptr, dt, out._ref, _stream_on(stream, dev))
+    dt, _, d, dev = _input_rows(x, out)
+    if out is None:
+        out = _out_rows(None, x.numel() // d if d else 0, d, dev, stream)
+    status = lib().tb_quant_e4m3(x.data_ptr(), dt, out._ref, _stream_on(stream, dev))
     if status:
         _check("tb_quant_e4m3", status)
     return out
@@ -903,12 +915,15 @@ def tb_gemm_e4m3(x: E4M3Rows, w: E4M3Weight, res: Optional[torch.Tensor] = None,
         dtype = _F32 if y_dtype == TB_F32 else res.dtype if y_dtype is None and res is not None else _BF16
         with _alloc_on(stream):
             y = torch.empty(shape, dtype=dtype, device=x.codes.device)
-    dt = _float_dtype(y, "y")
+    dtype = y.dtype
+    dt = _FLOATS.get(dtype)
+    if dt is None or y.shape != shape or y.get_device() != dev or not y.is_contiguous():
+        _float_dtype(y, "y")
+        _dense(y, "y", dtype, shape, dev)
     if y_dtype is not None and y_dtype != dt:
         raise ValueError("y has another type than y_dtype")
-    y_ptr = _dense(y, "y", y.dtype, shape, dev)
-    res_ptr = None if res is None else _dense(res, "res", y.dtype, shape, dev)
-    status = lib().tb_gemm_e4m3(x_ref, w_ref, res_ptr, y_ptr, dt, _stream_on(stream, dev))
+    res_ptr = None if res is None else _dense(res, "res", dtype, shape, dev)
+    status = lib().tb_gemm_e4m3(x_ref, w_ref, res_ptr, y.data_ptr(), dt, _stream_on(stream, dev))
     if status:
         _check("tb_gemm_e4m3", status)
     return y
