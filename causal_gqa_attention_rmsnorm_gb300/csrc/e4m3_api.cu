@@ -196,6 +196,7 @@ tb_status tb_gemm_e4m3(const tb_e4m3* x, const tb_e4m3* w, const void* res, void
   a.res = res;
   a.y = y;
   a.y_dtype = y_dtype;
+  if (!device_error_word()) return report(TB_ERR_CUDA, "cannot resolve the device error word");
   const int tile = tile_of(a, 1);
   return done(tile ? launch_gemm_e4m3_few(a, tile, (cudaStream_t)stream) : launch_gemm_e4m3_many(a, (cudaStream_t)stream),
               "tb_gemm_e4m3");
@@ -229,6 +230,7 @@ tb_status tb_gated_e4m3(const tb_e4m3* x, const tb_e4m3* w1, const tb_e4m3* w3, 
   a.y = y;
   a.y_dtype = y_dtype;
   a.y_scale = static_cast<uint8_t*>(y_scale);
+  if (!device_error_word()) return report(TB_ERR_CUDA, "cannot resolve the device error word");
   const int tile = tile_of(a, 2);
   return done(tile ? launch_gated_e4m3_few(a, tile, (cudaStream_t)stream) : launch_gated_e4m3_many(a, (cudaStream_t)stream),
               "tb_gated_e4m3");

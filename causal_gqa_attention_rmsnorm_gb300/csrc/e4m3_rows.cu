@@ -52,9 +52,10 @@ __device__ __forceinline__ void store8(bf16* p, const float (&v)[8]) {
 // The codes of a thread's eight values v·s·g of a block that 16 lanes hold (g: or all
 // ones); the first of the 16 also stores the scale.  t = v·g comes first, so that the
 // row's s and the block's 2^-e are one factor: s·2^-e is exact, and the largest |t|·s is
-// the largest |t·s| (rounding keeps the order).  An infinite t, which v·g may be where
-// v·s·g is not, has the block done again in the other order and with infinities told
-// from values; a NaN is passed over by the maximum and kept by the conversion.
+// the largest |t·s| (rounding keeps the order).  A block whose largest |t|·s is no finite
+// number (an infinity in it, v·g beyond fp32 where v·s·g is not, a row without a finite
+// s) is done again in the other order and with infinities told from values; a NaN is
+// passed over by the maximum and kept by the conversion.
 template <typename T, bool NORM>
 __device__ __forceinline__ void put_block(const float (&v)[8], float s, const Eight<T>& g, bool in, uint8_t* codes,
                                           uint8_t* scale) {
@@ -66,7 +67,7 @@ __device__ __forceinline__ void put_block(const float (&v)[8], float s, const Ei
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float f = s;
-  if (__any_sync(0xffffffffu, top == INFINITY)) {
+  if (__any_sync(0xffffffffu, !(top * s < INFINITY))) {
     top = 0.f;
     f = 1.f;
 #pragma unroll

@@ -437,7 +437,8 @@ typedef struct {
  *  x     : device, dense [out->rows, out->cols] of dtype (TB_F32 or TB_BF16).
  *  r, h  : NULL, or both given: r dense [rows, cols] of r_dtype, h receives the sum in
  *          dtype.  h may be x itself, or r itself where the types agree.  The norm takes
- *          the fp32 sum, before h's rounding.
+ *          the fp32 sum, before h's rounding; its mean square is fp32 too (a row above
+ *          1e19 / sqrt(cols) may have an infinite one, which gives zeros).
  *  g     : device [cols] of dtype.
  *  out   : rows; at most 32768 columns (TB_ERR_UNSUPPORTED above).
  * Pointers 16-byte aligned; but for h, what is written overlaps nothing that is read. */

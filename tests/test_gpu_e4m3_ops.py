@@ -1,5 +1,9 @@
 """The 8-bit projections against fp64, element by element (e4m3_helpers derives the
 tolerances)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -11,6 +15,7 @@ from e4m3_helpers import (BF16, CODE, F32, HALF, SCALE, bytes_of, check_product,
 from oracle import e4m3 as ref
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def gen(seed):
@@ -115,6 +120,26 @@ def test_rows_with_infinities_and_nan():
     no_error()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_without_a_finite_result(dtype):
+    """Rows of zeros without eps, results beyond fp32, an infinite gain: NaN codes where the
+    value is none, the scale of what is finite, and nothing of it in the rows beside."""
+    x = torch.randn(5, 272, generator=gen(3))
+    x[1] = 0
+    gain = torch.ones(272)
+    gain[7], gain[130] = 3e38, float("inf")
+    x[2, 7], x[3, 130] = 200.0, 0.0
+    x, gain = x.to(dtype), gain.to(dtype)
+    out, _ = tb.tb_rmsnorm_e4m3(x.cuda(), gain.cuda(), 0.0)
+    no_error()
+    with np.errstate(all="ignore"):
+        y = ref.norm(f64(x), f64(gain), 0.0)
+    y = np.where(np.abs(y) <= 3.4028234e38, y, np.nan)                # fp32's range
+    assert np.isnan(y[1]).all() and np.isnan(y[3, 130]) and np.isnan(y[2, 7]) and np.isfinite(np.delete(y[0], [7, 130])).all()
+    check_rows(bytes_of(out.codes), bytes_of(out.scale), y, NORM_OFF * np.abs(y))
+    assert (bytes_of(out.scale)[1] == 27).all()
+
+
 @pytest.mark.parametrize("M,d", [(2, 400), (400, 768)])
 def test_norm_in_place_gives_the_same(M, d):
     g = gen(5)
@@ -207,6 +232,33 @@ def test_gemm_nan_stays_in_its_row_and_its_column():
     assert torch.equal(y[~hit], clean[~hit])
 
 
+@pytest.mark.parametrize("tile", [16, 64, 128, -1])
+def test_gemm_far_scales(form, tile):
+    """Scales whose product leaves fp32: infinity above, 0 (or a subnormal) below, and
+    zeros stay zeros under any scale."""
+    form(tile)
+    M, N, K = 20, 16, 256
+    x = torch.zeros(M, K, dtype=torch.uint8)
+    x[:, 5], x[:, 200] = 0x38, 0x38                    # 1 in each block
+    x[1, 5] = x[2, 200] = 0
+    xs = torch.full((M, 2), 127, dtype=torch.uint8)
+    xs[0], xs[1], xs[2] = 247, torch.tensor([254, 127]), torch.tensor([127, 0])
+    xs[3], xs[4] = torch.tensor([27, 127]), torch.tensor([0, 0])
+    w = torch.zeros(N, K, dtype=torch.uint8)
+    w[:, 5], w[:, 200] = 0x38, 0xB8                    # 1 and -1
+    w[1, 5], w[1, 200] = 0, 0
+    ws = torch.tensor([[247, 127]], dtype=torch.uint8)
+    y = tb.tb_gemm_e4m3(tb.E4M3Rows(x.view(CODE).cuda(), xs.view(SCALE).cuda()),
+                        tb.E4M3Weight(w.view(CODE).cuda(), ws.view(SCALE).cuda()), y_dtype=tb.TB_F32)
+    no_error()
+    got = f64(y)
+    assert (got[:, 1] == 0).all()                      # a row of zero weights
+    cols = [0] + list(range(2, N))
+    want = {0: np.inf, 1: -1.0, 2: 2.0 ** 120, 3: 2.0 ** 20 - 1, 4: 2.0 ** -7, 5: 2.0 ** 120}
+    for m, v in want.items():
+        assert (got[m, cols] == v).all(), (m, v, got[m, :3])
+
+
 @pytest.mark.parametrize("M", [1, 16, 40, 100, 130])
 def test_gemm_writes_its_rows_only(M):
     g = gen(M)
@@ -239,6 +291,28 @@ def test_gated(M, F, K, out_dtype):
         no_error()
         assert y.dtype is out_dtype
         assert (np.abs(f64(y) - exact) <= off + 2 * HALF[out_dtype] * (np.abs(exact) + off)).all()
+
+
+@pytest.mark.parametrize("tile,M", [(16, 3), (32, 30), (64, 70), (-1, 200)])
+def test_gated_infinities_and_nan_become_nan_codes(form, tile, M):
+    """Results beyond fp32 and NaN are NaN codes, and the scale is that of the others."""
+    form(tile)
+    g = gen(M)
+    F, K = 272, 144
+    x, w1, w3 = make_rows(tb, M, K, g), make_weight(tb, F, K, g), make_weight(tb, F, K, g)
+    x.codes.view(torch.uint8)[1] = 0x7E                # 448 throughout: gates and values of thousands
+    x.scale.view(torch.uint8)[1] = 200
+    x.codes.view(torch.uint8)[0, 100] = 0x7F
+    w3.codes.view(torch.uint8)[130] = 0xFF
+    out = tb.tb_gated_e4m3(x, w1, w3)
+    no_error()
+    exact, off = gated_and_off(rows_np(x), weight_np(w1), weight_np(w3), K)
+    sure = np.isfinite(exact) & (np.abs(exact) + off < 3.4e38)
+    gone = ~np.isfinite(exact) | (np.abs(exact) - off > 3.41e38)
+    assert gone[0].all() and gone[1].any() and gone[2:, 130].all() and (sure | gone)[[0] + list(range(2, M))].all()
+    v = ref.VALUES[bytes_of(out.codes)]
+    assert np.isnan(v[gone]).all() and np.isfinite(v[2:][sure[2:]]).all()
+    check_rows(bytes_of(out.codes)[2:], bytes_of(out.scale)[2:], np.where(sure, exact, np.nan)[2:], np.where(sure, off, 0)[2:])
 
 
 def test_gated_gates_far_below_zero():
@@ -397,6 +471,50 @@ def test_both_kernels_agree_on_what_nan_reaches(form):
     assert all(torch.equal(t, hit) for t in got)
 
 
+# ---- offsets beyond 32 bits -----------------------------------------------------------
+
+def test_rows_beyond_2_31_values():
+    M, d = 540_000, 4096                               # 2.2e9 values
+    x = torch.ones(M, d, dtype=BF16, device="cuda")
+    x[-3:] = torch.randn(3, d, generator=gen(1)).to(BF16)
+    r = torch.zeros(M, d, dtype=BF16, device="cuda")
+    r[-2] = 0.5
+    out = tb.tb_quant_e4m3(x)
+    no_error()
+    check_rows(bytes_of(out.codes[-4:]), bytes_of(out.scale[-4:]), f64(x[-4:]), np.zeros((4, d)))
+    tb.tb_rmsnorm_e4m3(x, torch.ones(d, dtype=BF16, device="cuda"), 1e-5, r=r, h=r, out=out)
+    no_error()
+    total = f64(x[-4:])
+    total[2] += 0.5
+    y = ref.norm(total, np.ones(d), 1e-5)
+    check_rows(bytes_of(out.codes[-4:]), bytes_of(out.scale[-4:]), y, NORM_OFF * np.abs(y))
+    assert (np.abs(f64(r[-4:]) - total) <= 2 * HALF[BF16] * np.abs(total) + 2.0 ** -23 * np.abs(total)).all()
+
+
+@pytest.mark.parametrize("tile", [64, -1])
+def test_products_beyond_2_31_values(form, tile):
+    form(tile)
+    g = gen(4)
+    M, N, K = 140_000, 16_000, 144                     # 2.24e9 results
+    few = make_rows(tb, 1000, K, g)
+    x = tb.E4M3Rows(few.codes.view(torch.uint8).repeat(140, 1).view(CODE), few.scale.view(torch.uint8).repeat(140, 1).view(SCALE))
+    w = make_weight(tb, N, K, g)
+    y = tb.tb_gemm_e4m3(x, w)
+    no_error()
+    want = y[:1000]
+    check_product(want[:8], *product(rows_np(few)[:8], weight_np(w)), K, BF16)
+    for i in (1, 70, 138, 139):
+        assert torch.equal(y[1000 * i:1000 * (i + 1)], want)
+    del y
+    a = tb.tb_gated_e4m3(x, w, w)
+    no_error()
+    c, s = a.codes.view(torch.uint8), a.scale.view(torch.uint8)
+    for i in (1, 70, 138, 139):
+        assert torch.equal(c[1000 * i:1000 * (i + 1)], c[:1000]) and torch.equal(s[1000 * i:1000 * (i + 1)], s[:1000])
+    exact, off = gated_and_off(rows_np(few)[:4], weight_np(w), weight_np(w), K)
+    check_rows(bytes_of(a.codes[:4]), bytes_of(a.scale[:4]), exact, off)
+
+
 # ---- together -----------------------------------------------------------------------
 
 def test_repeated_calls_streams_and_graphs_give_the_same_bits():
@@ -431,6 +549,52 @@ def test_repeated_calls_streams_and_graphs_give_the_same_bits():
     torch.cuda.synchronize()
     assert torch.equal(y, first.flip(0))               # rows do not know each other
     no_error()
+
+
+@pytest.mark.parametrize("M", [3, 700])
+def test_two_streams_at_once(M):
+    """No call leaves anything behind that another one uses."""
+    g = gen(21)
+    K, N = 1040, 2064
+    w, w3 = make_weight(tb, N, K, g), make_weight(tb, N, K, g)
+    xs = [make_rows(tb, M, K, g) for _ in range(2)]
+    want = [(tb.tb_gemm_e4m3(x, w), tb.tb_gated_e4m3(x, w, w3, out_dtype=tb.TB_BF16)) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            got[i].append((tb.tb_gemm_e4m3(xs[i], w, stream=s), tb.tb_gated_e4m3(xs[i], w, w3, out_dtype=tb.TB_BF16, stream=s)))
+    torch.cuda.synchronize()
+    no_error()
+    for i in range(2):
+        for a, b in got[i]:
+            assert torch.equal(a, want[i][0]) and torch.equal(b, want[i][1])
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing of the launches' set-up is forbidden while a graph is captured."""
+    code = """
+import torch, causal_gqa_attention_rmsnorm_gb300 as tb
+x = torch.randn(300, 512, device="cuda").to(torch.bfloat16)
+g = torch.ones(512, dtype=torch.bfloat16, device="cuda")
+w = torch.randn(512, 4112, device="cuda") * .05
+def go():
+    n, _ = tb.tb_rmsnorm_e4m3(x, g, 1e-5)
+    p = tb.tb_pack_e4m3(w)
+    return tb.tb_gemm_e4m3(n, p), tb.tb_gated_e4m3(n, p, p, out_dtype=tb.TB_BF16), tb.tb_gemm_e4m3(tb.tb_quant_e4m3(x[:3]), p)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = go()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, go()))
+assert tb.tb_get_device_error() == 0
+print("fine")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.stdout.strip().endswith("fine"), r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("B,n", [(3, 1), (2, 37)])
