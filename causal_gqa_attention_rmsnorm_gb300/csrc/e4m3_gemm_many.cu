@@ -170,11 +170,13 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
       for (int tile = tile0; ok && tile < tiles; tile += tstep, ++local) {
         const int acc = local & 1;
         if (!mbar_wait_warp(&tempty[acc], ((local >> 1) & 1) ^ 1u, abort_flag, err)) break;
+        // (the scales first: the tile before holds the shared columns up a little longer)
+        if (!mbar_wait_warp(&sfull[set & 1], (set >> 1) & 1, abort_flag, err)) break;
         if (local && !mbar_wait_warp(shared_free, (local - 1) & 1, abort_flag, err)) break;
         const uint32_t d = tmem + acc * C::ACC1;
         for (int kb = 0; ok && kb < kblocks; kb += kSet, ++set) {
           const uint32_t sb = set & 1, sf = tmem + C::SETS_AT + sb * C::SET_COLS;
-          if (!(ok = mbar_wait_warp(&sfull[sb], (set >> 1) & 1, abort_flag, err))) break;
+          if (kb && !(ok = mbar_wait_warp(&sfull[sb], (set >> 1) & 1, abort_flag, err))) break;
 #pragma unroll
           for (int b = 0; b < kSet; ++b) {
             if (kb + b < kblocks) {
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
       if (!(ok = mbar_wait_warp(&tfull[acc], (local >> 1) & 1, abort_flag, err))) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + acc * C::ACC1;
-      // 32 columns of this lane's row, finished but for the residual; `last`: the piece's
+      // 32 columns of this lane's row, finished but for the residual
       auto take = [&](int c, bool free_shared, bool free_all, float (&v)[32]) {
         uint32_t r[32], u[32];
         tmem_ld32(taddr + c, r);
@@ -292,13 +294,17 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
         for (int j = 0; j < 32; ++j)
           v[j] = GATED ? gated(__uint_as_float(r[j]), __uint_as_float(u[j])) : __uint_as_float(r[j]);
       };
+      // the 32 columns (of gated ones the pairs) that reach into the shared ones, at once
+      const int c_first = acc ? 0 : COLS - 32;
+      float v0[32];
+      take(c_first, true, false, v0);
 #pragma unroll 1
       for (int i = 0; i < pieces; ++i, ++n) {
         const uint32_t b = n & 1;
         int row, col;
         const bool in = where(tile, acc, i, row, col);
         const int c0 = piece_of(i, acc) * wide;
-        const bool first = i == 0, last = i + 1 == pieces;
+        const bool last = i + 1 == pieces;
         uint8_t* mine = buf + b * C::PIECE + lane * 128;
         if (res) {
           // the next piece's residual, once the store before this one has left its buffer
@@ -325,7 +331,12 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
           for (int q = 0; q < 4; ++q) {
             const int cq = acc ? q : (q + 3) & 3;      // shared columns first, as the pieces go
             float v[32];
-            take(cq * 32, q == 0, false, v);
+            if (q == 0) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = v0[j];
+            } else {
+              take(cq * 32, false, false, v);
+            }
 #pragma unroll
             for (int j = 0; j < 32; j += 2) top = fmax3(top, fabsf(v[j]), fabsf(v[j + 1]));
             tmem_st32(keep + cq * 32, *reinterpret_cast<const uint32_t(*)[32]>(v));
@@ -371,7 +382,12 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
           if (row + lane < a.M) a.y_scale[(size_t)(row + lane) * n_tiles + col / 128] = (uint8_t)(e + 127);
         } else if constexpr (ESIZE == 4) {
           float v[32];
-          take(c0, first, last, v);
+          if (i == 0) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = v0[j];
+          } else {
+            take(c0, false, last, v);
+          }
 #pragma unroll
           for (int p = 0; p < 8; ++p) {
             float4 t = make_float4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
@@ -389,7 +405,12 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
             // accumulator 1's the lower: that half first)
             const int hh = acc ? h : h ^ 1;
             float v[32];
-            take(c0 + 32 * hh, first && h == 0, last && h == 1, v);
+            if (i == 0 && h == 0) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = v0[j];
+            } else {
+              take(c0 + 32 * hh, false, last && h == 1, v);
+            }
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
               uint4* at = part(4 * hh + p);
