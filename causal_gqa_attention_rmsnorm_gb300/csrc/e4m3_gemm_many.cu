@@ -254,24 +254,23 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
     // piece i of a tile in accumulator `acc`, the one with the shared columns first: the
     // last of accumulator 0, the first of accumulator 1
     auto piece_of = [&](int i, int acc) { return acc ? i : (i == 0 ? pieces - 1 : i - 1); };
-    auto where = [&](int tile, int acc, int i, int& row, int& col) {
+    // first row and column of the warp's part of a tile
+    auto corner = [&](int tile) {
       int mu, nt;
       place(tile, m_units, n_tiles, group, mu, nt);
-      row = (mu * 2 + (int)rank) * kRowsCta + quad * 32;
-      col = nt * COLS + piece_of(i, acc) * wide;
-      return row < a.M && col < a.N;
+      return make_int2((mu * 2 + (int)rank) * kRowsCta + quad * 32, nt * COLS);
     };
     uint32_t n = 0, rphase = 0;        // pieces so far; bit b: the parity of buffer b's next residual
-    auto request = [&](int tile, int acc, int i, uint32_t b) {
-      int row, col;
-      if (tile >= tiles || !where(tile, acc, i, row, col) || lane != 0) return;
+    auto request = [&](int row, int col, uint32_t b) {
+      if (row >= a.M || col >= a.N || lane != 0) return;
       mbar_arrive_expect_tx(&rfull[w * 2 + b], C::PIECE);
       tma_load_3d(&tmRes, buf + b * C::PIECE, &rfull[w * 2 + b], col * ESIZE, row, 0);
     };
-    if (res) request(tile0, 0, 0, 0);
+    int2 at = corner(tile0), next = at;
+    if (res) request(at.x, at.y + piece_of(0, 0) * wide, 0);
     bool ok = true;
     int local = 0;
-    for (int tile = tile0; ok && tile < tiles; tile += tstep, ++local) {
+    for (int tile = tile0; ok && tile < tiles; tile += tstep, ++local, at = next) {
       const int acc = local & 1;
       if (!(ok = mbar_wait_warp(&tfull[acc], (local >> 1) & 1, abort_flag, err))) break;
       tc_fence_after();
@@ -298,20 +297,21 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
       const int c_first = acc ? 0 : COLS - 32;
       float v0[32];
       take(c_first, true, false, v0);
+      const int row = at.x;
+      next = tile + tstep < tiles ? corner(tile + tstep) : make_int2(a.M, 0);
 #pragma unroll 1
       for (int i = 0; i < pieces; ++i, ++n) {
         const uint32_t b = n & 1;
-        int row, col;
-        const bool in = where(tile, acc, i, row, col);
-        const int c0 = piece_of(i, acc) * wide;
+        const int c0 = piece_of(i, acc) * wide, col = at.y + c0;
+        const bool in = row < a.M && col < a.N;
         const bool last = i + 1 == pieces;
         uint8_t* mine = buf + b * C::PIECE + lane * 128;
         if (res) {
           // the next piece's residual, once the store before this one has left its buffer
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
-          if (last) request(tile + tstep, acc ^ 1, 0, b ^ 1);
-          else request(tile, acc, i + 1, b ^ 1);
+          if (last) request(next.x, next.y + piece_of(0, acc ^ 1) * wide, b ^ 1);
+          else request(row, at.y + piece_of(i + 1, acc) * wide, b ^ 1);
           if (in) {
             if (!(ok = mbar_wait_warp(&rfull[w * 2 + b], rphase >> b & 1, abort_flag, err))) break;
             rphase ^= 1u << b;
@@ -399,35 +399,57 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
             *at = t;
           }
         } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // (of accumulator 0's first piece the upper half holds the shared columns, of
-            // accumulator 1's the lower: that half first)
-            const int hh = acc ? h : h ^ 1;
-            float v[32];
-            if (i == 0 && h == 0) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = v0[j];
-            } else {
-              take(c0 + 32 * hh, false, last && h == 1, v);
-            }
+          // (of accumulator 0's first piece the upper half is there already, of accumulator
+          // 1's the lower)
+          auto half = [&](int hh, const float (&v)[32]) {
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-              uint4* at = part(4 * hh + p);
-              uint4 r = make_uint4(0, 0, 0, 0), o;
-              if (res) r = *at;
-              const uint32_t* rr = &r.x;
+              uint4* to = part(4 * hh + p);
+              uint4 o;
               uint32_t* oo = &o.x;
+              if (res) {
+                const uint4 r = *to;
+                const uint32_t* rr = &r.x;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float lo = v[8 * p + 2 * k] + __uint_as_float(rr[k] << 16);
-                const float hi = v[8 * p + 2 * k + 1] + __uint_as_float(rr[k] & 0xffff0000u);
-                const __nv_bfloat162 t = res ? __floats2bfloat162_rn(lo, hi)
-                                             : __floats2bfloat162_rn(v[8 * p + 2 * k], v[8 * p + 2 * k + 1]);
-                oo[k] = *reinterpret_cast<const uint32_t*>(&t);
+                for (int k = 0; k < 4; ++k) {
+                  const __nv_bfloat162 t = __floats2bfloat162_rn(v[8 * p + 2 * k] + __uint_as_float(rr[k] << 16),
+                                                                 v[8 * p + 2 * k + 1] + __uint_as_float(rr[k] & 0xffff0000u));
+                  oo[k] = *reinterpret_cast<const uint32_t*>(&t);
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const __nv_bfloat162 t = __floats2bfloat162_rn(v[8 * p + 2 * k], v[8 * p + 2 * k + 1]);
+                  oo[k] = *reinterpret_cast<const uint32_t*>(&t);
+                }
               }
-              *at = o;
+              *to = o;
             }
+          };
+          if (i == 0) {
+            float v[32];
+            take(c0 + (acc ? 32 : 0), false, last, v);
+            half(acc ? 0 : 1, v0);
+            half(acc ? 1 : 0, v);
+          } else if constexpr (GATED) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float v[32];
+              take(c0 + 32 * h, false, last && h == 1, v);
+              half(h, v);
+            }
+          } else {
+            uint32_t r[2][32];
+            tmem_ld32(taddr + c0, r[0]);
+            tmem_ld32(taddr + c0 + 32, r[1]);
+            tmem_wait_ld();
+            if (last) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(tempty_cl[acc]);
+            }
+            half(0, reinterpret_cast<const float(&)[32]>(r[0]));
+            half(1, reinterpret_cast<const float(&)[32]>(r[1]));
           }
         }
         fence_proxy_async();
