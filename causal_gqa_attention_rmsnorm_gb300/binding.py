@@ -766,6 +766,10 @@ class _Coded:
             raise ValueError(f"codes must be [rows, cols], got {tuple(codes.shape)}")
         rows, cols = codes.shape
         dev = codes.get_device()
+        if dev < 0:
+            raise ValueError(f"codes must be a CUDA tensor, got one on {codes.device}")
+        if rows >= 1 << 31 or cols >= 1 << 31:       # (the C struct would take them modulo 2^32)
+            raise ValueError(f"at most 2^31 - 1 rows and columns, got {rows} and {cols}")
         code_ptr = _dense(codes, "codes", _E4M3, (rows, cols), dev)
         scale_ptr = _dense(scale, "scale", _E8M0, self._scales(rows, cols), dev)
         self.codes, self.scale, self.dev, self.rows, self.cols = codes, scale, dev, rows, cols

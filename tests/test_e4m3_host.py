@@ -182,6 +182,25 @@ def test_handles_take_dense_tensors_of_their_shapes(on_gpu):
             bad()
 
 
+def test_handles_refuse_cpu_tensors_and_counts_beyond_the_struct(monkeypatch):
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        rows(4, 256)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+
+    class Tall:
+        """Stands in for a tensor of 2^32 + 4 rows."""
+        shape = (2 ** 32 + 4, 16)
+
+        def dim(self):
+            return 2
+
+        def get_device(self):
+            return 0
+
+    with pytest.raises(ValueError, match="2\\^31 - 1"):
+        tb.E4M3Rows(Tall(), None)
+
+
 def test_binding_refusals(on_gpu):
     x, w = rows(4, 256), weight(32, 256)
     f = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype)
