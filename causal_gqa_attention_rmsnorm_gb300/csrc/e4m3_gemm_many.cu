@@ -69,7 +69,7 @@ template <bool GATED, int ESIZE>
 __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
     k_e4m3_many(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                 const __grid_constant__ CUtensorMap tmW3, const __grid_constant__ CUtensorMap tmY,
-                const __grid_constant__ CUtensorMap tmRes, GemmArgs a, int m_units, int n_tiles, int group, int* err) {
+                const __grid_constant__ CUtensorMap tmRes, GemmArgs a, int m_units, int n_tiles, int group, int stream, int* err) {
   using C = ManyCfg;
   constexpr int STAGES = C::STAGES;
   constexpr int COLS = GATED ? 128 : 256;               // columns of y per tile
@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
   if (warp == 0) {
     if (lane == 0) {
       pdl_wait();
+      const uint64_t first = policy_evict_first();
       int stage = 0;
       uint32_t phase = 0;
       int issued = 0;
@@ -150,7 +151,8 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
           // both CTAs' copies complete on the even CTA's barrier
           const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
-          tma_load_3d_pair(&tmX, sa, fb, kb * kBlk, xrow, 0);
+          if (stream) tma_load_3d_pair_hint(&tmX, sa, fb, kb * kBlk, xrow, 0, first);
+          else tma_load_3d_pair(&tmX, sa, fb, kb * kBlk, xrow, 0);
           tma_load_3d_pair(tw, sa + C::A_BYTES, fb, kb * kBlk, wrow, 0);
           if (issued < STAGES) ++issued;
           if (++stage == STAGES) stage = 0, phase ^= 1u;
@@ -275,7 +277,8 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
     auto request = [&](int row, int col, uint32_t b) {
       if (row >= a.M || col >= a.N || lane != 0) return;
       mbar_arrive_expect_tx(&rfull[w * 2 + b], C::PIECE);
-      tma_load_3d(&tmRes, buf + b * C::PIECE, &rfull[w * 2 + b], col * ESIZE, row, 0);
+      if (stream) tma_load_3d_hint(&tmRes, buf + b * C::PIECE, &rfull[w * 2 + b], col * ESIZE, row, 0, policy_evict_first());
+      else tma_load_3d(&tmRes, buf + b * C::PIECE, &rfull[w * 2 + b], col * ESIZE, row, 0);
     };
     int2 at = corner(tile0), next = at;
     if (res) request(at.x, at.y + piece_of(0, 0) * wide, 0);
@@ -465,7 +468,10 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
         }
         fence_proxy_async();
         __syncwarp();
-        if (in && lane == 0) tma_store_3d(&tmY, buf + b * C::PIECE, col * ESIZE, row, 0);
+        if (in && lane == 0) {
+          if (stream) tma_store_3d_hint(&tmY, buf + b * C::PIECE, col * ESIZE, row, 0, policy_evict_first());
+          else tma_store_3d(&tmY, buf + b * C::PIECE, col * ESIZE, row, 0);
+        }
         if (lane == 0) bulk_commit();
       }
     }
@@ -535,12 +541,19 @@ template <bool GATED, int ESIZE> cudaError_t go(const GemmArgs& a, cudaStream_t 
   const long long tiles = (long long)m_units * n_tiles;
   if (tiles > 0x7fffffffLL / 2) return cudaErrorInvalidValue;
   // Weights beyond what L2 keeps, short rows: groups of 32 row units, so that a weight
-  // tile is read once per group.
+  // tile is read once per group.  (Groups of 4, 8, 16 and 64 units for 16384 x 4096 x 14336,
+  // which has none, 566, 561, 566 and 641 us for 564; for gated 8192 x 14336 x 4096 566, 548,
+  // 540 and 534 for 533.)
   const size_t w_bytes = (size_t)a.N * a.K * (GATED ? 2 : 1);
   const int group = a.K <= 8192 && w_bytes > (size_t(48) << 20) && m_units > 1 ? std::min(m_units, 32) : 0;
+  // Column tiles fastest and all of a row unit resident at once, y too large to stay in L2
+  // for its reader: X, the residual and y pass through once and need not push the weights
+  // out (16384 x 4096 x 14336 with the residual 539 -> 533 us, after seconds of load 632 ->
+  // 619; X alone changes nothing.  In groups, where X is read again, 602 -> 711).
+  const int stream = group == 0 && n_tiles <= clusters[dev] && (size_t)a.M * a.N * ESIZE > (size_t(64) << 20);
   cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(tiles, clusters[dev]));
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_e4m3_many<GATED, ESIZE>, tx, tw, tw3, ty, tr, a, m_units, n_tiles, group, device_error_word());
+  return cudaLaunchKernelEx(&cfg, k_e4m3_many<GATED, ESIZE>, tx, tw, tw3, ty, tr, a, m_units, n_tiles, group, stream, device_error_word());
 }
 
 }  // namespace

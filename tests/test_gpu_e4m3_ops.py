@@ -430,6 +430,20 @@ def test_gemm_many(form, M, N, K, dtype, with_res):
         assert torch.equal(tb.tb_gemm_e4m3(x, w, res=res, y=res), y)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gemm_many_past_l2(form, dtype):
+    """Results too large to stay in L2 take their own cache hints."""
+    form(-1)
+    g = gen(6)
+    M, N, K = 9001, 4112, 144
+    x, w = make_rows(tb, M, K, g), make_weight(tb, N, K, g)
+    res = (torch.randn(M, N, generator=g) * 100).to(dtype).cuda()
+    y = tb.tb_gemm_e4m3(x, w, res=res)
+    no_error()
+    check_product(y, *product(rows_np(x), weight_np(w), f64(res)), K, dtype)
+    assert torch.equal(tb.tb_gemm_e4m3(x, w, res=res, y=res), y)
+
+
 @pytest.mark.parametrize("M,F,K", [(1, 16, 16), (129, 144, 400), (333, 2048, 768), (300, 272, 2064), (1000, 1040, 528),
                                    (2100, 1296, 272)])
 @pytest.mark.parametrize("out_dtype", ["codes", BF16, F32])
