@@ -28,14 +28,6 @@ __device__ __forceinline__ float4 get4(const void* y, int y_dtype, size_t at) {
                      __uint_as_float(w.y & 0xffff0000u));
 }
 
-__device__ __forceinline__ void put1(void* y, int y_dtype, size_t at, float v) {
-  if (y_dtype == TB_F32) static_cast<float*>(y)[at] = v;
-  else static_cast<bf16*>(y)[at] = __float2bfloat16_rn(v);
-}
-__device__ __forceinline__ float get1(const void* y, int y_dtype, size_t at) {
-  return y_dtype == TB_F32 ? static_cast<const float*>(y)[at] : __bfloat162float(static_cast<const bf16*>(y)[at]);
-}
-
 // Up to four exponent bytes of consecutive K blocks as one word, the first in the low
 // byte; `n` of them exist.  Missing ones read as 2^0.
 __device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int n) {

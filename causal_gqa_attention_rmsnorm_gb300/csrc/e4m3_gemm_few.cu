@@ -125,6 +125,22 @@ __device__ __forceinline__ void finish_rows(const GemmArgs& a, const float* part
   }
 }
 
+// P rows of a column of y (`live` of them exist), with the residual at `at` of res.
+template <typename T, int P>
+__device__ __forceinline__ void put_column(T* y, const T* res, size_t at, int N, int live, float (&v)[P]) {
+  if (res) {
+    const T* r = res + at;
+    float add[P];
+#pragma unroll
+    for (int k = 0; k < P; ++k) add[k] = k < live ? to_f(r[(size_t)k * N]) : 0.f;
+#pragma unroll
+    for (int k = 0; k < P; ++k) v[k] += add[k];
+  }
+#pragma unroll
+  for (int k = 0; k < P; ++k)
+    if (k < live) y[(size_t)k * N] = from_f<T>(v[k]);
+}
+
 template <int NT, int MATS, int CPS, bool ONE>
 __global__ void __launch_bounds__(192, CPS)
     k_e4m3_few(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW3,
@@ -187,41 +203,48 @@ __global__ void __launch_bounds__(192, CPS)
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol = policy_evict_first();
-      const bool once = a.M <= NT;              // the weights are read once: they need not stay in L2
-      bool dep = false;
-      auto release = [&]() {
-        pdl_wait();
-        dep = true;
-        const int held = nkb < STAGES ? nkb : STAGES;
-        for (int h = 0; h < held; ++h)
-          tma_load_3d(&tmX, smem + h * C::STAGE_BYTES + C::W_BYTES, &full[h], (kb0 + h) * kBlk, m0, 0);
-      };
-      int j = 0;
-      for (; j < nkb; ++j) {
-        const int st = j % STAGES;
-        if (!mbar_wait(&empty[st], ((j / STAGES) & 1) ^ 1u, abort_flag, err)) break;
-        uint8_t* sw = smem + st * C::STAGE_BYTES;
-        const int k = (kb0 + j) * kBlk;
-        mbar_arrive_expect_tx(&full[st], C::STAGE_BYTES);
-        if (once) {
-          tma_load_3d_hint(&tmW, sw, &full[st], k, wt * kBlk, 0, pol);
-          if constexpr (MATS == 2) tma_load_3d_hint(&tmW3, sw + kBlk * kBlk, &full[st], k, wt * kBlk, 0, pol);
-        } else {
-          tma_load_3d(&tmW, sw, &full[st], k, wt * kBlk, 0);
-          if constexpr (MATS == 2) tma_load_3d(&tmW3, sw + kBlk * kBlk, &full[st], k, wt * kBlk, 0);
-        }
-        if (dep) tma_load_3d(&tmX, sw + C::W_BYTES, &full[st], k, m0, 0);
-        else if (j + 1 == STAGES) release();
+    // (the whole warp, its elected lane issuing)
+    const uint32_t elected = elect_one();
+    const uint64_t pol = policy_evict_first();
+    const bool once = a.M <= NT;                // the weights are read once: they need not stay in L2
+    const uint32_t ring = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
+    const int wrow = wt * kBlk;
+    bool dep = false;
+    auto release = [&]() {
+      pdl_wait();
+      dep = true;
+      const int held = nkb < STAGES ? nkb : STAGES;
+#pragma unroll 1
+      for (int h = 0; h < held; ++h)
+        tma_load_3d_elected<1>(&tmX, ring + h * C::STAGE_BYTES + C::W_BYTES, full0 + h * 8, (kb0 + h) * kBlk, m0, 0, elected);
+    };
+    uint32_t st = 0, phase = 0;
+    int j = 0;
+#pragma unroll 1
+    for (; j < nkb; ++j) {
+      if (!__all_sync(0xffffffffu, mbar_try_wait(empty0 + st * 8, phase ^ 1u)) &&
+          !mbar_wait_warp(&empty[st], phase ^ 1u, abort_flag, err))
+        break;
+      const uint32_t sw = ring + st * C::STAGE_BYTES, bar = full0 + st * 8;
+      const int k = (kb0 + j) * kBlk;
+      mbar_expect_elected(bar, C::STAGE_BYTES, elected);
+      if (once) {
+        tma_load_3d_elected<1>(&tmW, sw, bar, k, wrow, 0, pol, elected);
+        if constexpr (MATS == 2) tma_load_3d_elected<1>(&tmW3, sw + kBlk * kBlk, bar, k, wrow, 0, pol, elected);
+      } else {
+        tma_load_3d_elected<1>(&tmW, sw, bar, k, wrow, 0, elected);
+        if constexpr (MATS == 2) tma_load_3d_elected<1>(&tmW3, sw + kBlk * kBlk, bar, k, wrow, 0, elected);
       }
-      if (!dep) release();
-      // every copy issued must land before the CTA may exit (earlier copies into the
-      // same stages were consumed, hence complete)
-      volatile int no_abort = 0;
-      for (int t = j - STAGES < 0 ? 0 : j - STAGES; t < j; ++t)
-        mbar_wait(&full[t % STAGES], (t / STAGES) & 1, &no_abort, err);
+      if (dep) tma_load_3d_elected<1>(&tmX, sw + C::W_BYTES, bar, k, m0, 0, elected);
+      else if (j + 1 == STAGES) release();
+      if (++st == STAGES) st = 0, phase ^= 1u;
     }
+    if (!dep) release();
+    // every copy issued must land before the CTA may exit (earlier copies into the same
+    // stages were consumed, hence complete)
+    volatile int no_abort = 0;
+    for (int t = j - STAGES < 0 ? 0 : j - STAGES; t < j; ++t)
+      mbar_wait_warp(&full[t % STAGES], (t / STAGES) & 1, &no_abort, err);
   } else if (warp == 1) {
     // The whole warp walks the blocks; its elected lane issues (mma_mx_k128).
     const uint32_t elected = elect_one();
@@ -303,7 +326,7 @@ __global__ void __launch_bounds__(192, CPS)
     // and stored if nothing has to be known of the row's other columns; else all goes to
     // shared memory.  (The last chunk's sums come after every instruction, and so after
     // every read of the ring.)
-    constexpr int P = NT < 32 ? NT : 32;
+    constexpr int P = 16;
     const int f = quad * 32 + lane, col = wt * kBlk + f;
     auto put = [&](int i, const float (&u)[MATS][P]) {
       if (splits > 1) {
@@ -323,16 +346,10 @@ __global__ void __launch_bounds__(192, CPS)
       }
       if (col >= a.N) return;
       const size_t at = (size_t)(m0 + i) * a.N + col;
-      if (MATS == 1 && a.res) {
-        float r[P];
-#pragma unroll
-        for (int k = 0; k < P; ++k) r[k] = i + k < rows ? get1(a.res, a.y_dtype, at + (size_t)k * a.N) : 0.f;
-#pragma unroll
-        for (int k = 0; k < P; ++k) v[k] += r[k];
-      }
-#pragma unroll
-      for (int k = 0; k < P; ++k)
-        if (i + k < rows) put1(a.y, a.y_dtype, at + (size_t)k * a.N, v[k]);
+      if (a.y_dtype == TB_F32)
+        put_column(static_cast<float*>(a.y) + at, static_cast<const float*>(MATS == 1 ? a.res : nullptr), at, a.N, rows - i, v);
+      else
+        put_column(static_cast<bf16*>(a.y) + at, static_cast<const bf16*>(MATS == 1 ? a.res : nullptr), at, a.N, rows - i, v);
     };
     if constexpr (ONE) {
       // all sets at once: one latency
@@ -345,8 +362,9 @@ __global__ void __launch_bounds__(192, CPS)
         if (i < nsets) place(i, v[i]);
       if (mbar_wait_warp(tfull, 0, abort_flag, err)) {
         tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < NT; i += P) {
+        // (a loop: code that runs once costs its way into the instruction cache)
+#pragma unroll 1
+        for (int i = 0; i < NT && i < rows; i += P) {
           float u[MATS][P];
 #pragma unroll
           for (int m = 0; m < MATS; ++m)
@@ -480,20 +498,20 @@ template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStrea
 // Rows of X per tile for M rows, or 0 where k_e4m3_many is the better one.
 //
 // Short K (up to 2048): a call is its fixed cost, which grows with the tile, so the
-// smallest tile whose tiles are all resident at once, two CTAs per SM; then 256 x 256
-// tiles, except for fp32 results.  Long K: the first tile whose tiles are resident twice
-// over, that is with K split in two or more; then 256 x 256 tiles, or up to 64 gated rows
-// one split less.  Measured, us, by rows per tile, and k_e4m3_many:
+// smallest tile whose tiles are all resident at once, two CTAs per SM; the largest only up
+// to 1024 or for fp32 results; then 256 x 256 tiles.  Long K: the first tile whose tiles
+// are resident twice over, that is with K split in two or more; then 256 x 256 tiles, or
+// up to 64 gated rows one split less.  Measured, us, by rows per tile, and k_e4m3_many:
 //                                32     64    128   many
-//   K 768, N 2304:    512 rows   6.0    6.2    8.5    8.0      1024: 11.1   7.2   9.0   8.1
-//        1371: 15.9  12.3   9.6   9.0   (of fp32: 16.4  13.0  10.5  11.3)
-//   K 1536, N 2304:   512        7.2    7.9    9.0    8.9
-//   K 4096, N 4096:   256       12.6   10.8   12.1   14.7       512: 24.2  14.9  14.0  14.8
-//   K 4096, N 14336:  128       26.1   17.1   15.7   17.4       256: 38.9  29.6  30.3  17.9
-//   K 14336, N 4096:  256       31.9   22.8   21.2   35.8       512: 62.9  37.4  34.9  36.2
-//   gated, K 768, F 2048:    333   8.1  10.4    -    9.5       1024: 15.8  12.0    -  10.5
-//   gated, K 4096, F 2048:   256  13.4  14.7    -   16.0        333: 18.9  18.1    -  16.2
-//   gated, K 4096, F 14336:   64  28.6  25.3    -   30.7        128: 52.4  43.9    -  31.3
+//   K 768, N 2304:    512 rows   5.5    5.6    7.3    7.7      1024:  9.9   6.4   8.0   8.0
+//        1371: 14.4  10.7   8.5   8.8   (of fp32: 14.7  11.5   9.3  11.2)
+//   K 1536, N 2304:   512        6.7    7.8    9.0    8.7      1371: 18.2  13.6  10.1   9.7
+//   K 4096, N 4096:   256       11.8   10.5   12.0   14.4       512: 22.4  14.3  13.7  14.6
+//   K 4096, N 14336:  128       24.3   17.0   15.7   17.1       256: 36.8  29.0  30.8  17.5
+//   K 14336, N 4096:  256       30.1   22.2   19.6   35.7       512: 59.2  36.3  32.1  36.1
+//   gated, K 768, F 2048:    333   7.9  10.5    -    9.6       1024: 15.4  12.0    -  10.5
+//   gated, K 4096, F 2048:   256  13.1  14.4    -   16.0        333: 18.4  17.9    -  16.1
+//   gated, K 4096, F 14336:   64  28.5  25.7    -   30.1        128: 51.6  43.6    -  30.6
 int e4m3_few_tile(int M, int N, int K, int mats, bool f32, int sms) {
   const long long wtiles = ((long long)N + kBlk - 1) / kBlk, slots = 2LL * sms;
   auto fits = [&](int nt, int times) { return wtiles * (((long long)M + nt - 1) / nt) * times <= slots; };
@@ -502,7 +520,7 @@ int e4m3_few_tile(int M, int N, int K, int mats, bool f32, int sms) {
   if (K <= 2048) {
     if (fits(32, 1)) return 32;
     if (mats == 1 && fits(64, 1)) return 64;
-    if (mats == 1 && f32 && fits(128, 1)) return 128;
+    if (mats == 1 && (f32 || K <= 1024) && fits(128, 1)) return 128;
   } else if (mats == 1) {
     if (fits(64, 2)) return 64;
     if (M > 64 && fits(128, 2)) return 128;

@@ -129,44 +129,43 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) {
-      pdl_wait();
-      const uint64_t first = policy_evict_first();
-      int stage = 0;
-      uint32_t phase = 0;
-      int issued = 0;
-      bool ok = true;
-      for (int tile = tile0; ok && tile < tiles; tile += tstep) {
-        int mu, nt;
-        place(tile, m_units, n_tiles, group, mu, nt);
-        const int xrow = (mu * 2 + (int)rank) * kRowsCta;       // a block past M reads zeros
-        const CUtensorMap* tw = GATED && rank ? &tmW3 : &tmW;
-        const int wrow = GATED ? nt * 128 : nt * 256 + (int)rank * 128;
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sa = smem + stage * C::STAGE_BYTES;
-          // both CTAs' copies complete on the even CTA's barrier
-          const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
-          if (stream) tma_load_3d_pair_hint(&tmX, sa, fb, kb * kBlk, xrow, 0, first);
-          else tma_load_3d_pair(&tmX, sa, fb, kb * kBlk, xrow, 0);
-          tma_load_3d_pair(tw, sa + C::A_BYTES, fb, kb * kBlk, wrow, 0);
-          if (issued < STAGES) ++issued;
-          if (++stage == STAGES) stage = 0, phase ^= 1u;
-        }
+    // (the whole warp, its elected lane issuing)
+    pdl_wait();
+    const uint32_t elected = elect_one();
+    const uint64_t first = policy_evict_first();
+    const uint32_t ring = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
+    const uint32_t even0 = mapa_shared(full0, 0);      // a pair's bytes complete on its even CTA's barriers
+    const CUtensorMap* tw = GATED && rank ? &tmW3 : &tmW;
+    uint32_t stage = 0, phase = 0;
+    int issued = 0;
+    bool ok = true;
+    for (int tile = tile0; ok && tile < tiles; tile += tstep) {
+      int mu, nt;
+      place(tile, m_units, n_tiles, group, mu, nt);
+      const int xrow = (mu * 2 + (int)rank) * kRowsCta;       // a block past M reads zeros
+      const int wrow = GATED ? nt * 128 : nt * 256 + (int)rank * 128;
+#pragma unroll 1
+      for (int kb = 0; kb < kblocks; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_try_wait(empty0 + stage * 8, phase ^ 1u)) &&
+            !(ok = mbar_wait_warp(&empty[stage], phase ^ 1u, abort_flag, err)))
+          break;
+        const uint32_t sa = ring + stage * C::STAGE_BYTES, bar = even0 + stage * 8;
+        if (rank == 0) mbar_expect_elected(full0 + stage * 8, 2 * C::STAGE_BYTES, elected);
+        if (stream) tma_load_3d_elected<2>(&tmX, sa, bar, kb * kBlk, xrow, 0, first, elected);
+        else tma_load_3d_elected<2>(&tmX, sa, bar, kb * kBlk, xrow, 0, elected);
+        tma_load_3d_elected<2>(tw, sa + C::A_BYTES, bar, kb * kBlk, wrow, 0, elected);
+        if (issued < STAGES) ++issued;
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
       }
-      // every copy must have landed before the CTA may exit (the odd CTA waits for the
-      // even one at the cluster barrier)
-      if (rank == 0) {
-        volatile int no_abort = 0;
-        for (int i = 0; i < issued; ++i) {
-          if (stage == 0) stage = STAGES, phase ^= 1u;
-          --stage;
-          mbar_wait(&full[stage], phase, &no_abort, err);
-        }
+    }
+    // every copy must have landed before the CTA may exit (the odd CTA waits for the even
+    // one at the cluster barrier)
+    if (rank == 0) {
+      volatile int no_abort = 0;
+      for (int i = 0; i < issued; ++i) {
+        if (stage == 0) stage = STAGES, phase ^= 1u;
+        --stage;
+        mbar_wait_warp(&full[stage], phase, &no_abort, err);
       }
     }
   } else if (warp == 1) {

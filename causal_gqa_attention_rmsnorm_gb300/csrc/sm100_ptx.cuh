@@ -552,15 +552,6 @@ __device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap* m, void* dst
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// The same with an L2 cache policy.
-__device__ __forceinline__ void tma_load_3d_pair_hint(const CUtensorMap* m, void* dst, uint32_t bar_cluster, int x, int y,
-                                                      int z, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z), "l"(policy)
-      : "memory");
-}
 // 2-D variant of tma_load_3d_pair.
 __device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* m, void* dst, uint32_t bar_cluster, int x, int y) {
   asm volatile(
@@ -703,6 +694,56 @@ __device__ __forceinline__ void mma_commit_pair_elected(uint32_t bar, uint32_t e
           bar),
       "h"((uint16_t)3), "r"(elected)
       : "memory");
+}
+
+// What a producer warp does, by its elected lane, for the reason given at mma_mx_k128 (a
+// stage's loads, issued in a branch on the lane, took 250 ns, so 170): an arrival that expects
+// bytes, and 3-D tiled TMA loads with or without an L2 policy, to addresses of this CTA's
+// shared memory, of one CTA or (CG 2) with the bytes counted on a barrier of the pair.
+__device__ __forceinline__ void mbar_expect_elected(uint32_t bar, uint32_t bytes, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred pe;\n\tsetp.ne.b32 pe, %2, 0;\n\t"
+      "@pe mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(elected)
+      : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tma_load_3d_elected(const CUtensorMap* m, uint32_t dst, uint32_t bar, int x, int y, int z,
+                                                    uint32_t elected) {
+  if constexpr (CG == 2) {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\tsetp.ne.b32 pe, %6, 0;\n\t"
+        "@pe cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(elected)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\tsetp.ne.b32 pe, %6, 0;\n\t"
+        "@pe cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(elected)
+        : "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tma_load_3d_elected(const CUtensorMap* m, uint32_t dst, uint32_t bar, int x, int y, int z,
+                                                    uint64_t policy, uint32_t elected) {
+  if constexpr (CG == 2) {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\tsetp.ne.b32 pe, %7, 0;\n\t"
+        "@pe cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy), "r"(elected)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\tsetp.ne.b32 pe, %7, 0;\n\t"
+        "@pe cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy), "r"(elected)
+        : "memory");
+  }
 }
 
 }  // namespace ptx

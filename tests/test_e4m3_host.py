@@ -133,7 +133,7 @@ def test_empty_calls_need_no_pointers(lib):
 
 @pytest.mark.parametrize("M,N,K,mats,f32,tile", [
     (1, 6144, 4096, 1, 0, 16), (16, 6144, 4096, 1, 0, 16), (17, 6144, 4096, 1, 0, 32), (33, 6144, 4096, 1, 0, 64),
-    (512, 2304, 768, 1, 0, 32), (513, 2304, 768, 1, 0, 64), (1371, 2304, 768, 1, 0, 0), (1371, 2304, 768, 1, 1, 128),
+    (512, 2304, 768, 1, 0, 32), (513, 2304, 768, 1, 0, 64), (1371, 2304, 768, 1, 0, 128), (1371, 2304, 1536, 1, 1, 128), (1371, 2304, 1536, 1, 0, 0),
     (2049, 2304, 768, 1, 1, 0), (256, 4096, 4096, 1, 0, 64), (257, 4096, 4096, 1, 0, 128), (512, 4096, 4096, 1, 0, 128),
     (513, 4096, 4096, 1, 0, 0), (64, 14336, 4096, 1, 0, 64), (128, 14336, 4096, 1, 0, 128), (129, 14336, 4096, 1, 0, 0),
     (32, 14336, 4096, 2, 0, 32), (64, 14336, 4096, 2, 0, 64), (65, 14336, 4096, 2, 0, 0), (333, 2048, 768, 2, 0, 32),
