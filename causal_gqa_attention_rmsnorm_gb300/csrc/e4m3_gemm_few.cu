@@ -16,18 +16,23 @@
 //   warp 1      issues the instructions, K blocks in order, and hands a chunk of K back
 //               after every kChunk scale sets;
 //   warps 2..5  put the scales into tensor memory, four K blocks at a time, ahead of
-//               the instructions; then take the sums: without a split straight to y,
-//               else to shared memory, where after a cluster barrier each CTA adds its
-//               share of the rows up over the cluster, in rank order, and finishes them.
+//               the instructions; then take the sums: without a split straight to y;
+//               with few rows of one matrix into the CTA of the cluster that finishes
+//               the row, by asynchronous stores that count on its barrier, so that no
+//               CTA waits for another's end; else to shared memory, where after a
+//               cluster barrier each CTA adds its share of the rows up over the
+//               cluster.  Always in rank order.
 // Chunks: the tensor core's accumulation cuts sums off instead of rounding them, which
 // shifts a sum of n instructions by up to n/2 steps of fp32.  A chunk is 64
 // instructions (2048 of K); the chunks are added with rounding, in registers.  (A part of
 // K of one chunk, the usual case, keeps no sums there.)
 //
 // Measured in a stream of calls: 1 x 128256 x 4096 79 us, 6.6 TB/s, as fast as memory is
-// copied; 32 x 14336 x 4096 gated 21.2 us (5.6 TB/s), 32 x 4096 x 14336 13.4 (4.5), 1 x
-// 6144 x 4096 7.1 (3.5): a call takes 4 us whatever it reads, of which 0.6 are the scales'
-// first load, 1 the first row tile's, 0.6 the cluster's barrier and 1 the partial sums.
+// copied; 32 x 14336 x 4096 gated 21.5 us (5.5 TB/s), 32 x 4096 x 14336 13.3 (4.5), 1 x
+// 6144 x 4096 6.1 (4.1): a call takes 3 to 4 us whatever it reads, of which 1 is the first
+// row tile's and the scales' load, 0.2 each K block's instructions, 0.5 the partial sums'
+// way.  (Partial sums read by the finishing CTA between two cluster barriers: 1 x 6144 x
+// 4096 7.1, 32 x 4096 x 14336 13.4; pushed row by row, 4 bytes at a time: 6.1 and 13.9.)
 // Tried: rings of 73 and 55 KB, which let three and four CTAs share an SM (13.7 and 15.3
 // us for 13.5), one CTA per SM with a ring of 216 KB (13.6; 1 x 6144 x 4096 8.0), clusters
 // of 3, 5 and 6 (7.8, 7.3 and 11.4 for 7.2: clusters of 6 do not all find a place at once).
@@ -49,10 +54,16 @@ constexpr int kSets = 8;         // scale sets held in tensor memory: two chunks
 template <int NT, int MATS, int CPS, bool ONE> struct FewCfg {
   static constexpr uint32_t W_BYTES = MATS * kBlk * kBlk;
   static constexpr uint32_t STAGE_BYTES = W_BYTES + NT * kBlk;
-  static constexpr uint32_t ROOM = CPS == 2 ? 110 * 1024 : 220 * 1024;
+  // With few rows of one matrix the partial sums of a split go straight into the CTA that
+  // adds them up, four rows of a column at a time; it has a place for them beside the ring
+  // (up to 8 parts of 4 rows, or 4 of 8, 2 of 16).
+  static constexpr bool PUSH = ONE && MATS == 1 && NT <= 32;
+  static constexpr uint32_t INBOX = PUSH ? 32 * kBlk * 4 : 0;
+  static constexpr uint32_t ROOM = (CPS == 2 ? 110 * 1024 : 220 * 1024) - INBOX;
   static constexpr int FIT = ROOM / STAGE_BYTES;
   static constexpr int STAGES = FIT > 12 ? 12 : FIT;
-  static constexpr uint32_t OFF_BAR = STAGES * STAGE_BYTES;
+  static constexpr uint32_t OFF_INBOX = STAGES * STAGE_BYTES;
+  static constexpr uint32_t OFF_BAR = OFF_INBOX + INBOX;
   static constexpr size_t SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t ACC = MATS * NT;                 // columns of one accumulator
   static constexpr uint32_t SET_COLS = 4 * MATS + 4;         // a word per weight row / 32 and row / 32
@@ -60,8 +71,8 @@ template <int NT, int MATS, int CPS, bool ONE> struct FewCfg {
   static constexpr uint32_t NEED = SETS_AT + (ONE ? kChunk : kSets) * SET_COLS;
   static constexpr uint32_t TMEM_COLS = NEED <= 128 ? 128 : NEED <= 256 ? 256 : 512;
   static_assert(CPS * TMEM_COLS <= 512, "tensor memory of an SM");
-  static_assert(STAGES >= 2 && (2 * STAGES + 2 * kSets + 6) * 8 + 8 <= 512, "barriers");
-  static_assert(MATS * NT * kBlk * 4 <= OFF_BAR, "the sums reuse the ring");
+  static_assert(STAGES >= 2 && (2 * STAGES + 2 * kSets + 7) * 8 + 8 <= 512, "barriers");
+  static_assert(MATS * NT * kBlk * 4 <= OFF_INBOX, "the sums reuse the ring");
 };
 
 // Rows t, t + 4, ... below t1 of a tile by one warp, four columns to a lane: the sums of
@@ -156,9 +167,11 @@ __global__ void __launch_bounds__(192, CPS)
   uint64_t* tfull = sempty + kSets;       // accumulators
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* inbox_full = drain + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(inbox_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* part_s = reinterpret_cast<float*>(smem);       // [MATS][NT][128] after the main loop
+  float4* inbox = reinterpret_cast<float4*>(smem + C::OFF_INBOX);  // [splits][tpr / 4][128], four rows each
 
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -170,7 +183,9 @@ __global__ void __launch_bounds__(192, CPS)
   const int nkb = (int)((long long)kblocks * (rank + 1) / splits) - kb0;   // >= 1: splits <= kblocks
   const int nsets = (nkb + kSet - 1) / kSet, nchunks = (nsets + kChunk - 1) / kChunk;
   const int rows = min(NT, a.M - m0);
-  const int tpr = (rows + splits - 1) / splits;         // rows each CTA of the cluster finishes
+  const bool push = C::PUSH && splits > 1;
+  int tpr = (rows + splits - 1) / splits;               // rows each CTA of the cluster finishes
+  if (push) tpr = (tpr + 3) & ~3;                       // (whole fours: some CTAs may have none)
   const int t0 = min(rows, rank * tpr), t1 = min(rows, t0 + tpr);
 
   if (threadIdx.x == 0) {
@@ -187,8 +202,10 @@ __global__ void __launch_bounds__(192, CPS)
       mbar_init(&tempty[s], 4);
     }
     mbar_init(drain, 1);
+    mbar_init(inbox_full, 1);
     *abort_flag = 0;
     fence_barrier_init();
+    if (push && t1 > t0) mbar_arrive_expect_tx(inbox_full, (uint32_t)((splits - 1) * ((t1 - t0 + 3) / 4) * kBlk * 16));
     prefetch_tmap(&tmW);
     if (MATS == 2) prefetch_tmap(&tmW3);
     prefetch_tmap(&tmX);
@@ -201,6 +218,8 @@ __global__ void __launch_bounds__(192, CPS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // (waited for where the first partial sums leave: the other CTAs' barriers exist then)
+  if (push) cluster_arrive();
 
   if (warp == 0) {
     // (the whole warp, its elected lane issuing)
@@ -329,6 +348,19 @@ __global__ void __launch_bounds__(192, CPS)
     constexpr int P = 16;
     const int f = quad * 32 + lane, col = wt * kBlk + f;
     auto put = [&](int i, const float (&u)[MATS][P]) {
+      if (push) {
+#pragma unroll
+        for (int k = 0; k < P; k += 4) {
+          const int four = (i + k) / 4, owner = four * 4 / tpr;
+          float4* to = inbox + (rank * (tpr / 4) + four - owner * (tpr / 4)) * kBlk + f;
+          if (i + k >= rows) break;
+          if (owner == rank) *to = make_float4(u[0][k], u[0][k + 1], u[0][k + 2], u[0][k + 3]);
+          else
+            st_async_f4(mapa_shared(smem_u32(to), (uint32_t)owner), u[0][k], u[0][k + 1], u[0][k + 2], u[0][k + 3],
+                        mapa_shared(smem_u32(inbox_full), (uint32_t)owner));
+        }
+        return;
+      }
       if (splits > 1) {
 #pragma unroll
         for (int m = 0; m < MATS; ++m)
@@ -360,7 +392,9 @@ __global__ void __launch_bounds__(192, CPS)
 #pragma unroll
       for (int i = 0; i < kChunk; ++i)
         if (i < nsets) place(i, v[i]);
-      if (mbar_wait_warp(tfull, 0, abort_flag, err)) {
+      const bool ok = mbar_wait_warp(tfull, 0, abort_flag, err);
+      if (push) cluster_wait();
+      if (ok) {
         tc_fence_after();
         // (a loop: code that runs once costs its way into the instruction cache)
 #pragma unroll 1
@@ -417,25 +451,50 @@ __global__ void __launch_bounds__(192, CPS)
     }
   }
 
-  // the sums of every CTA of the cluster are in shared memory
-  tc_fence_before();
-  __syncwarp();
-  if (splits > 1) cluster_sync();
-  else __syncthreads();
+  if (push) {
+    if (warp < 2) {
+      cluster_wait();
+    } else if (t1 > t0 && mbar_wait_cluster_warp(inbox_full, 0, abort_flag, err)) {
+      // a column of the tile per thread, which has put this CTA's own share there itself
+      const int f = (warp & 3) * 32 + lane, col = wt * kBlk + f;
+      if (col < a.N) {
+        for (int t = t0; t < t1; t += 4) {
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int r = 0; r < splits; ++r) {          // in rank order
+            const float4 p = inbox[(r * (tpr / 4) + (t - t0) / 4) * kBlk + f];
+            v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+          }
+          const size_t at = (size_t)(m0 + t) * a.N + col;
+          if (a.y_dtype == TB_F32)
+            put_column(static_cast<float*>(a.y) + at, static_cast<const float*>(a.res), at, a.N, t1 - t, v);
+          else
+            put_column(static_cast<bf16*>(a.y) + at, static_cast<const bf16*>(a.res), at, a.N, t1 - t, v);
+        }
+      }
+    }
+  } else {
+    // the sums of every CTA of the cluster are in shared memory
+    tc_fence_before();
+    __syncwarp();
+    if (splits > 1) cluster_sync();
+    else __syncthreads();
 
-  if (warp >= 2) {
-    const int t = t0 + warp - 2;
-    if (splits == 8) finish_rows<NT, MATS, 8, 1>(a, part_s, m0, wt, t, t1, lane);
-    else if (splits == 4) finish_rows<NT, MATS, 4, 2>(a, part_s, m0, wt, t, t1, lane);
-    else if (splits == 2) finish_rows<NT, MATS, 2, 4>(a, part_s, m0, wt, t, t1, lane);
-    else if (MATS == 2 && a.y_dtype == TB_E4M3) finish_rows<NT, MATS, 1, 4>(a, part_s, m0, wt, t, t1, lane);
+    if (warp >= 2) {
+      const int t = t0 + warp - 2;
+      if (splits == 8) finish_rows<NT, MATS, 8, 1>(a, part_s, m0, wt, t, t1, lane);
+      else if (splits == 4) finish_rows<NT, MATS, 4, 2>(a, part_s, m0, wt, t, t1, lane);
+      else if (splits == 2) finish_rows<NT, MATS, 2, 4>(a, part_s, m0, wt, t, t1, lane);
+      else if (MATS == 2 && a.y_dtype == TB_E4M3) finish_rows<NT, MATS, 1, 4>(a, part_s, m0, wt, t, t1, lane);
+    }
   }
 
   // no CTA leaves (and frees its shared memory) while another still reads it
   tc_fence_before();
   __syncwarp();
-  if (splits > 1) cluster_sync();
+  if (splits > 1 && !push) cluster_sync();
   else __syncthreads();
+  // (what was pushed has all arrived; a CTA that gave up stays until the others are gone)
+  if (push && *abort_flag) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
