@@ -289,9 +289,11 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + acc * C::ACC1;
       // 32 columns of this lane's row, finished but for the residual
-      auto take = [&](int c, bool free_shared, bool free_all, float (&v)[32]) {
-        uint32_t r[32], u[32];
-        tmem_ld32(taddr + c, r);
+      auto take = [&](int c, bool free_shared, bool free_all, auto& v) {
+        constexpr int BY = sizeof(v) / sizeof(v[0]);   // 32 columns each
+        uint32_t r[BY][32], u[32];
+#pragma unroll
+        for (int t = 0; t < BY; ++t) tmem_ld32(taddr + c + 32 * t, r[t]);
         if constexpr (GATED) tmem_ld32(taddr + 128 + c, u);
         tmem_wait_ld();
         if (free_shared || free_all) {
@@ -303,175 +305,152 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
           }
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          v[j] = GATED ? gated(__uint_as_float(r[j]), __uint_as_float(u[j])) : __uint_as_float(r[j]);
+        for (int t = 0; t < BY; ++t)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[t][j] = GATED ? gated(__uint_as_float(r[t][j]), __uint_as_float(u[j])) : __uint_as_float(r[t][j]);
       };
-      // the 32 columns (of gated ones the pairs) that reach into the shared ones, at once
-      const int c_first = acc ? 0 : COLS - 32;
-      float v0[32];
-      take(c_first, true, false, v0);
       const int row = at.x;
-      next = tile + tstep < tiles ? corner(tile + tstep) : make_int2(a.M, 0);
-#pragma unroll 1
-      for (int i = 0; i < pieces; ++i, ++n) {
+      uint8_t* mine = nullptr;           // this lane's row of the current piece
+      // its 16-byte part p lies at p ^ (row % 8)
+      auto part = [&](int p) { return reinterpret_cast<uint4*>(mine + ((p ^ (lane & 7)) << 4)); };
+      // Piece i, into a buffer that its last store has left and that holds the residual.
+      auto open = [&](int i) {
         const uint32_t b = n & 1;
-        const int c0 = piece_of(i, acc) * wide, col = at.y + c0;
-        const bool in = row < a.M && col < a.N;
-        const bool last = i + 1 == pieces;
-        uint8_t* mine = buf + b * C::PIECE + lane * 128;
-        if (res) {
-          // the next piece's residual, once the store before this one has left its buffer
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-          if (last) request(next.x, next.y + piece_of(0, acc ^ 1) * wide, b ^ 1);
-          else request(row, at.y + piece_of(i + 1, acc) * wide, b ^ 1);
-          if (in) {
-            if (!(ok = mbar_wait_warp(&rfull[w * 2 + b], rphase >> b & 1, abort_flag, err))) break;
-            rphase ^= 1u << b;
-          }
-        } else {
+        mine = buf + b * C::PIECE + lane * 128;
+        if (!res) {
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
+          return;
         }
-        // a piece's 16-byte part p lies at p ^ (row % 8)
-        auto part = [&](int p) { return reinterpret_cast<uint4*>(mine + ((p ^ (lane & 7)) << 4)); };
-        if constexpr (ESIZE == 1) {
-          // The values go back to tensor memory, into those of their columns that no other
-          // tile uses, until the row's scale is known: 128 of them would not stay in registers.
-          const uint32_t keep = taddr + (acc ? 128 : 0);
-          float top = 0.f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int cq = acc ? q : (q + 3) & 3;      // shared columns first, as the pieces go
-            float v[32];
-            if (q == 0) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = v0[j];
-            } else {
-              take(cq * 32, false, false, v);
-            }
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) top = fmax3(top, fabsf(v[j]), fabsf(v[j + 1]));
-            tmem_st32(keep + cq * 32, *reinterpret_cast<const uint32_t(*)[32]>(v));
+        // (the next piece's is requested once the store before this one has left its buffer)
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        if (i + 1 == pieces) request(next.x, next.y + piece_of(0, acc ^ 1) * wide, b ^ 1);
+        else request(row, at.y + piece_of(i + 1, acc) * wide, b ^ 1);
+        if (row < a.M && at.y + piece_of(i, acc) * wide < a.N) {
+          ok = mbar_wait_warp(&rfull[w * 2 + b], rphase >> b & 1, abort_flag, err);
+          rphase ^= 1u << b;
+        }
+      };
+      auto close = [&](int i) {
+        const int col = at.y + piece_of(i, acc) * wide;
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          if (row < a.M && col < a.N) {
+            if (stream) tma_store_3d_hint(&tmY, buf + (n & 1) * C::PIECE, col * ESIZE, row, 0, policy_evict_first());
+            else tma_store_3d(&tmY, buf + (n & 1) * C::PIECE, col * ESIZE, row, 0);
           }
-          tmem_wait_st();
-          const bool wild = top == INFINITY;           // an infinity: told from values one by one
-          if (wild) top = 0.f;
-          if (__any_sync(0xffffffffu, wild)) {
+          bulk_commit();
+        }
+        ++n;
+      };
+      // All loops here stay loops: unrolled, their code was fetched anew for each tile
+      // (gated 16384 x 768 x 768 33.6 us, 25.9 so).  The 32 columns that reach into the
+      // shared ones come first, and addresses after them.
+      if constexpr (ESIZE == 1) {
+        // The values go back to tensor memory, into those of their columns that no other
+        // tile uses, until the row's scale is known: 128 of them would not stay in registers.
+        const uint32_t keep = taddr + (acc ? 128 : 0);
+        float top = 0.f;
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              uint32_t r[32];
-              tmem_ld32(keep + q * 32, r);
-              tmem_wait_ld();
-              if (wild) {
+        for (int q = 0; q < 4; ++q) {
+          const int cq = acc ? q : (q + 3) & 3;
+          float v[1][32];
+          take(cq * 32, q == 0, false, v);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) top = fmaxf(top, finite_mag(__uint_as_float(r[j])));
-              }
-            }
-          }
-          const int e = block_exponent(top);
-          const float inv = pow2i(-e);
-#pragma unroll
+          for (int j = 0; j < 32; j += 2) top = fmax3(top, fabsf(v[0][j]), fabsf(v[0][j + 1]));
+          tmem_st32(keep + cq * 32, *reinterpret_cast<const uint32_t(*)[32]>(v[0]));
+        }
+        next = tile + tstep < tiles ? corner(tile + tstep) : make_int2(a.M, 0);
+        tmem_wait_st();
+        const bool wild = top == INFINITY;           // an infinity: told from values one by one
+        if (wild) top = 0.f;
+        if (__any_sync(0xffffffffu, wild)) {
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
-            uint32_t r[32], k[8];
+            uint32_t r[32];
             tmem_ld32(keep + q * 32, r);
             tmem_wait_ld();
-            if (q == 3) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(tempty_cl[acc]);
-            }
             if (wild) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(to_code(__uint_as_float(r[j]), 1.f));
+              for (int j = 0; j < 32; ++j) top = fmaxf(top, finite_mag(__uint_as_float(r[j])));
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              k[j] = codes_of4(__uint_as_float(r[4 * j]) * inv, __uint_as_float(r[4 * j + 1]) * inv,
-                               __uint_as_float(r[4 * j + 2]) * inv, __uint_as_float(r[4 * j + 3]) * inv);
-            *part(2 * q) = make_uint4(k[0], k[1], k[2], k[3]);
-            *part(2 * q + 1) = make_uint4(k[4], k[5], k[6], k[7]);
           }
-          if (row + lane < a.M) a.y_scale[(size_t)(row + lane) * n_tiles + col / 128] = (uint8_t)(e + 127);
-        } else if constexpr (ESIZE == 4) {
-          float v[32];
-          if (i == 0) {
+        }
+        const int e = block_exponent(top);
+        const float inv = pow2i(-e);
+        open(0);
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t r[32], k[8];
+          tmem_ld32(keep + q * 32, r);
+          tmem_wait_ld();
+          if (q == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty_cl[acc]);
+          }
+          if (wild) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = v0[j];
-          } else {
-            take(c0, false, last, v);
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(to_code(__uint_as_float(r[j]), 1.f));
           }
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            float4 t = make_float4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
-            float4* at = reinterpret_cast<float4*>(part(p));
-            if (res) {
-              const float4 r = *at;
-              t = make_float4(t.x + r.x, t.y + r.y, t.z + r.z, t.w + r.w);
-            }
-            *at = t;
-          }
-        } else {
-          // (of accumulator 0's first piece the upper half is there already, of accumulator
-          // 1's the lower)
-          auto half = [&](int hh, const float (&v)[32]) {
+          for (int j = 0; j < 8; ++j)
+            k[j] = codes_of4(__uint_as_float(r[4 * j]) * inv, __uint_as_float(r[4 * j + 1]) * inv,
+                             __uint_as_float(r[4 * j + 2]) * inv, __uint_as_float(r[4 * j + 3]) * inv);
+          *part(2 * q) = make_uint4(k[0], k[1], k[2], k[3]);
+          *part(2 * q + 1) = make_uint4(k[4], k[5], k[6], k[7]);
+        }
+        if (row + lane < a.M) a.y_scale[(size_t)(row + lane) * n_tiles + at.y / 128] = (uint8_t)(e + 127);
+        close(0);
+      } else {
+        // 32 columns of a piece at a time, in 16 bits without gates its 64 at once
+        // (16384 x 1024 x 256 16.5 us by 32, 14.5 so).
+        constexpr int BY = ESIZE == 2 && !GATED ? 2 : 1, SUB = ESIZE == 2 ? 2 / BY : 1;
+#pragma unroll 1
+        for (int x = 0; ok && x < pieces * SUB; ++x) {
+          const int i = x / SUB, h = x % SUB;
+          // (of accumulator 0's first piece the upper half holds the shared columns)
+          const int hh = SUB == 2 && !acc && i == 0 ? h ^ 1 : h;
+          float v[BY][32];
+          take(piece_of(i, acc) * wide + 32 * hh, x == 0, x + 1 == pieces * SUB, v);
+          if (x == 0) next = tile + tstep < tiles ? corner(tile + tstep) : make_int2(a.M, 0);
+          if (h == 0) open(i);
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              uint4* to = part(4 * hh + p);
-              uint4 o;
-              uint32_t* oo = &o.x;
+          for (int p = 0; p < 8 * BY * ESIZE / 4; ++p) {
+            uint4* to = part((SUB == 2 ? 4 * hh : 0) + p);
+            if constexpr (ESIZE == 4) {
+              float4 t = make_float4(v[0][4 * p], v[0][4 * p + 1], v[0][4 * p + 2], v[0][4 * p + 3]);
+              if (res) {
+                const float4 r = *reinterpret_cast<const float4*>(to);
+                t = make_float4(t.x + r.x, t.y + r.y, t.z + r.z, t.w + r.w);
+              }
+              *reinterpret_cast<float4*>(to) = t;
+            } else {
+              float* f = &v[p / 4][8 * (p % 4)];
               if (res) {
                 const uint4 r = *to;
                 const uint32_t* rr = &r.x;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const __nv_bfloat162 t = __floats2bfloat162_rn(v[8 * p + 2 * k] + __uint_as_float(rr[k] << 16),
-                                                                 v[8 * p + 2 * k + 1] + __uint_as_float(rr[k] & 0xffff0000u));
-                  oo[k] = *reinterpret_cast<const uint32_t*>(&t);
+                  f[2 * k] += __uint_as_float(rr[k] << 16);
+                  f[2 * k + 1] += __uint_as_float(rr[k] & 0xffff0000u);
                 }
-              } else {
+              }
+              uint4 o;
+              uint32_t* oo = &o.x;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const __nv_bfloat162 t = __floats2bfloat162_rn(v[8 * p + 2 * k], v[8 * p + 2 * k + 1]);
-                  oo[k] = *reinterpret_cast<const uint32_t*>(&t);
-                }
+              for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+                oo[k] = *reinterpret_cast<const uint32_t*>(&t);
               }
               *to = o;
             }
-          };
-          if (i == 0) {
-            float v[32];
-            take(c0 + (acc ? 32 : 0), false, last, v);
-            half(acc ? 0 : 1, v0);
-            half(acc ? 1 : 0, v);
-          } else if constexpr (GATED) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float v[32];
-              take(c0 + 32 * h, false, last && h == 1, v);
-              half(h, v);
-            }
-          } else {
-            uint32_t r[2][32];
-            tmem_ld32(taddr + c0, r[0]);
-            tmem_ld32(taddr + c0 + 32, r[1]);
-            tmem_wait_ld();
-            if (last) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(tempty_cl[acc]);
-            }
-            half(0, reinterpret_cast<const float(&)[32]>(r[0]));
-            half(1, reinterpret_cast<const float(&)[32]>(r[1]));
           }
+          if (h == SUB - 1) close(i);
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (in && lane == 0) {
-          if (stream) tma_store_3d_hint(&tmY, buf + b * C::PIECE, col * ESIZE, row, 0, policy_evict_first());
-          else tma_store_3d(&tmY, buf + b * C::PIECE, col * ESIZE, row, 0);
-        }
-        if (lane == 0) bulk_commit();
       }
     }
     // a residual that was requested lands before the CTA ends, whatever became of its sums
