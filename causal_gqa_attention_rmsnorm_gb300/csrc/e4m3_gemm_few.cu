@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(192, CPS)
       const int t = t0 + warp - 2;
       if (splits == 8) finish_rows<NT, MATS, 8, 1>(a, part_s, m0, wt, t, t1, lane);
       else if (splits == 4) finish_rows<NT, MATS, 4, 2>(a, part_s, m0, wt, t, t1, lane);
-      else if (splits == 2) finish_rows<NT, MATS, 2, 4>(a, part_s, m0, wt, t, t1, lane);
-      else if (MATS == 2 && a.y_dtype == TB_E4M3) finish_rows<NT, MATS, 1, 4>(a, part_s, m0, wt, t, t1, lane);
+      else if (splits == 2) finish_rows<NT, MATS, 2, 2>(a, part_s, m0, wt, t, t1, lane);
+      else if (MATS == 2 && a.y_dtype == TB_E4M3) finish_rows<NT, MATS, 1, 2>(a, part_s, m0, wt, t, t1, lane);
     }
   }
 
@@ -556,7 +556,7 @@ template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStrea
 
 // Rows of X per tile for M rows, or 0 where k_e4m3_many is the better one.
 //
-// Short K (up to 2048): a call is its fixed cost, which grows with the tile, so the
+// Short K (up to 2048, gated 1024): a call is its fixed cost, which grows with the tile, so the
 // smallest tile whose tiles are all resident at once, two CTAs per SM; the largest only up
 // to 1024 or for fp32 results; then 256 x 256 tiles.  Long K: the first tile whose tiles
 // are resident twice over, that is with K split in two or more; then 256 x 256 tiles, or
@@ -568,15 +568,16 @@ template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStrea
 //   K 4096, N 4096:   256       11.8   10.5   12.0   14.4       512: 22.4  14.3  13.7  14.6
 //   K 4096, N 14336:  128       24.3   17.0   15.7   17.1       256: 36.8  29.0  30.8  17.5
 //   K 14336, N 4096:  256       30.1   22.2   19.6   35.7       512: 59.2  36.3  32.1  36.1
-//   gated, K 768, F 2048:    333   7.9  10.5    -    9.6       1024: 15.4  12.0    -  10.5
-//   gated, K 4096, F 2048:   256  13.1  14.4    -   16.0        333: 18.4  17.9    -  16.1
-//   gated, K 4096, F 14336:   64  28.5  25.7    -   30.1        128: 51.6  43.6    -  30.6
+//   gated, K 768, F 2048:    512   8.3  11.1    -    8.8       1024: 15.5  12.2    -   9.7
+//   gated, K 1536, F 4096:   128   9.5  12.2    -    9.9        192: 10.6  12.7    -  10.0
+//   gated, K 4096, F 2048:   256  13.1  14.5    -   14.9        333: 18.4  18.0    -  15.1
+//   gated, K 4096, F 14336:   64  28.6  25.6    -   28.8        128: 51.8  43.8    -  29.4
 int e4m3_few_tile(int M, int N, int K, int mats, bool f32, int sms) {
   const long long wtiles = ((long long)N + kBlk - 1) / kBlk, slots = 2LL * sms;
   auto fits = [&](int nt, int times) { return wtiles * (((long long)M + nt - 1) / nt) * times <= slots; };
   if (M <= 16) return 16;
   if (M <= 32) return 32;
-  if (K <= 2048) {
+  if (K <= (mats == 1 ? 2048 : 1024)) {
     if (fits(32, 1)) return 32;
     if (mats == 1 && fits(64, 1)) return 64;
     if (mats == 1 && (f32 || K <= 1024) && fits(128, 1)) return 128;

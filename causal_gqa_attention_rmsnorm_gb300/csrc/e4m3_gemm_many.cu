@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
         ++n;
       };
       // All loops here stay loops: unrolled, their code was fetched anew for each tile
-      // (gated 16384 x 768 x 768 33.6 us, 25.9 so).  The 32 columns that reach into the
+      // (gated 16384 x 768 x 768 33.6 us, 26.0 so).  The 32 columns that reach into the
       // shared ones come first, and addresses after them.
       if constexpr (ESIZE == 1) {
         // The values go back to tensor memory, into those of their columns that no other
