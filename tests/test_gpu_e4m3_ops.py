@@ -140,6 +140,53 @@ def test_norm_without_a_finite_result(dtype):
     assert (bytes_of(out.scale)[1] == 27).all()
 
 
+# one of each number of eights per thread that the rule takes for these types, with warps,
+# a CTA's last block and its last eight partly filled
+MANY_ROWS = [(401, 240, BF16, None), (401, 496, BF16, None), (401, 656, BF16, None), (403, 1008, BF16, None),
+             (402, 2000, BF16, None), (2050, 1936, BF16, None), (401, 4112, BF16, None), (310, 5136, BF16, None),
+             (401, 496, BF16, BF16), (401, 656, BF16, F32), (403, 1008, BF16, BF16), (310, 8176, BF16, F32), (310, 8208, BF16, BF16),
+             (4099, 240, F32, None), (4099, 496, F32, None), (4099, 656, F32, None), (4099, 1008, F32, None),
+             (401, 1040, F32, None), (305, 12304, F32, None), (401, 1008, F32, BF16), (401, 4080, F32, F32),
+             (310, 4112, F32, F32), (401, 2064, F32, BF16), (310, 4112, F32, BF16), (305, 12304, F32, BF16)]
+
+
+@pytest.mark.parametrize("M,d,dtype,r_dtype", MANY_ROWS)
+def test_norm_of_many_rows(M, d, dtype, r_dtype):
+    """With a NaN, an infinity, a row of zeros without eps and a result beyond fp32 among them."""
+    g = gen(M + d)
+    x = stream_rows(M, d, dtype, g)
+    gain = (1 + 0.1 * torch.randn(d, generator=g)).to(dtype).cuda()
+    r = None if r_dtype is None else torch.randn(M, d, generator=g).to(r_dtype).cuda()
+    x[1, 7], x[3, d - 1], x[5] = float("nan"), float("inf"), 0
+    gain[d // 2] = 3e38
+    if r is not None:
+        r[5] = 0
+    out, h = tb.tb_rmsnorm_e4m3(x, gain, 0.0, r=r)
+    no_error()
+    total = f64(x) + (0 if r is None else f64(r))
+    if r is not None:
+        fine = np.isfinite(total)
+        assert (np.abs(f64(h) - total)[fine] <= 2 * (HALF[dtype] + 2.0 ** -24) * np.abs(total)[fine]).all()
+        assert (np.isnan(f64(h)) == np.isnan(total)).all() and (np.isinf(f64(h)) == np.isinf(total)).all()
+    with np.errstate(all="ignore"):
+        y = ref.norm(total, f64(gain), 0.0)
+    assert np.isnan(y[1]).all() and np.isnan(y[5]).all() and (np.delete(y[3], d - 1) == 0).all()
+    y = np.where(np.abs(y) <= 3.4028234e38, y, np.nan)                # fp32's range
+    check_rows(bytes_of(out.codes), bytes_of(out.scale), y, NORM_OFF * np.abs(y))
+
+
+@pytest.mark.parametrize("M,d,dtype", [(401, 240, BF16), (401, 496, BF16), (401, 1008, BF16), (310, 8208, BF16), (401, 240, F32), (401, 1008, F32),
+                                       (310, 4112, F32)])
+def test_quant_of_many_rows(M, d, dtype):
+    x = stream_rows(M, d, dtype, gen(M + d))
+    x[1, 7], x[3, d - 1], x[5] = float("nan"), float("inf"), 0
+    x[7, :128] = float("-inf")
+    out = tb.tb_quant_e4m3(x)
+    no_error()
+    check_rows(bytes_of(out.codes), bytes_of(out.scale), f64(x), np.zeros((M, d)))
+    assert bytes_of(out.scale)[7, 0] == 27                           # no finite value at all
+
+
 @pytest.mark.parametrize("M,d", [(2, 400), (400, 768)])
 def test_norm_in_place_gives_the_same(M, d):
     g = gen(5)
