@@ -3,24 +3,29 @@
 // The clusters of two CTAs walk the tiles (persistent).  A CTA stages its own 128 rows
 // of X and 128 rows of W per K block of 128 (32 KB, six stages); the even CTA issues
 // M = 256 instructions that read B from both CTAs' shared memory.  In the gated product
-// the even CTA stages rows of W1 and the odd one the same rows of W3, so that the
-// accumulator's columns 0..127 are gates and 128..255 what they gate: one tile is one
-// block of 128 columns of the result, and a row's scale is decided in one thread.
+// one CTA stages rows of W1 and the other the same rows of W3, so that half of the
+// accumulator's columns are gates and half what they gate: one tile is one block of 128
+// columns of the result.  Accumulator 0 has the gates first and accumulator 1 last.
 //   warp 0      TMA;
 //   warp 1      issues the instructions (even CTA);
-//   warps 2..5  epilogue, a row of the tile per lane;
-//   warps 6..9  put the scales into tensor memory, four K blocks at a time.
+//   warps 2..9  epilogue, half a row of the tile per lane;
+//   warps 10..13  put the scales of four K blocks at a time into shared memory, from where
+//               the issuing warp has them copied to tensor memory.
 // Tensor memory holds two accumulators of 256 columns and two scale sets of 12, which
 // is more than its 512 columns: accumulator 0 takes columns 0..255, accumulator 1
 // columns 224..479, and the 32 columns that they share are read first when a tile is
 // finished; the next tile's instructions wait for that (and not for the rest).
 //
-// Measured in a stream of calls: 16384 x 4096 x 14336 with the residual 535 us (3590
-// TFLOP/s, 0.93 of twice cuBLAS's bf16 rate), gated 8192 x 14336 x 4096 519 us (3700);
-// over seconds the power limit holds both near 3000 at 1.4 to 1.6 GHz.  A K block takes
-// the tensor cores 516 cycles and a tile's change 2400 more (the last instructions' end,
-// the shared columns' way out, the first instructions' start): tensor pipe 75 % busy at K
-// = 4096 and, on 3.4 waves of tiles, at 14336.
+// Measured in a stream of calls: 16384 x 4096 x 14336 with the residual 535-550 us (3500-3590
+// TFLOP/s, 0.91-0.93 of twice cuBLAS's bf16 rate), gated 8192 x 14336 x 4096 510-520 us
+// (3700); the power limit sets both (over seconds near 3000 at 1.4 to 1.6 GHz).  Short K:
+// 16384 x 768 x 768 13.1 us, gated 8192 x 2048 x 768 24.3 (there SiLU and the chain from the
+// sums to the store take longer than a tile's 3100 cycles of instructions).
+// What short K gained: scales through shared memory and the issuing warp's copies, where
+// they had been stored to tensor memory by warps that first waited for a set's last
+// instruction (17.6 -> 13.2 us, gated 31.5 -> 27); eight epilogue warps for four (gated
+// 16384 x 2048 x 768 to fp32 59 -> 53 us); both for the smallest calls (gated 256 x 2048 x 768
+// 8.7 -> 7.3).
 // Tried: operands in a branch on the lane instead of a converged warp (650 us for 569 at
 // that time); three more sets of scales by sharing 64 columns (672 for 650: the division
 // by five sat in the issuing warp); clusters of two pairs that multicast X (557 for 551:
@@ -42,12 +47,15 @@ constexpr int kRowsCta = 128;    // rows of X per CTA
 struct ManyCfg {
   static constexpr int STAGES = 6;
   static constexpr uint32_t A_BYTES = kRowsCta * kBlk, B_BYTES = 128 * kBlk, STAGE_BYTES = A_BYTES + B_BYTES;
-  // two pieces of 32 rows x 128 bytes of y for each epilogue warp
-  static constexpr uint32_t OFF_EPI = STAGES * STAGE_BYTES, PIECE = 32 * 128;
-  static constexpr uint32_t OFF_BAR = OFF_EPI + 4 * 2 * PIECE;
-  static constexpr size_t SMEM = OFF_BAR + 256 + 1024;
+  // two pieces of 32 rows x 64 bytes of y for each epilogue warp
+  static constexpr uint32_t OFF_EPI = STAGES * STAGE_BYTES, PIECE = 32 * 64;
+  // scale sets: a word of four scales for each of the CTA's rows of X, row 32 c + l at 16 l + 4 c,
+  // and eight rows of 16 bytes of the one word of either half of W
+  static constexpr uint32_t OFF_SF = OFF_EPI + 8 * 2 * PIECE, SF_W = 512, SF_BYTES = 768;
+  static constexpr uint32_t OFF_EXP = OFF_SF + 2 * SF_BYTES, OFF_BAR = OFF_EXP + 512;
+  static constexpr size_t SMEM = OFF_BAR + 384;
   static constexpr uint32_t ACC1 = 224, SETS_AT = 480, SET_COLS = 16;
-  static constexpr int THREADS = 320;
+  static constexpr int THREADS = 448;
 };
 
 // Tile -> (row unit of 256, column tile): column tiles fastest, or in groups of
@@ -73,20 +81,25 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
   using C = ManyCfg;
   constexpr int STAGES = C::STAGES;
   constexpr int COLS = GATED ? 128 : 256;               // columns of y per tile
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {                         // (every CTA alike; the tiles' swizzle needs it)
+    if (threadIdx.x == 0) atomicOr(err, TB_DEVERR_TIMEOUT);
+    return;
+  }
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + STAGES;
   uint64_t* sfull = empty + STAGES;                     // scale sets
-  uint64_t* sempty = sfull + 2;
-  uint64_t* tfull = sempty + 2;                         // accumulators
+  uint64_t* sempty = sfull + 2;                         // ... copied to tensor memory
+  uint64_t* sdone = sempty + 2;                         // ... and used there
+  uint64_t* tfull = sdone + 2;                         // accumulators
   uint64_t* tempty = tfull + 2;
   uint64_t* shared_free = tempty + 2;                   // the columns both accumulators use
   uint64_t* rfull = shared_free + 1;                    // residual pieces, two for each epilogue warp
-  uint64_t* drain = rfull + 8;
+  uint64_t* efull = rfull + 16;                         // exponents of both halves of 32 rows
+  uint64_t* drain = efull + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * STAGES + 16) * 8 + 8 <= 256, "barriers");
+  static_assert((2 * STAGES + 32) * 8 + 8 <= 384, "barriers");
 
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -103,11 +116,13 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sfull[s], 8);        // four warps of each CTA, on the even CTA's
       mbar_init(&sempty[s], 1);
+      mbar_init(&sdone[s], 1);
       mbar_init(&tfull[s], 1);
-      mbar_init(&tempty[s], 8);
+      mbar_init(&tempty[s], 16);      // eight epilogue warps
     }
     mbar_init(shared_free, 8);
-    for (int i = 0; i < 8; ++i) mbar_init(&rfull[i], 1);
+    for (int i = 0; i < 16; ++i) mbar_init(&rfull[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&efull[i], 2);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -135,11 +150,12 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
     const uint64_t first = policy_evict_first();
     const uint32_t ring = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
     const uint32_t even0 = mapa_shared(full0, 0);      // a pair's bytes complete on its even CTA's barriers
-    const CUtensorMap* tw = GATED && rank ? &tmW3 : &tmW;
     uint32_t stage = 0, phase = 0;
     int issued = 0;
+    uint32_t acc = 0;
     bool ok = true;
-    for (int tile = tile0; ok && tile < tiles; tile += tstep) {
+    for (int tile = tile0; ok && tile < tiles; tile += tstep, acc ^= 1) {
+      const CUtensorMap* tw = GATED && rank != acc ? &tmW3 : &tmW;
       int mu, nt;
       place(tile, m_units, n_tiles, group, mu, nt);
       const int xrow = (mu * 2 + (int)rank) * kRowsCta;       // a block past M reads zeros
@@ -182,13 +198,20 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
       for (int tile = tile0; ok && tile < tiles; tile += tstep, ++local) {
         const int acc = local & 1;
         if (!mbar_wait_warp(&tempty[acc], ((local >> 1) & 1) ^ 1u, abort_flag, err)) break;
-        // (the scales first: the tile before holds the shared columns up a little longer)
-        if (!mbar_wait_warp(&sfull[set & 1], (set >> 1) & 1, abort_flag, err)) break;
-        if (local && !mbar_wait_warp(shared_free, (local - 1) & 1, abort_flag, err)) break;
         const uint32_t d = tmem + acc * C::ACC1;
         for (int kb = 0; ok && kb < kblocks; kb += kSet, ++set) {
           const uint32_t sb = set & 1, sf = tmem + C::SETS_AT + sb * C::SET_COLS;
-          if (kb && !(ok = mbar_wait_warp(&sfull[sb], (set >> 1) & 1, abort_flag, err))) break;
+          if (!(ok = mbar_wait_warp(&sfull[sb], (set >> 1) & 1, abort_flag, err))) break;
+          // the place in tensor memory: free when the set before the last is done, while the last
+          // one's instructions run
+          if (!(ok = mbar_wait_warp(&sdone[sb], ((set >> 1) & 1) ^ 1u, abort_flag, err))) break;
+          const uint32_t at = smem_u32(smem) + C::OFF_SF + sb * C::SF_BYTES;
+          tmem_copy_pair_elected(sf, desc_rows16(at, 128), elected);
+          tmem_copy_pair_elected(sf + 4, desc_rows16(at + C::SF_W, 0), elected);
+          tmem_copy_pair_elected(sf + 8, desc_rows16(at + C::SF_W + 128, 0), elected);
+          mma_commit_pair_elected(smem_u32(&sempty[sb]), elected);
+          // (after the scales: the tile before holds the shared columns up a little longer)
+          if (kb == 0 && local && !(ok = mbar_wait_warp(shared_free, (local - 1) & 1, abort_flag, err))) break;
 #pragma unroll
           for (int b = 0; b < kSet; ++b) {
             if (kb + b < kblocks) {
@@ -203,7 +226,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
               if (++stage == STAGES) stage = 0, phase ^= 1u;
             }
           }
-          mma_commit_pair_elected(smem_u32(&sempty[sb]), elected);
+          mma_commit_pair_elected(smem_u32(&sdone[sb]), elected);
         }
         if (ok) mma_commit_pair_elected(smem_u32(&tfull[acc]), elected);
       }
@@ -212,65 +235,61 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
       volatile int no_abort = 0;
       mbar_wait_warp(drain, 0, &no_abort, err);
     }
-  } else if (warp >= 6) {
-    // Scales.  Words of set s + 1 are requested before the wait for set s's place.
+  } else if (warp >= 10) {
+    // Scales: a word for a row of X per lane, and of two warps one for a half of W.  Those of
+    // set s + 1 are requested before the wait for set s's place.
     pdl_wait();
-    const uint32_t at0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::SETS_AT;
+    const int c = warp & 3;
+    uint8_t* put = smem + C::OFF_SF;
     const int nb = (a.N + kBlk - 1) / kBlk;
     int set = 0;
-    int tile = tile0, s = 0;
-    uint32_t x[4], w[2];
+    int tile = tile0, s = 0, acc = 0;
+    uint32_t x = 0, w = 0;
     auto load = [&]() {
       int mu, nt;
       place(tile, m_units, n_tiles, group, mu, nt);
       const int kb = s * kSet, n = min(kSet, kblocks - kb);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int m = (mu * 2 + (int)rank) * kRowsCta + c * 32 + lane;
-        x[c] = m < a.M ? scale_word(a.x.scale + (size_t)m * kblocks + kb, n) : 0x7f7f7f7fu;
-      }
-      const int b0 = GATED ? nt : 2 * nt, b1 = GATED ? nt : 2 * nt + 1;
-      w[0] = scale_word(a.w.scale + (size_t)b0 * kblocks + kb, n);
-      w[1] = b1 < nb ? scale_word((GATED ? a.w3.scale : a.w.scale) + (size_t)b1 * kblocks + kb, n) : 0x7f7f7f7fu;
+      const int m = (mu * 2 + (int)rank) * kRowsCta + c * 32 + lane, b = GATED ? nt : 2 * nt + c;
+      x = m < a.M ? scale_word(a.x.scale + (size_t)m * kblocks + kb, n) : 0x7f7f7f7fu;
+      if (c < 2) w = b < nb ? scale_word((GATED && c != acc ? a.w3.scale : a.w.scale) + (size_t)b * kblocks + kb, n) : 0x7f7f7f7fu;
     };
     const uint32_t sfull_cl[2] = {mapa_shared(smem_u32(&sfull[0]), 0), mapa_shared(smem_u32(&sfull[1]), 0)};
     bool more = tile < tiles;
     if (more) load();
     for (; more; ++set) {
       if (!mbar_wait_warp(&sempty[set & 1], ((set >> 1) & 1) ^ 1u, abort_flag, err)) break;
-      tc_fence_after();
-      const uint32_t at = at0 + (set & 1) * C::SET_COLS;
-      tmem_st4(at, x[0], x[1], x[2], x[3]);
-      tmem_st4(at + 4, w[0], w[0], w[0], w[0]);
-      tmem_st4(at + 8, w[1], w[1], w[1], w[1]);
-      if (++s == nsets) s = 0, tile += tstep;
-      more = tile < tiles;
-      tmem_wait_st();
-      tc_fence_before();
+      uint8_t* to = put + (set & 1) * C::SF_BYTES;
+      *reinterpret_cast<uint32_t*>(to + 16 * lane + 4 * c) = x;
+      if (c < 2) *reinterpret_cast<uint32_t*>(to + C::SF_W + 128 * c + 4 * lane) = w;
+      fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(sfull_cl[set & 1]);
+      if (++s == nsets) s = 0, tile += tstep, acc ^= 1;
+      more = tile < tiles;
       if (more) load();
     }
   } else {
-    // Epilogue: a lane has a row of the tile.  A piece of 128 bytes of each of the warp's
-    // 32 rows goes through shared memory (128-byte swizzle) to a TMA store, which drops what
+    // Epilogue: a lane has half a row of the tile, a warp 32 of those.  A piece of 64 bytes
+    // of each goes through shared memory (64-byte swizzle) to a TMA store, which drops what
     // lies past M or N; the next piece's residual is on its way into the other buffer
     // meanwhile, the next tile's first one before its sums are there.
     pdl_wait();
-    const int quad = warp & 3, w = warp - 2;
+    const int quad = warp & 3, w = warp - 2, half = w >> 2;
     uint8_t* buf = smem + C::OFF_EPI + w * 2 * C::PIECE;
     const uint32_t tempty_cl[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
     const uint32_t shared_cl = mapa_shared(smem_u32(shared_free), 0);
-    constexpr int pieces = COLS * ESIZE / 128, wide = 128 / ESIZE;   // of a tile; columns of one
+    constexpr int CHUNKS = COLS / 64, PER = ESIZE == 4 ? 2 : 1;      // of 32 columns; pieces of one
+    constexpr int wide = 64 / ESIZE, pieces = ESIZE == 1 ? 1 : CHUNKS * PER;
     const bool res = !GATED && a.res;
-    // piece i of a tile in accumulator `acc`, the one with the shared columns first: the
-    // last of accumulator 0, the first of accumulator 1
-    auto piece_of = [&](int i, int acc) { return acc ? i : (i == 0 ? pieces - 1 : i - 1); };
+    // The half's chunk k in accumulator `acc`, the one with the shared columns first: the last
+    // of accumulator 0, the first of accumulator 1; and the first column of its piece i.
+    auto chunk_of = [&](int k, int acc) { return acc || !half ? k : (k == 0 ? CHUNKS - 1 : k - 1); };
+    auto piece_at = [&](int i, int acc) { return ESIZE == 1 ? 0 : chunk_of(i / PER, acc) * 32 + i % PER * wide; };
     // first row and column of the warp's part of a tile
     auto corner = [&](int tile) {
       int mu, nt;
       place(tile, m_units, n_tiles, group, mu, nt);
-      return make_int2((mu * 2 + (int)rank) * kRowsCta + quad * 32, nt * COLS);
+      return make_int2((mu * 2 + (int)rank) * kRowsCta + quad * 32, nt * COLS + half * (COLS / 2));
     };
     uint32_t n = 0, rphase = 0;        // pieces so far; bit b: the parity of buffer b's next residual
     auto request = [&](int row, int col, uint32_t b) {
@@ -280,44 +299,48 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
       else tma_load_3d(&tmRes, buf + b * C::PIECE, &rfull[w * 2 + b], col * ESIZE, row, 0);
     };
     int2 at = corner(tile0), next = at;
-    if (res) request(at.x, at.y + piece_of(0, 0) * wide, 0);
+    if (res) request(at.x, at.y + piece_at(0, 0), 0);
     bool ok = true;
     int local = 0;
     for (int tile = tile0; ok && tile < tiles; tile += tstep, ++local, at = next) {
       const int acc = local & 1;
       if (!(ok = mbar_wait_warp(&tfull[acc], (local >> 1) & 1, abort_flag, err))) break;
       tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + acc * C::ACC1;
-      // 32 columns of this lane's row, finished but for the residual
-      auto take = [&](int c, bool free_shared, bool free_all, auto& v) {
-        constexpr int BY = sizeof(v) / sizeof(v[0]);   // 32 columns each
-        uint32_t r[BY][32], u[32];
-#pragma unroll
-        for (int t = 0; t < BY; ++t) tmem_ld32(taddr + c + 32 * t, r[t]);
-        if constexpr (GATED) tmem_ld32(taddr + 128 + c, u);
-        tmem_wait_ld();
-        if (free_shared || free_all) {
+      const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + acc * C::ACC1 + half * (COLS / 2);
+      // Chunk k: 32 columns of this lane's row, finished but for the residual.
+      auto take = [&](int k, bool free_all, float (&v)[32]) {
+        const uint32_t from = taddr + chunk_of(k, acc) * 32;
+        const bool free_shared = k == 0 && half != acc;
+        uint32_t r[32], u[32];
+        // what the gates gate, which is what lies in the shared columns, before the gates: gated
+        // 8192 x 2048 x 768 25.5 us together, 24.3 so
+        if constexpr (GATED) tmem_ld32(from + (acc ? 0 : 128), u);
+        else tmem_ld32(from, r);
+        if (free_shared) {
+          tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            if (free_shared) mbar_arrive_cluster(shared_cl);
-            if (free_all) mbar_arrive_cluster(tempty_cl[acc]);
-          }
+          if (lane == 0) mbar_arrive_cluster(shared_cl);
+        }
+        if constexpr (GATED) tmem_ld32(from + (acc ? 128 : 0), r);
+        tmem_wait_ld();
+        if (free_all) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty_cl[acc]);
         }
 #pragma unroll
-        for (int t = 0; t < BY; ++t)
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            v[t][j] = GATED ? gated(__uint_as_float(r[t][j]), __uint_as_float(u[j])) : __uint_as_float(r[t][j]);
+        for (int j = 0; j < 32; ++j)
+          v[j] = GATED ? gated(__uint_as_float(r[j]), __uint_as_float(u[j])) : __uint_as_float(r[j]);
       };
       const int row = at.x;
       uint8_t* mine = nullptr;           // this lane's row of the current piece
-      // its 16-byte part p lies at p ^ (row % 8)
-      auto part = [&](int p) { return reinterpret_cast<uint4*>(mine + ((p ^ (lane & 7)) << 4)); };
+      // its 16-byte part p lies at p ^ (row / 2 % 4)
+      auto part = [&](int p) { return reinterpret_cast<uint4*>(mine + ((p ^ (lane >> 1 & 3)) << 4)); };
       // Piece i, into a buffer that its last store has left and that holds the residual.
       auto open = [&](int i) {
         const uint32_t b = n & 1;
-        mine = buf + b * C::PIECE + lane * 128;
+        mine = buf + b * C::PIECE + lane * 64;
         if (!res) {
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
@@ -326,15 +349,15 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
         // (the next piece's is requested once the store before this one has left its buffer)
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
-        if (i + 1 == pieces) request(next.x, next.y + piece_of(0, acc ^ 1) * wide, b ^ 1);
-        else request(row, at.y + piece_of(i + 1, acc) * wide, b ^ 1);
-        if (row < a.M && at.y + piece_of(i, acc) * wide < a.N) {
+        if (i + 1 == pieces) request(next.x, next.y + piece_at(0, acc ^ 1), b ^ 1);
+        else request(row, at.y + piece_at(i + 1, acc), b ^ 1);
+        if (row < a.M && at.y + piece_at(i, acc) < a.N) {
           ok = mbar_wait_warp(&rfull[w * 2 + b], rphase >> b & 1, abort_flag, err);
           rphase ^= 1u << b;
         }
       };
       auto close = [&](int i) {
-        const int col = at.y + piece_of(i, acc) * wide;
+        const int col = at.y + piece_at(i, acc);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
@@ -347,21 +370,20 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
         ++n;
       };
       // All loops here stay loops: unrolled, their code was fetched anew for each tile
-      // (gated 16384 x 768 x 768 33.6 us, 26.0 so).  The 32 columns that reach into the
-      // shared ones come first, and addresses after them.
+      // (gated 16384 x 768 x 768 33.6 us, 26.0 so with four warps).  The chunk that reaches
+      // into the shared columns comes first, and addresses after it.
       if constexpr (ESIZE == 1) {
-        // The values go back to tensor memory, into those of their columns that no other
-        // tile uses, until the row's scale is known: 128 of them would not stay in registers.
+        // The values go back to tensor memory, into those of their columns that no other tile
+        // uses, until the row's scale is known; the two warps of a row exchange exponents.
         const uint32_t keep = taddr + (acc ? 128 : 0);
         float top = 0.f;
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          const int cq = acc ? q : (q + 3) & 3;
-          float v[1][32];
-          take(cq * 32, q == 0, false, v);
+        for (int q = 0; q < CHUNKS; ++q) {
+          float v[32];
+          take(q, false, v);
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) top = fmax3(top, fabsf(v[0][j]), fabsf(v[0][j + 1]));
-          tmem_st32(keep + cq * 32, *reinterpret_cast<const uint32_t(*)[32]>(v[0]));
+          for (int j = 0; j < 32; j += 2) top = fmax3(top, fabsf(v[j]), fabsf(v[j + 1]));
+          tmem_st32(keep + chunk_of(q, acc) * 32, *reinterpret_cast<const uint32_t(*)[32]>(v));
         }
         next = tile + tstep < tiles ? corner(tile + tstep) : make_int2(a.M, 0);
         tmem_wait_st();
@@ -369,7 +391,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
         if (wild) top = 0.f;
         if (__any_sync(0xffffffffu, wild)) {
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < CHUNKS; ++q) {
             uint32_t r[32];
             tmem_ld32(keep + q * 32, r);
             tmem_wait_ld();
@@ -379,15 +401,23 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
             }
           }
         }
-        const int e = block_exponent(top);
+        // [accumulator][half][row]: a warp is here again two tiles later, past the other's
+        // arrival of the tile between, which follows that one's reading
+        volatile int8_t* exps = reinterpret_cast<volatile int8_t*>(smem + C::OFF_EXP) + acc * 256;
+        const int half_e = block_exponent(top);
+        exps[half * 128 + quad * 32 + lane] = (int8_t)half_e;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&efull[quad]);
+        if (!(ok = mbar_wait_warp(&efull[quad], local & 1, abort_flag, err))) break;
+        const int e = max(half_e, (int)exps[(half ^ 1) * 128 + quad * 32 + lane]);
         const float inv = pow2i(-e);
         open(0);
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < CHUNKS; ++q) {
           uint32_t r[32], k[8];
           tmem_ld32(keep + q * 32, r);
           tmem_wait_ld();
-          if (q == 3) {
+          if (q == CHUNKS - 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty_cl[acc]);
@@ -403,53 +433,51 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
           *part(2 * q) = make_uint4(k[0], k[1], k[2], k[3]);
           *part(2 * q + 1) = make_uint4(k[4], k[5], k[6], k[7]);
         }
-        if (row + lane < a.M) a.y_scale[(size_t)(row + lane) * n_tiles + at.y / 128] = (uint8_t)(e + 127);
+        if (!half && row + lane < a.M) a.y_scale[(size_t)(row + lane) * n_tiles + at.y / 128] = (uint8_t)(e + 127);
         close(0);
       } else {
-        // 32 columns of a piece at a time, in 16 bits without gates its 64 at once
-        // (16384 x 1024 x 256 16.5 us by 32, 14.5 so).
-        constexpr int BY = ESIZE == 2 && !GATED ? 2 : 1, SUB = ESIZE == 2 ? 2 / BY : 1;
 #pragma unroll 1
-        for (int x = 0; ok && x < pieces * SUB; ++x) {
-          const int i = x / SUB, h = x % SUB;
-          // (of accumulator 0's first piece the upper half holds the shared columns)
-          const int hh = SUB == 2 && !acc && i == 0 ? h ^ 1 : h;
-          float v[BY][32];
-          take(piece_of(i, acc) * wide + 32 * hh, x == 0, x + 1 == pieces * SUB, v);
-          if (x == 0) next = tile + tstep < tiles ? corner(tile + tstep) : make_int2(a.M, 0);
-          if (h == 0) open(i);
+        for (int k = 0; ok && k < CHUNKS; ++k) {
+          float v[32];
+          take(k, k + 1 == CHUNKS, v);
+          if (k == 0) next = tile + tstep < tiles ? corner(tile + tstep) : make_int2(a.M, 0);
 #pragma unroll
-          for (int p = 0; p < 8 * BY * ESIZE / 4; ++p) {
-            uint4* to = part((SUB == 2 ? 4 * hh : 0) + p);
-            if constexpr (ESIZE == 4) {
-              float4 t = make_float4(v[0][4 * p], v[0][4 * p + 1], v[0][4 * p + 2], v[0][4 * p + 3]);
-              if (res) {
-                const float4 r = *reinterpret_cast<const float4*>(to);
-                t = make_float4(t.x + r.x, t.y + r.y, t.z + r.z, t.w + r.w);
-              }
-              *reinterpret_cast<float4*>(to) = t;
-            } else {
-              float* f = &v[p / 4][8 * (p % 4)];
-              if (res) {
-                const uint4 r = *to;
-                const uint32_t* rr = &r.x;
+          for (int h = 0; h < PER; ++h) {
+            open(k * PER + h);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  f[2 * k] += __uint_as_float(rr[k] << 16);
-                  f[2 * k + 1] += __uint_as_float(rr[k] & 0xffff0000u);
+            for (int p = 0; p < 4; ++p) {
+              uint4* to = part(p);
+              if constexpr (ESIZE == 4) {
+                const float* f = v + 16 * h + 4 * p;
+                float4 t = make_float4(f[0], f[1], f[2], f[3]);
+                if (res) {
+                  const float4 r = *reinterpret_cast<const float4*>(to);
+                  t = make_float4(t.x + r.x, t.y + r.y, t.z + r.z, t.w + r.w);
                 }
-              }
-              uint4 o;
-              uint32_t* oo = &o.x;
+                *reinterpret_cast<float4*>(to) = t;
+              } else {
+                float* f = v + 8 * p;
+                if (res) {
+                  const uint4 r = *to;
+                  const uint32_t* rr = &r.x;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-                oo[k] = *reinterpret_cast<const uint32_t*>(&t);
+                  for (int j = 0; j < 4; ++j) {
+                    f[2 * j] += __uint_as_float(rr[j] << 16);
+                    f[2 * j + 1] += __uint_as_float(rr[j] & 0xffff0000u);
+                  }
+                }
+                uint4 o;
+                uint32_t* oo = &o.x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+                  oo[j] = *reinterpret_cast<const uint32_t*>(&t);
+                }
+                *to = o;
               }
-              *to = o;
             }
+            close(k * PER + h);
           }
-          if (h == SUB - 1) close(i);
         }
       }
     }
@@ -482,11 +510,11 @@ template <bool GATED, int ESIZE> cudaError_t go(const GemmArgs& a, cudaStream_t 
   tw3 = tw;
   if (GATED && (e = make_tmap_rows(&tw3, 1, a.w3.codes, 1, (uint64_t)a.N, (uint64_t)a.K, kBlk, 128)) != cudaSuccess)
     return e;
-  // y and the residual by bytes: a piece is 128 of each of 32 rows
+  // y and the residual by bytes: a piece is 64 of each of 32 rows
   const uint64_t row_bytes = (uint64_t)a.N * ESIZE;
-  if ((e = make_tmap_rows(&ty, 1, a.y, 1, (uint64_t)a.M, row_bytes, 128, 32)) != cudaSuccess) return e;
+  if ((e = make_tmap_rows(&ty, 1, a.y, 1, (uint64_t)a.M, row_bytes, 64, 32)) != cudaSuccess) return e;
   tr = ty;
-  if (a.res && (e = make_tmap_rows(&tr, 1, a.res, 1, (uint64_t)a.M, row_bytes, 128, 32)) != cudaSuccess) return e;
+  if (a.res && (e = make_tmap_rows(&tr, 1, a.res, 1, (uint64_t)a.M, row_bytes, 64, 32)) != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;

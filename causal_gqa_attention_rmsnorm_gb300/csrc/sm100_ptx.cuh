@@ -706,6 +706,27 @@ __device__ __forceinline__ void mma_commit_pair_elected(uint32_t bar, uint32_t e
       : "memory");
 }
 
+// Shared-memory matrix descriptor of 32 rows of 16 bytes without a swizzle: 8-row groups
+// of 128 bytes, `stride` apart (0: the same eight rows four times).
+__device__ __forceinline__ uint64_t desc_rows16(uint32_t saddr, uint32_t stride) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(stride >> 4) << 32;      // stride byte offset: next 8-row group
+  d |= (uint64_t)1 << 46;                  // descriptor version for sm_100
+  return d;
+}
+
+// Four columns of tensor memory, lanes 0..31 and the same in 32..63 and so on, from 32 rows
+// of 16 bytes of shared memory, in both CTAs of a pair from their own.  Instructions that the
+// same thread issues after it see them.  By the elected lane.
+__device__ __forceinline__ void tmem_copy_pair_elected(uint32_t taddr, uint64_t desc, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred pe;\n\tsetp.ne.b32 pe, %2, 0;\n\t"
+      "@pe tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+      "l"(desc), "r"(elected)
+      : "memory");
+}
+
 // What a producer warp does, by its elected lane, for the reason given at mma_mx_k128 (a
 // stage's loads, issued in a branch on the lane, took 250 ns, so 170): an arrival that expects
 // bytes, and 3-D tiled TMA loads with or without an L2 policy, to addresses of this CTA's
