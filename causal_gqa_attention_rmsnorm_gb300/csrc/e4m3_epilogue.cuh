@@ -21,11 +21,21 @@ __device__ __forceinline__ void put4(void* y, int y_dtype, size_t at, float4 v) 
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
 }
-__device__ __forceinline__ float4 get4(const void* y, int y_dtype, size_t at) {
-  if (y_dtype == TB_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(y) + at);
-  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(y) + at);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xffff0000u));
+// The fours at at(0), ..., at(B - 1).  (All are requested before the first is converted: with
+// the type told apart for each, 512 x 4096 x 14336 took 52.0 us, 37.7 so.)
+template <int B, typename At> __device__ __forceinline__ void get4(float4 (&v)[B], const void* y, int y_dtype, At at) {
+  if (y_dtype == TB_F32) {
+#pragma unroll
+    for (int b = 0; b < B; ++b) v[b] = *reinterpret_cast<const float4*>(static_cast<const float*>(y) + at(b));
+    return;
+  }
+  uint2 w[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b) w[b] = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(y) + at(b));
+#pragma unroll
+  for (int b = 0; b < B; ++b)
+    v[b] = make_float4(__uint_as_float(w[b].x << 16), __uint_as_float(w[b].x & 0xffff0000u), __uint_as_float(w[b].y << 16),
+                       __uint_as_float(w[b].y & 0xffff0000u));
 }
 
 // Up to four exponent bytes of consecutive K blocks as one word, the first in the low

@@ -85,11 +85,15 @@ __device__ __forceinline__ void finish_rows(const GemmArgs& a, const float* part
   const uint32_t base = smem_u32(part_s) + 16u * lane;
   for (; t < t1; t += 4 * B) {
     float4 v[B], p[B][MATS][S];
+    if constexpr (MATS == 1) {
+      if (a.res && col < a.N)
+        get4<B>(v, a.res, a.y_dtype, [&](int b) { return (size_t)(m0 + min(t + 4 * b, t1 - 1)) * a.N + col; });
+      else
+        for (int b = 0; b < B; ++b) v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       const int tb = min(t + 4 * b, t1 - 1);         // (past the last: again, not stored)
-      v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (MATS == 1 && a.res && col < a.N) v[b] = get4(a.res, a.y_dtype, (size_t)(m0 + tb) * a.N + col);
 #pragma unroll
       for (int m = 0; m < MATS; ++m)
 #pragma unroll
@@ -136,16 +140,18 @@ __device__ __forceinline__ void finish_rows(const GemmArgs& a, const float* part
   }
 }
 
-// P rows of a column of y (`live` of them exist), with the residual at `at` of res.
+// P rows of a column of y (`live`, at least one, of them exist), with the residual at `at` of
+// res.  (Its loads depend on nothing, so that all are on their way together: 1024 x 2304 x
+// 768 21.0 us by a branch for each, 10.0 so; 9.5 with the lines in L2 by then.)
 template <typename T, int P>
 __device__ __forceinline__ void put_column(T* y, const T* res, size_t at, int N, int live, float (&v)[P]) {
   if (res) {
     const T* r = res + at;
-    float add[P];
+    T add[P];
 #pragma unroll
-    for (int k = 0; k < P; ++k) add[k] = k < live ? to_f(r[(size_t)k * N]) : 0.f;
+    for (int k = 0; k < P; ++k) add[k] = r[(size_t)min(k, live - 1) * N];
 #pragma unroll
-    for (int k = 0; k < P; ++k) v[k] += add[k];
+    for (int k = 0; k < P; ++k) v[k] += to_f(add[k]);
   }
 #pragma unroll
   for (int k = 0; k < P; ++k)
@@ -383,6 +389,13 @@ __global__ void __launch_bounds__(192, CPS)
       else
         put_column(static_cast<bf16*>(a.y) + at, static_cast<const bf16*>(MATS == 1 ? a.res : nullptr), at, a.N, rows - i, v);
     };
+    // the residual that this CTA adds comes into L2 meanwhile
+    auto ahead = [&]() {
+      const int t = t0 + (int)threadIdx.x - 64, c = wt * kBlk;
+      const uint32_t e = a.y_dtype == TB_F32 ? 4 : 2;
+      if (MATS == 1 && a.res && t < t1)
+        prefetch_l2_bulk(static_cast<const uint8_t*>(a.res) + ((size_t)(m0 + t) * a.N + c) * e, (uint32_t)min(kBlk, a.N - c) * e);
+    };
     if constexpr (ONE) {
       // all sets at once: one latency
       Words v[kChunk];
@@ -392,6 +405,7 @@ __global__ void __launch_bounds__(192, CPS)
 #pragma unroll
       for (int i = 0; i < kChunk; ++i)
         if (i < nsets) place(i, v[i]);
+      ahead();
       const bool ok = mbar_wait_warp(tfull, 0, abort_flag, err);
       if (push) cluster_wait();
       if (ok) {
@@ -410,6 +424,7 @@ __global__ void __launch_bounds__(192, CPS)
         }
       }
     } else {
+      ahead();
       bool ok = true;
       int fed = 0;
       float acc[MATS][NT];
@@ -556,31 +571,35 @@ template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStrea
 
 // Rows of X per tile for M rows, or 0 where k_e4m3_many is the better one.
 //
-// Short K (up to 2048, gated 1024): a call is its fixed cost, which grows with the tile, so the
-// smallest tile whose tiles are all resident at once, two CTAs per SM; the largest only up
-// to 1024 or for fp32 results; then 256 x 256 tiles.  Long K: the first tile whose tiles
-// are resident twice over, that is with K split in two or more; then 256 x 256 tiles, or
-// up to 64 gated rows one split less.  Measured, us, by rows per tile, and k_e4m3_many:
+// Short K (up to 2048): a call is its fixed cost, which grows with the tile, so the smallest
+// tile whose tiles are all resident at once, two CTAs per SM; the largest, and gated ones,
+// only up to 128 rows, where half of k_e4m3_many's tile is empty, or (the largest) for fp32
+// results without a residual; then 256 x 256 tiles.  Long K: the first tile whose tiles are
+// resident twice over, that is with K split in two or more; then 256 x 256 tiles, or up to
+// 64 gated rows one split less.  Measured, us, by rows per tile, and k_e4m3_many:
 //                                32     64    128   many
-//   K 768, N 2304:    512 rows   5.5    5.6    7.3    7.7      1024:  9.9   6.4   8.0   8.0
-//        1371: 14.4  10.7   8.5   8.8   (of fp32: 14.7  11.5   9.3  11.2)
-//   K 1536, N 2304:   512        6.7    7.8    9.0    8.7      1371: 18.2  13.6  10.1   9.7
-//   K 4096, N 4096:   256       11.8   10.5   12.0   14.4       512: 22.4  14.3  13.7  14.6
-//   K 4096, N 14336:  128       24.3   17.0   15.7   17.1       256: 36.8  29.0  30.8  17.5
-//   K 14336, N 4096:  256       30.1   22.2   19.6   35.7       512: 59.2  36.3  32.1  36.1
-//   gated, K 768, F 2048:    512   8.3  11.1    -    8.8       1024: 15.5  12.2    -   9.7
-//   gated, K 1536, F 4096:   128   9.5  12.2    -    9.9        192: 10.6  12.7    -  10.0
-//   gated, K 4096, F 2048:   256  13.1  14.5    -   14.9        333: 18.4  18.0    -  15.1
-//   gated, K 4096, F 14336:   64  28.6  25.6    -   28.8        128: 51.8  43.8    -  29.4
-int e4m3_few_tile(int M, int N, int K, int mats, bool f32, int sms) {
+//   K 768, N 2304:    512 rows   5.4    5.6    7.2    7.0      1024:  9.8   6.5   8.1   7.2
+//        1371: 14.3  10.6   8.6   7.9   (to fp32: 14.8  11.3   9.3   9.4; residual: - - 14.6  12.4)
+//   K 1024, N 32768:  128       21.9   14.7   10.6   12.3
+//   K 1536, N 2304:   512        6.8    8.0    9.4    8.7      1371: 18.8  13.6  10.1   9.6
+//        (to fp32: 18.9  13.8  10.0  11.1)
+//   K 4096, N 4096:   256       11.8   10.7   12.1   14.4       512: 22.4  14.3  14.0  14.5
+//   K 4096, N 14336:  128       24.5   17.0   15.9   17.1       256: 36.9  28.9  30.4  17.4
+//   K 14336, N 4096:  256       30.2   22.4   19.9   35.4       512: 59.4  36.3  31.8  35.8
+//   gated, K 768, F 2048:    128   6.8   9.8    -    7.2        256:  7.7   9.9    -   7.2
+//   gated, K 1536, F 4096:   128   9.5  12.0    -    9.5        192: 10.5  12.5    -   9.5
+//   gated, K 2048, F 11008:   96  14.5  19.7    -   17.1
+//   gated, K 4096, F 2048:   256  13.1  14.4    -   14.5        333: 18.2  17.6    -  14.7
+//   gated, K 4096, F 14336:   64  28.6  25.6    -   28.1        128: 52.1  43.9    -  28.8
+int e4m3_few_tile(int M, int N, int K, int mats, bool f32_alone, int sms) {
   const long long wtiles = ((long long)N + kBlk - 1) / kBlk, slots = 2LL * sms;
   auto fits = [&](int nt, int times) { return wtiles * (((long long)M + nt - 1) / nt) * times <= slots; };
   if (M <= 16) return 16;
   if (M <= 32) return 32;
-  if (K <= (mats == 1 ? 2048 : 1024)) {
-    if (fits(32, 1)) return 32;
+  if (K <= 2048) {
+    if ((mats == 1 || M <= 128) && fits(32, 1)) return 32;
     if (mats == 1 && fits(64, 1)) return 64;
-    if (mats == 1 && (f32 || K <= 1024) && fits(128, 1)) return 128;
+    if (mats == 1 && (f32_alone || M <= 128) && fits(128, 1)) return 128;
   } else if (mats == 1) {
     if (fits(64, 2)) return 64;
     if (M > 64 && fits(128, 2)) return 128;
