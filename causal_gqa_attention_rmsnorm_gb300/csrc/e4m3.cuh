@@ -80,7 +80,7 @@ struct GemmArgs {
   int y_dtype;
 };
 // e4m3_gemm_few.cu: any sizes; tiles of 16, 32, 64 or (not gated) 128 rows
-int e4m3_few_tile(int M, int N, int K, int mats, bool f32_alone, int sms);
+int e4m3_few_tile(int M, int N, int K, int mats, bool light, int sms);
 cudaError_t launch_gemm_e4m3_few(const GemmArgs& a, int tile, cudaStream_t s);
 cudaError_t launch_gated_e4m3_few(const GemmArgs& a, int tile, cudaStream_t s);
 // e4m3_gemm_many.cu: CTA pairs, any sizes

@@ -85,7 +85,8 @@ std::atomic<int> g_form{0};            // test hook: 16 to 128 rows per tile, or
 int tile_of(const GemmArgs& a, int mats) {
   const int form = g_form.load(std::memory_order_relaxed);
   if (form) return form < 0 ? 0 : mats == 2 && form > 64 ? 64 : form;
-  const int tile = e4m3_few_tile(a.M, a.N, a.K, mats, a.y_dtype == TB_F32 && !a.res, sm_count());
+  const bool light = mats == 2 ? a.y_dtype != TB_E4M3 : a.y_dtype == TB_F32 && !a.res;
+  const int tile = e4m3_few_tile(a.M, a.N, a.K, mats, light, sm_count());
   if (tile == 0 && a.y_dtype == TB_F32 && a.K > 4096) return mats == 2 ? 64 : 128;
   return tile;
 }
@@ -242,8 +243,8 @@ tb_status tb_gated_e4m3(const tb_e4m3* x, const tb_e4m3* w1, const tb_e4m3* w3, 
 TB_API int32_t tbx_e4m3_form(int32_t form) {
   return g_form.exchange(form == 16 || form == 32 || form == 64 || form == 128 || form == -1 ? form : 0);
 }
-TB_API int32_t tbx_e4m3_few_tile(int32_t M, int32_t N, int32_t K, int32_t mats, int32_t f32_alone, int32_t sms) {
-  return e4m3_few_tile(M, N, K, mats, f32_alone != 0, sms);
+TB_API int32_t tbx_e4m3_few_tile(int32_t M, int32_t N, int32_t K, int32_t mats, int32_t light, int32_t sms) {
+  return e4m3_few_tile(M, N, K, mats, light != 0, sms);
 }
 
 }  // extern "C"

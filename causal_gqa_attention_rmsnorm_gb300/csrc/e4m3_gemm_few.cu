@@ -573,8 +573,8 @@ template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStrea
 //
 // Short K (up to 2048): a call is its fixed cost, which grows with the tile, so the smallest
 // tile whose tiles are all resident at once, two CTAs per SM; the largest, and gated ones,
-// only up to 128 rows, where half of k_e4m3_many's tile is empty, or (the largest) for fp32
-// results without a residual; then 256 x 256 tiles.  Long K: the first tile whose tiles are
+// only up to 128 rows, where half of k_e4m3_many's tile is empty, or for `light` results
+// (fp32 without a residual; gated ones not to codes); then 256 x 256 tiles.  Long K: the first tile whose tiles are
 // resident twice over, that is with K split in two or more; then 256 x 256 tiles, or up to
 // 64 gated rows one split less.  Measured, us, by rows per tile, and k_e4m3_many:
 //                                32     64    128   many
@@ -587,19 +587,20 @@ template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStrea
 //   K 4096, N 14336:  128       24.5   17.0   15.9   17.1       256: 36.9  28.9  30.4  17.4
 //   K 14336, N 4096:  256       30.2   22.4   19.9   35.4       512: 59.4  36.3  31.8  35.8
 //   gated, K 768, F 2048:    128   6.8   9.8    -    7.2        256:  7.7   9.9    -   7.2
+//        (to bf16: 128  5.7   7.2    -    7.0        333:  6.8   7.9    -   7.0)
 //   gated, K 1536, F 4096:   128   9.5  12.0    -    9.5        192: 10.5  12.5    -   9.5
 //   gated, K 2048, F 11008:   96  14.5  19.7    -   17.1
 //   gated, K 4096, F 2048:   256  13.1  14.4    -   14.5        333: 18.2  17.6    -  14.7
 //   gated, K 4096, F 14336:   64  28.6  25.6    -   28.1        128: 52.1  43.9    -  28.8
-int e4m3_few_tile(int M, int N, int K, int mats, bool f32_alone, int sms) {
+int e4m3_few_tile(int M, int N, int K, int mats, bool light, int sms) {
   const long long wtiles = ((long long)N + kBlk - 1) / kBlk, slots = 2LL * sms;
   auto fits = [&](int nt, int times) { return wtiles * (((long long)M + nt - 1) / nt) * times <= slots; };
   if (M <= 16) return 16;
   if (M <= 32) return 32;
   if (K <= 2048) {
-    if ((mats == 1 || M <= 128) && fits(32, 1)) return 32;
+    if ((mats == 1 || light || M <= 128) && fits(32, 1)) return 32;
     if (mats == 1 && fits(64, 1)) return 64;
-    if (mats == 1 && (f32_alone || M <= 128) && fits(128, 1)) return 128;
+    if (mats == 1 && (light || M <= 128) && fits(128, 1)) return 128;
   } else if (mats == 1) {
     if (fits(64, 2)) return 64;
     if (M > 64 && fits(128, 2)) return 128;

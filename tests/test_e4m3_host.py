@@ -131,17 +131,17 @@ def test_empty_calls_need_no_pointers(lib):
 
 # ---- the rule for the kernel --------------------------------------------------------
 
-@pytest.mark.parametrize("M,N,K,mats,f32_alone,tile", [
+@pytest.mark.parametrize("M,N,K,mats,light,tile", [
     (1, 6144, 4096, 1, 0, 16), (16, 6144, 4096, 1, 0, 16), (17, 6144, 4096, 1, 0, 32), (33, 6144, 4096, 1, 0, 64),
     (512, 2304, 768, 1, 0, 32), (513, 2304, 768, 1, 0, 64), (1371, 2304, 768, 1, 1, 128), (1371, 2304, 768, 1, 0, 0), (128, 20000, 768, 1, 0, 128),
     (129, 20000, 768, 1, 0, 0), (1371, 2304, 1536, 1, 1, 128), (1371, 2304, 1536, 1, 0, 0),
     (2049, 2304, 768, 1, 1, 0), (256, 4096, 4096, 1, 0, 64), (257, 4096, 4096, 1, 0, 128), (512, 4096, 4096, 1, 0, 128),
     (513, 4096, 4096, 1, 0, 0), (64, 14336, 4096, 1, 0, 64), (128, 14336, 4096, 1, 0, 128), (129, 14336, 4096, 1, 0, 0),
-    (32, 14336, 4096, 2, 0, 32), (64, 14336, 4096, 2, 0, 64), (65, 14336, 4096, 2, 0, 0), (128, 2048, 768, 2, 0, 32), (129, 2048, 768, 2, 0, 0), (96, 11008, 2048, 2, 0, 32),
+    (32, 14336, 4096, 2, 0, 32), (64, 14336, 4096, 2, 0, 64), (65, 14336, 4096, 2, 0, 0), (128, 2048, 768, 2, 0, 32), (129, 2048, 768, 2, 0, 0), (333, 2048, 768, 2, 1, 32), (96, 11008, 2048, 2, 0, 32),
     (1024, 2048, 768, 2, 0, 0), (128, 4096, 1536, 2, 0, 32), (192, 4096, 1536, 2, 0, 0), (256, 2048, 4096, 2, 0, 32), (333, 2048, 4096, 2, 0, 0),
     (2 ** 31 - 1024, 16, 16, 1, 0, 0), (2 ** 31 - 1024, 16, 16, 2, 1, 0), (64, 2 ** 28, 16, 1, 0, 64)])
-def test_tile_rule(lib, M, N, K, mats, f32_alone, tile):
-    assert lib.tbx_e4m3_few_tile(M, N, K, mats, f32_alone, 152) == tile
+def test_tile_rule(lib, M, N, K, mats, light, tile):
+    assert lib.tbx_e4m3_few_tile(M, N, K, mats, light, 152) == tile
 
 
 # ---- the binding ----------------------------------------------------------------
