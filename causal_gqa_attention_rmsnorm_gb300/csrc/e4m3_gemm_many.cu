@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
         const uint32_t d = tmem + acc * C::ACC1;
         for (int kb = 0; ok && kb < kblocks; kb += kSet, ++set) {
           const uint32_t sb = set & 1, sf = tmem + C::SETS_AT + sb * C::SET_COLS;
-          if (!(ok = mbar_wait_warp(&sfull[sb], (set >> 1) & 1, abort_flag, err))) break;
+          if (!(ok = mbar_wait_cluster_warp(&sfull[sb], (set >> 1) & 1, abort_flag, err))) break;
           // the place in tensor memory: free when the set before the last is done, while the last
           // one's instructions run
           if (!(ok = mbar_wait_warp(&sdone[sb], ((set >> 1) & 1) ^ 1u, abort_flag, err))) break;
@@ -263,6 +263,9 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
       if (c < 2) *reinterpret_cast<uint32_t*>(to + C::SF_W + 128 * c + 4 * lane) = w;
       fence_proxy_async();
       __syncwarp();
+      // (What is published was written into this CTA's own shared memory, is visible to the
+      // copies there since the fence, and is read by them only.  A release at cluster scope
+      // would wait for more: 16384 x 768 x 768 16.7 us for 13.2.)
       if (lane == 0) mbar_arrive_cluster(sfull_cl[set & 1]);
       if (++s == nsets) s = 0, tile += tstep, acc ^= 1;
       more = tile < tiles;
