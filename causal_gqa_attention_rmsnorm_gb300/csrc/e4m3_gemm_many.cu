@@ -334,7 +334,9 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
         }
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          v[j] = GATED ? gated(__uint_as_float(r[j]), __uint_as_float(u[j])) : __uint_as_float(r[j]);
+          v[j] = !GATED ? __uint_as_float(r[j])
+                 : ESIZE == 4 ? gated(__uint_as_float(r[j]), __uint_as_float(u[j]))
+                              : gated_short(__uint_as_float(r[j]), __uint_as_float(u[j]));
       };
       const int row = at.x;
       uint8_t* mine = nullptr;           // this lane's row of the current piece

@@ -284,7 +284,7 @@ template <typename T, typename RT, bool NORM> int eights_per_thread(int M, int e
     if (RES) return eights <= 1024 ? 4 : 8;
     return narrow <= 8 ? (M > 2048 ? 8 : 4) : eights <= 640 ? 4 : 8;
   }
-  if (narrow <= 4) return !RES && M > 4096 ? narrow : 1;
+  if (narrow <= 4) return !RES && M > 2048 ? narrow : 1;
   if (!RES) return eights <= 1536 ? 4 : 8;
   return eights <= 512 ? 2 : std::is_same<RT, bf16>::value && eights <= 1536 ? 4 : 8;
 }
