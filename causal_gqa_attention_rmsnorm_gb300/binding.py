@@ -450,7 +450,8 @@ def tbx_set_stat_poll_ns(ns: int) -> int:
 
 def tbx_e4m3_form(form: int) -> int:
     """Test hook: the form that later 8-bit products take (0: by the rule; 16, 32, 64 or
-    128: the few-rows kernel with so many rows per tile; -1: the many-rows kernel);
+    128: the few-rows kernel with so many rows per tile; -1: the many-rows kernel; -2: the
+    same with a CTA to a tile);
     returns the previous one."""
     return int(lib().tbx_e4m3_form(int(form)))
 

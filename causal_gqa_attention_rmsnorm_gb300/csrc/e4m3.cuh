@@ -79,12 +79,12 @@ struct GemmArgs {
   uint8_t* y_scale;
   int y_dtype;
 };
-// e4m3_gemm_few.cu: any sizes; tiles of 16, 32, 64 or (not gated) 128 rows
+// e4m3_gemm_few.cu: any sizes; tiles of 16, 32, 64 or (not gated) 128 rows; the rule
 int e4m3_few_tile(int M, int N, int K, int mats, bool light, int sms);
 cudaError_t launch_gemm_e4m3_few(const GemmArgs& a, int tile, cudaStream_t s);
 cudaError_t launch_gated_e4m3_few(const GemmArgs& a, int tile, cudaStream_t s);
 // e4m3_gemm_many.cu: CTA pairs, any sizes
-cudaError_t launch_gemm_e4m3_many(const GemmArgs& a, cudaStream_t s);
-cudaError_t launch_gated_e4m3_many(const GemmArgs& a, cudaStream_t s);
+cudaError_t launch_gemm_e4m3_many(const GemmArgs& a, bool one, cudaStream_t s);
+cudaError_t launch_gated_e4m3_many(const GemmArgs& a, bool one, cudaStream_t s);
 
 }  // namespace tb

@@ -76,18 +76,18 @@ tb_status check_weights(const tb_e4m3* w, const char* name, const tb_e4m3* x, bo
   return TB_OK;
 }
 
-// The rows per tile of k_e4m3_few, or 0 for k_e4m3_many.  An fp32 result keeps fp32's
+// The rows per tile of k_e4m3_few, or 0 for k_e4m3_many, -1 with a CTA to a tile.  An fp32 result keeps fp32's
 // sums: k_e4m3_many has one accumulator for all of K, whose cut-off sums are off by up to
 // 2^-24 per instruction of 32 (relative to 64 bits, normal rows: K 4096 2.2e-7, 14336
 // 1.0e-6, against 1.2e-7 in chunks), so from K = 4096 on an fp32 result is formed in
 // chunks.
-std::atomic<int> g_form{0};            // test hook: 16 to 128 rows per tile, or -1 for many
+std::atomic<int> g_form{0};            // test hook: 16 to 128 rows per tile, or -1 and -2 for many
 int tile_of(const GemmArgs& a, int mats) {
   const int form = g_form.load(std::memory_order_relaxed);
-  if (form) return form < 0 ? 0 : mats == 2 && form > 64 ? 64 : form;
+  if (form) return form == -1 ? 0 : form == -2 ? -1 : mats == 2 && form > 64 ? 64 : form;
   const bool light = mats == 2 ? a.y_dtype != TB_E4M3 : a.y_dtype == TB_F32 && !a.res;
   const int tile = e4m3_few_tile(a.M, a.N, a.K, mats, light, sm_count());
-  if (tile == 0 && a.y_dtype == TB_F32 && a.K > 4096) return mats == 2 ? 64 : 128;
+  if (tile <= 0 && a.y_dtype == TB_F32 && a.K > 4096) return mats == 2 ? 64 : 128;
   return tile;
 }
 
@@ -199,7 +199,7 @@ tb_status tb_gemm_e4m3(const tb_e4m3* x, const tb_e4m3* w, const void* res, void
   a.y_dtype = y_dtype;
   if (!device_error_word()) return report(TB_ERR_CUDA, "cannot resolve the device error word");
   const int tile = tile_of(a, 1);
-  return done(tile ? launch_gemm_e4m3_few(a, tile, (cudaStream_t)stream) : launch_gemm_e4m3_many(a, (cudaStream_t)stream),
+  return done(tile > 0 ? launch_gemm_e4m3_few(a, tile, (cudaStream_t)stream) : launch_gemm_e4m3_many(a, tile < 0, (cudaStream_t)stream),
               "tb_gemm_e4m3");
 }
 
@@ -233,15 +233,16 @@ tb_status tb_gated_e4m3(const tb_e4m3* x, const tb_e4m3* w1, const tb_e4m3* w3, 
   a.y_scale = static_cast<uint8_t*>(y_scale);
   if (!device_error_word()) return report(TB_ERR_CUDA, "cannot resolve the device error word");
   const int tile = tile_of(a, 2);
-  return done(tile ? launch_gated_e4m3_few(a, tile, (cudaStream_t)stream) : launch_gated_e4m3_many(a, (cudaStream_t)stream),
+  return done(tile > 0 ? launch_gated_e4m3_few(a, tile, (cudaStream_t)stream) : launch_gated_e4m3_many(a, tile < 0, (cudaStream_t)stream),
               "tb_gated_e4m3");
 }
 
 // Test hooks: the form that later products of this process take (0: by the rule; 16, 32,
-// 64 or 128: k_e4m3_few with so many rows per tile; -1: k_e4m3_many), returning the
+// 64 or 128: k_e4m3_few with so many rows per tile; -1: k_e4m3_many; -2: the same with a
+// CTA to a tile), returning the
 // previous one; and the rule itself.
 TB_API int32_t tbx_e4m3_form(int32_t form) {
-  return g_form.exchange(form == 16 || form == 32 || form == 64 || form == 128 || form == -1 ? form : 0);
+  return g_form.exchange(form == 16 || form == 32 || form == 64 || form == 128 || form == -1 || form == -2 ? form : 0);
 }
 TB_API int32_t tbx_e4m3_few_tile(int32_t M, int32_t N, int32_t K, int32_t mats, int32_t light, int32_t sms) {
   return e4m3_few_tile(M, N, K, mats, light != 0, sms);

@@ -569,14 +569,17 @@ template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStrea
 
 }  // namespace
 
-// Rows of X per tile for M rows, or 0 where k_e4m3_many is the better one.
+// Rows of X per tile for M rows, or 0 where k_e4m3_many is the better one, -1 with a CTA
+// to a tile.
 //
 // Short K (up to 2048): a call is its fixed cost, which grows with the tile, so the smallest
 // tile whose tiles are all resident at once, two CTAs per SM; the largest, and gated ones,
 // only up to 128 rows, where half of k_e4m3_many's tile is empty, or for `light` results
 // (fp32 without a residual; gated ones not to codes); then 256 x 256 tiles.  Long K: the first tile whose tiles are
-// resident twice over, that is with K split in two or more; then 256 x 256 tiles, or up to
-// 64 gated rows one split less.  Measured, us, by rows per tile, and k_e4m3_many:
+// resident twice over, that is with K split in two or more; then 256 x 256 tiles.  (64 rows
+// of one matrix: one split less.)  Up to 128 rows, where the second CTA of a pair would have
+// none, a CTA to a tile once there are more tiles than pairs, which then are fewer rounds.
+// Measured, us, by rows per tile, and k_e4m3_many:
 //                                32     64    128   many
 //   K 768, N 2304:    512 rows   5.4    5.6    7.2    7.0      1024:  9.8   6.5   8.1   7.2
 //        1371: 14.3  10.6   8.6   7.9   (to fp32: 14.8  11.3   9.3   9.4; residual: - - 14.6  12.4)
@@ -591,7 +594,10 @@ template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStrea
 //   gated, K 1536, F 4096:   128   9.5  12.0    -    9.5        192: 10.5  12.5    -   9.5
 //   gated, K 2048, F 11008:   96  14.5  19.7    -   17.1
 //   gated, K 4096, F 2048:   256  13.1  14.4    -   14.5        333: 18.2  17.6    -  14.7
-//   gated, K 4096, F 14336:   64  28.6  25.6    -   28.1        128: 52.1  43.9    -  28.8
+//   gated, K 4096, F 14336:   64  29.1  25.2    -   27.1, a CTA to a tile 23.9
+//                            128  52.3  43.8    -   27.9                  23.7
+//   gated, K 4096, F 11008:  128  38.8  39.3    -   27.4                  21.0
+//   K 768, N 50304:          128    -   19.5  18.7  14.1                  12.9
 int e4m3_few_tile(int M, int N, int K, int mats, bool light, int sms) {
   const long long wtiles = ((long long)N + kBlk - 1) / kBlk, slots = 2LL * sms;
   auto fits = [&](int nt, int times) { return wtiles * (((long long)M + nt - 1) / nt) * times <= slots; };
@@ -607,7 +613,9 @@ int e4m3_few_tile(int M, int N, int K, int mats, bool light, int sms) {
   } else if (fits(32, 2)) {
     return 32;
   }
-  return M <= 64 ? 64 : 0;
+  if (M <= 64 && mats == 1) return 64;
+  const long long tiles = mats == 1 ? (wtiles + 1) / 2 : wtiles;        // 256 x 256
+  return M <= 128 && 2 * tiles > sms ? -1 : 0;
 }
 
 cudaError_t launch_gemm_e4m3_few(const GemmArgs& a, int tile, cudaStream_t s) {

@@ -1,4 +1,5 @@
-// The products of e4m3_gemm_few.cu for many rows: 256 x 256 tiles on CTA pairs.
+// The products of e4m3_gemm_few.cu for many rows: 256 x 256 tiles on CTA pairs, or, for up to
+// 128 rows, 128 x 256 on single CTAs.
 //
 // The clusters of two CTAs walk the tiles (persistent).  A CTA stages its own 128 rows
 // of X and 128 rows of W per K block of 128 (32 KB, six stages); the even CTA issues
@@ -6,6 +7,7 @@
 // one CTA stages rows of W1 and the other the same rows of W3, so that half of the
 // accumulator's columns are gates and half what they gate: one tile is one block of 128
 // columns of the result.  Accumulator 0 has the gates first and accumulator 1 last.
+// Or (CG 1) each CTA has tiles of its own, of 128 rows: all 256 rows of W, four stages.
 //   warp 0      TMA;
 //   warp 1      issues the instructions (even CTA);
 //   warps 2..9  epilogue, half a row of the tile per lane;
@@ -25,7 +27,8 @@
 // they had been stored to tensor memory by warps that first waited for a set's last
 // instruction (17.6 -> 13.2 us, gated 31.5 -> 27); eight epilogue warps for four (gated
 // 16384 x 2048 x 768 to fp32 59 -> 53 us); both for the smallest calls (gated 256 x 2048 x 768
-// 8.7 -> 7.3).
+// 8.7 -> 7.3).  Single CTAs: gated 128 x 14336 x 4096 29.1 -> 24.7, whose 112 tiles are one
+// round of 152 CTAs and two of 76 pairs.
 // Tried: operands in a branch on the lane instead of a converged warp (650 us for 569 at
 // that time); three more sets of scales by sharing 64 columns (672 for 650: the division
 // by five sat in the issuing warp); clusters of two pairs that multicast X (557 for 551:
@@ -44,9 +47,10 @@ using namespace ptx;
 constexpr int kSet = 4;          // K blocks per scale set
 constexpr int kRowsCta = 128;    // rows of X per CTA
 
-struct ManyCfg {
-  static constexpr int STAGES = 6;
-  static constexpr uint32_t A_BYTES = kRowsCta * kBlk, B_BYTES = 128 * kBlk, STAGE_BYTES = A_BYTES + B_BYTES;
+// CG: CTAs that share a tile.
+template <int CG> struct ManyCfg {
+  static constexpr int STAGES = CG == 2 ? 6 : 4;
+  static constexpr uint32_t A_BYTES = kRowsCta * kBlk, B_BYTES = (256 / CG) * kBlk, STAGE_BYTES = A_BYTES + B_BYTES;
   // two pieces of 32 rows x 64 bytes of y for each epilogue warp
   static constexpr uint32_t OFF_EPI = STAGES * STAGE_BYTES, PIECE = 32 * 64;
   // scale sets: a word of four scales for each of the CTA's rows of X, row 32 c + l at 16 l + 4 c,
@@ -73,12 +77,12 @@ __device__ __forceinline__ void place(int tile, int m_units, int n_tiles, int gr
 }
 
 // ESIZE: bytes of an element of y.
-template <bool GATED, int ESIZE>
-__global__ void __launch_bounds__(ManyCfg::THREADS, 1)
+template <int CG, bool GATED, int ESIZE>
+__global__ void __launch_bounds__(ManyCfg<CG>::THREADS, 1)
     k_e4m3_many(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                 const __grid_constant__ CUtensorMap tmW3, const __grid_constant__ CUtensorMap tmY,
                 const __grid_constant__ CUtensorMap tmRes, GemmArgs a, int m_units, int n_tiles, int group, int stream, int* err) {
-  using C = ManyCfg;
+  using C = ManyCfg<CG>;
   constexpr int STAGES = C::STAGES;
   constexpr int COLS = GATED ? 128 : 256;               // columns of y per tile
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -105,8 +109,8 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = m_units * n_tiles;
   const int kblocks = (a.K + kBlk - 1) / kBlk, nsets = (kblocks + kSet - 1) / kSet;
-  const uint32_t rank = cluster_ctarank();
-  const int tile0 = (int)cluster_id_x(), tstep = (int)nclusters_x();
+  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;
+  const int tile0 = CG == 2 ? (int)cluster_id_x() : (int)blockIdx.x, tstep = CG == 2 ? (int)nclusters_x() : (int)gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -114,13 +118,13 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sfull[s], 8);        // four warps of each CTA, on the even CTA's
+      mbar_init(&sfull[s], 4 * CG);   // four warps of each CTA, on the even CTA's
       mbar_init(&sempty[s], 1);
       mbar_init(&sdone[s], 1);
       mbar_init(&tfull[s], 1);
-      mbar_init(&tempty[s], 16);      // eight epilogue warps
+      mbar_init(&tempty[s], 8 * CG);  // eight epilogue warps
     }
-    mbar_init(shared_free, 8);
+    mbar_init(shared_free, 4 * CG);
     for (int i = 0; i < 16; ++i) mbar_init(&rfull[i], 1);
     for (int i = 0; i < 4; ++i) mbar_init(&efull[i], 2);
     mbar_init(drain, 1);
@@ -133,15 +137,24 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
   }
   // both CTAs' barriers exist before either CTA's copies or commits reach them
   __syncthreads();
-  cluster_sync();
+  if (CG == 2) cluster_sync();
   if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, 512);
-    tmem_relinquish_pair();
+    if constexpr (CG == 2) {
+      tmem_alloc_pair(tmem_slot, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  auto commit = [](uint32_t bar, uint32_t elected) {
+    if constexpr (CG == 2) mma_commit_pair_elected(bar, elected);
+    else mma_commit_elected(bar, elected);
+  };
 
   if (warp == 0) {
     // (the whole warp, its elected lane issuing)
@@ -149,16 +162,17 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
     const uint32_t elected = elect_one();
     const uint64_t first = policy_evict_first();
     const uint32_t ring = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
-    const uint32_t even0 = mapa_shared(full0, 0);      // a pair's bytes complete on its even CTA's barriers
+    const uint32_t even0 = CG == 2 ? mapa_shared(full0, 0) : full0;    // a pair's bytes complete on its even CTA's barriers
     uint32_t stage = 0, phase = 0;
     int issued = 0;
     uint32_t acc = 0;
     bool ok = true;
     for (int tile = tile0; ok && tile < tiles; tile += tstep, acc ^= 1) {
-      const CUtensorMap* tw = GATED && rank != acc ? &tmW3 : &tmW;
+      // the first 128 rows of B, of a pair those of this CTA; the others of a single CTA
+      const CUtensorMap *tw = GATED && rank != acc ? &tmW3 : &tmW, *tw2 = GATED && !acc ? &tmW3 : &tmW;
       int mu, nt;
       place(tile, m_units, n_tiles, group, mu, nt);
-      const int xrow = (mu * 2 + (int)rank) * kRowsCta;       // a block past M reads zeros
+      const int xrow = (mu * CG + (int)rank) * kRowsCta;      // a block past M reads zeros
       const int wrow = GATED ? nt * 128 : nt * 256 + (int)rank * 128;
 #pragma unroll 1
       for (int kb = 0; kb < kblocks; ++kb) {
@@ -166,10 +180,12 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
             !(ok = mbar_wait_warp(&empty[stage], phase ^ 1u, abort_flag, err)))
           break;
         const uint32_t sa = ring + stage * C::STAGE_BYTES, bar = even0 + stage * 8;
-        if (rank == 0) mbar_expect_elected(full0 + stage * 8, 2 * C::STAGE_BYTES, elected);
-        if (stream) tma_load_3d_elected<2>(&tmX, sa, bar, kb * kBlk, xrow, 0, first, elected);
-        else tma_load_3d_elected<2>(&tmX, sa, bar, kb * kBlk, xrow, 0, elected);
-        tma_load_3d_elected<2>(tw, sa + C::A_BYTES, bar, kb * kBlk, wrow, 0, elected);
+        if (rank == 0) mbar_expect_elected(full0 + stage * 8, CG * C::STAGE_BYTES, elected);
+        if (stream) tma_load_3d_elected<CG>(&tmX, sa, bar, kb * kBlk, xrow, 0, first, elected);
+        else tma_load_3d_elected<CG>(&tmX, sa, bar, kb * kBlk, xrow, 0, elected);
+        tma_load_3d_elected<CG>(tw, sa + C::A_BYTES, bar, kb * kBlk, wrow, 0, elected);
+        if constexpr (CG == 1)
+          tma_load_3d_elected<CG>(tw2, sa + C::A_BYTES + 128 * kBlk, bar, kb * kBlk, GATED ? wrow : wrow + 128, 0, elected);
         if (issued < STAGES) ++issued;
         if (++stage == STAGES) stage = 0, phase ^= 1u;
       }
@@ -206,10 +222,10 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
           // one's instructions run
           if (!(ok = mbar_wait_warp(&sdone[sb], ((set >> 1) & 1) ^ 1u, abort_flag, err))) break;
           const uint32_t at = smem_u32(smem) + C::OFF_SF + sb * C::SF_BYTES;
-          tmem_copy_pair_elected(sf, desc_rows16(at, 128), elected);
-          tmem_copy_pair_elected(sf + 4, desc_rows16(at + C::SF_W, 0), elected);
-          tmem_copy_pair_elected(sf + 8, desc_rows16(at + C::SF_W + 128, 0), elected);
-          mma_commit_pair_elected(smem_u32(&sempty[sb]), elected);
+          tmem_copy_elected<CG>(sf, desc_rows16(at, 128), elected);
+          tmem_copy_elected<CG>(sf + 4, desc_rows16(at + C::SF_W, 0), elected);
+          tmem_copy_elected<CG>(sf + 8, desc_rows16(at + C::SF_W + 128, 0), elected);
+          commit(smem_u32(&sempty[sb]), elected);
           // (after the scales: the tile before holds the shared columns up a little longer)
           if (kb == 0 && local && !(ok = mbar_wait_warp(shared_free, (local - 1) & 1, abort_flag, err))) break;
 #pragma unroll
@@ -220,18 +236,18 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
                 break;
               tc_fence_after();
               const uint32_t lo = desc0 + stage * NEXT;
-              mma_mx_k128<2>(d, lo, lo + (C::A_BYTES >> 4), desc_hi, idesc_mx_e4m3(2 * kRowsCta, 256, b), sf, sf + 4,
+              mma_mx_k128<CG>(d, lo, lo + (C::A_BYTES >> 4), desc_hi, idesc_mx_e4m3(CG * kRowsCta, 256, b), sf, sf + 4,
                            kb + b != 0, elected);
-              mma_commit_pair_elected(empty0 + stage * 8, elected);      // frees the stage in both CTAs
+              commit(empty0 + stage * 8, elected);      // frees the stage in both CTAs
               if (++stage == STAGES) stage = 0, phase ^= 1u;
             }
           }
-          mma_commit_pair_elected(smem_u32(&sdone[sb]), elected);
+          commit(smem_u32(&sdone[sb]), elected);
         }
-        if (ok) mma_commit_pair_elected(smem_u32(&tfull[acc]), elected);
+        if (ok) commit(smem_u32(&tfull[acc]), elected);
       }
       // all of them must be done before tensor memory is released
-      mma_commit_pair_elected(smem_u32(drain), elected);
+      commit(smem_u32(drain), elected);
       volatile int no_abort = 0;
       mbar_wait_warp(drain, 0, &no_abort, err);
     }
@@ -249,7 +265,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
       int mu, nt;
       place(tile, m_units, n_tiles, group, mu, nt);
       const int kb = s * kSet, n = min(kSet, kblocks - kb);
-      const int m = (mu * 2 + (int)rank) * kRowsCta + c * 32 + lane, b = GATED ? nt : 2 * nt + c;
+      const int m = (mu * CG + (int)rank) * kRowsCta + c * 32 + lane, b = GATED ? nt : 2 * nt + c;
       x = m < a.M ? scale_word(a.x.scale + (size_t)m * kblocks + kb, n) : 0x7f7f7f7fu;
       if (c < 2) w = b < nb ? scale_word((GATED && c != acc ? a.w3.scale : a.w.scale) + (size_t)b * kblocks + kb, n) : 0x7f7f7f7fu;
     };
@@ -292,7 +308,7 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
     auto corner = [&](int tile) {
       int mu, nt;
       place(tile, m_units, n_tiles, group, mu, nt);
-      return make_int2((mu * 2 + (int)rank) * kRowsCta + quad * 32, nt * COLS + half * (COLS / 2));
+      return make_int2((mu * CG + (int)rank) * kRowsCta + quad * 32, nt * COLS + half * (COLS / 2));
     };
     uint32_t n = 0, rphase = 0;        // pieces so far; bit b: the parity of buffer b's next residual
     auto request = [&](int row, int col, uint32_t b) {
@@ -498,15 +514,16 @@ __global__ void __launch_bounds__(ManyCfg::THREADS, 1)
   // either CTA releases the pair's tensor memory.
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  if (CG == 2) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    if constexpr (CG == 2) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
   }
 }
 
-template <bool GATED, int ESIZE> cudaError_t go(const GemmArgs& a, cudaStream_t s) {
-  using C = ManyCfg;
+template <int CG, bool GATED, int ESIZE> cudaError_t go(const GemmArgs& a, cudaStream_t s) {
+  using C = ManyCfg<CG>;
   CUtensorMap tx, tw, tw3, ty, tr;
   cudaError_t e = make_tmap_rows(&tx, 1, a.x.codes, 1, (uint64_t)a.M, (uint64_t)a.K, kBlk, kRowsCta);
   if (e != cudaSuccess) return e;
@@ -522,7 +539,7 @@ template <bool GATED, int ESIZE> cudaError_t go(const GemmArgs& a, cudaStream_t 
   if (a.res && (e = make_tmap_rows(&tr, 1, a.res, 1, (uint64_t)a.M, row_bytes, 64, 32)) != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = CG;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -537,17 +554,17 @@ template <bool GATED, int ESIZE> cudaError_t go(const GemmArgs& a, cudaStream_t 
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!clusters[dev]) {
-    e = cudaFuncSetAttribute(k_e4m3_many<GATED, ESIZE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    e = cudaFuncSetAttribute(k_e4m3_many<CG, GATED, ESIZE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;
     int n = 0;
-    cfg.gridDim = dim3(2 * (sm_count() / 2));
+    cfg.gridDim = dim3(CG * (sm_count() / CG));
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&n, k_e4m3_many<GATED, ESIZE>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, k_e4m3_many<CG, GATED, ESIZE>, &cfg);
     if (e != cudaSuccess) return e;
     if (n <= 0) return cudaErrorNotSupported;
     clusters[dev] = n;
   }
-  const int m_units = (int)((a.M + 2LL * kRowsCta - 1) / (2 * kRowsCta));
+  const int m_units = (int)((a.M + 1LL * CG * kRowsCta - 1) / (CG * kRowsCta));
   const int n_tiles = GATED ? (a.N + 127) / 128 : (a.N + 255) / 256;
   const long long tiles = (long long)m_units * n_tiles;
   if (tiles > 0x7fffffffLL / 2) return cudaErrorInvalidValue;
@@ -562,18 +579,20 @@ template <bool GATED, int ESIZE> cudaError_t go(const GemmArgs& a, cudaStream_t 
   // out (16384 x 4096 x 14336 with the residual 539 -> 533 us, after seconds of load 632 ->
   // 619; X alone changes nothing.  In groups, where X is read again, 602 -> 711).
   const int stream = group == 0 && n_tiles <= clusters[dev] && (size_t)a.M * a.N * ESIZE > (size_t(64) << 20);
-  cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(tiles, clusters[dev]));
+  cfg.gridDim = dim3(CG * (unsigned)std::min<long long>(tiles, clusters[dev]));
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_e4m3_many<GATED, ESIZE>, tx, tw, tw3, ty, tr, a, m_units, n_tiles, group, stream, device_error_word());
+  return cudaLaunchKernelEx(&cfg, k_e4m3_many<CG, GATED, ESIZE>, tx, tw, tw3, ty, tr, a, m_units, n_tiles, group, stream, device_error_word());
 }
 
 }  // namespace
 
-cudaError_t launch_gemm_e4m3_many(const GemmArgs& a, cudaStream_t s) {
-  return a.y_dtype == TB_F32 ? go<false, 4>(a, s) : go<false, 2>(a, s);
+cudaError_t launch_gemm_e4m3_many(const GemmArgs& a, bool one, cudaStream_t s) {
+  if (one) return a.y_dtype == TB_F32 ? go<1, false, 4>(a, s) : go<1, false, 2>(a, s);
+  return a.y_dtype == TB_F32 ? go<2, false, 4>(a, s) : go<2, false, 2>(a, s);
 }
-cudaError_t launch_gated_e4m3_many(const GemmArgs& a, cudaStream_t s) {
-  return a.y_dtype == TB_E4M3 ? go<true, 1>(a, s) : a.y_dtype == TB_F32 ? go<true, 4>(a, s) : go<true, 2>(a, s);
+cudaError_t launch_gated_e4m3_many(const GemmArgs& a, bool one, cudaStream_t s) {
+  if (one) return a.y_dtype == TB_E4M3 ? go<1, true, 1>(a, s) : a.y_dtype == TB_F32 ? go<1, true, 4>(a, s) : go<1, true, 2>(a, s);
+  return a.y_dtype == TB_E4M3 ? go<2, true, 1>(a, s) : a.y_dtype == TB_F32 ? go<2, true, 4>(a, s) : go<2, true, 2>(a, s);
 }
 
 }  // namespace tb

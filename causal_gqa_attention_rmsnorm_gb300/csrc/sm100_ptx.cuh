@@ -717,14 +717,22 @@ __device__ __forceinline__ uint64_t desc_rows16(uint32_t saddr, uint32_t stride)
 }
 
 // Four columns of tensor memory, lanes 0..31 and the same in 32..63 and so on, from 32 rows
-// of 16 bytes of shared memory, in both CTAs of a pair from their own.  Instructions that the
-// same thread issues after it see them.  By the elected lane.
-__device__ __forceinline__ void tmem_copy_pair_elected(uint32_t taddr, uint64_t desc, uint32_t elected) {
-  asm volatile(
-      "{\n\t.reg .pred pe;\n\tsetp.ne.b32 pe, %2, 0;\n\t"
-      "@pe tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
-      "l"(desc), "r"(elected)
-      : "memory");
+// of 16 bytes of shared memory; of a pair (CG 2) in both CTAs, from their own.  Instructions
+// that the same thread issues after it see them.  By the elected lane.
+template <int CG> __device__ __forceinline__ void tmem_copy_elected(uint32_t taddr, uint64_t desc, uint32_t elected) {
+  if constexpr (CG == 2) {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\tsetp.ne.b32 pe, %2, 0;\n\t"
+        "@pe tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(desc), "r"(elected)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\tsetp.ne.b32 pe, %2, 0;\n\t"
+        "@pe tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(desc), "r"(elected)
+        : "memory");
+  }
 }
 
 // What a producer warp does, by its elected lane, for the reason given at mma_mx_k128 (a

@@ -137,7 +137,8 @@ def test_empty_calls_need_no_pointers(lib):
     (129, 20000, 768, 1, 0, 0), (1371, 2304, 1536, 1, 1, 128), (1371, 2304, 1536, 1, 0, 0),
     (2049, 2304, 768, 1, 1, 0), (256, 4096, 4096, 1, 0, 64), (257, 4096, 4096, 1, 0, 128), (512, 4096, 4096, 1, 0, 128),
     (513, 4096, 4096, 1, 0, 0), (64, 14336, 4096, 1, 0, 64), (128, 14336, 4096, 1, 0, 128), (129, 14336, 4096, 1, 0, 0),
-    (32, 14336, 4096, 2, 0, 32), (64, 14336, 4096, 2, 0, 64), (65, 14336, 4096, 2, 0, 0), (128, 2048, 768, 2, 0, 32), (129, 2048, 768, 2, 0, 0), (333, 2048, 768, 2, 1, 32), (96, 11008, 2048, 2, 0, 32),
+    (32, 14336, 4096, 2, 0, 32), (64, 14336, 4096, 2, 0, -1), (128, 14336, 4096, 2, 0, -1), (129, 14336, 4096, 2, 0, 0),
+    (64, 8192, 4096, 2, 0, 32), (65, 8192, 4096, 2, 0, 0), (128, 50304, 768, 1, 0, -1), (129, 50304, 768, 1, 0, 0), (64, 50304, 768, 1, 0, 64), (128, 2048, 768, 2, 0, 32), (129, 2048, 768, 2, 0, 0), (333, 2048, 768, 2, 1, 32), (96, 11008, 2048, 2, 0, 32),
     (1024, 2048, 768, 2, 0, 0), (128, 4096, 1536, 2, 0, 32), (192, 4096, 1536, 2, 0, 0), (256, 2048, 4096, 2, 0, 32), (333, 2048, 4096, 2, 0, 0),
     (2 ** 31 - 1024, 16, 16, 1, 0, 0), (2 ** 31 - 1024, 16, 16, 2, 1, 0), (64, 2 ** 28, 16, 1, 0, 64)])
 def test_tile_rule(lib, M, N, K, mats, light, tile):

@@ -279,7 +279,7 @@ def test_gemm_nan_stays_in_its_row_and_its_column():
     assert torch.equal(y[~hit], clean[~hit])
 
 
-@pytest.mark.parametrize("tile", [16, 64, 128, -1])
+@pytest.mark.parametrize("tile", [16, 64, 128, -1, -2])
 def test_gemm_far_scales(form, tile):
     """Scales whose product leaves fp32: infinity above, 0 (or a subnormal) below, and
     zeros stay zeros under any scale."""
@@ -340,7 +340,7 @@ def test_gated(M, F, K, out_dtype):
         assert (np.abs(f64(y) - exact) <= off + 2 * HALF[out_dtype] * (np.abs(exact) + off)).all()
 
 
-@pytest.mark.parametrize("tile,M", [(16, 3), (32, 30), (64, 70), (-1, 200)])
+@pytest.mark.parametrize("tile,M", [(16, 3), (32, 30), (64, 70), (-1, 200), (-2, 200)])
 def test_gated_infinities_and_nan_become_nan_codes(form, tile, M):
     """Results beyond fp32 and NaN are NaN codes, and the scale is that of the others."""
     form(tile)
@@ -372,7 +372,7 @@ def test_gated_gates_far_below_zero():
     one = torch.full((M, 1), 127, dtype=torch.uint8).view(SCALE).cuda()
     big = torch.full((1, 1), 131, dtype=torch.uint8).view(SCALE).cuda()
     unit = torch.full((1, 1), 127, dtype=torch.uint8).view(SCALE).cuda()
-    for form in (16, 64, -1):
+    for form in (16, 64, -1, -2):
         tbx_e4m3_form(form)
         y = tb.tb_gated_e4m3(tb.E4M3Rows(x.view(CODE).cuda(), one), tb.E4M3Weight(w1.view(CODE).cuda(), big),
                              tb.E4M3Weight(w3.view(CODE).cuda(), unit), out_dtype=tb.TB_F32)
@@ -461,10 +461,11 @@ MANY = [(1, 16, 16), (128, 256, 128), (129, 272, 144), (256, 512, 512), (300, 11
         (1371, 2304, 768), (700, 8192, 400), (5000, 1040, 272), (260, 256, 9216)]
 
 
+@pytest.mark.parametrize("tile", [-1, -2])
 @pytest.mark.parametrize("M,N,K", MANY)
-@pytest.mark.parametrize("dtype,with_res", [(F32, False), (BF16, True), (F32, True)])
-def test_gemm_many(form, M, N, K, dtype, with_res):
-    form(-1)
+@pytest.mark.parametrize("dtype,with_res", [(F32, False), (BF16, False), (BF16, True), (F32, True)])
+def test_gemm_many(form, tile, M, N, K, dtype, with_res):
+    form(tile)
     g = gen(M + N + K)
     x, w = make_rows(tb, M, K, g), make_weight(tb, N, K, g)
     res = (torch.randn(M, N, generator=g) * 100).to(dtype).cuda() if with_res else None
@@ -478,9 +479,10 @@ def test_gemm_many(form, M, N, K, dtype, with_res):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_gemm_many_past_l2(form, dtype):
+@pytest.mark.parametrize("tile", [-1, -2])
+def test_gemm_many_past_l2(form, tile, dtype):
     """Results too large to stay in L2 take their own cache hints."""
-    form(-1)
+    form(tile)
     g = gen(6)
     M, N, K = 9001, 4112, 144
     x, w = make_rows(tb, M, K, g), make_weight(tb, N, K, g)
@@ -494,8 +496,9 @@ def test_gemm_many_past_l2(form, dtype):
 @pytest.mark.parametrize("M,F,K", [(1, 16, 16), (129, 144, 400), (333, 2048, 768), (300, 272, 2064), (1000, 1040, 528),
                                    (2100, 1296, 272)])
 @pytest.mark.parametrize("out_dtype", ["codes", BF16, F32])
-def test_gated_many(form, M, F, K, out_dtype):
-    form(-1)
+@pytest.mark.parametrize("tile", [-1, -2])
+def test_gated_many(form, tile, M, F, K, out_dtype):
+    form(tile)
     g = gen(M + F + K)
     x, w1, w3 = make_rows(tb, M, K, g), make_weight(tb, F, K, g), make_weight(tb, F, K, g)
     w1.scale.view(torch.uint8).sub_(int(np.log2(K) / 2) + 11)
@@ -523,7 +526,7 @@ def test_both_kernels_agree_on_what_nan_reaches(form):
     w.codes.view(torch.uint8)[5, 527] = 0xFF
     w.scale.view(torch.uint8)[2, 1] = 255
     got = []
-    for f in (16, 32, 64, 128, -1):
+    for f in (16, 32, 64, 128, -1, -2):
         form(f)
         got.append(torch.isnan(tb.tb_gemm_e4m3(x, w)))
     no_error()
@@ -552,7 +555,7 @@ def test_rows_beyond_2_31_values():
     assert (np.abs(f64(r[-4:]) - total) <= 2 * HALF[BF16] * np.abs(total) + 2.0 ** -23 * np.abs(total)).all()
 
 
-@pytest.mark.parametrize("tile", [64, -1])
+@pytest.mark.parametrize("tile", [64, -1, -2])
 def test_products_beyond_2_31_values(form, tile):
     form(tile)
     g = gen(4)
