@@ -455,6 +455,7 @@ __global__ void __launch_bounds__(192, CPS)
       if (ok) {
 #pragma unroll
         for (int i = 0; i < NT; i += P) {
+          if (i >= rows) break;
           float u[MATS][P];
 #pragma unroll
           for (int m = 0; m < MATS; ++m)

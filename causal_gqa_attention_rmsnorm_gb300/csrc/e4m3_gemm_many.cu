@@ -19,8 +19,8 @@
 // finished; the next tile's instructions wait for that (and not for the rest).
 //
 // Measured in a stream of calls: 16384 x 4096 x 14336 with the residual 535-550 us (3500-3590
-// TFLOP/s, 0.91-0.93 of twice cuBLAS's bf16 rate), gated 8192 x 14336 x 4096 500-505 us
-// (3820); the power limit sets both (over seconds near 3000 at 1.4 to 1.6 GHz).  Short K:
+// TFLOP/s, 0.91-0.93 of twice cuBLAS's bf16 rate), gated 8192 x 14336 x 4096 500-515 us
+// (3740-3850); the power limit sets both (over seconds near 3000 at 1.4 to 1.6 GHz).  Short K:
 // 16384 x 768 x 768 13.1 us, gated 8192 x 2048 x 768 21.6 (a tile's instructions take 3100 cycles
 // there, its change 1200; without SiLU, stores and the exponents' exchange 19.8).
 // What short K gained: scales through shared memory and the issuing warp's copies, where
