@@ -56,9 +56,11 @@ __device__ __forceinline__ void store8(bf16* p, const float (&v)[8]) {
 
 // The codes of a thread's P eights y = v·s·g of a block that 16/P neighbouring lanes hold
 // (columns c + 128/P·p on, those below d); the first of the lanes also stores the scale.
-// v·g comes first, so that the row's s and the block's 2^-e are one factor: s·2^-e is exact,
-// and the largest |v·g|·s is the largest |v·g·s| (rounding keeps the order).  False if the
-// largest |v·g|·s is no finite number: put_wild then writes the block again.  A NaN is passed
+// v·g comes first, so that the row's s and the block's 2^-e are one factor: s·2^-e is exact
+// (for s below 2^28, as e is -100 or more), and the largest |v·g|·s is the largest |v·g·s|
+// (rounding keeps the order).  False if the largest |v·g|·s is no finite number, or if s is
+// 2^28 or more, where s·2^-e may be infinite (zeros would become NaN) and v·g below fp32's
+// normal numbers where v·s·g is not: put_wild then writes the block again.  A NaN is passed
 // over by the maximum and kept by the conversion.
 template <typename T, bool NORM, int P>
 __device__ __forceinline__ bool put_block(const float (&v)[P][8], float s, const Eight<T> (&g)[P], int c, int d, uint8_t* codes,
@@ -83,11 +85,12 @@ __device__ __forceinline__ bool put_block(const float (&v)[P][8], float s, const
           make_uint2(codes_of4(t[p][0] * f, t[p][1] * f, t[p][2] * f, t[p][3] * f),
                      codes_of4(t[p][4] * f, t[p][5] * f, t[p][6] * f, t[p][7] * f));
   if (threadIdx.x % (16 / P) == 0 && c < d) scale[c / kBlk] = (uint8_t)(e + 127);
-  return top < INFINITY;
+  return top < INFINITY && s < 0x1p28f;
 }
 
 // The same of a block with an infinity in it, with v·g beyond fp32 where v·s·g is not, or of
-// a row without a finite s: in the order v·s·g, infinities told from values one by one, and
+// a row whose s is 2^28 or more (its mean square + eps below 2^-56: rows of 3.7e-9, or zeros,
+// with an eps of next to nothing) or no finite number: in the order v·s·g, infinities told from values one by one, and
 // from memory once more, so that put_block need not keep its values.  By whole warps (the
 // shuffles); `mine`: whether this thread's block is one.
 template <typename T, typename RT, bool NORM, int P>

@@ -438,7 +438,8 @@ typedef struct {
  *  r, h  : NULL, or both given: r dense [rows, cols] of r_dtype, h receives the sum in
  *          dtype.  h may be x itself, or r itself where the types agree.  The norm takes
  *          the fp32 sum, before h's rounding; its mean square is fp32 too (a row above
- *          1e19 / sqrt(cols) may have an infinite one, which gives zeros).
+ *          1e19 / sqrt(cols) may have an infinite one, which gives zeros; of values below
+ *          1e-19 the squares lose bits, which shows where eps is smaller still).
  *  g     : device [cols] of dtype.
  *  out   : rows; at most 32768 columns (TB_ERR_UNSUPPORTED above).
  * Pointers 16-byte aligned; but for h, what is written overlaps nothing that is read. */
