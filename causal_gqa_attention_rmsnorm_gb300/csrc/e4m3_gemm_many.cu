@@ -9,7 +9,7 @@
 // columns of the result.  Accumulator 0 has the gates first and accumulator 1 last.
 // Or (CG 1) each CTA has tiles of its own, of 128 rows: all 256 rows of W, four stages.
 //   warp 0      TMA;
-//   warp 1      issues the instructions (even CTA);
+//   warp 1      issues the instructions (even CTA), or tells that CTA of scales (odd CTA);
 //   warps 2..9  epilogue, half a row of the tile per lane;
 //   warps 10..13  put the scales of four K blocks at a time into shared memory, from where
 //               the issuing warp has them copied to tensor memory.
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(ManyCfg<CG>::THREADS, 1)
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sfull[s], 4 * CG);   // four warps of each CTA, on the even CTA's
+      mbar_init(&sfull[s], CG == 2 && rank == 0 ? 5 : 4);   // this CTA's four warps, and the odd CTA's warp 1
       mbar_init(&sempty[s], 1);
       mbar_init(&sdone[s], 1);
       mbar_init(&tfull[s], 1);
@@ -250,6 +250,20 @@ __global__ void __launch_bounds__(ManyCfg<CG>::THREADS, 1)
       commit(smem_u32(drain), elected);
       volatile int no_abort = 0;
       mbar_wait_warp(drain, 0, &no_abort, err);
+    } else {
+      // The issuing warp has this CTA's scales copied too, from this CTA's shared memory: what
+      // the scale warps wrote and this one has seen is released to it at cluster scope.  (By
+      // the scale warps themselves, who have loads on their way: 16384 x 768 x 768 16.7 us
+      // for 13.2.)
+      const uint32_t even[2] = {mapa_shared(smem_u32(&sfull[0]), 0), mapa_shared(smem_u32(&sfull[1]), 0)};
+      bool ok = true;
+      int set = 0;
+      for (int tile = tile0; ok && tile < tiles; tile += tstep) {
+        for (int s = 0; s < nsets; ++s, ++set) {
+          if (!(ok = mbar_wait_warp(&sfull[set & 1], (set >> 1) & 1, abort_flag, err))) break;
+          if (lane == 0) mbar_arrive_release_cluster(even[set & 1]);
+        }
+      }
     }
   } else if (warp >= 10) {
     // Scales: a word for a row of X per lane, and of two warps one for a half of W.  Those of
@@ -269,7 +283,6 @@ __global__ void __launch_bounds__(ManyCfg<CG>::THREADS, 1)
       x = m < a.M ? scale_word(a.x.scale + (size_t)m * kblocks + kb, n) : 0x7f7f7f7fu;
       if (c < 2) w = b < nb ? scale_word((GATED && c != acc ? a.w3.scale : a.w.scale) + (size_t)b * kblocks + kb, n) : 0x7f7f7f7fu;
     };
-    const uint32_t sfull_cl[2] = {mapa_shared(smem_u32(&sfull[0]), 0), mapa_shared(smem_u32(&sfull[1]), 0)};
     bool more = tile < tiles;
     if (more) load();
     for (; more; ++set) {
@@ -279,10 +292,7 @@ __global__ void __launch_bounds__(ManyCfg<CG>::THREADS, 1)
       if (c < 2) *reinterpret_cast<uint32_t*>(to + C::SF_W + 128 * c + 4 * lane) = w;
       fence_proxy_async();
       __syncwarp();
-      // (What is published was written into this CTA's own shared memory, is visible to the
-      // copies there since the fence, and is read by them only.  A release at cluster scope
-      // would wait for more: 16384 x 768 x 768 16.7 us for 13.2.)
-      if (lane == 0) mbar_arrive_cluster(sfull_cl[set & 1]);
+      if (lane == 0) mbar_arrive(&sfull[set & 1]);
       if (++s == nsets) s = 0, tile += tstep, acc ^= 1;
       more = tile < tiles;
       if (more) load();
