@@ -234,7 +234,10 @@ template <typename T> __global__ void __launch_bounds__(256) k_pack_e4m3(const T
   extern __shared__ float tile[];      // [128][129]
   __shared__ float tops[8];
   const int k0 = blockIdx.x * kBlk;
-  for (int n0 = blockIdx.y * kBlk; n0 < N; n0 += gridDim.y * kBlk) {
+  // (blocks are counted, not columns of w: these and the grid's step go beyond 31 bits together)
+  const int blocks = (N + kBlk - 1) / kBlk;
+  for (int nb = blockIdx.y; nb < blocks; nb += gridDim.y) {
+    const int n0 = nb * kBlk;
     float top = 0.f;
     for (int i = threadIdx.x; i < kBlk * kBlk; i += 256) {
       const int k = i / kBlk, n = i % kBlk;
@@ -250,7 +253,7 @@ template <typename T> __global__ void __launch_bounds__(256) k_pack_e4m3(const T
     for (int i = 0; i < 8; ++i) top = fmaxf(top, tops[i]);
     const int e = block_exponent(top);
     const float inv = pow2i(-e);
-    if (threadIdx.x == 0) scale[(size_t)(n0 / kBlk) * gridDim.x + blockIdx.x] = (uint8_t)(e + 127);
+    if (threadIdx.x == 0) scale[(size_t)nb * gridDim.x + blockIdx.x] = (uint8_t)(e + 127);
     for (int i = threadIdx.x; i < kBlk * (kBlk / 4); i += 256) {
       const int n = i / (kBlk / 4), k = i % (kBlk / 4) * 4;
       if (n0 + n < N && k0 + k < K)    // (K is a multiple of 16)

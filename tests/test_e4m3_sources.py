@@ -20,3 +20,11 @@ def test_what_a_cta_writes_is_released_to_the_other_cta_at_cluster_scope():
     assert {barriers[name] for name in re.findall(r"mbar_arrive_release_cluster\((\w+)", text)} == {"sfull"}
     assert re.findall(r"mbar_wait\w*\(&sfull\[sb\]", text) == ["mbar_wait_cluster_warp(&sfull[sb]"]
     assert "mbarrier.arrive.release.cluster.shared::cluster.b64" in source("sm100_ptx.cuh")
+
+
+def test_packing_walks_blocks_of_columns():
+    """Up to 2^31 - 1024 columns in steps of up to 65535 blocks of 128: a column's number
+    would pass 31 bits on its way past the last one, a block's does not."""
+    start, bound, step = re.search(r"for \(int (\w+) = blockIdx\.y; \1 < (\w+); \1 \+= ([^)]+)\)", source("e4m3_rows.cu")).groups()
+    assert (start, bound, step) == ("nb", "blocks", "gridDim.y")
+    assert (2 ** 31 - 1024 + 127) // 128 + 65535 < 2 ** 31 <= 2 ** 31 - 1024 + 65535 * 128

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import causal_gqa_attention_rmsnorm_gb300 as tb
-from e4m3_helpers import BF16, F32, bytes_of, check_rows
+from e4m3_helpers import BF16, CODE, F32, SCALE, bytes_of, check_rows
 from oracle import e4m3 as ref
 from test_gpu_e4m3_ops import MANY_ROWS, NORM_OFF, f64, gen, no_error
 
@@ -50,3 +50,32 @@ def test_norm_of_rows_near_zero(M, d, dtype, r_dtype, eps):
     assert np.isfinite(y).all()
     # v·g may round below fp32's normal numbers, by 2^-150, before an s of less than 2^28
     check_rows(bytes_of(out.codes), bytes_of(out.scale), y, NORM_OFF * np.abs(y) + 2.0 ** -122)
+
+
+# ---- the largest counts -------------------------------------------------------------
+
+def test_pack_of_the_most_columns():
+    """Columns counted past 31 bits on the way: the first and the last of each step of the
+    grid, and zeros everywhere else."""
+    K, N = 16, 2 ** 31 - 1024
+    w = torch.zeros(K, N, dtype=BF16, device="cuda")
+    step = 65535 * 128
+    places = sorted({0, 127, 128, step - 1, step, 100 * step + 3, 255 * step, 256 * step - 128, 256 * step, N - 129, N - 1})
+    places = [p for p in places if p < N]
+    v = torch.randn(K, len(places), generator=gen(1)).to(BF16).cuda()
+    for i, p in enumerate(places):
+        w[:, p] = v[:, i]
+    codes = torch.full((N, K), 9, dtype=torch.uint8, device="cuda")
+    scale = torch.full((-(-N // 128), 1), 9, dtype=torch.uint8, device="cuda")
+    tb.tb_pack_e4m3(w, out=tb.E4M3Weight(codes.view(CODE), scale.view(SCALE)))
+    no_error()
+    e = np.array([ref.exponent(f64(w[:, p // 128 * 128:p // 128 * 128 + 128])) for p in places])
+    assert (scale.cpu().numpy()[[p // 128 for p in places], 0].astype(int) - 127 == e).all()
+    for i, p in enumerate(places):
+        q = f64(v[:, i]) / 2.0 ** e[i]
+        assert (np.abs(ref.VALUES[codes[p].cpu().numpy()] - q) <= ref.half_step(q)).all()
+        codes[p] = 0
+        scale[p // 128] = 27
+    assert (scale == 27).all()
+    for i in range(0, N, 2 ** 27):
+        assert not codes[i:i + 2 ** 27].any()
