@@ -300,6 +300,13 @@ int skinny_max_tokens();
 // K ranges per weight tile (the cluster size) for `tiles` 128-row weight tiles
 // of `kblocks` K blocks over `slots` resident CTAs (-1 for a non-positive argument)
 int skinny_split_count(int tiles, int kblocks, int slots);
+// Tensor memory is handed out by an allocation that waits, without a limit, for what other
+// CTAs of the SM hold; and the CTAs of a cluster wait for one another.  So that no two calls
+// (of two streams, say) can each hold what the other waits for, CTAs of clusters that together
+// find room on an SM find tensor memory there too.  What a CTA of k_gemm_skinny takes of
+// either, for the others to reckon with:
+constexpr size_t kSkinnyLeastSmem = 57 * 1024, kSkinnyMostTmem = 64;
+constexpr size_t kSmemOfSm = 228 * 1024, kSmemPerCta = 1024;        // what the SM has, and keeps for itself
 cudaError_t gemm_skinny_qkv(const void* A, const void* B, int M, int N, int K, const Dims& D, const QKVArgs& e,
                             cudaStream_t s);
 cudaError_t gemm_skinny_wo(const void* A, const void* B, int M, int N, int K, const Dims& D, const WoArgs& e,

@@ -64,13 +64,19 @@ template <int NT, int MATS, int CPS, bool ONE> struct FewCfg {
   static constexpr int STAGES = FIT > 12 ? 12 : FIT;
   static constexpr uint32_t OFF_INBOX = STAGES * STAGE_BYTES;
   static constexpr uint32_t OFF_BAR = OFF_INBOX + INBOX;
-  static constexpr size_t SMEM = OFF_BAR + 512 + 1024;
+  // (with two CTAs per SM at least 88 KB: beside two that hold 256 columns of tensor memory each,
+  // no CTA of another cluster may start that waits for more)
+  static constexpr size_t NEEDED = OFF_BAR + 512 + 1024, LEAST = CPS == 2 ? 88 * 1024 : 0;
+  static constexpr size_t SMEM = NEEDED > LEAST ? NEEDED : LEAST;
   static constexpr uint32_t ACC = MATS * NT;                 // columns of one accumulator
   static constexpr uint32_t SET_COLS = 4 * MATS + 4;         // a word per weight row / 32 and row / 32
   static constexpr uint32_t SETS_AT = ONE ? ACC : 2 * ACC;
   static constexpr uint32_t NEED = SETS_AT + (ONE ? kChunk : kSets) * SET_COLS;
   static constexpr uint32_t TMEM_COLS = NEED <= 128 ? 128 : NEED <= 256 ? 256 : 512;
   static_assert(CPS * TMEM_COLS <= 512, "tensor memory of an SM");
+  static_assert(2 * TMEM_COLS + kSkinnyMostTmem <= 512 || 2 * SMEM + kSkinnyLeastSmem + 3 * kSmemPerCta > kSmemOfSm,
+                "a third CTA that waits for tensor memory");
+  static_assert(CPS == 2 || SMEM + kSkinnyLeastSmem + 2 * kSmemPerCta > kSmemOfSm, "a second one");
   static_assert(STAGES >= 2 && (2 * STAGES + 2 * kSets + 7) * 8 + 8 <= 512, "barriers");
   static_assert(MATS * NT * kBlk * 4 <= OFF_INBOX, "the sums reuse the ring");
 };

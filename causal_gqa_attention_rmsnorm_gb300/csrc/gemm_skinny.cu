@@ -52,6 +52,7 @@ template <int NT, int CPS = 2> struct SkCfg {
   static constexpr size_t SMEM = OFF_MISC + 16 + 1024;
   static constexpr uint32_t TMEM_COLS = NT <= 32 ? 32 : 64;
   static_assert(NT * kRows * 4 <= OFF_BAR, "the partial tile reuses the stage ring");
+  static_assert(SMEM >= kSkinnyLeastSmem && TMEM_COLS <= kSkinnyMostTmem, "what other kernels reckon with");
 };
 
 template <int NT, class Epi, int CPS>

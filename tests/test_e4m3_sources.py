@@ -28,3 +28,35 @@ def test_packing_walks_blocks_of_columns():
     start, bound, step = re.search(r"for \(int (\w+) = blockIdx\.y; \1 < (\w+); \1 \+= ([^)]+)\)", source("e4m3_rows.cu")).groups()
     assert (start, bound, step) == ("nb", "blocks", "gridDim.y")
     assert (2 ** 31 - 1024 + 127) // 128 + 65535 < 2 ** 31 <= 2 ** 31 - 1024 + 65535 * 128
+
+
+def test_ctas_that_wait_for_others_find_tensor_memory_where_they_find_shared_memory():
+    """Tensor memory is waited for without a limit, and the CTAs of a cluster wait for one
+    another: whatever CTAs of the two products for few rows share an SM (228 KB, 1 KB each for
+    itself), their 32-bit columns are at most its 512."""
+    text, skinny = source("e4m3_gemm_few.cu"), source("gemm_skinny.cu")
+    least = re.search(r"CPS == 2 \? (\d+) \* 1024 : 0", text)
+    ctas = []
+    forms = {tuple(map(int, f)) for f in re.findall(r"return go<(\d+), (\d+), (\d+)>", text)}
+    assert len(forms) == 7
+    for nt, mats, cps in forms:
+        for one, per_sm in ((True, 2), (False, cps)):
+            stage = mats * 128 * 128 + nt * 128
+            inbox = 32 * 128 * 4 if one and mats == 1 and nt <= 32 else 0
+            stages = min(12, ((110 if per_sm == 2 else 220) * 1024 - inbox) // stage)
+            smem = stages * stage + inbox + 512 + 1024
+            if least and per_sm == 2:
+                smem = max(smem, int(least[1]) * 1024)
+            columns = mats * nt * (1 if one else 2) + (4 if one else 8) * (4 * mats + 4)
+            ctas.append((smem, next(c for c in (128, 256, 512) if c >= columns)))
+    assert re.search(r"TMEM_COLS = NT <= 32 \? 32 : 64", skinny)
+    for nt, stages in ((16, 5), (32, 5), (48, 4), (64, 4), (16, 3), (32, 3)):
+        ctas.append((stages * (16384 + nt * 128) + 128 + 256 + 2048 + 16 + 1024, 32 if nt <= 32 else 64))
+
+    def fill(room, columns, first):
+        assert columns <= 512, columns
+        for i in range(first, len(ctas)):
+            if ctas[i][0] + 1024 <= room:
+                fill(room - ctas[i][0] - 1024, columns + ctas[i][1], i)
+
+    fill(228 * 1024, 0, 0)
