@@ -388,7 +388,6 @@ template <int DH, bool E4>
 __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
     k_attn_many(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const ManyArgs m) {
-  pdl_trigger();
   using C = ManyCfg<DH, E4>;
   const AttnArgs& a = m.a;
   int* err = a.c.err;
@@ -462,6 +461,7 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_trigger();                                // (only now: common.cuh)
   pdl_wait();                                   // the plan, and whatever wrote q and the cache
   const long long total = m.pre[(size_t)a.c.B * m.pairs] * a.c.Hkv;
   const int parts = parts_of(m, total);

@@ -28,12 +28,14 @@ inline int log2_dh(int dh) {
 
 // Programmatic dependent launch.  The kernels of a decode step are launched
 // (launch_pdl) so that each may be scheduled while the one before it drains:
-// a kernel calls pdl_trigger() at its start, which lets the next launch as
+// a kernel calls pdl_trigger() at its start, which lets the next launch in as
 // soon as every CTA of this one has started, and pdl_wait() before it touches
 // any global memory an earlier kernel of the stream writes or reads — the wait
 // returns once the previous grid has completed and its writes are visible.
 // Every CTA passes pdl_wait() before it exits, so completion is ordered along
-// the whole chain.  Without the launch attribute both are no-ops.
+// the whole chain.  Without the launch attribute both are no-ops.  A kernel that
+// takes tensor memory calls pdl_trigger() once it has it: a CTA of the next launch
+// could otherwise be given what this one still waits for, and wait for this one.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -185,7 +185,6 @@ __global__ void __launch_bounds__(192, CPS)
   float* part_s = reinterpret_cast<float*>(smem);       // [MATS][NT][128] after the main loop
   float4* inbox = reinterpret_cast<float4*>(smem + C::OFF_INBOX);  // [splits][tpr / 4][128], four rows each
 
-  pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();              // blockIdx.x % splits
   const int tile = (int)(blockIdx.x / splits);
@@ -230,6 +229,7 @@ __global__ void __launch_bounds__(192, CPS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_trigger();                                // (only now: common.cuh)
   // (waited for where the first partial sums leave: the other CTAs' barriers exist then)
   if (push) cluster_arrive();
 

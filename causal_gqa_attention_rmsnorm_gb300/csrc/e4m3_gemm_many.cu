@@ -105,7 +105,6 @@ __global__ void __launch_bounds__(ManyCfg<CG>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   static_assert((2 * STAGES + 32) * 8 + 8 <= 384, "barriers");
 
-  pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = m_units * n_tiles;
   const int kblocks = (a.K + kBlk - 1) / kBlk, nsets = (kblocks + kSet - 1) / kSet;
@@ -151,6 +150,7 @@ __global__ void __launch_bounds__(ManyCfg<CG>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_trigger();                                // (only now: common.cuh)
   auto commit = [](uint32_t bar, uint32_t elected) {
     if constexpr (CG == 2) mma_commit_pair_elected(bar, elected);
     else mma_commit_elected(bar, elected);

@@ -75,7 +75,6 @@ __global__ void __launch_bounds__(192, CPS)
   static_assert(sizeof(RowAux) * NT <= C::RA_BYTES, "row inputs");
   RowAux* ra_s = reinterpret_cast<RowAux*>(smem + C::OFF_RA);
 
-  pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = blockIdx.x / splits;
   const int rank = (int)cluster_ctarank();                    // blockIdx.x % splits
@@ -104,6 +103,7 @@ __global__ void __launch_bounds__(192, CPS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_trigger();                                // (only now: common.cuh)
 
   if (warp == 0) {
     if (lane == 0) {

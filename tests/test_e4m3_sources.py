@@ -1,4 +1,5 @@
 """Rules that the sources of the 8-bit projections keep, read from the files."""
+import glob
 import os
 import re
 
@@ -60,3 +61,19 @@ def test_ctas_that_wait_for_others_find_tensor_memory_where_they_find_shared_mem
                 fill(room - ctas[i][0] - 1024, columns + ctas[i][1], i)
 
     fill(228 * 1024, 0, 0)
+
+
+def test_dependents_are_let_in_once_tensor_memory_is_there():
+    """The allocation waits for CTAs of the SM; one of the next launch among them would be
+    waiting for this one to end."""
+    seen = 0
+    for path in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
+        text = code(path)
+        for kernel in re.split(r"__global__", text)[1:]:
+            took = [m.start() for m in re.finditer(r"\btmem_alloc(?:_pair)?\(", kernel)]
+            let = [m.start() for m in re.finditer(r"\bpdl_trigger\(\)", kernel)]
+            if took and let:
+                seen += 1
+                barrier = kernel.index("__syncthreads()", took[-1])
+                assert min(let) > barrier, os.path.basename(path)
+    assert seen == 4
