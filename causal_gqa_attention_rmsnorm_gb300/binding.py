@@ -123,6 +123,8 @@ def lib() -> ctypes.CDLL:
         L.tbx_e4m3_form.restype = c_int32
         L.tbx_e4m3_few_tile.argtypes = [c_int32] * 6
         L.tbx_e4m3_few_tile.restype = c_int32
+        L.tbx_e4m3_tile.argtypes = [c_int32] * 7
+        L.tbx_e4m3_tile.restype = c_int32
         L.tb_embed.argtypes = [c_void_p, c_int32, c_int32, c_int32, c_void_p, ctypes.c_int64, c_void_p, c_void_p]
         L.tb_lm_head_packed_bytes.argtypes = [P(tb_head_cfg)]
         L.tb_lm_head_packed_bytes.restype = c_size_t

@@ -76,19 +76,29 @@ tb_status check_weights(const tb_e4m3* w, const char* name, const tb_e4m3* x, bo
   return TB_OK;
 }
 
-// The rows per tile of k_e4m3_few, or 0 for k_e4m3_many, -1 with a CTA to a tile.  An fp32 result keeps fp32's
-// sums: k_e4m3_many has one accumulator for all of K, whose cut-off sums are off by up to
-// 2^-24 per instruction of 32 (relative to 64 bits, normal rows: K 4096 2.2e-7, 14336
-// 1.0e-6, against 1.2e-7 in chunks), so from K = 4096 on an fp32 result is formed in
-// chunks.
+// k_e4m3_many has one accumulator for all of K, k_e4m3_few one for each 2048 of it, added up
+// with rounding.  The tensor core cuts its sums off, so that one accumulator is off the more
+// the longer it is.  Measured against 64 bits, relative to the results' size, rows and weights
+// of both signs / of one sign (there all of it in one direction):
+//     K                  1024         2048         4096         14336        65536        2^20
+//     one accumulator  5.4e-8/1.6e-7 1.0e-7/4.3e-7 2.1e-7/1.2e-6 9.8e-7/7.6e-6 7.6e-6/5.0e-5 3.0e-4/2.5e-3
+//     parts of 2048    3.8e-8/7.3e-8 4.8e-8/7.3e-8 6.0e-8/7.5e-8 1.1e-7/3.6e-7 1.2e-7/4.1e-7 1.9e-7/4.1e-7
+//     fp32 sums        3.9e-8/6.0e-8 5.7e-8/9.9e-8 5.8e-8/4.7e-8 8.2e-8/5.8e-8 1.7e-7/1.2e-7 3.0e-7/7.9e-7
+// So an fp32 result is formed in parts beyond K = 4096, and one of bf16 or codes, half a step
+// of which is 2e-3 or more, beyond K = 65536.
+constexpr int kOneF32 = 4096, kOne16 = 65536;
+
+// The rows per tile of k_e4m3_few, or 0 for k_e4m3_many, -1 with a CTA to a tile.
+int rule(int M, int N, int K, int mats, int y_dtype, bool res, int sms) {
+  const bool light = mats == 2 ? y_dtype != TB_E4M3 : y_dtype == TB_F32 && !res;
+  const int tile = e4m3_few_tile(M, N, K, mats, light, sms);
+  return tile > 0 || K <= (y_dtype == TB_F32 ? kOneF32 : kOne16) ? tile : mats == 2 ? 64 : 128;
+}
 std::atomic<int> g_form{0};            // test hook: 16 to 128 rows per tile, or -1 and -2 for many
 int tile_of(const GemmArgs& a, int mats) {
   const int form = g_form.load(std::memory_order_relaxed);
   if (form) return form == -1 ? 0 : form == -2 ? -1 : mats == 2 && form > 64 ? 64 : form;
-  const bool light = mats == 2 ? a.y_dtype != TB_E4M3 : a.y_dtype == TB_F32 && !a.res;
-  const int tile = e4m3_few_tile(a.M, a.N, a.K, mats, light, sm_count());
-  if (tile <= 0 && a.y_dtype == TB_F32 && a.K > 4096) return mats == 2 ? 64 : 128;
-  return tile;
+  return rule(a.M, a.N, a.K, mats, a.y_dtype, a.res != nullptr, sm_count());
 }
 
 RowsArgs rows_args(const void* x, const tb_e4m3* out) {
@@ -240,12 +250,15 @@ tb_status tb_gated_e4m3(const tb_e4m3* x, const tb_e4m3* w1, const tb_e4m3* w3, 
 // Test hooks: the form that later products of this process take (0: by the rule; 16, 32,
 // 64 or 128: k_e4m3_few with so many rows per tile; -1: k_e4m3_many; -2: the same with a
 // CTA to a tile), returning the
-// previous one; and the rule itself.
+// previous one; and the rule itself, for the tiles alone and with the type of the result.
 TB_API int32_t tbx_e4m3_form(int32_t form) {
   return g_form.exchange(form == 16 || form == 32 || form == 64 || form == 128 || form == -1 || form == -2 ? form : 0);
 }
 TB_API int32_t tbx_e4m3_few_tile(int32_t M, int32_t N, int32_t K, int32_t mats, int32_t light, int32_t sms) {
   return e4m3_few_tile(M, N, K, mats, light != 0, sms);
+}
+TB_API int32_t tbx_e4m3_tile(int32_t M, int32_t N, int32_t K, int32_t mats, int32_t y_dtype, int32_t res, int32_t sms) {
+  return rule(M, N, K, mats, y_dtype, res != 0, sms);
 }
 
 }  // extern "C"

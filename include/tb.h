@@ -462,13 +462,17 @@ TB_API tb_status tb_pack_e4m3(const void* w, int32_t dtype, const tb_e4m3* out, 
  *  res  : NULL, or device, dense [M, N] of y_dtype.
  *  y    : device, dense [M, N] of y_dtype (TB_F32 or TB_BF16), 16-byte aligned.  It may
  *         be res itself and overlaps nothing else that is read.
- * Products and sums are fp32, rounded once to y_dtype. */
+ * Products are exact and rounded once to y_dtype after their sum, which is fp32 and formed by
+ * the tensor cores.  These cut off what fp32 addition would round: sums of terms of both signs
+ * are off by 2e-7 of the results' size at K = 4096, sums of terms of one sign come out 1.2e-6
+ * low there.  Of an fp32 result no accumulator holds more than 4096 of K, of one in bf16 (or
+ * codes) 65536; longer sums are formed in parts of 2048, added with rounding (4e-7 or less). */
 TB_API tb_status tb_gemm_e4m3(const tb_e4m3* x, const tb_e4m3* w, const void* res, void* y, int32_t y_dtype, void* stream);
 
 /* The gated half of the MLP: SiLU(x·w1) * (x·w3), x rows [M, K], w1 and w3 weights
  * [F, K], F a multiple of 16.  With y_dtype TB_F32 or TB_BF16, y is dense [M, F]; with
  * TB_E4M3, y receives codes [M, F] and y_scale their scales [M, ceil(F/128)], rows as
- * tb_gemm_e4m3 takes them (y_scale NULL otherwise). */
+ * tb_gemm_e4m3 takes them (y_scale NULL otherwise).  The two sums as in tb_gemm_e4m3. */
 TB_API tb_status tb_gated_e4m3(const tb_e4m3* x, const tb_e4m3* w1, const tb_e4m3* w3, void* y, int32_t y_dtype,
                                void* y_scale, void* stream);
 

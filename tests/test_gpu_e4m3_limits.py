@@ -79,3 +79,74 @@ def test_pack_of_the_most_columns():
     assert (scale == 27).all()
     for i in range(0, N, 2 ** 27):
         assert not codes[i:i + 2 ** 27].any()
+
+
+# ---- long sums ----------------------------------------------------------------------
+#
+# The tensor core cuts its sums off.  In an accumulator of 64 instructions a sum of
+# magnitudes S is off by at most (2·64 + 8)·2^-23·S (e4m3_helpers), and the parts are added
+# with rounding, 2^-24 of what is summed up for each:
+
+def in_parts(K):
+    return (2 * 64 + 8) * 2.0 ** -23 + -(-K // 2048) * 2.0 ** -24
+
+
+def one_sign(n, K, g, device="cuda"):
+    """Codes of |N(0, 1)| times 40."""
+    return (torch.randn(n, K, generator=g, device=device) * 40).abs().clamp(max=448).to(CODE)
+
+
+def flat_scales(shape, e):
+    return torch.full(shape, 127 + e, dtype=torch.uint8, device="cuda").view(SCALE)
+
+
+def exact_product(x, w):
+    """Of codes, in fp64 on the GPU, some columns of K at a time (for which every sum is exact
+    but for fp64's own rounding)."""
+    y = torch.zeros(x.shape[0], w.shape[0], dtype=torch.float64, device="cuda")
+    for k in range(0, x.shape[1], 1 << 15):
+        y += x[:, k:k + (1 << 15)].double() @ w[:, k:k + (1 << 15)].double().T
+    return y
+
+
+def check_between(got, exact, off):
+    """got is a rounding, to its type, of a value within the factor 1 +- off of exact (> 0)."""
+    low, high = (exact * (1 - off)).to(got.dtype), (exact * (1 + off)).to(got.dtype)
+    bad = ~((got >= low) & (got <= high))
+    assert not bad.any(), (int(bad.sum()), bad.numel(), ((got.double() - exact) / exact)[bad][:4].tolist())
+
+
+def test_gemm_of_a_very_long_sum():
+    """Values of one sign, whose cut-off sums are all off in the same direction: bf16 results
+    are those of sums in parts (one accumulator comes out 2.5e-3 low, which is more than half
+    a step)."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    M, N, K = 1030, 2560, 1 << 20
+    xc, wc = one_sign(M, K, g), one_sign(N, K, g)
+    x = tb.E4M3Rows(xc, flat_scales((M, K // 128), -8))
+    w = tb.E4M3Weight(wc, flat_scales((N // 128, K // 128), -8))
+    y = tb.tb_gemm_e4m3(x, w)
+    no_error()
+    rows = [0, 1, 127, 128, 500, 1023, 1024, 1029]
+    check_between(y[rows], exact_product(xc[rows], wc) * 2.0 ** -16, in_parts(K))
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, "codes"])
+def test_gated_of_very_long_sums(out_dtype):
+    """The same for gates of hundreds, where SiLU is the gate itself."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    M, F, K = 300, 2048, 1 << 20
+    xc, wc, vc = one_sign(M, K, g), one_sign(F, K, g), one_sign(F, K, g)
+    x = tb.E4M3Rows(xc, flat_scales((M, K // 128), -10))
+    w1, w3 = (tb.E4M3Weight(c, flat_scales((F // 128, K // 128), -10)) for c in (wc, vc))
+    out = tb.tb_gated_e4m3(x, w1, w3, out_dtype=tb.TB_BF16 if out_dtype is BF16 else None)
+    no_error()
+    rows = [0, 127, 128, 255, 256, 299]
+    a, b = exact_product(xc[rows], wc) * 2.0 ** -20, exact_product(xc[rows], vc) * 2.0 ** -20
+    assert a.min() > 200                              # SiLU(a) = a to 1e-80
+    off = 2.01 * in_parts(K) + 8 * 2.0 ** -24
+    if out_dtype is BF16:
+        check_between(out[rows], a * b, off)
+    else:
+        y = (a * b).cpu().numpy()
+        check_rows(bytes_of(out.codes[rows]), bytes_of(out.scale[rows]), y, off * y)
