@@ -5,9 +5,9 @@ import pytest
 import torch
 
 import causal_gqa_attention_rmsnorm_gb300 as tb
-from e4m3_helpers import BF16, CODE, F32, SCALE, bytes_of, check_rows
+from e4m3_helpers import BF16, CODE, F32, HALF, SCALE, bytes_of, check_rows
 from oracle import e4m3 as ref
-from test_gpu_e4m3_ops import MANY_ROWS, NORM_OFF, f64, gen, no_error
+from test_gpu_e4m3_ops import MANY_ROWS, NORM_OFF, f64, form, gen, no_error  # noqa: F401 (form is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -150,3 +150,43 @@ def test_gated_of_very_long_sums(out_dtype):
     else:
         y = (a * b).cpu().numpy()
         check_rows(bytes_of(out.codes[rows]), bytes_of(out.scale[rows]), y, off * y)
+
+
+def off_by(y, exact):
+    """The largest deviation of fp32 results (> 0), less half a step, relative to exact."""
+    return (((y.double() - exact).abs() - 2 * HALF[F32] * exact) / exact).max().item()
+
+
+@pytest.mark.parametrize("tile", [0, 16, 32, 64, 128])
+@pytest.mark.parametrize("K", [14336, 65536])
+def test_fp32_sums_are_formed_in_parts(form, tile, K):
+    """Of one sign: the bound, 1.7e-5, is a quarter of what one of 14336 terms is worth, and a third
+    of what one accumulator loses at 65536 (5.0e-5)."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    M, N = 1030, 2560
+    xc, wc = one_sign(M, K, g), one_sign(N, K, g)
+    x, w = tb.E4M3Rows(xc, flat_scales((M, K // 128), -8)), tb.E4M3Weight(wc, flat_scales((N // 128, K // 128), -8))
+    exact = exact_product(xc, wc) * 2.0 ** -16
+    form(tile)
+    y = tb.tb_gemm_e4m3(x, w, y_dtype=tb.TB_F32)
+    res = torch.zeros_like(y)
+    with_res = tb.tb_gemm_e4m3(x, w, res=res)
+    no_error()
+    assert off_by(y, exact) <= in_parts(K) and off_by(with_res, exact) <= in_parts(K)
+
+
+@pytest.mark.parametrize("tile", [0, 16, 32, 64])
+@pytest.mark.parametrize("K", [14336, 65536])
+def test_gated_fp32_sums_are_formed_in_parts(form, tile, K):
+    g = torch.Generator(device="cuda").manual_seed(K + 1)
+    M, F = 300, 2048
+    xc, wc, vc = one_sign(M, K, g), one_sign(F, K, g), one_sign(F, K, g)
+    x = tb.E4M3Rows(xc, flat_scales((M, K // 128), -7))
+    w1, w3 = (tb.E4M3Weight(c, flat_scales((F // 128, K // 128), -8)) for c in (wc, vc))
+    a, b = exact_product(xc, wc) * 2.0 ** -15, exact_product(xc, vc) * 2.0 ** -15
+    assert a.min() > 200                              # SiLU(a) = a to 1e-80
+    off = 2.01 * in_parts(K) + 8 * 2.0 ** -24
+    form(tile)
+    y = tb.tb_gated_e4m3(x, w1, w3, out_dtype=tb.TB_F32)
+    no_error()
+    assert off_by(y, a * b) <= off
