@@ -761,7 +761,9 @@ def _blocks(n: int) -> int:
 
 class _Coded:
     """Codes [rows, cols] and their scales: two dense tensors, read once, here.  (A
-    handle to keep: a tensor that is resized or given other memory needs a new one.)"""
+    handle to keep: a tensor that is resized or given other memory needs a new one.
+    Its attributes are fixed, since the calls go by what was read here, and it is what
+    keeps the tensors' memory.)"""
     __slots__ = ("codes", "scale", "dev", "rows", "cols", "_struct", "_ref")
 
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor):
@@ -775,9 +777,16 @@ class _Coded:
             raise ValueError(f"at most 2^31 - 1 rows and columns, got {rows} and {cols}")
         code_ptr = _dense(codes, "codes", _E4M3, (rows, cols), dev)
         scale_ptr = _dense(scale, "scale", _E8M0, self._scales(rows, cols), dev)
-        self.codes, self.scale, self.dev, self.rows, self.cols = codes, scale, dev, rows, cols
-        self._struct = tb_e4m3(code_ptr, scale_ptr, rows, cols)
-        self._ref = ctypes.byref(self._struct)
+        struct = tb_e4m3(code_ptr, scale_ptr, rows, cols)
+        fix = object.__setattr__
+        for name, value in zip(_Coded.__slots__, (codes, scale, dev, rows, cols, struct, ctypes.byref(struct))):
+            fix(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name} of {type(self).__name__} is fixed: other tensors need a handle of their own")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name} of {type(self).__name__} is fixed")
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda"):
