@@ -806,7 +806,11 @@ class E4M3Rows(_Coded):
 
 class E4M3Weight(_Coded):
     """Weights as codes [out, in] with one power-of-two scale per block of 128 x 128,
-    scale [ceil(out / 128), ceil(in / 128)] (tb_pack_e4m3 makes them)."""
+    scale [ceil(out / 128), ceil(in / 128)] (tb_pack_e4m3 makes them).  The products
+    request the codes before kernels ahead of them in the stream have ended: they are
+    written by tb_pack_e4m3, or by work outside the library that lets no kernel behind it
+    start early (torch's own copies and kernels do not; a kernel that releases its
+    dependents before its writes are done does)."""
     __slots__ = ()
 
     @staticmethod

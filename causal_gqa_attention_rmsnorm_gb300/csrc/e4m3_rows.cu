@@ -263,6 +263,9 @@ template <typename T> __global__ void __launch_bounds__(256) k_pack_e4m3(const T
     }
     __syncthreads();
   }
+  // A product may request these before this grid's end has been waited for (common.cuh): what
+  // lets it in is that the CTAs are through, so they are once their codes can be seen.
+  asm volatile("fence.acq_rel.gpu;\n\tfence.proxy.async.global;" ::: "memory");
 }
 
 // Eights per thread.  Few rows: one, for the shortest chain.  Narrow rows: as many as let

@@ -452,9 +452,12 @@ TB_API tb_status tb_rmsnorm_e4m3(const void* x, int32_t dtype, const void* r, in
 TB_API tb_status tb_quant_e4m3(const void* x, int32_t dtype, const tb_e4m3* out, void* stream);
 
 /* Weights w (device, [in, out] of dtype, as everywhere in this header) to codes:
- * out->rows is `out`, out->cols is `in`.  Done once per weight set.  (The products request
- * weights before kernels of this library ahead of them in the stream have ended: weights
- * are written by this call, or by work outside the library, not by its other calls.) */
+ * out->rows is `out`, out->cols is `in`.  Done once per weight set.
+ *   The products request weights (codes, not scales) before kernels ahead of them in the
+ * stream have ended.  So weights are written by this call, or by work outside the library that
+ * lets no kernel behind it start early: copies and ordinary kernels, not one that releases its
+ * dependents (programmatic dependent launch) before its writes are done; and not by the
+ * library's other calls. */
 TB_API tb_status tb_pack_e4m3(const void* w, int32_t dtype, const tb_e4m3* out, void* stream);
 
 /* y[m, n] = res[m, n] + sum_k x[m, k] w[n, k]

@@ -190,3 +190,37 @@ def test_gated_fp32_sums_are_formed_in_parts(form, tile, K):
     y = tb.tb_gated_e4m3(x, w1, w3, out_dtype=tb.TB_F32)
     no_error()
     assert off_by(y, a * b) <= off
+
+
+# ---- weights that were written just ahead ---------------------------------------------
+
+@pytest.mark.parametrize("M", [1, 20, 300])
+def test_weights_packed_just_ahead_are_the_ones_used(M):
+    """Set after set into the same tensors, by packing, and by copies outside the library,
+    with nothing between them and the product, or other calls of the library."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    K, N, sets = 512, 2048, 12
+    x = tb.tb_quant_e4m3(torch.randn(M, K, generator=g, device="cuda"))
+    ws = [torch.randn(K, N, generator=g, device="cuda").to(BF16) for _ in range(sets)]
+    packed = [tb.tb_pack_e4m3(w) for w in ws]
+    torch.cuda.synchronize()
+    want = [tb.tb_gemm_e4m3(x, p) for p in packed]
+    gated = [tb.tb_gated_e4m3(x, p, p, out_dtype=tb.TB_BF16) for p in packed]
+    torch.cuda.synchronize()
+    w8 = tb.E4M3Weight.empty(N, K)
+    other = torch.randn(64, K, generator=g, device="cuda")
+    got = []
+    for _ in range(4):
+        for i in range(sets):
+            tb.tb_pack_e4m3(ws[i], out=w8)
+            if i % 3 == 1:
+                tb.tb_quant_e4m3(other)
+            got.append((tb.tb_gemm_e4m3(x, w8), want[i]))
+            w8.codes.view(torch.uint8).copy_(packed[i - 1].codes.view(torch.uint8))
+            w8.scale.view(torch.uint8).copy_(packed[i - 1].scale.view(torch.uint8))
+            if i % 3 == 2:
+                tb.tb_quant_e4m3(other)
+            got.append((tb.tb_gated_e4m3(x, w8, w8, out_dtype=tb.TB_BF16), gated[i - 1]))
+    torch.cuda.synchronize()
+    no_error()
+    assert all(torch.equal(a, b) for a, b in got)
