@@ -14,7 +14,8 @@ __device__ __forceinline__ float gated(float g, float u) { return __fdividef(g, 
 
 // The same where the result is rounded to 16 bits or fewer and there are many: 2^x and 1/x as
 // the hardware has them.  The exponent's rounding shifts e^-g by up to |g|·2^-23, which SiLU
-// feels by at most 0.28·|g|·2^-23, and the two functions add 2^-21.
+// feels by at most 0.28·|g|·2^-23 (and relative to its size by |g|·2^-23, for gates far below
+// zero), and the two functions add 2^-21 of its size.  Below -87 1/x is 0, as above.
 __device__ __forceinline__ float gated_short(float g, float u) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));

@@ -475,7 +475,9 @@ TB_API tb_status tb_gemm_e4m3(const tb_e4m3* x, const tb_e4m3* w, const void* re
 /* The gated half of the MLP: SiLU(x·w1) * (x·w3), x rows [M, K], w1 and w3 weights
  * [F, K], F a multiple of 16.  With y_dtype TB_F32 or TB_BF16, y is dense [M, F]; with
  * TB_E4M3, y receives codes [M, F] and y_scale their scales [M, ceil(F/128)], rows as
- * tb_gemm_e4m3 takes them (y_scale NULL otherwise).  The two sums as in tb_gemm_e4m3. */
+ * tb_gemm_e4m3 takes them (y_scale NULL otherwise).  The two sums as in tb_gemm_e4m3.
+ * SiLU(g) is off by at most 2^-20 of its size in an fp32 result, 2^-21 + |g|·2^-23 of it in
+ * one of bf16 or codes; for gates below -87, where it is under 1e-35, it may be 0. */
 TB_API tb_status tb_gated_e4m3(const tb_e4m3* x, const tb_e4m3* w1, const tb_e4m3* w3, void* y, int32_t y_dtype,
                                void* y_scale, void* stream);
 

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import causal_gqa_attention_rmsnorm_gb300 as tb
-from e4m3_helpers import BF16, CODE, F32, HALF, SCALE, bytes_of, check_rows
+from e4m3_helpers import (BF16, CODE, F32, HALF, SCALE, bytes_of, check_product, check_rows, gated_and_off, make_rows, make_weight,
+                          product, rows_np, weight_np)
 from oracle import e4m3 as ref
 from test_gpu_e4m3_ops import MANY_ROWS, NORM_OFF, f64, form, gen, no_error  # noqa: F401 (form is a fixture)
 
@@ -224,3 +225,92 @@ def test_weights_packed_just_ahead_are_the_ones_used(M):
     torch.cuda.synchronize()
     no_error()
     assert all(torch.equal(a, b) for a, b in got)
+
+
+# ---- weights beyond L2, whose tiles go in groups ----------------------------------------
+
+def repeated_rows(M, P, K, g):
+    """M rows of which P differ, P odd and no part of a tile: row m is row m % P."""
+    few = make_rows(tb, P, K, g)
+    n = -(-M // P)
+    x = tb.E4M3Rows(few.codes.view(torch.uint8).repeat(n, 1)[:M].contiguous().view(CODE),
+                    few.scale.view(torch.uint8).repeat(n, 1)[:M].contiguous().view(SCALE))
+    return few, x
+
+
+def all_repeat(t, P):
+    u = t.view(torch.uint8) if t.element_size() == 1 else t
+    for i in range(0, u.shape[0], P):
+        if not torch.equal(u[i:i + P], u[:min(P, u.shape[0] - i)]):
+            return False
+    return True
+
+
+@pytest.mark.parametrize("tile", [0, -1, -2])
+@pytest.mark.parametrize("M", [257, 8453])
+def test_gemm_of_large_weights(form, tile, M):
+    """More than 48 MB of weights and K up to 8192: tiles in groups of 32 units of rows, the
+    last group smaller, the last unit and the last column tile partly filled."""
+    form(tile)
+    g = gen(M)
+    N, K, P = 24592, 2064, 97
+    few, x = repeated_rows(M, P, K, g)
+    w = make_weight(tb, N, K, g)
+    for dtype in (BF16, F32):
+        res = (torch.randn(P, N, generator=g) * 100).to(dtype).cuda()
+        y = tb.tb_gemm_e4m3(x, w, res=res.repeat(-(-M // P), 1)[:M].contiguous())
+        no_error()
+        check_product(y[:P], *product(rows_np(few), weight_np(w), f64(res)), K, dtype)
+        assert all_repeat(y, P)
+
+
+@pytest.mark.parametrize("tile", [0, -1, -2])
+@pytest.mark.parametrize("M,out_dtype", [(257, "codes"), (8453, "codes"), (8453, BF16)])
+def test_gated_of_large_weights(form, tile, M, out_dtype):
+    form(tile)
+    g = gen(M + 1)
+    F, K, P = 12400, 2064, 97
+    few, x = repeated_rows(M, P, K, g)
+    w1, w3 = make_weight(tb, F, K, g), make_weight(tb, F, K, g)
+    w1.scale.view(torch.uint8).sub_(int(np.log2(K) / 2) + 11)
+    exact, off = gated_and_off(rows_np(few), weight_np(w1), weight_np(w3), K)
+    out = tb.tb_gated_e4m3(x, w1, w3, out_dtype=None if out_dtype == "codes" else tb.TB_BF16)
+    no_error()
+    if out_dtype == "codes":
+        check_rows(bytes_of(out.codes[:P]), bytes_of(out.scale[:P]), exact, off)
+        assert all_repeat(out.codes, P) and all_repeat(out.scale, P)
+    else:
+        assert (np.abs(f64(out[:P]) - exact) <= off + 2 * HALF[BF16] * (np.abs(exact) + off)).all()
+        assert all_repeat(out, P)
+
+
+# ---- gates far from zero, to bf16 and codes ----------------------------------------------
+
+@pytest.mark.parametrize("tile", [16, 32, 64, -1, -2])
+@pytest.mark.parametrize("out_dtype", [BF16, "codes"])
+@pytest.mark.parametrize("up", [0, 40])
+def test_far_gates_to_few_bits(form, tile, out_dtype, up):
+    """Gates of every size a code has, of both signs, up to 7168, those below zero also in a
+    block of their own from 0 to -112.  SiLU's short form has 2^x of an argument rounded by up to
+    |g|·2^-23 of its effect and two functions within 2^-21 together; below -87, where it is
+    under 1e-35, it may be 0."""
+    form(tile)
+    M, F, K = 140, 384, 128
+    x = torch.zeros(M, K, dtype=torch.uint8)
+    x[:, 0] = 0x38
+    w1, w3 = torch.zeros(F, K, dtype=torch.uint8), torch.zeros(F, K, dtype=torch.uint8)
+    size = torch.arange(128, dtype=torch.uint8).clamp(max=126)
+    w1[:128, 0], w1[128:256, 0], w1[256:, 0], w3[:, 0] = size + 128, size + 128, size, 0x38
+    s1 = torch.tensor([[125], [131], [131]], dtype=torch.uint8)
+    out = tb.tb_gated_e4m3(tb.E4M3Rows(x.view(CODE).cuda(), flat_scales((M, 1), 0)), tb.E4M3Weight(w1.view(CODE).cuda(), s1.view(SCALE).cuda()),
+                           tb.E4M3Weight(w3.view(CODE).cuda(), flat_scales((3, 1), up)), out_dtype=tb.TB_BF16 if out_dtype is BF16 else None)
+    no_error()
+    gates = ref.VALUES[w1[:, 0].numpy()] * np.repeat([0.25, 16.0, 16.0], 128)
+    with np.errstate(over="ignore"):
+        want = np.tile(ref.silu(gates) * 2.0 ** up, (M, 1))
+    assert np.isfinite(want).all() and (gates == -112).any() and (gates == 7168).any()
+    off = (np.abs(gates) * 2.0 ** -23 + 2.0 ** -21) * np.abs(want) + 1e-35 * 2.0 ** up
+    if out_dtype is BF16:
+        assert (np.abs(f64(out) - want) <= off + 2 * HALF[BF16] * (np.abs(want) + off)).all()
+    else:
+        check_rows(bytes_of(out.codes), bytes_of(out.scale), want, off)
