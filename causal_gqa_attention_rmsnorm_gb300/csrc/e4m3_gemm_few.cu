@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(192, CPS)
       mbar_wait_warp(&full[t % STAGES], (t / STAGES) & 1, &no_abort, err);
   } else if (warp == 1) {
     // The whole warp walks the blocks; its elected lane issues (mma_mx_k128).
+    pdl_wait();                           // (the limit of its waits is for this kernel's work)
     const uint32_t elected = elect_one();
     const uint64_t desc = desc_kmajor_sw128(smem_u32(smem));
     const uint32_t desc_hi = (uint32_t)(desc >> 32), desc0 = (uint32_t)desc;

@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(ManyCfg<CG>::THREADS, 1)
     }
   } else if (warp == 1) {
     // The whole warp walks the blocks; its elected lane issues (mma_mx_k128).
+    pdl_wait();                           // (the limit of its waits is for this kernel's work)
     if (rank == 0) {
       const uint32_t elected = elect_one();
       const uint64_t desc = desc_kmajor_sw128(smem_u32(smem));

@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(192, CPS)
         mbar_wait(&full[t % STAGES], (t / STAGES) & 1, &no_abort, err);
     }
   } else if (warp == 1) {
+    pdl_wait();                           // (the limit of its waits is for this kernel's work)
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16(kRows, NT);
       bool ok = true;

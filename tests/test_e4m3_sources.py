@@ -77,3 +77,17 @@ def test_dependents_are_let_in_once_tensor_memory_is_there():
                 barrier = kernel.index("__syncthreads()", took[-1])
                 assert min(let) > barrier, os.path.basename(path)
     assert seen == 4
+
+
+def test_waits_with_a_limit_begin_when_the_kernel_ahead_has_ended():
+    """A CTA may be resident long before: no warp counts that time against the two seconds
+    after which a wait is given up."""
+    for name in ("e4m3_gemm_few.cu", "e4m3_gemm_many.cu", "gemm_skinny.cu"):
+        text = source(name)
+        roles = re.split(r"\n  (?:if|\} else if) \(warp (?:==|>=) \d+\) \{|\n  \} else \{", text[text.index("pdl_trigger()"):])[1:]
+        roles = [r for r in roles if "mbar_wait" in r or "mbar_try_wait" in r][:4]
+        assert len(roles) >= 3
+        for r in roles[:3]:
+            first = re.search(r"mbar_(?:try_)?wait\w*\(", r).start()
+            # (the loads of the few-rows kernels wait for a stage only once all have been filled and released)
+            assert "pdl_wait()" in r[:first] or "release();" in r, name
