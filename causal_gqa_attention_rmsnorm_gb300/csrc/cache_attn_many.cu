@@ -456,12 +456,12 @@ __global__ void __launch_bounds__((ManyCfg<DH, E4>::THREADS), 1)
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
+    pdl_trigger();                                // (only now: common.cuh)
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_trigger();                                // (only now: common.cuh)
   pdl_wait();                                   // the plan, and whatever wrote q and the cache
   const long long total = m.pre[(size_t)a.c.B * m.pairs] * a.c.Hkv;
   const int parts = parts_of(m, total);

@@ -224,12 +224,12 @@ __global__ void __launch_bounds__(192, CPS)
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
+    pdl_trigger();                                // (only now: common.cuh)
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_trigger();                                // (only now: common.cuh)
   // (waited for where the first partial sums leave: the other CTAs' barriers exist then)
   if (push) cluster_arrive();
 
@@ -278,13 +278,13 @@ __global__ void __launch_bounds__(192, CPS)
       mbar_wait_warp(&full[t % STAGES], (t / STAGES) & 1, &no_abort, err);
   } else if (warp == 1) {
     // The whole warp walks the blocks; its elected lane issues (mma_mx_k128).
-    pdl_wait();                           // (the limit of its waits is for this kernel's work)
     const uint32_t elected = elect_one();
     const uint64_t desc = desc_kmajor_sw128(smem_u32(smem));
     const uint32_t desc_hi = (uint32_t)(desc >> 32), desc0 = (uint32_t)desc;
     const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
     uint32_t stage = 0, phase = 0;
     bool ok = true;
+    pdl_wait();                           // (the limit of its waits is for this kernel's work)
     for (int set = 0; ok && set < nsets; ++set) {
       const int chunk = set / kChunk, buf = chunk & 1;
       const bool first = set % kChunk == 0, last = set + 1 == nsets;

@@ -145,12 +145,12 @@ __global__ void __launch_bounds__(ManyCfg<CG>::THREADS, 1)
       tmem_alloc(tmem_slot, 512);
       tmem_relinquish();
     }
+    pdl_trigger();                        // (only now: common.cuh)
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_trigger();                                // (only now: common.cuh)
   auto commit = [](uint32_t bar, uint32_t elected) {
     if constexpr (CG == 2) mma_commit_pair_elected(bar, elected);
     else mma_commit_elected(bar, elected);

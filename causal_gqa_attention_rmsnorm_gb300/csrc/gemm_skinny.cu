@@ -98,12 +98,12 @@ __global__ void __launch_bounds__(192, CPS)
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
+    pdl_trigger();                                // (only now: common.cuh)
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_trigger();                                // (only now: common.cuh)
 
   if (warp == 0) {
     if (lane == 0) {
