@@ -23,7 +23,8 @@
 //               cluster barrier each CTA adds its share of the rows up over the
 //               cluster.  Always in rank order.
 // Chunks: the tensor core's accumulation cuts sums off instead of rounding them, which
-// shifts a sum of n instructions by up to n/2 steps of fp32.  A chunk is 64
+// shifts a sum of n instructions by up to n steps of fp32 (terms of one sign: 3 steps at 64
+// instructions, 10 at 128, 64 at 448, 0.65 n at 32768).  A chunk is 64
 // instructions (2048 of K); the chunks are added with rounding, in registers.  (A part of
 // K of one chunk, the usual case, keeps no sums there.)
 //
@@ -64,10 +65,7 @@ template <int NT, int MATS, int CPS, bool ONE> struct FewCfg {
   static constexpr int STAGES = FIT > 12 ? 12 : FIT;
   static constexpr uint32_t OFF_INBOX = STAGES * STAGE_BYTES;
   static constexpr uint32_t OFF_BAR = OFF_INBOX + INBOX;
-  // (with two CTAs per SM at least 88 KB: beside two that hold 256 columns of tensor memory each,
-  // no CTA of another cluster may start that waits for more)
-  static constexpr size_t NEEDED = OFF_BAR + 512 + 1024, LEAST = CPS == 2 ? 88 * 1024 : 0;
-  static constexpr size_t SMEM = NEEDED > LEAST ? NEEDED : LEAST;
+  static constexpr size_t SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t ACC = MATS * NT;                 // columns of one accumulator
   static constexpr uint32_t SET_COLS = 4 * MATS + 4;         // a word per weight row / 32 and row / 32
   static constexpr uint32_t SETS_AT = ONE ? ACC : 2 * ACC;
@@ -562,7 +560,8 @@ template <int NT, int MATS, int CPS, bool ONE> cudaError_t launch(const GemmArgs
   return cudaLaunchKernelEx(&cfg, k_e4m3_few<NT, MATS, CPS, ONE>, tw, tw3, tx, a, wtiles, sp, device_error_word());
 }
 
-// CPS: CTAs per SM of the form with several chunks (the one with one chunk has two).
+// CPS: CTAs per SM of the form with several chunks (the one with one chunk has two; gated
+// tiles of 64 rows are for long sums, and for them alone).
 template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStream_t s) {
   const int wtiles = (a.N + kBlk - 1) / kBlk, kblocks = (a.K + kBlk - 1) / kBlk;
   const long long tiles = (long long)wtiles * ((a.M + NT - 1) / NT);
@@ -570,9 +569,11 @@ template <int NT, int MATS, int CPS> cudaError_t go(const GemmArgs& a, cudaStrea
     const long long slots = (long long)cps * sm_count();
     return tiles > slots ? 1 : skinny_split_count((int)tiles, kblocks, (int)slots);
   };
-  const int two = split(2);
-  if ((kblocks + two - 1) / two <= kSet * kChunk) return launch<NT, MATS, 2, true>(a, wtiles, two, s);
-  return launch<NT, MATS, CPS, false>(a, wtiles, CPS == 2 ? two : split(CPS), s);
+  if constexpr (MATS == 1 || NT < 64) {
+    const int two = split(2);
+    if ((kblocks + two - 1) / two <= kSet * kChunk) return launch<NT, MATS, 2, true>(a, wtiles, two, s);
+  }
+  return launch<NT, MATS, CPS, false>(a, wtiles, split(CPS), s);
 }
 
 }  // namespace

@@ -314,3 +314,43 @@ def test_far_gates_to_few_bits(form, tile, out_dtype, up):
         assert (np.abs(f64(out) - want) <= off + 2 * HALF[BF16] * (np.abs(want) + off)).all()
     else:
         check_rows(bytes_of(out.codes), bytes_of(out.scale), want, off)
+
+
+# ---- beside other calls ---------------------------------------------------------------
+
+def test_products_beside_a_decode_step():
+    """On two streams at once: steps of the bf16 block over its cache, and 8-bit products of
+    every form that takes tensor memory in another amount."""
+    import workloads
+    from helpers import block_config, to_device
+    s = workloads.BlockShape("beside", "decode", "bf16", B=4, T=512, d=1024, H=8, Hkv=2, dh=128, f=4096, rope_base=5e5, eps=1e-5,
+                             gains="normal")
+    inp = workloads.make_block_inputs(s, seed=3)
+    lens0 = torch.tensor([5, 100, 300, 500], dtype=torch.int32).cuda()
+    kc, vc = workloads.make_decode_cache(s, 3, lens0.cpu(), fill=0.0, device="cuda")
+    kv, cfg, dev = tb.KVCache(kc, vc, lens0.clone()), block_config(s, max_pos=512), to_device(inp)
+    packed = tb.tb_pack_weights(cfg, dev)
+    g = gen(8)
+    calls = []
+    for M, N, K, y in ((3, 2064, 4112, F32), (40, 4096, 4608, F32), (100, 2560, 1024, BF16), (300, 2304, 768, BF16)):
+        x, w, w3 = make_rows(tb, M, K, g), make_weight(tb, N, K, g), make_weight(tb, N, K, g)
+        dt = tb.TB_F32 if y is F32 else tb.TB_BF16
+        calls.append(lambda x=x, w=w, dt=dt: tb.tb_gemm_e4m3(x, w, y_dtype=dt))
+        calls.append(lambda x=x, w=w, w3=w3, dt=dt: tb.tb_gated_e4m3(x, w, w3, out_dtype=dt))
+
+    def step():
+        kv.lens.copy_(lens0)
+        return tb.tb_block_decode(cfg, packed, dev["x"], kv)
+
+    want_step, want = step(), [c() for c in calls]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    steps, got = [], []
+    for _ in range(8):
+        with torch.cuda.stream(a):
+            steps += [step() for _ in range(4)]
+        with torch.cuda.stream(b):
+            got += [(c(), w) for c, w in zip(calls, want)]
+    torch.cuda.synchronize()
+    no_error()
+    assert all(torch.equal(y, want_step) for y in steps) and all(torch.equal(y, w) for y, w in got)
