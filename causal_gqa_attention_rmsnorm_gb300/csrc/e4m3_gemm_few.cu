@@ -29,8 +29,8 @@
 // K of one chunk, the usual case, keeps no sums there.)
 //
 // Measured in a stream of calls: 1 x 128256 x 4096 77 us, 6.8 TB/s, as fast as memory is
-// copied; 32 x 14336 x 4096 gated 21.1 us (5.6 TB/s), 32 x 4096 x 14336 13.0 (4.6), 1 x
-// 6144 x 4096 6.1 (4.1): a call takes 3 to 4 us whatever it reads, of which 1 is the first
+// copied; 32 x 14336 x 4096 gated 21.5 us (5.5 TB/s), 32 x 4096 x 14336 12.9 (4.6), 1 x
+// 6144 x 4096 6.0 (4.2): a call takes 3 to 4 us whatever it reads, of which 1 is the first
 // row tile's and the scales' load, 0.2 each K block's instructions, 0.5 the partial sums'
 // way.  (Partial sums read by the finishing CTA between two cluster barriers: 1 x 6144 x
 // 4096 7.1, 32 x 4096 x 14336 13.4; pushed row by row, 4 bytes at a time: 6.1 and 13.9.)

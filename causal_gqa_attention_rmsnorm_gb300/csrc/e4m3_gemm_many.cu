@@ -18,11 +18,11 @@
 // columns 224..479, and the 32 columns that they share are read first when a tile is
 // finished; the next tile's instructions wait for that (and not for the rest).
 //
-// Measured in a stream of calls: 16384 x 4096 x 14336 with the residual 535-550 us (3500-3590
-// TFLOP/s, 0.91-0.93 of twice cuBLAS's bf16 rate), gated 8192 x 14336 x 4096 500-515 us
-// (3740-3850); the power limit sets both (over seconds near 3000 at 1.4 to 1.6 GHz).  Short K:
-// 16384 x 768 x 768 13.1 us, gated 8192 x 2048 x 768 21.6 (a tile's instructions take 3100 cycles
-// there, its change 1200; without SiLU, stores and the exponents' exchange 19.8).
+// Measured in short graphs of calls: 16384 x 4096 x 14336 with the residual 535-565 us
+// (3400-3590 TFLOP/s, 0.88-0.93 of twice cuBLAS's bf16 rate), gated 8192 x 14336 x 4096 500-515
+// us (3740-3850); the power limit sets both (over seconds 646 and 595 us, 2980 and 3240 at 1.4
+// to 1.6 GHz).  Short K: 16384 x 768 x 768 12.7-14.0 us, 16384 x 2304 x 768 27.3, gated 8192 x
+// 2048 x 768 21.4-22.4 (a tile's instructions take 3100 cycles there, its change 1200; without SiLU, stores and the exponents' exchange 19.8).
 // What short K gained: scales through shared memory and the issuing warp's copies, where
 // they had been stored to tensor memory by warps that first waited for a set's last
 // instruction (17.6 -> 13.2 us, gated 31.5 -> 27); eight epilogue warps for four (gated
@@ -582,7 +582,10 @@ template <int CG, bool GATED, int ESIZE> cudaError_t go(const GemmArgs& a, cudaS
   // Weights beyond what L2 keeps, short rows: groups of 32 row units, so that a weight
   // tile is read once per group.  (Groups of 4, 8, 16 and 64 units for 16384 x 4096 x 14336,
   // which has none, 566, 561, 566 and 641 us for 564; for gated 8192 x 14336 x 4096 566, 548,
-  // 540 and 534 for 533.)
+  // 540 and 534 for 533.)  Off and on, us: gated 8192 x 14336 x 4096 605 and 520, 16384 x 14336 x
+  // 4096 620 and 597, gated 4096 x 14336 x 6144 508 and 425, 8192 x 14336 x 8192 718 and 580, 8192 x
+  // 8192 x 8192 361 and 371, 8192 x 8192 x 14336 630 and 620; after seconds of load 16384 x 4096 x
+  // 14336 627 and 671, so that long rows go without (though gated 4096 x 14336 x 10240 822 and 665).
   const size_t w_bytes = (size_t)a.N * a.K * (GATED ? 2 : 1);
   const int group = a.K <= 8192 && w_bytes > (size_t(48) << 20) && m_units > 1 ? std::min(m_units, 32) : 0;
   // Column tiles fastest and all of a row unit resident at once, y too large to stay in L2

@@ -465,11 +465,11 @@ TB_API tb_status tb_pack_e4m3(const void* w, int32_t dtype, const tb_e4m3* out, 
  *  res  : NULL, or device, dense [M, N] of y_dtype.
  *  y    : device, dense [M, N] of y_dtype (TB_F32 or TB_BF16), 16-byte aligned.  It may
  *         be res itself and overlaps nothing else that is read.
- * Products are exact and rounded once to y_dtype after their sum, which is fp32 and formed by
- * the tensor cores.  These cut off what fp32 addition would round: sums of terms of both signs
- * are off by 2e-7 of the results' size at K = 4096, sums of terms of one sign come out 1.2e-6
- * low there.  Of an fp32 result no accumulator holds more than 4096 of K, of one in bf16 (or
- * codes) 65536; longer sums are formed in parts of 2048, added with rounding (4e-7 or less). */
+ * Products are exact; their sum is fp32, formed by the tensor cores, and rounded once to
+ * y_dtype.  The tensor cores cut off what fp32 addition would round: sums of terms of both
+ * signs are off by 2e-7 of the results' size at K = 4096, sums of terms of one sign come out
+ * 1.2e-6 low there.  Of an fp32 result no accumulator holds more than 4096 of K, of one in bf16
+ * (or codes) 65536; longer sums are formed in parts of 2048, added with rounding (4e-7). */
 TB_API tb_status tb_gemm_e4m3(const tb_e4m3* x, const tb_e4m3* w, const void* res, void* y, int32_t y_dtype, void* stream);
 
 /* The gated half of the MLP: SiLU(x·w1) * (x·w3), x rows [M, K], w1 and w3 weights
